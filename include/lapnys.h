@@ -69,7 +69,8 @@ typedef enum {
   LAPNYS_ETIMEOUT = 3, /* a bounded device wait expired (see lapnys_device_status) */
   LAPNYS_ENOSPC = 4,   /* ctx or workspace smaller than the *_bytes functions require */
   LAPNYS_ENOTSUP = 5,  /* valid request outside what this build supports (e.g. d) */
-  LAPNYS_ESCRATCH = 6  /* problem too large for the built-in scratch of lapnys_fwd_static */
+  LAPNYS_ESCRATCH = 6, /* problem too large for the built-in scratch of lapnys_fwd_static */
+  LAPNYS_EPAGE = 7     /* a block table named a block that is not there (see lapnys_device_status) */
 } lapnys_status;
 
 enum { LAPNYS_F32 = 0, LAPNYS_BF16 = 1 };
@@ -260,10 +261,96 @@ int lapnys_block_bwd(const void* x, const void* w_qkv, const void* w_o, const vo
                      float eps, int iters, int tied, cudaStream_t stream, int dtype,
                      unsigned flags, void* ws, size_t ws_bytes);
 
-/* Synchronises the current device and reports whether a bounded device-side
- * wait (tensor-core pipeline barriers) expired since the last clear:
- * LAPNYS_ETIMEOUT if so (the affected results are invalid), LAPNYS_OK if not,
- * LAPNYS_ECUDA if the device reported an error.  clear != 0 resets the flag. */
+/* ---- softmax attention over a window and the first tokens --------------
+ * The local, exact attention beside the kernel attention above.  Query i of
+ * sequence b stands at position p = q_pos[b] + i, among that sequence's
+ * n = lens[b] keys; key j is visible to it iff
+ *
+ *     0 <= p < n,  j < n,  j <= p + right  and  (j >= p - left or j < sinks),
+ *
+ * and   s = scale q.k,  P = softmax of s over the visible keys,  o = P v.
+ *  - q, out, dout, dq: [B][Hq][Nq][d]; k, v, dk, dv: [B][Hkv][Nk][d]; Hq a
+ *    multiple of Hkv (query head h reads key head h / (Hq / Hkv)); contiguous
+ *    DEVICE arrays of element type `dtype`, 16-byte aligned.  d a multiple of
+ *    16 up to 128 (else ENOTSUP).  1 <= Nq, Nk <= 2^28; offsets are 64-bit.
+ *  - left, right >= 0, or -1 for no bound; right = 0 is causal; sinks >= 0.
+ *    scale > 0 (1 / sqrt(d) is the usual one).
+ *  - lens (int32 [B], device, or NULL for Nk) cuts a padded batch: rows of k, v
+ *    at and behind lens[b] may hold anything.  Values are read as min(max(lens,
+ *    0), Nk).  q_pos (int32 [B], device, or NULL for Nk - Nq: the queries are
+ *    the last tokens).  A query that sees no key (padding, an empty sequence)
+ *    gives out = 0, lse = -inf, and takes no part in any gradient; k, v rows
+ *    that no query sees get gradient 0.  Every element of out, dq, dk, dv is
+ *    written.
+ *  - Keys, values and queries inside a sequence have to be finite for finite
+ *    results: what one query does not see may still meet it as 0 * value.
+ *  - lse [B][Hq][Nq] float: log2 of the sum of exp(s); may be NULL in the
+ *    forward; the backward reads the forward's.
+ *  - fp32 arithmetic; bf16 tensors: products of bf16 operands with fp32 sums,
+ *    P and dS rounded to bf16 between products, outputs rounded once.
+ *  - Deterministic.  One workspace per call in flight, of
+ *    lapnys_window_workspace_bytes (may be 0: ws NULL); 0 also for invalid
+ *    arguments. */
+size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int left,
+                                     int right, int sinks, int dtype, int backward);
+int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                      const int32_t* lens, const int32_t* q_pos, int B, int Hq, int Hkv, int Nq,
+                      int Nk, int d, int left, int right, int sinks, float scale,
+                      cudaStream_t stream, int dtype, void* ws, size_t ws_bytes);
+int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
+                      const void* dout, const float* lse, const int32_t* lens,
+                      const int32_t* q_pos, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                      int Nq, int Nk, int d, int left, int right, int sinks, float scale,
+                      cudaStream_t stream, int dtype, void* ws, size_t ws_bytes);
+
+/* ---- the same attention over a cache held in 8 bits --------------------
+ * The serving form: keys and values as e4m3 in blocks of `block` tokens (16, 32,
+ * 64 or 128), with one float scale, a power of two, for each block and head:
+ * k = k_cache * k_scale.
+ *  - k_cache, v_cache: [blocks][Hkv][block][d] bytes, 16-byte aligned;
+ *    k_scale, v_scale: [blocks][Hkv] float.
+ *  - table: int32 [B][max_blocks], token j of sequence b lies in slot j % block
+ *    of block table[b][j / block].  Only entries of blocks that hold a token
+ *    which the call reads or writes are looked at.  An entry outside
+ *    [0, blocks) is no error of the call: nothing is read or written there, its
+ *    tokens are invisible (or dropped), and lapnys_device_status reports
+ *    LAPNYS_EPAGE.  Sequences may share blocks that are only read.
+ *
+ * lapnys_cache_append rounds N new tokens k, v [B][Hkv][N][d] (dtype) into the
+ * cache: token i goes to position start[b] + i, as far as that is inside
+ * [0, min(lens[b], max_blocks * block)) (lens NULL: no bound of its own).
+ *    scale = 2^ceil(log2(amax / 448)), amax over the block's new finite values,
+ *            at least 2^-100; a block that held tokens before start[b] keeps its
+ *            scale if that is larger, else its tokens are rounded again to the
+ *            new one (exact but for values that become subnormal);
+ *    value = e4m3(x / scale), to nearest, ties to even; infinities saturate, NaN
+ *            stays NaN.
+ * Slots behind the last new token stay as they were.  No two sequences of a
+ * call may append to the same block (its content would be undefined).
+ *
+ * lapnys_cache_attention: q, out [B][Hq][Nq][d] (dtype); lens int32 [B] counts
+ * the sequence's tokens in the cache, q_pos NULL means lens[b] - Nq (the
+ * queries are its last tokens).  Mask, empty rows and scale as above; meant for
+ * a few queries a call (any number is right).  Workspace:
+ * lapnys_cache_workspace_bytes (may be 0). */
+int lapnys_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale,
+                        float* v_scale, const int32_t* table, const int32_t* start,
+                        const int32_t* lens, int B, int Hkv, int N, int d, int block, int blocks,
+                        int max_blocks, cudaStream_t stream, int dtype);
+size_t lapnys_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int block, int blocks,
+                                    int max_blocks, int left, int right, int sinks, int dtype);
+int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, const int32_t* table,
+                           const int32_t* lens, const int32_t* q_pos, void* out, int B, int Hq,
+                           int Hkv, int Nq, int d, int block, int blocks, int max_blocks, int left,
+                           int right, int sinks, float scale, cudaStream_t stream, int dtype,
+                           void* ws, size_t ws_bytes);
+
+/* Synchronises the current device and reports what kernels recorded since the
+ * last clear: LAPNYS_ETIMEOUT if a bounded device-side wait (tensor-core
+ * pipeline barriers) expired (the affected results are invalid), LAPNYS_EPAGE if
+ * a block table named a block that is not there, LAPNYS_OK if neither,
+ * LAPNYS_ECUDA if the device reported an error.  clear != 0 resets both. */
 int lapnys_device_status(int clear);
 
 /* Self-test of the failure detection (no passage of the paper corresponds to

@@ -12,7 +12,7 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblapnys.so")
 
 (LAPNYS_OK, LAPNYS_EINVAL, LAPNYS_ECUDA, LAPNYS_ETIMEOUT, LAPNYS_ENOSPC, LAPNYS_ENOTSUP,
- LAPNYS_ESCRATCH) = range(7)
+ LAPNYS_ESCRATCH, LAPNYS_EPAGE) = range(8)
 LAPNYS_F32, LAPNYS_BF16 = 0, 1
 LAPNYS_NORM, LAPNYS_GAUSS, LAPNYS_NORM_BATCH = 1, 2, 4
 
@@ -24,6 +24,8 @@ EXPORTS = (
     "lapnys_device_status", "lapnys_block_ctx_bytes", "lapnys_block_workspace_bytes",
     "lapnys_block_fwd", "lapnys_block_bwd", "lapnys_wait_selftest",
     "lapnys_fma_probe",
+    "lapnys_window_workspace_bytes", "lapnys_window_fwd", "lapnys_window_bwd",
+    "lapnys_cache_append", "lapnys_cache_workspace_bytes", "lapnys_cache_attention",
 )
 
 
@@ -90,6 +92,18 @@ def load() -> ctypes.CDLL:
     lib.lapnys_profile_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(I),
                                         ctypes.POINTER(ctypes.c_double), I]
     lib.lapnys_profile_read.restype = I
+    lib.lapnys_window_workspace_bytes.argtypes = [I] * 11
+    lib.lapnys_window_workspace_bytes.restype = S
+    lib.lapnys_window_fwd.argtypes = [P] * 7 + [I] * 9 + [F, P, I, P, S]
+    lib.lapnys_window_fwd.restype = I
+    lib.lapnys_window_bwd.argtypes = [P] * 11 + [I] * 9 + [F, P, I, P, S]
+    lib.lapnys_window_bwd.restype = I
+    lib.lapnys_cache_append.argtypes = [P] * 9 + [I] * 7 + [P, I]
+    lib.lapnys_cache_append.restype = I
+    lib.lapnys_cache_workspace_bytes.argtypes = [I] * 12
+    lib.lapnys_cache_workspace_bytes.restype = S
+    lib.lapnys_cache_attention.argtypes = [P] * 9 + [I] * 11 + [F, P, I, P, S]
+    lib.lapnys_cache_attention.restype = I
     _lib = lib
     return lib
 

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "win.cuh"
+
 namespace lapnys {
 
 struct Prob {
@@ -300,5 +302,49 @@ bool bwd_tc_shape(int dtype, int d);
 int bwd_tc_groups(int m);
 int bwd_tc_splits(int BH, int m, int N);
 cudaError_t run_bwd_tc(const Prob& p, int mode, const BwdTcArgs& a, cudaStream_t st);
+
+// ---- windowed softmax attention and the 8-bit cache (win.cuh) --------------
+// tiles of queries and keys on the FP32 pipe
+int win_tile_rows();
+cudaError_t run_win_fwd(const WinArgs& a, bool bf16, cudaStream_t st);
+cudaError_t run_win_bwd(const WinArgs& a, bool bf16, cudaStream_t st);
+// dK, dV of the key tiles with first tokens, from their chunks' partials
+cudaError_t run_win_join(const WinArgs& a, int tile_rows, bool bf16, cudaStream_t st);
+
+// a few queries per sequence, the keys split over blocks; table null: plain
+// keys and values, else the cache (w.Nk = max_blocks * T)
+struct TokenArgs {
+  WinArgs w;
+  const float* k_scale;    // [blocks][Hkv]
+  const float* v_scale;
+  const int32_t* table;    // [B][max_blocks]
+  int T, blocks, max_blocks;
+  int rtiles, splits;      // row tiles of 16, shares of the keys
+  float* part_o;           // [rows][splits][d]
+  float2* part_ml;         // [rows][splits]: maximum, sum
+  int* err;                // bit 1: a table named a block that is not there
+};
+struct TokenShape {
+  int rtiles, splits;
+  size_t o_bytes, ml_bytes;
+};
+TokenShape token_shape(int B, int Hkv, int g, int Nq, int d, long long keys, int left, int right,
+                       int sinks);
+cudaError_t run_token(TokenArgs& t, bool bf16, cudaStream_t st);
+
+struct AppendArgs {
+  const void* k;           // [B][Hkv][N][d]
+  const void* v;
+  uint8_t* k_cache;        // [blocks][Hkv][T][d] e4m3
+  uint8_t* v_cache;
+  float* k_scale;          // [blocks][Hkv]
+  float* v_scale;
+  const int32_t* table;    // [B][max_blocks]
+  const int32_t* start;    // [B]
+  const int32_t* lens;     // [B] or null
+  int B, Hkv, N, d, T, blocks, max_blocks, nt;
+  int* err;
+};
+cudaError_t run_cache_append(AppendArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace lapnys

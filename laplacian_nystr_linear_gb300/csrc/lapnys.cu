@@ -379,10 +379,12 @@ const char* lapnys_strerror(int status) {
     case LAPNYS_ECUDA: return "CUDA launch failed";
     case LAPNYS_ETIMEOUT: return "bounded device wait expired";
     case LAPNYS_ENOSPC: return "ctx or workspace buffer too small";
-    case LAPNYS_ENOTSUP: return "unsupported configuration (d must be 16, 32, 64 or 128)";
+    case LAPNYS_ENOTSUP: return "unsupported configuration (d must be 16, 32, 64 or 128; "
+                                "windowed attention and the cache: a multiple of 16 up to 128)";
     case LAPNYS_ESCRATCH:
       return "problem needs more scratch than the 32 MiB built into lapnys_fwd_static; "
              "call lapnys_fwd with a caller-owned workspace";
+    case LAPNYS_EPAGE: return "a block table names a block that the cache does not have";
   }
   return "unknown status";
 }
@@ -848,7 +850,7 @@ int lapnys_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return LAPNYS_ECUDA;
   const int v = read_wait_error(clear != 0);
   if (v < 0) return LAPNYS_ECUDA;
-  return v ? LAPNYS_ETIMEOUT : LAPNYS_OK;
+  return v & 1 ? LAPNYS_ETIMEOUT : (v & 2 ? LAPNYS_EPAGE : LAPNYS_OK);
 }
 
 uint64_t lapnys_launch_count(void) { return g_launches; }

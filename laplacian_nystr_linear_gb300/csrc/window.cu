@@ -1,0 +1,248 @@
+// C ABI of the windowed attention and of the attention over an 8-bit cache
+// (include/lapnys.h has the contract): argument checks, workspaces, and the
+// choice of kernel.
+#include <math.h>
+#include <string.h>
+
+#include "../../include/lapnys.h"
+#include "internal.h"
+#include "win.cuh"
+
+namespace lapnys {
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// a side of the window: -1 is open; as the kernels take it
+bool side(int given, int* out) {
+  if (given < -1) return false;
+  *out = given < 0 || given > kWinUnbounded ? kWinUnbounded : given;
+  return true;
+}
+
+int check_mask(WinArgs& a, int left, int right, int sinks, float scale) {
+  if (!side(left, &a.left) || !side(right, &a.right) || sinks < 0) return LAPNYS_EINVAL;
+  if (!(scale > 0.f) || !isfinite(scale)) return LAPNYS_EINVAL;
+  a.sinks = sinks > kWinMaxLen ? kWinMaxLen : sinks;
+  a.scale = scale;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  return LAPNYS_OK;
+}
+
+int check_dims(WinArgs& a, int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || Nk <= 0 || d <= 0) return LAPNYS_EINVAL;
+  if (Hq % Hkv != 0 || Nq > kWinMaxLen || Nk > kWinMaxLen) return LAPNYS_EINVAL;
+  if (d % 16 != 0 || d > 128) return LAPNYS_ENOTSUP;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.g = Hq / Hkv; a.Nq = Nq; a.Nk = Nk; a.d = d;
+  // grids are one-dimensional, a block for at least 16 rows or keys
+  const long long tiles = (long long)B * Hq * ((Nq + 15LL) / 16 + (Nk + 15LL) / 16);
+  return tiles < 1LL << 30 ? LAPNYS_OK : LAPNYS_EINVAL;
+}
+
+// Few queries go to the kernel that splits the keys (k_token.cu): it reads the
+// keys once for 16 rows (query heads of a group x queries).
+bool few(int g, int Nq) { return Nq <= 8 || g * Nq <= 16; }
+
+struct WinWs {
+  TokenShape tok;
+  size_t o, ml;                 // forward, few queries
+  size_t D, part;               // backward
+  int stiles, chunks, chunk_rows;
+  size_t total;
+};
+
+WinWs window_ws(const WinArgs& a, bool backward, int tile) {
+  WinWs w;
+  memset(&w, 0, sizeof(w));
+  size_t o = 0;
+  if (!backward) {
+    if (few(a.g, a.Nq)) {
+      w.tok = token_shape(a.B, a.Hkv, a.g, a.Nq, a.d, a.Nk, a.left, a.right, a.sinks);
+      w.o = o; o = align256(o + w.tok.o_bytes);
+      w.ml = o; o = align256(o + w.tok.ml_bytes);
+    }
+  } else {
+    w.D = o; o = align256(o + (size_t)a.B * a.Hq * a.Nq * 4);
+    // Key tiles with first tokens that queries beyond the window see too: their
+    // queries in ranges as long as an ordinary tile's, or longer where enough
+    // blocks run anyway (four for each of 152 SMs), which bounds the partials.
+    const int S = a.sinks < a.Nk ? a.sinks : a.Nk;
+    const long long reach = (long long)a.left + a.right + tile;
+    if (S > 0 && reach < a.Nq) {
+      w.stiles = (S + tile - 1) / tile;
+      long long n = (a.Nq + reach - 1) / reach;
+      const long long most = 608 / ((long long)a.B * a.Hkv * w.stiles) + 1;
+      n = n < most ? n : most;
+      w.chunk_rows = (int)(((a.Nq + n - 1) / n + tile - 1) / tile * tile);
+      w.chunks = (a.Nq + w.chunk_rows - 1) / w.chunk_rows;
+      w.part = o;
+      o = align256(o + (size_t)a.B * a.Hkv * w.stiles * w.chunks * 2 * tile * a.d * 4);
+    }
+  }
+  w.total = o;
+  return w;
+}
+
+int check_window(WinArgs& a, int B, int Hq, int Hkv, int Nq, int Nk, int d, int left, int right,
+                 int sinks, float scale, int dtype) {
+  int rc = check_dims(a, B, Hq, Hkv, Nq, Nk, d);
+  if (rc != LAPNYS_OK) return rc;
+  if ((rc = check_mask(a, left, right, sinks, scale)) != LAPNYS_OK) return rc;
+  return dtype == LAPNYS_F32 || dtype == LAPNYS_BF16 ? LAPNYS_OK : LAPNYS_EINVAL;
+}
+
+// a cache: `blocks` blocks of `block` tokens, at most max_blocks of them a sequence
+int check_cache(WinArgs& a, int B, int Hq, int Hkv, int Nq, int d, int block, int blocks,
+                int max_blocks, int dtype) {
+  if (block != 16 && block != 32 && block != 64 && block != 128) return LAPNYS_EINVAL;
+  if (blocks <= 0 || max_blocks <= 0 || (long long)max_blocks * block > kWinMaxLen)
+    return LAPNYS_EINVAL;
+  if (dtype != LAPNYS_F32 && dtype != LAPNYS_BF16) return LAPNYS_EINVAL;
+  return check_dims(a, B, Hq, Hkv, Nq, max_blocks * block, d);
+}
+
+int status(cudaError_t e) { return e == cudaSuccess ? LAPNYS_OK : LAPNYS_ECUDA; }
+
+}  // namespace
+}  // namespace lapnys
+
+using namespace lapnys;
+
+extern "C" {
+
+size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int left,
+                                     int right, int sinks, int dtype, int backward) {
+  WinArgs a;
+  memset(&a, 0, sizeof(a));
+  if (check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, 1.f, dtype) != LAPNYS_OK) return 0;
+  return window_ws(a, backward != 0, win_tile_rows()).total;
+}
+
+int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                      const int32_t* lens, const int32_t* q_pos, int B, int Hq, int Hkv, int Nq,
+                      int Nk, int d, int left, int right, int sinks, float scale,
+                      cudaStream_t stream, int dtype, void* ws, size_t ws_bytes) {
+  NvtxScope nvtx_scope("lapnys_window_fwd");
+  TokenArgs t;
+  memset(&t, 0, sizeof(t));
+  WinArgs& a = t.w;
+  const int rc = check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, scale, dtype);
+  if (rc != LAPNYS_OK) return rc;
+  if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
+    return LAPNYS_EINVAL;
+  const WinWs w = window_ws(a, false, win_tile_rows());
+  if (w.total > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
+  if (ws_bytes < w.total) return LAPNYS_ENOSPC;
+  a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
+  if (few(a.g, Nq)) {
+    t.rtiles = w.tok.rtiles;
+    t.splits = w.tok.splits;
+    t.part_o = (float*)((uint8_t*)ws + w.o);
+    t.part_ml = (float2*)((uint8_t*)ws + w.ml);
+    return status(run_token(t, dtype == LAPNYS_BF16, stream));
+  }
+  return status(run_win_fwd(a, dtype == LAPNYS_BF16, stream));
+}
+
+int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
+                      const void* dout, const float* lse, const int32_t* lens,
+                      const int32_t* q_pos, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                      int Nq, int Nk, int d, int left, int right, int sinks, float scale,
+                      cudaStream_t stream, int dtype, void* ws, size_t ws_bytes) {
+  NvtxScope nvtx_scope("lapnys_window_bwd");
+  WinArgs a;
+  memset(&a, 0, sizeof(a));
+  const int rc = check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, scale, dtype);
+  if (rc != LAPNYS_OK) return rc;
+  const void* all[] = {q, k, v, out, dout, dq, dk, dv, ws};
+  for (const void* p : all)
+    if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
+  if (!lse || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4)) return LAPNYS_EINVAL;
+  const WinWs w = window_ws(a, true, win_tile_rows());
+  if (ws_bytes < w.total) return LAPNYS_ENOSPC;
+  a.q = q; a.k = k; a.v = v; a.out = const_cast<void*>(out); a.dout = dout;
+  a.lse = const_cast<float*>(lse); a.lens = lens; a.q_pos = q_pos;
+  a.dq = dq; a.dk = dk; a.dv = dv;
+  a.D = (float*)((uint8_t*)ws + w.D);
+  a.part = (float*)((uint8_t*)ws + w.part);
+  a.stiles = w.stiles; a.chunks = w.chunks; a.chunk_rows = w.chunk_rows;
+  return status(run_win_bwd(a, dtype == LAPNYS_BF16, stream));
+}
+
+int lapnys_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale,
+                        float* v_scale, const int32_t* table, const int32_t* start,
+                        const int32_t* lens, int B, int Hkv, int N, int d, int block, int blocks,
+                        int max_blocks, cudaStream_t stream, int dtype) {
+  NvtxScope nvtx_scope("lapnys_cache_append");
+  WinArgs a;
+  memset(&a, 0, sizeof(a));
+  const int rc = check_cache(a, B, Hkv, Hkv, N, d, block, blocks, max_blocks, dtype);
+  if (rc != LAPNYS_OK) return rc;
+  const void* all[] = {k, v, k_cache, v_cache};
+  for (const void* p : all)
+    if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
+  const void* words[] = {k_scale, v_scale, table, start};
+  for (const void* p : words)
+    if (!p || !aligned(p, 4)) return LAPNYS_EINVAL;
+  if (!aligned(lens, 4)) return LAPNYS_EINVAL;
+  AppendArgs p;
+  memset(&p, 0, sizeof(p));
+  p.k = k; p.v = v;
+  p.k_cache = (uint8_t*)k_cache; p.v_cache = (uint8_t*)v_cache;
+  p.k_scale = k_scale; p.v_scale = v_scale;
+  p.table = table; p.start = start; p.lens = lens;
+  p.B = B; p.Hkv = Hkv; p.N = N; p.d = d; p.T = block; p.blocks = blocks; p.max_blocks = max_blocks;
+  p.err = wait_error_address();
+  if (p.err == nullptr) return LAPNYS_ECUDA;
+  return status(run_cache_append(p, dtype == LAPNYS_BF16, stream));
+}
+
+size_t lapnys_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int block, int blocks,
+                                    int max_blocks, int left, int right, int sinks, int dtype) {
+  WinArgs a;
+  memset(&a, 0, sizeof(a));
+  if (check_cache(a, B, Hq, Hkv, Nq, d, block, blocks, max_blocks, dtype) != LAPNYS_OK) return 0;
+  if (check_mask(a, left, right, sinks, 1.f) != LAPNYS_OK) return 0;
+  const TokenShape s = token_shape(B, Hkv, a.g, Nq, d, a.Nk, a.left, a.right, a.sinks);
+  return align256(s.o_bytes) + align256(s.ml_bytes);
+}
+
+int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, const int32_t* table,
+                           const int32_t* lens, const int32_t* q_pos, void* out, int B, int Hq,
+                           int Hkv, int Nq, int d, int block, int blocks, int max_blocks, int left,
+                           int right, int sinks, float scale, cudaStream_t stream, int dtype,
+                           void* ws, size_t ws_bytes) {
+  NvtxScope nvtx_scope("lapnys_cache_attention");
+  TokenArgs t;
+  memset(&t, 0, sizeof(t));
+  WinArgs& a = t.w;
+  int rc = check_cache(a, B, Hq, Hkv, Nq, d, block, blocks, max_blocks, dtype);
+  if (rc != LAPNYS_OK) return rc;
+  if ((rc = check_mask(a, left, right, sinks, scale)) != LAPNYS_OK) return rc;
+  const void* all[] = {q, k_cache, v_cache, out};
+  for (const void* p : all)
+    if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
+  const void* words[] = {k_scale, v_scale, table, lens};
+  for (const void* p : words)
+    if (!p || !aligned(p, 4)) return LAPNYS_EINVAL;
+  if (!aligned(q_pos, 4)) return LAPNYS_EINVAL;
+  const TokenShape s = token_shape(B, Hkv, a.g, Nq, d, a.Nk, a.left, a.right, a.sinks);
+  const size_t need = align256(s.o_bytes) + align256(s.ml_bytes);
+  if (need > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
+  if (ws_bytes < need) return LAPNYS_ENOSPC;
+  a.q = q; a.k = k_cache; a.v = v_cache; a.out = out; a.lens = lens; a.q_pos = q_pos;
+  t.k_scale = k_scale; t.v_scale = v_scale; t.table = table;
+  t.T = block; t.blocks = blocks; t.max_blocks = max_blocks;
+  t.rtiles = s.rtiles;
+  t.splits = s.splits;
+  t.part_o = (float*)ws;
+  t.part_ml = (float2*)((uint8_t*)ws + align256(s.o_bytes));
+  t.err = wait_error_address();
+  if (t.err == nullptr) return LAPNYS_ECUDA;
+  return status(run_token(t, dtype == LAPNYS_BF16, stream));
+}
+
+}  // extern "C"
