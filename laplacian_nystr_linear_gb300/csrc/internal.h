@@ -311,6 +311,10 @@ cudaError_t run_win_bwd(const WinArgs& a, bool bf16, cudaStream_t st);
 // dK, dV of the key tiles with first tokens, from their chunks' partials
 cudaError_t run_win_join(const WinArgs& a, int tile_rows, bool bf16, cudaStream_t st);
 
+// the forward on the tensor cores, bf16
+cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st);
+bool win_map(CUtensorMap* t, const void* p, int BH, int N, int d, int rows);
+
 // a few queries per sequence, the keys split over blocks; table null: plain
 // keys and values, else the cache (w.Nk = max_blocks * T)
 struct TokenArgs {

@@ -1,0 +1,496 @@
+// Windowed softmax attention, forward, bf16, on the tcgen05 tensor cores
+// (visibility rule: win.cuh; operand tiles: win_tc.cuh).
+//
+// One CTA per SM walks over items of two tiles of 128 query rows that share their
+// keys: the same rows of two query heads of a group when the group's size is
+// even, else neighbouring rows of one head.  The keys come in steps of at most
+// 128: first the steps of the first tokens, then the window's, from its first
+// key on (TMA rows start anywhere), a last step as wide as it has to be (a
+// multiple of 16), so four first tokens cost a step of 16 keys.
+//
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1, one row per thread: scores
+//                   from tensor memory, exp2 in fp32, P as bf16 back into the
+//                   scores' columns.  The running maximum is only moved when it
+//                   grows by more than 2^8 (P <= 2^8: fp32 sums and bf16's
+//                   relative rounding are as good there), so the outputs are
+//                   rescaled on few steps;
+//   warp 8          TMA: K and V tiles through one ring;
+//   warp 9          issues  S = Q K^T  (both operands in shared memory)  and
+//                   O += P V  (P in tensor memory, V as it lies: MN-major):
+//                   PV0 QK0' PV1 QK1' ..., so one tile's softmax runs under the
+//                   other tile's products.  S of a step is complete only when
+//                   the tile's products before it are, so O needs no barrier of
+//                   its own within an item.
+//
+// Bound: 4 d flops per visible pair on the tensor pipe, or one exponential per
+// pair on the special-function pipe, whichever is longer (d = 64: the latter).
+// Rows of V at and behind the sequence's end are zeroed in shared memory (P is 0
+// there, but 0 * NaN is not); rows behind the tensor's are zero by TMA.
+// Every wait is bounded, as in the other tensor-core kernels.
+#include <cstring>
+
+#include "internal.h"
+#include "win_tc.cuh"
+
+namespace lapnys {
+
+namespace {
+using namespace wtc;
+constexpr int FT = 128;                 // query rows of a tile, keys of a step
+constexpr int FTH = 384;                // three warpgroups: two of softmax, one that issues
+// registers a thread: 256 * 208 + 128 * 80 <= 384 * 168, the launch's share
+constexpr int FREG_SOFTMAX = 208, FREG_ISSUE = 88;
+constexpr uint32_t PANEL = FT * 128;    // a panel: 128 rows of 64 features, 16 KB
+template <int NP>
+struct FwdShape {
+  static constexpr uint32_t TILE = NP * PANEL;
+  static constexpr int NST = NP == 1 ? 8 : 4;
+  static constexpr uint32_t SMEM = (2 + NST) * TILE + 1024;
+};
+constexpr float kMoveMax = 8.f;         // the maximum moves when it grows by 2^8
+
+struct FwdMaps {
+  CUtensorMap q, k, v;                  // boxes of 64 x 128
+  CUtensorMap k16, v16;                 // boxes of 64 x 16 for narrow steps
+};
+struct FwdGeom {
+  int qt;                               // tiles of 128 query rows
+  int npair;                            // items per (batch, key head): pairs of heads or of tiles
+  int by_head;                          // 1: an item's tiles are two heads
+  long long items;
+  int* err;
+};
+
+struct FwdItem {
+  int b, hk;
+  int head[2], i0[2], i1[2];            // query head and rows of both tiles
+  WinSeq sq;
+  WinRange kr;                          // keys that either tile sees
+  WinRange own[2];
+  int ns, nw;                           // steps of the first tokens, of the window
+};
+__device__ __forceinline__ FwdItem fwd_item(const WinArgs& a, const FwdGeom& gm, long long it) {
+  FwdItem r;
+  // the last query tiles first: with an open left side they see the most keys
+  const int heads = a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g);
+  const int tq = gm.npair - 1 - (int)(it / heads);
+  int h = (int)(it % heads);
+  const int per = gm.by_head ? a.g / 2 : a.g;
+  const int e = h % per;
+  h /= per;
+  r.hk = h % a.Hkv;
+  r.b = h / a.Hkv;
+  r.sq = win_seq(a, r.b);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    r.head[s] = r.hk * a.g + (gm.by_head ? 2 * e + s : e);
+    r.i0[s] = min(a.Nq, (gm.by_head ? tq : 2 * tq + s) * FT);
+    r.i1[s] = min(a.Nq, r.i0[s] + FT);
+    r.own[s] = r.i0[s] < r.i1[s] ? win_keys(a, r.sq, r.i0[s], r.i1[s]) : WinRange{0, 0, 0};
+  }
+  r.kr = win_keys(a, r.sq, r.i0[0], r.i1[1]);
+  r.ns = (r.kr.S + FT - 1) / FT;
+  r.nw = r.kr.hi > r.kr.lo ? (r.kr.hi - r.kr.lo + FT - 1) / FT : 0;
+  return r;
+}
+// step j of an item: keys [j0, je), and the width of its products
+struct FwdStep {
+  int j0, je, w;
+};
+__device__ __forceinline__ FwdStep fwd_step(const FwdItem& r, int j) {
+  FwdStep s;
+  if (j < r.ns) {
+    s.j0 = j * FT;
+    s.je = min(r.kr.S, s.j0 + FT);
+  } else {
+    s.j0 = r.kr.lo + (j - r.ns) * FT;
+    s.je = min(r.kr.hi, s.j0 + FT);
+  }
+  s.w = (s.je - s.j0 + 15) & ~15;
+  return s;
+}
+// does a tile that sees the keys `o` see any of the step's?
+__device__ __forceinline__ bool fwd_active(const WinArgs& a, const WinRange& o, const FwdStep& s) {
+  return s.j0 < o.hi && (s.je > o.lo || s.j0 < a.sinks);
+}
+}  // namespace
+
+template <int NP>
+__global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ FwdMaps mp,
+                                                       const WinArgs a, const FwdGeom gm) {
+  using SH = FwdShape<NP>;
+  constexpr int NST = SH::NST;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full[NST], empty[NST];
+  __shared__ __align__(8) uint64_t qfull[2], qempty[2];   // Q tile landed; its products done
+  __shared__ __align__(8) uint64_t sfull[2];              // scores ready
+  __shared__ __align__(8) uint64_t pfull[2];              // P written (128 arrivals)
+  __shared__ __align__(8) uint64_t ofull[2], oempty[2];   // outputs ready; read out (128 arrivals)
+  __shared__ __align__(8) uint64_t drain;
+  __shared__ uint32_t tmem_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t qbuf = base, ring = base + 2 * SH::TILE;
+  auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
+
+  if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(bar(&full[i]), 1);
+      tc::mbar_init(bar(&empty[i]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(bar(&qfull[s]), 1);
+      tc::mbar_init(bar(&qempty[s]), 1);
+      tc::mbar_init(bar(&sfull[s]), 1);
+      tc::mbar_init(bar(&pfull[s]), FT);
+      tc::mbar_init(bar(&ofull[s]), 1);
+      tc::mbar_init(bar(&oempty[s]), FT);
+    }
+    tc::mbar_init(bar(&drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_s;
+  // tensor memory: scores (then P) of both tiles, outputs of both
+  const uint32_t tS[2] = {tmem, tmem + FT}, tO[2] = {tmem + 2 * FT, tmem + 2 * FT + NP * 64};
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FREG_ISSUE));
+  if (warp == 8) {
+    // ---------------- TMA ----------------
+    if (lane == 0) {
+      int n = 0;                       // tiles issued to the ring
+      int nq[2] = {0, 0};              // Q tiles issued
+      bool bad = false;
+      auto load = [&](const CUtensorMap* wide, const CUtensorMap* narrow, const FwdStep& s, int bh) {
+        const int st = n % NST;
+        if (!wait_or_flag(gm.err, bar(&empty[st]), ((n / NST) & 1) ^ 1u)) return false;
+        const uint32_t dst = ring + st * SH::TILE;
+        tc::mbar_expect_tx(bar(&full[st]), (uint32_t)(NP * s.w * 128));
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {
+          if (s.w == FT) {
+            tma3(dst + p * PANEL, wide, 64 * p, s.j0, bh, bar(&full[st]));
+          } else {
+#pragma unroll 1
+            for (int r = 0; r < s.w; r += 16)
+              tma3(dst + p * PANEL + r * 128, narrow, 64 * p, s.j0 + r, bh, bar(&full[st]));
+          }
+        }
+        ++n;
+        return true;
+      };
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const FwdItem r = fwd_item(a, gm, it);
+        const int steps = r.ns + r.nw;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (r.own[t].hi == 0) continue;
+          if (!wait_or_flag(gm.err, bar(&qempty[t]), (nq[t] & 1) ^ 1u)) { bad = true; break; }
+          tc::mbar_expect_tx(bar(&qfull[t]), SH::TILE);
+          for (int p = 0; p < NP; ++p)
+            tma3(qbuf + t * SH::TILE + p * PANEL, &mp.q, 64 * p, r.i0[t], r.b * a.Hq + r.head[t],
+                 bar(&qfull[t]));
+          ++nq[t];
+        }
+        const int bh = r.b * a.Hkv + r.hk;
+#pragma unroll 1
+        for (int j = 0; j < steps && !bad; ++j) {
+          const FwdStep s = fwd_step(r, j);
+          bad = !load(&mp.k, &mp.k16, s, bh) || !load(&mp.v, &mp.v16, s, bh);
+        }
+      }
+      // every copy has landed before the block ends, also after an expired wait
+#pragma unroll 1
+      for (int i = n > NST ? n - NST : 0; i < n; ++i)
+        wait_or_flag(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (nq[t]) wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)(nq[t] - 1) & 1u);
+    }
+  } else if (warp == 9) {
+    // ---------------- products ----------------
+    int n = 0;                          // ring tiles taken
+    int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
+    bool bad = false;
+    const int ksteps = a.d / 16;
+    auto slot = [&](int i) { return ring + (i % NST) * SH::TILE; };
+    auto take = [&](int i) {            // the whole warp waits for ring tile i
+      return wait_warp(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
+    };
+    auto qk = [&](int t, int i, int w) {
+      const uint32_t A = qbuf + t * SH::TILE, B = slot(i), id = idesc(FT, w, false);
+      if (lane == 0)
+#pragma unroll 1
+        for (int k = 0; k < ksteps; ++k) {
+          const uint32_t off = (k >> 2) * PANEL + (k & 3) * 32;
+          tc::mma_bf16(tS[t], desc_k(A + off), desc_k(B + off), id, k > 0);
+        }
+    };
+    auto pv = [&](int t, int i, int w, bool acc) {
+      const uint32_t B = slot(i), id = idesc(FT, a.d, true);
+      if (lane == 0)
+#pragma unroll 1
+        for (int k = 0; k < w / 16; ++k)
+          mma_ts(tO[t], tS[t] + 8 * k, desc_mn(B + k * 2048, PANEL), id, acc || k > 0);
+    };
+    auto commit = [&](uint64_t* b) {
+      if (lane == 0) tc::commit(bar(b));
+      __syncwarp();
+    };
+    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      const FwdItem r = fwd_item(a, gm, it);
+      const int steps = r.ns + r.nw;
+      if (steps == 0) continue;
+      int left[2] = {0, 0};             // steps that the tile still takes part in
+#pragma unroll 1
+      for (int j = 0; j < steps; ++j) {
+        const FwdStep s = fwd_step(r, j);
+        left[0] += fwd_active(a, r.own[0], s);
+        left[1] += fwd_active(a, r.own[1], s);
+      }
+      int todo[2] = {left[0], left[1]};  // scores still to be issued
+      bool begun[2] = {false, false};
+      // scores of step j for tile t, when it takes part
+      auto scores = [&](int t, int j, int i) {
+        const FwdStep s = fwd_step(r, j);
+        if (!fwd_active(a, r.own[t], s)) return true;
+        if (todo[t] == left[t] && !begun[t] &&
+            !wait_warp(gm.err, bar(&qfull[t]), (uint32_t)nq[t]++ & 1u))
+          return false;
+        tc::fence_after();
+        qk(t, i, s.w);
+        commit(&sfull[t]);
+        if (--todo[t] == 0) commit(&qempty[t]);
+        return true;
+      };
+      const int n0 = n;                 // K of step j: n0 + 2 j, V: n0 + 2 j + 1
+      n += 2 * steps;
+      if (!take(n0) || !scores(0, 0, n0) || !scores(1, 0, n0)) { bad = true; break; }
+      commit(&empty[n0 % NST]);
+#pragma unroll 1
+      for (int j = 0; j < steps && !bad; ++j) {
+        const int iv = n0 + 2 * j + 1, ik = iv + 1;
+        const FwdStep s = fwd_step(r, j);
+        const bool more = j + 1 < steps;
+        if (!take(iv) || (more && !take(ik))) { bad = true; break; }
+        if (s.j0 + s.w > r.sq.len) {
+          // V rows at and behind the end: zeros (16 bytes per lane and turn)
+          const int r0 = r.sq.len - s.j0, c = (s.w - r0) * 8;
+#pragma unroll 1
+          for (int e = lane; e < c * NP; e += 32) {
+            const uint32_t dst = slot(iv) + (e / c) * PANEL + r0 * 128 + (e % c) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (bad) break;
+          if (fwd_active(a, r.own[t], s)) {
+            if (!wait_warp(gm.err, bar(&pfull[t]), (uint32_t)np[t]++ & 1u) ||
+                (!begun[t] && !wait_warp(gm.err, bar(&oempty[t]), ((uint32_t)no[t]++ & 1u) ^ 1u))) {
+              bad = true;
+              break;
+            }
+            tc::fence_after();
+            pv(t, iv, s.w, begun[t]);
+            begun[t] = true;
+            if (--left[t] == 0) commit(&ofull[t]);
+          }
+          if (more && !scores(t, j + 1, ik)) bad = true;
+        }
+        commit(&empty[iv % NST]);
+        if (more) commit(&empty[ik % NST]);
+      }
+    }
+    if (bad) {  // what was issued ends before tensor memory is freed
+      commit(&drain);
+      wait_warp(gm.err, bar(&drain), 0);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FREG_SOFTMAX));
+    // ---------------- softmax ----------------
+    const int t = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t S = (t ? tS[1] : tS[0]) + lanes, O = (t ? tO[1] : tO[0]) + lanes;
+    const float c = a.scale_log2;
+    int nsf = 0, nof = 0;
+    bool bad = false;
+    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      const FwdItem r = fwd_item(a, gm, it);
+      // (registers, not an indexed array)
+      const WinRange own = t ? r.own[1] : r.own[0];
+      const int i0 = t ? r.i0[1] : r.i0[0], i1 = t ? r.i1[1] : r.i1[0];
+      const int head = t ? r.head[1] : r.head[0];
+      const int steps = r.ns + r.nw, i = i0 + row;
+      WinRow wr = win_row(a, r.sq, i);
+      if (i >= i1) wr = WinRow{0, 0, 0};
+      // keys that every row of the tile sees: no mask
+      const int p0 = r.sq.qp + i0, p1 = r.sq.qp + i1 - 1;
+      const bool rows_ok = i1 - i0 == FT && p0 >= 0 && p1 < r.sq.len;
+      const int free_lo = p1 - a.left, free_hi = min(p0 + a.right, r.sq.len - 1);
+      float m = -INFINITY;
+      float l0 = 0.f, l1 = 0.f;
+      bool any = false;
+      for (int j = 0; j < steps; ++j) {
+        const FwdStep s = fwd_step(r, j);
+        if (!fwd_active(a, own, s)) continue;
+        if (!wait_warp(gm.err, bar(&sfull[t]), (uint32_t)nsf & 1u)) {
+          bad = true;
+          break;
+        }
+        ++nsf;
+        tc::fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ld32(S + 32 * q, v[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ld_wait(v[q]);
+        const bool whole = rows_ok && s.je - s.j0 == FT && s.j0 + FT - 1 <= free_hi &&
+                           (s.j0 >= free_lo || s.je <= a.sinks);
+        if (!whole) {
+          const int h = min(wr.hi, s.je) - s.j0, l = wr.lo - s.j0, z = wr.S - s.j0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t bits = seen_bits(l - 32 * q, h - 32 * q, z - 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1u)) v[q][e] = 0xff800000u;   // -inf
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx = fmaxf(fmaxf(mx, __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
+        const bool move = (mx - m) * c > kMoveMax || (m == -INFINITY && mx > m);
+        const float mn = move ? mx : m;
+        if (any && __any_sync(0xffffffffu, move)) {
+          const float f = move ? exp2_ftz((m - mn) * c) : 1.f;   // m = -inf: 0
+          l0 *= f;
+          l1 *= f;
+#pragma unroll 1
+          for (int q = 0; q < a.d; q += 16) {
+            uint32_t o[16];
+            tc::tmem_ld<16>(O + q, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            st16(O + q, o);
+          }
+        }
+        any = true;
+        m = mn;
+        const float off = m == -INFINITY ? 0.f : -m * c;
+        const f32x2 c2 = pack2(c, c), off2 = pack2(off, off);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, off2));
+            const float y0 = exp2_ftz(x.x), y1 = exp2_ftz(x.y);
+            l0 += y0;
+            l1 += y1;
+            p[e >> 1] = pack(y0, y1);
+          }
+          st16(S + 16 * q, p);
+        }
+        st_wait();
+        tc::fence_before();
+        arrive(bar(&pfull[t]));
+      }
+      if (bad) break;
+      const float l = l0 + l1;
+      if (i < i1 && a.lse)
+        a.lse[((size_t)r.b * a.Hq + head) * a.Nq + i] = l == 0.f ? -INFINITY : fmaf(m, c, log2f(l));
+      const float w = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      if (any) {
+        if (!wait_warp(gm.err, bar(&ofull[t]), (uint32_t)nof & 1u)) {
+          bad = true;
+          break;
+        }
+        ++nof;
+        tc::fence_after();
+      }
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.out +
+                           (((size_t)r.b * a.Hq + head) * a.Nq + i) * a.d;
+#pragma unroll 1
+      for (int q = 0; q < a.d; q += 16) {
+        uint32_t o[16];
+        if (any) {
+          tc::tmem_ld<16>(O + q, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0;
+        }
+        if (i >= i1) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(o[e + x]) * w;
+          *reinterpret_cast<uint4*>(dst + q + e) =
+              make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+        }
+      }
+      if (any) {
+        tc::fence_before();
+        arrive(bar(&oempty[t]));
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+// [B H][N][d] bf16, boxes of 64 features x `rows` rows
+bool win_map(CUtensorMap* t, const void* p, int BH, int N, int d, int rows) {
+  const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)BH};
+  const cuuint64_t stride[2] = {(cuuint64_t)d * 2, (cuuint64_t)N * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  return encode_tiled_bf16_sw128(t, 3, p, dim, stride, box);
+}
+
+namespace {
+template <int NP>
+cudaError_t fwd_go(const FwdMaps& mp, const WinArgs& a, const FwdGeom& gm, cudaStream_t st) {
+  constexpr size_t smem = FwdShape<NP>::SMEM;
+  cudaError_t e = allow_smem(k_win_fwd_tc<NP>, smem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(gm.items < sms ? gm.items : sms);
+  return launch("win_fwd_tc", k_win_fwd_tc<NP>, dim3(grid), dim3(FTH), smem, st, mp, a, gm);
+}
+}  // namespace
+
+cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st) {
+  FwdMaps mp;
+  FwdGeom gm;
+  gm.err = wait_error_address();
+  if (gm.err == nullptr) return cudaErrorInvalidSymbol;
+  gm.qt = (a.Nq + FT - 1) / FT;
+  gm.by_head = a.g % 2 == 0;
+  gm.npair = gm.by_head ? gm.qt : (gm.qt + 1) / 2;
+  gm.items = (long long)a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g) * gm.npair;
+  if (!win_map(&mp.q, a.q, a.B * a.Hq, a.Nq, a.d, FT) ||
+      !win_map(&mp.k, a.k, a.B * a.Hkv, a.Nk, a.d, FT) ||
+      !win_map(&mp.v, a.v, a.B * a.Hkv, a.Nk, a.d, FT) ||
+      !win_map(&mp.k16, a.k, a.B * a.Hkv, a.Nk, a.d, 16) ||
+      !win_map(&mp.v16, a.v, a.B * a.Hkv, a.Nk, a.d, 16))
+    return cudaErrorInvalidValue;
+  return a.d <= 64 ? fwd_go<1>(mp, a, gm, st) : fwd_go<2>(mp, a, gm, st);
+}
+
+}  // namespace lapnys

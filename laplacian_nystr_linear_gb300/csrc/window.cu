@@ -143,7 +143,8 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
     t.part_ml = (float2*)((uint8_t*)ws + w.ml);
     return status(run_token(t, dtype == LAPNYS_BF16, stream));
   }
-  return status(run_win_fwd(a, dtype == LAPNYS_BF16, stream));
+  if (dtype == LAPNYS_BF16) return status(run_win_fwd_tc(a, stream));
+  return status(run_win_fwd(a, false, stream));
 }
 
 int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
