@@ -304,15 +304,18 @@ int bwd_tc_splits(int BH, int m, int N);
 cudaError_t run_bwd_tc(const Prob& p, int mode, const BwdTcArgs& a, cudaStream_t st);
 
 // ---- windowed softmax attention and the 8-bit cache (win.cuh) --------------
-// tiles of queries and keys on the FP32 pipe
+// fp32: on the FP32 pipe, in tiles of win_tile_rows()
 int win_tile_rows();
-cudaError_t run_win_fwd(const WinArgs& a, bool bf16, cudaStream_t st);
-cudaError_t run_win_bwd(const WinArgs& a, bool bf16, cudaStream_t st);
+cudaError_t run_win_fwd(const WinArgs& a, cudaStream_t st);
+cudaError_t run_win_bwd(const WinArgs& a, cudaStream_t st);
 // dK, dV of the key tiles with first tokens, from their chunks' partials
 cudaError_t run_win_join(const WinArgs& a, int tile_rows, bool bf16, cudaStream_t st);
 
 // the forward on the tensor cores, bf16
 cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st);
+// and the backward (partials of key tiles of win_tc_tile_rows())
+int win_tc_tile_rows();
+cudaError_t run_win_bwd_tc(const WinArgs& a, cudaStream_t st);
 bool win_map(CUtensorMap* t, const void* p, int BH, int N, int d, int rows);
 
 // a few queries per sequence, the keys split over blocks; table null: plain

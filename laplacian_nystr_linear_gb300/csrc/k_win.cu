@@ -1,5 +1,5 @@
-// Windowed softmax attention on the FP32 pipe (visibility rule: win.cuh):
-// forward, query gradients, key and value gradients.
+// Windowed softmax attention of fp32 tensors on the FP32 pipe (visibility rule:
+// win.cuh): forward, query gradients, key and value gradients.
 //
 //   s = scale q.k over the visible keys, P = softmax(s), o = P v
 //   D = dout.o, dV = P^T dout, dP = dout V^T, dS = P (dP - D),
@@ -24,8 +24,8 @@ constexpr int WPS = WT + 4;   // row stride of the P tiles
 
 // rows [r0, r1) (r1 - r0 <= 64) of a row-major [..][d] matrix into a padded
 // tile of 64 rows x DP columns, zeros elsewhere
-template <int DP, typename T>
-__device__ __forceinline__ void win_load(float* s, const T* g, int d, int r0, int r1) {
+template <int DP>
+__device__ __forceinline__ void win_load(float* s, const float* g, int d, int r0, int r1) {
   constexpr int C4 = DP / 4;
   for (int id = threadIdx.x; id < WT * C4; id += kThreads) {
     const int r = id / C4, c = (id % C4) * 4;
@@ -101,7 +101,7 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 }  // namespace
 
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_fwd(WinArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(kThreads) k_win_fwd(WinArgs a) {
   const WinSeq sq = win_seq(a, b);
   const WinRange kr = win_keys(a, sq, i0, i1);
   const size_t kv0 = ((size_t)b * a.Hkv + h / a.g) * a.Nk * a.d;
-  const T* K = (const T*)a.k + kv0;
-  const T* V = (const T*)a.v + kv0;
+  const float* K = (const float*)a.k + kv0;
+  const float* V = (const float*)a.v + kv0;
   const size_t q0 = ((size_t)b * a.Hq + h) * a.Nq;
-  win_load<DP>(Qs, (const T*)a.q + q0 * a.d, a.d, i0, i1);
+  win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i0, i1);
 
   WinRow row[4];
   float m[4], l[4];
@@ -180,14 +180,14 @@ __global__ void __launch_bounds__(kThreads) k_win_fwd(WinArgs a) {
     for (int u = 0; u < DP / 64; ++u) {
       const int c = 4 * tx + 64 * u;
       if (c < a.d)
-        st4((T*)a.out + (q0 + i) * a.d + c,
+        st4((float*)a.out + (q0 + i) * a.d + c,
             make_float4(o[r][u].x * w, o[r][u].y * w, o[r][u].z * w, o[r][u].w * w));
     }
   }
 }
 
 // dQ of one tile of queries, and D = dout.o of its rows for the kernel below
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -202,11 +202,11 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
   const WinSeq sq = win_seq(a, b);
   const WinRange kr = win_keys(a, sq, i0, i1);
   const size_t kv0 = ((size_t)b * a.Hkv + h / a.g) * a.Nk * a.d;
-  const T* K = (const T*)a.k + kv0;
-  const T* V = (const T*)a.v + kv0;
+  const float* K = (const float*)a.k + kv0;
+  const float* V = (const float*)a.v + kv0;
   const size_t q0 = ((size_t)b * a.Hq + h) * a.Nq;
-  win_load<DP>(Qs, (const T*)a.q + q0 * a.d, a.d, i0, i1);
-  win_load<DP>(Os, (const T*)a.dout + q0 * a.d, a.d, i0, i1);
+  win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i0, i1);
+  win_load<DP>(Os, (const float*)a.dout + q0 * a.d, a.d, i0, i1);
 
   WinRow row[4];
   float ls[4], D[4];
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
       o[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
       const int c = 4 * tx + 64 * u;
       if (i < i1 && c < a.d) {
-        const float4 x = ld4((const T*)a.dout + (q0 + i) * a.d + c);
-        const float4 y = ld4((const T*)a.out + (q0 + i) * a.d + c);
+        const float4 x = ld4((const float*)a.dout + (q0 + i) * a.d + c);
+        const float4 y = ld4((const float*)a.out + (q0 + i) * a.d + c);
         s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
       }
     }
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
     for (int u = 0; u < DP / 64; ++u) {
       const int c = 4 * tx + 64 * u;
       if (c < a.d)
-        st4((T*)a.dq + (q0 + i) * a.d + c,
+        st4((float*)a.dq + (q0 + i) * a.d + c,
             make_float4(o[r][u].x * a.scale, o[r][u].y * a.scale, o[r][u].z * a.scale,
                         o[r][u].w * a.scale));
     }
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
 // see it.  A tile that holds first tokens is seen by every later query: its
 // queries are cut into `chunks` ranges of `chunk_rows`, one block each, whose
 // fp32 partials k_win_join adds in their order.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
     i1 = min(i1, (c + 1) * a.chunk_rows);
   }
   const size_t kv0 = ((size_t)b * a.Hkv + hk) * a.Nk;
-  win_load<DP>(Ks, (const T*)a.k + kv0 * a.d, a.d, j0, j1);
-  win_load<DP>(Vs, (const T*)a.v + kv0 * a.d, a.d, j0, j1);
+  win_load<DP>(Ks, (const float*)a.k + kv0 * a.d, a.d, j0, j1);
+  win_load<DP>(Vs, (const float*)a.v + kv0 * a.d, a.d, j0, j1);
   float4 dk[4][DP / 64], dv[4][DP / 64];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
     for (int i = i0; i < i1; i += WT) {
       const int ie = min(i1, i + WT);
       __syncthreads();
-      win_load<DP>(Qs, (const T*)a.q + q0 * a.d, a.d, i, ie);
-      win_load<DP>(Os, (const T*)a.dout + q0 * a.d, a.d, i, ie);
+      win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i, ie);
+      win_load<DP>(Os, (const float*)a.dout + q0 * a.d, a.d, i, ie);
       if (tid < WT) {
         Ls[tid] = i + tid < ie ? a.lse[q0 + i + tid] : 0.f;
         Ds[tid] = i + tid < ie ? a.D[q0 + i + tid] : 0.f;
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
         st4(p, x);
         st4(p + (size_t)WT * a.d, dv[r][u]);
       } else if (j < a.Nk) {
-        st4((T*)a.dk + (kv0 + j) * a.d + c, x);
-        st4((T*)a.dv + (kv0 + j) * a.d + c, dv[r][u]);
+        st4((float*)a.dk + (kv0 + j) * a.d + c, x);
+        st4((float*)a.dv + (kv0 + j) * a.d + c, dv[r][u]);
       }
     }
   }
@@ -389,29 +389,29 @@ __global__ void __launch_bounds__(256) k_win_join(WinArgs a, int tile_rows) {
 }
 
 namespace {
-template <typename T, int DP>
+template <int DP>
 cudaError_t fwd_t(const WinArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(3 * WT * row_stride(DP) + WT * WPS) * 4;
-  cudaError_t e = allow_smem(k_win_fwd<T, DP>, smem);
+  cudaError_t e = allow_smem(k_win_fwd<DP>, smem);
   if (e != cudaSuccess) return e;
   const long long n = (long long)a.B * a.Hq * ((a.Nq + WT - 1) / WT);
-  return launch("win_fwd", k_win_fwd<T, DP>, dim3((unsigned)n), dim3(kThreads), smem, st, a);
+  return launch("win_fwd", k_win_fwd<DP>, dim3((unsigned)n), dim3(kThreads), smem, st, a);
 }
-template <typename T, int DP>
+template <int DP>
 cudaError_t bwd_t(const WinArgs& a, cudaStream_t st) {
   const size_t sq = (size_t)(4 * WT * row_stride(DP) + WT * WPS) * 4;
   const size_t sk = (size_t)(4 * WT * row_stride(DP) + 2 * WT * WPS + 2 * WT) * 4;
   cudaError_t e;
-  if ((e = allow_smem(k_win_dq<T, DP>, sq)) != cudaSuccess) return e;
-  if ((e = allow_smem(k_win_dkv<T, DP>, sk)) != cudaSuccess) return e;
+  if ((e = allow_smem(k_win_dq<DP>, sq)) != cudaSuccess) return e;
+  if ((e = allow_smem(k_win_dkv<DP>, sk)) != cudaSuccess) return e;
   const long long nq = (long long)a.B * a.Hq * ((a.Nq + WT - 1) / WT);
-  e = launch("win_dq", k_win_dq<T, DP>, dim3((unsigned)nq), dim3(kThreads), sq, st, a);
+  e = launch("win_dq", k_win_dq<DP>, dim3((unsigned)nq), dim3(kThreads), sq, st, a);
   if (e != cudaSuccess) return e;
   const int kt = (a.Nk + WT - 1) / WT;
   const long long nk = (long long)a.B * a.Hkv * (a.stiles * a.chunks + kt - a.stiles);
-  e = launch("win_dkv", k_win_dkv<T, DP>, dim3((unsigned)nk), dim3(kThreads), sk, st, a);
+  e = launch("win_dkv", k_win_dkv<DP>, dim3((unsigned)nk), dim3(kThreads), sk, st, a);
   if (e != cudaSuccess || a.stiles == 0) return e;
-  return run_win_join(a, WT, sizeof(T) == 2, st);
+  return run_win_join(a, WT, false, st);
 }
 }  // namespace
 
@@ -425,16 +425,12 @@ cudaError_t run_win_join(const WinArgs& a, int tile_rows, bool bf16, cudaStream_
 
 int win_tile_rows() { return WT; }
 
-cudaError_t run_win_fwd(const WinArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16)
-    return a.d <= 64 ? fwd_t<__nv_bfloat16, 64>(a, st) : fwd_t<__nv_bfloat16, 128>(a, st);
-  return a.d <= 64 ? fwd_t<float, 64>(a, st) : fwd_t<float, 128>(a, st);
+cudaError_t run_win_fwd(const WinArgs& a, cudaStream_t st) {
+  return a.d <= 64 ? fwd_t<64>(a, st) : fwd_t<128>(a, st);
 }
 
-cudaError_t run_win_bwd(const WinArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16)
-    return a.d <= 64 ? bwd_t<__nv_bfloat16, 64>(a, st) : bwd_t<__nv_bfloat16, 128>(a, st);
-  return a.d <= 64 ? bwd_t<float, 64>(a, st) : bwd_t<float, 128>(a, st);
+cudaError_t run_win_bwd(const WinArgs& a, cudaStream_t st) {
+  return a.d <= 64 ? bwd_t<64>(a, st) : bwd_t<128>(a, st);
 }
 
 }  // namespace lapnys

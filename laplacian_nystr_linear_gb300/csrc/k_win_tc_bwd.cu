@@ -1,0 +1,849 @@
+// Windowed softmax attention, backward, bf16, on the tcgen05 tensor cores
+// (visibility rule: win.cuh; operand tiles: win_tc.cuh; formulas: k_win.cu).
+//
+// Two kernels, so that every sum has one owner and one order (deterministic, no
+// atomics): scores are computed in both, 7 products of 128 x 128 x d per tile of
+// pairs instead of 5.
+//   k_win_dq_tc   128 queries stay, keys in steps of 128:
+//                 S = Q K^T, dP = dO V^T, dS = P (dP - D) as bf16, dQ += dS K
+//   k_win_dkv_tc  128 keys stay, the queries of the group's heads in steps of
+//                 128: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+// with P = exp2(scale log2(e) s - lse) from the forward's log-sum.  The bf16
+// tile that was just computed is the left operand of its product, from tensor
+// memory, over the columns it came from; K, Q, dO tiles are read as they lie in
+// shared memory both K-major (scores) and MN-major (gradients).
+//
+//   warps 0-7   elementwise work, one row and half of the columns per thread
+//               (columns of the other half are read before either overwrites
+//               them: one barrier of the 256 threads);
+//   warp 8      TMA (the resident tiles, and two rings);
+//   warp 9      issues the products, in an order that keeps the tensor pipe busy
+//               while the elementwise warps work on the other product:
+//                 dq:   dP(j+1) dQ(j) S(j+2)    (S in two buffers)
+//                 dkv:  dV(j) S(j+1) dK(j) dP(j+1)
+//   warp 10     dkv: log-sum and D of a step's queries into shared memory.
+//
+// Key tiles with first tokens are seen by all later queries: their queries are
+// cut into chunks, one item each, with fp32 partials that k_win_join adds.
+// Rows behind a sequence's end are zeroed in shared memory where they are
+// summed over (0 * NaN).  Every wait is bounded.
+#include <cstring>
+
+#include "internal.h"
+#include "win_tc.cuh"
+
+namespace lapnys {
+
+namespace {
+using namespace wtc;
+constexpr int BT = 128;                 // rows and columns of a tile
+constexpr int BTH = 384;
+// registers a thread: 256 * 208 + 128 * 88 <= 384 * 168, the launch's share
+constexpr int BREG_EW = 208, BREG_ISSUE = 88;
+constexpr uint32_t PANEL = BT * 128;
+constexpr int NRING1 = 3, NRING2 = 2;   // tiles of the rings (K, V; Q, dO)
+template <int NP>
+struct BwdShape {
+  static constexpr uint32_t TILE = NP * PANEL;
+  static constexpr uint32_t SMEM = (2 + NRING1 + NRING2) * TILE + 1024;
+};
+struct BwdMaps {
+  CUtensorMap q, k, v, dout;              // boxes of 64 x 128
+  CUtensorMap q16, k16, v16, dout16;      // boxes of 64 x 16 for narrow steps
+};
+struct BwdGeom {
+  int tiles;                              // query tiles (dq); key items of a head (dkv)
+  long long items;
+  int* err;
+};
+
+// barrier of the 256 elementwise threads; `ok` of all of them
+__device__ __forceinline__ bool ew_sync_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, 1, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void ew_sync() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
+
+// a tile of w rows (a multiple of 16) from row r0 of head bh
+template <int NP>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* wide,
+                                          const CUtensorMap* narrow, int r0, int w, int bh,
+                                          uint32_t bar) {
+#pragma unroll 1
+  for (int p = 0; p < NP; ++p) {
+    if (w == BT) {
+      tma3(dst + p * PANEL, wide, 64 * p, r0, bh, bar);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < w; r += 16) tma3(dst + p * PANEL + r * 128, narrow, 64 * p, r0 + r, bh, bar);
+    }
+  }
+}
+// rows [r0, w) of a tile to zero, by one warp
+template <int NP>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int w, int lane) {
+  const int c = (w - r0) * 8;
+#pragma unroll 1
+  for (int e = lane; e < c * NP; e += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (e / c) * PANEL + r0 * 128 +
+                                                                  (e % c) * 16),
+                 "r"(0)
+                 : "memory");
+}
+// D = A B^T over the features, both from shared memory
+__device__ __forceinline__ void mma_features(uint32_t d, uint32_t A, uint32_t B, int ksteps, uint32_t id) {
+#pragma unroll 1
+  for (int k = 0; k < ksteps; ++k) {
+    const uint32_t off = (k >> 2) * PANEL + (k & 3) * 32;
+    tc::mma_bf16(d, desc_k(A + off), desc_k(B + off), id, k > 0);
+  }
+}
+// D (+)= A B over B's w rows, A in tensor memory
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t A, uint32_t B, int w, uint32_t id, bool acc) {
+#pragma unroll 1
+  for (int k = 0; k < w / 16; ++k)
+    mma_ts(d, A + 8 * k, desc_mn(B + k * 2048, PANEL), id, acc || k > 0);
+}
+
+struct Step {
+  int r0, re, w;        // rows [r0, re) and the width of the products
+};
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+namespace {
+struct DqItem {
+  int b, h, i0, i1;
+  WinSeq sq;
+  WinRange kr;
+  int ns, steps;
+};
+__device__ __forceinline__ DqItem dq_item(const WinArgs& a, const BwdGeom& gm, long long it) {
+  DqItem r;
+  const int heads = a.B * a.Hq;
+  const int tile = gm.tiles - 1 - (int)(it / heads), h = (int)(it % heads);
+  r.b = h / a.Hq;
+  r.h = h % a.Hq;
+  r.i0 = tile * BT;
+  r.i1 = min(a.Nq, r.i0 + BT);
+  r.sq = win_seq(a, r.b);
+  r.kr = win_keys(a, r.sq, r.i0, r.i1);
+  r.ns = (r.kr.S + BT - 1) / BT;
+  r.steps = r.ns + (r.kr.hi - r.kr.lo + BT - 1) / BT;
+  return r;
+}
+__device__ __forceinline__ Step dq_step(const DqItem& r, int j) {
+  Step s;
+  const bool first = j < r.ns;
+  s.r0 = first ? j * BT : r.kr.lo + (j - r.ns) * BT;
+  s.re = min(first ? r.kr.S : r.kr.hi, s.r0 + BT);
+  s.w = (s.re - s.r0 + 15) & ~15;
+  return s;
+}
+}  // namespace
+
+template <int NP>
+__global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ BwdMaps mp,
+                                                      const WinArgs a, const BwdGeom gm) {
+  using SH = BwdShape<NP>;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t kfull[NRING1], kempty[NRING1], vfull[NRING2], vempty[NRING2];
+  __shared__ __align__(8) uint64_t qfull, qempty;       // Q and dO landed; their products done
+  __shared__ __align__(8) uint64_t sfull[2], dpfull, dsfull, ofull, oempty, drain;
+  __shared__ uint32_t tmem_s;
+  __shared__ float Dh[2][BT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t Qb = base, Ob = Qb + SH::TILE, Kr = Ob + SH::TILE, Vr = Kr + NRING1 * SH::TILE;
+  auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
+  if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
+  if (tid == 0) {
+    for (int i = 0; i < NRING1; ++i) {
+      tc::mbar_init(bar(&kfull[i]), 1);
+      tc::mbar_init(bar(&kempty[i]), 1);
+    }
+    for (int i = 0; i < NRING2; ++i) {
+      tc::mbar_init(bar(&vfull[i]), 1);
+      tc::mbar_init(bar(&vempty[i]), 1);
+    }
+    tc::mbar_init(bar(&qfull), 1);
+    tc::mbar_init(bar(&qempty), 1);
+    tc::mbar_init(bar(&sfull[0]), 1);
+    tc::mbar_init(bar(&sfull[1]), 1);
+    tc::mbar_init(bar(&dpfull), 1);
+    tc::mbar_init(bar(&dsfull), 256);
+    tc::mbar_init(bar(&ofull), 1);
+    tc::mbar_init(bar(&oempty), 256);
+    tc::mbar_init(bar(&drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_s;
+  // tensor memory: S (then dS) in two buffers, dP, dQ
+  const uint32_t tS = tmem, tP = tmem + 2 * BT, tO = tmem + 3 * BT;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BREG_ISSUE));
+    if (warp == 8 && lane == 0) {
+      // ---------------- TMA ----------------
+      int n = 0, nq = 0;
+      bool bad = false;
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DqItem r = dq_item(a, gm, it);
+        if (r.steps == 0) continue;
+        if (!wait_or_flag(gm.err, bar(&qempty), (nq & 1) ^ 1u)) break;
+        tc::mbar_expect_tx(bar(&qfull), 2 * SH::TILE);
+        const int bq = r.b * a.Hq + r.h, bk = r.b * a.Hkv + r.h / a.g;
+        load_rows<NP>(Qb, &mp.q, nullptr, r.i0, BT, bq, bar(&qfull));
+        load_rows<NP>(Ob, &mp.dout, nullptr, r.i0, BT, bq, bar(&qfull));
+        ++nq;
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j, ++n) {
+          const Step s = dq_step(r, j);
+          const int sk = n % NRING1, sv = n % NRING2;
+          if (!wait_or_flag(gm.err, bar(&kempty[sk]), ((n / NRING1) & 1) ^ 1u) ||
+              !wait_or_flag(gm.err, bar(&vempty[sv]), ((n / NRING2) & 1) ^ 1u)) {
+            bad = true;
+            break;
+          }
+          tc::mbar_expect_tx(bar(&kfull[sk]), (uint32_t)(NP * s.w * 128));
+          load_rows<NP>(Kr + sk * SH::TILE, &mp.k, &mp.k16, s.r0, s.w, bk, bar(&kfull[sk]));
+          tc::mbar_expect_tx(bar(&vfull[sv]), (uint32_t)(NP * s.w * 128));
+          load_rows<NP>(Vr + sv * SH::TILE, &mp.v, &mp.v16, s.r0, s.w, bk, bar(&vfull[sv]));
+        }
+      }
+      // every copy has landed before the block ends, also after an expired wait
+#pragma unroll 1
+      for (int i = n > NRING1 ? n - NRING1 : 0; i < n; ++i) {
+        wait_or_flag(gm.err, bar(&kfull[i % NRING1]), (uint32_t)(i / NRING1) & 1u);
+        if (i >= n - NRING2) wait_or_flag(gm.err, bar(&vfull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
+      }
+      if (nq) wait_or_flag(gm.err, bar(&qfull), (uint32_t)(nq - 1) & 1u);
+    } else if (warp == 9) {
+      // ---------------- products ----------------
+      int n = 0, nq = 0, no = 0;        // steps, items
+      bool bad = false;
+      const int ksteps = a.d / 16;
+      auto commit = [&](uint64_t* b) {
+        if (lane == 0) tc::commit(bar(b));
+        __syncwarp();
+      };
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DqItem r = dq_item(a, gm, it);
+        if (r.steps == 0) continue;
+        if (!wait_warp(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
+        const int n0 = n;
+        n += r.steps;
+        auto scores = [&](int j) {
+          const Step s = dq_step(r, j);
+          const int i = n0 + j, sk = i % NRING1;
+          const uint32_t K = Kr + sk * SH::TILE;
+          if (!wait_warp(gm.err, bar(&kfull[sk]), (uint32_t)(i / NRING1) & 1u)) return false;
+          if (s.r0 + s.w > r.sq.len) {
+            zero_rows<NP>(K, r.sq.len - s.r0, s.w, lane);
+            tc::fence_async_smem();
+            __syncwarp();
+          }
+          tc::fence_after();
+          if (lane == 0) mma_features(tS + (i & 1) * BT, Qb, K, ksteps, idesc(BT, s.w, false));
+          commit(&sfull[i & 1]);
+          return true;
+        };
+        auto grads = [&](int j) {
+          const Step s = dq_step(r, j);
+          const int i = n0 + j, sv = i % NRING2;
+          if (!wait_warp(gm.err, bar(&vfull[sv]), (uint32_t)(i / NRING2) & 1u)) return false;
+          tc::fence_after();
+          if (lane == 0)
+            mma_features(tP, Ob, Vr + sv * SH::TILE, ksteps, idesc(BT, s.w, false));
+          commit(&dpfull);
+          commit(&vempty[sv]);
+          if (j + 1 == r.steps) commit(&qempty);   // the last product that reads Q or dO
+          return true;
+        };
+        if (!scores(0) || !grads(0) || (r.steps > 1 && !scores(1))) { bad = true; break; }
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j) {
+          const Step s = dq_step(r, j);
+          const int i = n0 + j, sk = i % NRING1;
+          if (!wait_warp(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
+          if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
+          if (j == 0 && !wait_warp(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u)) { bad = true; break; }
+          tc::fence_after();
+          if (lane == 0)
+            mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w, idesc(BT, a.d, true), j > 0);
+          commit(&kempty[sk]);
+          if (j + 1 == r.steps) commit(&ofull);
+          if (j + 2 < r.steps && !scores(j + 2)) { bad = true; break; }
+        }
+      }
+      if (bad) {  // what was issued ends before tensor memory is freed
+        commit(&drain);
+        wait_warp(gm.err, bar(&drain), 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BREG_EW));
+    // ---------------- elementwise ----------------
+    const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const float c = a.scale_log2;
+    int n = 0, no = 0;
+    bool fine = true;                      // no wait of this warp has expired
+    for (long long it = blockIdx.x; it < gm.items; it += gridDim.x) {
+      const DqItem r = dq_item(a, gm, it);
+      const int i = r.i0 + row;
+      const size_t qrow = ((size_t)r.b * a.Hq + r.h) * a.Nq + i;
+      WinRow wr = win_row(a, r.sq, i);
+      // D = dout.out, half of the features each
+      float D = 0.f, lse = 0.f;
+      if (i < r.i1) {
+        lse = a.lse[qrow];
+        const int hd = a.d / 2;
+        const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + half * hd;
+        const __nv_bfloat16* y = (const __nv_bfloat16*)a.out + qrow * a.d + half * hd;
+#pragma unroll 4
+        for (int e = 0; e < hd; e += 8) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + e));
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(y + e));
+          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            D = fmaf(__uint_as_float(us[z] << 16), __uint_as_float(ws[z] << 16), D);
+            D = fmaf(__uint_as_float(us[z] & 0xffff0000u), __uint_as_float(ws[z] & 0xffff0000u), D);
+          }
+        }
+      }
+      Dh[half][row] = D;
+      ew_sync();
+      D = Dh[0][row] + Dh[1][row];
+      if (half == 0 && i < r.i1) a.D[qrow] = D;
+
+      const int p0 = r.sq.qp + r.i0, p1 = r.sq.qp + r.i1 - 1;
+      const bool rows_ok = r.i1 - r.i0 == BT && p0 >= 0 && p1 < r.sq.len;
+      const int free_lo = p1 - a.left, free_hi = min(p0 + a.right, r.sq.len - 1);
+#pragma unroll 1
+      for (int j = 0; j < r.steps; ++j, ++n) {
+        const Step s = dq_step(r, j);
+        const uint32_t S = tS + (n & 1) * BT + lanes, P = tP + lanes;
+        fine = wait_or_flag(gm.err, bar(&sfull[n & 1]), (uint32_t)(n >> 1) & 1u) && fine;
+        tc::fence_after();
+        uint32_t v[2][32];
+        ld32(S + c0, v[0]);
+        ld32(S + c0 + 32, v[1]);
+        ld_wait(v[0]);
+        ld_wait(v[1]);
+        tc::fence_before();
+        // both halves are read before dS is written over them
+        fine = ew_sync_all(fine);
+        if (!fine) break;
+        tc::fence_after();
+        const f32x2 c2 = pack2(c, c), o2 = pack2(-lse, -lse);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, o2));
+            v[q][e] = __float_as_uint(exp2_ftz(x.x));
+            v[q][e + 1] = __float_as_uint(exp2_ftz(x.y));
+          }
+        fine = wait_warp(gm.err, bar(&dpfull), (uint32_t)n & 1u);
+        tc::fence_after();
+        const bool whole = rows_ok && s.re - s.r0 == BT && s.r0 + BT - 1 <= free_hi &&
+                           (s.r0 >= free_lo || s.re <= a.sinks);
+        const int h = min(wr.hi, s.re) - s.r0 - c0, l = wr.lo - s.r0 - c0, z = wr.S - s.r0 - c0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t dp[32], o[16];
+          ld32(P + c0 + 32 * q, dp);
+          ld_wait(dp);
+          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, z - 32 * q);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x = __uint_as_float(v[q][e]) * (__uint_as_float(dp[e]) - D);
+            float y = __uint_as_float(v[q][e + 1]) * (__uint_as_float(dp[e + 1]) - D);
+            if (!whole) {
+              x = bits >> e & 1u ? x : 0.f;
+              y = bits >> (e + 1) & 1u ? y : 0.f;
+            }
+            o[e >> 1] = pack(x, y);
+          }
+          st16(S + c0 / 2 + 16 * q, o);
+        }
+        st_wait();
+        tc::fence_before();
+        arrive(bar(&dsfull));
+      }
+      // (uniform: also after the loop's break; and Dh is read before the next
+      // item writes it)
+      if (r.steps > 0) fine = wait_or_flag(gm.err, bar(&ofull), (uint32_t)no & 1u) && fine;
+      fine = ew_sync_all(fine);
+      if (!fine) break;
+      if (r.steps > 0) {
+        ++no;
+        tc::fence_after();
+      }
+      // d / 16 pieces of 16 columns, shared by the halves
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.dq + qrow * a.d;
+#pragma unroll 1
+      for (int q = 16 * half; q < a.d; q += 32) {
+        uint32_t o[16];
+        if (r.steps > 0) {
+          tc::tmem_ld<16>(tO + lanes + q, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0;
+        }
+        if (i >= r.i1) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(o[e + x]) * a.scale;
+          *reinterpret_cast<uint4*>(dst + q + e) =
+              make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+        }
+      }
+      if (r.steps > 0) {
+        tc::fence_before();
+        arrive(bar(&oempty));
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// dK, dV
+// ---------------------------------------------------------------------------
+namespace {
+struct DkvItem {
+  int b, hk, tile, chunk;       // chunk < 0: an ordinary tile
+  int j0, j1;                   // keys of the tile, of the sequence
+  int i0, i1;                   // queries
+  int per, steps;               // steps of one head, of all
+  WinSeq sq;
+};
+__device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const BwdGeom& gm, long long it) {
+  DkvItem r;
+  const int heads = a.B * a.Hkv;
+  const int t = (int)(it / heads), h = (int)(it % heads);
+  r.b = h / a.Hkv;
+  r.hk = h % a.Hkv;
+  const int nf = a.stiles * a.chunks;
+  r.chunk = t < nf ? t % a.chunks : -1;
+  r.tile = t < nf ? t / a.chunks : t - nf + a.stiles;
+  r.sq = win_seq(a, r.b);
+  r.j0 = r.tile * BT;
+  r.j1 = min(min(a.Nk, r.j0 + BT), r.sq.len);
+  win_queries(a, r.sq, r.j0, r.j1, &r.i0, &r.i1);
+  if (r.chunk >= 0) {
+    r.i0 = max(r.i0, r.chunk * a.chunk_rows);
+    r.i1 = min(r.i1, (r.chunk + 1) * a.chunk_rows);
+  }
+  r.per = r.i1 > r.i0 ? (r.i1 - r.i0 + BT - 1) / BT : 0;
+  r.steps = r.per * a.g;
+  return r;
+}
+// step j: rows of query head hk g + j / per
+__device__ __forceinline__ Step dkv_step(const DkvItem& r, int j) {
+  Step s;
+  s.r0 = r.i0 + (j % r.per) * BT;
+  s.re = min(r.i1, s.r0 + BT);
+  s.w = (s.re - s.r0 + 15) & ~15;
+  return s;
+}
+}  // namespace
+
+template <int NP>
+__global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ BwdMaps mp,
+                                                       const WinArgs a, const BwdGeom gm) {
+  using SH = BwdShape<NP>;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t qfull[NRING1], qempty[NRING1], ofull[NRING2], oempty[NRING2];
+  __shared__ __align__(8) uint64_t lfull[2], lempty[2];   // log-sums of a step
+  __shared__ __align__(8) uint64_t dfull, dempty;         // D of a step
+  __shared__ __align__(8) uint64_t kvfull, kvempty;       // K and V landed; their products done
+  __shared__ __align__(8) uint64_t sfull, pfull, dpfull, dsfull, gfull, gempty, drain;
+  __shared__ uint32_t tmem_s;
+  __shared__ __align__(16) float Ls[2][BT], Ds[BT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t Kb = base, Vb = Kb + SH::TILE, Qr = Vb + SH::TILE, Or = Qr + NRING1 * SH::TILE;
+  auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
+  if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
+  if (tid == 0) {
+    for (int i = 0; i < NRING1; ++i) {
+      tc::mbar_init(bar(&qfull[i]), 1);
+      tc::mbar_init(bar(&qempty[i]), 1);
+    }
+    for (int i = 0; i < NRING2; ++i) {
+      tc::mbar_init(bar(&ofull[i]), 1);
+      tc::mbar_init(bar(&oempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(&lfull[i]), 32);
+      tc::mbar_init(bar(&lempty[i]), 256);
+    }
+    tc::mbar_init(bar(&dfull), 32);
+    tc::mbar_init(bar(&dempty), 256);
+    tc::mbar_init(bar(&kvfull), 1);
+    tc::mbar_init(bar(&kvempty), 1);
+    tc::mbar_init(bar(&sfull), 1);
+    tc::mbar_init(bar(&pfull), 256);
+    tc::mbar_init(bar(&dpfull), 1);
+    tc::mbar_init(bar(&dsfull), 256);
+    tc::mbar_init(bar(&gfull), 1);
+    tc::mbar_init(bar(&gempty), 256);
+    tc::mbar_init(bar(&drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_s;
+  // tensor memory: S^T (then P^T), dP^T (then dS^T), dV, dK
+  const uint32_t tS = tmem, tP = tmem + BT, tV = tmem + 2 * BT, tK = tmem + 3 * BT;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BREG_ISSUE));
+    if (warp == 8 && lane == 0) {
+      // ---------------- TMA ----------------
+      int n = 0, nk = 0;
+      bool bad = false;
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DkvItem r = dkv_item(a, gm, it);
+        if (r.steps == 0) continue;
+        if (!wait_or_flag(gm.err, bar(&kvempty), (nk & 1) ^ 1u)) break;
+        tc::mbar_expect_tx(bar(&kvfull), 2 * SH::TILE);
+        const int bk = r.b * a.Hkv + r.hk;
+        load_rows<NP>(Kb, &mp.k, nullptr, r.j0, BT, bk, bar(&kvfull));
+        load_rows<NP>(Vb, &mp.v, nullptr, r.j0, BT, bk, bar(&kvfull));
+        ++nk;
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j, ++n) {
+          const Step s = dkv_step(r, j);
+          const int bq = r.b * a.Hq + r.hk * a.g + j / r.per;
+          const int sq = n % NRING1, so = n % NRING2;
+          if (!wait_or_flag(gm.err, bar(&qempty[sq]), ((n / NRING1) & 1) ^ 1u) ||
+              !wait_or_flag(gm.err, bar(&oempty[so]), ((n / NRING2) & 1) ^ 1u)) {
+            bad = true;
+            break;
+          }
+          tc::mbar_expect_tx(bar(&qfull[sq]), (uint32_t)(NP * s.w * 128));
+          load_rows<NP>(Qr + sq * SH::TILE, &mp.q, &mp.q16, s.r0, s.w, bq, bar(&qfull[sq]));
+          tc::mbar_expect_tx(bar(&ofull[so]), (uint32_t)(NP * s.w * 128));
+          load_rows<NP>(Or + so * SH::TILE, &mp.dout, &mp.dout16, s.r0, s.w, bq, bar(&ofull[so]));
+        }
+      }
+#pragma unroll 1
+      for (int i = n > NRING1 ? n - NRING1 : 0; i < n; ++i) {
+        wait_or_flag(gm.err, bar(&qfull[i % NRING1]), (uint32_t)(i / NRING1) & 1u);
+        if (i >= n - NRING2) wait_or_flag(gm.err, bar(&ofull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
+      }
+      if (nk) wait_or_flag(gm.err, bar(&kvfull), (uint32_t)(nk - 1) & 1u);
+    } else if (warp == 10) {
+      // ---------------- log-sums and D of the steps' queries ----------------
+      int n = 0;
+      bool bad = false;
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DkvItem r = dkv_item(a, gm, it);
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j, ++n) {
+          const Step s = dkv_step(r, j);
+          const size_t q0 = ((size_t)r.b * a.Hq + r.hk * a.g + j / r.per) * a.Nq;
+          float x[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = s.r0 + lane + 32 * e;
+            x[e] = i < s.re ? a.lse[q0 + i] : INFINITY;
+            y[e] = i < s.re ? a.D[q0 + i] : 0.f;
+          }
+          if (!wait_warp(gm.err, bar(&lempty[n & 1]), ((n >> 1) & 1) ^ 1u)) { bad = true; break; }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Ls[n & 1][lane + 32 * e] = x[e];
+          arrive(bar(&lfull[n & 1]));
+          if (!wait_warp(gm.err, bar(&dempty), ((uint32_t)n & 1u) ^ 1u)) { bad = true; break; }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Ds[lane + 32 * e] = y[e];
+          arrive(bar(&dfull));
+        }
+      }
+    } else if (warp == 9) {
+      // ---------------- products ----------------
+      int n = 0, nk = 0, ng = 0;
+      bool bad = false;
+      const int ksteps = a.d / 16;
+      auto commit = [&](uint64_t* b) {
+        if (lane == 0) tc::commit(bar(b));
+        __syncwarp();
+      };
+      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DkvItem r = dkv_item(a, gm, it);
+        if (r.steps == 0) continue;
+        if (!wait_warp(gm.err, bar(&kvfull), (uint32_t)nk++ & 1u)) { bad = true; break; }
+        const int n0 = n;
+        n += r.steps;
+        // rows behind the sequence's end: zeros
+        auto clean = [&](const Step& s, uint32_t tile) {
+          const int e = r.sq.len - r.sq.qp - s.r0;
+          if (s.w > e) {
+            zero_rows<NP>(tile, e, s.w, lane);
+            tc::fence_async_smem();
+            __syncwarp();
+          }
+        };
+        auto scores = [&](int j) {
+          const Step s = dkv_step(r, j);
+          const int i = n0 + j, sq = i % NRING1;
+          const uint32_t Q = Qr + sq * SH::TILE;
+          if (!wait_warp(gm.err, bar(&qfull[sq]), (uint32_t)(i / NRING1) & 1u)) return false;
+          clean(s, Q);
+          tc::fence_after();
+          if (lane == 0) mma_features(tS, Kb, Q, ksteps, idesc(BT, s.w, false));
+          commit(&sfull);
+          return true;
+        };
+        auto grads = [&](int j) {
+          const Step s = dkv_step(r, j);
+          const int i = n0 + j, so = i % NRING2;
+          const uint32_t O = Or + so * SH::TILE;
+          if (!wait_warp(gm.err, bar(&ofull[so]), (uint32_t)(i / NRING2) & 1u)) return false;
+          clean(s, O);
+          tc::fence_after();
+          if (lane == 0) mma_features(tP, Vb, O, ksteps, idesc(BT, s.w, false));
+          commit(&dpfull);
+          if (j + 1 == r.steps) commit(&kvempty);   // the last product that reads K or V
+          return true;
+        };
+        if (!scores(0) || !grads(0)) { bad = true; break; }
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j) {
+          const Step s = dkv_step(r, j);
+          const int i = n0 + j, sq = i % NRING1, so = i % NRING2;
+          if (!wait_warp(gm.err, bar(&pfull), (uint32_t)i & 1u) ||
+              (j == 0 && !wait_warp(gm.err, bar(&gempty), ((uint32_t)ng++ & 1u) ^ 1u))) {
+            bad = true;
+            break;
+          }
+          tc::fence_after();
+          const uint32_t id = idesc(BT, a.d, true);
+          if (lane == 0) mma_rows(tV, tS, Or + so * SH::TILE, s.w, id, j > 0);
+          commit(&oempty[so]);
+          if (j + 1 < r.steps && !scores(j + 1)) { bad = true; break; }
+          if (!wait_warp(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
+          tc::fence_after();
+          if (lane == 0) mma_rows(tK, tP, Qr + sq * SH::TILE, s.w, id, j > 0);
+          commit(&qempty[sq]);
+          if (j + 1 == r.steps) commit(&gfull);
+          if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
+        }
+      }
+      if (bad) {  // what was issued ends before tensor memory is freed
+        commit(&drain);
+        wait_warp(gm.err, bar(&drain), 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BREG_EW));
+    // ---------------- elementwise: rows are keys, columns queries ----------------
+    const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t S = tS + lanes, P = tP + lanes;
+    const float c = a.scale_log2;
+    int n = 0, ng = 0;
+    bool bad = false;
+    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      const DkvItem r = dkv_item(a, gm, it);
+      const int j = r.j0 + row;
+      // positions [pl, ph) see this key
+      int pl = j - a.right, ph = j < a.sinks ? r.sq.len : min(r.sq.len, j + a.left + 1);
+      if (j >= r.j1) ph = pl = -kWinUnbounded;
+      const bool keys_ok = r.j1 - r.j0 == BT;
+      const int all_lo = r.j0 + BT - 1 - a.right;
+      const int all_hi = r.j0 + BT <= a.sinks ? r.sq.len : min(r.sq.len, r.j0 + a.left + 1);
+#pragma unroll 1
+      for (int k = 0; k < r.steps; ++k, ++n) {
+        const Step s = dkv_step(r, k);
+        const int ps = r.sq.qp + s.r0;            // position of the step's first query
+        const bool whole = keys_ok && s.re - s.r0 == BT && ps >= all_lo && ps + BT <= all_hi;
+        const int l = pl - ps - c0, h = min(ph - ps, s.re - s.r0) - c0;
+        const float* L = &Ls[n & 1][c0];
+        const float* D = &Ds[c0];
+        bool ok = wait_or_flag(gm.err, bar(&lfull[n & 1]), (uint32_t)(n >> 1) & 1u);
+        ok = wait_or_flag(gm.err, bar(&sfull), (uint32_t)n & 1u) && ok;
+        tc::fence_after();
+        uint32_t v[2][32];
+        ld32(S + c0, v[0]);
+        ld32(S + c0 + 32, v[1]);
+        ld_wait(v[0]);
+        ld_wait(v[1]);
+        tc::fence_before();
+        if (!ew_sync_all(ok)) { bad = true; break; }   // read by all before P^T is written over it
+        tc::fence_after();
+        const f32x2 c2 = pack2(c, c);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[16];
+          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, 0);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 ls = lds4(L + 32 * q + e);
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])),
+                                          c2, pack2(-ls.x, -ls.y)));
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3])),
+                                          c2, pack2(-ls.z, -ls.w)));
+            float p[4] = {exp2_ftz(x.x), exp2_ftz(x.y), exp2_ftz(y.x), exp2_ftz(y.y)};
+            if (!whole)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) p[z] = bits >> (e + z) & 1u ? p[z] : 0.f;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[q][e + z] = __float_as_uint(p[z]);
+            o[e >> 1] = pack(p[0], p[1]);
+            o[(e >> 1) + 1] = pack(p[2], p[3]);
+          }
+          st16(S + c0 / 2 + 16 * q, o);
+        }
+        st_wait();
+        tc::fence_before();
+        arrive(bar(&pfull));
+        arrive(bar(&lempty[n & 1]));
+
+        ok = wait_or_flag(gm.err, bar(&dfull), (uint32_t)n & 1u);
+        ok = wait_or_flag(gm.err, bar(&dpfull), (uint32_t)n & 1u) && ok;
+        tc::fence_after();
+        uint32_t dp[2][32];
+        ld32(P + c0, dp[0]);
+        ld32(P + c0 + 32, dp[1]);
+        ld_wait(dp[0]);
+        ld_wait(dp[1]);
+        tc::fence_before();
+        if (!ew_sync_all(ok)) { bad = true; break; }
+        tc::fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[16];
+          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, 0);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 ds = lds4(D + 32 * q + e);
+            const float dd[4] = {ds.x, ds.y, ds.z, ds.w};
+            float x[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              x[z] = __uint_as_float(v[q][e + z]) * (__uint_as_float(dp[q][e + z]) - dd[z]);
+              if (!whole) x[z] = bits >> (e + z) & 1u ? x[z] : 0.f;
+            }
+            o[e >> 1] = pack(x[0], x[1]);
+            o[(e >> 1) + 1] = pack(x[2], x[3]);
+          }
+          st16(P + c0 / 2 + 16 * q, o);
+        }
+        st_wait();
+        tc::fence_before();
+        arrive(bar(&dsfull));
+        arrive(bar(&dempty));
+      }
+      if (bad) break;
+      if (r.steps > 0) {
+        if (!ew_sync_all(wait_or_flag(gm.err, bar(&gfull), (uint32_t)ng & 1u))) { bad = true; break; }
+        ++ng;
+        tc::fence_after();
+      }
+      // dK by the first half of the threads, dV by the second
+      const uint32_t G = (half ? tV : tK) + lanes;
+      const float f = half ? 1.f : a.scale;
+      const size_t krow = ((size_t)r.b * a.Hkv + r.hk) * a.Nk + j;
+      __nv_bfloat16* dst = (__nv_bfloat16*)(half ? a.dv : a.dk) + krow * a.d;
+      float* part = a.part + (((((size_t)r.b * a.Hkv + r.hk) * a.stiles + r.tile) * a.chunks +
+                               (r.chunk >= 0 ? r.chunk : 0)) * 2 + half) * BT * a.d + (size_t)row * a.d;
+#pragma unroll 1
+      for (int q = 0; q < a.d; q += 16) {
+        uint32_t o[16];
+        if (r.steps > 0) {
+          tc::tmem_ld<16>(G + q, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0;
+        }
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * f;
+        if (r.chunk >= 0) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) st4(part + q + e, make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+        } else if (j < a.Nk) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            *reinterpret_cast<uint4*>(dst + q + e) =
+                make_uint4(pack(x[e], x[e + 1]), pack(x[e + 2], x[e + 3]), pack(x[e + 4], x[e + 5]),
+                           pack(x[e + 6], x[e + 7]));
+        }
+      }
+      if (r.steps > 0) {
+        tc::fence_before();
+        arrive(bar(&gempty));
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+namespace {
+template <int NP>
+cudaError_t bwd_go(const BwdMaps& mp, const WinArgs& a, int* err, cudaStream_t st) {
+  constexpr size_t smem = BwdShape<NP>::SMEM;
+  cudaError_t e;
+  if ((e = allow_smem(k_win_dq_tc<NP>, smem)) != cudaSuccess) return e;
+  if ((e = allow_smem(k_win_dkv_tc<NP>, smem)) != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  BwdGeom gm;
+  gm.err = err;
+  gm.tiles = (a.Nq + BT - 1) / BT;
+  gm.items = (long long)a.B * a.Hq * gm.tiles;
+  e = launch("win_dq_tc", k_win_dq_tc<NP>, dim3((unsigned)(gm.items < sms ? gm.items : sms)),
+             dim3(BTH), smem, st, mp, a, gm);
+  if (e != cudaSuccess) return e;
+  gm.tiles = a.stiles * a.chunks + (a.Nk + BT - 1) / BT - a.stiles;
+  gm.items = (long long)a.B * a.Hkv * gm.tiles;
+  e = launch("win_dkv_tc", k_win_dkv_tc<NP>, dim3((unsigned)(gm.items < sms ? gm.items : sms)),
+             dim3(BTH), smem, st, mp, a, gm);
+  if (e != cudaSuccess || a.stiles == 0) return e;
+  return run_win_join(a, BT, true, st);
+}
+}  // namespace
+
+int win_tc_tile_rows() { return BT; }
+
+cudaError_t run_win_bwd_tc(const WinArgs& a, cudaStream_t st) {
+  int* err = wait_error_address();
+  if (err == nullptr) return cudaErrorInvalidSymbol;
+  BwdMaps mp;
+  const int bq = a.B * a.Hq, bk = a.B * a.Hkv;
+  if (!win_map(&mp.q, a.q, bq, a.Nq, a.d, BT) || !win_map(&mp.q16, a.q, bq, a.Nq, a.d, 16) ||
+      !win_map(&mp.dout, a.dout, bq, a.Nq, a.d, BT) || !win_map(&mp.dout16, a.dout, bq, a.Nq, a.d, 16) ||
+      !win_map(&mp.k, a.k, bk, a.Nk, a.d, BT) || !win_map(&mp.k16, a.k, bk, a.Nk, a.d, 16) ||
+      !win_map(&mp.v, a.v, bk, a.Nk, a.d, BT) || !win_map(&mp.v16, a.v, bk, a.Nk, a.d, 16))
+    return cudaErrorInvalidValue;
+  return a.d <= 64 ? bwd_go<1>(mp, a, err, st) : bwd_go<2>(mp, a, err, st);
+}
+
+}  // namespace lapnys

@@ -52,6 +52,9 @@ struct WinWs {
   size_t total;
 };
 
+// rows of the backward's key tiles: bf16 on the tensor cores, fp32 on the FP32 pipe
+int tile_rows(int dtype) { return dtype == LAPNYS_BF16 ? win_tc_tile_rows() : win_tile_rows(); }
+
 WinWs window_ws(const WinArgs& a, bool backward, int tile) {
   WinWs w;
   memset(&w, 0, sizeof(w));
@@ -116,7 +119,7 @@ size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int
   WinArgs a;
   memset(&a, 0, sizeof(a));
   if (check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, 1.f, dtype) != LAPNYS_OK) return 0;
-  return window_ws(a, backward != 0, win_tile_rows()).total;
+  return window_ws(a, backward != 0, tile_rows(dtype)).total;
 }
 
 int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
@@ -132,7 +135,7 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
       !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
     return LAPNYS_EINVAL;
-  const WinWs w = window_ws(a, false, win_tile_rows());
+  const WinWs w = window_ws(a, false, tile_rows(dtype));
   if (w.total > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
@@ -144,7 +147,7 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
     return status(run_token(t, dtype == LAPNYS_BF16, stream));
   }
   if (dtype == LAPNYS_BF16) return status(run_win_fwd_tc(a, stream));
-  return status(run_win_fwd(a, false, stream));
+  return status(run_win_fwd(a, stream));
 }
 
 int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
@@ -161,7 +164,7 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
   for (const void* p : all)
     if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
   if (!lse || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4)) return LAPNYS_EINVAL;
-  const WinWs w = window_ws(a, true, win_tile_rows());
+  const WinWs w = window_ws(a, true, tile_rows(dtype));
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = const_cast<void*>(out); a.dout = dout;
   a.lse = const_cast<float*>(lse); a.lens = lens; a.q_pos = q_pos;
@@ -169,7 +172,8 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
   a.D = (float*)((uint8_t*)ws + w.D);
   a.part = (float*)((uint8_t*)ws + w.part);
   a.stiles = w.stiles; a.chunks = w.chunks; a.chunk_rows = w.chunk_rows;
-  return status(run_win_bwd(a, dtype == LAPNYS_BF16, stream));
+  if (dtype == LAPNYS_BF16) return status(run_win_bwd_tc(a, stream));
+  return status(run_win_bwd(a, stream));
 }
 
 int lapnys_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale,
