@@ -15,7 +15,7 @@
 //                   relative rounding are as good there), so the outputs are
 //                   rescaled on few steps;
 //   warp 8          TMA: K and V tiles through one ring;
-//   warp 9          issues  S = Q K^T  (both operands in shared memory)  and
+//   warp 9          one thread issues  S = Q K^T  (both operands in shared memory)  and
 //                   O += P V  (P in tensor memory, V as it lies: MN-major):
 //                   PV0 QK0' PV1 QK1' ..., so one tile's softmax runs under the
 //                   other tile's products.  S of a step is complete only when
@@ -38,8 +38,8 @@ namespace {
 using namespace wtc;
 constexpr int FT = 128;                 // query rows of a tile, keys of a step
 constexpr int FTH = 384;                // three warpgroups: two of softmax, one that issues
-// registers a thread: 256 * 208 + 128 * 80 <= 384 * 168, the launch's share
-constexpr int FREG_SOFTMAX = 208, FREG_ISSUE = 88;
+// registers a thread: 256 * 200 + 128 * 104 <= 384 * 168, the launch's share
+constexpr int FREG_SOFTMAX = 200, FREG_ISSUE = 104;
 constexpr uint32_t PANEL = FT * 128;    // a panel: 128 rows of 64 features, 16 KB
 template <int NP>
 struct FwdShape {
@@ -211,36 +211,24 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       for (int t = 0; t < 2; ++t)
         if (nq[t]) wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)(nq[t] - 1) & 1u);
     }
-  } else if (warp == 9) {
+  } else if (warp == 9 && lane == 0) {
     // ---------------- products ----------------
     int n = 0;                          // ring tiles taken
     int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
     bool bad = false;
     const int ksteps = a.d / 16;
+    const uint32_t id_pv = idesc(FT, a.d, true);
     auto slot = [&](int i) { return ring + (i % NST) * SH::TILE; };
-    auto take = [&](int i) {            // the whole warp waits for ring tile i
-      return wait_warp(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
+    auto take = [&](int i) {            // ring tile i has landed
+      return wait_or_flag(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
     };
     auto qk = [&](int t, int i, int w) {
-      const uint32_t A = qbuf + t * SH::TILE, B = slot(i), id = idesc(FT, w, false);
-      if (lane == 0)
-#pragma unroll 1
-        for (int k = 0; k < ksteps; ++k) {
-          const uint32_t off = (k >> 2) * PANEL + (k & 3) * 32;
-          tc::mma_bf16(tS[t], desc_k(A + off), desc_k(B + off), id, k > 0);
-        }
+      mma_features<NP>(tS[t], qbuf + t * SH::TILE, slot(i), ksteps, idesc(FT, w, false));
     };
     auto pv = [&](int t, int i, int w, bool acc) {
-      const uint32_t B = slot(i), id = idesc(FT, a.d, true);
-      if (lane == 0)
-#pragma unroll 1
-        for (int k = 0; k < w / 16; ++k)
-          mma_ts(tO[t], tS[t] + 8 * k, desc_mn(B + k * 2048, PANEL), id, acc || k > 0);
+      mma_rows(tO[t], tS[t], slot(i), w / 16, id_pv, acc);
     };
-    auto commit = [&](uint64_t* b) {
-      if (lane == 0) tc::commit(bar(b));
-      __syncwarp();
-    };
+    auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
     for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const FwdItem r = fwd_item(a, gm, it);
       const int steps = r.ns + r.nw;
@@ -259,7 +247,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         const FwdStep s = fwd_step(r, j);
         if (!fwd_active(a, r.own[t], s)) return true;
         if (todo[t] == left[t] && !begun[t] &&
-            !wait_warp(gm.err, bar(&qfull[t]), (uint32_t)nq[t]++ & 1u))
+            !wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)nq[t]++ & 1u))
           return false;
         tc::fence_after();
         qk(t, i, s.w);
@@ -277,23 +265,15 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         const FwdStep s = fwd_step(r, j);
         const bool more = j + 1 < steps;
         if (!take(iv) || (more && !take(ik))) { bad = true; break; }
-        if (s.j0 + s.w > r.sq.len) {
-          // V rows at and behind the end: zeros (16 bytes per lane and turn)
-          const int r0 = r.sq.len - s.j0, c = (s.w - r0) * 8;
-#pragma unroll 1
-          for (int e = lane; e < c * NP; e += 32) {
-            const uint32_t dst = slot(iv) + (e / c) * PANEL + r0 * 128 + (e % c) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-          }
-          tc::fence_async_smem();
-          __syncwarp();
+        if (s.j0 + s.w > r.sq.len && r.sq.len < a.Nk) {
+          zero_rows<NP>(slot(iv), r.sq.len - s.j0, s.w);   // V rows at and behind the end
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (bad) break;
           if (fwd_active(a, r.own[t], s)) {
-            if (!wait_warp(gm.err, bar(&pfull[t]), (uint32_t)np[t]++ & 1u) ||
-                (!begun[t] && !wait_warp(gm.err, bar(&oempty[t]), ((uint32_t)no[t]++ & 1u) ^ 1u))) {
+            if (!wait_or_flag(gm.err, bar(&pfull[t]), (uint32_t)np[t]++ & 1u) ||
+                (!begun[t] && !wait_or_flag(gm.err, bar(&oempty[t]), ((uint32_t)no[t]++ & 1u) ^ 1u))) {
               bad = true;
               break;
             }
@@ -310,7 +290,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
     }
     if (bad) {  // what was issued ends before tensor memory is freed
       commit(&drain);
-      wait_warp(gm.err, bar(&drain), 0);
+      wait_or_flag(gm.err, bar(&drain), 0);
     }
   }
   } else {
@@ -337,7 +317,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       const bool rows_ok = i1 - i0 == FT && p0 >= 0 && p1 < r.sq.len;
       const int free_lo = p1 - a.left, free_hi = min(p0 + a.right, r.sq.len - 1);
       float m = -INFINITY;
-      float l0 = 0.f, l1 = 0.f;
+      f32x2 ls[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};   // sums of the row, four chains
       bool any = false;
       for (int j = 0; j < steps; ++j) {
         const FwdStep s = fwd_step(r, j);
@@ -365,18 +345,21 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
               if (!(bits >> e & 1u)) v[q][e] = 0xff800000u;   // -inf
           }
         }
-        float mx = -INFINITY;
+        float mq[4];                       // four chains: one is as long as its latencies
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+          mq[q] = fmaxf(__uint_as_float(v[q][0]), __uint_as_float(v[q][1]));
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mx = fmaxf(fmaxf(mx, __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
+          for (int e = 2; e < 32; e += 2)
+            mq[q] = fmaxf(fmaxf(mq[q], __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
+        }
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const bool move = (mx - m) * c > kMoveMax || (m == -INFINITY && mx > m);
         const float mn = move ? mx : m;
         if (any && __any_sync(0xffffffffu, move)) {
           const float f = move ? exp2_ftz((m - mn) * c) : 1.f;   // m = -inf: 0
-          l0 *= f;
-          l1 *= f;
+          ls[0] = mul2(ls[0], pack2(f, f));
+          ls[1] = mul2(ls[1], pack2(f, f));
 #pragma unroll 1
           for (int q = 0; q < a.d; q += 16) {
             uint32_t o[16];
@@ -397,8 +380,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
           for (int e = 0; e < 32; e += 2) {
             const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, off2));
             const float y0 = exp2_ftz(x.x), y1 = exp2_ftz(x.y);
-            l0 += y0;
-            l1 += y1;
+            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], pack2(y0, y1));
             p[e >> 1] = pack(y0, y1);
           }
           st16(S + 16 * q, p);
@@ -408,7 +390,8 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         arrive(bar(&pfull[t]));
       }
       if (bad) break;
-      const float l = l0 + l1;
+      const float2 la = unpack2(ls[0]), lb = unpack2(ls[1]);
+      const float l = (la.x + la.y) + (lb.x + lb.y);
       if (i < i1 && a.lse)
         a.lse[((size_t)r.b * a.Hq + head) * a.Nq + i] = l == 0.f ? -INFINITY : fmaf(m, c, log2f(l));
       const float w = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);

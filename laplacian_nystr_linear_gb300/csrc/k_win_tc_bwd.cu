@@ -17,7 +17,7 @@
 //               (columns of the other half are read before either overwrites
 //               them: one barrier of the 256 threads);
 //   warp 8      TMA (the resident tiles, and two rings);
-//   warp 9      issues the products, in an order that keeps the tensor pipe busy
+//   warp 9      one thread issues the products, in an order that keeps the tensor pipe busy
 //               while the elementwise warps work on the other product:
 //                 dq:   dP(j+1) dQ(j) S(j+2)    (S in two buffers)
 //                 dkv:  dV(j) S(j+1) dK(j) dP(j+1)
@@ -38,8 +38,6 @@ namespace {
 using namespace wtc;
 constexpr int BT = 128;                 // rows and columns of a tile
 constexpr int BTH = 384;
-// registers a thread: 256 * 208 + 128 * 88 <= 384 * 168, the launch's share
-constexpr int BREG_EW = 208, BREG_ISSUE = 88;
 constexpr uint32_t PANEL = BT * 128;
 constexpr int NRING1 = 3, NRING2 = 2;   // tiles of the rings (K, V; Q, dO)
 template <int NP>
@@ -85,32 +83,6 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* wide,
     }
   }
 }
-// rows [r0, w) of a tile to zero, by one warp
-template <int NP>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int w, int lane) {
-  const int c = (w - r0) * 8;
-#pragma unroll 1
-  for (int e = lane; e < c * NP; e += 32)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (e / c) * PANEL + r0 * 128 +
-                                                                  (e % c) * 16),
-                 "r"(0)
-                 : "memory");
-}
-// D = A B^T over the features, both from shared memory
-__device__ __forceinline__ void mma_features(uint32_t d, uint32_t A, uint32_t B, int ksteps, uint32_t id) {
-#pragma unroll 1
-  for (int k = 0; k < ksteps; ++k) {
-    const uint32_t off = (k >> 2) * PANEL + (k & 3) * 32;
-    tc::mma_bf16(d, desc_k(A + off), desc_k(B + off), id, k > 0);
-  }
-}
-// D (+)= A B over B's w rows, A in tensor memory
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t A, uint32_t B, int w, uint32_t id, bool acc) {
-#pragma unroll 1
-  for (int k = 0; k < w / 16; ++k)
-    mma_ts(d, A + 8 * k, desc_mn(B + k * 2048, PANEL), id, acc || k > 0);
-}
-
 struct Step {
   int r0, re, w;        // rows [r0, re) and the width of the products
 };
@@ -193,7 +165,6 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   const uint32_t tS = tmem, tP = tmem + 2 * BT, tO = tmem + 3 * BT;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BREG_ISSUE));
     if (warp == 8 && lane == 0) {
       // ---------------- TMA ----------------
       int n = 0, nq = 0;
@@ -229,43 +200,37 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         if (i >= n - NRING2) wait_or_flag(gm.err, bar(&vfull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
       }
       if (nq) wait_or_flag(gm.err, bar(&qfull), (uint32_t)(nq - 1) & 1u);
-    } else if (warp == 9) {
+    } else if (warp == 9 && lane == 0) {
       // ---------------- products ----------------
       int n = 0, nq = 0, no = 0;        // steps, items
       bool bad = false;
       const int ksteps = a.d / 16;
-      auto commit = [&](uint64_t* b) {
-        if (lane == 0) tc::commit(bar(b));
-        __syncwarp();
-      };
+      auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
       for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DqItem r = dq_item(a, gm, it);
         if (r.steps == 0) continue;
-        if (!wait_warp(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
+        if (!wait_or_flag(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
         const int n0 = n;
         n += r.steps;
         auto scores = [&](int j) {
           const Step s = dq_step(r, j);
           const int i = n0 + j, sk = i % NRING1;
           const uint32_t K = Kr + sk * SH::TILE;
-          if (!wait_warp(gm.err, bar(&kfull[sk]), (uint32_t)(i / NRING1) & 1u)) return false;
-          if (s.r0 + s.w > r.sq.len) {
-            zero_rows<NP>(K, r.sq.len - s.r0, s.w, lane);
-            tc::fence_async_smem();
-            __syncwarp();
+          if (!wait_or_flag(gm.err, bar(&kfull[sk]), (uint32_t)(i / NRING1) & 1u)) return false;
+          if (s.r0 + s.w > r.sq.len && r.sq.len < a.Nk) {
+            zero_rows<NP>(K, r.sq.len - s.r0, s.w);
           }
           tc::fence_after();
-          if (lane == 0) mma_features(tS + (i & 1) * BT, Qb, K, ksteps, idesc(BT, s.w, false));
+          mma_features<NP>(tS + (i & 1) * BT, Qb, K, ksteps, idesc(BT, s.w, false));
           commit(&sfull[i & 1]);
           return true;
         };
         auto grads = [&](int j) {
           const Step s = dq_step(r, j);
           const int i = n0 + j, sv = i % NRING2;
-          if (!wait_warp(gm.err, bar(&vfull[sv]), (uint32_t)(i / NRING2) & 1u)) return false;
+          if (!wait_or_flag(gm.err, bar(&vfull[sv]), (uint32_t)(i / NRING2) & 1u)) return false;
           tc::fence_after();
-          if (lane == 0)
-            mma_features(tP, Ob, Vr + sv * SH::TILE, ksteps, idesc(BT, s.w, false));
+          mma_features<NP>(tP, Ob, Vr + sv * SH::TILE, ksteps, idesc(BT, s.w, false));
           commit(&dpfull);
           commit(&vempty[sv]);
           if (j + 1 == r.steps) commit(&qempty);   // the last product that reads Q or dO
@@ -276,12 +241,11 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         for (int j = 0; j < r.steps; ++j) {
           const Step s = dq_step(r, j);
           const int i = n0 + j, sk = i % NRING1;
-          if (!wait_warp(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
+          if (!wait_or_flag(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
           if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
-          if (j == 0 && !wait_warp(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u)) { bad = true; break; }
+          if (j == 0 && !wait_or_flag(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u)) { bad = true; break; }
           tc::fence_after();
-          if (lane == 0)
-            mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w, idesc(BT, a.d, true), j > 0);
+          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, idesc(BT, a.d, true), j > 0);
           commit(&kempty[sk]);
           if (j + 1 == r.steps) commit(&ofull);
           if (j + 2 < r.steps && !scores(j + 2)) { bad = true; break; }
@@ -289,11 +253,10 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       }
       if (bad) {  // what was issued ends before tensor memory is freed
         commit(&drain);
-        wait_warp(gm.err, bar(&drain), 0);
+        wait_or_flag(gm.err, bar(&drain), 0);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BREG_EW));
     // ---------------- elementwise ----------------
     const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -519,7 +482,6 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
   const uint32_t tS = tmem, tP = tmem + BT, tV = tmem + 2 * BT, tK = tmem + 3 * BT;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BREG_ISSUE));
     if (warp == 8 && lane == 0) {
       // ---------------- TMA ----------------
       int n = 0, nk = 0;
@@ -582,38 +544,33 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           arrive(bar(&dfull));
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == 9 && lane == 0) {
       // ---------------- products ----------------
       int n = 0, nk = 0, ng = 0;
       bool bad = false;
       const int ksteps = a.d / 16;
-      auto commit = [&](uint64_t* b) {
-        if (lane == 0) tc::commit(bar(b));
-        __syncwarp();
-      };
+      auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
       for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DkvItem r = dkv_item(a, gm, it);
         if (r.steps == 0) continue;
-        if (!wait_warp(gm.err, bar(&kvfull), (uint32_t)nk++ & 1u)) { bad = true; break; }
+        if (!wait_or_flag(gm.err, bar(&kvfull), (uint32_t)nk++ & 1u)) { bad = true; break; }
         const int n0 = n;
         n += r.steps;
         // rows behind the sequence's end: zeros
         auto clean = [&](const Step& s, uint32_t tile) {
           const int e = r.sq.len - r.sq.qp - s.r0;
-          if (s.w > e) {
-            zero_rows<NP>(tile, e, s.w, lane);
-            tc::fence_async_smem();
-            __syncwarp();
+          if (s.w > e && r.sq.len - r.sq.qp < a.Nq) {
+            zero_rows<NP>(tile, e, s.w);
           }
         };
         auto scores = [&](int j) {
           const Step s = dkv_step(r, j);
           const int i = n0 + j, sq = i % NRING1;
           const uint32_t Q = Qr + sq * SH::TILE;
-          if (!wait_warp(gm.err, bar(&qfull[sq]), (uint32_t)(i / NRING1) & 1u)) return false;
+          if (!wait_or_flag(gm.err, bar(&qfull[sq]), (uint32_t)(i / NRING1) & 1u)) return false;
           clean(s, Q);
           tc::fence_after();
-          if (lane == 0) mma_features(tS, Kb, Q, ksteps, idesc(BT, s.w, false));
+          mma_features<NP>(tS, Kb, Q, ksteps, idesc(BT, s.w, false));
           commit(&sfull);
           return true;
         };
@@ -621,10 +578,10 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           const Step s = dkv_step(r, j);
           const int i = n0 + j, so = i % NRING2;
           const uint32_t O = Or + so * SH::TILE;
-          if (!wait_warp(gm.err, bar(&ofull[so]), (uint32_t)(i / NRING2) & 1u)) return false;
+          if (!wait_or_flag(gm.err, bar(&ofull[so]), (uint32_t)(i / NRING2) & 1u)) return false;
           clean(s, O);
           tc::fence_after();
-          if (lane == 0) mma_features(tP, Vb, O, ksteps, idesc(BT, s.w, false));
+          mma_features<NP>(tP, Vb, O, ksteps, idesc(BT, s.w, false));
           commit(&dpfull);
           if (j + 1 == r.steps) commit(&kvempty);   // the last product that reads K or V
           return true;
@@ -634,19 +591,19 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         for (int j = 0; j < r.steps; ++j) {
           const Step s = dkv_step(r, j);
           const int i = n0 + j, sq = i % NRING1, so = i % NRING2;
-          if (!wait_warp(gm.err, bar(&pfull), (uint32_t)i & 1u) ||
-              (j == 0 && !wait_warp(gm.err, bar(&gempty), ((uint32_t)ng++ & 1u) ^ 1u))) {
+          if (!wait_or_flag(gm.err, bar(&pfull), (uint32_t)i & 1u) ||
+              (j == 0 && !wait_or_flag(gm.err, bar(&gempty), ((uint32_t)ng++ & 1u) ^ 1u))) {
             bad = true;
             break;
           }
           tc::fence_after();
           const uint32_t id = idesc(BT, a.d, true);
-          if (lane == 0) mma_rows(tV, tS, Or + so * SH::TILE, s.w, id, j > 0);
+          mma_rows(tV, tS, Or + so * SH::TILE, s.w / 16, id, j > 0);
           commit(&oempty[so]);
           if (j + 1 < r.steps && !scores(j + 1)) { bad = true; break; }
-          if (!wait_warp(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
+          if (!wait_or_flag(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
           tc::fence_after();
-          if (lane == 0) mma_rows(tK, tP, Qr + sq * SH::TILE, s.w, id, j > 0);
+          mma_rows(tK, tP, Qr + sq * SH::TILE, s.w / 16, id, j > 0);
           commit(&qempty[sq]);
           if (j + 1 == r.steps) commit(&gfull);
           if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
@@ -654,11 +611,10 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       }
       if (bad) {  // what was issued ends before tensor memory is freed
         commit(&drain);
-        wait_warp(gm.err, bar(&drain), 0);
+        wait_or_flag(gm.err, bar(&drain), 0);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BREG_EW));
     // ---------------- elementwise: rows are keys, columns queries ----------------
     const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;

@@ -60,6 +60,44 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
       : "memory");
 }
 
+// Products of one tile, issued by one thread.  Consecutive 16-deep slices differ
+// by a constant in the descriptors' address field (16-byte units), so the loops
+// are unrolled over one base: built anew per slice, the descriptors cost more
+// than the product (prompt of 32768 tokens, heads of 128: 820 us so).
+// D (+)= A B^T over d features, A and B in shared memory
+template <int NP>
+__device__ __forceinline__ void mma_features(uint32_t d_tmem, uint32_t A, uint32_t B, int ksteps,
+                                             uint32_t id) {
+  const uint64_t da = desc_k(A), db = desc_k(B);
+#pragma unroll
+  for (int k = 0; k < 4 * NP; ++k) {
+    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+    if (k < ksteps) tc::mma_bf16(d_tmem, da + off, db + off, id, k > 0);
+  }
+}
+// D (+)= A B over the `slices` 16-row slices of B, A in tensor memory
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t A, uint32_t B, int slices,
+                                         uint32_t id, bool acc) {
+  const uint64_t db = desc_mn(B, 16384);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < slices) mma_ts(d_tmem, A + 8 * k, db + 128 * k, id, acc || k > 0);
+}
+
+// rows [r0, w) of an NP-panel tile to zero, by the thread that issues the products
+template <int NP>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int w) {
+#pragma unroll 1
+  for (int r = r0; r < w; ++r)
+#pragma unroll
+    for (int e = 0; e < 8 * NP; ++e)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (e >> 3) * 16384 +
+                                                                    r * 128 + (e & 7) * 16),
+                   "r"(0)
+                   : "memory");
+  tc::fence_async_smem();
+}
+
 // 32 columns of this lane's row, not waited for: ld_wait makes them valid
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
@@ -105,6 +143,16 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
 }
 __device__ __forceinline__ void st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
