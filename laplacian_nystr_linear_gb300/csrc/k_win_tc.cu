@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FREG_ISSUE));
   if (warp == 8) {
     // ---------------- TMA ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int n = 0;                       // tiles issued to the ring
       int nq[2] = {0, 0};              // Q tiles issued
       bool bad = false;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       for (int t = 0; t < 2; ++t)
         if (nq[t]) wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)(nq[t] - 1) & 1u);
     }
-  } else if (warp == 9 && lane == 0) {
+  } else if (warp == 9 && elect_one()) {
     // ---------------- products ----------------
     int n = 0;                          // ring tiles taken
     int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};

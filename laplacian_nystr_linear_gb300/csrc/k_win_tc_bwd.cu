@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   const uint32_t tS = tmem, tP = tmem + 2 * BT, tO = tmem + 3 * BT;
 
   if (warp >= 8) {
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
       // ---------------- TMA ----------------
       int n = 0, nq = 0;
       bool bad = false;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         if (i >= n - NRING2) wait_or_flag(gm.err, bar(&vfull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
       }
       if (nq) wait_or_flag(gm.err, bar(&qfull), (uint32_t)(nq - 1) & 1u);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
       // ---------------- products ----------------
       int n = 0, nq = 0, no = 0;        // steps, items
       bool bad = false;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
   const uint32_t tS = tmem, tP = tmem + BT, tV = tmem + 2 * BT, tK = tmem + 3 * BT;
 
   if (warp >= 8) {
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
       // ---------------- TMA ----------------
       int n = 0, nk = 0;
       bool bad = false;
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           arrive(bar(&dfull));
         }
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
       // ---------------- products ----------------
       int n = 0, nk = 0, ng = 0;
       bool bad = false;

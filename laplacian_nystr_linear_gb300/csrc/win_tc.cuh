@@ -23,7 +23,18 @@ __device__ __forceinline__ bool wait_or_flag(int* err, uint32_t bar, uint32_t pa
   if (!ok) atomicOr(err, 1);
   return ok;
 }
-// the same for a whole warp, with one answer
+// true in one thread of the (converged) warp.  The compiler knows a branch on it
+// to hold one thread and keeps what it computes there in uniform registers, which
+// is where the products' and copies' descriptors have to be; behind `lane == 0` it
+// moves every operand there anew
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
+// wait_or_flag for a whole warp, with one answer
 __device__ __forceinline__ bool wait_warp(int* err, uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_or_flag(err, bar, parity));
 }
