@@ -13,9 +13,10 @@
 // memory, over the columns it came from; K, Q, dO tiles are read as they lie in
 // shared memory both K-major (scores) and MN-major (gradients).
 //
-//   warps 0-7   elementwise work, one row and half of the columns per thread
-//               (columns of the other half are read before either overwrites
-//               them: one barrier of the 256 threads);
+//   warps 0-7   elementwise work, one row and half of the columns per thread.
+//               Each half writes its bf16 values (32 columns) over its own 64
+//               columns, so the halves need no barrier and drift apart: one's
+//               exponentials run under the other's multiplications;
 //   warp 8      TMA (the resident tiles, and two rings);
 //   warp 9      one thread issues the products, in an order that keeps the tensor pipe busy
 //               while the elementwise warps work on the other product:
@@ -51,22 +52,9 @@ struct BwdMaps {
 };
 struct BwdGeom {
   int tiles;                              // query tiles (dq); key items of a head (dkv)
-  long long items;
+  int items;
   int* err;
 };
-
-// barrier of the 256 elementwise threads; `ok` of all of them
-__device__ __forceinline__ bool ew_sync_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, 1, 256, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void ew_sync() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
 
 // a tile of w rows (a multiple of 16) from row r0 of head bh
 template <int NP>
@@ -86,6 +74,29 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* wide,
 struct Step {
   int r0, re, w;        // rows [r0, re) and the width of the products
 };
+
+// dS = P (dP - D) of 32 columns to tensor memory; not whole: only where `bits`
+// are set (a select, not a product: what is not seen may be anything)
+__device__ __forceinline__ void ds_store(uint32_t dst, const uint32_t (&p)[32],
+                                         const uint32_t (&dp)[32], f32x2 minus_D, bool whole,
+                                         uint32_t bits) {
+  uint32_t o[16];
+  float x[32];
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float2 y = unpack2(mul2(pack2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])),
+                                  add2(pack2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), minus_D)));
+    x[e] = y.x;
+    x[e + 1] = y.y;
+  }
+  if (!whole) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1u ? x[e] : 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(x[e], x[e + 1]);
+  st16(dst, o);
+}
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -98,10 +109,10 @@ struct DqItem {
   WinRange kr;
   int ns, steps;
 };
-__device__ __forceinline__ DqItem dq_item(const WinArgs& a, const BwdGeom& gm, long long it) {
+__device__ __forceinline__ DqItem dq_item(const WinArgs& a, const BwdGeom& gm, int it) {
   DqItem r;
   const int heads = a.B * a.Hq;
-  const int tile = gm.tiles - 1 - (int)(it / heads), h = (int)(it % heads);
+  const int tile = gm.tiles - 1 - it / heads, h = it % heads;
   r.b = h / a.Hq;
   r.h = h % a.Hq;
   r.i0 = tile * BT;
@@ -130,6 +141,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   __shared__ __align__(8) uint64_t kfull[NRING1], kempty[NRING1], vfull[NRING2], vempty[NRING2];
   __shared__ __align__(8) uint64_t qfull, qempty;       // Q and dO landed; their products done
   __shared__ __align__(8) uint64_t sfull[2], dpfull, dsfull, ofull, oempty, drain;
+  __shared__ __align__(8) uint64_t dhfull;              // both halves of D written
   __shared__ uint32_t tmem_s;
   __shared__ float Dh[2][BT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -150,6 +162,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
     tc::mbar_init(bar(&qempty), 1);
     tc::mbar_init(bar(&sfull[0]), 1);
     tc::mbar_init(bar(&sfull[1]), 1);
+    tc::mbar_init(bar(&dhfull), 256);
     tc::mbar_init(bar(&dpfull), 1);
     tc::mbar_init(bar(&dsfull), 256);
     tc::mbar_init(bar(&ofull), 1);
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       // ---------------- TMA ----------------
       int n = 0, nq = 0;
       bool bad = false;
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DqItem r = dq_item(a, gm, it);
         if (r.steps == 0) continue;
         if (!wait_or_flag(gm.err, bar(&qempty), (nq & 1) ^ 1u)) break;
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       bool bad = false;
       const int ksteps = a.d / 16;
       auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DqItem r = dq_item(a, gm, it);
         if (r.steps == 0) continue;
         if (!wait_or_flag(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
           if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
           if (j == 0 && !wait_or_flag(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u)) { bad = true; break; }
           tc::fence_after();
-          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, idesc(BT, a.d, true), j > 0);
+          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, idesc(BT, a.d, true), j > 0, 32);
           commit(&kempty[sk]);
           if (j + 1 == r.steps) commit(&ofull);
           if (j + 2 < r.steps && !scores(j + 2)) { bad = true; break; }
@@ -261,16 +274,16 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
     const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float c = a.scale_log2;
-    int n = 0, no = 0;
-    bool fine = true;                      // no wait of this warp has expired
-    for (long long it = blockIdx.x; it < gm.items; it += gridDim.x) {
+    int n = 0, no = 0, nd = 0;
+    bool bad = false;
+    for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const DqItem r = dq_item(a, gm, it);
       const int i = r.i0 + row;
       const size_t qrow = ((size_t)r.b * a.Hq + r.h) * a.Nq + i;
-      WinRow wr = win_row(a, r.sq, i);
+      const WinRow wr = win_row(a, r.sq, i);
       // D = dout.out, half of the features each
       float D = 0.f, lse = 0.f;
-      if (i < r.i1) {
+      if (i < r.i1 && r.steps > 0) {
         lse = a.lse[qrow];
         const int hd = a.d / 2;
         const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + half * hd;
@@ -287,31 +300,31 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
           }
         }
       }
-      Dh[half][row] = D;
-      ew_sync();
-      D = Dh[0][row] + Dh[1][row];
-      if (half == 0 && i < r.i1) a.D[qrow] = D;
+      if (r.steps > 0) {
+        // (written again for the next item only behind `ofull`, for which the other
+        // half has worked through this one's steps)
+        Dh[half][row] = D;
+        arrive(bar(&dhfull));
+        if (!wait_warp(gm.err, bar(&dhfull), (uint32_t)nd++ & 1u)) break;
+        D = Dh[0][row] + Dh[1][row];
+        if (half == 0 && i < r.i1) a.D[qrow] = D;
+      }
 
       const int p0 = r.sq.qp + r.i0, p1 = r.sq.qp + r.i1 - 1;
       const bool rows_ok = r.i1 - r.i0 == BT && p0 >= 0 && p1 < r.sq.len;
       const int free_lo = p1 - a.left, free_hi = min(p0 + a.right, r.sq.len - 1);
+      const f32x2 c2 = pack2(c, c), o2 = pack2(-lse, -lse), D2 = pack2(-D, -D);
 #pragma unroll 1
       for (int j = 0; j < r.steps; ++j, ++n) {
         const Step s = dq_step(r, j);
-        const uint32_t S = tS + (n & 1) * BT + lanes, P = tP + lanes;
-        fine = wait_or_flag(gm.err, bar(&sfull[n & 1]), (uint32_t)(n >> 1) & 1u) && fine;
+        const uint32_t S = tS + (n & 1) * BT + lanes + c0, P = tP + lanes + c0;
+        if (!wait_warp(gm.err, bar(&sfull[n & 1]), (uint32_t)(n >> 1) & 1u)) { bad = true; break; }
         tc::fence_after();
         uint32_t v[2][32];
-        ld32(S + c0, v[0]);
-        ld32(S + c0 + 32, v[1]);
+        ld32(S, v[0]);
+        ld32(S + 32, v[1]);
         ld_wait(v[0]);
         ld_wait(v[1]);
-        tc::fence_before();
-        // both halves are read before dS is written over them
-        fine = ew_sync_all(fine);
-        if (!fine) break;
-        tc::fence_after();
-        const f32x2 c2 = pack2(c, c), o2 = pack2(-lse, -lse);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -320,39 +333,25 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
             v[q][e] = __float_as_uint(exp2_ftz(x.x));
             v[q][e + 1] = __float_as_uint(exp2_ftz(x.y));
           }
-        fine = wait_warp(gm.err, bar(&dpfull), (uint32_t)n & 1u);
+        if (!wait_warp(gm.err, bar(&dpfull), (uint32_t)n & 1u)) { bad = true; break; }
         tc::fence_after();
+        uint32_t dp[2][32];
+        ld32(P, dp[0]);
+        ld32(P + 32, dp[1]);
         const bool whole = rows_ok && s.re - s.r0 == BT && s.r0 + BT - 1 <= free_hi &&
                            (s.r0 >= free_lo || s.re <= a.sinks);
         const int h = min(wr.hi, s.re) - s.r0 - c0, l = wr.lo - s.r0 - c0, z = wr.S - s.r0 - c0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t dp[32], o[16];
-          ld32(P + c0 + 32 * q, dp);
-          ld_wait(dp);
-          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, z - 32 * q);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x = __uint_as_float(v[q][e]) * (__uint_as_float(dp[e]) - D);
-            float y = __uint_as_float(v[q][e + 1]) * (__uint_as_float(dp[e + 1]) - D);
-            if (!whole) {
-              x = bits >> e & 1u ? x : 0.f;
-              y = bits >> (e + 1) & 1u ? y : 0.f;
-            }
-            o[e >> 1] = pack(x, y);
-          }
-          st16(S + c0 / 2 + 16 * q, o);
-        }
+        ld_wait(dp[0]);
+        ld_wait(dp[1]);
+        ds_store(S, v[0], dp[0], D2, whole, whole ? 0u : seen_bits(l, h, z));
+        ds_store(S + 16, v[1], dp[1], D2, whole, whole ? 0u : seen_bits(l - 32, h - 32, z - 32));
         st_wait();
         tc::fence_before();
         arrive(bar(&dsfull));
       }
-      // (uniform: also after the loop's break; and Dh is read before the next
-      // item writes it)
-      if (r.steps > 0) fine = wait_or_flag(gm.err, bar(&ofull), (uint32_t)no & 1u) && fine;
-      fine = ew_sync_all(fine);
-      if (!fine) break;
+      if (bad) break;
       if (r.steps > 0) {
+        if (!wait_warp(gm.err, bar(&ofull), (uint32_t)no & 1u)) break;
         ++no;
         tc::fence_after();
       }
@@ -400,10 +399,10 @@ struct DkvItem {
   int per, steps;               // steps of one head, of all
   WinSeq sq;
 };
-__device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const BwdGeom& gm, long long it) {
+__device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const BwdGeom& gm, int it) {
   DkvItem r;
   const int heads = a.B * a.Hkv;
-  const int t = (int)(it / heads), h = (int)(it % heads);
+  const int t = it / heads, h = it % heads;
   r.b = h / a.Hkv;
   r.hk = h % a.Hkv;
   const int nf = a.stiles * a.chunks;
@@ -421,14 +420,25 @@ __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const BwdGeom& gm,
   r.steps = r.per * a.g;
   return r;
 }
-// step j: rows of query head hk g + j / per
-__device__ __forceinline__ Step dkv_step(const DkvItem& r, int j) {
-  Step s;
-  s.r0 = r.i0 + (j % r.per) * BT;
-  s.re = min(r.i1, s.r0 + BT);
-  s.w = (s.re - s.r0 + 15) & ~15;
-  return s;
-}
+// the steps of an item in their order: rows of query head hk g + e
+struct StepWalk {
+  int e, r0;
+  __device__ __forceinline__ Step step(const DkvItem& r) const {
+    Step s;
+    s.r0 = r0;
+    s.re = min(r.i1, r0 + BT);
+    s.w = (s.re - r0 + 15) & ~15;
+    return s;
+  }
+  __device__ __forceinline__ void next(const DkvItem& r) {
+    r0 += BT;
+    if (r0 >= r.i1) {
+      r0 = r.i0;
+      ++e;
+    }
+  }
+};
+__device__ __forceinline__ StepWalk dkv_walk(const DkvItem& r) { return StepWalk{0, r.i0}; }
 }  // namespace
 
 template <int NP>
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       // ---------------- TMA ----------------
       int n = 0, nk = 0;
       bool bad = false;
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DkvItem r = dkv_item(a, gm, it);
         if (r.steps == 0) continue;
         if (!wait_or_flag(gm.err, bar(&kvempty), (nk & 1) ^ 1u)) break;
@@ -495,10 +505,11 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         load_rows<NP>(Kb, &mp.k, nullptr, r.j0, BT, bk, bar(&kvfull));
         load_rows<NP>(Vb, &mp.v, nullptr, r.j0, BT, bk, bar(&kvfull));
         ++nk;
+        StepWalk wk = dkv_walk(r);
 #pragma unroll 1
-        for (int j = 0; j < r.steps; ++j, ++n) {
-          const Step s = dkv_step(r, j);
-          const int bq = r.b * a.Hq + r.hk * a.g + j / r.per;
+        for (int j = 0; j < r.steps; ++j, ++n, wk.next(r)) {
+          const Step s = wk.step(r);
+          const int bq = r.b * a.Hq + r.hk * a.g + wk.e;
           const int sq = n % NRING1, so = n % NRING2;
           if (!wait_or_flag(gm.err, bar(&qempty[sq]), ((n / NRING1) & 1) ^ 1u) ||
               !wait_or_flag(gm.err, bar(&oempty[so]), ((n / NRING2) & 1) ^ 1u)) {
@@ -521,12 +532,13 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       // ---------------- log-sums and D of the steps' queries ----------------
       int n = 0;
       bool bad = false;
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DkvItem r = dkv_item(a, gm, it);
+        StepWalk wk = dkv_walk(r);
 #pragma unroll 1
-        for (int j = 0; j < r.steps; ++j, ++n) {
-          const Step s = dkv_step(r, j);
-          const size_t q0 = ((size_t)r.b * a.Hq + r.hk * a.g + j / r.per) * a.Nq;
+        for (int j = 0; j < r.steps; ++j, ++n, wk.next(r)) {
+          const Step s = wk.step(r);
+          const size_t q0 = ((size_t)r.b * a.Hq + r.hk * a.g + wk.e) * a.Nq;
           float x[4], y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       bool bad = false;
       const int ksteps = a.d / 16;
       auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DkvItem r = dkv_item(a, gm, it);
         if (r.steps == 0) continue;
         if (!wait_or_flag(gm.err, bar(&kvfull), (uint32_t)nk++ & 1u)) { bad = true; break; }
@@ -563,9 +575,8 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
             zero_rows<NP>(tile, e, s.w);
           }
         };
-        auto scores = [&](int j) {
-          const Step s = dkv_step(r, j);
-          const int i = n0 + j, sq = i % NRING1;
+        auto scores = [&](const Step& s, int i) {
+          const int sq = i % NRING1;
           const uint32_t Q = Qr + sq * SH::TILE;
           if (!wait_or_flag(gm.err, bar(&qfull[sq]), (uint32_t)(i / NRING1) & 1u)) return false;
           clean(s, Q);
@@ -574,23 +585,25 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           commit(&sfull);
           return true;
         };
-        auto grads = [&](int j) {
-          const Step s = dkv_step(r, j);
-          const int i = n0 + j, so = i % NRING2;
+        auto grads = [&](const Step& s, int i) {
+          const int so = i % NRING2;
           const uint32_t O = Or + so * SH::TILE;
           if (!wait_or_flag(gm.err, bar(&ofull[so]), (uint32_t)(i / NRING2) & 1u)) return false;
           clean(s, O);
           tc::fence_after();
           mma_features<NP>(tP, Vb, O, ksteps, idesc(BT, s.w, false));
           commit(&dpfull);
-          if (j + 1 == r.steps) commit(&kvempty);   // the last product that reads K or V
+          if (i + 1 == n) commit(&kvempty);   // the last product that reads K or V
           return true;
         };
-        if (!scores(0) || !grads(0)) { bad = true; break; }
+        StepWalk wk = dkv_walk(r);
+        Step s = wk.step(r);
+        if (!scores(s, n0) || !grads(s, n0)) { bad = true; break; }
 #pragma unroll 1
         for (int j = 0; j < r.steps; ++j) {
-          const Step s = dkv_step(r, j);
           const int i = n0 + j, sq = i % NRING1, so = i % NRING2;
+          wk.next(r);
+          const Step next = wk.step(r);
           if (!wait_or_flag(gm.err, bar(&pfull), (uint32_t)i & 1u) ||
               (j == 0 && !wait_or_flag(gm.err, bar(&gempty), ((uint32_t)ng++ & 1u) ^ 1u))) {
             bad = true;
@@ -598,15 +611,16 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           }
           tc::fence_after();
           const uint32_t id = idesc(BT, a.d, true);
-          mma_rows(tV, tS, Or + so * SH::TILE, s.w / 16, id, j > 0);
+          mma_rows(tV, tS, Or + so * SH::TILE, s.w / 16, id, j > 0, 32);
           commit(&oempty[so]);
-          if (j + 1 < r.steps && !scores(j + 1)) { bad = true; break; }
+          if (j + 1 < r.steps && !scores(next, i + 1)) { bad = true; break; }
           if (!wait_or_flag(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
           tc::fence_after();
-          mma_rows(tK, tP, Qr + sq * SH::TILE, s.w / 16, id, j > 0);
+          mma_rows(tK, tP, Qr + sq * SH::TILE, s.w / 16, id, j > 0, 32);
           commit(&qempty[sq]);
           if (j + 1 == r.steps) commit(&gfull);
-          if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
+          if (j + 1 < r.steps && !grads(next, i + 1)) { bad = true; break; }
+          s = next;
         }
       }
       if (bad) {  // what was issued ends before tensor memory is freed
@@ -622,7 +636,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
     const float c = a.scale_log2;
     int n = 0, ng = 0;
     bool bad = false;
-    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+    for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const DkvItem r = dkv_item(a, gm, it);
       const int j = r.j0 + row;
       // positions [pl, ph) see this key
@@ -631,30 +645,31 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       const bool keys_ok = r.j1 - r.j0 == BT;
       const int all_lo = r.j0 + BT - 1 - a.right;
       const int all_hi = r.j0 + BT <= a.sinks ? r.sq.len : min(r.sq.len, r.j0 + a.left + 1);
+      const f32x2 c2 = pack2(c, c);
+      StepWalk wk = dkv_walk(r);
 #pragma unroll 1
-      for (int k = 0; k < r.steps; ++k, ++n) {
-        const Step s = dkv_step(r, k);
+      for (int k = 0; k < r.steps; ++k, ++n, wk.next(r)) {
+        const Step s = wk.step(r);
         const int ps = r.sq.qp + s.r0;            // position of the step's first query
         const bool whole = keys_ok && s.re - s.r0 == BT && ps >= all_lo && ps + BT <= all_hi;
         const int l = pl - ps - c0, h = min(ph - ps, s.re - s.r0) - c0;
+        const uint32_t bits[2] = {whole ? 0u : seen_bits(l, h, 0), whole ? 0u : seen_bits(l - 32, h - 32, 0)};
         const float* L = &Ls[n & 1][c0];
         const float* D = &Ds[c0];
-        bool ok = wait_or_flag(gm.err, bar(&lfull[n & 1]), (uint32_t)(n >> 1) & 1u);
-        ok = wait_or_flag(gm.err, bar(&sfull), (uint32_t)n & 1u) && ok;
+        const bool ok = wait_or_flag(gm.err, bar(&lfull[n & 1]), (uint32_t)(n >> 1) & 1u);
+        if (!wait_warp(gm.err, bar(&sfull), (uint32_t)n & 1u) || !__all_sync(0xffffffffu, ok)) {
+          bad = true;
+          break;
+        }
         tc::fence_after();
         uint32_t v[2][32];
         ld32(S + c0, v[0]);
         ld32(S + c0 + 32, v[1]);
         ld_wait(v[0]);
         ld_wait(v[1]);
-        tc::fence_before();
-        if (!ew_sync_all(ok)) { bad = true; break; }   // read by all before P^T is written over it
-        tc::fence_after();
-        const f32x2 c2 = pack2(c, c);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t o[16];
-          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, 0);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 ls = lds4(L + 32 * q + e);
@@ -662,51 +677,59 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
                                           c2, pack2(-ls.x, -ls.y)));
             const float2 y = unpack2(fma2(pack2(__uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3])),
                                           c2, pack2(-ls.z, -ls.w)));
-            float p[4] = {exp2_ftz(x.x), exp2_ftz(x.y), exp2_ftz(y.x), exp2_ftz(y.y)};
-            if (!whole)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) p[z] = bits >> (e + z) & 1u ? p[z] : 0.f;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) v[q][e + z] = __float_as_uint(p[z]);
-            o[e >> 1] = pack(p[0], p[1]);
-            o[(e >> 1) + 1] = pack(p[2], p[3]);
+            v[q][e] = __float_as_uint(exp2_ftz(x.x));
+            v[q][e + 1] = __float_as_uint(exp2_ftz(x.y));
+            v[q][e + 2] = __float_as_uint(exp2_ftz(y.x));
+            v[q][e + 3] = __float_as_uint(exp2_ftz(y.y));
           }
-          st16(S + c0 / 2 + 16 * q, o);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits[q] >> e & 1u)) v[q][e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            o[e >> 1] = pack(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+          st16(S + c0 + 16 * q, o);
         }
         st_wait();
         tc::fence_before();
         arrive(bar(&pfull));
         arrive(bar(&lempty[n & 1]));
 
-        ok = wait_or_flag(gm.err, bar(&dfull), (uint32_t)n & 1u);
-        ok = wait_or_flag(gm.err, bar(&dpfull), (uint32_t)n & 1u) && ok;
+        const bool okd = wait_or_flag(gm.err, bar(&dfull), (uint32_t)n & 1u);
+        if (!wait_warp(gm.err, bar(&dpfull), (uint32_t)n & 1u) || !__all_sync(0xffffffffu, okd)) {
+          bad = true;
+          break;
+        }
         tc::fence_after();
         uint32_t dp[2][32];
         ld32(P + c0, dp[0]);
         ld32(P + c0 + 32, dp[1]);
         ld_wait(dp[0]);
         ld_wait(dp[1]);
-        tc::fence_before();
-        if (!ew_sync_all(ok)) { bad = true; break; }
-        tc::fence_after();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t o[16];
-          const uint32_t bits = whole ? 0xffffffffu : seen_bits(l - 32 * q, h - 32 * q, 0);
+          float x[32];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 ds = lds4(D + 32 * q + e);
-            const float dd[4] = {ds.x, ds.y, ds.z, ds.w};
-            float x[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              x[z] = __uint_as_float(v[q][e + z]) * (__uint_as_float(dp[q][e + z]) - dd[z]);
-              if (!whole) x[z] = bits >> (e + z) & 1u ? x[z] : 0.f;
-            }
-            o[e >> 1] = pack(x[0], x[1]);
-            o[(e >> 1) + 1] = pack(x[2], x[3]);
+            const float2 y = unpack2(mul2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])),
+                                          add2(pack2(__uint_as_float(dp[q][e]), __uint_as_float(dp[q][e + 1])),
+                                               pack2(-ds.x, -ds.y))));
+            const float2 w = unpack2(mul2(pack2(__uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3])),
+                                          add2(pack2(__uint_as_float(dp[q][e + 2]), __uint_as_float(dp[q][e + 3])),
+                                               pack2(-ds.z, -ds.w))));
+            x[e] = y.x; x[e + 1] = y.y; x[e + 2] = w.x; x[e + 3] = w.y;
           }
-          st16(P + c0 / 2 + 16 * q, o);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = bits[q] >> e & 1u ? x[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(x[e], x[e + 1]);
+          st16(P + c0 + 16 * q, o);
         }
         st_wait();
         tc::fence_before();
@@ -715,7 +738,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
       }
       if (bad) break;
       if (r.steps > 0) {
-        if (!ew_sync_all(wait_or_flag(gm.err, bar(&gfull), (uint32_t)ng & 1u))) { bad = true; break; }
+        if (!wait_warp(gm.err, bar(&gfull), (uint32_t)ng & 1u)) break;
         ++ng;
         tc::fence_after();
       }
@@ -774,12 +797,12 @@ cudaError_t bwd_go(const BwdMaps& mp, const WinArgs& a, int* err, cudaStream_t s
   BwdGeom gm;
   gm.err = err;
   gm.tiles = (a.Nq + BT - 1) / BT;
-  gm.items = (long long)a.B * a.Hq * gm.tiles;
+  gm.items = a.B * a.Hq * gm.tiles;
   e = launch("win_dq_tc", k_win_dq_tc<NP>, dim3((unsigned)(gm.items < sms ? gm.items : sms)),
              dim3(BTH), smem, st, mp, a, gm);
   if (e != cudaSuccess) return e;
   gm.tiles = a.stiles * a.chunks + (a.Nk + BT - 1) / BT - a.stiles;
-  gm.items = (long long)a.B * a.Hkv * gm.tiles;
+  gm.items = a.B * a.Hkv * gm.tiles;
   e = launch("win_dkv_tc", k_win_dkv_tc<NP>, dim3((unsigned)(gm.items < sms ? gm.items : sms)),
              dim3(BTH), smem, st, mp, a, gm);
   if (e != cudaSuccess || a.stiles == 0) return e;

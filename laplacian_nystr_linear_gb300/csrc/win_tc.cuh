@@ -86,13 +86,14 @@ __device__ __forceinline__ void mma_features(uint32_t d_tmem, uint32_t A, uint32
     if (k < ksteps) tc::mma_bf16(d_tmem, da + off, db + off, id, k > 0);
   }
 }
-// D (+)= A B over the `slices` 16-row slices of B, A in tensor memory
+// D (+)= A B over the `slices` 16-row slices of B, A in tensor memory; slices 4 to
+// 7 of A lie `skip` columns behind their place
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t A, uint32_t B, int slices,
-                                         uint32_t id, bool acc) {
+                                         uint32_t id, bool acc, uint32_t skip = 0) {
   const uint64_t db = desc_mn(B, 16384);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    if (k < slices) mma_ts(d_tmem, A + 8 * k, db + 128 * k, id, acc || k > 0);
+    if (k < slices) mma_ts(d_tmem, A + 8 * k + (k < 4 ? 0 : skip), db + 128 * k, id, acc || k > 0);
 }
 
 // rows [r0, w) of an NP-panel tile to zero, by the thread that issues the products
