@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "win.cuh"
 
 namespace lapnys {
@@ -66,6 +68,21 @@ template <typename Kern>
 inline cudaError_t allow_smem(Kern kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
+
+// the same, once per kernel and device (each kernel keeps its own `done`)
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};
+  template <typename Kern>
+  cudaError_t allow(Kern kern, size_t bytes, int dev) {
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = allow_smem(kern, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
+// the current device and its number of SMs (looked up once per device)
+cudaError_t device_sms(int* dev, int* sms);
 
 // ---- launchers (return the first CUDA error, cudaSuccess otherwise) -------
 // tensor-core forward passes (bf16, d = 32 or 64, m > 64): the query pass

@@ -533,8 +533,10 @@ cudaError_t go(TokenArgs& t, cudaStream_t st) {
   using TQ = typename std::conditional<Kind<KIND>::QF32, float, __nv_bfloat16>::type;
   constexpr size_t join = (size_t)TNW * 16 * (DP + 2) * 4;
   constexpr size_t smem = token_smem<KIND, DP>() > join ? token_smem<KIND, DP>() : join;
-  cudaError_t e = allow_smem(k_token<KIND, DP>, smem);
-  if (e != cudaSuccess) return e;
+  static SmemOnce once;
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess || (e = once.allow(k_token<KIND, DP>, smem, dev)) != cudaSuccess) return e;
   const long long n = (long long)t.w.B * t.w.Hkv * t.rtiles * t.splits;
   e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)n), dim3(32 * TNW), smem, st, t);
   if (e != cudaSuccess || t.splits == 1) return e;

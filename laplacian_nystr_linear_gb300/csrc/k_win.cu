@@ -392,8 +392,10 @@ namespace {
 template <int DP>
 cudaError_t fwd_t(const WinArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(3 * WT * row_stride(DP) + WT * WPS) * 4;
-  cudaError_t e = allow_smem(k_win_fwd<DP>, smem);
-  if (e != cudaSuccess) return e;
+  static SmemOnce once;
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess || (e = once.allow(k_win_fwd<DP>, smem, dev)) != cudaSuccess) return e;
   const long long n = (long long)a.B * a.Hq * ((a.Nq + WT - 1) / WT);
   return launch("win_fwd", k_win_fwd<DP>, dim3((unsigned)n), dim3(kThreads), smem, st, a);
 }
@@ -401,9 +403,12 @@ template <int DP>
 cudaError_t bwd_t(const WinArgs& a, cudaStream_t st) {
   const size_t sq = (size_t)(4 * WT * row_stride(DP) + WT * WPS) * 4;
   const size_t sk = (size_t)(4 * WT * row_stride(DP) + 2 * WT * WPS + 2 * WT) * 4;
-  cudaError_t e;
-  if ((e = allow_smem(k_win_dq<DP>, sq)) != cudaSuccess) return e;
-  if ((e = allow_smem(k_win_dkv<DP>, sk)) != cudaSuccess) return e;
+  static SmemOnce once_q, once_kv;
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess || (e = once_q.allow(k_win_dq<DP>, sq, dev)) != cudaSuccess ||
+      (e = once_kv.allow(k_win_dkv<DP>, sk, dev)) != cudaSuccess)
+    return e;
   const long long nq = (long long)a.B * a.Hq * ((a.Nq + WT - 1) / WT);
   e = launch("win_dq", k_win_dq<DP>, dim3((unsigned)nq), dim3(kThreads), sq, st, a);
   if (e != cudaSuccess) return e;

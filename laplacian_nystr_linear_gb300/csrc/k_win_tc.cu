@@ -57,7 +57,7 @@ struct FwdGeom {
   int qt;                               // tiles of 128 query rows
   int npair;                            // items per (batch, key head): pairs of heads or of tiles
   int by_head;                          // 1: an item's tiles are two heads
-  long long items;
+  int items;
   int* err;
 };
 
@@ -69,12 +69,12 @@ struct FwdItem {
   WinRange own[2];
   int ns, nw;                           // steps of the first tokens, of the window
 };
-__device__ __forceinline__ FwdItem fwd_item(const WinArgs& a, const FwdGeom& gm, long long it) {
+__device__ __forceinline__ FwdItem fwd_item(const WinArgs& a, const FwdGeom& gm, int it) {
   FwdItem r;
   // the last query tiles first: with an open left side they see the most keys
   const int heads = a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g);
-  const int tq = gm.npair - 1 - (int)(it / heads);
-  int h = (int)(it % heads);
+  const int tq = gm.npair - 1 - it / heads;
+  int h = it % heads;
   const int per = gm.by_head ? a.g / 2 : a.g;
   const int e = h % per;
   h /= per;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         ++n;
         return true;
       };
-      for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const FwdItem r = fwd_item(a, gm, it);
         const int steps = r.ns + r.nw;
 #pragma unroll
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       mma_rows(tO[t], tS[t], slot(i), w / 16, id_pv, acc);
     };
     auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
-    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+    for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const FwdItem r = fwd_item(a, gm, it);
       const int steps = r.ns + r.nw;
       if (steps == 0) continue;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
     const float c = a.scale_log2;
     int nsf = 0, nof = 0;
     bool bad = false;
-    for (long long it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+    for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const FwdItem r = fwd_item(a, gm, it);
       // (registers, not an indexed array)
       const WinRange own = t ? r.own[1] : r.own[0];
@@ -448,11 +448,10 @@ namespace {
 template <int NP>
 cudaError_t fwd_go(const FwdMaps& mp, const WinArgs& a, const FwdGeom& gm, cudaStream_t st) {
   constexpr size_t smem = FwdShape<NP>::SMEM;
-  cudaError_t e = allow_smem(k_win_fwd_tc<NP>, smem);
-  if (e != cudaSuccess) return e;
+  static SmemOnce once;
   int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess || (e = once.allow(k_win_fwd_tc<NP>, smem, dev)) != cudaSuccess) return e;
   const unsigned grid = (unsigned)(gm.items < sms ? gm.items : sms);
   return launch("win_fwd_tc", k_win_fwd_tc<NP>, dim3(grid), dim3(FTH), smem, st, mp, a, gm);
 }
@@ -466,7 +465,7 @@ cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st) {
   gm.qt = (a.Nq + FT - 1) / FT;
   gm.by_head = a.g % 2 == 0;
   gm.npair = gm.by_head ? gm.qt : (gm.qt + 1) / 2;
-  gm.items = (long long)a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g) * gm.npair;
+  gm.items = a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g) * gm.npair;
   if (!win_map(&mp.q, a.q, a.B * a.Hq, a.Nq, a.d, FT) ||
       !win_map(&mp.k, a.k, a.B * a.Hkv, a.Nk, a.d, FT) ||
       !win_map(&mp.v, a.v, a.B * a.Hkv, a.Nk, a.d, FT) ||

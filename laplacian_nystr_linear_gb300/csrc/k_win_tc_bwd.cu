@@ -788,12 +788,12 @@ namespace {
 template <int NP>
 cudaError_t bwd_go(const BwdMaps& mp, const WinArgs& a, int* err, cudaStream_t st) {
   constexpr size_t smem = BwdShape<NP>::SMEM;
-  cudaError_t e;
-  if ((e = allow_smem(k_win_dq_tc<NP>, smem)) != cudaSuccess) return e;
-  if ((e = allow_smem(k_win_dkv_tc<NP>, smem)) != cudaSuccess) return e;
+  static SmemOnce once_q, once_kv;
   int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess || (e = once_q.allow(k_win_dq_tc<NP>, smem, dev)) != cudaSuccess ||
+      (e = once_kv.allow(k_win_dkv_tc<NP>, smem, dev)) != cudaSuccess)
+    return e;
   BwdGeom gm;
   gm.err = err;
   gm.tiles = (a.Nq + BT - 1) / BT;

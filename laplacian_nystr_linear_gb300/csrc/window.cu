@@ -105,9 +105,23 @@ int check_cache(WinArgs& a, int B, int Hq, int Hkv, int Nq, int d, int block, in
   return check_dims(a, B, Hq, Hkv, Nq, max_blocks * block, d);
 }
 
+std::atomic<int> g_sms[64];
+
 int status(cudaError_t e) { return e == cudaSuccess ? LAPNYS_OK : LAPNYS_ECUDA; }
 
 }  // namespace
+
+cudaError_t device_sms(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  const int i = *dev;
+  *sms = i < 64 ? g_sms[i].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, i);
+  if (e == cudaSuccess && i < 64) g_sms[i].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+
 }  // namespace lapnys
 
 using namespace lapnys;

@@ -7,7 +7,7 @@ right is no bound.  Marshalling only: every step runs in liblapnys kernels.
 """
 from __future__ import annotations
 
-import dataclasses
+import functools
 import math
 from typing import NamedTuple, Optional
 
@@ -15,11 +15,10 @@ import torch
 
 from . import _lib
 from ._lib import check, load
-from .api import _dtype, _ptr, _stream
+from .api import _DT, _dtype
 
 
-@dataclasses.dataclass(frozen=True)
-class WindowParams:
+class WindowParams(NamedTuple):
     """Shape and mask of one call: q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d]."""
     B: int
     Hq: int
@@ -33,7 +32,7 @@ class WindowParams:
     scale: float
 
     def dims(self):
-        return (self.B, self.Hq, self.Hkv, self.Nq, self.Nk, self.d, self.left, self.right, self.sinks)
+        return self[:9]
 
     @staticmethod
     def of(q: torch.Tensor, k: torch.Tensor, left: int, right: int = 0, sinks: int = 0,
@@ -59,17 +58,23 @@ def _scale(scale, d):
 
 
 def _tensor(t, name, shape, dtype, device):
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous()
-            or t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or not t.is_cuda or not t.is_contiguous() or t.device != device):
         raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)} and {dtype}"
                          f" on {device}")
-    if t.data_ptr() & 15 and t.numel() and dtype != torch.int32:
-        raise ValueError(f"{name} must be 16-byte aligned")
 
 
 def _batch(t, name, B, device):
     if t is not None:
         _tensor(t, name, (B,), torch.int32, device)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class _on:
@@ -111,8 +116,8 @@ def _check_window(q, k, v, lens, q_pos, p: WindowParams):
     _batch(q_pos, "q_pos", p.B, dev)
 
 
+@functools.lru_cache(maxsize=256)
 def window_workspace_bytes(p: WindowParams, dtype: torch.dtype, backward: bool = False) -> int:
-    from .api import _DT
     return load().lapnys_window_workspace_bytes(*p.dims(), _DT[dtype], int(backward))
 
 
@@ -129,8 +134,8 @@ def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=No
             _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype), dev)
         rc = load().lapnys_window_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse) if need_lse else None, _ptr(lens),
-            _ptr(q_pos), *p.dims(), p.scale, _stream(dev), _dtype(q), _ptr(ws), _nbytes(ws))
+            _at(q), _at(k), _at(v), _at(out), _at(lse) if need_lse else None, _at(lens),
+            _at(q_pos), *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_fwd")
     return out, (lse if need_lse else None)
 
@@ -151,8 +156,8 @@ def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, 
             _tensor(t, name, like.shape, q.dtype, dev)
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype, True), dev)
         rc = load().lapnys_window_bwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(lens), _ptr(q_pos),
-            _ptr(dq), _ptr(dk), _ptr(dv), *p.dims(), p.scale, _stream(dev), _dtype(q), _ptr(ws),
+            _at(q), _at(k), _at(v), _at(out), _at(dout), _at(lse), _at(lens), _at(q_pos),
+            _at(dq), _at(dk), _at(dv), *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws),
             _nbytes(ws))
     check(rc, "lapnys_window_bwd")
     return dq, dk, dv
@@ -230,16 +235,21 @@ def cache_append(cache: KVCache, k, v, table, start, lens=None) -> None:
     _batch(lens, "lens", B, dev)
     with _on(dev):
         rc = load().lapnys_cache_append(
-            _ptr(k), _ptr(v), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-            _ptr(table), _ptr(start), _ptr(lens), B, Hkv, N, d, *geometry, _stream(dev), dt)
+            _at(k), _at(v), _at(cache.k), _at(cache.v), _at(cache.k_scale), _at(cache.v_scale),
+            _at(table), _at(start), _at(lens), B, Hkv, N, d, *geometry, _on_stream(dev), dt)
     check(rc, "lapnys_cache_append")
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_workspace(*sizes) -> int:
+    return load().lapnys_cache_workspace_bytes(*sizes)
 
 
 def cache_workspace_bytes(q, cache: KVCache, table, left=-1, right=0, sinks=0) -> int:
     B, Hq, Nq, d = q.shape
     blocks, Hkv, block, _ = cache.k.shape
-    return load().lapnys_cache_workspace_bytes(B, Hq, Hkv, Nq, d, block, blocks, table.shape[1],
-                                               left, right, sinks, _dtype(q))
+    return _cache_workspace(B, Hq, Hkv, Nq, d, block, blocks, table.shape[1], left, right, sinks,
+                            _dtype(q))
 
 
 def cache_attention(q, cache: KVCache, table, lens, left=-1, right=0, sinks=0, scale=None,
@@ -262,10 +272,10 @@ def cache_attention(q, cache: KVCache, table, lens, left=-1, right=0, sinks=0, s
     with _on(dev):
         out = torch.empty_like(q) if out is None else out
         _tensor(out, "out", q.shape, q.dtype, dev)
-        ws = _workspace(ws, cache_workspace_bytes(q, cache, table, left, right, sinks), dev)
+        ws = _workspace(ws, _cache_workspace(B, Hq, Hkv, Nq, d, *geometry, left, right, sinks, dt), dev)
         rc = load().lapnys_cache_attention(
-            _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-            _ptr(table), _ptr(lens), _ptr(q_pos), _ptr(out), B, Hq, Hkv, Nq, d, *geometry, left, right,
-            sinks, _scale(scale, d), _stream(dev), dt, _ptr(ws), _nbytes(ws))
+            _at(q), _at(cache.k), _at(cache.v), _at(cache.k_scale), _at(cache.v_scale),
+            _at(table), _at(lens), _at(q_pos), _at(out), B, Hq, Hkv, Nq, d, *geometry, left, right,
+            sinks, _scale(scale, d), _on_stream(dev), dt, _at(ws), _nbytes(ws))
     check(rc, "lapnys_cache_attention")
     return out
