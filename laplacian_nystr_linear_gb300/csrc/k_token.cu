@@ -6,7 +6,7 @@
 // What bounds it: every visible key and value is read once, for all the query
 // heads that share it, and nothing else is large.  So the work is split over the
 // keys: a block takes one (sequence, key head, 16 query rows) and one contiguous
-// share of the visible groups of 16 keys, its warps take groups in turn, each
+// share of the visible groups of 16 or 32 keys, its warps take groups in turn, each
 // with a ring of asynchronous copies of its own (no block barrier in the loop),
 // and k_token_join adds the shares.  Shares are cut on the device from the
 // sequence's own length, so a ragged batch stays even within a sequence.
@@ -17,9 +17,17 @@
 // features (scores), and column n of output step nt is feature n DP / 8 + nt
 // (P V), so both operands come from shared memory in 16-byte reads without bank
 // conflicts (the swizzles below).
-//   - 8-bit: e4m3 -> f16 is exact; q is scaled per row by a power of two to fit
-//     f16 (a row's features below 2^-38 of its largest are lost); p is kept as
-//     2^10 p in f16.  fp32 queries: q and p in two f16 parts (2^-22).
+//   - 8-bit, bf16 queries: the e4m3 product (m16n8k32) takes the cache's bytes as
+//     they are; q and p are the sum of two e4m3 parts each, x = x0 + x1 / 16 with
+//     x0 = e4m3(x), x1 = e4m3(16 (x - x0)).  q is scaled per row by a power of two
+//     (its 8 bits fit the two parts exactly; features below 2^-14 of the row's
+//     largest are off by up to 2^-21 of that), p is kept as 2^8 p (off by 2^-8 of
+//     itself like a bf16 rounding, or 2^-22 of the row's largest).  Values are
+//     transposed four keys at a time by byte permutes.  Converting the cache to
+//     f16 instead costs four instructions per two values: 768 a group of 16 keys
+//     in all, 2.8 TB/s.
+//   - 8-bit, fp32 queries: e4m3 -> f16 is exact; q (scaled per row) and 2^10 p in
+//     two f16 parts (2^-22).
 //   - bf16: q, k, v as they are, p rounded to bf16 (2^-9, below the rounding of
 //     the output; sums, maxima and outputs are fp32 throughout).
 //   - fp32: all operands in three bf16 parts, six products (2^-24 each).
@@ -34,22 +42,26 @@ namespace lapnys {
 
 namespace {
 constexpr int TNW = 4;      // warps of a block
-constexpr int TGK = 16;     // keys of a group
 enum : int { TK_BF16 = 0, TK_E4M3 = 1, TK_E4M3_F32 = 2, TK_F32 = 3 };
 
 template <int KIND>
 struct Kind {
   static constexpr int ES = KIND == TK_F32 ? 4 : (KIND == TK_BF16 ? 2 : 1);  // bytes of k, v
   static constexpr bool QF32 = KIND == TK_E4M3_F32 || KIND == TK_F32;
-  static constexpr bool F16 = KIND == TK_E4M3 || KIND == TK_E4M3_F32;
-  static constexpr int PARTS = KIND == TK_F32 ? 3 : (KIND == TK_E4M3_F32 ? 2 : 1);
-  static constexpr float SHIFT = F16 ? 10.f : 0.f;  // p is held as 2^SHIFT p
+  static constexpr bool E4 = KIND == TK_E4M3;       // e4m3 products
+  static constexpr bool F16 = KIND == TK_E4M3_F32;  // f16 products
+  static constexpr int GK = E4 ? 32 : 16;           // keys of a group
+  static constexpr int PARTS = KIND == TK_F32 ? 3 : (E4 || F16 ? 2 : 1);
+  static constexpr float SHIFT = E4 ? 8.f : (F16 ? 10.f : 0.f);  // p is held as 2^SHIFT p
+  static constexpr int QEXP = E4 ? 7 : 13;  // a row's largest |q| is scaled to [2^QEXP, 2^(QEXP + 1))
+  static constexpr int TRAIL = 32;          // bytes behind a ring slot: scales of the keys, of the
+                                            // values, and whether there is a block, per 16 keys
 };
 template <int KIND, int DP>
-__host__ __device__ constexpr int ring_stages() { return KIND == TK_F32 && DP == 128 ? 3 : 4; }
+__host__ __device__ constexpr int ring_stages() { return (KIND == TK_F32 || KIND == TK_E4M3) && DP == 128 ? 3 : 4; }
 template <int KIND, int DP>
 __host__ __device__ constexpr size_t token_smem() {
-  return (size_t)TNW * ring_stages<KIND, DP>() * (2 * TGK * DP * Kind<KIND>::ES + 16);
+  return (size_t)TNW * ring_stages<KIND, DP>() * (2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + Kind<KIND>::TRAIL);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -66,15 +78,31 @@ __device__ __forceinline__ void mma_bf(float (&d)[4], const uint32_t (&a)[4], ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16) mma_f16(d, a, b0, b1); else mma_bf(d, a, b0, b1);
+__device__ __forceinline__ void mma_e4(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // two e4m3 values (low 16 bits) -> two f16, exact
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
   return r;
+}
+// four values (|x| <= 448) as four e4m3 bytes, and 16 times what those leave as four more
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+__device__ __forceinline__ void split_e4(float a, float b, float c, float d, uint32_t* hi, uint32_t* lo) {
+  const uint32_t h = e4m3x4(a, b, c, d);
+  const uint32_t w0 = e4m3x2_f16(h), w1 = e4m3x2_f16(h >> 16);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+  *hi = h;
+  *lo = e4m3x4((a - x.x) * 16.f, (b - x.y) * 16.f, (c - y.x) * 16.f, (d - y.y) * 16.f);
 }
 // two fp32 as PARTS 16-bit parts, the parts' sum nearest to them
 template <int KIND>
@@ -96,7 +124,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[Kind<KIND>
   }
 }
 
-// byte offset of a row's 16-byte chunk in a tile of TGK rows of RB bytes.  A key
+// byte offset of a row's 16-byte chunk in a tile of rows of RB bytes.  A key
 // row is read 16 bytes per thread at chunk t + 4 i of rows gid (t = lane % 4,
 // gid = lane / 4): odd rows swap their halves.
 template <int RB>
@@ -126,14 +154,15 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 template <int KIND, int DP>
 __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
   using X = Kind<KIND>;
-  constexpr int ES = X::ES, RB = DP * ES, NP = X::PARTS;
+  constexpr int ES = X::ES, RB = DP * ES, NP = X::PARTS, GK = X::GK, NU = GK / 8, NH = GK / 16;
   constexpr int NST = ring_stages<KIND, DP>();
-  constexpr int TILE = TGK * RB, STG = 2 * TILE;
-  constexpr int KS = DP / 16;                  // k steps of the scores
+  constexpr int TILE = GK * RB, STG = 2 * TILE, SLOT = STG + X::TRAIL;
+  constexpr int KS = DP / 16;                  // 16-feature steps of the scores
   constexpr int NT = DP / 8;                   // column steps of P V
   constexpr int PIECE = 16 / ES;               // features of a 16-byte piece
-  constexpr int KSP = PIECE / 4;               // k steps of a piece
+  constexpr int KSP = PIECE / 4;               // steps of a piece, four features a thread each
   constexpr int CH = RB / 16;                  // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;                 // rows that a warp copies at once
   using TQ = typename std::conditional<X::QF32, float, __nv_bfloat16>::type;
   extern __shared__ __align__(128) uint8_t ring[];
   const WinArgs& a = t.w;
@@ -146,16 +175,109 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
   WinSeq sq = win_seq(a, b);
   if (!a.q_pos && t.table) sq.qp = sq.len - a.Nq;
   const WinRange kr = win_keys(a, sq, 0, a.Nq);
+  // keys [free_lo, free_hi) (or first tokens) are seen by every query: no mask
+  const bool rows_ok = sq.qp >= 0 && sq.qp + a.Nq <= sq.len;
+  const int free_lo = sq.qp + a.Nq - 1 - a.left, free_hi = rows_ok ? min(sq.len, sq.qp + a.right + 1) : -1;
 
   // this block's share of the groups: first tokens' groups, then the window's
-  const int gs = (kr.S + TGK - 1) / TGK, w0 = kr.lo / TGK;
-  const int G = gs + (kr.hi > kr.lo ? (kr.hi + TGK - 1) / TGK - w0 : 0);
+  const int gs = (kr.S + GK - 1) / GK, w0 = kr.lo / GK;
+  const int G = gs + (kr.hi > kr.lo ? (kr.hi + GK - 1) / GK - w0 : 0);
   const int g0 = (int)((long long)G * sp / t.splits), g1 = (int)((long long)G * (sp + 1) / t.splits);
+
+  uint8_t* my = ring + warp * NST * SLOT;
+  const uint32_t my_s = smem_addr(my);
+  const size_t plain = ((size_t)b * a.Hkv + hk) * a.Nk;
+  // what a lane copies: chunk `lc` of rows lr, lr + RPI, ..
+  const int lr = lane / CH, lc = lane % CH;
+
+  // first key of group gi and the range of keys that its phase counts
+  auto group = [&](int gi, int* j0, int* jb, int* je) {
+    const bool f = gi < gs;
+    *j0 = (f ? gi : w0 + gi - gs) * GK;
+    *jb = f ? 0 : kr.lo;
+    *je = f ? kr.S : kr.hi;
+  };
+  auto has_keys = [](int j, int jb, int je) { return j < je && j + 16 > jb; };
+  // the cache blocks that hold the 16-key parts of group gi; only those of parts
+  // with keys of the phase are looked up
+  auto blocks_of = [&](int gi, int (&blk)[NH]) {
+    int j0, jb, je;
+    group(gi, &j0, &jb, &je);
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+      blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)b * t.max_blocks + (j0 + 16 * h) / t.T] : -1;
+  };
+  // copies of group gi into ring slot st
+  auto issue = [&](int gi, int st, const int (&blk)[NH]) {
+    int j0, jb, je;
+    group(gi, &j0, &jb, &je);
+    const uint32_t dst = my_s + st * SLOT;
+    size_t tok[NH];
+    bool there[NH], full = j0 >= jb && j0 + GK <= je && a.d == DP;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      there[h] = true;
+      if (t.table) {
+        there[h] = (unsigned)blk[h] < (unsigned)t.blocks;
+        if (!there[h] && lane == 0 && has_keys(j0 + 16 * h, jb, je)) atomicOr(t.err, 2);
+        const size_t bh = (size_t)(there[h] ? blk[h] : 0) * a.Hkv + hk;
+        tok[h] = bh * t.T + (j0 + 16 * h) % t.T;
+        if (lane == 0) {
+          cp_async4(dst + STG + 4 * h, t.k_scale + bh);
+          cp_async4(dst + STG + 8 + 4 * h, t.v_scale + bh);
+          *reinterpret_cast<int*>(my + st * SLOT + STG + 16 + 4 * h) = there[h];
+        }
+      } else {
+        tok[h] = plain + j0 + 16 * h;
+      }
+      full = full && there[h];
+    }
+    const uint8_t* gk[NH];
+    const uint8_t* gv[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const size_t off = ((tok[h] + lr) * a.d + lc * PIECE) * ES;
+      gk[h] = (const uint8_t*)a.k + off;
+      gv[h] = (const uint8_t*)a.v + off;
+    }
+    if (full) {
+#pragma unroll
+      for (int u = 0; u < GK / RPI; ++u) {
+        constexpr int RH = 16 / RPI;       // copies of a half
+        const int off = (u % RH) * RPI * RB;
+        cp_async16(dst + k_off<RB>(u * RPI + lr, lc), gk[u / RH] + off, true);
+        cp_async16(dst + TILE + v_off<RB>(u * RPI + lr, lc), gv[u / RH] + off, true);
+      }
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < GK / RPI; ++u) {
+        const int r = u * RPI + lr, h = NH > 1 ? r >> 4 : 0;
+        const bool in = NH > 1 && h ? there[NH - 1] : there[0];
+        const bool ok = in && lc * PIECE < a.d && j0 + r >= jb && j0 + r < je;
+        const size_t off = (size_t)(r % 16 - lr) * a.d * ES;
+        const uint8_t* pk = NH > 1 && h ? gk[NH - 1] : gk[0];
+        const uint8_t* pv = NH > 1 && h ? gv[NH - 1] : gv[0];
+        cp_async16(dst + k_off<RB>(r, lc), ok ? pk + off : (const uint8_t*)a.k, ok);
+        cp_async16(dst + TILE + v_off<RB>(r, lc), ok ? pv + off : (const uint8_t*)a.v, ok);
+      }
+    }
+  };
+
+  int gi = g0 + warp, gn = gi;       // group to compute, group to issue
+  int blk[NH] = {};
+  if (t.table && gn < g1) blocks_of(gn, blk);
+#pragma unroll
+  for (int st = 0; st < NST - 1; ++st) {
+    if (gn < g1) issue(gn, st, blk);
+    gn += TNW;
+    if (t.table && gn < g1) blocks_of(gn, blk);
+    cp_commit();
+  }
 
   // the rows this thread meets: gid and gid + 8 of the tile
   WinRow row[2];
   float qs[2];                       // score factor of the row
-  uint32_t qf[NP][KS][4];
+  uint32_t qf[NP][X::E4 ? DP / 32 : KS][4];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int rr = rt * 16 + gid + 8 * r;
@@ -173,74 +295,34 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
     }
     float down = 1.f;
     qs[r] = a.scale_log2;
-    if constexpr (X::F16) {
+    if constexpr (X::F16 || X::E4) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the largest feature to [2^13, 2^14)
-      const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
+      const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - X::QEXP;
       if (mx > 0.f && mx < INFINITY) {
         const int h = max(-126, min(126, -ex));
         down = __uint_as_float((uint32_t)(h + 127) << 23);
         qs[r] *= __uint_as_float((uint32_t)(127 - h) << 23);
       }
     }
+    if constexpr (X::E4) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      uint32_t w[NP];
-      split<KIND>(x[s].x * down, x[s].y * down, w);
+      for (int s = 0; s < KS; ++s)   // step s / 2: its first (a0, a1) or second (a2, a3) four
+        split_e4(x[s].x * down, x[s].y * down, x[s].z * down, x[s].w * down,
+                 &qf[0][s >> 1][2 * (s & 1) + r], &qf[1][s >> 1][2 * (s & 1) + r]);
+    } else {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) qf[p][s][r] = w[p];
-      split<KIND>(x[s].z * down, x[s].w * down, w);
+      for (int s = 0; s < KS; ++s) {
+        uint32_t w[NP];
+        split<KIND>(x[s].x * down, x[s].y * down, w);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = w[p];
+        for (int p = 0; p < NP; ++p) qf[p][s][r] = w[p];
+        split<KIND>(x[s].z * down, x[s].w * down, w);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = w[p];
+      }
     }
   }
-
-  uint8_t* my = ring + warp * NST * (STG + 16);
-  const uint32_t my_s = smem_addr(my);
-  const size_t plain = ((size_t)b * a.Hkv + hk) * a.Nk;
-
-  // first key of group gi and the range of keys that its phase counts
-  auto group = [&](int gi, int* j0, int* jb, int* je) {
-    const bool f = gi < gs;
-    *j0 = (f ? gi : w0 + gi - gs) * TGK;
-    *jb = f ? 0 : kr.lo;
-    *je = f ? kr.S : kr.hi;
-  };
-  auto block_of = [&](int gi) -> int {   // the cache block that holds group gi
-    int j0, jb, je;
-    group(gi, &j0, &jb, &je);
-    return t.table[(size_t)b * t.max_blocks + j0 / t.T];
-  };
-  // copies of group gi into ring slot st
-  auto issue = [&](int gi, int st, int blk) {
-    int j0, jb, je;
-    group(gi, &j0, &jb, &je);
-    const uint32_t dst = my_s + st * (STG + 16);
-    size_t tok;
-    bool there = true;
-    if (t.table) {
-      there = (unsigned)blk < (unsigned)t.blocks;
-      if (!there && lane == 0) atomicOr(t.err, 2);
-      const size_t bh = (size_t)(there ? blk : 0) * a.Hkv + hk;
-      tok = bh * t.T + j0 % t.T;
-      if (lane == 0) {
-        cp_async4(dst + STG, t.k_scale + bh);
-        cp_async4(dst + STG + 4, t.v_scale + bh);
-        *reinterpret_cast<int*>(my + st * (STG + 16) + STG + 8) = there;
-      }
-    } else {
-      tok = plain + j0;
-    }
-#pragma unroll
-    for (int u = 0; u < TGK * CH / 32; ++u) {
-      const int id = u * 32 + lane, r = id / CH, c = id % CH;
-      const bool ok = there && c * PIECE < a.d && j0 + r >= jb && j0 + r < je;
-      const size_t off = ok ? ((tok + r) * a.d + c * PIECE) * ES : 0;
-      cp_async16(dst + k_off<RB>(r, c), (const uint8_t*)a.k + off, ok);
-      cp_async16(dst + TILE + v_off<RB>(r, c), (const uint8_t*)a.v + off, ok);
-    }
-  };
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[NT][4];
@@ -249,35 +331,46 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 
-  int gi = g0 + warp, gn = gi;       // group to compute, group to issue
-  int blk = t.table && gn < g1 ? block_of(gn) : 0;
-#pragma unroll
-  for (int st = 0; st < NST - 1; ++st) {
-    if (gn < g1) issue(gn, st, blk);
-    gn += TNW;
-    if (t.table && gn < g1) blk = block_of(gn);
-    cp_commit();
-  }
   int st = 0;
+#pragma unroll 1
   for (; gi < g1; gi += TNW) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
     __syncwarp();
-    const uint8_t* Kt = my + st * (STG + 16);
+    // the slot of the group before is free: its copies run under this group's work
+    if (gn < g1) issue(gn, st == 0 ? NST - 1 : st - 1, blk);
+    gn += TNW;
+    if (t.table && gn < g1) blocks_of(gn, blk);
+    cp_commit();
+    const uint8_t* Kt = my + st * SLOT;
     const uint8_t* Vt = Kt + TILE;
     int j0, jb, je;
     group(gi, &j0, &jb, &je);
-    float ksc = 1.f, vsc = 1.f;
-    if (t.table) {
-      ksc = *reinterpret_cast<const float*>(Kt + STG);
-      vsc = *reinterpret_cast<const float*>(Kt + STG + 4);
-      if (!*reinterpret_cast<const int*>(Kt + STG + 8)) je = jb;  // no such block: no keys
+    float ksc[NH], vsc[NH];
+    bool there[NH], all = true;        // a part without a block has no keys
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      ksc[h] = vsc[h] = 1.f;
+      there[h] = true;
+      if (t.table) {
+        ksc[h] = reinterpret_cast<const float*>(Kt + STG)[h];
+        vsc[h] = reinterpret_cast<const float*>(Kt + STG)[2 + h];
+        there[h] = reinterpret_cast<const int*>(Kt + STG)[4 + h] != 0;
+        all = all && there[h];
+      }
+    }
+    if constexpr (NH == 2) {           // (its P is 0: any finite scale will do)
+      if (!there[0]) vsc[0] = there[1] ? vsc[1] : 0.f;
+      if (!there[1]) vsc[1] = vsc[0];
+    } else if (!there[0]) {
+      vsc[0] = 0.f;
     }
     // ---- scores ----
-    float s[2][4];
+    float s[NU][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NU; ++u) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+      float s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < DP / 4 / PIECE; ++i) {
         const uint4 kv = *reinterpret_cast<const uint4*>(Kt + k_off<RB>(8 * u + gid, tq + 4 * i));
@@ -293,6 +386,12 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         } else if constexpr (KIND == TK_BF16) {
           mma_bf(s[u], qf[0][2 * i], w[0], w[1]);
           mma_bf(s[u], qf[0][2 * i + 1], w[2], w[3]);
+        } else if constexpr (X::E4) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            mma_e4(s[u], qf[0][2 * i + x], w[2 * x], w[2 * x + 1]);
+            mma_e4(s1, qf[1][2 * i + x], w[2 * x], w[2 * x + 1]);
+          }
         } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -302,23 +401,38 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
           }
         }
       }
+      if constexpr (X::E4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][e] = fmaf(s1[e], 0.0625f, s[u][e]);
+      }
     }
     // ---- softmax, running maximum and sum ----
-    float p[2][4];
+    const bool whole = all && j0 >= jb && j0 + GK <= je && j0 + GK <= free_hi &&
+                       (j0 >= free_lo || j0 + GK <= a.sinks);
+    float p[NU][4];
     bool up = false;
     float f[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      float qk[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) qk[h] = qs[r] * ksc[h];
       float mx = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = j0 + 8 * u + 2 * tq + e;
-          float& x = s[u][2 * r + e];
-          x = j >= jb && j < je && win_sees(row[r], j) ? x * (qs[r] * ksc) : -INFINITY;
-          mx = fmaxf(mx, x);
-        }
+        for (int e = 0; e < 2; ++e) s[u][2 * r + e] *= qk[u / 2];
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = j0 + 8 * u + 2 * tq + e;
+            if (!(there[u / 2] && j >= jb && j < je && win_sees(row[r], j))) s[u][2 * r + e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < NU; ++u) mx = fmaxf(fmaxf(mx, s[u][2 * r]), s[u][2 * r + 1]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       mx = fmaxf(mx, m[r]);
@@ -326,12 +440,13 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       f[r] = exp2f(m[r] - mu);
       up = up || mx > m[r];
       m[r] = mx;
+      const float off = X::SHIFT - mu;
       float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = exp2f(s[u][2 * r + e] - mu + X::SHIFT);
+          const float x = exp2f(s[u][2 * r + e] + off);
           p[u][2 * r + e] = x;
           sum += x;
         }
@@ -343,87 +458,141 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         o[n][0] *= f[0]; o[n][1] *= f[0]; o[n][2] *= f[1]; o[n][3] *= f[1];
       }
     }
-    uint32_t pf[NP][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t w[NP];
-        split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
-#pragma unroll
-        for (int x = 0; x < NP; ++x) pf[x][2 * u + r] = w[x];
-      }
     // ---- P V ----
-    if constexpr (KIND == TK_E4M3 || KIND == TK_E4M3_F32) {
-      constexpr int W = DP / 8 / 4;  // 32-bit words of a thread's value row piece
-      uint32_t v[4][W];
+    if constexpr (X::E4) {
+      // the k of a thread: keys 2 tq, 2 tq + 1 of the group's four runs of 8
+      uint32_t pf[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
-        if constexpr (W == 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
-          v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(Vt + v_off<RB>(rr, gid >> 1) + 8 * (gid & 1));
-          v[e][0] = x.x; v[e][1] = x.y;
-        }
-      }
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int sel = (n & 3) | (((n & 3) + 4) << 4);
-        const uint32_t b0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], sel));
-        const uint32_t b1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], sel));
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 2; ++r)
+          split_e4(p[2 * h][2 * r], p[2 * h][2 * r + 1], p[2 * h + 1][2 * r], p[2 * h + 1][2 * r + 1],
+                   &pf[0][2 * h + r], &pf[1][2 * h + r]);
+      // halves of unlike scale (blocks of 16 tokens) go one after the other
+      const bool apart = vsc[0] != vsc[1];
+#pragma unroll 1
+      for (int pass = 0; pass <= (int)apart; ++pass) {
+        uint32_t pa[2][4];
 #pragma unroll
-        for (int x = NP - 1; x >= 0; --x) mma_f16(c, pf[x], b0, b1);
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = fmaf(c[e], vsc, o[n][e]);
-      }
-    } else if constexpr (KIND == TK_BF16) {
-      constexpr int W = DP / 16;
+          for (int e = 0; e < 4; ++e) pa[x][e] = apart && (e >> 1) != pass ? 0u : pf[x][e];
+        const float vs = pass ? vsc[1] : vsc[0], vs1 = vs * 0.0625f;
+        constexpr int W = DP / 8 / 4;  // 32-bit words of a thread's piece of a value row
+        uint32_t v[8][W];
 #pragma unroll
-      for (int h = 0; h < W / 4; ++h) {
-        uint32_t v[4][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
-          const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid * (W / 4) + h));
-          v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+        for (int e = 0; e < 8; ++e) {
+          const int rr = 8 * (e >> 1) + 2 * tq + (e & 1);
+          if constexpr (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(Vt + v_off<RB>(rr, gid >> 1) + 8 * (gid & 1));
+            v[e][0] = x.x; v[e][1] = x.y;
+          }
         }
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int sel = n & 1 ? 0x7632 : 0x5410;
-          mma_bf(o[8 * h + n], pf[0], __byte_perm(v[0][n >> 1], v[1][n >> 1], sel),
-                 __byte_perm(v[2][n >> 1], v[3][n >> 1], sel));
+        for (int w = 0; w < W; ++w) {
+          uint32_t bt[2][4];           // four keys of each of the word's four columns
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x0 = __byte_perm(v[4 * h][w], v[4 * h + 1][w], 0x5140);
+            const uint32_t x1 = __byte_perm(v[4 * h + 2][w], v[4 * h + 3][w], 0x5140);
+            const uint32_t y0 = __byte_perm(v[4 * h][w], v[4 * h + 1][w], 0x7362);
+            const uint32_t y1 = __byte_perm(v[4 * h + 2][w], v[4 * h + 3][w], 0x7362);
+            bt[h][0] = __byte_perm(x0, x1, 0x5410);
+            bt[h][1] = __byte_perm(x0, x1, 0x7632);
+            bt[h][2] = __byte_perm(y0, y1, 0x5410);
+            bt[h][3] = __byte_perm(y0, y1, 0x7632);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_e4(c0, pa[0], bt[0][x], bt[1][x]);
+            mma_e4(c1, pa[1], bt[0][x], bt[1][x]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[4 * w + x][e] = fmaf(c0[e], vs, fmaf(c1[e], vs1, o[4 * w + x][e]));
+          }
         }
       }
     } else {
+      uint32_t pf[NP][4];
 #pragma unroll
-      for (int h = 0; h < DP / 32; ++h) {
-        float v[4][4];
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t w[NP];
+          split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
+#pragma unroll
+          for (int x = 0; x < NP; ++x) pf[x][2 * u + r] = w[x];
+        }
+      if constexpr (KIND == TK_E4M3_F32) {
+        constexpr int W = DP / 8 / 4;
+        uint32_t v[4][W];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
-          const float4 x = *reinterpret_cast<const float4*>(Vt + v_off<RB>(rr, gid * (DP / 32) + h));
-          v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          if constexpr (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(Vt + v_off<RB>(rr, gid >> 1) + 8 * (gid & 1));
+            v[e][0] = x.x; v[e][1] = x.y;
+          }
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t b0[3], b1[3];
-          split3_bf16x2(v[0][n], v[1][n], b0);
-          split3_bf16x2(v[2][n], v[3][n], b1);
+        for (int n = 0; n < NT; ++n) {
+          const int sel = (n & 3) | (((n & 3) + 4) << 4);
+          const uint32_t b0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], sel));
+          const uint32_t b1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], sel));
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int x = 2; x >= 0; --x)
+          for (int x = NP - 1; x >= 0; --x) mma_f16(c, pf[x], b0, b1);
 #pragma unroll
-            for (int y = 0; y <= x; ++y) mma_bf(o[4 * h + n], pf[y], b0[x - y], b1[x - y]);
+          for (int e = 0; e < 4; ++e) o[n][e] = fmaf(c[e], vsc[0], o[n][e]);
+        }
+      } else if constexpr (KIND == TK_BF16) {
+        constexpr int W = DP / 16;
+#pragma unroll
+        for (int h = 0; h < W / 4; ++h) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
+            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid * (W / 4) + h));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          }
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const int sel = n & 1 ? 0x7632 : 0x5410;
+            mma_bf(o[8 * h + n], pf[0], __byte_perm(v[0][n >> 1], v[1][n >> 1], sel),
+                   __byte_perm(v[2][n >> 1], v[3][n >> 1], sel));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < DP / 32; ++h) {
+          float v[4][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
+            const float4 x = *reinterpret_cast<const float4*>(Vt + v_off<RB>(rr, gid * (DP / 32) + h));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          }
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            uint32_t b0[3], b1[3];
+            split3_bf16x2(v[0][n], v[1][n], b0);
+            split3_bf16x2(v[2][n], v[3][n], b1);
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+              for (int y = 0; y <= x; ++y) mma_bf(o[4 * h + n], pf[y], b0[x - y], b1[x - y]);
+          }
         }
       }
     }
-    __syncwarp();
-    if (gn < g1) issue(gn, st == 0 ? NST - 1 : st - 1, blk);
-    gn += TNW;
-    if (t.table && gn < g1) blk = block_of(gn);
-    cp_commit();
     if (++st == NST) st = 0;
   }
   cp_wait_all();
@@ -522,7 +691,7 @@ namespace {
 // (so that short and long sequences of a batch even out), each share at least
 // two groups a warp.  From the dimensions alone.
 int shares(int blocks, long long keys) {
-  const long long most = (keys / TGK + 2 * TNW - 1) / (2 * TNW);
+  const long long most = (keys / 16 + 2 * TNW - 1) / (2 * TNW);
   long long s = (152 * 6 + blocks - 1) / blocks;
   s = s > most ? most : s;
   return (int)(s < 1 ? 1 : (s > 256 ? 256 : s));
@@ -552,7 +721,7 @@ TokenShape token_shape(int B, int Hkv, int g, int Nq, int d, long long keys, int
   s.rtiles = (g * Nq + 15) / 16;
   long long seen = keys;
   if (left < kWinUnbounded && right < kWinUnbounded) {
-    const long long w = (long long)left + right + Nq + sinks + 2 * TGK;
+    const long long w = (long long)left + right + Nq + sinks + 64;
     if (w < seen) seen = w;
   }
   const long long blocks = (long long)B * Hkv * s.rtiles;
