@@ -55,6 +55,30 @@ inline cudaError_t launch(const char* name, Kern kern, dim3 grid, dim3 block, si
   return e;
 }
 
+// launch() of a kernel that may start while the one before it on the stream still
+// runs; it waits for that one itself (griddepcontrol.wait)
+template <typename Kern, typename... Args>
+inline cudaError_t launch_after(const char* name, Kern kern, dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t st, Args... args) {
+  nvtxRangePushA(name);
+  const int slot = prof_begin(name, st);
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  prof_end(slot, st);
+  count_launch();
+  nvtxRangePop();
+  return e;
+}
+
 // an NVTX range over a scope (the library's entry points)
 struct NvtxScope {
   explicit NvtxScope(const char* name) { nvtxRangePushA(name); }
@@ -336,24 +360,29 @@ cudaError_t run_win_bwd_tc(const WinArgs& a, cudaStream_t st);
 bool win_map(CUtensorMap* t, const void* p, int BH, int N, int d, int rows);
 
 // a few queries per sequence, the keys split over blocks; table null: plain
-// keys and values, else the cache (w.Nk = max_blocks * T)
+// keys and values, else the cache (w.Nk = max_blocks << Tshift)
 struct TokenArgs {
   WinArgs w;
   const float* k_scale;    // [blocks][Hkv]
   const float* v_scale;
   const int32_t* table;    // [B][max_blocks]
-  int T, blocks, max_blocks;
-  int rtiles, splits;      // row tiles of 16, shares of the keys
-  float* part_o;           // [rows][splits][d]
-  float2* part_ml;         // [rows][splits]: maximum, sum
+  int Tshift, blocks, max_blocks;  // log2 of a block's tokens
+  int rtiles, slots;       // row tiles of 16; blocks to fill
+  long long grid;
+  bool joined;             // some rows may be shared out
+  float* part_o;           // [block][16][d]
+  float2* part_ml;         // [block][16]: maximum, sum
+  int2* info;              // [B][Hkv][rtiles]: first block, shares
   int* err;                // bit 1: a table named a block that is not there
 };
 struct TokenShape {
-  int rtiles, splits;
-  size_t o_bytes, ml_bytes;
+  int rtiles, slots;
+  long long grid;
+  bool joined;
+  size_t o_bytes, ml_bytes, info_bytes;
 };
-TokenShape token_shape(int B, int Hkv, int g, int Nq, int d, long long keys, int left, int right,
-                       int sinks);
+TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int d, long long keys,
+                       int left, int right, int sinks);
 cudaError_t run_token(TokenArgs& t, bool bf16, cudaStream_t st);
 
 struct AppendArgs {

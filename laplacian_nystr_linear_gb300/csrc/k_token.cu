@@ -8,8 +8,11 @@
 // keys: a block takes one (sequence, key head, 16 query rows) and one contiguous
 // share of the visible groups of 16 or 32 keys, its warps take groups in turn, each
 // with a ring of asynchronous copies of its own (no block barrier in the loop),
-// and k_token_join adds the shares.  Shares are cut on the device from the
-// sequence's own length, so a ragged batch stays even within a sequence.
+// and k_token_join adds the shares.  Shares are cut on the device, from all
+// sequences' lengths, so that they are alike in a ragged batch and, where it can
+// be, all blocks run at once: a block's start and end (dependent loads of the
+// lengths, the table, the queries; the join of its warps) cost 4 us, as much as
+// 0.2 MB of cache.
 //
 // Products on the warp-level tensor instruction (m16n8k16), rows = (query head
 // of the group, query), with the contraction's order chosen so that no operand
@@ -17,17 +20,14 @@
 // features (scores), and column n of output step nt is feature n DP / 8 + nt
 // (P V), so both operands come from shared memory in 16-byte reads without bank
 // conflicts (the swizzles below).
-//   - 8-bit, bf16 queries: the e4m3 product (m16n8k32) takes the cache's bytes as
-//     they are; q and p are the sum of two e4m3 parts each, x = x0 + x1 / 16 with
-//     x0 = e4m3(x), x1 = e4m3(16 (x - x0)).  q is scaled per row by a power of two
-//     (its 8 bits fit the two parts exactly; features below 2^-14 of the row's
-//     largest are off by up to 2^-21 of that), p is kept as 2^8 p (off by 2^-8 of
-//     itself like a bf16 rounding, or 2^-22 of the row's largest).  Values are
-//     transposed four keys at a time by byte permutes.  Converting the cache to
-//     f16 instead costs four instructions per two values: 768 a group of 16 keys
-//     in all, 2.8 TB/s.
-//   - 8-bit, fp32 queries: e4m3 -> f16 is exact; q (scaled per row) and 2^10 p in
-//     two f16 parts (2^-22).
+//   - 8-bit: e4m3 -> f16 is exact (one instruction for two; the e4m3 form of the
+//     product is no instruction of its own here: it ran as two f16 ones with more
+//     conversions, 1576 instructions for 32 keys against about 600).  q is scaled
+//     per row by a power of two to fit f16 (features below 2^-38 of the row's
+//     largest are lost).  p is kept as 2^10 p (v_scale / reference) in f16, the
+//     reference a scale of the values seen so far, so that P V adds up without a
+//     product per element; outputs are rescaled when the reference moves.  fp32
+//     queries: q and p in two f16 parts (2^-22).
 //   - bf16: q, k, v as they are, p rounded to bf16 (2^-9, below the rounding of
 //     the output; sums, maxima and outputs are fp32 throughout).
 //   - fp32: all operands in three bf16 parts, six products (2^-24 each).
@@ -48,39 +48,30 @@ template <int KIND>
 struct Kind {
   static constexpr int ES = KIND == TK_F32 ? 4 : (KIND == TK_BF16 ? 2 : 1);  // bytes of k, v
   static constexpr bool QF32 = KIND == TK_E4M3_F32 || KIND == TK_F32;
-  static constexpr bool E4 = KIND == TK_E4M3;       // e4m3 products
-  static constexpr bool F16 = KIND == TK_E4M3_F32;  // f16 products
-  static constexpr int GK = E4 ? 32 : 16;           // keys of a group
-  static constexpr int PARTS = KIND == TK_F32 ? 3 : (E4 || F16 ? 2 : 1);
-  static constexpr float SHIFT = E4 ? 8.f : (F16 ? 10.f : 0.f);  // p is held as 2^SHIFT p
-  static constexpr int QEXP = E4 ? 7 : 13;  // a row's largest |q| is scaled to [2^QEXP, 2^(QEXP + 1))
+  static constexpr bool F16 = KIND == TK_E4M3 || KIND == TK_E4M3_F32;  // f16 products
+  static constexpr int GK = KIND == TK_E4M3 ? 32 : 16;                  // keys of a group
+  static constexpr int PARTS = KIND == TK_F32 ? 3 : (KIND == TK_E4M3_F32 ? 2 : 1);
+  static constexpr float SHIFT = F16 ? 10.f : 0.f;  // p is held as 2^SHIFT p
   static constexpr int TRAIL = 32;          // bytes behind a ring slot: scales of the keys, of the
                                             // values, and whether there is a block, per 16 keys
 };
 template <int KIND, int DP>
-__host__ __device__ constexpr int ring_stages() { return (KIND == TK_F32 || KIND == TK_E4M3) && DP == 128 ? 3 : 4; }
+__host__ __device__ constexpr int ring_stages() { return DP == 128 && KIND != TK_E4M3_F32 ? 3 : 4; }
 template <int KIND, int DP>
 __host__ __device__ constexpr size_t token_smem() {
   return (size_t)TNW * ring_stages<KIND, DP>() * (2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + Kind<KIND>::TRAIL);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -90,19 +81,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
   return r;
-}
-// four values (|x| <= 448) as four e4m3 bytes, and 16 times what those leave as four more
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
-         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
-}
-__device__ __forceinline__ void split_e4(float a, float b, float c, float d, uint32_t* hi, uint32_t* lo) {
-  const uint32_t h = e4m3x4(a, b, c, d);
-  const uint32_t w0 = e4m3x2_f16(h), w1 = e4m3x2_f16(h >> 16);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w0));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w1));
-  *hi = h;
-  *lo = e4m3x4((a - x.x) * 16.f, (b - x.y) * 16.f, (c - y.x) * 16.f, (d - y.y) * 16.f);
 }
 // two fp32 as PARTS 16-bit parts, the parts' sum nearest to them
 template <int KIND>
@@ -167,22 +145,57 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
   extern __shared__ __align__(128) uint8_t ring[];
   const WinArgs& a = t.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tq = lane & 3;
-  const int sp = blockIdx.x % t.splits;
-  const int rt = (blockIdx.x / t.splits) % t.rtiles;
-  const int hk = (blockIdx.x / (t.splits * t.rtiles)) % a.Hkv;
-  const int b = blockIdx.x / (t.splits * t.rtiles * a.Hkv);
-  const int R = a.g * a.Nq;
-  WinSeq sq = win_seq(a, b);
-  if (!a.q_pos && t.table) sq.qp = sq.len - a.Nq;
+  const int R = a.g * a.Nq, heads = a.Hkv * t.rtiles;
+  // the groups of sequence b: first tokens' groups, then the window's
+  auto seq_of = [&](int b) {
+    WinSeq q = win_seq(a, b);
+    if (!a.q_pos && t.table) q.qp = q.len - a.Nq;
+    return q;
+  };
+  auto groups_of = [&](const WinRange& r) {
+    return (r.S + GK - 1) / GK + (r.hi > r.lo ? (r.hi + GK - 1) / GK - r.lo / GK : 0);
+  };
+  // ---- this block's share: every warp goes over the sequences ----
+  // shares of at most L groups; L such that all shares run at once where more
+  // blocks do than there are rows to share out
+  long long total = 0;
+  for (int b = lane; b < a.B; b += 32) total += groups_of(win_keys(a, seq_of(b), 0, a.Nq));
+#pragma unroll
+  for (int k = 16; k; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+  const int rows = a.B * heads;
+  const int want = t.slots > 2 * rows ? t.slots - rows : t.slots;
+  const int L = max(2 * TNW, (int)((total * heads + want - 1) / want));
+  int base = 0, b = -1, share = 0, shares = 1;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int n = b0 + lane < a.B ? max(1, (groups_of(win_keys(a, seq_of(b0 + lane), 0, a.Nq)) + L - 1) / L) : 0;
+    int upto = n;                     // shares of one (head, row tile), up to this sequence
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += x;
+    }
+    const bool mine = n > 0 && (int)blockIdx.x >= base + (upto - n) * heads && (int)blockIdx.x < base + upto * heads;
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      b = b0 + src;
+      shares = __shfl_sync(0xffffffffu, n, src);
+      share = blockIdx.x - (base + (__shfl_sync(0xffffffffu, upto, src) - shares) * heads);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, upto, 31) * heads;
+  }
+  if (b < 0) return;                  // more blocks than shares
+  const int sp = share % shares, hr = share / shares;
+  const int hk = hr / t.rtiles, rt = hr - hk * t.rtiles;
+  const WinSeq sq = seq_of(b);
   const WinRange kr = win_keys(a, sq, 0, a.Nq);
   // keys [free_lo, free_hi) (or first tokens) are seen by every query: no mask
   const bool rows_ok = sq.qp >= 0 && sq.qp + a.Nq <= sq.len;
   const int free_lo = sq.qp + a.Nq - 1 - a.left, free_hi = rows_ok ? min(sq.len, sq.qp + a.right + 1) : -1;
-
-  // this block's share of the groups: first tokens' groups, then the window's
-  const int gs = (kr.S + GK - 1) / GK, w0 = kr.lo / GK;
-  const int G = gs + (kr.hi > kr.lo ? (kr.hi + GK - 1) / GK - w0 : 0);
-  const int g0 = (int)((long long)G * sp / t.splits), g1 = (int)((long long)G * (sp + 1) / t.splits);
+  const int gs = (kr.S + GK - 1) / GK, w0 = kr.lo / GK, G = groups_of(kr);
+  const int g0 = (int)((long long)G * sp / shares), g1 = (int)((long long)G * (sp + 1) / shares);
+  if (sp == 0 && tid == 0) t.info[b * heads + hr] = make_int2(blockIdx.x, shares);
 
   uint8_t* my = ring + warp * NST * SLOT;
   const uint32_t my_s = smem_addr(my);
@@ -205,7 +218,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
     group(gi, &j0, &jb, &je);
 #pragma unroll
     for (int h = 0; h < NH; ++h)
-      blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)b * t.max_blocks + (j0 + 16 * h) / t.T] : -1;
+      blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)b * t.max_blocks + ((j0 + 16 * h) >> t.Tshift)] : -1;
   };
   // copies of group gi into ring slot st
   auto issue = [&](int gi, int st, const int (&blk)[NH]) {
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         there[h] = (unsigned)blk[h] < (unsigned)t.blocks;
         if (!there[h] && lane == 0 && has_keys(j0 + 16 * h, jb, je)) atomicOr(t.err, 2);
         const size_t bh = (size_t)(there[h] ? blk[h] : 0) * a.Hkv + hk;
-        tok[h] = bh * t.T + (j0 + 16 * h) % t.T;
+        tok[h] = (bh << t.Tshift) + ((j0 + 16 * h) & ((1 << t.Tshift) - 1));
         if (lane == 0) {
           cp_async4(dst + STG + 4 * h, t.k_scale + bh);
           cp_async4(dst + STG + 8 + 4 * h, t.v_scale + bh);
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
   // the rows this thread meets: gid and gid + 8 of the tile
   WinRow row[2];
   float qs[2];                       // score factor of the row
-  uint32_t qf[NP][X::E4 ? DP / 32 : KS][4];
+  uint32_t qf[NP][KS][4];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int rr = rt * 16 + gid + 8 * r;
@@ -295,36 +308,31 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
     }
     float down = 1.f;
     qs[r] = a.scale_log2;
-    if constexpr (X::F16 || X::E4) {
+    if constexpr (X::F16) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - X::QEXP;
+      // the largest feature to [2^13, 2^14)
+      const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
       if (mx > 0.f && mx < INFINITY) {
         const int h = max(-126, min(126, -ex));
         down = __uint_as_float((uint32_t)(h + 127) << 23);
         qs[r] *= __uint_as_float((uint32_t)(127 - h) << 23);
       }
     }
-    if constexpr (X::E4) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s)   // step s / 2: its first (a0, a1) or second (a2, a3) four
-        split_e4(x[s].x * down, x[s].y * down, x[s].z * down, x[s].w * down,
-                 &qf[0][s >> 1][2 * (s & 1) + r], &qf[1][s >> 1][2 * (s & 1) + r]);
-    } else {
+    for (int s = 0; s < KS; ++s) {
+      uint32_t w[NP];
+      split<KIND>(x[s].x * down, x[s].y * down, w);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint32_t w[NP];
-        split<KIND>(x[s].x * down, x[s].y * down, w);
+      for (int p = 0; p < NP; ++p) qf[p][s][r] = w[p];
+      split<KIND>(x[s].z * down, x[s].w * down, w);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) qf[p][s][r] = w[p];
-        split<KIND>(x[s].z * down, x[s].w * down, w);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = w[p];
-      }
+      for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = w[p];
     }
   }
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float vref = 1.f;                  // reference of the values' scales: v = vref x what o holds
   float o[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -358,52 +366,45 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         all = all && there[h];
       }
     }
-    if constexpr (NH == 2) {           // (its P is 0: any finite scale will do)
-      if (!there[0]) vsc[0] = there[1] ? vsc[1] : 0.f;
-      if (!there[1]) vsc[1] = vsc[0];
-    } else if (!there[0]) {
-      vsc[0] = 0.f;
-    }
     // ---- scores ----
     float s[NU][4];
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
-      float s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < DP / 4 / PIECE; ++i) {
+    for (int i = 0; i < DP / 4 / PIECE; ++i) {
+      uint32_t w[NU][4];
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
         const uint4 kv = *reinterpret_cast<const uint4*>(Kt + k_off<RB>(8 * u + gid, tq + 4 * i));
-        const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
-        if constexpr (KIND == TK_F32) {
+        w[u][0] = kv.x; w[u][1] = kv.y; w[u][2] = kv.z; w[u][3] = kv.w;
+      }
+      if constexpr (KIND == TK_F32) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
           uint32_t p0[3], p1[3];
-          split3_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1]), p0);
-          split3_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3]), p1);
+          split3_bf16x2(__uint_as_float(w[u][0]), __uint_as_float(w[u][1]), p0);
+          split3_bf16x2(__uint_as_float(w[u][2]), __uint_as_float(w[u][3]), p1);
 #pragma unroll
           for (int x = 2; x >= 0; --x)
 #pragma unroll
             for (int y = 0; y <= x; ++y) mma_bf(s[u], qf[y][i], p0[x - y], p1[x - y]);
-        } else if constexpr (KIND == TK_BF16) {
-          mma_bf(s[u], qf[0][2 * i], w[0], w[1]);
-          mma_bf(s[u], qf[0][2 * i + 1], w[2], w[3]);
-        } else if constexpr (X::E4) {
+        }
+      } else if constexpr (KIND == TK_BF16) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            mma_e4(s[u], qf[0][2 * i + x], w[2 * x], w[2 * x + 1]);
-            mma_e4(s1, qf[1][2 * i + x], w[2 * x], w[2 * x + 1]);
-          }
-        } else {
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t b0 = e4m3x2_f16(w[x]), b1 = e4m3x2_f16(w[x] >> 16);
+          for (int u = 0; u < NU; ++u) mma_bf(s[u], qf[0][2 * i + x], w[u][2 * x], w[u][2 * x + 1]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const uint32_t b0 = e4m3x2_f16(w[u][x]), b1 = e4m3x2_f16(w[u][x] >> 16);
 #pragma unroll
             for (int p = NP - 1; p >= 0; --p) mma_f16(s[u], qf[p][4 * i + x], b0, b1);
           }
-        }
-      }
-      if constexpr (X::E4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[u][e] = fmaf(s1[e], 0.0625f, s[u][e]);
       }
     }
     // ---- softmax, running maximum and sum ----
@@ -459,80 +460,52 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       }
     }
     // ---- P V ----
-    if constexpr (X::E4) {
-      // the k of a thread: keys 2 tq, 2 tq + 1 of the group's four runs of 8
-      uint32_t pf[2][4];
+    if constexpr (X::F16) {
+      // p (v_scale / reference): the reference follows a larger scale at once, and
+      // a smaller one below 2^-16 of it (one below 2^-64, as of a block of zeros,
+      // adds less than fp32 holds beside what it was set for)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < NH; ++h) {
+        if (!there[h]) continue;
+        const float r = vsc[h] / vref;
+        if (r > 1.f || (r < 0x1p-16f && r >= 0x1p-64f)) {
+          const float x = vref / vsc[h];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          split_e4(p[2 * h][2 * r], p[2 * h][2 * r + 1], p[2 * h + 1][2 * r], p[2 * h + 1][2 * r + 1],
-                   &pf[0][2 * h + r], &pf[1][2 * h + r]);
-      // halves of unlike scale (blocks of 16 tokens) go one after the other
-      const bool apart = vsc[0] != vsc[1];
-#pragma unroll 1
-      for (int pass = 0; pass <= (int)apart; ++pass) {
-        uint32_t pa[2][4];
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pa[x][e] = apart && (e >> 1) != pass ? 0u : pf[x][e];
-        const float vs = pass ? vsc[1] : vsc[0], vs1 = vs * 0.0625f;
-        constexpr int W = DP / 8 / 4;  // 32-bit words of a thread's piece of a value row
-        uint32_t v[8][W];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rr = 8 * (e >> 1) + 2 * tq + (e & 1);
-          if constexpr (W == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
-            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(Vt + v_off<RB>(rr, gid >> 1) + 8 * (gid & 1));
-            v[e][0] = x.x; v[e][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          uint32_t bt[2][4];           // four keys of each of the word's four columns
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x0 = __byte_perm(v[4 * h][w], v[4 * h + 1][w], 0x5140);
-            const uint32_t x1 = __byte_perm(v[4 * h + 2][w], v[4 * h + 3][w], 0x5140);
-            const uint32_t y0 = __byte_perm(v[4 * h][w], v[4 * h + 1][w], 0x7362);
-            const uint32_t y1 = __byte_perm(v[4 * h + 2][w], v[4 * h + 3][w], 0x7362);
-            bt[h][0] = __byte_perm(x0, x1, 0x5410);
-            bt[h][1] = __byte_perm(x0, x1, 0x7632);
-            bt[h][2] = __byte_perm(y0, y1, 0x5410);
-            bt[h][3] = __byte_perm(y0, y1, 0x7632);
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4(c0, pa[0], bt[0][x], bt[1][x]);
-            mma_e4(c1, pa[1], bt[0][x], bt[1][x]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[4 * w + x][e] = fmaf(c0[e], vs, fmaf(c1[e], vs1, o[4 * w + x][e]));
-          }
+            for (int e = 0; e < 4; ++e) o[n][e] *= x;
+          vref = vsc[h];
         }
       }
-    } else {
-      uint32_t pf[NP][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int h = 0; h < NH; ++h) {
+        const float r = there[h] ? vsc[h] / vref : 0.f;
+        if (r != 1.f) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t w[NP];
-          split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
+          for (int u = 2 * h; u < 2 * h + 2; ++u)
 #pragma unroll
-          for (int x = 0; x < NP; ++x) pf[x][2 * u + r] = w[x];
+            for (int e = 0; e < 4; ++e) p[u][e] *= r;
         }
-      if constexpr (KIND == TK_E4M3_F32) {
-        constexpr int W = DP / 8 / 4;
+      }
+    }
+    uint32_t pf[NP][NU / 2][4];
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t w[NP];
+        split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
+#pragma unroll
+        for (int x = 0; x < NP; ++x) pf[x][u >> 1][2 * (u & 1) + r] = w[x];
+      }
+#pragma unroll
+    for (int g = 0; g < NU / 2; ++g) {     // 16 keys each
+      if constexpr (X::F16) {
+        constexpr int W = DP / 8 / 4;  // 32-bit words of a thread's piece of a value row
         uint32_t v[4][W];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
+          const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
           if constexpr (W == 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
@@ -546,11 +519,8 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
           const int sel = (n & 3) | (((n & 3) + 4) << 4);
           const uint32_t b0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], sel));
           const uint32_t b1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], sel));
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int x = NP - 1; x >= 0; --x) mma_f16(c, pf[x], b0, b1);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] = fmaf(c[e], vsc[0], o[n][e]);
+          for (int x = NP - 1; x >= 0; --x) mma_f16(o[n], pf[x][g], b0, b1);
         }
       } else if constexpr (KIND == TK_BF16) {
         constexpr int W = DP / 16;
@@ -559,14 +529,14 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
           uint32_t v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
+            const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
             const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid * (W / 4) + h));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             const int sel = n & 1 ? 0x7632 : 0x5410;
-            mma_bf(o[8 * h + n], pf[0], __byte_perm(v[0][n >> 1], v[1][n >> 1], sel),
+            mma_bf(o[8 * h + n], pf[0][g], __byte_perm(v[0][n >> 1], v[1][n >> 1], sel),
                    __byte_perm(v[2][n >> 1], v[3][n >> 1], sel));
           }
         }
@@ -576,7 +546,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
           float v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int rr = 2 * tq + (e & 1) + 8 * (e >> 1);
+            const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
             const float4 x = *reinterpret_cast<const float4*>(Vt + v_off<RB>(rr, gid * (DP / 32) + h));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
@@ -588,7 +558,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
 #pragma unroll
             for (int x = 2; x >= 0; --x)
 #pragma unroll
-              for (int y = 0; y <= x; ++y) mma_bf(o[4 * h + n], pf[y], b0[x - y], b1[x - y]);
+              for (int y = 0; y <= x; ++y) mma_bf(o[4 * h + n], pf[y][g], b0[x - y], b1[x - y]);
           }
         }
       }
@@ -596,6 +566,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
     if (++st == NST) st = 0;
   }
   cp_wait_all();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -612,8 +583,8 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
     float* dst = So + (warp * 16 + gid + 8 * r) * DP;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      dst[2 * tq * NT + n] = o[n][2 * r];
-      dst[(2 * tq + 1) * NT + n] = o[n][2 * r + 1];
+      dst[2 * tq * NT + n] = o[n][2 * r] * vref;
+      dst[(2 * tq + 1) * NT + n] = o[n][2 * r + 1] * vref;
     }
     if (tq == 0) {
       Sm[warp * 16 + gid + 8 * r] = m[r];
@@ -640,61 +611,85 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       acc.z = fmaf(x.z, f, acc.z); acc.w = fmaf(x.w, f, acc.w);
     }
     const size_t qrow = ((size_t)b * a.Hq + hk * a.g + rr / a.Nq) * a.Nq + rr % a.Nq;
-    if (t.splits == 1) {
+    if (shares == 1) {
       const float w = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
       st4((TQ*)a.out + qrow * a.d + c, make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w));
       if (a.lse && c == 0) a.lse[qrow] = sum == 0.f ? -INFINITY : mx + log2f(sum) - X::SHIFT;
     } else {
-      const size_t part = qrow * t.splits + sp;
+      const size_t part = (size_t)blockIdx.x * 16 + r;
       st4(t.part_o + part * a.d + c, acc);
       if (c == 0) t.part_ml[part] = make_float2(mx, sum);
     }
   }
 }
 
-// out = sum over a row's shares, one warp a row
+// out = sum over a row's shares: a block a row, its warps take shares in turn
 template <typename TQ>
 __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
+  __shared__ __align__(16) float So[4][128];
+  __shared__ float Sm[4], Sl[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while k_token still ran
   const WinArgs& a = t.w;
-  const long long rows = (long long)a.B * a.Hq * a.Nq;
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  const float2* ml = t.part_ml + r * t.splits;
+  const long long qrow = blockIdx.x;                     // (b, query head, query)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = 4 * lane;
+  const int i = (int)(qrow % a.Nq), hq = (int)(qrow / a.Nq % a.Hq), b = (int)(qrow / a.Nq / a.Hq);
+  const int rr = (hq % a.g) * a.Nq + i;
+  const int2 in = t.info[((size_t)b * a.Hkv + hq / a.g) * t.rtiles + rr / 16];
+  if (in.y == 1) return;                                 // written already
+  const size_t row0 = (size_t)in.x * 16 + rr % 16;
   float mx = -INFINITY;
-  for (int s = lane; s < t.splits; s += 32) mx = fmaxf(mx, ml[s].x);
+  for (int s = lane; s < in.y; s += 32) mx = fmaxf(mx, t.part_ml[row0 + (size_t)s * 16].x);
 #pragma unroll
   for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
   const float mu = mx == -INFINITY ? 0.f : mx;
-  const int c = 4 * lane;
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < t.splits; ++s) {
-    const float2 x = ml[s];
+  for (int s = warp; s < in.y; s += 4) {
+    const size_t row = row0 + (size_t)s * 16;
+    const float2 x = t.part_ml[row];
     const float f = exp2f(x.x - mu);
     sum = fmaf(x.y, f, sum);
     if (c < a.d) {
-      const float4 v = ld4(t.part_o + (r * t.splits + s) * a.d + c);
+      const float4 v = *reinterpret_cast<const float4*>(t.part_o + row * a.d + c);
       acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
     }
   }
+  st4(&So[warp][c], acc);
+  if (lane == 0) Sl[warp] = sum;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const float4 v = lds4(&So[w][c]);
+    sum += Sl[w];
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+  }
   const float w = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
   if (c < a.d)
-    st4((TQ*)a.out + r * a.d + c, make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w));
-  if (a.lse && lane == 0) a.lse[r] = sum == 0.f ? -INFINITY : mx + log2f(sum) - shift;
+    st4((TQ*)a.out + qrow * a.d + c, make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w));
+  if (a.lse && lane == 0) a.lse[qrow] = sum == 0.f ? -INFINITY : mx + log2f(sum) - shift;
 }
 
 namespace {
-// the shares of a row tile's keys: about three blocks for each that fits at once
-// (so that short and long sequences of a batch even out), each share at least
-// two groups a warp.  From the dimensions alone.
-int shares(int blocks, long long keys) {
-  const long long most = (keys / 16 + 2 * TNW - 1) / (2 * TNW);
-  long long s = (152 * 6 + blocks - 1) / blocks;
-  s = s > most ? most : s;
-  return (int)(s < 1 ? 1 : (s > 256 ? 256 : s));
+// blocks of k_token that run at once, by their shared memory (227 KB an SM, 1 KB
+// a block for the system)
+template <int KIND, int DP>
+constexpr int blocks_per_sm() { return (int)(232448 / (token_smem<KIND, DP>() + 1024)); }
+
+int slots_of(int kind, int d) {
+  const int sms = 152;   // from the type alone: workspaces do not depend on the device
+  switch (kind) {
+    case TK_BF16: return sms * (d <= 64 ? blocks_per_sm<TK_BF16, 64>() : blocks_per_sm<TK_BF16, 128>());
+    case TK_E4M3: return sms * (d <= 64 ? blocks_per_sm<TK_E4M3, 64>() : blocks_per_sm<TK_E4M3, 128>());
+    case TK_E4M3_F32:
+      return sms * (d <= 64 ? blocks_per_sm<TK_E4M3_F32, 64>() : blocks_per_sm<TK_E4M3_F32, 128>());
+    default: return sms * (d <= 64 ? blocks_per_sm<TK_F32, 64>() : blocks_per_sm<TK_F32, 128>());
+  }
+}
+int kind_of(bool cache, bool bf16) {
+  return cache ? (bf16 ? TK_E4M3 : TK_E4M3_F32) : (bf16 ? TK_BF16 : TK_F32);
 }
 
 template <int KIND, int DP>
@@ -706,29 +701,34 @@ cudaError_t go(TokenArgs& t, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess || (e = once.allow(k_token<KIND, DP>, smem, dev)) != cudaSuccess) return e;
-  const long long n = (long long)t.w.B * t.w.Hkv * t.rtiles * t.splits;
-  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)n), dim3(32 * TNW), smem, st, t);
-  if (e != cudaSuccess || t.splits == 1) return e;
+  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW), smem, st, t);
+  if (e != cudaSuccess || !t.joined) return e;
   const long long rows = (long long)t.w.B * t.w.Hq * t.w.Nq;
-  return launch("token_join", k_token_join<TQ>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, t,
-                Kind<KIND>::SHIFT);
+  return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(128), 0, st, t,
+                      Kind<KIND>::SHIFT);
 }
 }  // namespace
 
-TokenShape token_shape(int B, int Hkv, int g, int Nq, int d, long long keys, int left, int right,
-                       int sinks) {
+TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int d, long long keys,
+                       int left, int right, int sinks) {
   TokenShape s;
   s.rtiles = (g * Nq + 15) / 16;
+  s.slots = slots_of(kind_of(cache, bf16), d);
+  // groups of a sequence at the most, and so blocks: a share holds at least two
+  // groups a warp, shares are at most `slots` beyond one for each row tile
   long long seen = keys;
   if (left < kWinUnbounded && right < kWinUnbounded) {
     const long long w = (long long)left + right + Nq + sinks + 64;
     if (w < seen) seen = w;
   }
-  const long long blocks = (long long)B * Hkv * s.rtiles;
-  s.splits = shares((int)(blocks < 1 << 20 ? blocks : 1 << 20), seen);
-  const size_t rows = (size_t)B * Hkv * g * Nq;
-  s.o_bytes = s.splits == 1 ? 0 : rows * s.splits * d * 4;
-  s.ml_bytes = s.splits == 1 ? 0 : rows * s.splits * 8;
+  const long long groups = seen / 16 + 3, rows = (long long)B * Hkv * s.rtiles;
+  const long long most = (groups + 2 * TNW - 1) / (2 * TNW);
+  s.grid = rows * (most < 1 ? 1 : most);
+  if (s.grid > rows + s.slots) s.grid = rows + s.slots;
+  s.joined = most > 1;
+  s.o_bytes = s.joined ? (size_t)s.grid * 16 * d * 4 : 0;
+  s.ml_bytes = s.joined ? (size_t)s.grid * 16 * 8 : 0;
+  s.info_bytes = (size_t)rows * 8;
   return s;
 }
 

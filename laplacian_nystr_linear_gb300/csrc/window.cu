@@ -44,9 +44,23 @@ int check_dims(WinArgs& a, int B, int Hq, int Hkv, int Nq, int Nk, int d) {
 // keys once for 16 rows (query heads of a group x queries).
 bool few(int g, int Nq) { return Nq <= 8 || g * Nq <= 16; }
 
+// a workspace's parts for k_token.cu
+size_t token_bytes(const TokenShape& s) {
+  return align256(s.o_bytes) + align256(s.ml_bytes) + align256(s.info_bytes);
+}
+void token_parts(TokenArgs& t, const TokenShape& s, void* ws) {
+  uint8_t* p = (uint8_t*)ws;
+  t.rtiles = s.rtiles;
+  t.slots = s.slots;
+  t.grid = s.grid;
+  t.joined = s.joined;
+  t.part_o = (float*)p;
+  t.part_ml = (float2*)(p + align256(s.o_bytes));
+  t.info = (int2*)(p + align256(s.o_bytes) + align256(s.ml_bytes));
+}
+
 struct WinWs {
-  TokenShape tok;
-  size_t o, ml;                 // forward, few queries
+  TokenShape tok;               // forward, few queries
   size_t D, part;               // backward
   int stiles, chunks, chunk_rows;
   size_t total;
@@ -55,15 +69,16 @@ struct WinWs {
 // rows of the backward's key tiles: bf16 on the tensor cores, fp32 on the FP32 pipe
 int tile_rows(int dtype) { return dtype == LAPNYS_BF16 ? win_tc_tile_rows() : win_tile_rows(); }
 
-WinWs window_ws(const WinArgs& a, bool backward, int tile) {
+WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
+  const int tile = tile_rows(dtype);
   WinWs w;
   memset(&w, 0, sizeof(w));
   size_t o = 0;
   if (!backward) {
     if (few(a.g, a.Nq)) {
-      w.tok = token_shape(a.B, a.Hkv, a.g, a.Nq, a.d, a.Nk, a.left, a.right, a.sinks);
-      w.o = o; o = align256(o + w.tok.o_bytes);
-      w.ml = o; o = align256(o + w.tok.ml_bytes);
+      w.tok = token_shape(false, dtype == LAPNYS_BF16, a.B, a.Hkv, a.g, a.Nq, a.d, a.Nk, a.left,
+                          a.right, a.sinks);
+      o = token_bytes(w.tok);
     }
   } else {
     w.D = o; o = align256(o + (size_t)a.B * a.Hq * a.Nq * 4);
@@ -133,7 +148,7 @@ size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int
   WinArgs a;
   memset(&a, 0, sizeof(a));
   if (check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, 1.f, dtype) != LAPNYS_OK) return 0;
-  return window_ws(a, backward != 0, tile_rows(dtype)).total;
+  return window_ws(a, backward != 0, dtype).total;
 }
 
 int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
@@ -149,15 +164,12 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
       !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
     return LAPNYS_EINVAL;
-  const WinWs w = window_ws(a, false, tile_rows(dtype));
+  const WinWs w = window_ws(a, false, dtype);
   if (w.total > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
   if (few(a.g, Nq)) {
-    t.rtiles = w.tok.rtiles;
-    t.splits = w.tok.splits;
-    t.part_o = (float*)((uint8_t*)ws + w.o);
-    t.part_ml = (float2*)((uint8_t*)ws + w.ml);
+    token_parts(t, w.tok, ws);
     return status(run_token(t, dtype == LAPNYS_BF16, stream));
   }
   if (dtype == LAPNYS_BF16) return status(run_win_fwd_tc(a, stream));
@@ -178,7 +190,7 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
   for (const void* p : all)
     if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
   if (!lse || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4)) return LAPNYS_EINVAL;
-  const WinWs w = window_ws(a, true, tile_rows(dtype));
+  const WinWs w = window_ws(a, true, dtype);
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = const_cast<void*>(out); a.dout = dout;
   a.lse = const_cast<float*>(lse); a.lens = lens; a.q_pos = q_pos;
@@ -224,8 +236,8 @@ size_t lapnys_cache_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int b
   memset(&a, 0, sizeof(a));
   if (check_cache(a, B, Hq, Hkv, Nq, d, block, blocks, max_blocks, dtype) != LAPNYS_OK) return 0;
   if (check_mask(a, left, right, sinks, 1.f) != LAPNYS_OK) return 0;
-  const TokenShape s = token_shape(B, Hkv, a.g, Nq, d, a.Nk, a.left, a.right, a.sinks);
-  return align256(s.o_bytes) + align256(s.ml_bytes);
+  return token_bytes(token_shape(true, dtype == LAPNYS_BF16, B, Hkv, a.g, Nq, d, a.Nk, a.left,
+                                 a.right, a.sinks));
 }
 
 int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -248,17 +260,16 @@ int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cac
   for (const void* p : words)
     if (!p || !aligned(p, 4)) return LAPNYS_EINVAL;
   if (!aligned(q_pos, 4)) return LAPNYS_EINVAL;
-  const TokenShape s = token_shape(B, Hkv, a.g, Nq, d, a.Nk, a.left, a.right, a.sinks);
-  const size_t need = align256(s.o_bytes) + align256(s.ml_bytes);
+  const TokenShape s = token_shape(true, dtype == LAPNYS_BF16, B, Hkv, a.g, Nq, d, a.Nk, a.left,
+                                   a.right, a.sinks);
+  const size_t need = token_bytes(s);
   if (need > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
   if (ws_bytes < need) return LAPNYS_ENOSPC;
   a.q = q; a.k = k_cache; a.v = v_cache; a.out = out; a.lens = lens; a.q_pos = q_pos;
   t.k_scale = k_scale; t.v_scale = v_scale; t.table = table;
-  t.T = block; t.blocks = blocks; t.max_blocks = max_blocks;
-  t.rtiles = s.rtiles;
-  t.splits = s.splits;
-  t.part_o = (float*)ws;
-  t.part_ml = (float2*)((uint8_t*)ws + align256(s.o_bytes));
+  t.Tshift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  t.blocks = blocks; t.max_blocks = max_blocks;
+  token_parts(t, s, ws);
   t.err = wait_error_address();
   if (t.err == nullptr) return LAPNYS_ECUDA;
   return status(run_token(t, dtype == LAPNYS_BF16, stream));
