@@ -188,6 +188,11 @@ bool encode_tiled_f32_sw128(CUtensorMap* t, int rank, const void* p, const cuuin
 bool encode_tiled_bf16_sw128(CUtensorMap* t, int rank, const void* p, const cuuint64_t* dim,
                              const cuuint64_t* stride, const cuuint32_t* box);
 
+// a map {d, N, outer} of elements of 1 (bytes), 2 (bf16) or 4 (fp32) bytes, boxes
+// of `row_bytes` (64 or 128, swizzled alike) x `rows`
+bool encode_tiled_rows(CUtensorMap* t, const void* p, int es, int d, int N, long long outer,
+                       int row_bytes, int rows);
+
 // ---- bf16 products of the attention block (k_proj.cu) ---------------------
 // Geometry: B batch entries of N tokens, embedding width C, H heads of d, S
 // projection blocks (3, or 2 when Q = K).  Operand sources (bf16):
@@ -367,18 +372,14 @@ struct TokenArgs {
   const float* v_scale;
   const int32_t* table;    // [B][max_blocks]
   int Tshift, blocks, max_blocks;  // log2 of a block's tokens
-  int rtiles, slots;       // row tiles of 16; blocks to fill
-  long long grid;
-  bool joined;             // some rows may be shared out
-  float* part_o;           // [block][16][d]
-  float2* part_ml;         // [block][16]: maximum, sum
-  int2* info;              // [B][Hkv][rtiles]: first block, shares
-  int* err;                // bit 1: a table named a block that is not there
+  int rtiles, grid;        // row tiles of 16; blocks
+  float* part_o;           // [parts][16][d], parts = rows + warps
+  float2* part_ml;         // [parts][16]: maximum, sum
+  int2* info;              // [rows]: the warps of its first and last part
+  int* err;                // bit 0: a wait expired; bit 1: a table named a block that is not there
 };
 struct TokenShape {
-  int rtiles, slots;
-  long long grid;
-  bool joined;
+  int rtiles, grid;
   size_t o_bytes, ml_bytes, info_bytes;
 };
 TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int d, long long keys,

@@ -701,6 +701,21 @@ bool encode_tiled_f32_sw128(CUtensorMap* t, int rank, const void* p, const cuuin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tiled_rows(CUtensorMap* t, const void* p, int es, int d, int N, long long outer,
+                       int row_bytes, int rows) {
+  EncodeTiled fn = encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)outer};
+  const cuuint64_t stride[2] = {(cuuint64_t)d * es, (cuuint64_t)N * d * es};
+  const cuuint32_t box[3] = {(cuuint32_t)(row_bytes / es), (cuuint32_t)rows, 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(t, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                       : (es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8),
+            3, const_cast<void*>(p), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tiled_bf16_sw128(CUtensorMap* t, int rank, const void* p, const cuuint64_t* dim,
                              const cuuint64_t* stride, const cuuint32_t* box) {
   EncodeTiled fn = encoder();

@@ -5,21 +5,21 @@
 //
 // What bounds it: every visible key and value is read once, for all the query
 // heads that share it, and nothing else is large.  So the work is split over the
-// keys: a block takes one (sequence, key head, 16 query rows) and one contiguous
-// share of the visible groups of 16 or 32 keys, its warps take groups in turn, each
-// with a ring of asynchronous copies of its own (no block barrier in the loop),
-// and k_token_join adds the shares.  Shares are cut on the device, from all
-// sequences' lengths, so that they are alike in a ragged batch and, where it can
-// be, all blocks run at once: a block's start and end (dependent loads of the
-// lengths, the table, the queries; the join of its warps) cost 4 us, as much as
-// 0.2 MB of cache.
+// keys, evenly and finely: the visible groups of 16 or 32 keys of all rows (a row:
+// one sequence, one key head, 16 query rows) are laid end to end, and each warp
+// takes one equal stretch, whatever the sequences' lengths are.  A warp keeps a
+// ring of TMA copies of its own that runs on across rows (no block barrier
+// anywhere), and leaves maximum, sum and output of each row that it met for
+// k_token_join.  Blocks that shared rows out by themselves lost 8 us a wave to
+// their start and end and, on ragged batches, a second wave (32 sequences, 8192
+// tokens at the most: 110 us).
 //
 // Products on the warp-level tensor instruction (m16n8k16), rows = (query head
 // of the group, query), with the contraction's order chosen so that no operand
 // is transposed or gathered: a thread's four k of step s are four neighbouring
 // features (scores), and column n of output step nt is feature n DP / 8 + nt
 // (P V), so both operands come from shared memory in 16-byte reads without bank
-// conflicts (the swizzles below).
+// conflicts (rows of 128 bytes in TMA's 128-byte swizzle).
 //   - 8-bit: e4m3 -> f16 is exact (one instruction for two; the e4m3 form of the
 //     product is no instruction of its own here: it ran as two f16 ones with more
 //     conversions, 1576 instructions for 32 keys against about 600).  q is scaled
@@ -36,7 +36,7 @@
 
 #include "common.cuh"
 #include "internal.h"
-#include "win.cuh"
+#include "win_tc.cuh"
 
 namespace lapnys {
 
@@ -52,14 +52,12 @@ struct Kind {
   static constexpr int GK = KIND == TK_E4M3 ? 32 : 16;                  // keys of a group
   static constexpr int PARTS = KIND == TK_F32 ? 3 : (KIND == TK_E4M3_F32 ? 2 : 1);
   static constexpr float SHIFT = F16 ? 10.f : 0.f;  // p is held as 2^SHIFT p
-  static constexpr int TRAIL = 32;          // bytes behind a ring slot: scales of the keys, of the
-                                            // values, and whether there is a block, per 16 keys
 };
 template <int KIND, int DP>
 __host__ __device__ constexpr int ring_stages() { return DP == 128 && KIND != TK_E4M3_F32 ? 3 : 4; }
 template <int KIND, int DP>
-__host__ __device__ constexpr size_t token_smem() {
-  return (size_t)TNW * ring_stages<KIND, DP>() * (2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + Kind<KIND>::TRAIL);
+__host__ __device__ constexpr size_t token_smem() {   // rings from a multiple of 1024 bytes on
+  return (size_t)TNW * ring_stages<KIND, DP>() * 2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + 1024;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -102,257 +100,338 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[Kind<KIND>
   }
 }
 
-// byte offset of a row's 16-byte chunk in a tile of rows of RB bytes.  A key
-// row is read 16 bytes per thread at chunk t + 4 i of rows gid (t = lane % 4,
-// gid = lane / 4): odd rows swap their halves.
-template <int RB>
-__device__ __forceinline__ uint32_t k_off(int row, int c) {
-  return (uint32_t)(row * RB + ((RB >= 128 ? c ^ ((row & 1) << 2) : c) << 4));
+// Byte offset of a row's 16-byte chunk c in a tile of GK rows of RB bytes, as TMA
+// leaves it: panels of 128 bytes a row, chunks XORed with the row mod 8 (rows of
+// 64 bytes: with half the row mod 4).
+// A key row is read at chunks 2 t, 2 t + 1 of each panel (t = lane % 4) and rows
+// gid (= lane / 4), a value row at chunk gid and rows 2 t + const: the eight lanes
+// of a phase meet eight chunks either way.
+template <int RB, int GK>
+__device__ __forceinline__ uint32_t tile_off(int row, int c) {
+  if constexpr (RB == 64)
+    return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+  else
+    return (uint32_t)((c >> 3) * (GK * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
-// a value row is read from rows 2 t + const at chunk(s) gid.. : eight lanes of a
-// phase hold two gid and four t, spread over the eight chunks of a line
+// the chunk of a thread's i-th piece of a key row
 template <int RB>
-__device__ __forceinline__ uint32_t v_off(int row, int c) {
-  if constexpr (RB == 64) {
-    const int line = row >> 1, cc = (((row & 1) << 2) | c) ^ ((line & 3) << 1);
-    return (uint32_t)(line * 128 + (cc << 4));
-  } else if constexpr (RB == 128) {
-    return (uint32_t)(row * RB + ((c ^ (row & 6)) << 4));
-  } else if constexpr (RB == 256) {
-    return (uint32_t)(row * RB + ((c ^ (((row >> 1) & 1) | (((row >> 2) & 1) << 2))) << 4));
-  } else {
-    return (uint32_t)(row * RB + ((c ^ ((row >> 1) & 3)) << 4));
-  }
+__device__ __forceinline__ int key_chunk(int t, int i) {
+  return RB == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 }  // namespace
 
+struct TokenMaps {
+  CUtensorMap k, v;   // {d, tokens, (batch or block, head)}, boxes of a panel x a copy's rows
+};
+
 template <int KIND, int DP>
-__global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
+__global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ TokenMaps mp, const TokenArgs t) {
   using X = Kind<KIND>;
   constexpr int ES = X::ES, RB = DP * ES, NP = X::PARTS, GK = X::GK, NU = GK / 8, NH = GK / 16;
   constexpr int NST = ring_stages<KIND, DP>();
-  constexpr int TILE = GK * RB, STG = 2 * TILE, SLOT = STG + X::TRAIL;
+  constexpr int TILE = GK * RB, SLOT = 2 * TILE;
   constexpr int KS = DP / 16;                  // 16-feature steps of the scores
   constexpr int NT = DP / 8;                   // column steps of P V
   constexpr int PIECE = 16 / ES;               // features of a 16-byte piece
   constexpr int KSP = PIECE / 4;               // steps of a piece, four features a thread each
   constexpr int CH = RB / 16;                  // 16-byte chunks of a row
-  constexpr int RPI = 32 / CH;                 // rows that a warp copies at once
+  constexpr int PANELS = RB == 64 ? 1 : RB / 128;
+  constexpr int VP = RB == 64 ? 8 : PIECE;     // features of a thread's piece of a value row
   using TQ = typename std::conditional<X::QF32, float, __nv_bfloat16>::type;
-  extern __shared__ __align__(128) uint8_t ring[];
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full_s[TNW][NST];      // a ring slot's copies landed
+  __shared__ float scale_s[TNW][NST][4];                  // of its keys, of its values, per 16 keys
+  __shared__ int there_s[TNW][NST][2];                    // whether these have a block
+  uint8_t* ring = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
   const WinArgs& a = t.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tq = lane & 3;
   const int R = a.g * a.Nq, heads = a.Hkv * t.rtiles;
-  // the groups of sequence b: first tokens' groups, then the window's
   auto seq_of = [&](int b) {
     WinSeq q = win_seq(a, b);
     if (!a.q_pos && t.table) q.qp = q.len - a.Nq;
     return q;
   };
+  // the groups of a sequence: first tokens' groups, then the window's
   auto groups_of = [&](const WinRange& r) {
     return (r.S + GK - 1) / GK + (r.hi > r.lo ? (r.hi + GK - 1) / GK - r.lo / GK : 0);
   };
-  // ---- this block's share: every warp goes over the sequences ----
-  // shares of at most L groups; L such that all shares run at once where more
-  // blocks do than there are rows to share out
+  // ---- this warp's stretch of all groups: `mine` of them from `at` on ----
+  const int w = blockIdx.x * TNW + warp, W = gridDim.x * TNW;
   long long total = 0;
-  for (int b = lane; b < a.B; b += 32) total += groups_of(win_keys(a, seq_of(b), 0, a.Nq));
+  for (int b = lane; b < a.B; b += 32) {
+    const int G = groups_of(win_keys(a, seq_of(b), 0, a.Nq));
+    total += G;
+    if (G == 0 && b % W == w)          // rows that nobody meets
+      for (int h = 0; h < heads; ++h) t.info[b * heads + h] = make_int2(0, -1);
+  }
 #pragma unroll
   for (int k = 16; k; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
-  const int rows = a.B * heads;
-  const int want = t.slots > 2 * rows ? t.slots - rows : t.slots;
-  const int L = max(2 * TNW, (int)((total * heads + want - 1) / want));
-  int base = 0, b = -1, share = 0, shares = 1;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? max(1, (groups_of(win_keys(a, seq_of(b0 + lane), 0, a.Nq)) + L - 1) / L) : 0;
-    int upto = n;                     // shares of one (head, row tile), up to this sequence
+  total *= heads;
+  const int each = max(2, (int)((total + W - 1) / W));
+  const long long at = min(total, (long long)w * each);
+  const int mine = (int)min(total - at, (long long)each);
+  if (mine <= 0) return;
+  // where it begins: the sequence (a scan over them), row and group
+  int b0 = 0, hr0 = 0, gi0 = 0;
+  long long base = 0;
+  for (int c = 0; c < a.B; c += 32) {
+    const int G = c + lane < a.B ? groups_of(win_keys(a, seq_of(c + lane), 0, a.Nq)) : 0;
+    long long upto = (long long)G * heads;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, k);
+      const long long x = __shfl_up_sync(0xffffffffu, upto, k);
       if (lane >= k) upto += x;
     }
-    const bool mine = n > 0 && (int)blockIdx.x >= base + (upto - n) * heads && (int)blockIdx.x < base + upto * heads;
-    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    const uint32_t who = __ballot_sync(0xffffffffu, at < base + upto);
     if (who) {
       const int src = __ffs(who) - 1;
-      b = b0 + src;
-      shares = __shfl_sync(0xffffffffu, n, src);
-      share = blockIdx.x - (base + (__shfl_sync(0xffffffffu, upto, src) - shares) * heads);
+      const long long off = at - base - __shfl_sync(0xffffffffu, upto - (long long)G * heads, src);
+      const int row_groups = __shfl_sync(0xffffffffu, G, src);
+      b0 = c + src;
+      hr0 = (int)(off / row_groups);
+      gi0 = (int)(off - (long long)hr0 * row_groups);
       break;
     }
-    base += __shfl_sync(0xffffffffu, upto, 31) * heads;
+    base += __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (b < 0) return;                  // more blocks than shares
-  const int sp = share % shares, hr = share / shares;
-  const int hk = hr / t.rtiles, rt = hr - hk * t.rtiles;
-  const WinSeq sq = seq_of(b);
-  const WinRange kr = win_keys(a, sq, 0, a.Nq);
-  // keys [free_lo, free_hi) (or first tokens) are seen by every query: no mask
-  const bool rows_ok = sq.qp >= 0 && sq.qp + a.Nq <= sq.len;
-  const int free_lo = sq.qp + a.Nq - 1 - a.left, free_hi = rows_ok ? min(sq.len, sq.qp + a.right + 1) : -1;
-  const int gs = (kr.S + GK - 1) / GK, w0 = kr.lo / GK, G = groups_of(kr);
-  const int g0 = (int)((long long)G * sp / shares), g1 = (int)((long long)G * (sp + 1) / shares);
-  if (sp == 0 && tid == 0) t.info[b * heads + hr] = make_int2(blockIdx.x, shares);
+
+  // a place in the stretch: row (b, hr) and its group gi, and the row's ranges
+  struct Cursor {
+    int b, hr, gi, G, gs, w0;
+    WinSeq sq;
+    WinRange kr;
+  };
+  auto enter = [&](Cursor& c) {        // the row's ranges, from the next row with groups on
+    for (;;) {
+      c.sq = seq_of(c.b);
+      c.kr = win_keys(a, c.sq, 0, a.Nq);
+      c.G = groups_of(c.kr);
+      if (c.G > 0) break;
+      ++c.b;                           // (the stretch ends before the last sequence does)
+    }
+    c.gs = (c.kr.S + GK - 1) / GK;
+    c.w0 = c.kr.lo / GK;
+  };
+  auto step = [&](Cursor& c) {         // true: another row
+    if (++c.gi < c.G) return false;
+    c.gi = 0;
+    if (++c.hr == heads) {
+      c.hr = 0;
+      ++c.b;
+    }
+    return true;
+  };
 
   uint8_t* my = ring + warp * NST * SLOT;
   const uint32_t my_s = smem_addr(my);
-  const size_t plain = ((size_t)b * a.Hkv + hk) * a.Nk;
-  // what a lane copies: chunk `lc` of rows lr, lr + RPI, ..
-  const int lr = lane / CH, lc = lane % CH;
+  auto full = [&](int st) { return smem_addr(&full_s[warp][st]); };
+  if (lane == 0) {
+    for (int i = 0; i < NST; ++i) tc::mbar_init(full(i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
 
-  // first key of group gi and the range of keys that its phase counts
-  auto group = [&](int gi, int* j0, int* jb, int* je) {
-    const bool f = gi < gs;
-    *j0 = (f ? gi : w0 + gi - gs) * GK;
-    *jb = f ? 0 : kr.lo;
-    *je = f ? kr.S : kr.hi;
+  // first key of the cursor's group and the range of keys that its phase counts
+  auto group = [&](const Cursor& c, int* j0, int* jb, int* je) {
+    const bool f = c.gi < c.gs;
+    *j0 = (f ? c.gi : c.w0 + c.gi - c.gs) * GK;
+    *jb = f ? 0 : c.kr.lo;
+    *je = f ? c.kr.S : c.kr.hi;
   };
   auto has_keys = [](int j, int jb, int je) { return j < je && j + 16 > jb; };
-  // the cache blocks that hold the 16-key parts of group gi; only those of parts
+  // the cache blocks that hold the 16-key parts of a group; only those of parts
   // with keys of the phase are looked up
-  auto blocks_of = [&](int gi, int (&blk)[NH]) {
+  auto blocks_of = [&](const Cursor& c, int (&blk)[NH]) {
     int j0, jb, je;
-    group(gi, &j0, &jb, &je);
+    group(c, &j0, &jb, &je);
 #pragma unroll
     for (int h = 0; h < NH; ++h)
-      blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)b * t.max_blocks + ((j0 + 16 * h) >> t.Tshift)] : -1;
+      blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)c.b * t.max_blocks + ((j0 + 16 * h) >> t.Tshift)] : -1;
   };
-  // copies of group gi into ring slot st
-  auto issue = [&](int gi, int st, const int (&blk)[NH]) {
+  // copies of the cursor's group into ring slot st: one box of GK rows for each panel, or one
+  // for each half where blocks hold 16 tokens
+  auto issue = [&](const Cursor& c, int st, const int (&blk)[NH]) {
     int j0, jb, je;
-    group(gi, &j0, &jb, &je);
-    const uint32_t dst = my_s + st * SLOT;
-    size_t tok[NH];
-    bool there[NH], full = j0 >= jb && j0 + GK <= je && a.d == DP;
+    group(c, &j0, &jb, &je);
+    const int hk = c.hr / t.rtiles;
+    bool there[NH];
+    int bh[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       there[h] = true;
+      bh[h] = c.b * a.Hkv + hk;
       if (t.table) {
         there[h] = (unsigned)blk[h] < (unsigned)t.blocks;
         if (!there[h] && lane == 0 && has_keys(j0 + 16 * h, jb, je)) atomicOr(t.err, 2);
-        const size_t bh = (size_t)(there[h] ? blk[h] : 0) * a.Hkv + hk;
-        tok[h] = (bh << t.Tshift) + ((j0 + 16 * h) & ((1 << t.Tshift) - 1));
-        if (lane == 0) {
-          cp_async4(dst + STG + 4 * h, t.k_scale + bh);
-          cp_async4(dst + STG + 8 + 4 * h, t.v_scale + bh);
-          *reinterpret_cast<int*>(my + st * SLOT + STG + 16 + 4 * h) = there[h];
+        bh[h] = (there[h] ? blk[h] : 0) * a.Hkv + hk;
+        if (lane == h) {
+          cp_async4(smem_addr(&scale_s[warp][st][h]), t.k_scale + bh[h]);
+          cp_async4(smem_addr(&scale_s[warp][st][2 + h]), t.v_scale + bh[h]);
+          there_s[warp][st][h] = there[h];
         }
-      } else {
-        tok[h] = plain + j0 + 16 * h;
       }
-      full = full && there[h];
     }
-    const uint8_t* gk[NH];
-    const uint8_t* gv[NH];
+    if (lane == 0) {
+      const uint32_t dst = my_s + st * SLOT, bar = full(st);
+      const bool one = NH == 1 || t.table == nullptr || t.Tshift > 4;   // one box
+      const bool first = there[0] || (one && there[NH - 1]);
+      const int parts = one ? (first ? 1 : 0) : (int)there[0] + (int)there[NH - 1];
+      tc::mbar_expect_tx(bar, (uint32_t)(parts * (one ? 2 * TILE : TILE)));
+      const int row = t.table ? j0 & ((1 << t.Tshift) - 1) : j0;
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const size_t off = ((tok[h] + lr) * a.d + lc * PIECE) * ES;
-      gk[h] = (const uint8_t*)a.k + off;
-      gv[h] = (const uint8_t*)a.v + off;
-    }
-    if (full) {
+      for (int h = 0; h < NH; ++h) {
+        if (one ? h > 0 || !first : !there[h]) continue;
+        const int src = one && !there[0] ? bh[NH - 1] : bh[h];
 #pragma unroll
-      for (int u = 0; u < GK / RPI; ++u) {
-        constexpr int RH = 16 / RPI;       // copies of a half
-        const int off = (u % RH) * RPI * RB;
-        cp_async16(dst + k_off<RB>(u * RPI + lr, lc), gk[u / RH] + off, true);
-        cp_async16(dst + TILE + v_off<RB>(u * RPI + lr, lc), gv[u / RH] + off, true);
-      }
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < GK / RPI; ++u) {
-        const int r = u * RPI + lr, h = NH > 1 ? r >> 4 : 0;
-        const bool in = NH > 1 && h ? there[NH - 1] : there[0];
-        const bool ok = in && lc * PIECE < a.d && j0 + r >= jb && j0 + r < je;
-        const size_t off = (size_t)(r % 16 - lr) * a.d * ES;
-        const uint8_t* pk = NH > 1 && h ? gk[NH - 1] : gk[0];
-        const uint8_t* pv = NH > 1 && h ? gv[NH - 1] : gv[0];
-        cp_async16(dst + k_off<RB>(r, lc), ok ? pk + off : (const uint8_t*)a.k, ok);
-        cp_async16(dst + TILE + v_off<RB>(r, lc), ok ? pv + off : (const uint8_t*)a.v, ok);
+        for (int p = 0; p < PANELS; ++p) {
+          const uint32_t to = dst + p * GK * 128 + h * 16 * (RB == 64 ? 64 : 128);
+          wtc::tma3(to, &mp.k, p * (128 / ES), row, src, bar);
+          wtc::tma3(to + TILE, &mp.v, p * (128 / ES), row, src, bar);
+        }
       }
     }
   };
 
-  int gi = g0 + warp, gn = gi;       // group to compute, group to issue
+  // cn: the next group to copy, `ahead` of them left; cu: the group to work on
+  Cursor cn, cu;
+  cn.b = b0; cn.hr = hr0; cn.gi = gi0;
+  enter(cn);
+  cu = cn;
+  int ahead = mine, left = mine;
   int blk[NH] = {};
-  if (t.table && gn < g1) blocks_of(gn, blk);
-#pragma unroll
-  for (int st = 0; st < NST - 1; ++st) {
-    if (gn < g1) issue(gn, st, blk);
-    gn += TNW;
-    if (t.table && gn < g1) blocks_of(gn, blk);
-    cp_commit();
-  }
-
-  // the rows this thread meets: gid and gid + 8 of the tile
-  WinRow row[2];
-  float qs[2];                       // score factor of the row
-  uint32_t qf[NP][KS][4];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int rr = rt * 16 + gid + 8 * r;
-    const bool ok = rr < R;
-    const int e = ok ? rr / a.Nq : 0, i = ok ? rr % a.Nq : 0;
-    row[r] = ok ? win_row(a, sq, i) : WinRow{0, 0, 0};
-    const TQ* q = (const TQ*)a.q + (((size_t)b * a.Hq + hk * a.g + e) * a.Nq + i) * a.d;
-    float4 x[KS];
-    float mx = 0.f;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int c = (tq + 4 * (s / KSP)) * PIECE + (s % KSP) * 4;
-      x[s] = ok && c < a.d ? ld4(q + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[s].x), fabsf(x[s].y)), fmaxf(fabsf(x[s].z), fabsf(x[s].w))));
-    }
-    float down = 1.f;
-    qs[r] = a.scale_log2;
-    if constexpr (X::F16) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the largest feature to [2^13, 2^14)
-      const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
-      if (mx > 0.f && mx < INFINITY) {
-        const int h = max(-126, min(126, -ex));
-        down = __uint_as_float((uint32_t)(h + 127) << 23);
-        qs[r] *= __uint_as_float((uint32_t)(127 - h) << 23);
+  if (t.table) blocks_of(cn, blk);
+  auto advance = [&](int st) {         // copy the next group, if any, and look up the one after
+    if (ahead > 0) {
+      issue(cn, st, blk);
+      if (--ahead > 0) {
+        if (step(cn)) enter(cn);
+        if (t.table) blocks_of(cn, blk);
       }
     }
+    cp_commit();
+  };
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      uint32_t w[NP];
-      split<KIND>(x[s].x * down, x[s].y * down, w);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) qf[p][s][r] = w[p];
-      split<KIND>(x[s].z * down, x[s].w * down, w);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = w[p];
-    }
-  }
+  for (int st = 0; st < NST - 1; ++st) advance(st);
 
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float vref = 1.f;                  // reference of the values' scales: v = vref x what o holds
+  // ---- the row's queries: rows gid and gid + 8 of the tile ----
+  WinRow row[2];
+  float qs[2];                         // score factor of the row
+  uint32_t qf[NP][KS][4];
+  int free_lo = 0, free_hi = -1;       // keys [free_lo, free_hi) every query sees: no mask
+  auto queries = [&](const Cursor& c) {
+    const int hk = c.hr / t.rtiles, rt = c.hr - hk * t.rtiles;
+    const bool rows_ok = c.sq.qp >= 0 && c.sq.qp + a.Nq <= c.sq.len;
+    free_lo = c.sq.qp + a.Nq - 1 - a.left;
+    free_hi = rows_ok ? min(c.sq.len, c.sq.qp + a.right + 1) : -1;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int rr = rt * 16 + gid + 8 * r;
+      const bool ok = rr < R;
+      const int e = ok ? rr / a.Nq : 0, i = ok ? rr % a.Nq : 0;
+      row[r] = ok ? win_row(a, c.sq, i) : WinRow{0, 0, 0};
+      const TQ* q = (const TQ*)a.q + (((size_t)c.b * a.Hq + hk * a.g + e) * a.Nq + i) * a.d;
+      float4 x[KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int f = key_chunk<RB>(tq, s / KSP) * PIECE + (s % KSP) * 4;
+        x[s] = ok && f < a.d ? ld4(q + f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float down = 1.f;
+      qs[r] = a.scale_log2;
+      if constexpr (X::F16) {
+        float mx = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[s].x), fabsf(x[s].y)), fmaxf(fabsf(x[s].z), fabsf(x[s].w))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the largest feature to [2^13, 2^14)
+        const int ex = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
+        if (mx > 0.f && mx < INFINITY) {
+          const int h = max(-126, min(126, -ex));
+          down = __uint_as_float((uint32_t)(h + 127) << 23);
+          qs[r] *= __uint_as_float((uint32_t)(127 - h) << 23);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t u[NP];
+        split<KIND>(x[s].x * down, x[s].y * down, u);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) qf[p][s][r] = u[p];
+        split<KIND>(x[s].z * down, x[s].w * down, u);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = u[p];
+      }
+    }
+  };
+
+  float m[2], l[2];
+  float vref;                        // reference of the values' scales: v = vref x what o holds
   float o[NT][4];
+  auto clear = [&]() {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    vref = 1.f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  };
+  // the row's share to memory: stretch w of row r is part w + r (unique, since one
+  // or the other grows from part to part, and a row's are consecutive)
+  const int first_gi = gi0;
+  auto leave = [&](const Cursor& c) {
+    const int rt = c.hr % t.rtiles, rowid = c.b * heads + c.hr;
+    const size_t part = (size_t)(w + rowid) * 16;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int rr = gid + 8 * r;
+      if (rt * 16 + rr >= R) continue;
+      if (tq == 0) t.part_ml[part + rr] = make_float2(m[r], l[r]);
+      float* dst = t.part_o + (part + rr) * a.d;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+          const int f = n / VP * (128 / ES) + (2 * tq + e) * VP + n % VP;
+          if (f < a.d)
+            st4(dst + f, make_float4(o[n][2 * r + e] * vref, o[n + 1][2 * r + e] * vref,
+                                     o[n + 2][2 * r + e] * vref, o[n + 3][2 * r + e] * vref));
+        }
+    }
+    // the row's first and last parts
+    if (lane == 0) {
+      const bool whole_start = !(c.b == b0 && c.hr == hr0) || first_gi == 0;
+      if (whole_start) t.info[rowid].x = w;
+      if (c.gi + 1 >= c.G) t.info[rowid].y = w;
+    }
+  };
+  queries(cu);
+  clear();
 
   int st = 0;
+  uint32_t ph = 0;                   // phase of the ring's round
+  bool bad = false;
 #pragma unroll 1
-  for (; gi < g1; gi += TNW) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+  for (;;) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");   // the scales
+    if (!wtc::wait_warp(t.err, full(st), ph)) {
+      bad = true;
+      break;
+    }
     __syncwarp();
     // the slot of the group before is free: its copies run under this group's work
-    if (gn < g1) issue(gn, st == 0 ? NST - 1 : st - 1, blk);
-    gn += TNW;
-    if (t.table && gn < g1) blocks_of(gn, blk);
-    cp_commit();
-    const uint8_t* Kt = my + st * SLOT;
-    const uint8_t* Vt = Kt + TILE;
+    advance(st == 0 ? NST - 1 : st - 1);
+    uint8_t* Kt = my + st * SLOT;
+    uint8_t* Vt = Kt + TILE;
     int j0, jb, je;
-    group(gi, &j0, &jb, &je);
+    group(cu, &j0, &jb, &je);
     float ksc[NH], vsc[NH];
     bool there[NH], all = true;        // a part without a block has no keys
 #pragma unroll
@@ -360,11 +439,23 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       ksc[h] = vsc[h] = 1.f;
       there[h] = true;
       if (t.table) {
-        ksc[h] = reinterpret_cast<const float*>(Kt + STG)[h];
-        vsc[h] = reinterpret_cast<const float*>(Kt + STG)[2 + h];
-        there[h] = reinterpret_cast<const int*>(Kt + STG)[4 + h] != 0;
+        ksc[h] = scale_s[warp][st][h];
+        vsc[h] = scale_s[warp][st][2 + h];
+        there[h] = there_s[warp][st][h] != 0;
         all = all && there[h];
       }
+    }
+    const bool inside = all && j0 >= jb && j0 + GK <= je;
+    if (!inside) {
+      // value rows that are no keys of the phase: zeros (0 * anything is not 0)
+#pragma unroll 1
+      for (int id = lane; id < GK * CH; id += 32) {
+        const int r = id / CH, j = j0 + r;
+        const bool in = (NH > 1 && r >= 16 ? there[NH - 1] : there[0]) && j >= jb && j < je;
+        if (!in) *reinterpret_cast<uint4*>(Vt + tile_off<RB, GK>(r, id % CH)) = make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
     }
     // ---- scores ----
     float s[NU][4];
@@ -377,7 +468,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       uint32_t w[NU][4];
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const uint4 kv = *reinterpret_cast<const uint4*>(Kt + k_off<RB>(8 * u + gid, tq + 4 * i));
+        const uint4 kv = *reinterpret_cast<const uint4*>(Kt + tile_off<RB, GK>(8 * u + gid, key_chunk<RB>(tq, i)));
         w[u][0] = kv.x; w[u][1] = kv.y; w[u][2] = kv.z; w[u][3] = kv.w;
       }
       if constexpr (KIND == TK_F32) {
@@ -408,7 +499,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
       }
     }
     // ---- softmax, running maximum and sum ----
-    const bool whole = all && j0 >= jb && j0 + GK <= je && j0 + GK <= free_hi &&
+    const bool whole = inside && j0 + GK <= free_hi &&
                        (j0 >= free_lo || j0 + GK <= a.sinks);
     float p[NU][4];
     bool up = false;
@@ -507,10 +598,10 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         for (int e = 0; e < 4; ++e) {
           const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
           if constexpr (W == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid));
+            const uint4 x = *reinterpret_cast<const uint4*>(Vt + tile_off<RB, GK>(rr, gid));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(Vt + v_off<RB>(rr, gid >> 1) + 8 * (gid & 1));
+            const uint2 x = *reinterpret_cast<const uint2*>(Vt + tile_off<RB, GK>(rr, gid >> 1) + 8 * (gid & 1));
             v[e][0] = x.x; v[e][1] = x.y;
           }
         }
@@ -523,14 +614,13 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
           for (int x = NP - 1; x >= 0; --x) mma_f16(o[n], pf[x][g], b0, b1);
         }
       } else if constexpr (KIND == TK_BF16) {
-        constexpr int W = DP / 16;
 #pragma unroll
-        for (int h = 0; h < W / 4; ++h) {
+        for (int h = 0; h < PANELS; ++h) {
           uint32_t v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
-            const uint4 x = *reinterpret_cast<const uint4*>(Vt + v_off<RB>(rr, gid * (W / 4) + h));
+            const uint4 x = *reinterpret_cast<const uint4*>(Vt + tile_off<RB, GK>(rr, 8 * h + gid));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
 #pragma unroll
@@ -542,12 +632,12 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < DP / 32; ++h) {
+        for (int h = 0; h < PANELS; ++h) {
           float v[4][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int rr = 16 * g + 2 * tq + (e & 1) + 8 * (e >> 1);
-            const float4 x = *reinterpret_cast<const float4*>(Vt + v_off<RB>(rr, gid * (DP / 32) + h));
+            const float4 x = *reinterpret_cast<const float4*>(Vt + tile_off<RB, GK>(rr, 8 * h + gid));
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
 #pragma unroll
@@ -563,89 +653,57 @@ __global__ void __launch_bounds__(32 * TNW) k_token(TokenArgs t) {
         }
       }
     }
-    if (++st == NST) st = 0;
+    __syncwarp();                      // the slot is read
+    if (++st == NST) {
+      st = 0;
+      ph ^= 1u;
+    }
+    const bool last = --left == 0;
+    if (last || cu.gi + 1 >= cu.G) leave(cu);
+    if (last) break;
+    if (step(cu)) {
+      enter(cu);
+      queries(cu);
+      clear();
+    }
   }
-  cp_wait_all();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-  }
-
-  // ---- the warps' shares joined in shared memory (the rings are free) ----
-  __syncthreads();
-  float* So = reinterpret_cast<float*>(ring);       // [TNW][16][DP]
-  float* Sm = So + TNW * 16 * DP;                   // [TNW][16] maxima, then sums
-  float* Sl = Sm + TNW * 16;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float* dst = So + (warp * 16 + gid + 8 * r) * DP;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      dst[2 * tq * NT + n] = o[n][2 * r] * vref;
-      dst[(2 * tq + 1) * NT + n] = o[n][2 * r + 1] * vref;
+  if (bad)   // copies in flight land before the block ends: the groups issued and not worked on
+    for (; left > ahead; --left) {
+      wtc::wait_or_flag(t.err, full(st), ph);
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
-    if (tq == 0) {
-      Sm[warp * 16 + gid + 8 * r] = m[r];
-      Sl[warp * 16 + gid + 8 * r] = l[r];
-    }
-  }
-  __syncthreads();
-  constexpr int C4 = DP / 4;
-  for (int id = tid; id < 16 * C4; id += 32 * TNW) {
-    const int r = id / C4, c = (id % C4) * 4, rr = rt * 16 + r;
-    if (rr >= R || c >= a.d) continue;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < TNW; ++w) mx = fmaxf(mx, Sm[w * 16 + r]);
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < TNW; ++w) {
-      const float f = exp2f(Sm[w * 16 + r] - mu);
-      const float4 x = lds4(So + (w * 16 + r) * DP + c);
-      sum += Sl[w * 16 + r] * f;
-      acc.x = fmaf(x.x, f, acc.x); acc.y = fmaf(x.y, f, acc.y);
-      acc.z = fmaf(x.z, f, acc.z); acc.w = fmaf(x.w, f, acc.w);
-    }
-    const size_t qrow = ((size_t)b * a.Hq + hk * a.g + rr / a.Nq) * a.Nq + rr % a.Nq;
-    if (shares == 1) {
-      const float w = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-      st4((TQ*)a.out + qrow * a.d + c, make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w));
-      if (a.lse && c == 0) a.lse[qrow] = sum == 0.f ? -INFINITY : mx + log2f(sum) - X::SHIFT;
-    } else {
-      const size_t part = (size_t)blockIdx.x * 16 + r;
-      st4(t.part_o + part * a.d + c, acc);
-      if (c == 0) t.part_ml[part] = make_float2(mx, sum);
-    }
-  }
+  cp_wait_all();
 }
 
-// out = sum over a row's shares: a block a row, its warps take shares in turn
+// out = sum over a row's parts: a block a row, its warps take parts in turn
 template <typename TQ>
 __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
   __shared__ __align__(16) float So[4][128];
-  __shared__ float Sm[4], Sl[4];
+  __shared__ float Sl[4];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while k_token still ran
   const WinArgs& a = t.w;
   const long long qrow = blockIdx.x;                     // (b, query head, query)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = 4 * lane;
   const int i = (int)(qrow % a.Nq), hq = (int)(qrow / a.Nq % a.Hq), b = (int)(qrow / a.Nq / a.Hq);
   const int rr = (hq % a.g) * a.Nq + i;
-  const int2 in = t.info[((size_t)b * a.Hkv + hq / a.g) * t.rtiles + rr / 16];
-  if (in.y == 1) return;                                 // written already
-  const size_t row0 = (size_t)in.x * 16 + rr % 16;
+  const size_t rowid = ((size_t)b * a.Hkv + hq / a.g) * t.rtiles + rr / 16;
+  const int2 in = t.info[rowid];
+  // parts; 0: the row sees nothing (or its warps gave up after an expired wait)
+  const int n = in.x >= 0 && in.y < t.grid * TNW && in.y >= in.x ? in.y - in.x + 1 : 0;
+  const size_t row0 = (rowid + in.x) * 16 + rr % 16;
   float mx = -INFINITY;
-  for (int s = lane; s < in.y; s += 32) mx = fmaxf(mx, t.part_ml[row0 + (size_t)s * 16].x);
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, t.part_ml[row0 + (size_t)s * 16].x);
 #pragma unroll
   for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = warp; s < in.y; s += 4) {
+  for (int s = warp; s < n; s += 4) {
     const size_t row = row0 + (size_t)s * 16;
     const float2 x = t.part_ml[row];
     const float f = exp2f(x.x - mu);
@@ -673,10 +731,10 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
 }
 
 namespace {
-// blocks of k_token that run at once, by their shared memory (227 KB an SM, 1 KB
-// a block for the system)
+// blocks of k_token that run at once, by their shared memory (227 KB an SM, 2 KB
+// a block for the system and the small arrays)
 template <int KIND, int DP>
-constexpr int blocks_per_sm() { return (int)(232448 / (token_smem<KIND, DP>() + 1024)); }
+constexpr int blocks_per_sm() { return (int)(232448 / (token_smem<KIND, DP>() + 2048)); }
 
 int slots_of(int kind, int d) {
   const int sms = 152;   // from the type alone: workspaces do not depend on the device
@@ -695,14 +753,23 @@ int kind_of(bool cache, bool bf16) {
 template <int KIND, int DP>
 cudaError_t go(TokenArgs& t, cudaStream_t st) {
   using TQ = typename std::conditional<Kind<KIND>::QF32, float, __nv_bfloat16>::type;
-  constexpr size_t join = (size_t)TNW * 16 * (DP + 2) * 4;
-  constexpr size_t smem = token_smem<KIND, DP>() > join ? token_smem<KIND, DP>() : join;
+  constexpr size_t smem = token_smem<KIND, DP>();
   static SmemOnce once;
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess || (e = once.allow(k_token<KIND, DP>, smem, dev)) != cudaSuccess) return e;
-  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW), smem, st, t);
-  if (e != cudaSuccess || !t.joined) return e;
+  // a panel's features x the rows of a copy: a group, or a block of 16 tokens
+  TokenMaps mp;
+  constexpr int ES = Kind<KIND>::ES;
+  const WinArgs& a = t.w;
+  const int box = t.table && t.Tshift == 4 ? 16 : Kind<KIND>::GK;
+  const int N = t.table ? 1 << t.Tshift : a.Nk;
+  const long long outer = t.table ? (long long)t.blocks * a.Hkv : (long long)a.B * a.Hkv;
+  for (int i = 0; i < 2; ++i)
+    if (!encode_tiled_rows(i ? &mp.v : &mp.k, i ? a.v : a.k, ES, a.d, N, outer, DP * ES == 64 ? 64 : 128, box))
+      return cudaErrorInvalidValue;
+  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW), smem, st, mp, t);
+  if (e != cudaSuccess) return e;
   const long long rows = (long long)t.w.B * t.w.Hq * t.w.Nq;
   return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(128), 0, st, t,
                       Kind<KIND>::SHIFT);
@@ -713,21 +780,19 @@ TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int
                        int left, int right, int sinks) {
   TokenShape s;
   s.rtiles = (g * Nq + 15) / 16;
-  s.slots = slots_of(kind_of(cache, bf16), d);
-  // groups of a sequence at the most, and so blocks: a share holds at least two
-  // groups a warp, shares are at most `slots` beyond one for each row tile
+  // all blocks at once, but no more warps than stretches of two groups
   long long seen = keys;
   if (left < kWinUnbounded && right < kWinUnbounded) {
     const long long w = (long long)left + right + Nq + sinks + 64;
     if (w < seen) seen = w;
   }
-  const long long groups = seen / 16 + 3, rows = (long long)B * Hkv * s.rtiles;
+  const long long rows = (long long)B * Hkv * s.rtiles, groups = rows * (seen / 16 + 3);
+  s.grid = slots_of(kind_of(cache, bf16), d);
   const long long most = (groups + 2 * TNW - 1) / (2 * TNW);
-  s.grid = rows * (most < 1 ? 1 : most);
-  if (s.grid > rows + s.slots) s.grid = rows + s.slots;
-  s.joined = most > 1;
-  s.o_bytes = s.joined ? (size_t)s.grid * 16 * d * 4 : 0;
-  s.ml_bytes = s.joined ? (size_t)s.grid * 16 * 8 : 0;
+  if (most < s.grid) s.grid = (int)most;
+  const size_t parts = (size_t)rows + (size_t)s.grid * TNW;
+  s.o_bytes = parts * 16 * d * 4;
+  s.ml_bytes = parts * 16 * 8;
   s.info_bytes = (size_t)rows * 8;
   return s;
 }

@@ -51,9 +51,7 @@ size_t token_bytes(const TokenShape& s) {
 void token_parts(TokenArgs& t, const TokenShape& s, void* ws) {
   uint8_t* p = (uint8_t*)ws;
   t.rtiles = s.rtiles;
-  t.slots = s.slots;
   t.grid = s.grid;
-  t.joined = s.joined;
   t.part_o = (float*)p;
   t.part_ml = (float2*)(p + align256(s.o_bytes));
   t.info = (int2*)(p + align256(s.o_bytes) + align256(s.ml_bytes));
@@ -116,6 +114,7 @@ int check_cache(WinArgs& a, int B, int Hq, int Hkv, int Nq, int d, int block, in
   if (block != 16 && block != 32 && block != 64 && block != 128) return LAPNYS_EINVAL;
   if (blocks <= 0 || max_blocks <= 0 || (long long)max_blocks * block > kWinMaxLen)
     return LAPNYS_EINVAL;
+  if (Hkv > 0 && (long long)blocks * Hkv >= 1LL << 31) return LAPNYS_EINVAL;
   if (dtype != LAPNYS_F32 && dtype != LAPNYS_BF16) return LAPNYS_EINVAL;
   return check_dims(a, B, Hq, Hkv, Nq, max_blocks * block, d);
 }
@@ -170,6 +169,8 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
   if (few(a.g, Nq)) {
     token_parts(t, w.tok, ws);
+    t.err = wait_error_address();
+    if (t.err == nullptr) return LAPNYS_ECUDA;
     return status(run_token(t, dtype == LAPNYS_BF16, stream));
   }
   if (dtype == LAPNYS_BF16) return status(run_win_fwd_tc(a, stream));
