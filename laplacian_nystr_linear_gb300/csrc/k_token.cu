@@ -7,10 +7,11 @@
 // heads that share it, and nothing else is large.  So the work is split over the
 // keys, evenly and finely: the visible groups of 16 or 32 keys of all rows (a row:
 // one sequence, one key head, 16 query rows) are laid end to end, and each warp
-// takes one equal stretch, whatever the sequences' lengths are.  A warp keeps a
-// ring of TMA copies of its own that runs on across rows (no block barrier
-// anywhere), and leaves maximum, sum and output of each row that it met for
-// k_token_join.  Blocks that shared rows out by themselves lost 8 us a wave to
+// takes one equal stretch, whatever the sequences' lengths are.  Each has a ring of
+// TMA copies of its own that runs on across rows, filled by one lane of a fifth
+// warp (the working warps spent a third of their time waiting for the copy engine
+// to take their requests), and leaves maximum, sum and output of each row that it
+// met for k_token_join.  Blocks that shared rows out by themselves lost 8 us a wave to
 // their start and end and, on ragged batches, a second wave (32 sequences, 8192
 // tokens at the most: 110 us).
 //
@@ -41,7 +42,7 @@
 namespace lapnys {
 
 namespace {
-constexpr int TNW = 4;      // warps of a block
+constexpr int TNW = 4;      // working warps of a block (and one that copies)
 enum : int { TK_BF16 = 0, TK_E4M3 = 1, TK_E4M3_F32 = 2, TK_F32 = 3 };
 
 template <int KIND>
@@ -59,6 +60,9 @@ template <int KIND, int DP>
 __host__ __device__ constexpr size_t token_smem() {   // rings from a multiple of 1024 bytes on
   return (size_t)TNW * ring_stages<KIND, DP>() * 2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + 1024;
 }
+// blocks of an SM: two (by registers), one where the rings are that large
+template <int KIND, int DP>
+__host__ __device__ constexpr int token_blocks() { return token_smem<KIND, DP>() > 113 * 1024 ? 1 : 2; }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -118,9 +122,6 @@ template <int RB>
 __device__ __forceinline__ int key_chunk(int t, int i) {
   return RB == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
 }  // namespace
 
 struct TokenMaps {
@@ -128,7 +129,7 @@ struct TokenMaps {
 };
 
 template <int KIND, int DP>
-__global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ TokenMaps mp, const TokenArgs t) {
+__global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_token(const __grid_constant__ TokenMaps mp, const TokenArgs t) {
   using X = Kind<KIND>;
   constexpr int ES = X::ES, RB = DP * ES, NP = X::PARTS, GK = X::GK, NU = GK / 8, NH = GK / 16;
   constexpr int NST = ring_stages<KIND, DP>();
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
   constexpr int VP = RB == 64 ? 8 : PIECE;     // features of a thread's piece of a value row
   using TQ = typename std::conditional<X::QF32, float, __nv_bfloat16>::type;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t full_s[TNW][NST];      // a ring slot's copies landed
+  __shared__ __align__(8) uint64_t full_s[TNW][NST], empty_s[TNW][NST];  // a ring slot's copies; its reader
+  __shared__ int start_s[TNW][4];                         // the stretches: row, group, groups
   __shared__ float scale_s[TNW][NST][4];                  // of its keys, of its values, per 16 keys
   __shared__ int there_s[TNW][NST][2];                    // whether these have a block
   uint8_t* ring = sm_raw + ((1024u - (smem_addr(sm_raw) & 1023u)) & 1023u);
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
   for (int b = lane; b < a.B; b += 32) {
     const int G = groups_of(win_keys(a, seq_of(b), 0, a.Nq));
     total += G;
-    if (G == 0 && b % W == w)          // rows that nobody meets
+    if (G == 0 && warp < TNW && b % W == w)   // rows that nobody meets
       for (int h = 0; h < heads; ++h) t.info[b * heads + h] = make_int2(0, -1);
   }
 #pragma unroll
@@ -173,7 +175,6 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
   const int each = max(2, (int)((total + W - 1) / W));
   const long long at = min(total, (long long)w * each);
   const int mine = (int)min(total - at, (long long)each);
-  if (mine <= 0) return;
   // where it begins: the sequence (a scan over them), row and group
   int b0 = 0, hr0 = 0, gi0 = 0;
   long long base = 0;
@@ -197,6 +198,17 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
     }
     base += __shfl_sync(0xffffffffu, upto, 31);
   }
+
+  auto bar = [](uint64_t* x) { return smem_addr(x); };
+  if (warp < TNW && lane == 0) {
+    start_s[warp][0] = b0; start_s[warp][1] = hr0; start_s[warp][2] = gi0; start_s[warp][3] = mine;
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(bar(&full_s[warp][i]), 2);     // the copies' request, the scales
+      tc::mbar_init(bar(&empty_s[warp][i]), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
 
   // a place in the stretch: row (b, hr) and its group gi, and the row's ranges
   struct Cursor {
@@ -225,15 +237,6 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
     return true;
   };
 
-  uint8_t* my = ring + warp * NST * SLOT;
-  const uint32_t my_s = smem_addr(my);
-  auto full = [&](int st) { return smem_addr(&full_s[warp][st]); };
-  if (lane == 0) {
-    for (int i = 0; i < NST; ++i) tc::mbar_init(full(i), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncwarp();
-
   // first key of the cursor's group and the range of keys that its phase counts
   auto group = [&](const Cursor& c, int* j0, int* jb, int* je) {
     const bool f = c.gi < c.gs;
@@ -251,70 +254,80 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
     for (int h = 0; h < NH; ++h)
       blk[h] = has_keys(j0 + 16 * h, jb, je) ? t.table[(size_t)c.b * t.max_blocks + ((j0 + 16 * h) >> t.Tshift)] : -1;
   };
-  // copies of the cursor's group into ring slot st: one box of GK rows for each panel, or one
-  // for each half where blocks hold 16 tokens
-  auto issue = [&](const Cursor& c, int st, const int (&blk)[NH]) {
-    int j0, jb, je;
-    group(c, &j0, &jb, &je);
-    const int hk = c.hr / t.rtiles;
-    bool there[NH];
-    int bh[NH];
+  if (warp == TNW) {
+    // ---- copies: lane i fills the ring of warp i, one box of GK rows for each
+    // panel of a group, or one for each half where blocks hold 16 tokens ----
+    if (lane >= TNW) return;
+    const uint32_t base = smem_addr(ring) + lane * NST * SLOT;
+    Cursor c;
+    c.b = start_s[lane][0]; c.hr = start_s[lane][1]; c.gi = start_s[lane][2];
+    const int n = start_s[lane][3];
+    int blk[NH] = {};
+    if (n > 0) {
+      enter(c);
+      if (t.table) blocks_of(c, blk);
+    }
+    int i = 0;
+    for (; i < n; ++i) {
+      const int st = i % NST;
+      const uint32_t full = bar(&full_s[lane][st]);
+      if (!wtc::wait_or_flag(t.err, bar(&empty_s[lane][st]), (uint32_t)(i / NST & 1) ^ 1u)) break;
+      int j0, jb, je;
+      group(c, &j0, &jb, &je);
+      const int hk = c.hr / t.rtiles;
+      bool there[NH];
+      int bh[NH];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      there[h] = true;
-      bh[h] = c.b * a.Hkv + hk;
-      if (t.table) {
-        there[h] = (unsigned)blk[h] < (unsigned)t.blocks;
-        if (!there[h] && lane == 0 && has_keys(j0 + 16 * h, jb, je)) atomicOr(t.err, 2);
-        bh[h] = (there[h] ? blk[h] : 0) * a.Hkv + hk;
-        if (lane == h) {
-          cp_async4(smem_addr(&scale_s[warp][st][h]), t.k_scale + bh[h]);
-          cp_async4(smem_addr(&scale_s[warp][st][2 + h]), t.v_scale + bh[h]);
-          there_s[warp][st][h] = there[h];
+      for (int h = 0; h < NH; ++h) {
+        there[h] = true;
+        bh[h] = c.b * a.Hkv + hk;
+        if (t.table) {
+          there[h] = (unsigned)blk[h] < (unsigned)t.blocks;
+          if (!there[h] && has_keys(j0 + 16 * h, jb, je)) atomicOr(t.err, 2);
+          bh[h] = (there[h] ? blk[h] : 0) * a.Hkv + hk;
         }
       }
-    }
-    if (lane == 0) {
-      const uint32_t dst = my_s + st * SLOT, bar = full(st);
+      const uint32_t dst = base + st * SLOT;
       const bool one = NH == 1 || t.table == nullptr || t.Tshift > 4;   // one box
-      const bool first = there[0] || (one && there[NH - 1]);
-      const int parts = one ? (first ? 1 : 0) : (int)there[0] + (int)there[NH - 1];
-      tc::mbar_expect_tx(bar, (uint32_t)(parts * (one ? 2 * TILE : TILE)));
+      const bool any = there[0] || there[NH - 1];
+      tc::mbar_expect_tx(full, one ? (any ? 2 * TILE : 0) : ((int)there[0] + (int)there[NH - 1]) * TILE);
       const int row = t.table ? j0 & ((1 << t.Tshift) - 1) : j0;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (one ? h > 0 || !first : !there[h]) continue;
+        if (one ? h > 0 || !any : !there[h]) continue;
         const int src = one && !there[0] ? bh[NH - 1] : bh[h];
 #pragma unroll
         for (int p = 0; p < PANELS; ++p) {
           const uint32_t to = dst + p * GK * 128 + h * 16 * (RB == 64 ? 64 : 128);
-          wtc::tma3(to, &mp.k, p * (128 / ES), row, src, bar);
-          wtc::tma3(to + TILE, &mp.v, p * (128 / ES), row, src, bar);
+          wtc::tma3(to, &mp.k, p * (128 / ES), row, src, full);
+          wtc::tma3(to + TILE, &mp.v, p * (128 / ES), row, src, full);
         }
       }
-    }
-  };
-
-  // cn: the next group to copy, `ahead` of them left; cu: the group to work on
-  Cursor cn, cu;
-  cn.b = b0; cn.hr = hr0; cn.gi = gi0;
-  enter(cn);
-  cu = cn;
-  int ahead = mine, left = mine;
-  int blk[NH] = {};
-  if (t.table) blocks_of(cn, blk);
-  auto advance = [&](int st) {         // copy the next group, if any, and look up the one after
-    if (ahead > 0) {
-      issue(cn, st, blk);
-      if (--ahead > 0) {
-        if (step(cn)) enter(cn);
-        if (t.table) blocks_of(cn, blk);
+      if (i + 1 < n) {
+        if (step(c)) enter(c);
+        if (t.table) blocks_of(c, blk);
       }
-    }
-    cp_commit();
-  };
+      if (t.table) {
 #pragma unroll
-  for (int st = 0; st < NST - 1; ++st) advance(st);
+        for (int h = 0; h < NH; ++h) {
+          scale_s[lane][st][h] = t.k_scale[bh[h]];
+          scale_s[lane][st][2 + h] = t.v_scale[bh[h]];
+          there_s[lane][st][h] = there[h];
+        }
+      }
+      wtc::arrive(full);
+    }
+    // every copy has landed before the block ends, also after an expired wait
+    for (int k = i > NST ? i - NST : 0; k < i; ++k)
+      wtc::wait_or_flag(t.err, bar(&full_s[lane][k % NST]), (uint32_t)(k / NST) & 1u);
+    return;
+  }
+  if (mine <= 0) return;
+  uint8_t* my = ring + warp * NST * SLOT;
+  Cursor cu;                           // the group to work on
+  cu.b = b0; cu.hr = hr0; cu.gi = gi0;
+  enter(cu);
+  int left = mine;
 
   // ---- the row's queries: rows gid and gid + 8 of the tile ----
   WinRow row[2];
@@ -417,17 +430,10 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
 
   int st = 0;
   uint32_t ph = 0;                   // phase of the ring's round
-  bool bad = false;
 #pragma unroll 1
   for (;;) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");   // the scales
-    if (!wtc::wait_warp(t.err, full(st), ph)) {
-      bad = true;
-      break;
-    }
+    if (!wtc::wait_warp(t.err, bar(&full_s[warp][st]), ph)) break;
     __syncwarp();
-    // the slot of the group before is free: its copies run under this group's work
-    advance(st == 0 ? NST - 1 : st - 1);
     uint8_t* Kt = my + st * SLOT;
     uint8_t* Vt = Kt + TILE;
     int j0, jb, je;
@@ -654,6 +660,7 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
       }
     }
     __syncwarp();                      // the slot is read
+    if (lane == 0) wtc::arrive(bar(&empty_s[warp][st]));
     if (++st == NST) {
       st = 0;
       ph ^= 1u;
@@ -668,15 +675,6 @@ __global__ void __launch_bounds__(32 * TNW) k_token(const __grid_constant__ Toke
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (bad)   // copies in flight land before the block ends: the groups issued and not worked on
-    for (; left > ahead; --left) {
-      wtc::wait_or_flag(t.err, full(st), ph);
-      if (++st == NST) {
-        st = 0;
-        ph ^= 1u;
-      }
-    }
-  cp_wait_all();
 }
 
 // out = sum over a row's parts: a block a row, its warps take parts in turn
@@ -731,19 +729,14 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
 }
 
 namespace {
-// blocks of k_token that run at once, by their shared memory (227 KB an SM, 2 KB
-// a block for the system and the small arrays)
-template <int KIND, int DP>
-constexpr int blocks_per_sm() { return (int)(232448 / (token_smem<KIND, DP>() + 2048)); }
-
 int slots_of(int kind, int d) {
   const int sms = 152;   // from the type alone: workspaces do not depend on the device
   switch (kind) {
-    case TK_BF16: return sms * (d <= 64 ? blocks_per_sm<TK_BF16, 64>() : blocks_per_sm<TK_BF16, 128>());
-    case TK_E4M3: return sms * (d <= 64 ? blocks_per_sm<TK_E4M3, 64>() : blocks_per_sm<TK_E4M3, 128>());
+    case TK_BF16: return sms * (d <= 64 ? token_blocks<TK_BF16, 64>() : token_blocks<TK_BF16, 128>());
+    case TK_E4M3: return sms * (d <= 64 ? token_blocks<TK_E4M3, 64>() : token_blocks<TK_E4M3, 128>());
     case TK_E4M3_F32:
-      return sms * (d <= 64 ? blocks_per_sm<TK_E4M3_F32, 64>() : blocks_per_sm<TK_E4M3_F32, 128>());
-    default: return sms * (d <= 64 ? blocks_per_sm<TK_F32, 64>() : blocks_per_sm<TK_F32, 128>());
+      return sms * (d <= 64 ? token_blocks<TK_E4M3_F32, 64>() : token_blocks<TK_E4M3_F32, 128>());
+    default: return sms * (d <= 64 ? token_blocks<TK_F32, 64>() : token_blocks<TK_F32, 128>());
   }
 }
 int kind_of(bool cache, bool bf16) {
@@ -768,7 +761,7 @@ cudaError_t go(TokenArgs& t, cudaStream_t st) {
   for (int i = 0; i < 2; ++i)
     if (!encode_tiled_rows(i ? &mp.v : &mp.k, i ? a.v : a.k, ES, a.d, N, outer, DP * ES == 64 ? 64 : 128, box))
       return cudaErrorInvalidValue;
-  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW), smem, st, mp, t);
+  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW + 32), smem, st, mp, t);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)t.w.B * t.w.Hq * t.w.Nq;
   return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(128), 0, st, t,
