@@ -24,23 +24,38 @@ namespace lapnys {
 
 namespace {
 constexpr int AT = 256;            // threads
-constexpr int AV = 128 * 128 / 8 / AT;  // vectors of 8 values a thread may hold
 constexpr int kMinScaleExp = -100;
 
-__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
-  const float4 a = ld4(p), b = ld4(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// eight values as they lie in memory, and as fp32
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ld4(p);
+    b = ld4(p + 4);
   }
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 // infinities saturate, NaN stays NaN
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -60,7 +75,8 @@ __device__ __forceinline__ float scale_for(float amax) {
 }
 }  // namespace
 
-template <typename T>
+// AV: vectors of eight values a thread holds (the block's most)
+template <typename T, int AV>
 __global__ void __launch_bounds__(AT) k_cache_append(AppendArgs a) {
   __shared__ float red[AT / 32];
   const int which = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.Hkv;
@@ -83,21 +99,25 @@ __global__ void __launch_bounds__(AT) k_cache_append(AppendArgs a) {
   uint8_t* dst = (which ? a.v_cache : a.k_cache) + bh * a.T * a.d;
   float* scp = (which ? a.v_scale : a.k_scale) + bh;
   const int nv = (fe - fs) * a.d / 8;
-  float v[AV][8];
-  float mx = 0.f;
+  Raw8<T> raw[AV];
 #pragma unroll
   for (int i = 0; i < AV; ++i) {
     const int id = i * AT + threadIdx.x;
-    if (id < nv) {
-      ld8(src + (size_t)id * 8, v[i]);
+    if (id < nv) raw[i].load(src + (size_t)id * 8);
+  }
+  const float was = held ? *scp : 0.f;
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < AV; ++i)
+    if (i * AT + (int)threadIdx.x < nv) {
+      float v[8];
+      raw[i].get(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float y = fabsf(v[i][e]);
+        const float y = fabsf(v[e]);
         mx = fmaxf(mx, y < INFINITY ? y : 0.f);
       }
     }
-  }
-  const float was = held ? *scp : 0.f;
 #pragma unroll
   for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
@@ -110,10 +130,13 @@ __global__ void __launch_bounds__(AT) k_cache_append(AppendArgs a) {
 #pragma unroll
   for (int i = 0; i < AV; ++i) {
     const int id = i * AT + threadIdx.x;
-    if (id < nv)
+    if (id < nv) {
+      float v[8];
+      raw[i].get(v);
       *reinterpret_cast<uint2*>(dst + (size_t)fs * a.d + (size_t)id * 8) =
-          make_uint2(to_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                     to_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
+          make_uint2(to_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                     to_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    }
   }
   if (held && sc != was) {
     const float f = was * inv;
@@ -126,12 +149,20 @@ __global__ void __launch_bounds__(AT) k_cache_append(AppendArgs a) {
   }
 }
 
+namespace {
+template <typename T>
+cudaError_t append_go(const AppendArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((long long)a.B * a.nt * a.Hkv * 2));
+  const int most = a.N < a.T ? a.N : a.T, nv = (most * a.d / 8 + AT - 1) / AT;
+  if (nv <= 1) return launch("cache_append", k_cache_append<T, 1>, grid, dim3(AT), 0, st, a);
+  if (nv <= 4) return launch("cache_append", k_cache_append<T, 4>, grid, dim3(AT), 0, st, a);
+  return launch("cache_append", k_cache_append<T, 8>, grid, dim3(AT), 0, st, a);
+}
+}  // namespace
+
 cudaError_t run_cache_append(AppendArgs& a, bool bf16, cudaStream_t st) {
   a.nt = (a.N + a.T - 2) / a.T + 1;
-  const long long n = (long long)a.B * a.nt * a.Hkv * 2;
-  if (bf16)
-    return launch("cache_append", k_cache_append<__nv_bfloat16>, dim3((unsigned)n), dim3(AT), 0, st, a);
-  return launch("cache_append", k_cache_append<float>, dim3((unsigned)n), dim3(AT), 0, st, a);
+  return bf16 ? append_go<__nv_bfloat16>(a, st) : append_go<float>(a, st);
 }
 
 }  // namespace lapnys
