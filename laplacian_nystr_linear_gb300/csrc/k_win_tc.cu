@@ -4,7 +4,7 @@
 // One CTA per SM walks over items of two tiles of 128 query rows that share their
 // keys: the same rows of two query heads of a group when the group's size is
 // even, else neighbouring rows of one head.  The keys come in steps of at most
-// 128: first the steps of the first tokens, then the window's, from its first
+// 64: first the steps of the first tokens, then the window's, from its first
 // key on (TMA rows start anywhere), a last step as wide as it has to be (a
 // multiple of 16), so four first tokens cost a step of 16 keys.
 //
@@ -14,13 +14,14 @@
 //                   grows by more than 2^8 (P <= 2^8: fp32 sums and bf16's
 //                   relative rounding are as good there), so the outputs are
 //                   rescaled on few steps;
-//   warp 8          TMA: K and V tiles through one ring;
-//   warp 9          one thread issues  S = Q K^T  (both operands in shared memory)  and
-//                   O += P V  (P in tensor memory, V as it lies: MN-major):
-//                   PV0 QK0' PV1 QK1' ..., so one tile's softmax runs under the
-//                   other tile's products.  S of a step is complete only when
-//                   the tile's products before it are, so O needs no barrier of
-//                   its own within an item.
+//   warp 8          TMA: K and V tiles through two rings;
+//   warp 9          one thread issues  S = Q K^T  (both operands in shared memory)
+//                   and  O += P V  (P in tensor memory, V as it lies: MN-major).
+//                   A tile has two score buffers, so the scores of the next step
+//                   are there when the softmax of this one ends.  Steps of 128 keys
+//                   leave no room for that beside two outputs of 128 columns: then
+//                   softmax, P V and the next Q K^T of a tile follow one another
+//                   (444 us for the prompt below; two tiles overlap only half of it).
 //
 // Bound: 4 d flops per visible pair on the tensor pipe, or one exponential per
 // pair on the special-function pipe, whichever is longer (d = 64: the latter).
@@ -36,21 +37,21 @@ namespace lapnys {
 
 namespace {
 using namespace wtc;
-constexpr int FT = 128;                 // query rows of a tile, keys of a step
-constexpr int FTH = 384;                // three warpgroups: two of softmax, one that issues
-// registers a thread: 256 * 200 + 128 * 104 <= 384 * 168, the launch's share
-constexpr int FREG_SOFTMAX = 200, FREG_ISSUE = 104;
-constexpr uint32_t PANEL = FT * 128;    // a panel: 128 rows of 64 features, 16 KB
+constexpr int FT = 128;                 // query rows of a tile
+constexpr int FK = 64;                  // keys of a step
+constexpr int FTH = 352;
+constexpr int FNST = 4;                 // tiles of the K ring and of the V ring
 template <int NP>
 struct FwdShape {
-  static constexpr uint32_t TILE = NP * PANEL;
-  static constexpr int NST = NP == 1 ? 8 : 4;
-  static constexpr uint32_t SMEM = (2 + NST) * TILE + 1024;
+  static constexpr uint32_t QTILE = NP * FT * 128;   // panels of 64 features: rows of 128 bytes
+  static constexpr uint32_t TILE = NP * FK * 128;
+  static constexpr uint32_t SMEM = 2 * QTILE + 2 * FNST * TILE + 1024;
 };
 constexpr float kMoveMax = 8.f;         // the maximum moves when it grows by 2^8
 
 struct FwdMaps {
-  CUtensorMap q, k, v;                  // boxes of 64 x 128
+  CUtensorMap q;                        // boxes of 64 x 128
+  CUtensorMap k, v;                     // boxes of 64 x 64
   CUtensorMap k16, v16;                 // boxes of 64 x 16 for narrow steps
 };
 struct FwdGeom {
@@ -89,8 +90,8 @@ __device__ __forceinline__ FwdItem fwd_item(const WinArgs& a, const FwdGeom& gm,
     r.own[s] = r.i0[s] < r.i1[s] ? win_keys(a, r.sq, r.i0[s], r.i1[s]) : WinRange{0, 0, 0};
   }
   r.kr = win_keys(a, r.sq, r.i0[0], r.i1[1]);
-  r.ns = (r.kr.S + FT - 1) / FT;
-  r.nw = r.kr.hi > r.kr.lo ? (r.kr.hi - r.kr.lo + FT - 1) / FT : 0;
+  r.ns = (r.kr.S + FK - 1) / FK;
+  r.nw = r.kr.hi > r.kr.lo ? (r.kr.hi - r.kr.lo + FK - 1) / FK : 0;
   return r;
 }
 // step j of an item: keys [j0, je), and the width of its products
@@ -100,11 +101,11 @@ struct FwdStep {
 __device__ __forceinline__ FwdStep fwd_step(const FwdItem& r, int j) {
   FwdStep s;
   if (j < r.ns) {
-    s.j0 = j * FT;
-    s.je = min(r.kr.S, s.j0 + FT);
+    s.j0 = j * FK;
+    s.je = min(r.kr.S, s.j0 + FK);
   } else {
-    s.j0 = r.kr.lo + (j - r.ns) * FT;
-    s.je = min(r.kr.hi, s.j0 + FT);
+    s.j0 = r.kr.lo + (j - r.ns) * FK;
+    s.je = min(r.kr.hi, s.j0 + FK);
   }
   s.w = (s.je - s.j0 + 15) & ~15;
   return s;
@@ -119,69 +120,68 @@ template <int NP>
 __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ FwdMaps mp,
                                                        const WinArgs a, const FwdGeom gm) {
   using SH = FwdShape<NP>;
-  constexpr int NST = SH::NST;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t full[NST], empty[NST];
+  __shared__ __align__(8) uint64_t kfull[FNST], kempty[FNST], vfull[FNST], vempty[FNST];
   __shared__ __align__(8) uint64_t qfull[2], qempty[2];   // Q tile landed; its products done
-  __shared__ __align__(8) uint64_t sfull[2];              // scores ready
-  __shared__ __align__(8) uint64_t pfull[2];              // P written (128 arrivals)
-  __shared__ __align__(8) uint64_t ofull[2], oempty[2];   // outputs ready; read out (128 arrivals)
-  __shared__ __align__(8) uint64_t drain;
+  __shared__ __align__(8) uint64_t sfull[2][2];           // scores ready, by tile and buffer
+  __shared__ __align__(8) uint64_t pfull[2][2];           // P written (128 arrivals)
+  // a step's P V done, by tile and parity of the step (a step is only known to have
+  // its P V behind it two steps later: one barrier's parity could not tell); O read out
+  __shared__ __align__(8) uint64_t pvdone[2][2], oempty[2];
+  __shared__ __align__(8) uint64_t drain[2];
   __shared__ uint32_t tmem_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
-  const uint32_t qbuf = base, ring = base + 2 * SH::TILE;
+  const uint32_t qbuf = base, kring = base + 2 * SH::QTILE, vring = kring + FNST * SH::TILE;
   auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
 
   if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
-    for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(bar(&full[i]), 1);
-      tc::mbar_init(bar(&empty[i]), 1);
+    for (int i = 0; i < FNST; ++i) {
+      tc::mbar_init(bar(&kfull[i]), 1);
+      tc::mbar_init(bar(&kempty[i]), 2);
+      tc::mbar_init(bar(&vfull[i]), 1);
+      tc::mbar_init(bar(&vempty[i]), 2);
     }
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(bar(&qfull[s]), 1);
-      tc::mbar_init(bar(&qempty[s]), 1);
-      tc::mbar_init(bar(&sfull[s]), 1);
-      tc::mbar_init(bar(&pfull[s]), FT);
-      tc::mbar_init(bar(&ofull[s]), 1);
-      tc::mbar_init(bar(&oempty[s]), FT);
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(bar(&qfull[t]), 1);
+      tc::mbar_init(bar(&qempty[t]), 1);
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(bar(&sfull[t][i]), 1);
+        tc::mbar_init(bar(&pfull[t][i]), FT);
+        tc::mbar_init(bar(&pvdone[t][i]), 1);
+      }
+      tc::mbar_init(bar(&oempty[t]), FT);
+      tc::mbar_init(bar(&drain[t]), 1);
     }
-    tc::mbar_init(bar(&drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_s;
-  // tensor memory: scores (then P) of both tiles, outputs of both
-  const uint32_t tS[2] = {tmem, tmem + FT}, tO[2] = {tmem + 2 * FT, tmem + 2 * FT + NP * 64};
+  // tensor memory: the scores' buffers (then P) of both tiles, outputs of both
+  const uint32_t tO = tmem + 4 * FK;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FREG_ISSUE));
   if (warp == 8) {
     // ---------------- TMA ----------------
     if (elect_one()) {
-      int n = 0;                       // tiles issued to the ring
+      int n = 0;                       // steps issued
       int nq[2] = {0, 0};              // Q tiles issued
       bool bad = false;
-      auto load = [&](const CUtensorMap* wide, const CUtensorMap* narrow, const FwdStep& s, int bh) {
-        const int st = n % NST;
-        if (!wait_or_flag(gm.err, bar(&empty[st]), ((n / NST) & 1) ^ 1u)) return false;
-        const uint32_t dst = ring + st * SH::TILE;
-        tc::mbar_expect_tx(bar(&full[st]), (uint32_t)(NP * s.w * 128));
-#pragma unroll 1
+      auto load = [&](const CUtensorMap* wide, const CUtensorMap* narrow, uint32_t dst, const FwdStep& s,
+                      int bh, uint32_t full) {
+        tc::mbar_expect_tx(full, (uint32_t)(NP * s.w * 128));
+#pragma unroll
         for (int p = 0; p < NP; ++p) {
-          if (s.w == FT) {
-            tma3(dst + p * PANEL, wide, 64 * p, s.j0, bh, bar(&full[st]));
+          if (s.w == FK) {
+            tma3(dst + p * FK * 128, wide, 64 * p, s.j0, bh, full);
           } else {
 #pragma unroll 1
             for (int r = 0; r < s.w; r += 16)
-              tma3(dst + p * PANEL + r * 128, narrow, 64 * p, s.j0 + r, bh, bar(&full[st]));
+              tma3(dst + p * FK * 128 + r * 128, narrow, 64 * p, s.j0 + r, bh, full);
           }
         }
-        ++n;
-        return true;
       };
       for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const FwdItem r = fwd_item(a, gm, it);
@@ -190,118 +190,116 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         for (int t = 0; t < 2; ++t) {
           if (r.own[t].hi == 0) continue;
           if (!wait_or_flag(gm.err, bar(&qempty[t]), (nq[t] & 1) ^ 1u)) { bad = true; break; }
-          tc::mbar_expect_tx(bar(&qfull[t]), SH::TILE);
+          tc::mbar_expect_tx(bar(&qfull[t]), SH::QTILE);
+#pragma unroll
           for (int p = 0; p < NP; ++p)
-            tma3(qbuf + t * SH::TILE + p * PANEL, &mp.q, 64 * p, r.i0[t], r.b * a.Hq + r.head[t],
+            tma3(qbuf + t * SH::QTILE + p * FT * 128, &mp.q, 64 * p, r.i0[t], r.b * a.Hq + r.head[t],
                  bar(&qfull[t]));
           ++nq[t];
         }
         const int bh = r.b * a.Hkv + r.hk;
 #pragma unroll 1
-        for (int j = 0; j < steps && !bad; ++j) {
+        for (int j = 0; j < steps && !bad; ++j, ++n) {
           const FwdStep s = fwd_step(r, j);
-          bad = !load(&mp.k, &mp.k16, s, bh) || !load(&mp.v, &mp.v16, s, bh);
+          const int st = n % FNST;
+          const uint32_t ph = (uint32_t)(n / FNST & 1) ^ 1u;
+          if (!wait_or_flag(gm.err, bar(&kempty[st]), ph)) { bad = true; break; }
+          load(&mp.k, &mp.k16, kring + st * SH::TILE, s, bh, bar(&kfull[st]));
+          if (!wait_or_flag(gm.err, bar(&vempty[st]), ph)) { bad = true; break; }
+          load(&mp.v, &mp.v16, vring + st * SH::TILE, s, bh, bar(&vfull[st]));
         }
       }
-      // every copy has landed before the block ends, also after an expired wait
-#pragma unroll 1
-      for (int i = n > NST ? n - NST : 0; i < n; ++i)
-        wait_or_flag(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
+      // every copy has landed before the block ends, also after an expired wait (then
+      // K of step n may be one more)
+      for (int i = n > FNST ? n - FNST : 0; i < n; ++i) {
+        wait_or_flag(gm.err, bar(&kfull[i % FNST]), (uint32_t)(i / FNST) & 1u);
+        wait_or_flag(gm.err, bar(&vfull[i % FNST]), (uint32_t)(i / FNST) & 1u);
+      }
+      if (bad) wait_or_flag(gm.err, bar(&kfull[n % FNST]), (uint32_t)(n / FNST) & 1u);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (nq[t]) wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)(nq[t] - 1) & 1u);
     }
-  } else if (warp == 9 && elect_one()) {
-    // ---------------- products ----------------
-    int n = 0;                          // ring tiles taken
-    int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
-    bool bad = false;
-    const int ksteps = a.d / 16;
-    const uint32_t id_pv = idesc(FT, a.d, true);
-    auto slot = [&](int i) { return ring + (i % NST) * SH::TILE; };
-    auto take = [&](int i) {            // ring tile i has landed
-      return wait_or_flag(gm.err, bar(&full[i % NST]), (uint32_t)(i / NST) & 1u);
-    };
-    auto qk = [&](int t, int i, int w) {
-      mma_features<NP>(tS[t], qbuf + t * SH::TILE, slot(i), ksteps, idesc(FT, w, false));
-    };
-    auto pv = [&](int t, int i, int w, bool acc) {
-      mma_rows(tO[t], tS[t], slot(i), w / 16, id_pv, acc);
-    };
-    auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
-    for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
-      const FwdItem r = fwd_item(a, gm, it);
-      const int steps = r.ns + r.nw;
-      if (steps == 0) continue;
-      int left[2] = {0, 0};             // steps that the tile still takes part in
+  } else if (warp >= 9) {
+    if (elect_one()) {
+      // ---------------- products: warp 9 for tile 0, warp 10 for tile 1 ----------------
+      const int t = warp - 9;
+      int n = 0;                        // steps begun
+      int nq = 0, no = 0;               // Q tiles, outputs
+      int ks = 0, kp = 0;               // scores, P V issued
+      bool bad = false;
+      const int ksteps = a.d / 16;
+      const uint32_t id_pv = idesc(FT, a.d, true);
+      const uint32_t S = tmem + 2 * t * FK, O = tO + t * NP * 64, Q = qbuf + t * SH::QTILE;
+      auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const FwdItem r = fwd_item(a, gm, it);
+        const WinRange own = t ? r.own[1] : r.own[0];
+        const int steps = r.ns + r.nw;
+        if (steps == 0) continue;
+        int todo = 0;                   // scores still to be issued
 #pragma unroll 1
-      for (int j = 0; j < steps; ++j) {
-        const FwdStep s = fwd_step(r, j);
-        left[0] += fwd_active(a, r.own[0], s);
-        left[1] += fwd_active(a, r.own[1], s);
-      }
-      int todo[2] = {left[0], left[1]};  // scores still to be issued
-      bool begun[2] = {false, false};
-      // scores of step j for tile t, when it takes part
-      auto scores = [&](int t, int j, int i) {
-        const FwdStep s = fwd_step(r, j);
-        if (!fwd_active(a, r.own[t], s)) return true;
-        if (todo[t] == left[t] && !begun[t] &&
-            !wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)nq[t]++ & 1u))
-          return false;
-        tc::fence_after();
-        qk(t, i, s.w);
-        commit(&sfull[t]);
-        if (--todo[t] == 0) commit(&qempty[t]);
-        return true;
-      };
-      const int n0 = n;                 // K of step j: n0 + 2 j, V: n0 + 2 j + 1
-      n += 2 * steps;
-      if (!take(n0) || !scores(0, 0, n0) || !scores(1, 0, n0)) { bad = true; break; }
-      commit(&empty[n0 % NST]);
+        for (int j = 0; j < steps; ++j) todo += fwd_active(a, own, fwd_step(r, j));
+        if (todo > 0 && !wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)nq++ & 1u)) { bad = true; break; }
+        bool begun = false;
+        const int n0 = n;
+        n += steps;
+        // scores of step j; both tiles release the step's K
+        auto scores = [&](int j, const FwdStep& s) {
+          const int st = (n0 + j) % FNST;
+          if (!wait_or_flag(gm.err, bar(&kfull[st]), (uint32_t)((n0 + j) / FNST) & 1u)) return false;
+          if (fwd_active(a, own, s)) {
+            tc::fence_after();
+            const int i = ks++;
+            mma_features<NP, FT, FK>(S + (i & 1) * FK, Q, kring + st * SH::TILE, ksteps,
+                                     idesc(FT, s.w, false));
+            commit(&sfull[t][i & 1]);
+            if (--todo == 0) commit(&qempty[t]);
+          }
+          commit(&kempty[st]);
+          return true;
+        };
+        FwdStep s = fwd_step(r, 0), s1 = fwd_step(r, min(1, steps - 1));
+        if (!scores(0, s) || (steps > 1 && !scores(1, s1))) { bad = true; break; }
 #pragma unroll 1
-      for (int j = 0; j < steps && !bad; ++j) {
-        const int iv = n0 + 2 * j + 1, ik = iv + 1;
-        const FwdStep s = fwd_step(r, j);
-        const bool more = j + 1 < steps;
-        if (!take(iv) || (more && !take(ik))) { bad = true; break; }
-        if (s.j0 + s.w > r.sq.len && r.sq.len < a.Nk) {
-          zero_rows<NP>(slot(iv), r.sq.len - s.j0, s.w);   // V rows at and behind the end
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (bad) break;
-          if (fwd_active(a, r.own[t], s)) {
-            if (!wait_or_flag(gm.err, bar(&pfull[t]), (uint32_t)np[t]++ & 1u) ||
-                (!begun[t] && !wait_or_flag(gm.err, bar(&oempty[t]), ((uint32_t)no[t]++ & 1u) ^ 1u))) {
+        for (int j = 0; j < steps; ++j) {
+          const int st = (n0 + j) % FNST;
+          const FwdStep s2 = fwd_step(r, min(j + 2, steps - 1));
+          if (!wait_or_flag(gm.err, bar(&vfull[st]), (uint32_t)((n0 + j) / FNST) & 1u)) { bad = true; break; }
+          if (fwd_active(a, own, s)) {
+            const uint32_t V = vring + st * SH::TILE;
+            if (s.j0 + s.w > r.sq.len && r.sq.len < a.Nk)
+              zero_rows<NP, FK>(V, r.sq.len - s.j0, s.w);   // rows at and behind the end
+            const int i = kp++;
+            if (!wait_or_flag(gm.err, bar(&pfull[t][i & 1]), (uint32_t)(i >> 1) & 1u) ||
+                (!begun && !wait_or_flag(gm.err, bar(&oempty[t]), ((uint32_t)no++ & 1u) ^ 1u))) {
               bad = true;
               break;
             }
             tc::fence_after();
-            pv(t, iv, s.w, begun[t]);
-            begun[t] = true;
-            if (--left[t] == 0) commit(&ofull[t]);
+            mma_rows<FK>(O, S + (i & 1) * FK, V, s.w / 16, id_pv, begun);
+            begun = true;
+            commit(&pvdone[t][i & 1]);
           }
-          if (more && !scores(t, j + 1, ik)) bad = true;
+          commit(&vempty[st]);
+          if (j + 2 < steps && !scores(j + 2, s2)) { bad = true; break; }
+          s = s1;
+          s1 = s2;
         }
-        commit(&empty[iv % NST]);
-        if (more) commit(&empty[ik % NST]);
+      }
+      if (bad) {  // what was issued ends before tensor memory is freed
+        commit(&drain[t]);
+        wait_or_flag(gm.err, bar(&drain[t]), 0);
       }
     }
-    if (bad) {  // what was issued ends before tensor memory is freed
-      commit(&drain);
-      wait_or_flag(gm.err, bar(&drain), 0);
-    }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FREG_SOFTMAX));
     // ---------------- softmax ----------------
     const int t = warp >> 2;
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t S = (t ? tS[1] : tS[0]) + lanes, O = (t ? tO[1] : tO[0]) + lanes;
+    const uint32_t S0 = tmem + 2 * t * FK + lanes, O = tO + t * NP * 64 + lanes;
     const float c = a.scale_log2;
-    int nsf = 0, nof = 0;
+    int k = 0;                            // steps of this tile
     bool bad = false;
     for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
       const FwdItem r = fwd_item(a, gm, it);
@@ -319,26 +317,27 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       float m = -INFINITY;
       f32x2 ls[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};   // sums of the row, four chains
       bool any = false;
+#pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const FwdStep s = fwd_step(r, j);
         if (!fwd_active(a, own, s)) continue;
-        if (!wait_warp(gm.err, bar(&sfull[t]), (uint32_t)nsf & 1u)) {
+        const uint32_t S = S0 + (k & 1) * FK;
+        if (!wait_warp(gm.err, bar(&sfull[t][k & 1]), (uint32_t)(k >> 1) & 1u)) {
           bad = true;
           break;
         }
-        ++nsf;
         tc::fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ld32(S + 32 * q, v[q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ld_wait(v[q]);
-        const bool whole = rows_ok && s.je - s.j0 == FT && s.j0 + FT - 1 <= free_hi &&
+        uint32_t v[2][32];
+        ld32(S, v[0]);
+        ld32(S + 32, v[1]);
+        const bool whole = rows_ok && s.je - s.j0 == FK && s.j0 + FK - 1 <= free_hi &&
                            (s.j0 >= free_lo || s.je <= a.sinks);
+        ld_wait(v[0]);
+        ld_wait(v[1]);
         if (!whole) {
           const int h = min(wr.hi, s.je) - s.j0, l = wr.lo - s.j0, z = wr.S - s.j0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const uint32_t bits = seen_bits(l - 32 * q, h - 32 * q, z - 32 * q);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -348,10 +347,12 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         float mq[4];                       // four chains: one is as long as its latencies
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          mq[q] = fmaxf(__uint_as_float(v[q][0]), __uint_as_float(v[q][1]));
+          const uint32_t (&x)[32] = v[q >> 1];
+          const int e0 = 16 * (q & 1);
+          mq[q] = fmaxf(__uint_as_float(x[e0]), __uint_as_float(x[e0 + 1]));
 #pragma unroll
-          for (int e = 2; e < 32; e += 2)
-            mq[q] = fmaxf(fmaxf(mq[q], __uint_as_float(v[q][e])), __uint_as_float(v[q][e + 1]));
+          for (int e = 2; e < 16; e += 2)
+            mq[q] = fmaxf(fmaxf(mq[q], __uint_as_float(x[e0 + e])), __uint_as_float(x[e0 + e + 1]));
         }
         const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const bool move = (mx - m) * c > kMoveMax || (m == -INFINITY && mx > m);
@@ -360,6 +361,12 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
           const float f = move ? exp2_ftz((m - mn) * c) : 1.f;   // m = -inf: 0
           ls[0] = mul2(ls[0], pack2(f, f));
           ls[1] = mul2(ls[1], pack2(f, f));
+          // the step before has been added up (and this one's P V waits for this P)
+          if (!wait_warp(gm.err, bar(&pvdone[t][(k - 1) & 1]), (uint32_t)((k - 1) >> 1) & 1u)) {
+            bad = true;
+            break;
+          }
+          tc::fence_after();
 #pragma unroll 1
           for (int q = 0; q < a.d; q += 16) {
             uint32_t o[16];
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         const float off = m == -INFINITY ? 0.f : -m * c;
         const f32x2 c2 = pack2(c, c), off2 = pack2(off, off);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -387,7 +394,8 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         }
         st_wait();
         tc::fence_before();
-        arrive(bar(&pfull[t]));
+        arrive(bar(&pfull[t][k & 1]));
+        ++k;
       }
       if (bad) break;
       const float2 la = unpack2(ls[0]), lb = unpack2(ls[1]);
@@ -396,15 +404,13 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         a.lse[((size_t)r.b * a.Hq + head) * a.Nq + i] = l == 0.f ? -INFINITY : fmaf(m, c, log2f(l));
       const float w = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       if (any) {
-        if (!wait_warp(gm.err, bar(&ofull[t]), (uint32_t)nof & 1u)) {
+        if (!wait_warp(gm.err, bar(&pvdone[t][(k - 1) & 1]), (uint32_t)((k - 1) >> 1) & 1u)) {
           bad = true;
           break;
         }
-        ++nof;
         tc::fence_after();
       }
-      __nv_bfloat16* dst = (__nv_bfloat16*)a.out +
-                           (((size_t)r.b * a.Hq + head) * a.Nq + i) * a.d;
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (((size_t)r.b * a.Hq + head) * a.Nq + i) * a.d;
 #pragma unroll 1
       for (int q = 0; q < a.d; q += 16) {
         uint32_t o[16];
@@ -467,8 +473,8 @@ cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st) {
   gm.npair = gm.by_head ? gm.qt : (gm.qt + 1) / 2;
   gm.items = a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g) * gm.npair;
   if (!win_map(&mp.q, a.q, a.B * a.Hq, a.Nq, a.d, FT) ||
-      !win_map(&mp.k, a.k, a.B * a.Hkv, a.Nk, a.d, FT) ||
-      !win_map(&mp.v, a.v, a.B * a.Hkv, a.Nk, a.d, FT) ||
+      !win_map(&mp.k, a.k, a.B * a.Hkv, a.Nk, a.d, FK) ||
+      !win_map(&mp.v, a.v, a.B * a.Hkv, a.Nk, a.d, FK) ||
       !win_map(&mp.k16, a.k, a.B * a.Hkv, a.Nk, a.d, 16) ||
       !win_map(&mp.v16, a.v, a.B * a.Hkv, a.Nk, a.d, 16))
     return cudaErrorInvalidValue;

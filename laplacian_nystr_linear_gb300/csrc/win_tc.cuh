@@ -75,35 +75,36 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
 // by a constant in the descriptors' address field (16-byte units), so the loops
 // are unrolled over one base: built anew per slice, the descriptors cost more
 // than the product (prompt of 32768 tokens, heads of 128: 820 us so).
-// D (+)= A B^T over d features, A and B in shared memory
-template <int NP>
+// D (+)= A B^T over d features, A and B in shared memory (panels of AR and BR rows)
+template <int NP, int AR = 128, int BR = 128>
 __device__ __forceinline__ void mma_features(uint32_t d_tmem, uint32_t A, uint32_t B, int ksteps,
                                              uint32_t id) {
   const uint64_t da = desc_k(A), db = desc_k(B);
 #pragma unroll
-  for (int k = 0; k < 4 * NP; ++k) {
-    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-    if (k < ksteps) tc::mma_bf16(d_tmem, da + off, db + off, id, k > 0);
-  }
+  for (int k = 0; k < 4 * NP; ++k)
+    if (k < ksteps)
+      tc::mma_bf16(d_tmem, da + (((k >> 2) * AR * 128 + (k & 3) * 32) >> 4),
+                   db + (((k >> 2) * BR * 128 + (k & 3) * 32) >> 4), id, k > 0);
 }
 // D (+)= A B over the `slices` 16-row slices of B, A in tensor memory; slices 4 to
 // 7 of A lie `skip` columns behind their place
+template <int BR = 128>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t A, uint32_t B, int slices,
                                          uint32_t id, bool acc, uint32_t skip = 0) {
-  const uint64_t db = desc_mn(B, 16384);
+  const uint64_t db = desc_mn(B, BR * 128);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int k = 0; k < BR / 16; ++k)
     if (k < slices) mma_ts(d_tmem, A + 8 * k + (k < 4 ? 0 : skip), db + 128 * k, id, acc || k > 0);
 }
 
 // rows [r0, w) of an NP-panel tile to zero, by the thread that issues the products
-template <int NP>
+template <int NP, int ROWS = 128>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int w) {
 #pragma unroll 1
   for (int r = r0; r < w; ++r)
 #pragma unroll
     for (int e = 0; e < 8 * NP; ++e)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (e >> 3) * 16384 +
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (e >> 3) * (ROWS * 128) +
                                                                     r * 128 + (e & 7) * 16),
                    "r"(0)
                    : "memory");
