@@ -110,9 +110,34 @@ __device__ __forceinline__ FwdStep fwd_step(const FwdItem& r, int j) {
   s.w = (s.je - s.j0 + 15) & ~15;
   return s;
 }
-// does a tile that sees the keys `o` see any of the step's?
-__device__ __forceinline__ bool fwd_active(const WinArgs& a, const WinRange& o, const FwdStep& s) {
-  return s.j0 < o.hi && (s.je > o.lo || s.j0 < a.sinks);
+// The steps that one tile takes part in, as step numbers: those of the first
+// tokens, those of the window that it sees, and window steps that still hold first
+// tokens (where both ranges are one); and the widths.
+struct FwdPlan {
+  int ns, steps, head, lo, hi;     // [0, head) and [lo, hi)
+  int wS, wW;                      // width of the last step of either kind
+  __device__ __forceinline__ bool on(int j) const { return j < head || (j >= lo && j < hi); }
+  __device__ __forceinline__ int width(int j) const {
+    return j == ns - 1 ? wS : (j == steps - 1 ? wW : FK);
+  }
+  __device__ __forceinline__ int count() const {
+    return max(head, 0) + max(0, hi - max(lo, head));
+  }
+};
+__device__ __forceinline__ FwdPlan fwd_plan(const WinArgs& a, const FwdItem& r, const WinRange& own) {
+  FwdPlan p;
+  p.ns = r.ns;
+  p.steps = r.ns + r.nw;
+  p.head = p.lo = p.hi = 0;
+  if (own.hi > 0) {
+    const int first = min(a.sinks, own.hi);        // first tokens that it may see
+    p.head = r.ns + (r.kr.lo < first ? (first - r.kr.lo + FK - 1) / FK : 0);
+    p.lo = r.ns + (own.lo - r.kr.lo) / FK;
+    p.hi = r.ns + (own.hi - r.kr.lo + FK - 1) / FK;
+  }
+  p.wS = (r.kr.S - (r.ns - 1) * FK + 15) & ~15;
+  p.wW = (r.kr.hi - r.kr.lo - (r.nw - 1) * FK + 15) & ~15;
+  return p;
 }
 }  // namespace
 
@@ -237,39 +262,40 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         const WinRange own = t ? r.own[1] : r.own[0];
         const int steps = r.ns + r.nw;
         if (steps == 0) continue;
-        int todo = 0;                   // scores still to be issued
-#pragma unroll 1
-        for (int j = 0; j < steps; ++j) todo += fwd_active(a, own, fwd_step(r, j));
+        const FwdPlan plan = fwd_plan(a, r, own);
+        int todo = plan.count();        // scores still to be issued
+        const int clean = r.sq.len < a.Nk ? r.sq.len : kWinUnbounded;   // V rows from here on: zeros
         if (todo > 0 && !wait_or_flag(gm.err, bar(&qfull[t]), (uint32_t)nq++ & 1u)) { bad = true; break; }
         bool begun = false;
         const int n0 = n;
         n += steps;
         // scores of step j; both tiles release the step's K
-        auto scores = [&](int j, const FwdStep& s) {
+        auto scores = [&](int j) {
           const int st = (n0 + j) % FNST;
           if (!wait_or_flag(gm.err, bar(&kfull[st]), (uint32_t)((n0 + j) / FNST) & 1u)) return false;
-          if (fwd_active(a, own, s)) {
+          if (plan.on(j)) {
             tc::fence_after();
             const int i = ks++;
             mma_features<NP, FT, FK>(S + (i & 1) * FK, Q, kring + st * SH::TILE, ksteps,
-                                     idesc(FT, s.w, false));
+                                     idesc(FT, plan.width(j), false));
             commit(&sfull[t][i & 1]);
             if (--todo == 0) commit(&qempty[t]);
           }
           commit(&kempty[st]);
           return true;
         };
-        FwdStep s = fwd_step(r, 0), s1 = fwd_step(r, min(1, steps - 1));
-        if (!scores(0, s) || (steps > 1 && !scores(1, s1))) { bad = true; break; }
+        if (!scores(0) || (steps > 1 && !scores(1))) { bad = true; break; }
 #pragma unroll 1
         for (int j = 0; j < steps; ++j) {
           const int st = (n0 + j) % FNST;
-          const FwdStep s2 = fwd_step(r, min(j + 2, steps - 1));
           if (!wait_or_flag(gm.err, bar(&vfull[st]), (uint32_t)((n0 + j) / FNST) & 1u)) { bad = true; break; }
-          if (fwd_active(a, own, s)) {
+          if (plan.on(j)) {
             const uint32_t V = vring + st * SH::TILE;
-            if (s.j0 + s.w > r.sq.len && r.sq.len < a.Nk)
-              zero_rows<NP, FK>(V, r.sq.len - s.j0, s.w);   // rows at and behind the end
+            const int w = plan.width(j);
+            if (j >= steps - 1 || j == r.ns - 1) {           // the last of either kind may end behind it
+              const int j0 = fwd_step(r, j).j0;
+              if (j0 + w > clean) zero_rows<NP, FK>(V, clean - j0, w);
+            }
             const int i = kp++;
             if (!wait_or_flag(gm.err, bar(&pfull[t][i & 1]), (uint32_t)(i >> 1) & 1u) ||
                 (!begun && !wait_or_flag(gm.err, bar(&oempty[t]), ((uint32_t)no++ & 1u) ^ 1u))) {
@@ -277,14 +303,12 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
               break;
             }
             tc::fence_after();
-            mma_rows<FK>(O, S + (i & 1) * FK, V, s.w / 16, id_pv, begun);
+            mma_rows<FK>(O, S + (i & 1) * FK, V, w / 16, id_pv, begun);
             begun = true;
             commit(&pvdone[t][i & 1]);
           }
           commit(&vempty[st]);
-          if (j + 2 < steps && !scores(j + 2, s2)) { bad = true; break; }
-          s = s1;
-          s1 = s2;
+          if (j + 2 < steps && !scores(j + 2)) { bad = true; break; }
         }
       }
       if (bad) {  // what was issued ends before tensor memory is freed
@@ -307,7 +331,8 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       const WinRange own = t ? r.own[1] : r.own[0];
       const int i0 = t ? r.i0[1] : r.i0[0], i1 = t ? r.i1[1] : r.i1[0];
       const int head = t ? r.head[1] : r.head[0];
-      const int steps = r.ns + r.nw, i = i0 + row;
+      const FwdPlan plan = fwd_plan(a, r, own);
+      const int steps = plan.steps, i = i0 + row;
       WinRow wr = win_row(a, r.sq, i);
       if (i >= i1) wr = WinRow{0, 0, 0};
       // keys that every row of the tile sees: no mask
@@ -319,8 +344,8 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
       bool any = false;
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
+        if (!plan.on(j)) continue;
         const FwdStep s = fwd_step(r, j);
-        if (!fwd_active(a, own, s)) continue;
         const uint32_t S = S0 + (k & 1) * FK;
         if (!wait_warp(gm.err, bar(&sfull[t][k & 1]), (uint32_t)(k >> 1) & 1u)) {
           bad = true;
