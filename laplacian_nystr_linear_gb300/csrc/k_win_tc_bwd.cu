@@ -18,10 +18,13 @@
 //               columns, so the halves need no barrier and drift apart: one's
 //               exponentials run under the other's multiplications;
 //   warp 8      TMA (the resident tiles, and two rings);
-//   warp 9      one thread issues the products, in an order that keeps the tensor pipe busy
-//               while the elementwise warps work on the other product:
-//                 dq:   dP(j+1) dQ(j) S(j+2)    (S in two buffers)
+//   warp 9 (dq: and 10)  one thread issues the products, the bf16 tile's product
+//               always before the one that overwrites it, so that their order needs
+//               no barrier:
+//                 dq:   dQ(j) S(j+2) (S in two buffers)  |  dP(j+1)
 //                 dkv:  dV(j) S(j+1) dK(j) dP(j+1)
+//               (two threads for dkv as well, dV S | dK dP: 4 heads of 128 for 16,
+//               244 -> 316 us, the score product then waits behind dK);
 //   warp 10     dkv: log-sum and D of a step's queries into shared memory.
 //
 // Key tiles with first tokens are seen by all later queries: their queries are
@@ -140,7 +143,8 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t kfull[NRING1], kempty[NRING1], vfull[NRING2], vempty[NRING2];
   __shared__ __align__(8) uint64_t qfull, qempty;       // Q and dO landed; their products done
-  __shared__ __align__(8) uint64_t sfull[2], dpfull, dsfull, ofull, oempty, drain;
+  __shared__ __align__(8) uint64_t sfull[2], dpfull, ofull, oempty, drain[2];
+  __shared__ __align__(8) uint64_t dsfull[2];           // (by parity: two threads wait for it)
   __shared__ __align__(8) uint64_t dhfull;              // both halves of D written
   __shared__ uint32_t tmem_s;
   __shared__ float Dh[2][BT];
@@ -159,15 +163,17 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       tc::mbar_init(bar(&vempty[i]), 1);
     }
     tc::mbar_init(bar(&qfull), 1);
-    tc::mbar_init(bar(&qempty), 1);
+    tc::mbar_init(bar(&qempty), 2);
     tc::mbar_init(bar(&sfull[0]), 1);
     tc::mbar_init(bar(&sfull[1]), 1);
     tc::mbar_init(bar(&dhfull), 256);
     tc::mbar_init(bar(&dpfull), 1);
-    tc::mbar_init(bar(&dsfull), 256);
+    tc::mbar_init(bar(&dsfull[0]), 256);
+    tc::mbar_init(bar(&dsfull[1]), 256);
     tc::mbar_init(bar(&ofull), 1);
     tc::mbar_init(bar(&oempty), 256);
-    tc::mbar_init(bar(&drain), 1);
+    tc::mbar_init(bar(&drain[0]), 1);
+    tc::mbar_init(bar(&drain[1]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc::fence_before();
@@ -214,10 +220,11 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       }
       if (nq) wait_or_flag(gm.err, bar(&qfull), (uint32_t)(nq - 1) & 1u);
     } else if (warp == 9 && elect_one()) {
-      // ---------------- products ----------------
+      // ---------------- scores and dQ ----------------
       int n = 0, nq = 0, no = 0;        // steps, items
       bool bad = false;
       const int ksteps = a.d / 16;
+      const uint32_t id = idesc(BT, BT, false), id_q = idesc(BT, a.d, true);
       auto commit = [&](uint64_t* b) { tc::commit(bar(b)); };
       for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
         const DqItem r = dq_item(a, gm, it);
@@ -225,48 +232,70 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         if (!wait_or_flag(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
         const int n0 = n;
         n += r.steps;
-        auto scores = [&](int j) {
-          const Step s = dq_step(r, j);
-          const int i = n0 + j, sk = i % NRING1;
+        auto scores = [&](const Step& s, int i) {
+          const int sk = i % NRING1;
           const uint32_t K = Kr + sk * SH::TILE;
           if (!wait_or_flag(gm.err, bar(&kfull[sk]), (uint32_t)(i / NRING1) & 1u)) return false;
-          if (s.r0 + s.w > r.sq.len && r.sq.len < a.Nk) {
-            zero_rows<NP>(K, r.sq.len - s.r0, s.w);
+          if (s.r0 + s.w > r.sq.len && r.sq.len < a.Nk) zero_rows<NP>(K, r.sq.len - s.r0, s.w);
+          tc::fence_after();
+          mma_features<NP>(tS + (i & 1) * BT, Qb, K, ksteps, s.w == BT ? id : idesc(BT, s.w, false));
+          commit(&sfull[i & 1]);
+          if (i + 1 == n) commit(&qempty);
+          return true;
+        };
+        Step s = dq_step(r, 0), s1 = dq_step(r, min(1, r.steps - 1));
+        if (!scores(s, n0) || (r.steps > 1 && !scores(s1, n0 + 1))) { bad = true; break; }
+#pragma unroll 1
+        for (int i = n0; i < n; ++i) {
+          const int sk = i % NRING1;
+          const Step s2 = dq_step(r, min(i - n0 + 2, r.steps - 1));
+          if (!wait_or_flag(gm.err, bar(&dsfull[i & 1]), (uint32_t)(i >> 1) & 1u) ||
+              (i == n0 && !wait_or_flag(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u))) {
+            bad = true;
+            break;
           }
           tc::fence_after();
-          mma_features<NP>(tS + (i & 1) * BT, Qb, K, ksteps, idesc(BT, s.w, false));
-          commit(&sfull[i & 1]);
-          return true;
-        };
-        auto grads = [&](int j) {
-          const Step s = dq_step(r, j);
-          const int i = n0 + j, sv = i % NRING2;
-          if (!wait_or_flag(gm.err, bar(&vfull[sv]), (uint32_t)(i / NRING2) & 1u)) return false;
-          tc::fence_after();
-          mma_features<NP>(tP, Ob, Vr + sv * SH::TILE, ksteps, idesc(BT, s.w, false));
-          commit(&dpfull);
-          commit(&vempty[sv]);
-          if (j + 1 == r.steps) commit(&qempty);   // the last product that reads Q or dO
-          return true;
-        };
-        if (!scores(0) || !grads(0) || (r.steps > 1 && !scores(1))) { bad = true; break; }
-#pragma unroll 1
-        for (int j = 0; j < r.steps; ++j) {
-          const Step s = dq_step(r, j);
-          const int i = n0 + j, sk = i % NRING1;
-          if (!wait_or_flag(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
-          if (j + 1 < r.steps && !grads(j + 1)) { bad = true; break; }
-          if (j == 0 && !wait_or_flag(gm.err, bar(&oempty), ((uint32_t)no++ & 1u) ^ 1u)) { bad = true; break; }
-          tc::fence_after();
-          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, idesc(BT, a.d, true), j > 0, 32);
+          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, id_q, i > n0, 32);
           commit(&kempty[sk]);
-          if (j + 1 == r.steps) commit(&ofull);
-          if (j + 2 < r.steps && !scores(j + 2)) { bad = true; break; }
+          if (i + 1 == n) commit(&ofull);
+          if (i + 2 < n && !scores(s2, i + 2)) { bad = true; break; }
+          s = s1;
+          s1 = s2;
         }
       }
       if (bad) {  // what was issued ends before tensor memory is freed
-        commit(&drain);
-        wait_or_flag(gm.err, bar(&drain), 0);
+        commit(&drain[0]);
+        wait_or_flag(gm.err, bar(&drain[0]), 0);
+      }
+    } else if (warp == 10 && elect_one()) {
+      // ---------------- dP ----------------
+      int n = 0, nq = 0;                // steps, items
+      bool bad = false;
+      const int ksteps = a.d / 16;
+      const uint32_t id = idesc(BT, BT, false);
+      for (int it = blockIdx.x; it < gm.items && !bad; it += gridDim.x) {
+        const DqItem r = dq_item(a, gm, it);
+        if (r.steps == 0) continue;
+        if (!wait_or_flag(gm.err, bar(&qfull), (uint32_t)nq++ & 1u)) { bad = true; break; }
+#pragma unroll 1
+        for (int j = 0; j < r.steps; ++j, ++n) {
+          const int sv = n % NRING2, w = dq_step(r, j).w;
+          // (the step before has been read)
+          if (!wait_or_flag(gm.err, bar(&vfull[sv]), (uint32_t)(n / NRING2) & 1u) ||
+              (n > 0 && !wait_or_flag(gm.err, bar(&dsfull[(n - 1) & 1]), (uint32_t)((n - 1) >> 1) & 1u))) {
+            bad = true;
+            break;
+          }
+          tc::fence_after();
+          mma_features<NP>(tP, Ob, Vr + sv * SH::TILE, ksteps, w == BT ? id : idesc(BT, w, false));
+          tc::commit(bar(&dpfull));
+          tc::commit(bar(&vempty[sv]));
+          if (j + 1 == r.steps) tc::commit(bar(&qempty));
+        }
+      }
+      if (bad) {
+        tc::commit(bar(&drain[1]));
+        wait_or_flag(gm.err, bar(&drain[1]), 0);
       }
     }
   } else {
@@ -347,7 +376,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         ds_store(S + 16, v[1], dp[1], D2, whole, whole ? 0u : seen_bits(l - 32, h - 32, z - 32));
         st_wait();
         tc::fence_before();
-        arrive(bar(&dsfull));
+        arrive(bar(&dsfull[n & 1]));
       }
       if (bad) break;
       if (r.steps > 0) {
