@@ -13,19 +13,21 @@
 // memory, over the columns it came from; K, Q, dO tiles are read as they lie in
 // shared memory both K-major (scores) and MN-major (gradients).
 //
-//   warps 0-7   elementwise work, one row and half of the columns per thread.
-//               Each half writes its bf16 values (32 columns) over its own 64
-//               columns, so the halves need no barrier and drift apart: one's
-//               exponentials run under the other's multiplications;
-//   warp 8      TMA (the resident tiles, and two rings);
-//   warp 9 (dq: and 10)  one thread issues the products, the bf16 tile's product
+//   warps 0-15  elementwise work, one row and a quarter of the columns per thread.
+//               Each group of columns writes its bf16 values (16 columns) over its
+//               own 32 columns, so the groups need no barrier and drift apart: one's
+//               exponentials run under the others' multiplications, and four warps
+//               a scheduler hide the latencies of tensor memory (two of half the
+//               columns each: 3700 cycles a step of dkv, the products take 1024);
+//   warp 16     TMA (the resident tiles, and two rings);
+//   warp 17 (dq: and 18)  one thread issues the products, the bf16 tile's product
 //               always before the one that overwrites it, so that their order needs
 //               no barrier:
 //                 dq:   dQ(j) S(j+2) (S in two buffers)  |  dP(j+1)
 //                 dkv:  dV(j) S(j+1) dK(j) dP(j+1)
 //               (two threads for dkv as well, dV S | dK dP: 4 heads of 128 for 16,
 //               244 -> 316 us, the score product then waits behind dK);
-//   warp 10     dkv: log-sum and D of a step's queries into shared memory.
+//   warp 18     dkv: log-sum and D of a step's queries into shared memory.
 //
 // Key tiles with first tokens are seen by all later queries: their queries are
 // cut into chunks, one item each, with fp32 partials that k_win_join adds.
@@ -41,7 +43,9 @@ namespace lapnys {
 namespace {
 using namespace wtc;
 constexpr int BT = 128;                 // rows and columns of a tile
-constexpr int BTH = 384;
+constexpr int BEW = 512;                // elementwise threads
+constexpr int BTH = BEW + 128;
+constexpr int WI = BEW / 32;            // first of the warps that copy and issue
 constexpr uint32_t PANEL = BT * 128;
 constexpr int NRING1 = 3, NRING2 = 2;   // tiles of the rings (K, V; Q, dO)
 template <int NP>
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t Qb = base, Ob = Qb + SH::TILE, Kr = Ob + SH::TILE, Vr = Kr + NRING1 * SH::TILE;
   auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
-  if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
+  if (warp == WI) tc::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
     for (int i = 0; i < NRING1; ++i) {
       tc::mbar_init(bar(&kfull[i]), 1);
@@ -166,12 +170,12 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
     tc::mbar_init(bar(&qempty), 2);
     tc::mbar_init(bar(&sfull[0]), 1);
     tc::mbar_init(bar(&sfull[1]), 1);
-    tc::mbar_init(bar(&dhfull), 256);
+    tc::mbar_init(bar(&dhfull), BEW);
     tc::mbar_init(bar(&dpfull), 1);
-    tc::mbar_init(bar(&dsfull[0]), 256);
-    tc::mbar_init(bar(&dsfull[1]), 256);
+    tc::mbar_init(bar(&dsfull[0]), BEW);
+    tc::mbar_init(bar(&dsfull[1]), BEW);
     tc::mbar_init(bar(&ofull), 1);
-    tc::mbar_init(bar(&oempty), 256);
+    tc::mbar_init(bar(&oempty), BEW);
     tc::mbar_init(bar(&drain[0]), 1);
     tc::mbar_init(bar(&drain[1]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -183,8 +187,8 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   // tensor memory: S (then dS) in two buffers, dP, dQ
   const uint32_t tS = tmem, tP = tmem + 2 * BT, tO = tmem + 3 * BT;
 
-  if (warp >= 8) {
-    if (warp == 8 && elect_one()) {
+  if (warp >= WI) {
+    if (warp == WI && elect_one()) {
       // ---------------- TMA ----------------
       int n = 0, nq = 0;
       bool bad = false;
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         if (i >= n - NRING2) wait_or_flag(gm.err, bar(&vfull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
       }
       if (nq) wait_or_flag(gm.err, bar(&qfull), (uint32_t)(nq - 1) & 1u);
-    } else if (warp == 9 && elect_one()) {
+    } else if (warp == WI + 1 && elect_one()) {
       // ---------------- scores and dQ ----------------
       int n = 0, nq = 0, no = 0;        // steps, items
       bool bad = false;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
             break;
           }
           tc::fence_after();
-          mma_rows(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, id_q, i > n0, 32);
+          mma_rows<BT, 32>(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, id_q, i > n0);
           commit(&kempty[sk]);
           if (i + 1 == n) commit(&ofull);
           if (i + 2 < n && !scores(s2, i + 2)) { bad = true; break; }
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         commit(&drain[0]);
         wait_or_flag(gm.err, bar(&drain[0]), 0);
       }
-    } else if (warp == 10 && elect_one()) {
+    } else if (warp == WI + 2 && elect_one()) {
       // ---------------- dP ----------------
       int n = 0, nq = 0;                // steps, items
       bool bad = false;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
     }
   } else {
     // ---------------- elementwise ----------------
-    const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
+    const int grp = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 32 * grp;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float c = a.scale_log2;
     int n = 0, no = 0, nd = 0;
@@ -310,33 +314,33 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       const int i = r.i0 + row;
       const size_t qrow = ((size_t)r.b * a.Hq + r.h) * a.Nq + i;
       const WinRow wr = win_row(a, r.sq, i);
-      // D = dout.out, half of the features each
+      // D = dout.out, half of the features by either of the first groups
       float D = 0.f, lse = 0.f;
-      if (i < r.i1 && r.steps > 0) {
-        lse = a.lse[qrow];
-        const int hd = a.d / 2;
-        const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + half * hd;
-        const __nv_bfloat16* y = (const __nv_bfloat16*)a.out + qrow * a.d + half * hd;
+      if (r.steps > 0) {
+        if (i < r.i1) lse = a.lse[qrow];
+        if (i < r.i1 && grp < 2) {
+          const int hd = a.d / 2;
+          const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + grp * hd;
+          const __nv_bfloat16* y = (const __nv_bfloat16*)a.out + qrow * a.d + grp * hd;
 #pragma unroll 4
-        for (int e = 0; e < hd; e += 8) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + e));
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(y + e));
-          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+          for (int e = 0; e < hd; e += 8) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + e));
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(y + e));
+            const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            D = fmaf(__uint_as_float(us[z] << 16), __uint_as_float(ws[z] << 16), D);
-            D = fmaf(__uint_as_float(us[z] & 0xffff0000u), __uint_as_float(ws[z] & 0xffff0000u), D);
+            for (int z = 0; z < 4; ++z) {
+              D = fmaf(__uint_as_float(us[z] << 16), __uint_as_float(ws[z] << 16), D);
+              D = fmaf(__uint_as_float(us[z] & 0xffff0000u), __uint_as_float(ws[z] & 0xffff0000u), D);
+            }
           }
         }
-      }
-      if (r.steps > 0) {
         // (written again for the next item only behind `ofull`, for which the other
-        // half has worked through this one's steps)
-        Dh[half][row] = D;
+        // groups have worked through this one's steps)
+        if (grp < 2) Dh[grp][row] = D;
         arrive(bar(&dhfull));
         if (!wait_warp(gm.err, bar(&dhfull), (uint32_t)nd++ & 1u)) break;
         D = Dh[0][row] + Dh[1][row];
-        if (half == 0 && i < r.i1) a.D[qrow] = D;
+        if (grp == 0 && i < r.i1) a.D[qrow] = D;
       }
 
       const int p0 = r.sq.qp + r.i0, p1 = r.sq.qp + r.i1 - 1;
@@ -349,31 +353,24 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         const uint32_t S = tS + (n & 1) * BT + lanes + c0, P = tP + lanes + c0;
         if (!wait_warp(gm.err, bar(&sfull[n & 1]), (uint32_t)(n >> 1) & 1u)) { bad = true; break; }
         tc::fence_after();
-        uint32_t v[2][32];
-        ld32(S, v[0]);
-        ld32(S + 32, v[1]);
-        ld_wait(v[0]);
-        ld_wait(v[1]);
+        uint32_t v[32];
+        ld32(S, v);
+        ld_wait(v);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), c2, o2));
-            v[q][e] = __float_as_uint(exp2_ftz(x.x));
-            v[q][e + 1] = __float_as_uint(exp2_ftz(x.y));
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, o2));
+          v[e] = __float_as_uint(exp2_ftz(x.x));
+          v[e + 1] = __float_as_uint(exp2_ftz(x.y));
+        }
         if (!wait_warp(gm.err, bar(&dpfull), (uint32_t)n & 1u)) { bad = true; break; }
         tc::fence_after();
-        uint32_t dp[2][32];
-        ld32(P, dp[0]);
-        ld32(P + 32, dp[1]);
+        uint32_t dp[32];
+        ld32(P, dp);
         const bool whole = rows_ok && s.re - s.r0 == BT && s.r0 + BT - 1 <= free_hi &&
                            (s.r0 >= free_lo || s.re <= a.sinks);
         const int h = min(wr.hi, s.re) - s.r0 - c0, l = wr.lo - s.r0 - c0, z = wr.S - s.r0 - c0;
-        ld_wait(dp[0]);
-        ld_wait(dp[1]);
-        ds_store(S, v[0], dp[0], D2, whole, whole ? 0u : seen_bits(l, h, z));
-        ds_store(S + 16, v[1], dp[1], D2, whole, whole ? 0u : seen_bits(l - 32, h - 32, z - 32));
+        ld_wait(dp);
+        ds_store(S, v, dp, D2, whole, whole ? 0u : seen_bits(l, h, z));
         st_wait();
         tc::fence_before();
         arrive(bar(&dsfull[n & 1]));
@@ -384,10 +381,10 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         ++no;
         tc::fence_after();
       }
-      // d / 16 pieces of 16 columns, shared by the halves
+      // d / 16 pieces of 16 columns, shared by the groups
       __nv_bfloat16* dst = (__nv_bfloat16*)a.dq + qrow * a.d;
 #pragma unroll 1
-      for (int q = 16 * half; q < a.d; q += 32) {
+      for (int q = 16 * grp; q < a.d; q += 64) {
         uint32_t o[16];
         if (r.steps > 0) {
           tc::tmem_ld<16>(tO + lanes + q, o);
@@ -414,7 +411,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (warp == WI) tc::tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -486,7 +483,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
   const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t Kb = base, Vb = Kb + SH::TILE, Qr = Vb + SH::TILE, Or = Qr + NRING1 * SH::TILE;
   auto bar = [](uint64_t* b) { return tc::smem_u32(b); };
-  if (warp == 9) tc::tmem_alloc(&tmem_s, 512);
+  if (warp == WI) tc::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
     for (int i = 0; i < NRING1; ++i) {
       tc::mbar_init(bar(&qfull[i]), 1);
@@ -498,18 +495,18 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(&lfull[i]), 32);
-      tc::mbar_init(bar(&lempty[i]), 256);
+      tc::mbar_init(bar(&lempty[i]), BEW);
     }
     tc::mbar_init(bar(&dfull), 32);
-    tc::mbar_init(bar(&dempty), 256);
+    tc::mbar_init(bar(&dempty), BEW);
     tc::mbar_init(bar(&kvfull), 1);
     tc::mbar_init(bar(&kvempty), 1);
     tc::mbar_init(bar(&sfull), 1);
-    tc::mbar_init(bar(&pfull), 256);
+    tc::mbar_init(bar(&pfull), BEW);
     tc::mbar_init(bar(&dpfull), 1);
-    tc::mbar_init(bar(&dsfull), 256);
+    tc::mbar_init(bar(&dsfull), BEW);
     tc::mbar_init(bar(&gfull), 1);
-    tc::mbar_init(bar(&gempty), 256);
+    tc::mbar_init(bar(&gempty), BEW);
     tc::mbar_init(bar(&drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -520,8 +517,8 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
   // tensor memory: S^T (then P^T), dP^T (then dS^T), dV, dK
   const uint32_t tS = tmem, tP = tmem + BT, tV = tmem + 2 * BT, tK = tmem + 3 * BT;
 
-  if (warp >= 8) {
-    if (warp == 8 && elect_one()) {
+  if (warp >= WI) {
+    if (warp == WI && elect_one()) {
       // ---------------- TMA ----------------
       int n = 0, nk = 0;
       bool bad = false;
@@ -557,7 +554,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         if (i >= n - NRING2) wait_or_flag(gm.err, bar(&ofull[i % NRING2]), (uint32_t)(i / NRING2) & 1u);
       }
       if (nk) wait_or_flag(gm.err, bar(&kvfull), (uint32_t)(nk - 1) & 1u);
-    } else if (warp == 10) {
+    } else if (warp == WI + 2) {
       // ---------------- log-sums and D of the steps' queries ----------------
       int n = 0;
       bool bad = false;
@@ -585,7 +582,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           arrive(bar(&dfull));
         }
       }
-    } else if (warp == 9 && elect_one()) {
+    } else if (warp == WI + 1 && elect_one()) {
       // ---------------- products ----------------
       int n = 0, nk = 0, ng = 0;
       bool bad = false;
@@ -640,12 +637,12 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           }
           tc::fence_after();
           const uint32_t id = idesc(BT, a.d, true);
-          mma_rows(tV, tS, Or + so * SH::TILE, s.w / 16, id, j > 0, 32);
+          mma_rows<BT, 32>(tV, tS, Or + so * SH::TILE, s.w / 16, id, j > 0);
           commit(&oempty[so]);
           if (j + 1 < r.steps && !scores(next, i + 1)) { bad = true; break; }
           if (!wait_or_flag(gm.err, bar(&dsfull), (uint32_t)i & 1u)) { bad = true; break; }
           tc::fence_after();
-          mma_rows(tK, tP, Qr + sq * SH::TILE, s.w / 16, id, j > 0, 32);
+          mma_rows<BT, 32>(tK, tP, Qr + sq * SH::TILE, s.w / 16, id, j > 0);
           commit(&qempty[sq]);
           if (j + 1 == r.steps) commit(&gfull);
           if (j + 1 < r.steps && !grads(next, i + 1)) { bad = true; break; }
@@ -659,7 +656,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
     }
   } else {
     // ---------------- elementwise: rows are keys, columns queries ----------------
-    const int half = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 64 * half;
+    const int grp = warp >> 2, row = 32 * (warp & 3) + lane, c0 = 32 * grp;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t S = tS + lanes, P = tP + lanes;
     const float c = a.scale_log2;
@@ -682,7 +679,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         const int ps = r.sq.qp + s.r0;            // position of the step's first query
         const bool whole = keys_ok && s.re - s.r0 == BT && ps >= all_lo && ps + BT <= all_hi;
         const int l = pl - ps - c0, h = min(ph - ps, s.re - s.r0) - c0;
-        const uint32_t bits[2] = {whole ? 0u : seen_bits(l, h, 0), whole ? 0u : seen_bits(l - 32, h - 32, 0)};
+        const uint32_t bits = whole ? 0u : seen_bits(l, h, 0);
         const float* L = &Ls[n & 1][c0];
         const float* D = &Ds[c0];
         const bool ok = wait_or_flag(gm.err, bar(&lfull[n & 1]), (uint32_t)(n >> 1) & 1u);
@@ -691,36 +688,29 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           break;
         }
         tc::fence_after();
-        uint32_t v[2][32];
-        ld32(S + c0, v[0]);
-        ld32(S + c0 + 32, v[1]);
-        ld_wait(v[0]);
-        ld_wait(v[1]);
+        uint32_t v[32], o[16];
+        ld32(S + c0, v);
+        ld_wait(v);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t o[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 ls = lds4(L + 32 * q + e);
-            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])),
-                                          c2, pack2(-ls.x, -ls.y)));
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3])),
-                                          c2, pack2(-ls.z, -ls.w)));
-            v[q][e] = __float_as_uint(exp2_ftz(x.x));
-            v[q][e + 1] = __float_as_uint(exp2_ftz(x.y));
-            v[q][e + 2] = __float_as_uint(exp2_ftz(y.x));
-            v[q][e + 3] = __float_as_uint(exp2_ftz(y.y));
-          }
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(bits[q] >> e & 1u)) v[q][e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            o[e >> 1] = pack(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
-          st16(S + c0 + 16 * q, o);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 ls = lds4(L + e);
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2,
+                                        pack2(-ls.x, -ls.y)));
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), c2,
+                                        pack2(-ls.z, -ls.w)));
+          v[e] = __float_as_uint(exp2_ftz(x.x));
+          v[e + 1] = __float_as_uint(exp2_ftz(x.y));
+          v[e + 2] = __float_as_uint(exp2_ftz(y.x));
+          v[e + 3] = __float_as_uint(exp2_ftz(y.y));
         }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits >> e & 1u)) v[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        st16(S + c0, o);
         st_wait();
         tc::fence_before();
         arrive(bar(&pfull));
@@ -732,34 +722,28 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
           break;
         }
         tc::fence_after();
-        uint32_t dp[2][32];
-        ld32(P + c0, dp[0]);
-        ld32(P + c0 + 32, dp[1]);
-        ld_wait(dp[0]);
-        ld_wait(dp[1]);
+        uint32_t dp[32];
+        ld32(P + c0, dp);
+        ld_wait(dp);
+        float x[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t o[16];
-          float x[32];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 ds = lds4(D + 32 * q + e);
-            const float2 y = unpack2(mul2(pack2(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])),
-                                          add2(pack2(__uint_as_float(dp[q][e]), __uint_as_float(dp[q][e + 1])),
-                                               pack2(-ds.x, -ds.y))));
-            const float2 w = unpack2(mul2(pack2(__uint_as_float(v[q][e + 2]), __uint_as_float(v[q][e + 3])),
-                                          add2(pack2(__uint_as_float(dp[q][e + 2]), __uint_as_float(dp[q][e + 3])),
-                                               pack2(-ds.z, -ds.w))));
-            x[e] = y.x; x[e + 1] = y.y; x[e + 2] = w.x; x[e + 3] = w.y;
-          }
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = bits[q] >> e & 1u ? x[e] : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(x[e], x[e + 1]);
-          st16(P + c0 + 16 * q, o);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 ds = lds4(D + e);
+          const float2 y = unpack2(mul2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                        add2(pack2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                             pack2(-ds.x, -ds.y))));
+          const float2 w = unpack2(mul2(pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                        add2(pack2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
+                                             pack2(-ds.z, -ds.w))));
+          x[e] = y.x; x[e + 1] = y.y; x[e + 2] = w.x; x[e + 3] = w.y;
         }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1u ? x[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(x[e], x[e + 1]);
+        st16(P + c0, o);
         st_wait();
         tc::fence_before();
         arrive(bar(&dsfull));
@@ -771,15 +755,16 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         ++ng;
         tc::fence_after();
       }
-      // dK by the first half of the threads, dV by the second
-      const uint32_t G = (half ? tV : tK) + lanes;
-      const float f = half ? 1.f : a.scale;
+      // dK by groups 0 and 1, dV by 2 and 3, pieces of 16 columns in turn
+      const int which = grp >> 1;
+      const uint32_t G = (which ? tV : tK) + lanes;
+      const float f = which ? 1.f : a.scale;
       const size_t krow = ((size_t)r.b * a.Hkv + r.hk) * a.Nk + j;
-      __nv_bfloat16* dst = (__nv_bfloat16*)(half ? a.dv : a.dk) + krow * a.d;
+      __nv_bfloat16* dst = (__nv_bfloat16*)(which ? a.dv : a.dk) + krow * a.d;
       float* part = a.part + (((((size_t)r.b * a.Hkv + r.hk) * a.stiles + r.tile) * a.chunks +
-                               (r.chunk >= 0 ? r.chunk : 0)) * 2 + half) * BT * a.d + (size_t)row * a.d;
+                               (r.chunk >= 0 ? r.chunk : 0)) * 2 + which) * BT * a.d + (size_t)row * a.d;
 #pragma unroll 1
-      for (int q = 0; q < a.d; q += 16) {
+      for (int q = 16 * (grp & 1); q < a.d; q += 32) {
         uint32_t o[16];
         if (r.steps > 0) {
           tc::tmem_ld<16>(G + q, o);
@@ -810,7 +795,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (warp == WI) tc::tmem_dealloc(tmem, 512);
 }
 
 namespace {

@@ -86,15 +86,15 @@ __device__ __forceinline__ void mma_features(uint32_t d_tmem, uint32_t A, uint32
       tc::mma_bf16(d_tmem, da + (((k >> 2) * AR * 128 + (k & 3) * 32) >> 4),
                    db + (((k >> 2) * BR * 128 + (k & 3) * 32) >> 4), id, k > 0);
 }
-// D (+)= A B over the `slices` 16-row slices of B, A in tensor memory; slices 4 to
-// 7 of A lie `skip` columns behind their place
-template <int BR = 128>
+// D (+)= A B over the `slices` 16-row slices of B, A in tensor memory: two slices
+// (16 columns) every PAIR columns
+template <int BR = 128, int PAIR = 16>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t A, uint32_t B, int slices,
-                                         uint32_t id, bool acc, uint32_t skip = 0) {
+                                         uint32_t id, bool acc) {
   const uint64_t db = desc_mn(B, BR * 128);
 #pragma unroll
   for (int k = 0; k < BR / 16; ++k)
-    if (k < slices) mma_ts(d_tmem, A + 8 * k + (k < 4 ? 0 : skip), db + 128 * k, id, acc || k > 0);
+    if (k < slices) mma_ts(d_tmem, A + PAIR * (k >> 1) + 8 * (k & 1), db + 128 * k, id, acc || k > 0);
 }
 
 // rows [r0, w) of an NP-panel tile to zero, by the thread that issues the products
