@@ -7,6 +7,7 @@ right is no bound.  Marshalling only: every step runs in liblapnys kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 import math
 from typing import NamedTuple, Optional
@@ -69,6 +70,9 @@ def _batch(t, name, B, device):
         _tensor(t, name, (B,), torch.int32, device)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -77,21 +81,9 @@ def _on_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-class _on:
+def _on(device):
     """The tensors' device as the current one."""
-
-    def __init__(self, device):
-        self.device, self.was = device, None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device.index != now:
-            self.was = now
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.was is not None:
-            torch.cuda.set_device(self.was)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _workspace(ws, need, device):
@@ -103,7 +95,7 @@ def _workspace(ws, need, device):
 
 
 def _nbytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    return 0 if ws is None else ws.nbytes
 
 
 def _check_window(q, k, v, lens, q_pos, p: WindowParams):
@@ -126,18 +118,22 @@ def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=No
     """lapnys_window_fwd: returns (out, lse); lse is None when need_lse is False."""
     _check_window(q, k, v, lens, q_pos, p)
     dev = q.device
+    if out is not None:
+        _tensor(out, "out", q.shape, q.dtype, dev)
+    if lse is not None:
+        _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
     with _on(dev):
         out = torch.empty_like(q) if out is None else out
-        _tensor(out, "out", q.shape, q.dtype, dev)
-        if need_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if lse is None else lse
-            _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
+        if not need_lse:
+            lse = None
+        elif lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype), dev)
         rc = load().lapnys_window_fwd(
-            _at(q), _at(k), _at(v), _at(out), _at(lse) if need_lse else None, _at(lens),
-            _at(q_pos), *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(lens), _at(q_pos),
+            *p, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_fwd")
-    return out, (lse if need_lse else None)
+    return out, lse
 
 
 def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, dq=None, dk=None,
@@ -146,19 +142,25 @@ def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, 
     _check_window(q, k, v, lens, q_pos, p)
     dev = q.device
     _tensor(out, "out", q.shape, q.dtype, dev)
-    _tensor(dout, "dout", q.shape, q.dtype, dev)
     _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        if t is not None:
+            _tensor(t, name, like.shape, q.dtype, dev)
+    return _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws)
+
+
+def _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws):
+    dev = q.device
+    _tensor(dout, "dout", q.shape, q.dtype, dev)
     with _on(dev):
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
-        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-            _tensor(t, name, like.shape, q.dtype, dev)
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype, True), dev)
         rc = load().lapnys_window_bwd(
-            _at(q), _at(k), _at(v), _at(out), _at(dout), _at(lse), _at(lens), _at(q_pos),
-            _at(dq), _at(dk), _at(dv), *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws),
-            _nbytes(ws))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+            _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p, _on_stream(dev),
+            _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_bwd")
     return dq, dk, dv
 
@@ -173,9 +175,9 @@ class _Window(torch.autograd.Function):
 
     @staticmethod
     def backward(fctx, dout):
-        q, k, v, out, lse, lens, q_pos = fctx.saved_tensors
-        dq, dk, dv = window_bwd(q, k, v, out, dout.contiguous(), lse, fctx.p, lens, q_pos)
-        return dq, dk, dv, None, None, None
+        q, k, v, out, lse, lens, q_pos = fctx.saved_tensors   # checked by the forward
+        return *_bwd(q, k, v, out, dout.contiguous(), lse, fctx.p, lens, q_pos, None, None, None,
+                     None), None, None, None
 
 
 def window_attention(q, k, v, left, right=0, sinks=0, scale=None, lens=None, q_pos=None):
