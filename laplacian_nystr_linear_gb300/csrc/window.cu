@@ -80,14 +80,14 @@ WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
     }
   } else {
     w.D = o; o = align256(o + (size_t)a.B * a.Hq * a.Nq * 4);
-    // Key tiles with first tokens that far more queries see than an ordinary tile's
-    // (four times as many: below that a launch for the partials costs more than the
-    // longer tile, 7 us of 40 for 1001 tokens): their queries in ranges as long as an
-    // ordinary tile's, or longer where enough blocks run anyway (four for each of
-    // 152 SMs), which bounds the partials.
+    // Key tiles with first tokens that more queries see than an ordinary tile's (twice
+    // as many; below that the partials' launch is not worth it): their queries in
+    // ranges as long as an ordinary tile's, or longer where enough blocks run anyway
+    // (four for each of 152 SMs), which bounds the partials.  As one item, the first
+    // tile of 8192 tokens with a window of 2048 runs for 600 us beside 226.
     const int S = a.sinks < a.Nk ? a.sinks : a.Nk;
     const long long reach = (long long)a.left + a.right + tile;
-    if (S > 0 && 4 * reach < a.Nq) {
+    if (S > 0 && 2 * reach < a.Nq) {
       w.stiles = (S + tile - 1) / tile;
       long long n = (a.Nq + reach - 1) / reach;
       const long long most = 608 / ((long long)a.B * a.Hkv * w.stiles) + 1;
