@@ -286,19 +286,23 @@ int lapnys_block_bwd(const void* x, const void* w_qkv, const void* w_o, const vo
  *    results: what one query does not see may still meet it as 0 * value.
  *  - lse [B][Hq][Nq] float: log2 of the sum of exp(s); may be NULL in the
  *    forward; the backward reads the forward's.
+ *  - rest (bf16 only; may be NULL): like out, what the rounding of out left, rounded
+ *    itself.  The backward takes D = dout.o from out + rest; without it D carries
+ *    out's rounding, which counts where a query sees few keys (dq off by 4e-3 of its
+ *    norm at two keys, with it by 2e-3).
  *  - fp32 arithmetic; bf16 tensors: products of bf16 operands with fp32 sums,
- *    P and dS rounded to bf16 between products, outputs rounded once.
+ *    P and (for dk) dS rounded to bf16 between products, outputs rounded once.
  *  - Deterministic.  One workspace per call in flight, of
  *    lapnys_window_workspace_bytes (may be 0: ws NULL); 0 also for invalid
  *    arguments. */
 size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int left,
                                      int right, int sinks, int dtype, int backward);
 int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
-                      const int32_t* lens, const int32_t* q_pos, int B, int Hq, int Hkv, int Nq,
-                      int Nk, int d, int left, int right, int sinks, float scale,
+                      void* rest, const int32_t* lens, const int32_t* q_pos, int B, int Hq,
+                      int Hkv, int Nq, int Nk, int d, int left, int right, int sinks, float scale,
                       cudaStream_t stream, int dtype, void* ws, size_t ws_bytes);
 int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
-                      const void* dout, const float* lse, const int32_t* lens,
+                      const void* dout, const float* lse, const void* rest, const int32_t* lens,
                       const int32_t* q_pos, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
                       int Nq, int Nk, int d, int left, int right, int sinks, float scale,
                       cudaStream_t stream, int dtype, void* ws, size_t ws_bytes);

@@ -94,9 +94,9 @@ def load() -> ctypes.CDLL:
     lib.lapnys_profile_read.restype = I
     lib.lapnys_window_workspace_bytes.argtypes = [I] * 11
     lib.lapnys_window_workspace_bytes.restype = S
-    lib.lapnys_window_fwd.argtypes = [P] * 7 + [I] * 9 + [F, P, I, P, S]
+    lib.lapnys_window_fwd.argtypes = [P] * 8 + [I] * 9 + [F, P, I, P, S]
     lib.lapnys_window_fwd.restype = I
-    lib.lapnys_window_bwd.argtypes = [P] * 11 + [I] * 9 + [F, P, I, P, S]
+    lib.lapnys_window_bwd.argtypes = [P] * 12 + [I] * 9 + [F, P, I, P, S]
     lib.lapnys_window_bwd.restype = I
     lib.lapnys_cache_append.argtypes = [P] * 9 + [I] * 7 + [P, I]
     lib.lapnys_cache_append.restype = I

@@ -723,8 +723,13 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
     acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
   }
   const float w = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  if (c < a.d)
-    st4((TQ*)a.out + qrow * a.d + c, make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w));
+  if (c < a.d) {
+    const float4 y = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
+    st4((TQ*)a.out + qrow * a.d + c, y);
+    if (a.rest)
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)a.rest + qrow * a.d + c) =
+          make_uint2(wtc::pack_rest(y.x, y.y, wtc::pack(y.x, y.y)), wtc::pack_rest(y.z, y.w, wtc::pack(y.z, y.w)));
+  }
   if (a.lse && lane == 0) a.lse[qrow] = sum == 0.f ? -INFINITY : mx + log2f(sum) - shift;
 }
 

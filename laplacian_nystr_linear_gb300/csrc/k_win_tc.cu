@@ -435,7 +435,9 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
         }
         tc::fence_after();
       }
-      __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (((size_t)r.b * a.Hq + head) * a.Nq + i) * a.d;
+      const size_t at = (((size_t)r.b * a.Hq + head) * a.Nq + i) * a.d;
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.out + at;
+      __nv_bfloat16* rest = a.rest ? (__nv_bfloat16*)a.rest + at : nullptr;
 #pragma unroll 1
       for (int q = 0; q < a.d; q += 16) {
         uint32_t o[16];
@@ -451,8 +453,7 @@ __global__ void __launch_bounds__(FTH, 1) k_win_fwd_tc(const __grid_constant__ F
           float f[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(o[e + x]) * w;
-          *reinterpret_cast<uint4*>(dst + q + e) =
-              make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+          store8(dst + q + e, rest ? rest + q + e : nullptr, f);
         }
       }
       if (any) {

@@ -5,7 +5,7 @@
 // atomics): scores are computed in both, 7 products of 128 x 128 x d per tile of
 // pairs instead of 5.
 //   k_win_dq_tc   128 queries stay, keys in steps of 128:
-//                 S = Q K^T, dP = dO V^T, dS = P (dP - D) as bf16, dQ += dS K
+//                 S = Q K^T, dP = dO V^T, dS = P (dP - D) as two bf16, dQ += dS K
 //   k_win_dkv_tc  128 keys stay, the queries of the group's heads in steps of
 //                 128: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 // with P = exp2(scale log2(e) s - lse) from the forward's log-sum.  The bf16
@@ -14,7 +14,7 @@
 // shared memory both K-major (scores) and MN-major (gradients).
 //
 //   warps 0-15  elementwise work, one row and a quarter of the columns per thread.
-//               Each group of columns writes its bf16 values (16 columns) over its
+//               Each group of columns writes its bf16 values (16 or 32 columns) over its
 //               own 32 columns, so the groups need no barrier and drift apart: one's
 //               exponentials run under the others' multiplications, and four warps
 //               a scheduler hide the latencies of tensor memory (two of half the
@@ -82,12 +82,15 @@ struct Step {
   int r0, re, w;        // rows [r0, re) and the width of the products
 };
 
-// dS = P (dP - D) of 32 columns to tensor memory; not whole: only where `bits`
-// are set (a select, not a product: what is not seen may be anything)
+// dS = P (dP - D) of 32 columns to tensor memory, as 16 columns of bf16 pairs and
+// 16 of what their rounding leaves (dS sums to 0 over a row, so what the keys have
+// in common cancels in dS K, but not in the roundings: with one bf16 dS, dQ is off
+// by 2.9e-3 of its norm for keys of a common part half their spread, with two by
+// 1.8e-3, of which the output's rounding is 1.7e-3).  Not whole: only where `bits`
+// are set (a select, not a product: what is not seen may be anything).
 __device__ __forceinline__ void ds_store(uint32_t dst, const uint32_t (&p)[32],
                                          const uint32_t (&dp)[32], f32x2 minus_D, bool whole,
                                          uint32_t bits) {
-  uint32_t o[16];
   float x[32];
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
@@ -100,9 +103,13 @@ __device__ __forceinline__ void ds_store(uint32_t dst, const uint32_t (&p)[32],
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1u ? x[e] : 0.f;
   }
+  uint32_t o[32];
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) o[e >> 1] = pack(x[e], x[e + 1]);
-  st16(dst, o);
+  for (int e = 0; e < 32; e += 2) {
+    o[e >> 1] = pack(x[e], x[e + 1]);
+    o[16 + (e >> 1)] = pack_rest(x[e], x[e + 1], o[e >> 1]);
+  }
+  st32(dst, o);
 }
 }  // namespace
 
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
           }
           tc::fence_after();
           mma_rows<BT, 32>(tO, tS + (i & 1) * BT, Kr + sk * SH::TILE, s.w / 16, id_q, i > n0);
+          mma_rows<BT, 32>(tO, tS + (i & 1) * BT + 16, Kr + sk * SH::TILE, s.w / 16, id_q, true);
           commit(&kempty[sk]);
           if (i + 1 == n) commit(&ofull);
           if (i + 2 < n && !scores(s2, i + 2)) { bad = true; break; }
@@ -314,7 +322,7 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       const int i = r.i0 + row;
       const size_t qrow = ((size_t)r.b * a.Hq + r.h) * a.Nq + i;
       const WinRow wr = win_row(a, r.sq, i);
-      // D = dout.out, half of the features by either of the first groups
+      // D = dout.(out + rest), half of the features by either of the first groups
       float D = 0.f, lse = 0.f;
       if (r.steps > 0) {
         if (i < r.i1) lse = a.lse[qrow];
@@ -322,17 +330,24 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
           const int hd = a.d / 2;
           const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + grp * hd;
           const __nv_bfloat16* y = (const __nv_bfloat16*)a.out + qrow * a.d + grp * hd;
+          const __nv_bfloat16* z = a.rest ? (const __nv_bfloat16*)a.rest + qrow * a.d + grp * hd : nullptr;
+          float rest = 0.f;
+          const auto dot = [](uint4 u, uint4 w, float sum) {
+            const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              sum = fmaf(__uint_as_float(us[c] << 16), __uint_as_float(ws[c] << 16), sum);
+              sum = fmaf(__uint_as_float(us[c] & 0xffff0000u), __uint_as_float(ws[c] & 0xffff0000u), sum);
+            }
+            return sum;
+          };
 #pragma unroll 4
           for (int e = 0; e < hd; e += 8) {
             const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + e));
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(y + e));
-            const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              D = fmaf(__uint_as_float(us[z] << 16), __uint_as_float(ws[z] << 16), D);
-              D = fmaf(__uint_as_float(us[z] & 0xffff0000u), __uint_as_float(ws[z] & 0xffff0000u), D);
-            }
+            D = dot(u, __ldg(reinterpret_cast<const uint4*>(y + e)), D);
+            if (z) rest = dot(u, __ldg(reinterpret_cast<const uint4*>(z + e)), rest);
           }
+          D += rest;
         }
         // (written again for the next item only behind `ofull`, for which the other
         // groups have worked through this one's steps)

@@ -23,6 +23,7 @@ struct WinArgs {
   const void* k;      // [B][Hkv][Nk][d]
   const void* v;
   void* out;          // [B][Hq][Nq][d]
+  void* rest;         // like out, bf16 only, or null: what rounding left of out, rounded
   float* lse;         // [B][Hq][Nq]: log2 of the sum of exp over the visible keys; -inf: none
   const int32_t* lens;   // [B] or null (Nk)
   const int32_t* q_pos;  // [B] or null (Nk - Nq)

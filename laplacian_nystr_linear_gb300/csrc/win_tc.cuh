@@ -172,6 +172,22 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// a pair's rounding, and the rounding of what it leaves
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t h) {
+  return pack(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+}
+// eight values of an output row, and what their rounding leaves when `rest` is set
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, __nv_bfloat16* rest, const float (&f)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = pack(f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (rest)
+    *reinterpret_cast<uint4*>(rest) =
+        make_uint4(pack_rest(f[0], f[1], h[0]), pack_rest(f[2], f[3], h[1]),
+                   pack_rest(f[4], f[5], h[2]), pack_rest(f[6], f[7], h[3]));
+}
+
 // columns [0, 32) of a tile's 32-column piece that a row sees, as bits: columns
 // [l, h) and [0, min(z, h)), all relative to the piece
 __device__ __forceinline__ uint32_t bits_below(int n) {

@@ -153,8 +153,8 @@ size_t lapnys_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int
 }
 
 int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
-                      const int32_t* lens, const int32_t* q_pos, int B, int Hq, int Hkv, int Nq,
-                      int Nk, int d, int left, int right, int sinks, float scale,
+                      void* rest, const int32_t* lens, const int32_t* q_pos, int B, int Hq,
+                      int Hkv, int Nq, int Nk, int d, int left, int right, int sinks, float scale,
                       cudaStream_t stream, int dtype, void* ws, size_t ws_bytes) {
   NvtxScope nvtx_scope("lapnys_window_fwd");
   TokenArgs t;
@@ -163,12 +163,14 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   const int rc = check_window(a, B, Hq, Hkv, Nq, Nk, d, left, right, sinks, scale, dtype);
   if (rc != LAPNYS_OK) return rc;
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
-      !aligned(out, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
+      !aligned(out, 16) || !aligned(rest, 16) || !aligned(lse, 4) || !aligned(lens, 4) ||
+      !aligned(q_pos, 4))
     return LAPNYS_EINVAL;
   const WinWs w = window_ws(a, false, dtype);
   if (w.total > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
+  a.rest = dtype == LAPNYS_BF16 ? rest : nullptr;
   if (few(a.g, Nq)) {
     token_parts(t, w.tok, ws);
     t.err = wait_error_address();
@@ -180,7 +182,7 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
 }
 
 int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* out,
-                      const void* dout, const float* lse, const int32_t* lens,
+                      const void* dout, const float* lse, const void* rest, const int32_t* lens,
                       const int32_t* q_pos, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
                       int Nq, int Nk, int d, int left, int right, int sinks, float scale,
                       cudaStream_t stream, int dtype, void* ws, size_t ws_bytes) {
@@ -192,11 +194,13 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
   const void* all[] = {q, k, v, out, dout, dq, dk, dv, ws};
   for (const void* p : all)
     if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
-  if (!lse || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4)) return LAPNYS_EINVAL;
+  if (!lse || !aligned(rest, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
+    return LAPNYS_EINVAL;
   const WinWs w = window_ws(a, true, dtype);
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = const_cast<void*>(out); a.dout = dout;
   a.lse = const_cast<float*>(lse); a.lens = lens; a.q_pos = q_pos;
+  a.rest = dtype == LAPNYS_BF16 ? const_cast<void*>(rest) : nullptr;
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.D = (float*)((uint8_t*)ws + w.D);
   a.part = (float*)((uint8_t*)ws + w.part);

@@ -114,14 +114,17 @@ def window_workspace_bytes(p: WindowParams, dtype: torch.dtype, backward: bool =
 
 
 def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=None, ws=None,
-               need_lse=True):
-    """lapnys_window_fwd: returns (out, lse); lse is None when need_lse is False."""
+               need_lse=True, rest=None):
+    """lapnys_window_fwd: returns (out, lse); lse is None when need_lse is False.  rest (bf16, like
+    out): filled with what the rounding of out left, for window_bwd."""
     _check_window(q, k, v, lens, q_pos, p)
     dev = q.device
     if out is not None:
         _tensor(out, "out", q.shape, q.dtype, dev)
     if lse is not None:
         _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
+    if rest is not None:
+        _tensor(rest, "rest", q.shape, q.dtype, dev)
     with _on(dev):
         out = torch.empty_like(q) if out is None else out
         if not need_lse:
@@ -130,15 +133,15 @@ def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=No
             lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype), dev)
         rc = load().lapnys_window_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(lens), _at(q_pos),
-            *p, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(rest), _at(lens),
+            _at(q_pos), *p, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_fwd")
     return out, lse
 
 
 def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, dq=None, dk=None,
-               dv=None, ws=None):
-    """lapnys_window_bwd: returns (dq, dk, dv)."""
+               dv=None, ws=None, rest=None):
+    """lapnys_window_bwd: returns (dq, dk, dv); rest: the forward's, if it kept one."""
     _check_window(q, k, v, lens, q_pos, p)
     dev = q.device
     _tensor(out, "out", q.shape, q.dtype, dev)
@@ -146,10 +149,12 @@ def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, 
     for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
         if t is not None:
             _tensor(t, name, like.shape, q.dtype, dev)
-    return _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws)
+    if rest is not None:
+        _tensor(rest, "rest", q.shape, q.dtype, dev)
+    return _bwd(q, k, v, out, dout, lse, rest, p, lens, q_pos, dq, dk, dv, ws)
 
 
-def _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws):
+def _bwd(q, k, v, out, dout, lse, rest, p, lens, q_pos, dq, dk, dv, ws):
     dev = q.device
     _tensor(dout, "dout", q.shape, q.dtype, dev)
     with _on(dev):
@@ -159,7 +164,7 @@ def _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws):
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype, True), dev)
         rc = load().lapnys_window_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
-            _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p, _on_stream(dev),
+            _at(rest), _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p, _on_stream(dev),
             _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_bwd")
     return dq, dk, dv
@@ -168,16 +173,17 @@ def _bwd(q, k, v, out, dout, lse, p, lens, q_pos, dq, dk, dv, ws):
 class _Window(torch.autograd.Function):
     @staticmethod
     def forward(fctx, q, k, v, lens, q_pos, p: WindowParams):
-        out, lse = window_fwd(q, k, v, p, lens, q_pos)
+        rest = torch.empty_like(q) if q.dtype == torch.bfloat16 else None
+        out, lse = window_fwd(q, k, v, p, lens, q_pos, rest=rest)
         fctx.p = p
-        fctx.save_for_backward(q, k, v, out, lse, lens, q_pos)
+        fctx.save_for_backward(q, k, v, out, lse, rest, lens, q_pos)
         return out
 
     @staticmethod
     def backward(fctx, dout):
-        q, k, v, out, lse, lens, q_pos = fctx.saved_tensors   # checked by the forward
-        return *_bwd(q, k, v, out, dout.contiguous(), lse, fctx.p, lens, q_pos, None, None, None,
-                     None), None, None, None
+        q, k, v, out, lse, rest, lens, q_pos = fctx.saved_tensors   # checked by the forward
+        return *_bwd(q, k, v, out, dout.contiguous(), lse, rest, fctx.p, lens, q_pos, None, None,
+                     None, None), None, None, None
 
 
 def window_attention(q, k, v, left, right=0, sinks=0, scale=None, lens=None, q_pos=None):

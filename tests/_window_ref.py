@@ -9,6 +9,8 @@ bf16 backward  dv: P and the result rounded once:            u |dv| + u P^T|do|
                dq, dk: dS and the result rounded once; D = do.o uses the rounded output, which is
                off by do_i = u (|o| + P|v|), so dS is off by P D_off with D_off = |do|.o_off:
                u |dq| + scale (u |dS| + P D_off) |K|, and the same transposed for dk.
+with rest      the backward reads out + rest, off by u^2 |o| + u P|v| only, and dq takes dS in two
+               parts (u^2); dk as before.
 fp32 sums      a score is off by at most (d + 4) 2^-24 scale |q|.|k| =: E (twice in P, twice more
                through the log-sum), a sum of n terms by (n + 16) 2^-24 of its terms' magnitudes.
 """
@@ -32,9 +34,10 @@ def visible(Nq, Nk, left, right, sinks, lens, q_pos, device):
 
 
 def reference(q, k, v, left, right, sinks, scale=None, lens=None, q_pos=None, dout=None,
-              extra_p=0.0, extra_s=0.0):
+              extra_p=0.0, extra_s=0.0, rest=False):
     """{name: (64-bit value, allowed error)} of out, lse and, with dout, dq, dk, dv.
-    extra_p, extra_s: further relative error of P and of the scores' magnitudes |q|.|k|."""
+    extra_p, extra_s: further relative error of P and of the scores' magnitudes |q|.|k|.
+    rest: the gradients' errors with the forward's rest, and ref["both"] for out + rest."""
     dt, dev = q.dtype, q.device
     B, Hq, Nq, d = q.shape
     Hkv, Nk = k.shape[1:3]
@@ -68,6 +71,9 @@ def reference(q, k, v, left, right, sinks, scale=None, lens=None, q_pos=None, do
     lse = torch.where(t > 0, mx + torch.log(t), -math.inf)[..., 0] / math.log(2)
     lse_off = torch.where(lse.isinf(), 0.0, 1.5 * pr[..., 0] + 4 * f * lse.abs() + 1e-30)
     got = {"out": (o, 1.01 * o_off + 1e-30), "lse": (lse, lse_off)}
+    if rest:
+        o_off = u * u * o.abs() + (up + pr) * Pv
+        got["both"] = (o, 1.01 * o_off + 1e-30)
     if dout is None:
         return got
     dO = torch.where(rows, dout.double(), 0.0)
@@ -77,13 +83,14 @@ def reference(q, k, v, left, right, sinks, scale=None, lens=None, q_pos=None, do
     back = (d + 16) * f
     dPm = dO.abs() @ V.abs().transpose(-1, -2)             # magnitudes of the sums in dP
     D_off = (dO.abs() * o_off).sum(-1, keepdim=True) + back * (dO.abs() * o.abs()).sum(-1, keepdim=True)
-    dS_off = up * dS.abs() + P * (D_off + back * dPm) + 2 * pr * P * (dP.abs() + D.abs())
+    dS_off = P * (D_off + back * dPm) + 2 * pr * P * (dP.abs() + D.abs())
+    up_q = up * up if rest else up
     tr = lambda x: x.transpose(-1, -2)  # noqa: E731
     kv = lambda x: x.reshape(B, Hkv, g, Nk, d).sum(2)      # noqa: E731
     n2 = (Nq * g + 16) * f
     dq, dk, dv = dS @ K * scale, kv(tr(dS) @ Q) * scale, kv(tr(P) @ dO)
-    dS_n = dS_off + (n + 16) * f * dS.abs()
-    dS_g = dS_off + n2 * dS.abs()
+    dS_n = dS_off + (up_q + (n + 16) * f) * dS.abs()
+    dS_g = dS_off + (up + n2) * dS.abs()
     dq_off = u * dq.abs() + scale * (dS_n @ K.abs())
     dk_off = u * dk.abs() + scale * kv(tr(dS_g) @ Q.abs())
     dv_off = u * dv.abs() + kv(tr(P * (up + 2 * pr + n2)) @ dO.abs())

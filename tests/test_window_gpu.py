@@ -81,6 +81,23 @@ def test_forward_and_backward(name, dtype):
         check(name_, x, ref[name_])
 
 
+@pytest.mark.parametrize("name", list(CASES))
+def test_rest_of_the_output(name):
+    """out + rest is the output before its rounding, and the gradients are the nearer for it."""
+    B, Hq, Hkv, Nq, Nk, d, left, right, sinks, lens, q_pos = CASES[name]
+    q, k, v, do = make(B, Hq, Hkv, Nq, Nk, d, BF)
+    lens, q_pos = ints(lens), ints(q_pos)
+    ref = reference(q, k, v, left, right, sinks, None, lens, q_pos, do, rest=True)
+    p = lap.WindowParams.of(q, k, left, right, sinks)
+    rest = torch.full_like(q, float("nan"))
+    out, lse = lap.window_fwd(q, k, v, p, lens, q_pos, rest=rest)
+    assert torch.equal(out, lap.window_fwd(q, k, v, p, lens, q_pos)[0])
+    check("both", out.double() + rest.double(), ref["both"])
+    for name_, x in zip(("dq", "dk", "dv"),
+                        lap.window_bwd(q, k, v, out, do, lse, p, lens, q_pos, rest=rest)):
+        check(name_, x, ref[name_])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_autograd_agrees_with_differences(dtype):
     """<grad, step> against the 64-bit loss's central difference along the same step.  The truncation

@@ -23,19 +23,19 @@ DIMS = dict(B=2, Hq=4, Hkv=2, Nq=100, Nk=100, d=64, left=10, right=0, sinks=1)
 
 
 def _fwd(lib, **kw):
-    a = dict(DIMS, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=FAKE, lens=None, q_pos=None, scale=0.1, dtype=1,
-             ws=None, ws_bytes=0)
+    a = dict(DIMS, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=FAKE, rest=None, lens=None, q_pos=None, scale=0.1,
+             dtype=1, ws=None, ws_bytes=0)
     a.update(kw)
-    return lib.lapnys_window_fwd(a["q"], a["k"], a["v"], a["out"], a["lse"], a["lens"], a["q_pos"],
-                                 *(a[n] for n in DIMS), a["scale"], None, a["dtype"], a["ws"],
+    return lib.lapnys_window_fwd(a["q"], a["k"], a["v"], a["out"], a["lse"], a["rest"], a["lens"],
+                                 a["q_pos"], *(a[n] for n in DIMS), a["scale"], None, a["dtype"], a["ws"],
                                  a["ws_bytes"])
 
 
 def _bwd(lib, **kw):
-    a = dict(DIMS, q=FAKE, k=FAKE, v=FAKE, out=FAKE, dout=FAKE, lse=FAKE, lens=None, q_pos=None, dq=FAKE,
+    a = dict(DIMS, q=FAKE, k=FAKE, v=FAKE, out=FAKE, dout=FAKE, lse=FAKE, rest=None, lens=None, q_pos=None, dq=FAKE,
              dk=FAKE, dv=FAKE, scale=0.1, dtype=1, ws=FAKE, ws_bytes=0)
     a.update(kw)
-    return lib.lapnys_window_bwd(a["q"], a["k"], a["v"], a["out"], a["dout"], a["lse"], a["lens"],
+    return lib.lapnys_window_bwd(a["q"], a["k"], a["v"], a["out"], a["dout"], a["lse"], a["rest"], a["lens"],
                                  a["q_pos"], a["dq"], a["dk"], a["dv"], *(a[n] for n in DIMS), a["scale"],
                                  None, a["dtype"], a["ws"], a["ws_bytes"])
 
@@ -43,7 +43,7 @@ def _bwd(lib, **kw):
 BAD = [dict(B=0), dict(Hq=0), dict(Hq=3), dict(Hkv=-1), dict(Nq=0), dict(Nk=0), dict(Nk=(1 << 28) + 1),
        dict(left=-2), dict(right=-2), dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan")),
        dict(scale=float("inf")), dict(scale=-1.0), dict(dtype=2), dict(q=None), dict(k=ODD), dict(v=None),
-       dict(out=ODD), dict(lse=ODD2), dict(lens=ODD2), dict(q_pos=ODD2), dict(B=1 << 20, Hq=1 << 10)]
+       dict(out=ODD), dict(lse=ODD2), dict(rest=ODD), dict(lens=ODD2), dict(q_pos=ODD2), dict(B=1 << 20, Hq=1 << 10)]
 
 
 @pytest.mark.parametrize("bad", BAD, ids=str)
