@@ -172,9 +172,13 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// a pair's rounding, and the rounding of what it leaves
+// what the rounding of a pair (h = pack(a, b)) leaves, rounded itself
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t h) {
-  return pack(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+  float x, y;
+  asm("{\n\t.reg .b16 l, u, one;\n\tmov.b32 {l, u}, %4;\n\tmov.b16 one, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, l, one, %2;\n\tfma.rn.f32.bf16 %1, u, one, %3;\n\t}"
+      : "=f"(x), "=f"(y) : "f"(a), "f"(b), "r"(h));
+  return pack(x, y);
 }
 // eight values of an output row, and what their rounding leaves when `rest` is set
 __device__ __forceinline__ void store8(__nv_bfloat16* dst, __nv_bfloat16* rest, const float (&f)[8]) {
