@@ -154,11 +154,11 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t kfull[NRING1], kempty[NRING1], vfull[NRING2], vempty[NRING2];
   __shared__ __align__(8) uint64_t qfull, qempty;       // Q and dO landed; their products done
-  __shared__ __align__(8) uint64_t sfull[2], dpfull, ofull, oempty, drain[2];
-  __shared__ __align__(8) uint64_t dsfull[2];           // (by parity: two threads wait for it)
-  __shared__ __align__(8) uint64_t dhfull;              // both halves of D written
+  __shared__ __align__(8) uint64_t sfull[2], dpfull, dpempty, ofull, oempty, drain[2];
+  __shared__ __align__(8) uint64_t dsfull[2];           // (by parity: a step can run ahead)
+  __shared__ __align__(8) uint64_t dhfull;              // D written
   __shared__ uint32_t tmem_s;
-  __shared__ float Dh[2][BT];
+  __shared__ float Ds[BT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = tc::smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t Qb = base, Ob = Qb + SH::TILE, Kr = Ob + SH::TILE, Vr = Kr + NRING1 * SH::TILE;
@@ -177,12 +177,13 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
     tc::mbar_init(bar(&qempty), 2);
     tc::mbar_init(bar(&sfull[0]), 1);
     tc::mbar_init(bar(&sfull[1]), 1);
-    tc::mbar_init(bar(&dhfull), BEW);
+    tc::mbar_init(bar(&dhfull), WI);
     tc::mbar_init(bar(&dpfull), 1);
-    tc::mbar_init(bar(&dsfull[0]), BEW);
-    tc::mbar_init(bar(&dsfull[1]), BEW);
+    tc::mbar_init(bar(&dpempty), WI);
+    tc::mbar_init(bar(&dsfull[0]), WI);
+    tc::mbar_init(bar(&dsfull[1]), WI);
     tc::mbar_init(bar(&ofull), 1);
-    tc::mbar_init(bar(&oempty), BEW);
+    tc::mbar_init(bar(&oempty), WI);
     tc::mbar_init(bar(&drain[0]), 1);
     tc::mbar_init(bar(&drain[1]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -292,9 +293,9 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
 #pragma unroll 1
         for (int j = 0; j < r.steps; ++j, ++n) {
           const int sv = n % NRING2, w = dq_step(r, j).w;
-          // (the step before has been read)
+          // (the step before is in registers)
           if (!wait_or_flag(gm.err, bar(&vfull[sv]), (uint32_t)(n / NRING2) & 1u) ||
-              (n > 0 && !wait_or_flag(gm.err, bar(&dsfull[(n - 1) & 1]), (uint32_t)((n - 1) >> 1) & 1u))) {
+              !wait_or_flag(gm.err, bar(&dpempty), ((uint32_t)n & 1u) ^ 1u)) {
             bad = true;
             break;
           }
@@ -322,39 +323,51 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
       const int i = r.i0 + row;
       const size_t qrow = ((size_t)r.b * a.Hq + r.h) * a.Nq + i;
       const WinRow wr = win_row(a, r.sq, i);
-      // D = dout.(out + rest), half of the features by either of the first groups
+      // D = dout.(out + rest): 8 rows of a warp, 8 lanes a row
       float D = 0.f, lse = 0.f;
       if (r.steps > 0) {
         if (i < r.i1) lse = a.lse[qrow];
-        if (i < r.i1 && grp < 2) {
-          const int hd = a.d / 2;
-          const __nv_bfloat16* x = (const __nv_bfloat16*)a.dout + qrow * a.d + grp * hd;
-          const __nv_bfloat16* y = (const __nv_bfloat16*)a.out + qrow * a.d + grp * hd;
-          const __nv_bfloat16* z = a.rest ? (const __nv_bfloat16*)a.rest + qrow * a.d + grp * hd : nullptr;
-          float rest = 0.f;
-          const auto dot = [](uint4 u, uint4 w, float sum) {
-            const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+        const int row8 = 8 * warp + (lane >> 3);
+        const size_t at = (((size_t)r.b * a.Hq + r.h) * a.Nq + r.i0 + row8) * a.d + 8 * (lane & 7);
+        uint4 x[2 * NP], y[2 * NP], z[2 * NP];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              sum = fmaf(__uint_as_float(us[c] << 16), __uint_as_float(ws[c] << 16), sum);
-              sum = fmaf(__uint_as_float(us[c] & 0xffff0000u), __uint_as_float(ws[c] & 0xffff0000u), sum);
-            }
-            return sum;
-          };
-#pragma unroll 4
-          for (int e = 0; e < hd; e += 8) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + e));
-            D = dot(u, __ldg(reinterpret_cast<const uint4*>(y + e)), D);
-            if (z) rest = dot(u, __ldg(reinterpret_cast<const uint4*>(z + e)), rest);
+        for (int e = 0; e < 2 * NP; ++e) {
+          const int t = 4 * (e & 1), f = 64 * (e >> 1);      // rows and features further on
+          x[e] = y[e] = z[e] = make_uint4(0, 0, 0, 0);
+          if (r.i0 + row8 + t < r.i1 && f + 8 * (lane & 7) < a.d) {
+            const size_t p = at + (size_t)t * a.d + f;
+            x[e] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.dout + p));
+            y[e] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.out + p));
+            if (a.rest) z[e] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.rest + p));
           }
-          D += rest;
         }
-        // (written again for the next item only behind `ofull`, for which the other
-        // groups have worked through this one's steps)
-        if (grp < 2) Dh[grp][row] = D;
-        arrive(bar(&dhfull));
+        const auto dot = [](uint4 u, uint4 w, float sum) {
+          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            sum = fmaf(__uint_as_float(us[c] << 16), __uint_as_float(ws[c] << 16), sum);
+            sum = fmaf(__uint_as_float(us[c] & 0xffff0000u), __uint_as_float(ws[c] & 0xffff0000u), sum);
+          }
+          return sum;
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float sum = 0.f, rest = 0.f;
+#pragma unroll
+          for (int e = t; e < 2 * NP; e += 2) {
+            sum = dot(x[e], y[e], sum);
+            rest = dot(x[e], z[e], rest);
+          }
+          sum += rest;
+#pragma unroll
+          for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          // (written again for the next item only behind `ofull`, for which all have
+          // worked through this one's steps)
+          if ((lane & 7) == 0) Ds[row8 + 4 * t] = sum;
+        }
+        arrive_warp(bar(&dhfull));
         if (!wait_warp(gm.err, bar(&dhfull), (uint32_t)nd++ & 1u)) break;
-        D = Dh[0][row] + Dh[1][row];
+        D = Ds[row];
         if (grp == 0 && i < r.i1) a.D[qrow] = D;
       }
 
@@ -385,10 +398,12 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
                            (s.r0 >= free_lo || s.re <= a.sinks);
         const int h = min(wr.hi, s.re) - s.r0 - c0, l = wr.lo - s.r0 - c0, z = wr.S - s.r0 - c0;
         ld_wait(dp);
+        tc::fence_before();
+        arrive_warp(bar(&dpempty));
         ds_store(S, v, dp, D2, whole, whole ? 0u : seen_bits(l, h, z));
         st_wait();
         tc::fence_before();
-        arrive(bar(&dsfull[n & 1]));
+        arrive_warp(bar(&dsfull[n & 1]));
       }
       if (bad) break;
       if (r.steps > 0) {
@@ -396,30 +411,23 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dq_tc(const __grid_constant__ Bw
         ++no;
         tc::fence_after();
       }
-      // d / 16 pieces of 16 columns, shared by the groups
-      __nv_bfloat16* dst = (__nv_bfloat16*)a.dq + qrow * a.d;
+      // pieces of 32 columns, shared by the groups
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.dq + (((size_t)r.b * a.Hq + r.h) * a.Nq + r.i0) * a.d;
 #pragma unroll 1
-      for (int q = 16 * grp; q < a.d; q += 64) {
-        uint32_t o[16];
+      for (int q = 32 * grp; q < a.d; q += 128) {
+        uint32_t o[32];
         if (r.steps > 0) {
-          tc::tmem_ld<16>(tO + lanes + q, o);
+          ld32(tO + lanes + q, o);
+          ld_wait(o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0;
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (i >= r.i1) continue;
-#pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          float f[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(o[e + x]) * a.scale;
-          *reinterpret_cast<uint4*>(dst + q + e) =
-              make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
-        }
+        store_bf16(dst + q, nullptr, a.d, 32 * (warp & 3), r.i1 - r.i0, (a.d - q) / 8, o, a.scale);
       }
       if (r.steps > 0) {
         tc::fence_before();
-        arrive(bar(&oempty));
+        arrive_warp(bar(&oempty));
       }
     }
   }
@@ -770,35 +778,39 @@ __global__ void __launch_bounds__(BTH, 1) k_win_dkv_tc(const __grid_constant__ B
         ++ng;
         tc::fence_after();
       }
-      // dK by groups 0 and 1, dV by 2 and 3, pieces of 16 columns in turn
+      // dK by groups 0 and 1, dV by 2 and 3, pieces of 32 columns in turn
       const int which = grp >> 1;
       const uint32_t G = (which ? tV : tK) + lanes;
       const float f = which ? 1.f : a.scale;
-      const size_t krow = ((size_t)r.b * a.Hkv + r.hk) * a.Nk + j;
-      __nv_bfloat16* dst = (__nv_bfloat16*)(which ? a.dv : a.dk) + krow * a.d;
-      float* part = a.part + (((((size_t)r.b * a.Hkv + r.hk) * a.stiles + r.tile) * a.chunks +
-                               (r.chunk >= 0 ? r.chunk : 0)) * 2 + which) * BT * a.d + (size_t)row * a.d;
+      const size_t head = (size_t)r.b * a.Hkv + r.hk;
+      __nv_bfloat16* dst = (__nv_bfloat16*)(which ? a.dv : a.dk) + (head * a.Nk + r.j0) * a.d;
+      float* part = a.part + (((head * a.stiles + r.tile) * a.chunks + (r.chunk >= 0 ? r.chunk : 0)) * 2 +
+                              which) * BT * a.d;
 #pragma unroll 1
-      for (int q = 16 * (grp & 1); q < a.d; q += 32) {
-        uint32_t o[16];
+      for (int q = 32 * (grp & 1); q < a.d; q += 64) {
+        uint32_t o[32];
         if (r.steps > 0) {
-          tc::tmem_ld<16>(G + q, o);
+          ld32(G + q, o);
+          ld_wait(o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0;
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * f;
         if (r.chunk >= 0) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) st4(part + q + e, make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
-        } else if (j < a.Nk) {
+          for (int h = 0; h < 2; ++h) {
+            uint4 x[4];
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(dst + q + e) =
-                make_uint4(pack(x[e], x[e + 1]), pack(x[e + 2], x[e + 3]), pack(x[e + 4], x[e + 5]),
-                           pack(x[e + 6], x[e + 7]));
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* p = o + 16 * h + 4 * e;
+              x[e] = make_uint4(__float_as_uint(__uint_as_float(p[0]) * f), __float_as_uint(__uint_as_float(p[1]) * f),
+                                __float_as_uint(__uint_as_float(p[2]) * f), __float_as_uint(__uint_as_float(p[3]) * f));
+            }
+            if (q + 16 * h < a.d)
+              store_rows(part + q + 16 * h, 4 * (size_t)a.d, 32 * (warp & 3), BT, 4, x);
+          }
+        } else {
+          store_bf16(dst + q, nullptr, a.d, 32 * (warp & 3), a.Nk - r.j0, (a.d - q) / 8, o, f);
         }
       }
       if (r.steps > 0) {

@@ -41,6 +41,11 @@ __device__ __forceinline__ bool wait_warp(int* err, uint32_t bar, uint32_t parit
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// one arrival of the whole warp (the lanes' fences come before the __syncwarp)
+__device__ __forceinline__ void arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
+}
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
                                      uint32_t mbar) {
   asm volatile(
@@ -146,7 +151,7 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {
       "r"(v[30]), "r"(v[31]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
       "%10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
@@ -180,6 +185,60 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t h) {
       : "=f"(x), "=f"(y) : "f"(a), "f"(b), "r"(h));
   return pack(x, y);
 }
+// Writes 16-byte pieces c of the warp's 32 rows (a row per lane, rows `first`..,
+// `stride` bytes apart, only those below `rows`; only `pieces` of 4).  Fours of lanes
+// change places first, so that they write 64 bytes of a row: a store then touches 8 rows
+// instead of 32, whose lines the load-store unit takes one by one.
+__device__ __forceinline__ void store_rows(void* tile, size_t stride, int first, int rows, int pieces,
+                                           uint4 (&c)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = 1; x <= 2; x <<= 1) {
+    const bool odd = lane & x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4& a = c[x == 1 ? 2 * h : h];
+      uint4& b = c[x == 1 ? 2 * h + 1 : h + 2];
+      const uint4 give = odd ? a : b;
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, x);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, x);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, x);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, x);
+      if (odd)
+        a = got;
+      else
+        b = got;
+    }
+  }
+  const int row = first + (lane & ~3), i = lane & 3;
+  uint8_t* dst = (uint8_t*)tile + row * stride + 16 * i;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (row + r < rows && i < pieces) *reinterpret_cast<uint4*>(dst + r * stride) = c[r];
+}
+// 32 columns of the rows, times f, as bf16 to `tile`, and what the rounding leaves to
+// `rest` when it is set
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* tile, __nv_bfloat16* rest, int d, int first,
+                                           int rows, int pieces, const uint32_t (&v)[32], float f) {
+  uint4 c[4], z[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x[8];
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * e + i]) * f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = pack(x[2 * i], x[2 * i + 1]);
+    c[e] = make_uint4(h[0], h[1], h[2], h[3]);
+    if (rest)
+      z[e] = make_uint4(pack_rest(x[0], x[1], h[0]), pack_rest(x[2], x[3], h[1]),
+                        pack_rest(x[4], x[5], h[2]), pack_rest(x[6], x[7], h[3]));
+  }
+  store_rows(tile, 2 * (size_t)d, first, rows, pieces, c);
+  if (rest) store_rows(rest, 2 * (size_t)d, first, rows, pieces, z);
+}
+
 // eight values of an output row, and what their rounding leaves when `rest` is set
 __device__ __forceinline__ void store8(__nv_bfloat16* dst, __nv_bfloat16* rest, const float (&f)[8]) {
   uint32_t h[4];
