@@ -14,6 +14,10 @@
 // met for k_token_join.  Blocks that shared rows out by themselves lost 8 us a wave to
 // their start and end and, on ragged batches, a second wave (32 sequences, 8192
 // tokens at the most: 110 us).
+// Measured: that batch, 32 heads of 128 on 8: 84 us + 8 for the join, 4.0 TB/s of the
+// cache's bytes (the copies alone, without a product, took 60 to 74); 4 sequences up to
+// 131072 tokens, 4 queries of 16 heads on 4: 87 + 16 us; 16 sequences of bf16 keys, window
+// 1024: 20 + 8 us, 3.4 TB/s.  Two blocks of an SM hold what registers allow.
 //
 // Products on the warp-level tensor instruction (m16n8k16), rows = (query head
 // of the group, query), with the contraction's order chosen so that no operand

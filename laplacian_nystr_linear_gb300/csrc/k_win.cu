@@ -11,7 +11,9 @@
 // columns of the outputs in registers; operand tiles in padded shared memory.
 // Rows of one tile belong to one half-warp, so P goes through shared memory
 // with a warp barrier only.  Bound by the FP32 pipe: 4 d (forward) and 14 d
-// (backward, scores recomputed in both kernels) operations per visible pair.
+// (backward, scores recomputed in both kernels) operations per visible pair; by its
+// latency where there are few tiles (196 tokens, one head of 32: 32, 35 and 47 us for 4
+// blocks of one to two steps, beside 100 us and more of the host's work for the call).
 #include "common.cuh"
 #include "internal.h"
 #include "win.cuh"

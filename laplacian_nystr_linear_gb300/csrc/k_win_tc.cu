@@ -15,16 +15,20 @@
 //                   relative rounding are as good there), so the outputs are
 //                   rescaled on few steps;
 //   warp 8          TMA: K and V tiles through two rings;
-//   warp 9          one thread issues  S = Q K^T  (both operands in shared memory)
-//                   and  O += P V  (P in tensor memory, V as it lies: MN-major).
-//                   A tile has two score buffers, so the scores of the next step
-//                   are there when the softmax of this one ends.  Steps of 128 keys
-//                   leave no room for that beside two outputs of 128 columns: then
-//                   softmax, P V and the next Q K^T of a tile follow one another
-//                   (444 us for the prompt below; two tiles overlap only half of it).
+//   warps 9, 10     one thread each issues a tile's  S = Q K^T  (both operands in
+//                   shared memory) and  O += P V  (P in tensor memory, V as it lies:
+//                   MN-major).  A tile has two score buffers, so the scores of the
+//                   next step are there when the softmax of this one ends.  Steps of
+//                   128 keys leave no room for that beside two outputs of 128 columns:
+//                   then softmax, P V and the next Q K^T of a tile follow one another
+//                   (a prompt of 32768: 444 us against 426).
 //
 // Bound: 4 d flops per visible pair on the tensor pipe, or one exponential per
 // pair on the special-function pipe, whichever is longer (d = 64: the latter).
+// Measured: a prompt of 32768 tokens, 8 heads of 128 on 2, window 4096: 428 us, 1.2
+// PFLOP/s; 16384 tokens, 2 x 16 heads of 64, window 1024: 260 us (0.51 PFLOP/s), the
+// softmax warps' arithmetic and the steps' latencies; 3136 tokens, 32 heads, windows
+// of 225: 35 us.
 // Rows of V at and behind the sequence's end are zeroed in shared memory (P is 0
 // there, but 0 * NaN is not); rows behind the tensor's are zero by TMA.
 // Every wait is bounded, as in the other tensor-core kernels.
@@ -55,7 +59,6 @@ struct FwdMaps {
   CUtensorMap k16, v16;                 // boxes of 64 x 16 for narrow steps
 };
 struct FwdGeom {
-  int qt;                               // tiles of 128 query rows
   int npair;                            // items per (batch, key head): pairs of heads or of tiles
   int by_head;                          // 1: an item's tiles are two heads
   int items;
@@ -501,9 +504,9 @@ cudaError_t run_win_fwd_tc(const WinArgs& a, cudaStream_t st) {
   FwdGeom gm;
   gm.err = wait_error_address();
   if (gm.err == nullptr) return cudaErrorInvalidSymbol;
-  gm.qt = (a.Nq + FT - 1) / FT;
+  const int qt = (a.Nq + FT - 1) / FT;
   gm.by_head = a.g % 2 == 0;
-  gm.npair = gm.by_head ? gm.qt : (gm.qt + 1) / 2;
+  gm.npair = gm.by_head ? qt : (qt + 1) / 2;
   gm.items = a.B * a.Hkv * (gm.by_head ? a.g / 2 : a.g) * gm.npair;
   if (!win_map(&mp.q, a.q, a.B * a.Hq, a.Nq, a.d, FT) ||
       !win_map(&mp.k, a.k, a.B * a.Hkv, a.Nk, a.d, FK) ||

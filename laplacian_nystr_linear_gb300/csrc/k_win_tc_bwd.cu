@@ -23,16 +23,26 @@
 //   warp 17 (dq: and 18)  one thread issues the products, the bf16 tile's product
 //               always before the one that overwrites it, so that their order needs
 //               no barrier:
-//                 dq:   dQ(j) S(j+2) (S in two buffers)  |  dP(j+1)
+//                 dq:   dQ(j) S(j+2) (S in two buffers)  |  dP(j+1), once dP(j) is
+//                       in registers
 //                 dkv:  dV(j) S(j+1) dK(j) dP(j+1)
-//               (two threads for dkv as well, dV S | dK dP: 4 heads of 128 for 16,
-//               244 -> 316 us, the score product then waits behind dK);
+//               (dkv of 2 x 16 heads of 64, 16384 tokens: 450 us; with two threads
+//               537; with dS beside P, S in two buffers and dP freed early as in dq
+//               478, with two threads 519.  Two blocks an SM with steps of 64: 558,
+//               and 393 for dq's 366);
 //   warp 18     dkv: log-sum and D of a step's queries into shared memory.
 //
 // Key tiles with first tokens are seen by all later queries: their queries are
 // cut into chunks, one item each, with fp32 partials that k_win_join adds.
 // Rows behind a sequence's end are zeroed in shared memory where they are
 // summed over (0 * NaN).  Every wait is bounded.
+//
+// Bound: 16 d flops per visible pair (with dS in two parts) on the tensor pipe, or the
+// elementwise warps.  Measured: 16384 tokens, 2 x 16 heads of 64, window 1024: dq 366,
+// dkv 450, join 13 us; issue slots 59 % and tensor pipe 41 % busy in dq: what the steps
+// wait for one another and some 4000 cycles an item of 9 steps for D, the outputs and
+// the next item's start.  8192 tokens, 16 heads of 128 on 4, window 2048: 185, 220 and
+// 6 us (0.73 PFLOP/s of the 10 d flops a pair that are needed).
 #include <cstring>
 
 #include "internal.h"
