@@ -281,13 +281,13 @@ int lapnys_block_bwd(const void* x, const void* w_qkv, const void* w_o, const vo
  *    the last tokens).  A query that sees no key (padding, an empty sequence)
  *    gives out = 0, lse = -inf, and takes no part in any gradient; k, v rows
  *    that no query sees get gradient 0.  Every element of out, dq, dk, dv is
- *    written.
+ *    written; outputs share no memory with inputs or with one another.
  *  - Keys, values and queries inside a sequence have to be finite for finite
  *    results: what one query does not see may still meet it as 0 * value.
  *  - lse [B][Hq][Nq] float: log2 of the sum of exp(s); may be NULL in the
  *    forward; the backward reads the forward's.
- *  - rest (bf16 only; may be NULL): like out, what the rounding of out left, rounded
- *    itself.  The backward takes D = dout.o from out + rest; without it D carries
+ *  - rest (bf16 only, else EINVAL; may be NULL): like out, what the rounding of out
+ *    left, rounded itself.  The backward takes D = dout.o from out + rest; without it D carries
  *    out's rounding, which counts where a query sees few keys (dq off by 4e-3 of its
  *    norm at two keys, with it by 2e-3).
  *  - fp32 arithmetic; bf16 tensors: products of bf16 operands with fp32 sums,

@@ -164,13 +164,13 @@ int lapnys_window_fwd(const void* q, const void* k, const void* v, void* out, fl
   if (rc != LAPNYS_OK) return rc;
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
       !aligned(out, 16) || !aligned(rest, 16) || !aligned(lse, 4) || !aligned(lens, 4) ||
-      !aligned(q_pos, 4))
+      !aligned(q_pos, 4) || (rest && dtype != LAPNYS_BF16))
     return LAPNYS_EINVAL;
   const WinWs w = window_ws(a, false, dtype);
   if (w.total > 0 && (!ws || !aligned(ws, 16))) return LAPNYS_EINVAL;
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.lens = lens; a.q_pos = q_pos;
-  a.rest = dtype == LAPNYS_BF16 ? rest : nullptr;
+  a.rest = rest;
   if (few(a.g, Nq)) {
     token_parts(t, w.tok, ws);
     t.err = wait_error_address();
@@ -194,13 +194,14 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
   const void* all[] = {q, k, v, out, dout, dq, dk, dv, ws};
   for (const void* p : all)
     if (!p || !aligned(p, 16)) return LAPNYS_EINVAL;
-  if (!lse || !aligned(rest, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4))
+  if (!lse || !aligned(rest, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(q_pos, 4) ||
+      (rest && dtype != LAPNYS_BF16))
     return LAPNYS_EINVAL;
   const WinWs w = window_ws(a, true, dtype);
   if (ws_bytes < w.total) return LAPNYS_ENOSPC;
   a.q = q; a.k = k; a.v = v; a.out = const_cast<void*>(out); a.dout = dout;
   a.lse = const_cast<float*>(lse); a.lens = lens; a.q_pos = q_pos;
-  a.rest = dtype == LAPNYS_BF16 ? const_cast<void*>(rest) : nullptr;
+  a.rest = const_cast<void*>(rest);
   a.dq = dq; a.dk = dk; a.dv = dv;
   a.D = (float*)((uint8_t*)ws + w.D);
   a.part = (float*)((uint8_t*)ws + w.part);

@@ -13,6 +13,7 @@ import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import check, load
@@ -124,7 +125,7 @@ def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=No
     if lse is not None:
         _tensor(lse, "lse", q.shape[:3], torch.float32, dev)
     if rest is not None:
-        _tensor(rest, "rest", q.shape, q.dtype, dev)
+        _tensor(rest, "rest", q.shape, torch.bfloat16, dev)
     with _on(dev):
         out = torch.empty_like(q) if out is None else out
         if not need_lse:
@@ -150,7 +151,7 @@ def window_bwd(q, k, v, out, dout, lse, p: WindowParams, lens=None, q_pos=None, 
         if t is not None:
             _tensor(t, name, like.shape, q.dtype, dev)
     if rest is not None:
-        _tensor(rest, "rest", q.shape, q.dtype, dev)
+        _tensor(rest, "rest", q.shape, torch.bfloat16, dev)
     return _bwd(q, k, v, out, dout, lse, rest, p, lens, q_pos, dq, dk, dv, ws)
 
 
@@ -164,8 +165,8 @@ def _bwd(q, k, v, out, dout, lse, rest, p, lens, q_pos, dq, dk, dv, ws):
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype, True), dev)
         rc = load().lapnys_window_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
-            _at(rest), _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p, _on_stream(dev),
-            _dtype(q), _at(ws), _nbytes(ws))
+            _at(rest), _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p,
+            _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_bwd")
     return dq, dk, dv
 
@@ -180,6 +181,7 @@ class _Window(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(fctx, dout):
         q, k, v, out, lse, rest, lens, q_pos = fctx.saved_tensors   # checked by the forward
         return *_bwd(q, k, v, out, dout.contiguous(), lse, rest, fctx.p, lens, q_pos, None, None,
@@ -194,6 +196,8 @@ def window_attention(q, k, v, left, right=0, sinks=0, scale=None, lens=None, q_p
     all) and the first `sinks` of its sequence, never beyond p + right.  lens: int32 [B], tokens of
     each sequence of a padded batch; q_pos: int32 [B], position of each sequence's first query
     (default Nk - Nq).  Queries that see nothing give zeros.  scale defaults to 1 / sqrt(d).
+    Gradients are of first order.  A step that is captured into a CUDA graph takes leaves that no
+    eager autograd graph still holds (their gradients would be added up on that graph's stream).
     """
     p = WindowParams.of(q, k, left, right, sinks, scale)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):

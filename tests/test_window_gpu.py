@@ -176,6 +176,36 @@ def test_streams_graphs_and_two_at_once():
             assert torch.equal(x, y)
 
 
+def test_shared_inputs_partial_gradients_and_second_order():
+    """One tensor as queries, keys and values; gradients asked of some inputs only; a broadcast
+    output gradient; second derivatives are refused."""
+    q, k, v, _ = make(2, 2, 2, 70, 70, 32, BF)
+    a = dict(left=20, right=3, sinks=1)
+    ones = torch.ones_like(q)
+    p = lap.WindowParams.of(q, k, 20, 3, 1)
+
+    def grads(q, k, v):
+        rest = torch.empty_like(q)
+        out, lse = lap.window_fwd(q, k, v, p, rest=rest)
+        return lap.window_bwd(q, k, v, out, ones, lse, p, rest=rest)
+
+    x = q.detach().requires_grad_(True)
+    lap.window_attention(x, x, x, **a).sum().backward()
+    parts = [g.float() for g in grads(q, q, q)]
+    # two sums of bf16 values, each rounded (2^-8 of at most the magnitudes' sum)
+    assert bool(((x.grad.float() - sum(parts)).abs() <= 2.0 ** -6 * sum(g.abs() for g in parts)).all())
+    want = grads(q, k, v)
+    for i in range(3):
+        t = [y.detach().requires_grad_(j == i) for j, y in enumerate((q, k, v))]
+        lap.window_attention(*t, **a).sum().backward()
+        assert torch.equal(t[i].grad, want[i])
+        assert all(y.grad is None for j, y in enumerate(t) if j != i)
+    y = q.detach().requires_grad_(True)
+    g, = torch.autograd.grad(lap.window_attention(y, k, v, **a).sum(), y, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_guarded_outputs_and_repeatability():
     """Every output element is written, nothing beside it, and twice the same."""
     for Nq, Nk in ((150, 150), (1, 150)):

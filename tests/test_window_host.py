@@ -43,7 +43,8 @@ def _bwd(lib, **kw):
 BAD = [dict(B=0), dict(Hq=0), dict(Hq=3), dict(Hkv=-1), dict(Nq=0), dict(Nk=0), dict(Nk=(1 << 28) + 1),
        dict(left=-2), dict(right=-2), dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan")),
        dict(scale=float("inf")), dict(scale=-1.0), dict(dtype=2), dict(q=None), dict(k=ODD), dict(v=None),
-       dict(out=ODD), dict(lse=ODD2), dict(rest=ODD), dict(lens=ODD2), dict(q_pos=ODD2), dict(B=1 << 20, Hq=1 << 10)]
+       dict(out=ODD), dict(lse=ODD2), dict(rest=ODD),
+       dict(rest=FAKE, dtype=0), dict(lens=ODD2), dict(q_pos=ODD2), dict(B=1 << 20, Hq=1 << 10)]
 
 
 @pytest.mark.parametrize("bad", BAD, ids=str)
