@@ -14,17 +14,20 @@
 // met for k_token_join.  Blocks that shared rows out by themselves lost 8 us a wave to
 // their start and end and, on ragged batches, a second wave (32 sequences, 8192
 // tokens at the most: 110 us).
-// Measured: that batch, 32 heads of 128 on 8: 84 us + 8 for the join, 4.0 TB/s of the
-// cache's bytes (the copies alone, without a product, took 60 to 74); 4 sequences up to
-// 131072 tokens, 4 queries of 16 heads on 4: 87 + 16 us; 16 sequences of bf16 keys, window
-// 1024: 20 + 8 us, 3.4 TB/s.  Two blocks of an SM hold what registers allow.
+// Measured: that batch, 32 heads of 128 on 8: 63 us + 8 for the join, 5.3 TB/s of the
+// cache's bytes; 4 sequences up to 131072 tokens, 4 queries of 16 heads on 4: 86 + 16 us;
+// 16 sequences of bf16 keys, window 1024: 19 + 8 us, 3.6 TB/s.
 //
-// Products on the warp-level tensor instruction (m16n8k16), rows = (query head
-// of the group, query), with the contraction's order chosen so that no operand
-// is transposed or gathered: a thread's four k of step s are four neighbouring
-// features (scores), and column n of output step nt is feature n DP / 8 + nt
-// (P V), so both operands come from shared memory in 16-byte reads without bank
-// conflicts (rows of 128 bytes in TMA's 128-byte swizzle).
+// Products on the warp-level tensor instruction (m16n8k16), with the contraction's
+// order chosen so that no operand is transposed or gathered: a thread's four k of step s
+// are four neighbouring features (scores), and column n of output step nt is feature
+// n DP / 8 + nt (P V), so keys and values come from shared memory in 16-byte reads
+// without bank conflicts (rows of 128 bytes in TMA's 128-byte swizzle).  Rows = (query
+// head of the group, query), 16 of them; where there are 8 at most (a token of 4 or 8
+// heads a key head) they are the products' columns instead and the keys, the values'
+// features their rows: half the products, half the registers for queries and outputs,
+// so three blocks of an SM instead of two (84 us for the batch above with 16 rows).  P
+// then has to be turned, one movmatrix for 8 keys.
 //   - 8-bit: e4m3 -> f16 is exact (one instruction for two; the e4m3 form of the
 //     product is no instruction of its own here: it ran as two f16 ones with more
 //     conversions, 1576 instructions for 32 keys against about 600).  q is scaled
@@ -58,15 +61,21 @@ struct Kind {
   static constexpr int PARTS = KIND == TK_F32 ? 3 : (KIND == TK_E4M3_F32 ? 2 : 1);
   static constexpr float SHIFT = F16 ? 10.f : 0.f;  // p is held as 2^SHIFT p
 };
-template <int KIND, int DP>
-__host__ __device__ constexpr int ring_stages() { return DP == 128 && KIND != TK_E4M3_F32 ? 3 : 4; }
-template <int KIND, int DP>
-__host__ __device__ constexpr size_t token_smem() {   // rings from a multiple of 1024 bytes on
-  return (size_t)TNW * ring_stages<KIND, DP>() * 2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + 1024;
+// ROWS: 16 query rows, or 8 where that is all there are
+template <int KIND, int DP, int ROWS>
+__host__ __device__ constexpr int ring_stages() {
+  return DP < 128 || KIND == TK_E4M3_F32 ? 4 : (ROWS == 8 && KIND != TK_F32 ? 2 : 3);
 }
-// blocks of an SM: two (by registers), one where the rings are that large
-template <int KIND, int DP>
-__host__ __device__ constexpr int token_blocks() { return token_smem<KIND, DP>() > 113 * 1024 ? 1 : 2; }
+template <int KIND, int DP, int ROWS>
+__host__ __device__ constexpr size_t token_smem() {   // rings from a multiple of 1024 bytes on
+  return (size_t)TNW * ring_stages<KIND, DP, ROWS>() * 2 * Kind<KIND>::GK * DP * Kind<KIND>::ES + 1024;
+}
+// blocks of an SM: two (by registers), three of 8 rows, fewer where the rings are that large
+template <int KIND, int DP, int ROWS>
+__host__ __device__ constexpr int token_blocks() {
+  constexpr size_t smem = token_smem<KIND, DP, ROWS>();
+  return smem > 113 * 1024 ? 1 : (smem > 74 * 1024 || ROWS == 16 || KIND == TK_E4M3_F32 ? 2 : 3);
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -81,6 +90,12 @@ __device__ __forceinline__ void mma_bf(float (&d)[4], const uint32_t (&a)[4], ui
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// an 8 x 8 tile of 16-bit values, a row's pair 2 t in lane 4 row + t: transposed
+__device__ __forceinline__ uint32_t turn(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // two e4m3 values (low 16 bits) -> two f16, exact
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
@@ -132,11 +147,12 @@ struct TokenMaps {
   CUtensorMap k, v;   // {d, tokens, (batch or block, head)}, boxes of a panel x a copy's rows
 };
 
-template <int KIND, int DP>
-__global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_token(const __grid_constant__ TokenMaps mp, const TokenArgs t) {
+template <int KIND, int DP, int ROWS>
+__global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>())) k_token(const __grid_constant__ TokenMaps mp, const TokenArgs t) {
   using X = Kind<KIND>;
   constexpr int ES = X::ES, RB = DP * ES, NP = X::PARTS, GK = X::GK, NU = GK / 8, NH = GK / 16;
-  constexpr int NST = ring_stages<KIND, DP>();
+  constexpr int NST = ring_stages<KIND, DP, ROWS>();
+  constexpr bool FEW = ROWS == 8;
   constexpr int TILE = GK * RB, SLOT = 2 * TILE;
   constexpr int KS = DP / 16;                  // 16-feature steps of the scores
   constexpr int NT = DP / 8;                   // column steps of P V
@@ -333,10 +349,13 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
   enter(cu);
   int left = mine;
 
-  // ---- the row's queries: rows gid and gid + 8 of the tile ----
+  // ---- the row's queries: 16 rows are the products' rows, 8 their columns; row[] and
+  // qs[] are those of this thread's scores: rows gid and gid + 8, or columns 2 tq and
+  // 2 tq + 1 ----
+  constexpr int QR = FEW ? 2 : 4;
   WinRow row[2];
   float qs[2];                         // score factor of the row
-  uint32_t qf[NP][KS][4];
+  uint32_t qf[NP][KS][QR];
   int free_lo = 0, free_hi = -1;       // keys [free_lo, free_hi) every query sees: no mask
   auto queries = [&](const Cursor& c) {
     const int hk = c.hr / t.rtiles, rt = c.hr - hk * t.rtiles;
@@ -344,7 +363,7 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
     free_lo = c.sq.qp + a.Nq - 1 - a.left;
     free_hi = rows_ok ? min(c.sq.len, c.sq.qp + a.right + 1) : -1;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < ROWS / 8; ++r) {
       const int rr = rt * 16 + gid + 8 * r;
       const bool ok = rr < R;
       const int e = ok ? rr / a.Nq : 0, i = ok ? rr % a.Nq : 0;
@@ -381,20 +400,30 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
         for (int p = 0; p < NP; ++p) qf[p][s][r] = u[p];
         split<KIND>(x[s].z * down, x[s].w * down, u);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) qf[p][s][2 + r] = u[p];
+        for (int p = 0; p < NP; ++p) qf[p][s][QR / 2 + r] = u[p];
+      }
+    }
+    if constexpr (FEW) {
+      const float own = qs[0];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = 2 * tq + e;
+        qs[e] = __shfl_sync(0xffffffffu, own, 4 * rr);
+        row[e] = rr < R ? win_row(a, c.sq, rr % a.Nq) : WinRow{0, 0, 0};
       }
     }
   };
 
   float m[2], l[2];
   float vref;                        // reference of the values' scales: v = vref x what o holds
-  float o[NT][4];
+  constexpr int NO = FEW ? NT / 2 : NT;
+  float o[NO][4];                    // 16 rows: [n] is column n; 8: [n] features 2 n, 2 n + 1
   auto clear = [&]() {
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
     vref = 1.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NO; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   };
@@ -404,22 +433,28 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
   auto leave = [&](const Cursor& c) {
     const int rt = c.hr % t.rtiles, rowid = c.b * heads + c.hr;
     const size_t part = (size_t)(w + rowid) * 16;
+    // (the lanes that share a row: 4, or the 8 of a column)
+    constexpr int X0 = FEW ? 4 : 1, X1 = FEW ? 16 : 2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int rr = gid + 8 * r;
+#pragma unroll
+      for (int x = X0; x <= X1; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+      const int rr = FEW ? 2 * tq + r : gid + 8 * r;
       if (rt * 16 + rr >= R) continue;
-      if (tq == 0) t.part_ml[part + rr] = make_float2(m[r], l[r]);
+      if ((FEW ? gid : tq) == 0) t.part_ml[part + rr] = make_float2(m[r], l[r]);
       float* dst = t.part_o + (part + rr) * a.d;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < (FEW ? 1 : 2); ++e)
 #pragma unroll
         for (int n = 0; n < NT; n += 4) {
-          const int f = n / VP * (128 / ES) + (2 * tq + e) * VP + n % VP;
-          if (f < a.d)
-            st4(dst + f, make_float4(o[n][2 * r + e] * vref, o[n + 1][2 * r + e] * vref,
-                                     o[n + 2][2 * r + e] * vref, o[n + 3][2 * r + e] * vref));
+          const int f = n / VP * (128 / ES) + (FEW ? gid : 2 * tq + e) * VP + n % VP;
+          if (f >= a.d) continue;
+          float4 y;
+          if constexpr (FEW)
+            y = make_float4(o[n / 2][r], o[n / 2][2 + r], o[n / 2 + 1][r], o[n / 2 + 1][2 + r]);
+          else
+            y = make_float4(o[n][2 * r + e], o[n + 1][2 * r + e], o[n + 2][2 * r + e], o[n + 3][2 * r + e]);
+          st4(dst + f, make_float4(y.x * vref, y.y * vref, y.z * vref, y.w * vref));
         }
     }
     // the row's first and last parts
@@ -468,9 +503,12 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
       __syncwarp();
     }
     // ---- scores ----
-    float s[NU][4];
+    // 16 rows: [u] is 8 keys, by row r the values [2 r + e] of keys 2 tq + e; 8: [h] is 16
+    // keys, the values [2 (u & 1) + e] of key 8 u + gid and column 2 tq + e
+    constexpr int NS = FEW ? NH : NU;
+    float s[NS][4];
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int u = 0; u < NS; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
 #pragma unroll
@@ -481,7 +519,40 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
         const uint4 kv = *reinterpret_cast<const uint4*>(Kt + tile_off<RB, GK>(8 * u + gid, key_chunk<RB>(tq, i)));
         w[u][0] = kv.x; w[u][1] = kv.y; w[u][2] = kv.z; w[u][3] = kv.w;
       }
-      if constexpr (KIND == TK_F32) {
+      if constexpr (FEW) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t (&lo)[4] = w[2 * h], (&hi)[4] = w[2 * h + 1];   // keys gid, gid + 8
+          if constexpr (KIND == TK_F32) {
+            uint32_t p[4][3];
+            split3_bf16x2(__uint_as_float(lo[0]), __uint_as_float(lo[1]), p[0]);
+            split3_bf16x2(__uint_as_float(hi[0]), __uint_as_float(hi[1]), p[1]);
+            split3_bf16x2(__uint_as_float(lo[2]), __uint_as_float(lo[3]), p[2]);
+            split3_bf16x2(__uint_as_float(hi[2]), __uint_as_float(hi[3]), p[3]);
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+              for (int y = 0; y <= x; ++y) {
+                const uint32_t k4[4] = {p[0][x - y], p[1][x - y], p[2][x - y], p[3][x - y]};
+                mma_bf(s[h], k4, qf[y][i][0], qf[y][i][1]);
+              }
+          } else if constexpr (KIND == TK_BF16) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t k4[4] = {lo[2 * x], hi[2 * x], lo[2 * x + 1], hi[2 * x + 1]};
+              mma_bf(s[h], k4, qf[0][2 * i + x][0], qf[0][2 * i + x][1]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t k4[4] = {e4m3x2_f16(lo[x]), e4m3x2_f16(hi[x]), e4m3x2_f16(lo[x] >> 16),
+                                      e4m3x2_f16(hi[x] >> 16)};
+#pragma unroll
+              for (int p = NP - 1; p >= 0; --p) mma_f16(s[h], k4, qf[p][4 * i + x][0], qf[p][4 * i + x][1]);
+            }
+          }
+        }
+      } else if constexpr (KIND == TK_F32) {
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           uint32_t p0[3], p1[3];
@@ -511,7 +582,12 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
     // ---- softmax, running maximum and sum ----
     const bool whole = inside && j0 + GK <= free_hi &&
                        (j0 >= free_lo || j0 + GK <= a.sinks);
-    float p[NU][4];
+    // value x of row r: its place, its key, its 16 keys
+    constexpr int NV = FEW ? NU : 2 * NU, X0 = FEW ? 4 : 1, X1 = FEW ? 16 : 2;
+    const auto at = [](int r, int x) { return FEW ? 2 * (x & 1) + r : 2 * r + (x & 1); };
+    const auto key = [&](int x) { return FEW ? 8 * x + gid : 8 * (x >> 1) + 2 * tq + (x & 1); };
+    constexpr int PER = FEW ? 2 : 4;
+    float p[NS][4];
     bool up = false;
     float f[2];
 #pragma unroll
@@ -521,22 +597,18 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
       for (int h = 0; h < NH; ++h) qk[h] = qs[r] * ksc[h];
       float mx = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) s[u][2 * r + e] *= qk[u / 2];
+      for (int x = 0; x < NV; ++x) s[x >> 1][at(r, x)] *= qk[x / PER];
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = j0 + 8 * u + 2 * tq + e;
-            if (!(there[u / 2] && j >= jb && j < je && win_sees(row[r], j))) s[u][2 * r + e] = -INFINITY;
-          }
+        for (int x = 0; x < NV; ++x) {
+          const int j = j0 + key(x);
+          if (!(there[x / PER] && j >= jb && j < je && win_sees(row[r], j))) s[x >> 1][at(r, x)] = -INFINITY;
+        }
       }
 #pragma unroll
-      for (int u = 0; u < NU; ++u) mx = fmaxf(fmaxf(mx, s[u][2 * r]), s[u][2 * r + 1]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      for (int x = 0; x < NV; x += 2) mx = fmaxf(fmaxf(mx, s[x >> 1][at(r, x)]), s[x >> 1][at(r, x + 1)]);
+#pragma unroll
+      for (int x = X0; x <= X1; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
       mx = fmaxf(mx, m[r]);
       const float mu = mx == -INFINITY ? 0.f : mx;
       f[r] = exp2f(m[r] - mu);
@@ -545,19 +617,17 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
       const float off = X::SHIFT - mu;
       float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = exp2f(s[u][2 * r + e] + off);
-          p[u][2 * r + e] = x;
-          sum += x;
-        }
+      for (int x = 0; x < NV; ++x) {
+        const float y = exp2f(s[x >> 1][at(r, x)] + off);
+        p[x >> 1][at(r, x)] = y;
+        sum += y;
+      }
       l[r] = l[r] * f[r] + sum;
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][0] *= f[0]; o[n][1] *= f[0]; o[n][2] *= f[1]; o[n][3] *= f[1];
+      for (int n = 0; n < NO; ++n) {
+        o[n][0] *= f[0]; o[n][1] *= f[FEW]; o[n][2] *= f[!FEW]; o[n][3] *= f[1];
       }
     }
     // ---- P V ----
@@ -572,7 +642,7 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
         if (r > 1.f || (r < 0x1p-16f && r >= 0x1p-64f)) {
           const float x = vref / vsc[h];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NO; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] *= x;
           vref = vsc[h];
@@ -583,22 +653,49 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
         const float r = there[h] ? vsc[h] / vref : 0.f;
         if (r != 1.f) {
 #pragma unroll
-          for (int u = 2 * h; u < 2 * h + 2; ++u)
+          for (int u = NS / NH * h; u < NS / NH * (h + 1); ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) p[u][e] *= r;
         }
       }
     }
-    uint32_t pf[NP][NU / 2][4];
+    uint32_t pf[NP][NH][QR];
+    if constexpr (FEW) {                   // keys by columns to columns by keys
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int u = 0; u < NU; ++u) {
         uint32_t w[NP];
-        split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
+        split<KIND>(p[u >> 1][2 * (u & 1)], p[u >> 1][2 * (u & 1) + 1], w);
 #pragma unroll
-        for (int x = 0; x < NP; ++x) pf[x][u >> 1][2 * (u & 1) + r] = w[x];
+        for (int x = 0; x < NP; ++x) pf[x][u >> 1][u & 1] = turn(w[x]);
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t w[NP];
+          split<KIND>(p[u][2 * r], p[u][2 * r + 1], w);
+#pragma unroll
+          for (int x = 0; x < NP; ++x) pf[x][u >> 1][2 * (u & 1) + r] = w[x];
+        }
+    }
+    // adds the values' features n and n + 1 (b: n, c: n + 1; keys 2 tq.. and 8 further)
+    const auto add = [&](float (*acc)[4], int x, int g, uint32_t b0, uint32_t b1, uint32_t c0, uint32_t c1) {
+      if constexpr (FEW) {
+        const uint32_t v4[4] = {b0, c0, b1, c1};
+        if constexpr (X::F16) mma_f16(acc[0], v4, pf[x][g][0], pf[x][g][1]);
+        else mma_bf(acc[0], v4, pf[x][g][0], pf[x][g][1]);
+      } else {
+        if constexpr (X::F16) {
+          mma_f16(acc[0], pf[x][g], b0, b1);
+          mma_f16(acc[1], pf[x][g], c0, c1);
+        } else {
+          mma_bf(acc[0], pf[x][g], b0, b1);
+          mma_bf(acc[1], pf[x][g], c0, c1);
+        }
+      }
+    };
+    constexpr int OS = FEW ? 2 : 1;        // features of an o[n]
 #pragma unroll
     for (int g = 0; g < NU / 2; ++g) {     // 16 keys each
       if constexpr (X::F16) {
@@ -616,12 +713,14 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
           }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int sel = (n & 3) | (((n & 3) + 4) << 4);
+        for (int n = 0; n < NT; n += 2) {
+          const int sel = (n & 3) | (((n & 3) + 4) << 4), nxt = sel + 0x11;
           const uint32_t b0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], sel));
           const uint32_t b1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], sel));
+          const uint32_t c0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], nxt));
+          const uint32_t c1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], nxt));
 #pragma unroll
-          for (int x = NP - 1; x >= 0; --x) mma_f16(o[n], pf[x][g], b0, b1);
+          for (int x = NP - 1; x >= 0; --x) add(&o[n / OS], x, g, b0, b1, c0, c1);
         }
       } else if constexpr (KIND == TK_BF16) {
 #pragma unroll
@@ -634,11 +733,11 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int sel = n & 1 ? 0x7632 : 0x5410;
-            mma_bf(o[8 * h + n], pf[0][g], __byte_perm(v[0][n >> 1], v[1][n >> 1], sel),
-                   __byte_perm(v[2][n >> 1], v[3][n >> 1], sel));
-          }
+          for (int n = 0; n < 8; n += 2)
+            add(&o[(8 * h + n) / OS], 0, g, __byte_perm(v[0][n >> 1], v[1][n >> 1], 0x5410),
+                __byte_perm(v[2][n >> 1], v[3][n >> 1], 0x5410),
+                __byte_perm(v[0][n >> 1], v[1][n >> 1], 0x7632),
+                __byte_perm(v[2][n >> 1], v[3][n >> 1], 0x7632));
         }
       } else {
 #pragma unroll
@@ -651,14 +750,17 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP>())) k_t
             v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t b0[3], b1[3];
+          for (int n = 0; n < 4; n += 2) {
+            uint32_t b0[3], b1[3], c0[3], c1[3];
             split3_bf16x2(v[0][n], v[1][n], b0);
             split3_bf16x2(v[2][n], v[3][n], b1);
+            split3_bf16x2(v[0][n + 1], v[1][n + 1], c0);
+            split3_bf16x2(v[2][n + 1], v[3][n + 1], c1);
 #pragma unroll
             for (int x = 2; x >= 0; --x)
 #pragma unroll
-              for (int y = 0; y <= x; ++y) mma_bf(o[4 * h + n], pf[y][g], b0[x - y], b1[x - y]);
+              for (int y = 0; y <= x; ++y)
+                add(&o[(4 * h + n) / OS], y, g, b0[x - y], b1[x - y], c0[x - y], c1[x - y]);
           }
         }
       }
@@ -738,28 +840,32 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
 }
 
 namespace {
-int slots_of(int kind, int d) {
+template <int KIND>
+int blocks_of(int d, bool eight) {
+  if (d <= 64) return eight ? token_blocks<KIND, 64, 8>() : token_blocks<KIND, 64, 16>();
+  return eight ? token_blocks<KIND, 128, 8>() : token_blocks<KIND, 128, 16>();
+}
+int slots_of(int kind, int d, bool eight) {
   const int sms = 152;   // from the type alone: workspaces do not depend on the device
   switch (kind) {
-    case TK_BF16: return sms * (d <= 64 ? token_blocks<TK_BF16, 64>() : token_blocks<TK_BF16, 128>());
-    case TK_E4M3: return sms * (d <= 64 ? token_blocks<TK_E4M3, 64>() : token_blocks<TK_E4M3, 128>());
-    case TK_E4M3_F32:
-      return sms * (d <= 64 ? token_blocks<TK_E4M3_F32, 64>() : token_blocks<TK_E4M3_F32, 128>());
-    default: return sms * (d <= 64 ? token_blocks<TK_F32, 64>() : token_blocks<TK_F32, 128>());
+    case TK_BF16: return sms * blocks_of<TK_BF16>(d, eight);
+    case TK_E4M3: return sms * blocks_of<TK_E4M3>(d, eight);
+    case TK_E4M3_F32: return sms * blocks_of<TK_E4M3_F32>(d, eight);
+    default: return sms * blocks_of<TK_F32>(d, eight);
   }
 }
 int kind_of(bool cache, bool bf16) {
   return cache ? (bf16 ? TK_E4M3 : TK_E4M3_F32) : (bf16 ? TK_BF16 : TK_F32);
 }
 
-template <int KIND, int DP>
+template <int KIND, int DP, int ROWS>
 cudaError_t go(TokenArgs& t, cudaStream_t st) {
   using TQ = typename std::conditional<Kind<KIND>::QF32, float, __nv_bfloat16>::type;
-  constexpr size_t smem = token_smem<KIND, DP>();
+  constexpr size_t smem = token_smem<KIND, DP, ROWS>();
   static SmemOnce once;
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
-  if (e != cudaSuccess || (e = once.allow(k_token<KIND, DP>, smem, dev)) != cudaSuccess) return e;
+  if (e != cudaSuccess || (e = once.allow(k_token<KIND, DP, ROWS>, smem, dev)) != cudaSuccess) return e;
   // a panel's features x the rows of a copy: a group, or a block of 16 tokens
   TokenMaps mp;
   constexpr int ES = Kind<KIND>::ES;
@@ -770,7 +876,7 @@ cudaError_t go(TokenArgs& t, cudaStream_t st) {
   for (int i = 0; i < 2; ++i)
     if (!encode_tiled_rows(i ? &mp.v : &mp.k, i ? a.v : a.k, ES, a.d, N, outer, DP * ES == 64 ? 64 : 128, box))
       return cudaErrorInvalidValue;
-  e = launch("token_attention", k_token<KIND, DP>, dim3((unsigned)t.grid), dim3(32 * TNW + 32), smem, st, mp, t);
+  e = launch("token_attention", k_token<KIND, DP, ROWS>, dim3((unsigned)t.grid), dim3(32 * TNW + 32), smem, st, mp, t);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)t.w.B * t.w.Hq * t.w.Nq;
   return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(128), 0, st, t,
@@ -789,7 +895,7 @@ TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int
     if (w < seen) seen = w;
   }
   const long long rows = (long long)B * Hkv * s.rtiles, groups = rows * (seen / 16 + 3);
-  s.grid = slots_of(kind_of(cache, bf16), d);
+  s.grid = slots_of(kind_of(cache, bf16), d, g * Nq <= 8);
   const long long most = (groups + 2 * TNW - 1) / (2 * TNW);
   if (most < s.grid) s.grid = (int)most;
   const size_t parts = (size_t)rows + (size_t)s.grid * TNW;
@@ -799,14 +905,15 @@ TokenShape token_shape(bool cache, bool bf16, int B, int Hkv, int g, int Nq, int
   return s;
 }
 
+template <int KIND>
+static cudaError_t go_kind(TokenArgs& t, cudaStream_t st) {
+  const bool eight = t.w.g * t.w.Nq <= 8;
+  if (t.w.d <= 64) return eight ? go<KIND, 64, 8>(t, st) : go<KIND, 64, 16>(t, st);
+  return eight ? go<KIND, 128, 8>(t, st) : go<KIND, 128, 16>(t, st);
+}
 cudaError_t run_token(TokenArgs& t, bool bf16, cudaStream_t st) {
-  const bool small = t.w.d <= 64;
-  if (t.table) {
-    if (bf16) return small ? go<TK_E4M3, 64>(t, st) : go<TK_E4M3, 128>(t, st);
-    return small ? go<TK_E4M3_F32, 64>(t, st) : go<TK_E4M3_F32, 128>(t, st);
-  }
-  if (bf16) return small ? go<TK_BF16, 64>(t, st) : go<TK_BF16, 128>(t, st);
-  return small ? go<TK_F32, 64>(t, st) : go<TK_F32, 128>(t, st);
+  if (t.table) return bf16 ? go_kind<TK_E4M3>(t, st) : go_kind<TK_E4M3_F32>(t, st);
+  return bf16 ? go_kind<TK_BF16>(t, st) : go_kind<TK_F32>(t, st);
 }
 
 }  // namespace lapnys
