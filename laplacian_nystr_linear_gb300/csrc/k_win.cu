@@ -1,19 +1,24 @@
-// Windowed softmax attention of fp32 tensors on the FP32 pipe (visibility rule:
-// win.cuh): forward, query gradients, key and value gradients.
+// Windowed softmax attention of fp32 tensors (visibility rule: win.cuh): forward,
+// query gradients, key and value gradients.
 //
 //   s = scale q.k over the visible keys, P = softmax(s), o = P v
 //   D = dout.o, dV = P^T dout, dP = dout V^T, dS = P (dP - D),
 //   dQ = scale dS K, dK = scale dS^T Q  (both summed over a group's query heads)
 //
 // One pass over the keys with the running maximum and sum of each row's softmax;
-// the backward recomputes P from the saved log-sum.  Tiles of 64 queries x 64
-// keys, 256 threads as 16 x 16, each thread 4 x 4 scores and 4 rows x DP / 16
-// columns of the outputs in registers; operand tiles in padded shared memory.
-// Rows of one tile belong to one half-warp, so P goes through shared memory
-// with a warp barrier only.  Bound by the FP32 pipe: 4 d (forward) and 14 d
-// (backward, scores recomputed in both kernels) operations per visible pair; by its
-// latency where there are few tiles (196 tokens, one head of 32: 32, 35 and 47 us for 4
-// blocks of one to two steps, beside 100 us and more of the host's work for the call).
+// the backward recomputes P from the saved log-sum.  Products on the warp-level
+// tensor instruction: every operand is three bf16 parts (24 bits) and a product the
+// six of their products above 2^-24 (98 TFLOP/s at the instruction's measured rate;
+// the FP32 pipe, with operands from shared memory, gave 25 to 30).  The
+// instruction's own sums run over one tile only; tiles are added up by the FP32 pipe.
+//
+// Tiles of 64 rows (queries; keys for dK, dV) x 64 columns, 8 warps: 16 rows and one
+// half of the columns each, so a warp's softmax and sums are its own and the halves
+// meet once, at the end.  Tiles are split when they are loaded, as three planes of
+// shared memory whose 16-byte chunks are XORed with the row (ldmatrix without bank
+// conflicts, plain or transposed); P and dS are split in registers.
+// Bound by the tensor instruction (4 d operations forward, 14 d backward for each
+// visible pair, times six); by its latency where there are few tiles.
 #include "common.cuh"
 #include "internal.h"
 #include "win.cuh"
@@ -21,252 +26,360 @@
 namespace lapnys {
 
 namespace {
-constexpr int WT = 64;        // queries and keys of a tile
-constexpr int WPS = WT + 4;   // row stride of the P tiles
+constexpr int WT = 64;        // rows and columns of a tile
 
-// rows [r0, r1) (r1 - r0 <= 64) of a row-major [..][d] matrix into a padded
-// tile of 64 rows x DP columns, zeros elsewhere
 template <int DP>
-__device__ __forceinline__ void win_load(float* s, const float* g, int d, int r0, int r1) {
-  constexpr int C4 = DP / 4;
-  for (int id = threadIdx.x; id < WT * C4; id += kThreads) {
-    const int r = id / C4, c = (id % C4) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < r1 && c < d) v = ld4(g + (size_t)(r0 + r) * d + c);
-    st4(s + r * row_stride(DP) + c, v);
-  }
+struct Planes {
+  static constexpr int RB = 2 * DP, PL = WT * RB;   // bytes of a row, of a plane
+  static constexpr int BYTES = 3 * PL;
+};
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int c) {
+  return tile + row * Planes<DP>::RB + ((c ^ (row & 7)) << 4);
 }
 
-// s[r][c] = X[4 ty + r] . Y[tx + 16 c]
+// rows [r0, r1) (r1 - r0 <= 64) of a row-major [..][d] matrix as a tile of 64 rows x DP
+// features in three planes, zeros elsewhere
 template <int DP>
-__device__ __forceinline__ void win_dot(const float* Xs, const float* Ys, int ty, int tx,
-                                        float (&s)[4][4]) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
-#pragma unroll 4
-  for (int e = 0; e < DP; e += 4) {
-    float4 x[4], y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = lds4(Xs + (4 * ty + r) * row_stride(DP) + e);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = lds4(Ys + (tx + 16 * c) * row_stride(DP) + e);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s[r][c] = fmaf(x[r].x, y[c].x, s[r][c]);
-        s[r][c] = fmaf(x[r].y, y[c].y, s[r][c]);
-        s[r][c] = fmaf(x[r].z, y[c].z, s[r][c]);
-        s[r][c] = fmaf(x[r].w, y[c].w, s[r][c]);
-      }
-  }
-}
-
-// o[r][..] += sum_j P[4 ty + r][j] Y[j][..]; thread tx owns columns 4 tx + 64 u
-template <int DP>
-__device__ __forceinline__ void win_acc(const float* Ps, const float* Ys, int ty, int tx,
-                                        float4 (&o)[4][DP / 64]) {
+__device__ __forceinline__ void load_planes(uint32_t tile, const float* g, int d, int r0, int r1) {
+  constexpr int C8 = DP / 8;
 #pragma unroll 2
-  for (int j = 0; j < WT; j += 4) {
-    float4 p[4];
+  for (int id = threadIdx.x; id < WT * C8; id += kThreads) {
+    const int r = id / C8, c = id % C8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (r0 + r < r1 && 8 * c < d) {
+      const float* p = g + (size_t)(r0 + r) * d + 8 * c;
+      x = ld4(p);
+      y = ld4(p + 4);
+    }
+    uint32_t w[4][3];
+    split3_bf16x2(x.x, x.y, w[0]);
+    split3_bf16x2(x.z, x.w, w[1]);
+    split3_bf16x2(y.x, y.y, w[2]);
+    split3_bf16x2(y.z, y.w, w[3]);
+    const uint32_t at = chunk_at<DP>(tile, r, c);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) p[r] = lds4(Ps + (4 * ty + r) * WPS + j);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int u = 0; u < DP / 64; ++u) {
-        const float4 y = lds4(Ys + (j + e) * row_stride(DP) + 4 * tx + 64 * u);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w = comp(p[r], e);
-          o[r][u].x = fmaf(w, y.x, o[r][u].x);
-          o[r][u].y = fmaf(w, y.y, o[r][u].y);
-          o[r][u].z = fmaf(w, y.z, o[r][u].z);
-          o[r][u].w = fmaf(w, y.w, o[r][u].w);
-        }
-      }
+    for (int q = 0; q < 3; ++q)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + q * Planes<DP>::PL),
+                   "r"(w[0][q]), "r"(w[1][q]), "r"(w[2][q]), "r"(w[3][q])
+                   : "memory");
   }
 }
 
-// sum or maximum over the 16 threads of a row
-__device__ __forceinline__ float row_max(float v) {
+__device__ __forceinline__ void ldm(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldm_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two neighbouring tiles of 8 columns: the six products, the smallest first
+__device__ __forceinline__ void six(float (&s)[4], float (&t)[4], const uint32_t (&a)[3][4],
+                                    const uint32_t (&b)[3][4]) {
 #pragma unroll
-  for (int k = 8; k; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
-  return v;
+  for (int x = 2; x >= 0; --x)
+#pragma unroll
+    for (int y = 0; y <= x; ++y) {
+      mma(s, a[y], b[x - y][0], b[x - y][1]);
+      mma(t, a[y], b[x - y][2], b[x - y][3]);
+    }
+}
+
+// s = rows [r0, r0 + 16) of X times rows [c0, c0 + 32) of Y, over d features: value
+// [n][2 h + e] is row r0 + lane / 4 + 8 h, column c0 + 8 n + 2 (lane % 4) + e
+template <int DP>
+__device__ __forceinline__ void dot_rows(uint32_t X, uint32_t Y, int d, int r0, int c0, float (&s)[4][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < d / 16; ++k) {
+    uint32_t x[3][4];
+    const uint32_t at = chunk_at<DP>(X, r0 + (lane & 15), 2 * k + (lane >> 4));
+#pragma unroll
+    for (int q = 0; q < 3; ++q) ldm(x[q], at + q * Planes<DP>::PL);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t y[3][4];
+      const uint32_t by = chunk_at<DP>(Y, c0 + 16 * n + (lane & 7) + 8 * (lane >> 4), 2 * k + (lane >> 3 & 1));
+#pragma unroll
+      for (int q = 0; q < 3; ++q) ldm(y[q], by + q * Planes<DP>::PL);
+      six(s[2 * n], s[2 * n + 1], x, y);
+    }
+  }
+}
+
+// values of dot_rows' layout as the left operand of add_rows
+__device__ __forceinline__ void as_left(const float (&p)[4][4], uint32_t (&w)[2][3][4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t u[3];
+      split3_bf16x2(p[2 * k + (e >> 1)][2 * (e & 1)], p[2 * k + (e >> 1)][2 * (e & 1) + 1], u);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) w[k][q][e] = u[q];
+    }
+}
+// o = f o + W Y: W 16 x 32, Y rows [c0, c0 + 32); [n] is 8 features in dot_rows' layout
+template <int DP>
+__device__ __forceinline__ void add_rows(const uint32_t (&w)[2][3][4], uint32_t Y, int d, int c0,
+                                         const float (&f)[2], float (&o)[DP / 8][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < DP / 16; ++n) {
+    if (16 * n >= d) break;
+    float t[2][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e >> 2][e & 3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t y[3][4];
+      const uint32_t at = chunk_at<DP>(Y, c0 + 16 * k + (lane & 15), 2 * n + (lane >> 4));
+#pragma unroll
+      for (int q = 0; q < 3; ++q) ldm_t(y[q], at + q * Planes<DP>::PL);
+      six(t[0], t[1], w[k], y);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[2 * n + (e >> 2)][e & 3] = fmaf(o[2 * n + (e >> 2)][e & 3], f[e >> 1 & 1], t[e >> 2][e & 3]);
+  }
+}
+
+// maximum or sum over the four threads of a row
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 __device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// One half's 16 x DP sums to shared memory for the other's warp of the same rows, and
+// from there: rows of DP + 8 floats, a warp's 16 rows from `at` on
+template <int DP>
+__device__ __forceinline__ void give(float* at, const float (&o)[DP / 8][4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 8; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-  return v;
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2*>(at + ((lane >> 2) + 8 * h) * (DP + 8) + 8 * n + 2 * (lane & 3)) =
+          make_float2(o[n][2 * h], o[n][2 * h + 1]);
+}
+// o = f o + g what was given
+template <int DP>
+__device__ __forceinline__ void take(const float* at, const float (&f)[2], const float (&g)[2],
+                                     float (&o)[DP / 8][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = *reinterpret_cast<const float2*>(at + ((lane >> 2) + 8 * h) * (DP + 8) + 8 * n + 2 * (lane & 3));
+      o[n][2 * h] = fmaf(x.x, g[h], o[n][2 * h] * f[h]);
+      o[n][2 * h + 1] = fmaf(x.y, g[h], o[n][2 * h + 1] * f[h]);
+    }
+}
+// a row's share of o, times w, to memory
+template <int DP>
+__device__ __forceinline__ void put_row(float* dst, int d, int h, float w, const float (&o)[DP / 8][4]) {
+  const int tq = threadIdx.x & 3;
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+    if (8 * n < d)
+      *reinterpret_cast<float2*>(dst + 8 * n + 2 * tq) = make_float2(o[n][2 * h] * w, o[n][2 * h + 1] * w);
 }
 }  // namespace
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_fwd(WinArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  float* Qs = sm;
-  float* Ks = Qs + WT * row_stride(DP);
-  float* Vs = Ks + WT * row_stride(DP);
-  float* Ps = Vs + WT * row_stride(DP);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  extern __shared__ __align__(128) uint8_t smw[];
+  using T = Planes<DP>;
+  const uint32_t Q = smem_addr(smw), K = Q + T::BYTES, V = K + T::BYTES;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tq = lane & 3;
+  const int r0 = 16 * (warp & 3), half = warp >> 2, c0 = 32 * half;
   const int qt = (a.Nq + WT - 1) / WT;
   const int h = (blockIdx.x / qt) % a.Hq, b = (blockIdx.x / qt) / a.Hq;
   const int i0 = (blockIdx.x % qt) * WT, i1 = min(a.Nq, i0 + WT);
   const WinSeq sq = win_seq(a, b);
   const WinRange kr = win_keys(a, sq, i0, i1);
   const size_t kv0 = ((size_t)b * a.Hkv + h / a.g) * a.Nk * a.d;
-  const float* K = (const float*)a.k + kv0;
-  const float* V = (const float*)a.v + kv0;
   const size_t q0 = ((size_t)b * a.Hq + h) * a.Nq;
-  win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i0, i1);
+  load_planes<DP>(Q, (const float*)a.q + q0 * a.d, a.d, i0, i1);
 
-  WinRow row[4];
-  float m[4], l[4];
-  float4 o[4][DP / 64];
+  WinRow row[2];
+  float m[2], l[2];
+  float o[DP / 8][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    row[r] = win_row(a, sq, i0 + 4 * ty + r);
+  for (int r = 0; r < 2; ++r) {
+    row[r] = win_row(a, sq, i0 + r0 + gid + 8 * r);
     m[r] = -INFINITY;
     l[r] = 0.f;
-#pragma unroll
-    for (int u = 0; u < DP / 64; ++u) o[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   for (int seg = 0; seg < 2; ++seg) {
     const int jb = seg ? kr.lo : 0, je = seg ? kr.hi : kr.S;
     for (int j0 = jb; j0 < je; j0 += WT) {
       __syncthreads();
-      win_load<DP>(Ks, K, a.d, j0, min(je, j0 + WT));
-      win_load<DP>(Vs, V, a.d, j0, min(je, j0 + WT));
+      load_planes<DP>(K, (const float*)a.k + kv0, a.d, j0, min(je, j0 + WT));
+      load_planes<DP>(V, (const float*)a.v + kv0, a.d, j0, min(je, j0 + WT));
       __syncthreads();
-      float s[4][4];
-      win_dot<DP>(Qs, Ks, ty, tx, s);
+      if (j0 + c0 >= je) continue;
+      float s[4][4], f[2];
+      dot_rows<DP>(Q, K, a.d, r0, c0, s);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 2; ++r) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j = j0 + tx + 16 * c;
-          s[r][c] = j < je && win_sees(row[r], j) ? s[r][c] * a.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[r][c]);
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + c0 + 8 * (e >> 1) + 2 * tq + (e & 1);
+          float& x = s[e >> 1][2 * r + (e & 1)];
+          x = j < je && win_sees(row[r], j) ? x * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, x);
         }
         mx = fmaxf(m[r], row_max(mx));
         const float mu = mx == -INFINITY ? 0.f : mx;
-        const float f = exp2f(m[r] - mu);
+        f[r] = exp2f(m[r] - mu);
         m[r] = mx;
         float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float p = exp2f(s[r][c] - mu);
-          sum += p;
-          Ps[(4 * ty + r) * WPS + tx + 16 * c] = p;
+        for (int e = 0; e < 8; ++e) {
+          float& x = s[e >> 1][2 * r + (e & 1)];
+          x = exp2f(x - mu);
+          sum += x;
         }
-        l[r] = l[r] * f + row_sum(sum);
-#pragma unroll
-        for (int u = 0; u < DP / 64; ++u) {
-          o[r][u].x *= f; o[r][u].y *= f; o[r][u].z *= f; o[r][u].w *= f;
-        }
+        l[r] = l[r] * f[r] + row_sum(sum);
       }
-      __syncwarp();
-      win_acc<DP>(Ps, Vs, ty, tx, o);
+      uint32_t w[2][3][4];
+      as_left(s, w);
+      add_rows<DP>(w, V, a.d, c0, f, o);
     }
   }
+  __syncthreads();
+  // the halves' sums, over the same maximum
+  float* buf = reinterpret_cast<float*>(smw) + r0 * (DP + 8);
+  float2* ml = reinterpret_cast<float2*>(reinterpret_cast<float*>(smw) + WT * (DP + 8)) + r0;
+  if (half) {
+    give<DP>(buf, o);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = i0 + 4 * ty + r;
+    for (int r = 0; r < 2; ++r)
+      if (tq == 0) ml[gid + 8 * r] = make_float2(m[r], l[r]);
+  }
+  __syncthreads();
+  if (half) return;
+  float f[2], g[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float2 x = ml[gid + 8 * r];
+    const float mx = fmaxf(m[r], x.x), mu = mx == -INFINITY ? 0.f : mx;
+    f[r] = exp2f(m[r] - mu);
+    g[r] = exp2f(x.x - mu);
+    l[r] = fmaf(l[r], f[r], x.y * g[r]);
+    m[r] = mx;
+  }
+  take<DP>(buf, f, g, o);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = i0 + r0 + gid + 8 * r;
     if (i >= i1) continue;
     const float w = l[r] > 0.f ? 1.f / l[r] : (l[r] == 0.f ? 0.f : l[r]);
-    if (a.lse && tx == 0) a.lse[q0 + i] = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
-#pragma unroll
-    for (int u = 0; u < DP / 64; ++u) {
-      const int c = 4 * tx + 64 * u;
-      if (c < a.d)
-        st4((float*)a.out + (q0 + i) * a.d + c,
-            make_float4(o[r][u].x * w, o[r][u].y * w, o[r][u].z * w, o[r][u].w * w));
-    }
+    if (a.lse && tq == 0) a.lse[q0 + i] = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
+    put_row<DP>((float*)a.out + (q0 + i) * a.d, a.d, r, w, o);
   }
 }
 
 // dQ of one tile of queries, and D = dout.o of its rows for the kernel below
 template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  float* Qs = sm;
-  float* Os = Qs + WT * row_stride(DP);
-  float* Ks = Os + WT * row_stride(DP);
-  float* Vs = Ks + WT * row_stride(DP);
-  float* Ps = Vs + WT * row_stride(DP);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  extern __shared__ __align__(128) uint8_t smw[];
+  using T = Planes<DP>;
+  const uint32_t Q = smem_addr(smw), O = Q + T::BYTES, K = O + T::BYTES, V = K + T::BYTES;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tq = lane & 3;
+  const int r0 = 16 * (warp & 3), half = warp >> 2, c0 = 32 * half;
   const int qt = (a.Nq + WT - 1) / WT;
   const int h = (blockIdx.x / qt) % a.Hq, b = (blockIdx.x / qt) / a.Hq;
   const int i0 = (blockIdx.x % qt) * WT, i1 = min(a.Nq, i0 + WT);
   const WinSeq sq = win_seq(a, b);
   const WinRange kr = win_keys(a, sq, i0, i1);
   const size_t kv0 = ((size_t)b * a.Hkv + h / a.g) * a.Nk * a.d;
-  const float* K = (const float*)a.k + kv0;
-  const float* V = (const float*)a.v + kv0;
   const size_t q0 = ((size_t)b * a.Hq + h) * a.Nq;
-  win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i0, i1);
-  win_load<DP>(Os, (const float*)a.dout + q0 * a.d, a.d, i0, i1);
+  load_planes<DP>(Q, (const float*)a.q + q0 * a.d, a.d, i0, i1);
+  load_planes<DP>(O, (const float*)a.dout + q0 * a.d, a.d, i0, i1);
 
-  WinRow row[4];
-  float ls[4], D[4];
-  float4 o[4][DP / 64];
+  WinRow row[2];
+  float ls[2], D[2];
+  float o[DP / 8][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = i0 + 4 * ty + r;
+  for (int r = 0; r < 2; ++r) {
+    const int i = i0 + r0 + gid + 8 * r;
     row[r] = win_row(a, sq, i);
     ls[r] = i < i1 ? a.lse[q0 + i] : 0.f;
     float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < DP / 64; ++u) {
-      o[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int c = 4 * tx + 64 * u;
-      if (i < i1 && c < a.d) {
-        const float4 x = ld4((const float*)a.dout + (q0 + i) * a.d + c);
-        const float4 y = ld4((const float*)a.out + (q0 + i) * a.d + c);
-        s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
-      }
+    for (int c = 4 * tq; i < i1 && c < a.d; c += 16) {
+      const float4 x = ld4((const float*)a.dout + (q0 + i) * a.d + c);
+      const float4 y = ld4((const float*)a.out + (q0 + i) * a.d + c);
+      s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
     }
     D[r] = row_sum(s);
-    if (tx == 0 && i < i1) a.D[q0 + i] = D[r];
+    if (half == 0 && tq == 0 && i < i1) a.D[q0 + i] = D[r];
   }
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  const float one[2] = {1.f, 1.f};
   for (int seg = 0; seg < 2; ++seg) {
     const int jb = seg ? kr.lo : 0, je = seg ? kr.hi : kr.S;
     for (int j0 = jb; j0 < je; j0 += WT) {
       __syncthreads();
-      win_load<DP>(Ks, K, a.d, j0, min(je, j0 + WT));
-      win_load<DP>(Vs, V, a.d, j0, min(je, j0 + WT));
+      load_planes<DP>(K, (const float*)a.k + kv0, a.d, j0, min(je, j0 + WT));
+      load_planes<DP>(V, (const float*)a.v + kv0, a.d, j0, min(je, j0 + WT));
       __syncthreads();
+      if (j0 + c0 >= je) continue;
       float s[4][4], dp[4][4];
-      win_dot<DP>(Qs, Ks, ty, tx, s);
-      win_dot<DP>(Os, Vs, ty, tx, dp);
+      dot_rows<DP>(Q, K, a.d, r0, c0, s);
+      dot_rows<DP>(O, V, a.d, r0, c0, dp);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int j = j0 + tx + 16 * c;
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, j = j0 + c0 + 8 * n + 2 * tq + (e & 1);
           const bool see = j < je && win_sees(row[r], j);
-          Ps[(4 * ty + r) * WPS + tx + 16 * c] =
-              see ? exp2f(fmaf(s[r][c], a.scale_log2, -ls[r])) * (dp[r][c] - D[r]) : 0.f;
+          s[n][e] = see ? exp2f(fmaf(s[n][e], a.scale_log2, -ls[r])) * (dp[n][e] - D[r]) : 0.f;
         }
-      __syncwarp();
-      win_acc<DP>(Ps, Ks, ty, tx, o);
+      uint32_t w[2][3][4];
+      as_left(s, w);
+      add_rows<DP>(w, K, a.d, c0, one, o);
     }
   }
+  __syncthreads();
+  float* buf = reinterpret_cast<float*>(smw) + r0 * (DP + 8);
+  if (half) give<DP>(buf, o);
+  __syncthreads();
+  if (half) return;
+  take<DP>(buf, one, one, o);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = i0 + 4 * ty + r;
-    if (i >= i1) continue;
-#pragma unroll
-    for (int u = 0; u < DP / 64; ++u) {
-      const int c = 4 * tx + 64 * u;
-      if (c < a.d)
-        st4((float*)a.dq + (q0 + i) * a.d + c,
-            make_float4(o[r][u].x * a.scale, o[r][u].y * a.scale, o[r][u].z * a.scale,
-                        o[r][u].w * a.scale));
-    }
+  for (int r = 0; r < 2; ++r) {
+    const int i = i0 + r0 + gid + 8 * r;
+    if (i < i1) put_row<DP>((float*)a.dq + (q0 + i) * a.d, a.d, r, a.scale, o);
   }
 }
 
@@ -276,16 +389,13 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
 // fp32 partials k_win_join adds in their order.
 template <int DP>
 __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  float* Ks = sm;
-  float* Vs = Ks + WT * row_stride(DP);
-  float* Qs = Vs + WT * row_stride(DP);
-  float* Os = Qs + WT * row_stride(DP);
-  float* Ps = Os + WT * row_stride(DP);
-  float* Ss = Ps + WT * WPS;
-  float* Ls = Ss + WT * WPS;   // log-sum and D of the tile's queries
+  extern __shared__ __align__(128) uint8_t smw[];
+  using T = Planes<DP>;
+  const uint32_t K = smem_addr(smw), V = K + T::BYTES, Q = V + T::BYTES, O = Q + T::BYTES;
+  float* Ls = reinterpret_cast<float*>(smw + 4 * T::BYTES);   // log-sum and D of the tile's queries
   float* Ds = Ls + WT;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tq = lane & 3;
+  const int r0 = 16 * (warp & 3), half = warp >> 2, c0 = 32 * half;
   const int kt = (a.Nk + WT - 1) / WT, items = a.stiles * a.chunks + kt - a.stiles;
   const int it = blockIdx.x % items, hk = (blockIdx.x / items) % a.Hkv, b = (blockIdx.x / items) / a.Hkv;
   const bool first = it < a.stiles * a.chunks;
@@ -301,67 +411,84 @@ __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
     i1 = min(i1, (c + 1) * a.chunk_rows);
   }
   const size_t kv0 = ((size_t)b * a.Hkv + hk) * a.Nk;
-  win_load<DP>(Ks, (const float*)a.k + kv0 * a.d, a.d, j0, j1);
-  win_load<DP>(Vs, (const float*)a.v + kv0 * a.d, a.d, j0, j1);
-  float4 dk[4][DP / 64], dv[4][DP / 64];
+  load_planes<DP>(K, (const float*)a.k + kv0 * a.d, a.d, j0, j1);
+  load_planes<DP>(V, (const float*)a.v + kv0 * a.d, a.d, j0, j1);
+  float dk[DP / 8][4], dv[DP / 8][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-    for (int u = 0; u < DP / 64; ++u) dk[r][u] = dv[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < 4; ++e) dk[n][e] = dv[n][e] = 0.f;
+  const float one[2] = {1.f, 1.f};
   for (int e = 0; e < a.g; ++e) {
     const size_t q0 = ((size_t)b * a.Hq + hk * a.g + e) * a.Nq;
     for (int i = i0; i < i1; i += WT) {
       const int ie = min(i1, i + WT);
       __syncthreads();
-      win_load<DP>(Qs, (const float*)a.q + q0 * a.d, a.d, i, ie);
-      win_load<DP>(Os, (const float*)a.dout + q0 * a.d, a.d, i, ie);
+      load_planes<DP>(Q, (const float*)a.q + q0 * a.d, a.d, i, ie);
+      load_planes<DP>(O, (const float*)a.dout + q0 * a.d, a.d, i, ie);
       if (tid < WT) {
         Ls[tid] = i + tid < ie ? a.lse[q0 + i + tid] : 0.f;
         Ds[tid] = i + tid < ie ? a.D[q0 + i + tid] : 0.f;
       }
       __syncthreads();
+      if (i + c0 >= ie) continue;
       float s[4][4], dp[4][4];
-      win_dot<DP>(Ks, Qs, ty, tx, s);
-      win_dot<DP>(Vs, Os, ty, tx, dp);
+      dot_rows<DP>(K, Q, a.d, r0, c0, s);
+      uint32_t seen = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int ii = tx + 16 * c;
-        WinRow row = win_row(a, sq, i + ii);
-        if (i + ii >= ie) row = WinRow{0, 0, 0};
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = j0 + 4 * ty + r;
-          const float p =
-              j < j1 && win_sees(row, j) ? exp2f(fmaf(s[r][c], a.scale_log2, -Ls[ii])) : 0.f;
-          Ps[(4 * ty + r) * WPS + ii] = p;
-          Ss[(4 * ty + r) * WPS + ii] = p != 0.f ? p * (dp[r][c] - Ds[ii]) : 0.f;
+        for (int c = 0; c < 2; ++c) {
+          const int ii = c0 + 8 * n + 2 * tq + c;
+          const WinRow row = i + ii < ie ? win_row(a, sq, i + ii) : WinRow{0, 0, 0};
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = j0 + r0 + gid + 8 * r;
+            const bool see = j < j1 && win_sees(row, j);
+            seen |= (uint32_t)see << (4 * n + 2 * r + c);
+            s[n][2 * r + c] = see ? exp2f(fmaf(s[n][2 * r + c], a.scale_log2, -Ls[ii])) : 0.f;
+          }
         }
-      }
-      __syncwarp();
-      win_acc<DP>(Ps, Os, ty, tx, dv);
-      win_acc<DP>(Ss, Qs, ty, tx, dk);
+      uint32_t w[2][3][4];
+      as_left(s, w);
+      add_rows<DP>(w, O, a.d, c0, one, dv);
+      dot_rows<DP>(V, O, a.d, r0, c0, dp);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          s[n][x] = seen >> (4 * n + x) & 1u ? s[n][x] * (dp[n][x] - Ds[c0 + 8 * n + 2 * tq + (x & 1)]) : 0.f;
+      as_left(s, w);
+      add_rows<DP>(w, Q, a.d, c0, one, dk);
     }
   }
+  __syncthreads();
+  // dK is put together by the first half's warps, dV by the other's
+  float* mine = reinterpret_cast<float*>(smw) + (size_t)(WT * half + r0) * (DP + 8);
+  float* other = reinterpret_cast<float*>(smw) + (size_t)(WT * (1 - half) + r0) * (DP + 8);
+  if (half)
+    give<DP>(other, dk);
+  else
+    give<DP>(other, dv);
+  __syncthreads();
+  float* part = first ? a.part + ((((size_t)b * a.Hkv + hk) * a.stiles + tile) * a.chunks + it % a.chunks) *
+                                     2 * WT * a.d
+                      : nullptr;
+  auto put = [&](float (&g)[DP / 8][4], float* grad, float* to, float f) {
+    take<DP>(mine, one, one, g);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = 4 * ty + r, j = j0 + row;
-#pragma unroll
-    for (int u = 0; u < DP / 64; ++u) {
-      const int c = 4 * tx + 64 * u;
-      if (c >= a.d) continue;
-      const float4 x = make_float4(dk[r][u].x * a.scale, dk[r][u].y * a.scale,
-                                   dk[r][u].z * a.scale, dk[r][u].w * a.scale);
-      if (first) {
-        float* p = a.part + (((((size_t)b * a.Hkv + hk) * a.stiles + tile) * a.chunks +
-                              it % a.chunks) * 2 * WT + row) * a.d + c;
-        st4(p, x);
-        st4(p + (size_t)WT * a.d, dv[r][u]);
-      } else if (j < a.Nk) {
-        st4((float*)a.dk + (kv0 + j) * a.d + c, x);
-        st4((float*)a.dv + (kv0 + j) * a.d + c, dv[r][u]);
-      }
+    for (int r = 0; r < 2; ++r) {
+      const int k = r0 + gid + 8 * r;
+      if (first)
+        put_row<DP>(to + (size_t)k * a.d, a.d, r, f, g);
+      else if (j0 + k < a.Nk)
+        put_row<DP>(grad + (kv0 + j0 + k) * a.d, a.d, r, f, g);
     }
-  }
+  };
+  if (half)
+    put(dv, (float*)a.dv, part + (size_t)WT * a.d, 1.f);
+  else
+    put(dk, (float*)a.dk, part, a.scale);
 }
 
 // dK and dV of the tiles that hold first tokens: the chunks' partials, added in
@@ -393,7 +520,8 @@ __global__ void __launch_bounds__(256) k_win_join(WinArgs a, int tile_rows) {
 namespace {
 template <int DP>
 cudaError_t fwd_t(const WinArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(3 * WT * row_stride(DP) + WT * WPS) * 4;
+  constexpr size_t smem = 3 * Planes<DP>::BYTES;
+  static_assert(smem >= (WT * (DP + 8) + 2 * WT) * 4);
   static SmemOnce once;
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
@@ -403,8 +531,8 @@ cudaError_t fwd_t(const WinArgs& a, cudaStream_t st) {
 }
 template <int DP>
 cudaError_t bwd_t(const WinArgs& a, cudaStream_t st) {
-  const size_t sq = (size_t)(4 * WT * row_stride(DP) + WT * WPS) * 4;
-  const size_t sk = (size_t)(4 * WT * row_stride(DP) + 2 * WT * WPS + 2 * WT) * 4;
+  constexpr size_t sq = 4 * Planes<DP>::BYTES, sk = sq + 2 * WT * 4;
+  static_assert(sq >= 2 * WT * (DP + 8) * 4);
   static SmemOnce once_q, once_kv;
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
