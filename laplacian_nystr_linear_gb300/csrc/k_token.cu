@@ -39,6 +39,8 @@
 //   - bf16: q, k, v as they are, p rounded to bf16 (2^-9, below the rounding of
 //     the output; sums, maxima and outputs are fp32 throughout).
 //   - fp32: all operands in three bf16 parts, six products (2^-24 each).
+//   With fp32 queries the products of 16 keys are added up by the FP32 pipe: the
+//   instruction's own sums are cut off, which 3000 keys a warp made 2e-5 of the output.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -511,9 +513,19 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
     for (int u = 0; u < NS; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+    // fp32 queries: the instruction cuts its sums off instead of rounding them, so it
+    // sums up to 8 products and the FP32 pipe adds those up
+    float part[NS][4];
+    float (*acc)[4] = NP > 1 ? part : s;
 #pragma unroll
     for (int i = 0; i < DP / 4 / PIECE; ++i) {
       uint32_t w[NU][4];
+      if constexpr (NP > 1) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[u][e] = 0.f;
+      }
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         const uint4 kv = *reinterpret_cast<const uint4*>(Kt + tile_off<RB, GK>(8 * u + gid, key_chunk<RB>(tq, i)));
@@ -534,13 +546,13 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
 #pragma unroll
               for (int y = 0; y <= x; ++y) {
                 const uint32_t k4[4] = {p[0][x - y], p[1][x - y], p[2][x - y], p[3][x - y]};
-                mma_bf(s[h], k4, qf[y][i][0], qf[y][i][1]);
+                mma_bf(acc[h], k4, qf[y][i][0], qf[y][i][1]);
               }
           } else if constexpr (KIND == TK_BF16) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t k4[4] = {lo[2 * x], hi[2 * x], lo[2 * x + 1], hi[2 * x + 1]};
-              mma_bf(s[h], k4, qf[0][2 * i + x][0], qf[0][2 * i + x][1]);
+              mma_bf(acc[h], k4, qf[0][2 * i + x][0], qf[0][2 * i + x][1]);
             }
           } else {
 #pragma unroll
@@ -548,7 +560,7 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
               const uint32_t k4[4] = {e4m3x2_f16(lo[x]), e4m3x2_f16(hi[x]), e4m3x2_f16(lo[x] >> 16),
                                       e4m3x2_f16(hi[x] >> 16)};
 #pragma unroll
-              for (int p = NP - 1; p >= 0; --p) mma_f16(s[h], k4, qf[p][4 * i + x][0], qf[p][4 * i + x][1]);
+              for (int p = NP - 1; p >= 0; --p) mma_f16(acc[h], k4, qf[p][4 * i + x][0], qf[p][4 * i + x][1]);
             }
           }
         }
@@ -561,13 +573,13 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
 #pragma unroll
           for (int x = 2; x >= 0; --x)
 #pragma unroll
-            for (int y = 0; y <= x; ++y) mma_bf(s[u], qf[y][i], p0[x - y], p1[x - y]);
+            for (int y = 0; y <= x; ++y) mma_bf(acc[u], qf[y][i], p0[x - y], p1[x - y]);
         }
       } else if constexpr (KIND == TK_BF16) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int u = 0; u < NU; ++u) mma_bf(s[u], qf[0][2 * i + x], w[u][2 * x], w[u][2 * x + 1]);
+          for (int u = 0; u < NU; ++u) mma_bf(acc[u], qf[0][2 * i + x], w[u][2 * x], w[u][2 * x + 1]);
       } else {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -575,8 +587,14 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
           for (int u = 0; u < NU; ++u) {
             const uint32_t b0 = e4m3x2_f16(w[u][x]), b1 = e4m3x2_f16(w[u][x] >> 16);
 #pragma unroll
-            for (int p = NP - 1; p >= 0; --p) mma_f16(s[u], qf[p][4 * i + x], b0, b1);
+            for (int p = NP - 1; p >= 0; --p) mma_f16(acc[u], qf[p][4 * i + x], b0, b1);
           }
+      }
+      if constexpr (NP > 1) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][e] += part[u][e];
       }
     }
     // ---- softmax, running maximum and sum ----
@@ -696,6 +714,19 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
       }
     };
     constexpr int OS = FEW ? 2 : 1;        // features of an o[n]
+    // o += what `sum` adds to zeros (fp32 queries), or sum(o)
+    const auto into = [&](float (*acc)[4], auto sum) {
+      if constexpr (NP > 1) {
+        float part[2][4] = {};
+        sum(part);
+#pragma unroll
+        for (int i = 0; i < 2 / OS; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] += part[i][e];
+      } else {
+        sum(acc);
+      }
+    };
 #pragma unroll
     for (int g = 0; g < NU / 2; ++g) {     // 16 keys each
       if constexpr (X::F16) {
@@ -719,8 +750,10 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
           const uint32_t b1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], sel));
           const uint32_t c0 = e4m3x2_f16(__byte_perm(v[0][n >> 2], v[1][n >> 2], nxt));
           const uint32_t c1 = e4m3x2_f16(__byte_perm(v[2][n >> 2], v[3][n >> 2], nxt));
+          into(&o[n / OS], [&](float (*to)[4]) {
 #pragma unroll
-          for (int x = NP - 1; x >= 0; --x) add(&o[n / OS], x, g, b0, b1, c0, c1);
+            for (int x = NP - 1; x >= 0; --x) add(to, x, g, b0, b1, c0, c1);
+          });
         }
       } else if constexpr (KIND == TK_BF16) {
 #pragma unroll
@@ -756,11 +789,12 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
             split3_bf16x2(v[2][n], v[3][n], b1);
             split3_bf16x2(v[0][n + 1], v[1][n + 1], c0);
             split3_bf16x2(v[2][n + 1], v[3][n + 1], c1);
+            into(&o[(4 * h + n) / OS], [&](float (*to)[4]) {
 #pragma unroll
-            for (int x = 2; x >= 0; --x)
+              for (int x = 2; x >= 0; --x)
 #pragma unroll
-              for (int y = 0; y <= x; ++y)
-                add(&o[(4 * h + n) / OS], y, g, b0[x - y], b1[x - y], c0[x - y], c1[x - y]);
+                for (int y = 0; y <= x; ++y) add(to, y, g, b0[x - y], b1[x - y], c0[x - y], c1[x - y]);
+            });
           }
         }
       }

@@ -233,6 +233,21 @@ def test_guarded_outputs_and_repeatability():
             assert torch.equal(x, y)
 
 
+def test_long_sums_of_fp32():
+    """One query over 2.9 M keys: its parts add up some 300 groups of 16 keys each, the parts (of 608
+    warps, four at a time) some 150.  Sums rounded to nearest walk at random: with n = 450 steps of
+    numerator and of denominator, each off by 2^-24 at most (uniform: a third of its square), four
+    standard deviations are below 4 sqrt(2 n) 2^-24.  Sums that are cut off drift by n 2^-24 and more."""
+    n, d = 608 * 16 * 300, 16
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.rand(s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = r(1, 1, 1, d) - 0.5, r(1, 1, n, d), 1 + r(1, 1, n, d)
+    out = lap.window_attention(q, k, v, -1)
+    s = (k[0, 0].double() @ q[0, 0, 0].double()) / 4
+    want = torch.softmax(s, 0) @ v[0, 0].double()
+    assert float((out[0, 0, 0].double() / want - 1).abs().max()) <= 4 * (2 * 450) ** 0.5 * 2.0 ** -24
+
+
 def test_long_offsets():
     """Keys beyond 2^31 elements: the last of many sequences."""
     B, Nk, d = 2, 2 ** 23 + 40, 128
