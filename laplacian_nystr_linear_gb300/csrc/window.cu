@@ -85,17 +85,29 @@ WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
     // ranges as long as an ordinary tile's, or longer where enough blocks run anyway
     // (four for each of 152 SMs), which bounds the partials.  As one item, the first
     // tile of 8192 tokens with a window of 2048 runs for 600 us beside 226.
-    const int S = a.sinks < a.Nk ? a.sinks : a.Nk;
-    const long long reach = (long long)a.left + a.right + tile;
+    const int S = a.sinks < a.Nk ? a.sinks : a.Nk, kt = (a.Nk + tile - 1) / tile;
+    const long long reach = (long long)a.left + a.right + tile, BH = (long long)a.B * a.Hkv;
     if (S > 0 && 2 * reach < a.Nq) {
       w.stiles = (S + tile - 1) / tile;
       long long n = (a.Nq + reach - 1) / reach;
-      const long long most = 608 / ((long long)a.B * a.Hkv * w.stiles) + 1;
+      const long long most = 608 / (BH * w.stiles) + 1;
       n = n < most ? n : most;
       w.chunk_rows = (int)(((a.Nq + n - 1) / n + tile - 1) / tile * tile);
+    } else if (2 * reach >= a.Nq && BH * kt < 152) {
+      // Every tile is seen by half of the queries or more, and there are fewer tiles than
+      // SMs: all tiles' queries in ranges, two items for each of 152 SMs, of four steps
+      // (tiles of one head's queries) or more (8 heads of 128 on 1, 2 x 1181 tokens, fp32:
+      // as 38 items forward + backward take 2171 us, cut 1112).
+      const long long least = (long long)tile * ((3 + a.g) / a.g);
+      const long long n = (304 + BH * kt - 1) / (BH * kt);
+      const long long rows = ((a.Nq + n - 1) / n + tile - 1) / tile * tile;
+      w.chunk_rows = (int)(rows > least ? rows : least);
+      w.stiles = w.chunk_rows < a.Nq ? kt : 0;
+    }
+    if (w.stiles > 0) {
       w.chunks = (a.Nq + w.chunk_rows - 1) / w.chunk_rows;
       w.part = o;
-      o = align256(o + (size_t)a.B * a.Hkv * w.stiles * w.chunks * 2 * tile * a.d * 4);
+      o = align256(o + (size_t)BH * w.stiles * w.chunks * 2 * tile * a.d * 4);
     }
   }
   w.total = o;

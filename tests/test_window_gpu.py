@@ -49,6 +49,8 @@ CASES = {
     "chunk_positions": (3, 2, 1, 64, 300, 128, 90, 7, 4, [300, 150, 280], [236, 120, -20]),
     "positions_off": (2, 2, 2, 40, 100, 16, 30, 0, 0, [100, 50], [90, 2000000000]),
     "group_8": (1, 16, 2, 140, 140, 128, 64, 0, 4, None, None),
+    "queries_cut": (1, 8, 1, 700, 700, 64, -1, -1, 0, None, None),
+    "queries_cut_causal": (2, 4, 1, 333, 333, 128, -1, 0, 4, [333, 200], None),
     "long_first": (1, 1, 1, 2500, 2500, 64, 50, 0, 4, None, None),
     "one_token": (3, 8, 2, 1, 777, 128, 300, 0, 4, [777, 1, 300], [776, 0, 299]),
     "one_token_64": (2, 4, 4, 1, 1000, 64, -1, 0, 0, None, None),
