@@ -20,11 +20,10 @@
 // shared memory whose 16-byte chunks are XORed with the row (ldmatrix without bank
 // conflicts, plain or transposed); P and dS are split in registers.
 // Bound by the tensor instruction (4 d operations forward, 14 d backward for each
-// visible pair, times six); by its latency where there are few tiles.  Measured: 4 heads
-// of 64, 4096 tokens, all visible: forward 368 us (47 TFLOP/s of the 4 d), with backward
-// 1680 us; the loads and splits of a tile stand before its products where one block
-// fills an SM (heads of 128: 27 to 37 TFLOP/s).  196 tokens, one head of 32: 21, 21 and
-// 24 us.
+// visible pair, times six); by its latency where there are few tiles.  Measured: 16 heads
+// of 64, 2432 tokens, all visible: 407, 554 and 759 us (60 TFLOP/s of the forward's 4 d,
+// 46 of the backward's 10 d); 8 heads of 128: 416, 605 and 790 us.  196 tokens, one head of
+// 32: 21, 21 and 24 us.
 #include "common.cuh"
 #include "internal.h"
 #include "win.cuh"
@@ -44,32 +43,50 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int c) {
   return tile + row * Planes<DP>::RB + ((c ^ (row & 7)) << 4);
 }
 
-// rows [r0, r1) (r1 - r0 <= 64) of a row-major [..][d] matrix as a tile of 64 rows x DP
-// features in three planes, zeros elsewhere
+// Rows [r0, r1) (r1 - r0 <= 64) of a row-major [..][d] matrix as 64 rows x DP features,
+// zeros elsewhere: this thread's pieces of 8 features, and from there to a tile's planes.
+// All pieces are asked for at once, and for wide heads, where one block fills an SM, before
+// the products of the tile before if registers allow it (8 heads of 128, 2432 tokens all
+// visible: forward 487 -> 416 us, dQ 653 -> 605 us).
+template <int DP>
+struct Pieces {
+  static constexpr int N = WT * DP / 8 / kThreads;
+  float4 x[N], y[N];
+  __device__ __forceinline__ void fetch(const float* g, int d, int r0, int r1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = threadIdx.x + i * kThreads, r = r0 + id / (DP / 8), c = id % (DP / 8);
+      x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < r1 && 8 * c < d) {
+        const float* p = g + (size_t)r * d + 8 * c;
+        x[i] = ld4(p);
+        y[i] = ld4(p + 4);
+      }
+    }
+  }
+  __device__ __forceinline__ void place(uint32_t tile) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = threadIdx.x + i * kThreads;
+      uint32_t w[4][3];
+      split3_bf16x2(x[i].x, x[i].y, w[0]);
+      split3_bf16x2(x[i].z, x[i].w, w[1]);
+      split3_bf16x2(y[i].x, y[i].y, w[2]);
+      split3_bf16x2(y[i].z, y[i].w, w[3]);
+      const uint32_t at = chunk_at<DP>(tile, id / (DP / 8), id % (DP / 8));
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + q * Planes<DP>::PL),
+                     "r"(w[0][q]), "r"(w[1][q]), "r"(w[2][q]), "r"(w[3][q])
+                     : "memory");
+    }
+  }
+};
 template <int DP>
 __device__ __forceinline__ void load_planes(uint32_t tile, const float* g, int d, int r0, int r1) {
-  constexpr int C8 = DP / 8;
-#pragma unroll 2
-  for (int id = threadIdx.x; id < WT * C8; id += kThreads) {
-    const int r = id / C8, c = id % C8;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    if (r0 + r < r1 && 8 * c < d) {
-      const float* p = g + (size_t)(r0 + r) * d + 8 * c;
-      x = ld4(p);
-      y = ld4(p + 4);
-    }
-    uint32_t w[4][3];
-    split3_bf16x2(x.x, x.y, w[0]);
-    split3_bf16x2(x.z, x.w, w[1]);
-    split3_bf16x2(y.x, y.y, w[2]);
-    split3_bf16x2(y.z, y.w, w[3]);
-    const uint32_t at = chunk_at<DP>(tile, r, c);
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + q * Planes<DP>::PL),
-                   "r"(w[0][q]), "r"(w[1][q]), "r"(w[2][q]), "r"(w[3][q])
-                   : "memory");
-  }
+  Pieces<DP> x;
+  x.fetch(g, d, r0, r1);
+  x.place(tile);
 }
 
 __device__ __forceinline__ void ldm(uint32_t (&r)[4], uint32_t at) {
@@ -246,43 +263,53 @@ __global__ void __launch_bounds__(kThreads) k_win_fwd(WinArgs a) {
   for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-  for (int seg = 0; seg < 2; ++seg) {
-    const int jb = seg ? kr.lo : 0, je = seg ? kr.hi : kr.S;
-    for (int j0 = jb; j0 < je; j0 += WT) {
-      __syncthreads();
-      load_planes<DP>(K, (const float*)a.k + kv0, a.d, j0, min(je, j0 + WT));
-      load_planes<DP>(V, (const float*)a.v + kv0, a.d, j0, min(je, j0 + WT));
-      __syncthreads();
-      if (j0 + c0 >= je) continue;
-      float s[4][4], f[2];
-      dot_rows<DP>(Q, K, a.d, r0, c0, s);
+  constexpr bool AHEAD = DP == 128;
+  const int ns = (kr.S + WT - 1) / WT, steps = ns + (kr.hi - kr.lo + WT - 1) / WT;
+  Pieces<DP> kp, vp;
+  auto fetch = [&](int t) {
+    const int j0 = t < ns ? t * WT : kr.lo + (t - ns) * WT, je = min(t < ns ? kr.S : kr.hi, j0 + WT);
+    kp.fetch((const float*)a.k + kv0, a.d, j0, je);
+    vp.fetch((const float*)a.v + kv0, a.d, j0, je);
+  };
+  if (AHEAD && steps > 0) fetch(0);
+#pragma unroll 1
+  for (int t = 0; t < steps; ++t) {
+    const int j0 = t < ns ? t * WT : kr.lo + (t - ns) * WT, je = min(t < ns ? kr.S : kr.hi, j0 + WT);
+    if (!AHEAD) fetch(t);
+    __syncthreads();
+    kp.place(K);
+    vp.place(V);
+    __syncthreads();
+    if (AHEAD && t + 1 < steps) fetch(t + 1);
+    if (j0 + c0 >= je) continue;
+    float s[4][4], f[2];
+    dot_rows<DP>(Q, K, a.d, r0, c0, s);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float mx = -INFINITY;
+    for (int r = 0; r < 2; ++r) {
+      float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = j0 + c0 + 8 * (e >> 1) + 2 * tq + (e & 1);
-          float& x = s[e >> 1][2 * r + (e & 1)];
-          x = j < je && win_sees(row[r], j) ? x * a.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, x);
-        }
-        mx = fmaxf(m[r], row_max(mx));
-        const float mu = mx == -INFINITY ? 0.f : mx;
-        f[r] = exp2f(m[r] - mu);
-        m[r] = mx;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float& x = s[e >> 1][2 * r + (e & 1)];
-          x = exp2f(x - mu);
-          sum += x;
-        }
-        l[r] = l[r] * f[r] + row_sum(sum);
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + c0 + 8 * (e >> 1) + 2 * tq + (e & 1);
+        float& x = s[e >> 1][2 * r + (e & 1)];
+        x = j < je && win_sees(row[r], j) ? x * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, x);
       }
-      uint32_t w[2][3][4];
-      as_left(s, w);
-      add_rows<DP>(w, V, a.d, c0, f, o);
+      mx = fmaxf(m[r], row_max(mx));
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      f[r] = exp2f(m[r] - mu);
+      m[r] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float& x = s[e >> 1][2 * r + (e & 1)];
+        x = exp2f(x - mu);
+        sum += x;
+      }
+      l[r] = l[r] * f[r] + row_sum(sum);
     }
+    uint32_t w[2][3][4];
+    as_left(s, w);
+    add_rows<DP>(w, V, a.d, c0, f, o);
   }
   __syncthreads();
   // the halves' sums, over the same maximum
@@ -357,29 +384,39 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   const float one[2] = {1.f, 1.f};
-  for (int seg = 0; seg < 2; ++seg) {
-    const int jb = seg ? kr.lo : 0, je = seg ? kr.hi : kr.S;
-    for (int j0 = jb; j0 < je; j0 += WT) {
-      __syncthreads();
-      load_planes<DP>(K, (const float*)a.k + kv0, a.d, j0, min(je, j0 + WT));
-      load_planes<DP>(V, (const float*)a.v + kv0, a.d, j0, min(je, j0 + WT));
-      __syncthreads();
-      if (j0 + c0 >= je) continue;
-      float s[4][4], dp[4][4];
-      dot_rows<DP>(Q, K, a.d, r0, c0, s);
-      dot_rows<DP>(O, V, a.d, r0, c0, dp);
+  constexpr bool AHEAD = DP == 128;
+  const int ns = (kr.S + WT - 1) / WT, steps = ns + (kr.hi - kr.lo + WT - 1) / WT;
+  Pieces<DP> kp, vp;
+  auto fetch = [&](int t) {
+    const int j0 = t < ns ? t * WT : kr.lo + (t - ns) * WT, je = min(t < ns ? kr.S : kr.hi, j0 + WT);
+    kp.fetch((const float*)a.k + kv0, a.d, j0, je);
+    vp.fetch((const float*)a.v + kv0, a.d, j0, je);
+  };
+  if (AHEAD && steps > 0) fetch(0);
+#pragma unroll 1
+  for (int t = 0; t < steps; ++t) {
+    const int j0 = t < ns ? t * WT : kr.lo + (t - ns) * WT, je = min(t < ns ? kr.S : kr.hi, j0 + WT);
+    if (!AHEAD) fetch(t);
+    __syncthreads();
+    kp.place(K);
+    vp.place(V);
+    __syncthreads();
+    if (AHEAD && t + 1 < steps) fetch(t + 1);
+    if (j0 + c0 >= je) continue;
+    float s[4][4], dp[4][4];
+    dot_rows<DP>(Q, K, a.d, r0, c0, s);
+    dot_rows<DP>(O, V, a.d, r0, c0, dp);
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e >> 1, j = j0 + c0 + 8 * n + 2 * tq + (e & 1);
-          const bool see = j < je && win_sees(row[r], j);
-          s[n][e] = see ? exp2f(fmaf(s[n][e], a.scale_log2, -ls[r])) * (dp[n][e] - D[r]) : 0.f;
-        }
-      uint32_t w[2][3][4];
-      as_left(s, w);
-      add_rows<DP>(w, K, a.d, c0, one, o);
-    }
+      for (int e = 0; e < 4; ++e) {
+        const int r = e >> 1, j = j0 + c0 + 8 * n + 2 * tq + (e & 1);
+        const bool see = j < je && win_sees(row[r], j);
+        s[n][e] = see ? exp2f(fmaf(s[n][e], a.scale_log2, -ls[r])) * (dp[n][e] - D[r]) : 0.f;
+      }
+    uint32_t w[2][3][4];
+    as_left(s, w);
+    add_rows<DP>(w, K, a.d, c0, one, o);
   }
   __syncthreads();
   float* buf = reinterpret_cast<float*>(smw) + r0 * (DP + 8);
@@ -397,9 +434,10 @@ __global__ void __launch_bounds__(kThreads) k_win_dq(WinArgs a) {
 // dK and dV of one tile of keys, over the queries (and the group's heads) that
 // see it.  A tile that holds first tokens is seen by every later query: its
 // queries are cut into `chunks` ranges of `chunk_rows`, one block each, whose
-// fp32 partials k_win_join adds in their order.
+// fp32 partials k_win_join adds in their order.  Heads to 64: two blocks of an SM, at the
+// price of some spilled registers (16 heads, 2432 tokens all visible: 890 -> 759 us).
 template <int DP>
-__global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) k_win_dkv(WinArgs a) {
   extern __shared__ __align__(128) uint8_t smw[];
   using T = Planes<DP>;
   const uint32_t K = smem_addr(smw), V = K + T::BYTES, Q = V + T::BYTES, O = Q + T::BYTES;
@@ -432,11 +470,15 @@ __global__ void __launch_bounds__(kThreads) k_win_dkv(WinArgs a) {
   const float one[2] = {1.f, 1.f};
   for (int e = 0; e < a.g; ++e) {
     const size_t q0 = ((size_t)b * a.Hq + hk * a.g + e) * a.Nq;
+#pragma unroll 1
     for (int i = i0; i < i1; i += WT) {
       const int ie = min(i1, i + WT);
+      Pieces<DP> qp, op;
+      qp.fetch((const float*)a.q + q0 * a.d, a.d, i, ie);
+      op.fetch((const float*)a.dout + q0 * a.d, a.d, i, ie);
       __syncthreads();
-      load_planes<DP>(Q, (const float*)a.q + q0 * a.d, a.d, i, ie);
-      load_planes<DP>(O, (const float*)a.dout + q0 * a.d, a.d, i, ie);
+      qp.place(Q);
+      op.place(O);
       if (tid < WT) {
         Ls[tid] = i + tid < ie ? a.lse[q0 + i + tid] : 0.f;
         Ds[tid] = i + tid < ie ? a.D[q0 + i + tid] : 0.f;
