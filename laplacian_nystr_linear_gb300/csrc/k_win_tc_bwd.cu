@@ -39,9 +39,9 @@
 //
 // Bound: 16 d flops per visible pair (with dS in two parts) on the tensor pipe, or the
 // elementwise warps.  Measured: 16384 tokens, 2 x 16 heads of 64, window 1024: dq 366,
-// dkv 450, join 13 us; issue slots 59 % and tensor pipe 41 % busy in dq: what the steps
-// wait for one another and some 4000 cycles an item of 9 steps for D, the outputs and
-// the next item's start.  8192 tokens, 16 heads of 128 on 4, window 2048: 185, 220 and
+// dkv 450, join 13 us; issue slots 59 % and tensor pipe 41 % busy in dq: the chain of a
+// step (scores, exponentials, dS, products) and what stands between items of 9 steps (D,
+// the outputs).  8192 tokens, 16 heads of 128 on 4, window 2048: 185, 220 and
 // 6 us (0.73 PFLOP/s of the 10 d flops a pair that are needed).
 #include <cstring>
 
