@@ -15,7 +15,7 @@
 // their start and end and, on ragged batches, a second wave (32 sequences, 8192
 // tokens at the most: 110 us).
 // Measured: that batch, 32 heads of 128 on 8: 63 us + 8 for the join, 5.3 TB/s of the
-// cache's bytes; 4 sequences up to 131072 tokens, 4 queries of 16 heads on 4: 86 + 16 us;
+// cache's bytes; 4 sequences up to 131072 tokens, 4 queries of 16 heads on 4: 86 + 10 us;
 // 16 sequences of bf16 keys, window 1024: 19 + 8 us, 3.6 TB/s.
 //
 // Products on the warp-level tensor instruction (m16n8k16), with the contraction's
@@ -52,6 +52,7 @@ namespace lapnys {
 
 namespace {
 constexpr int TNW = 4;      // working warps of a block (and one that copies)
+constexpr int JNW = 16;     // warps that join a row's parts, at the most
 enum : int { TK_BF16 = 0, TK_E4M3 = 1, TK_E4M3_F32 = 2, TK_F32 = 3 };
 
 template <int KIND>
@@ -819,10 +820,11 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
 
 // out = sum over a row's parts: a block a row, its warps take parts in turn
 template <typename TQ>
-__global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
-  __shared__ __align__(16) float So[4][128];
-  __shared__ float Sl[4];
+__global__ void __launch_bounds__(32 * JNW) k_token_join(TokenArgs t, float shift) {
+  __shared__ __align__(16) float So[JNW][128];
+  __shared__ float Sl[JNW];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while k_token still ran
+  const int warps = blockDim.x >> 5;
   const WinArgs& a = t.w;
   const long long qrow = blockIdx.x;                     // (b, query head, query)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = 4 * lane;
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = warp; s < n; s += 4) {
+  for (int s = warp; s < n; s += warps) {
     const size_t row = row0 + (size_t)s * 16;
     const float2 x = t.part_ml[row];
     const float f = exp2f(x.x - mu);
@@ -856,8 +858,7 @@ __global__ void __launch_bounds__(128) k_token_join(TokenArgs t, float shift) {
   if (lane == 0) Sl[warp] = sum;
   __syncthreads();
   if (warp) return;
-#pragma unroll
-  for (int w = 1; w < 4; ++w) {
+  for (int w = 1; w < warps; ++w) {
     const float4 v = lds4(&So[w][c]);
     sum += Sl[w];
     acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
@@ -913,7 +914,11 @@ cudaError_t go(TokenArgs& t, cudaStream_t st) {
   e = launch("token_attention", k_token<KIND, DP, ROWS>, dim3((unsigned)t.grid), dim3(32 * TNW + 32), smem, st, mp, t);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)t.w.B * t.w.Hq * t.w.Nq;
-  return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(128), 0, st, t,
+  // rows of many parts (32 on the average): more warps (4 sequences of 131072 tokens, 76
+  // parts: 16.4 us with 4 warps, 10.5 with 16; 32 sequences of 8192, 7 parts: 8.1 and 11.5)
+  const long long tiles = (long long)a.B * a.Hkv * t.rtiles;
+  const int warps = (long long)t.grid * TNW >= 32 * tiles ? JNW : 4;
+  return launch_after("token_join", k_token_join<TQ>, dim3((unsigned)rows), dim3(32 * warps), 0, st, t,
                       Kind<KIND>::SHIFT);
 }
 }  // namespace
