@@ -87,19 +87,22 @@ WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
     // tile of 8192 tokens with a window of 2048 runs for 600 us beside 226.
     const int S = a.sinks < a.Nk ? a.sinks : a.Nk, kt = (a.Nk + tile - 1) / tile;
     const long long reach = (long long)a.left + a.right + tile, BH = (long long)a.B * a.Hkv;
+    const long long steps = (long long)a.g * ((a.Nq + tile - 1) / tile);   // of a tile that all see
     if (S > 0 && 2 * reach < a.Nq) {
       w.stiles = (S + tile - 1) / tile;
       long long n = (a.Nq + reach - 1) / reach;
       const long long most = 608 / (BH * w.stiles) + 1;
       n = n < most ? n : most;
       w.chunk_rows = (int)(((a.Nq + n - 1) / n + tile - 1) / tile * tile);
-    } else if (2 * reach >= a.Nq && BH * kt < 152) {
+    } else if (2 * reach >= a.Nq && (BH * kt < 152 || (BH * kt < 304 && steps >= 64))) {
       // Every tile is seen by half of the queries or more, and there are fewer tiles than
-      // SMs: all tiles' queries in ranges, two items for each of 152 SMs, of four steps
-      // (tiles of one head's queries) or more (8 heads of 128 on 1, 2 x 1181 tokens, fp32:
-      // as 38 items forward + backward take 2171 us, cut 1112).
+      // SMs, or long ones that fill the SMs once and a little: all tiles' queries in
+      // ranges, two items for each of 152 SMs (four of long ones), of four steps (tiles of
+      // one head's queries) or more.  fp32, heads of 128, forward + backward: 8 heads on 1,
+      // 2 x 1181 tokens, 38 tiles: 2171 us as they are, 1031 cut; 20 on 5, 1986 tokens, 155
+      // tiles: 4717 and 3775 us.
       const long long least = (long long)tile * ((3 + a.g) / a.g);
-      const long long n = (304 + BH * kt - 1) / (BH * kt);
+      const long long n = ((steps < 64 ? 304 : 608) + BH * kt - 1) / (BH * kt);
       const long long rows = ((a.Nq + n - 1) / n + tile - 1) / tile * tile;
       w.chunk_rows = (int)(rows > least ? rows : least);
       w.stiles = w.chunk_rows < a.Nq ? kt : 0;
