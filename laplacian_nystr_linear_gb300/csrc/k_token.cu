@@ -653,19 +653,19 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
     if constexpr (X::F16) {
       // p (v_scale / reference): the reference follows a larger scale at once, and
       // a smaller one below 2^-16 of it (one below 2^-64, as of a block of zeros,
-      // adds less than fp32 holds beside what it was set for)
+      // adds less than fp32 holds beside what it was set for).  One step for the whole
+      // group, to its largest scale: no factor below is above 1 (p is held to 2^10 of f16's 2^16)
+      float big = 0.f;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        if (!there[h]) continue;
-        const float r = vsc[h] / vref;
-        if (r > 1.f || (r < 0x1p-16f && r >= 0x1p-64f)) {
-          const float x = vref / vsc[h];
+      for (int h = 0; h < NH; ++h) big = fmaxf(big, there[h] ? vsc[h] : 0.f);
+      const float to = big / vref;
+      if (to > 1.f || (to < 0x1p-16f && to >= 0x1p-64f)) {
+        const float x = vref / big;
 #pragma unroll
-          for (int n = 0; n < NO; ++n)
+        for (int n = 0; n < NO; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= x;
-          vref = vsc[h];
-        }
+          for (int e = 0; e < 4; ++e) o[n][e] *= x;
+        vref = big;
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
