@@ -33,7 +33,7 @@
 //     conversions, 1576 instructions for 32 keys against about 600).  q is scaled
 //     per row by a power of two to fit f16 (features below 2^-38 of the row's
 //     largest are lost).  p is kept as 2^10 p (v_scale / reference) in f16, the
-//     reference a scale of the values seen so far, so that P V adds up without a
+//     reference about the row's largest p v_scale so far, so that P V adds up without a
 //     product per element; outputs are rescaled when the reference moves.  fp32
 //     queries: q and p in two f16 parts (2^-22).
 //   - bf16: q, k, v as they are, p rounded to bf16 (2^-9, below the rounding of
@@ -53,6 +53,8 @@ namespace lapnys {
 namespace {
 constexpr int TNW = 4;      // working warps of a block (and one that copies)
 constexpr int JNW = 16;     // warps that join a row's parts, at the most
+constexpr int kRefMin = -126, kRefMax = 126;   // of the values' scales: range of the reference
+constexpr int kRefSlack = 4;                   // 2^10 p, four powers more and a factor below 2: in f16
 enum : int { TK_BF16 = 0, TK_E4M3 = 1, TK_E4M3_F32 = 2, TK_F32 = 3 };
 
 template <int KIND>
@@ -106,6 +108,9 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
   return r;
 }
+// exponent of a positive fp32 (subnormals and 0 count as the smallest), and 2^e for -127 < e < 128
+__device__ __forceinline__ int exponent(float x) { return max((int)(__float_as_uint(x) >> 23) - 127, kRefMin); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // two fp32 as PARTS 16-bit parts, the parts' sum nearest to them
 template <int KIND>
 __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[Kind<KIND>::PARTS]) {
@@ -418,13 +423,17 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
   };
 
   float m[2], l[2];
-  float vref;                        // reference of the values' scales: v = vref x what o holds
+  // reference of the values' scales by row, below all of them at first: o holds v 2^-vref; and
+  // the row's maximum beside which what it holds was some 2^vref
+  int vref[2];
+  float mref[2];
   constexpr int NO = FEW ? NT / 2 : NT;
   float o[NO][4];                    // 16 rows: [n] is column n; 8: [n] features 2 n, 2 n + 1
   auto clear = [&]() {
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    vref = 1.f;
+    vref[0] = vref[1] = kRefMin;
+    mref[0] = mref[1] = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NO; ++n)
 #pragma unroll
@@ -446,6 +455,7 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
       if (rt * 16 + rr >= R) continue;
       if ((FEW ? gid : tq) == 0) t.part_ml[part + rr] = make_float2(m[r], l[r]);
       float* dst = t.part_o + (part + rr) * a.d;
+      const float unit = X::F16 ? pow2(vref[r]) : 1.f;
 #pragma unroll
       for (int e = 0; e < (FEW ? 1 : 2); ++e)
 #pragma unroll
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
             y = make_float4(o[n / 2][r], o[n / 2][2 + r], o[n / 2 + 1][r], o[n / 2 + 1][2 + r]);
           else
             y = make_float4(o[n][2 * r + e], o[n + 1][2 * r + e], o[n + 2][2 * r + e], o[n + 3][2 * r + e]);
-          st4(dst + f, make_float4(y.x * vref, y.y * vref, y.z * vref, y.w * vref));
+          st4(dst + f, make_float4(y.x * unit, y.y * unit, y.z * unit, y.w * unit));
         }
     }
     // the row's first and last parts
@@ -643,6 +653,64 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
       }
       l[r] = l[r] * f[r] + sum;
     }
+    // ---- the values' scales: p becomes p v_scale 2^-vref ----
+    // A row's reference follows the largest p v_scale so far, not v_scale alone: large values of
+    // no weight may not push small ones with all the weight out of f16.  It is looked at again
+    // where a scale is over 2^kRefSlack above it, or below it by as much in a group that moves
+    // the row's maximum.  So p v_scale 2^-vref stays below 2^15 and the row's largest above
+    // 2^4, and what f16 cuts off (2^-25) is 2^-29 of that or less.
+    if constexpr (X::F16) {
+      int ex[NH], hi = kRefMin, lo = kRefMax;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        ex[h] = there[h] ? exponent(vsc[h]) : kRefMin;
+        hi = max(hi, ex[h]);
+        if (there[h]) lo = min(lo, ex[h]);
+      }
+      bool move = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        move = move || hi > vref[r] + kRefSlack || (f[r] < 1.f && lo < vref[r] - kRefSlack);
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          int own = kRefMin;               // the group's largest p v_scale, as a power of two above it
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            float w = 0.f;
+#pragma unroll
+            for (int x = h * PER; x < (h + 1) * PER; ++x) w = fmaxf(w, p[x >> 1][at(r, x)]);
+#pragma unroll
+            for (int x = X0; x <= X1; x <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, x));
+            if (w > 0.f) own = max(own, ex[h] + exponent(w) + 1 - (int)X::SHIFT);
+          }
+          // what o holds was 2^vref beside the maximum mref
+          const float held = (float)vref[r] + fmaxf(mref[r] - m[r], -400.f);
+          int to = max(own, (int)ceilf(held));
+          if (m[r] == -INFINITY) to = hi;  // nothing seen so far
+          to = min(max(to, hi - 120), kRefMax);   // (the factors below are finite)
+          if (to > vref[r] || to < vref[r] - kRefSlack) {
+            f[r] = scalbnf(f[r], vref[r] - to);
+            vref[r] = to;
+          }
+          mref[r] = m[r] + (fmaxf(held, (float)own) - (float)vref[r]);
+        }
+        up = true;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (f[r] < 1.f) mref[r] = m[r];
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float inv = pow2(-vref[r]);
+        float to[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) to[h] = there[h] ? vsc[h] * inv : 0.f;
+#pragma unroll
+        for (int x = 0; x < NV; ++x) p[x >> 1][at(r, x)] *= to[x / PER];
+      }
+    }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int n = 0; n < NO; ++n) {
@@ -650,34 +718,6 @@ __global__ void __launch_bounds__(32 * TNW + 32, (token_blocks<KIND, DP, ROWS>()
       }
     }
     // ---- P V ----
-    if constexpr (X::F16) {
-      // p (v_scale / reference): the reference follows a larger scale at once, and
-      // a smaller one below 2^-16 of it (one below 2^-64, as of a block of zeros,
-      // adds less than fp32 holds beside what it was set for).  One step for the whole
-      // group, to its largest scale: no factor below is above 1 (p is held to 2^10 of f16's 2^16)
-      float big = 0.f;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) big = fmaxf(big, there[h] ? vsc[h] : 0.f);
-      const float to = big / vref;
-      if (to > 1.f || (to < 0x1p-16f && to >= 0x1p-64f)) {
-        const float x = vref / big;
-#pragma unroll
-        for (int n = 0; n < NO; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= x;
-        vref = big;
-      }
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const float r = there[h] ? vsc[h] / vref : 0.f;
-        if (r != 1.f) {
-#pragma unroll
-          for (int u = NS / NH * h; u < NS / NH * (h + 1); ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[u][e] *= r;
-        }
-      }
-    }
     uint32_t pf[NP][NH][QR];
     if constexpr (FEW) {                   // keys by columns to columns by keys
 #pragma unroll
