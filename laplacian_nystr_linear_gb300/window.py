@@ -13,6 +13,7 @@ import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -69,6 +70,13 @@ def _tensor(t, name, shape, dtype, device):
 def _batch(t, name, B, device):
     if t is not None:
         _tensor(t, name, (B,), torch.int32, device)
+
+
+def _no_tangent(name, *tensors):
+    """Refuses dual tensors, whose tangents the kernels would drop."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} has no forward-mode derivative")
 
 
 _HERE = contextlib.nullcontext()
@@ -183,6 +191,7 @@ class _Window(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(fctx, dout):
+        _no_tangent("window_attention's backward", dout)
         q, k, v, out, lse, rest, lens, q_pos = fctx.saved_tensors   # checked by the forward
         return *_bwd(q, k, v, out, dout.contiguous(), lse, rest, fctx.p, lens, q_pos, None, None,
                      None, None), None, None, None
@@ -196,9 +205,10 @@ def window_attention(q, k, v, left, right=0, sinks=0, scale=None, lens=None, q_p
     all) and the first `sinks` of its sequence, never beyond p + right.  lens: int32 [B], tokens of
     each sequence of a padded batch; q_pos: int32 [B], position of each sequence's first query
     (default Nk - Nq).  Queries that see nothing give zeros.  scale defaults to 1 / sqrt(d).
-    Gradients are of first order.  A step that is captured into a CUDA graph takes leaves that no
+    Gradients are of first order, by reverse mode only.  A step that is captured into a CUDA graph takes leaves that no
     eager autograd graph still holds (their gradients would be added up on that graph's stream).
     """
+    _no_tangent("window_attention", q, k, v)
     p = WindowParams.of(q, k, left, right, sinks, scale)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _Window.apply(q, k, v, lens, q_pos, p)
@@ -235,6 +245,7 @@ def cache_append(cache: KVCache, k, v, table, start, lens=None) -> None:
     """lapnys_cache_append: rounds the new tokens k, v [B, Hkv, N, d] (float32 or bfloat16) into the
     cache; token i of sequence b goes to position start[b] + i while that is below lens[b].
     table: int32 [B, max_blocks]; start, lens: int32 [B]."""
+    _no_tangent("cache_append", k, v)
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")
     B, Hkv, N, d = k.shape
@@ -268,7 +279,8 @@ def cache_attention(q, cache: KVCache, table, lens, left=-1, right=0, sinks=0, s
                     q_pos=None, out=None, ws=None):
     """lapnys_cache_attention: attention of a few queries q [B, Hq, Nq, d] (float32 or bfloat16) over
     the cache, with window_attention's mask.  lens: int32 [B], the sequences' tokens in the cache;
-    q_pos: int32 [B], default lens - Nq (the queries are the last tokens).  No autograd."""
+    q_pos: int32 [B], default lens - Nq (the queries are the last tokens).  No derivatives."""
+    _no_tangent("cache_attention", q)
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, d]")
     if torch.is_grad_enabled() and q.requires_grad:
