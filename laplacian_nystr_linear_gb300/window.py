@@ -244,8 +244,10 @@ def _check_cache(cache: KVCache, table, heads, d, B, device):
 def cache_append(cache: KVCache, k, v, table, start, lens=None) -> None:
     """lapnys_cache_append: rounds the new tokens k, v [B, Hkv, N, d] (float32 or bfloat16) into the
     cache; token i of sequence b goes to position start[b] + i while that is below lens[b].
-    table: int32 [B, max_blocks]; start, lens: int32 [B]."""
+    table: int32 [B, max_blocks]; start, lens: int32 [B].  No derivatives."""
     _no_tangent("cache_append", k, v)
+    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
+        raise ValueError("cache_append has no gradient: detach k and v")
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, d]")
     B, Hkv, N, d = k.shape

@@ -42,3 +42,14 @@ def test_function_transforms_are_refused():
     q, k, v, _, _ = _operands()
     with pytest.raises(ValueError, match="forward-mode"):
         torch.func.jvp(lambda q: lap.window_attention(q, k, v, 4), (q,), (torch.ones_like(q),))
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_append_refuses_what_requires_a_gradient(which):
+    _, k, v, cache, table = _operands()
+    x = {"k": k, "v": v}
+    x[which].requires_grad_(True)
+    with pytest.raises(ValueError, match="gradient"):
+        lap.cache_append(cache, k, v, table, table[0])
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # refused only as not on a GPU
+        lap.cache_append(cache, k, v, table, table[0])
