@@ -21,6 +21,19 @@ from ._lib import check, load
 from .api import _DT, _dtype
 
 
+def _sizes(*sizes):
+    """Sizes as the C entries take them: ctypes would cut them to 32 bits."""
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
+        raise ValueError(f"sizes must be below 2**31: {sizes}")
+    return sizes
+
+
+@functools.lru_cache(maxsize=256)
+def _reach(*tokens):
+    """Sides and first tokens the same way: from 2^28 tokens on they are as good as any."""
+    return tuple(max(-2 ** 31, min(int(t), 2 ** 31 - 1)) for t in tokens)
+
+
 class WindowParams(NamedTuple):
     """Shape and mask of one call: q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d]."""
     B: int
@@ -34,8 +47,9 @@ class WindowParams(NamedTuple):
     sinks: int
     scale: float
 
+    @functools.lru_cache(maxsize=256)
     def dims(self):
-        return self[:9]
+        return *_sizes(*self[:6]), *_reach(*self[6:9])
 
     @staticmethod
     def of(q: torch.Tensor, k: torch.Tensor, left: int, right: int = 0, sinks: int = 0,
@@ -143,7 +157,7 @@ def window_fwd(q, k, v, p: WindowParams, lens=None, q_pos=None, out=None, lse=No
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype), dev)
         rc = load().lapnys_window_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(rest), _at(lens),
-            _at(q_pos), *p, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
+            _at(q_pos), *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_fwd")
     return out, lse
 
@@ -173,8 +187,8 @@ def _bwd(q, k, v, out, dout, lse, rest, p, lens, q_pos, dq, dk, dv, ws):
         ws = _workspace(ws, window_workspace_bytes(p, q.dtype, True), dev)
         rc = load().lapnys_window_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(),
-            _at(rest), _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *p,
-            _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
+            _at(rest), _at(lens), _at(q_pos), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            *p.dims(), p.scale, _on_stream(dev), _dtype(q), _at(ws), _nbytes(ws))
     check(rc, "lapnys_window_bwd")
     return dq, dk, dv
 
@@ -261,7 +275,7 @@ def cache_append(cache: KVCache, k, v, table, start, lens=None) -> None:
     with _on(dev):
         rc = load().lapnys_cache_append(
             _at(k), _at(v), _at(cache.k), _at(cache.v), _at(cache.k_scale), _at(cache.v_scale),
-            _at(table), _at(start), _at(lens), B, Hkv, N, d, *geometry, _on_stream(dev), dt)
+            _at(table), _at(start), _at(lens), *_sizes(B, Hkv, N, d, *geometry), _on_stream(dev), dt)
     check(rc, "lapnys_cache_append")
 
 
@@ -273,8 +287,8 @@ def _cache_workspace(*sizes) -> int:
 def cache_workspace_bytes(q, cache: KVCache, table, left=-1, right=0, sinks=0) -> int:
     B, Hq, Nq, d = q.shape
     blocks, Hkv, block, _ = cache.k.shape
-    return _cache_workspace(B, Hq, Hkv, Nq, d, block, blocks, table.shape[1], left, right, sinks,
-                            _dtype(q))
+    return _cache_workspace(*_sizes(B, Hq, Hkv, Nq, d, block, blocks, table.shape[1]),
+                            *_reach(left, right, sinks), _dtype(q))
 
 
 def cache_attention(q, cache: KVCache, table, lens, left=-1, right=0, sinks=0, scale=None,
@@ -295,13 +309,14 @@ def cache_attention(q, cache: KVCache, table, lens, left=-1, right=0, sinks=0, s
     geometry = _check_cache(cache, table, Hkv, d, B, dev)
     _tensor(lens, "lens", (B,), torch.int32, dev)
     _batch(q_pos, "q_pos", B, dev)
+    sizes, reach = _sizes(B, Hq, Hkv, Nq, d, *geometry), _reach(left, right, sinks)
     with _on(dev):
         out = torch.empty_like(q) if out is None else out
         _tensor(out, "out", q.shape, q.dtype, dev)
-        ws = _workspace(ws, _cache_workspace(B, Hq, Hkv, Nq, d, *geometry, left, right, sinks, dt), dev)
+        ws = _workspace(ws, _cache_workspace(*sizes, *reach, dt), dev)
         rc = load().lapnys_cache_attention(
             _at(q), _at(cache.k), _at(cache.v), _at(cache.k_scale), _at(cache.v_scale),
-            _at(table), _at(lens), _at(q_pos), _at(out), B, Hq, Hkv, Nq, d, *geometry, left, right,
-            sinks, _scale(scale, d), _on_stream(dev), dt, _at(ws), _nbytes(ws))
+            _at(table), _at(lens), _at(q_pos), _at(out), *sizes, *reach,
+            _scale(scale, d), _on_stream(dev), dt, _at(ws), _nbytes(ws))
     check(rc, "lapnys_cache_attention")
     return out

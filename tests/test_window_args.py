@@ -53,3 +53,38 @@ def test_append_refuses_what_requires_a_gradient(which):
         lap.cache_append(cache, k, v, table, table[0])
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # refused only as not on a GPU
         lap.cache_append(cache, k, v, table, table[0])
+
+
+BIG = 2 ** 32      # cut to 32 bits: 0
+
+
+@pytest.mark.parametrize("given,kept", [(BIG, 2 ** 31 - 1), (BIG + 5, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                        (2 ** 31 - 1, 2 ** 31 - 1), (-1, -1), (7, 7), (-BIG, -2 ** 31),
+                                        (1 - 2 ** 33, -2 ** 31)])
+def test_wide_windows_do_not_wrap(given, kept):
+    q = torch.zeros((1, 2, 8, 16))
+    assert lap.WindowParams.of(q, q, given, given, given).dims()[6:] == (kept, kept, kept)
+    p = lap.WindowParams(1, 2, 2, 8, 8, 16, given, given, given, 1.0)
+    assert p.dims()[6:] == (kept, kept, kept)
+
+
+def test_wide_windows_over_the_cache_do_not_wrap():
+    q, cache = torch.zeros((1, 2, 1, 16)), lap.cache_alloc(2000, 2, 16, 16, device="cpu")
+    table = torch.zeros((1, 2000), dtype=torch.int32)
+    need = lap.cache_workspace_bytes(q, cache, table, left=-1, right=0)
+    assert lap.cache_workspace_bytes(q, cache, table, left=0, right=0) < need
+    for wide in (BIG, BIG + 5, 2 ** 31):
+        assert lap.cache_workspace_bytes(q, cache, table, left=wide, right=0) == need
+        assert lap.cache_workspace_bytes(q, cache, table, left=0, right=wide) == need
+        assert lap.cache_workspace_bytes(q, cache, table, left=0, right=0, sinks=wide) == need
+    assert lap.cache_workspace_bytes(q, cache, table, left=-BIG) == 0      # not a window
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    for i in range(6):
+        dims = [1, 2, 2, 8, 8, 16]
+        dims[i] += BIG
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            lap.window_workspace_bytes(lap.WindowParams(*dims, 4, 0, 0, 1.0), torch.bfloat16)
+    with pytest.raises(ValueError, match="2\\*\\*31"):
+        window._sizes(1, BIG + 5)
