@@ -89,11 +89,12 @@ WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
     const long long reach = (long long)a.left + a.right + tile, BH = (long long)a.B * a.Hkv;
     const long long steps = (long long)a.g * ((a.Nq + tile - 1) / tile);   // of a tile that all see
     if (S > 0 && 2 * reach < a.Nq) {
-      w.stiles = (S + tile - 1) / tile;
+      const int st = (S + tile - 1) / tile;
       long long n = (a.Nq + reach - 1) / reach;
-      const long long most = 608 / (BH * w.stiles) + 1;
+      const long long most = 608 / (BH * st) + 1;
       n = n < most ? n : most;
       w.chunk_rows = (int)(((a.Nq + n - 1) / n + tile - 1) / tile * tile);
+      w.stiles = w.chunk_rows < a.Nq ? st : 0;
     } else if (2 * reach >= a.Nq && (BH * kt < 152 || (BH * kt < 304 && steps >= 64))) {
       // Every tile is seen by half of the queries or more, and there are fewer tiles than
       // SMs, or long ones that fill the SMs once and a little: all tiles' queries in

@@ -88,3 +88,14 @@ def test_sizes_beyond_32_bits_are_refused():
             lap.window_workspace_bytes(lap.WindowParams(*dims, 4, 0, 0, 1.0), torch.bfloat16)
     with pytest.raises(ValueError, match="2\\*\\*31"):
         window._sizes(1, BIG + 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_no_partials_where_the_first_tokens_tiles_are_not_cut(dtype):
+    """As many key tiles with first tokens as blocks run at once: their queries stay whole, and the
+    backward needs D (4 bytes a query row) alone."""
+    rows = 32 * 8 * 4096
+    p = lap.WindowParams(32, 8, 8, 4096, 4096, 128, 511, 0, 1024, 0.1)
+    assert lap.window_workspace_bytes(p, dtype, True) == 4 * rows
+    p = p._replace(B=1, Hq=2, Hkv=2)      # few tiles: cut
+    assert lap.window_workspace_bytes(p, dtype, True) > 4 * rows / 128

@@ -5,6 +5,7 @@ import torch
 
 import laplacian_nystr_linear_gb300 as lap
 
+from tests._window_ref import check, reference
 from tests.test_window_gpu import make
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,16 @@ def test_windows_wider_than_32_bits(wide):
     want = lap.cache_attention(q, cache, table, n, left=-1)
     assert torch.equal(lap.cache_attention(q, cache, table, n, left=wide), want)
     assert torch.equal(lap.cache_attention(q, cache, table, n, left=3, sinks=wide), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["f32", "bf16"])
+def test_first_tokens_of_many_heads(dtype):
+    """Key tiles with first tokens whose queries are not cut, since there are as many as fill the GPU."""
+    q, k, v, do = make(80, 4, 4, 600, 600, 16, dtype)
+    p = lap.WindowParams.of(q, k, 63, 0, 200)
+    assert lap.window_workspace_bytes(p, dtype, True) == 4 * 80 * 4 * 600
+    out, lse = lap.window_fwd(q, k, v, p)
+    ref = reference(q, k, v, 63, 0, 200, dout=do)
+    check("out", out, ref["out"])
+    for name, x in zip(("dq", "dk", "dv"), lap.window_bwd(q, k, v, out, do, lse, p)):
+        check(name, x, ref[name])
