@@ -108,8 +108,8 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
   return r;
 }
-// exponent of a positive fp32 (subnormals and 0 count as the smallest), and 2^e for -127 < e < 128
-__device__ __forceinline__ int exponent(float x) { return max((int)(__float_as_uint(x) >> 23) - 127, kRefMin); }
+// exponent of a magnitude (subnormals and 0 count as the smallest), and 2^e for -127 < e < 128
+__device__ __forceinline__ int exponent(float x) { return max((int)(__float_as_uint(x) << 1 >> 24) - 127, kRefMin); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // two fp32 as PARTS 16-bit parts, the parts' sum nearest to them
 template <int KIND>

@@ -177,3 +177,16 @@ def test_weights_that_rise_little_by_little(small, Nq, dtype):
     q[..., 1] = q[..., 0]
     cache = cache._replace(k=k.to(torch.float8_e4m3fn))
     compare_many(512, q, cache, table, torch.tensor([nb * T], dtype=torch.int32, device="cuda"))
+
+
+@DTYPES
+def test_a_negative_scale_turns_the_sign(dtype):
+    """Not what cache_append stores, but a cache of a user's own: its scales are factors."""
+    cache = clone(filled(8, 2, 16, 64), "cuda")
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None].contiguous()
+    lens = torch.tensor([125], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 8, 1, 64), generator=torch.Generator().manual_seed(2)).cuda().to(dtype)
+    want = lap.cache_attention(q, cache, table, lens)
+    assert torch.equal(lap.cache_attention(q, cache._replace(v_scale=-cache.v_scale), table, lens), -want)
+    cache.v_scale[::2] *= -1.5
+    compare(q, cache, table, lens)
