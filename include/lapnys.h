@@ -327,11 +327,13 @@ int lapnys_window_bwd(const void* q, const void* k, const void* v, const void* o
  *    scale = 2^ceil(log2(amax / 448)), amax over the block's new finite values,
  *            at least 2^-100; a block that held tokens before start[b] keeps its
  *            scale if that is larger, else its tokens are rounded again to the
- *            new one (exact but for values that become subnormal);
- *    value = e4m3(x / scale), to nearest, ties to even; infinities saturate, NaN
- *            stays NaN.
+ *            new one (exact but for values that become subnormal, off by 2^-10 of the
+ *            new scale at most each time);
+ *    value = e4m3(x / scale), to nearest, ties to even; infinities saturate (to
+ *            448 scale, which is a number to later calls), NaN stays NaN.
  * Slots behind the last new token stay as they were.  No two sequences of a
- * call may append to the same block (its content would be undefined).
+ * call may append to the same block, nor one sequence to a block twice (its content would be
+ * undefined).
  *
  * lapnys_cache_attention: q, out [B][Hq][Nq][d] (dtype); lens int32 [B] counts
  * the sequence's tokens in the cache, q_pos NULL means lens[b] - Nq (the

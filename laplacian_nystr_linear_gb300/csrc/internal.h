@@ -350,11 +350,12 @@ int bwd_tc_splits(int BH, int m, int N);
 cudaError_t run_bwd_tc(const Prob& p, int mode, const BwdTcArgs& a, cudaStream_t st);
 
 // ---- windowed softmax attention and the 8-bit cache (win.cuh) --------------
-// fp32: on the FP32 pipe, in tiles of win_tile_rows()
+// fp32: products of three bf16 parts on the warp-level tensor instruction, in tiles of
+// win_tile_rows()
 int win_tile_rows();
 cudaError_t run_win_fwd(const WinArgs& a, cudaStream_t st);
 cudaError_t run_win_bwd(const WinArgs& a, cudaStream_t st);
-// dK, dV of the key tiles with first tokens, from their chunks' partials
+// dK, dV of the key tiles whose queries were cut, from their ranges' partials
 cudaError_t run_win_join(const WinArgs& a, int tile_rows, bool bf16, cudaStream_t st);
 
 // the forward on the tensor cores, bf16

@@ -8,13 +8,15 @@
 // magnitude still lands in (224, 448]) and makes a later, larger scale harmless:
 // the block's earlier tokens are multiplied by the ratio of the scales, exactly,
 // unless a value becomes subnormal (below 2^-6 of the new scale: off by at most
-// 2^-10 of it more).  So appending one token at a time gives the values of one
-// call, but for those.
+// 2^-10 of it more each time the scale grows).  So appending one token at a time gives the
+// values of one call, but for those and for infinities: one is stored as 448 of the scale of
+// its call, which is a number like any other when the scale grows later.
 //
 // One block of threads per (sequence, cache block, head, keys or values): the
 // new tokens are read once, kept in registers over the reduction and written as
 // 8 bytes per 8 values.  Bound by DRAM for prompts (4 of up to 4099 tokens, 8 heads of
-// 128, bf16: 23 us, 4.4 TB/s), by the launch for one token (7.5 us for 32 sequences).
+// 128, bf16: 23 us, 4.4 TB/s; fp32 31 us,
+// 5.4 TB/s), by the launch for one token (7.5 us for 32 sequences).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -15,8 +15,9 @@
 // their start and end and, on ragged batches, a second wave (32 sequences, 8192
 // tokens at the most: 110 us).
 // Measured: that batch, 32 heads of 128 on 8: 63 us + 8 for the join, 5.3 TB/s of the
-// cache's bytes; 4 sequences up to 131072 tokens, 4 queries of 16 heads on 4: 86 + 10 us;
-// 16 sequences of bf16 keys, window 1024: 19 + 8 us, 3.6 TB/s.
+// cache's bytes; 4 sequences up to 131072 tokens, 4 queries of 16 heads on 4: 77 + 10 us;
+// 16 sequences of bf16 keys, window 1024: 19 + 8 us, 3.6 TB/s.  fp32 queries: 85, 142 and (fp32
+// keys) 35 us, bound by the products of their parts and the registers those take.
 //
 // Products on the warp-level tensor instruction (m16n8k16), with the contraction's
 // order chosen so that no operand is transposed or gathered: a thread's four k of step s
@@ -36,8 +37,8 @@
 //     reference about the row's largest p v_scale so far, so that P V adds up without a
 //     product per element; outputs are rescaled when the reference moves.  fp32
 //     queries: q and p in two f16 parts (2^-22).
-//   - bf16: q, k, v as they are, p rounded to bf16 (2^-9, below the rounding of
-//     the output; sums, maxima and outputs are fp32 throughout).
+//   - bf16: q, k, v as they are, p rounded to bf16 (2^-8 of each, as the
+//     output's own rounding; sums, maxima and outputs are fp32 throughout).
 //   - fp32: all operands in three bf16 parts, six products (2^-24 each).
 //   With fp32 queries the products of 16 keys are added up by the FP32 pipe: the
 //   instruction's own sums are cut off, which 3000 keys a warp made 2e-5 of the output.

@@ -33,7 +33,8 @@
 //   warp 18     dkv: log-sum and D of a step's queries into shared memory.
 //
 // Key tiles with first tokens are seen by all later queries: their queries are
-// cut into chunks, one item each, with fp32 partials that k_win_join adds.
+// cut into chunks, one item each, with fp32 partials that k_win_join adds; so are all
+// tiles' where there are few with many queries each (wide windows).
 // Rows behind a sequence's end are zeroed in shared memory where they are
 // summed over (0 * NaN).  Every wait is bounded.
 //

@@ -36,8 +36,10 @@ struct WinArgs {
   void* dq;
   void* dk;
   void* dv;
-  float* part;        // fp32 partial dK, dV of the key tiles that hold first tokens
-  int stiles, chunks, chunk_rows;  // those tiles, and their query ranges
+  // The first `stiles` key tiles (those with first tokens, or all where few tiles have many
+  // queries each) have their queries cut into `chunks` ranges of chunk_rows
+  float* part;        // their fp32 partial dK, dV
+  int stiles, chunks, chunk_rows;
 };
 
 struct WinSeq {

@@ -64,7 +64,7 @@ struct WinWs {
   size_t total;
 };
 
-// rows of the backward's key tiles: bf16 on the tensor cores, fp32 on the FP32 pipe
+// rows of the backward's key tiles: bf16 by tcgen05, fp32 by the warp-level instruction
 int tile_rows(int dtype) { return dtype == LAPNYS_BF16 ? win_tc_tile_rows() : win_tile_rows(); }
 
 WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
@@ -84,7 +84,8 @@ WinWs window_ws(const WinArgs& a, bool backward, int dtype) {
     // as many; below that the partials' launch is not worth it): their queries in
     // ranges as long as an ordinary tile's, or longer where enough blocks run anyway
     // (four for each of 152 SMs), which bounds the partials.  As one item, the first
-    // tile of 8192 tokens with a window of 2048 runs for 600 us beside 226.
+    // tile of 8192 tokens with a window of 2048 runs for 600 us beside 226.  One range would be
+    // partials for nothing: then the tiles are like any other.
     const int S = a.sinks < a.Nk ? a.sinks : a.Nk, kt = (a.Nk + tile - 1) / tile;
     const long long reach = (long long)a.left + a.right + tile, BH = (long long)a.B * a.Hkv;
     const long long steps = (long long)a.g * ((a.Nq + tile - 1) / tile);   // of a tile that all see
