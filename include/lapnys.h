@@ -292,7 +292,8 @@ int lapnys_block_bwd(const void* x, const void* w_qkv, const void* w_o, const vo
  *    norm at two keys, with it by 2e-3).
  *  - fp32 arithmetic; bf16 tensors: products of bf16 operands with fp32 sums,
  *    P and (for dk) dS rounded to bf16 between products, outputs rounded once.
- *    fp32 tensors: magnitudes above bf16's largest (3.39e38) count as infinite.
+ *    fp32 tensors: magnitudes above bf16's largest (3.39e38) count as infinite, and
+ *    those below 2^-110 are held to 2^-134 (three bf16 parts), not to 24 bits.
  *  - Deterministic.  One workspace per call in flight, of
  *    lapnys_window_workspace_bytes (may be 0: ws NULL); 0 also for invalid
  *    arguments. */
