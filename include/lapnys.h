@@ -354,6 +354,60 @@ int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cac
                            int right, int sinks, float scale, cudaStream_t stream, int dtype,
                            void* ws, size_t ws_bytes);
 
+/* ---- rotary positions ---------------------------------------------------
+ * Pairs of features of q [B][Hq][N][d] and k [B][Hkv][N][d] (k NULL with
+ * Hkv = 0: q alone) turned by the token's position p:
+ *     (a, b) -> factor (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p w_i,
+ * pair i < rot / 2 being features (i, i + rot / 2) (LAPNYS_HALF) or (2 i, 2 i + 1)
+ * (LAPNYS_INTERLEAVED); features from rot (even, 2 .. d) on are copied.
+ *  - turns: rot / 2 words, w_i in units of 2^-64 of a turn (p w_i is taken modulo
+ *    a turn exactly, for any p).
+ *  - p = start[b] + n (start int32 [B], NULL: 0), or positions[b][n] (int32
+ *    [B][N]); not both.
+ *  - inverse != 0 turns back (by the same factor): the gradient.
+ *  - q_out, k_out: like q, k; each may be its input itself, and overlaps nothing
+ *    else.  Any alignment of the elements' own (16 bytes, with d, rot and, in the
+ *    half layout, rot / 2 multiples of 16 bytes of elements, is faster). */
+#define LAPNYS_HALF 0
+#define LAPNYS_INTERLEAVED 1
+int lapnys_rotary(const void* q, const void* k, void* q_out, void* k_out, const uint64_t* turns,
+                  const int32_t* start, const int32_t* positions, int B, int Hq, int Hkv, int N,
+                  int d, int rot, int layout, float factor, int inverse, cudaStream_t stream,
+                  int dtype);
+
+/* ---- the residual of a block with the norms around it -------------------
+ *     h = x + m n(u),  m = gate scale,  n(u) = unit(u) post_weight + post_bias
+ *     y = unit(h) weight + bias
+ * over rows of C features; unit(z) = z / sqrt(mean(z^2) + eps) (LAPNYS_RMS) or
+ * (z - mean(z)) / sqrt(mean((z - mean(z))^2) + eps) (LAPNYS_LAYER).  pre is the
+ * norm of h, post that of u; LAPNYS_NONE: y is not formed, n(u) = u.
+ *  - x, u, h, y [B][N][C] of `dtype`, any alignment of the elements' own (16 bytes
+ *    and C a multiple of 16 bytes of elements is faster); C <= 16384
+ *    (LAPNYS_ENOTSUP above).  u NULL: h = x, and h may be NULL.  h is rounded once,
+ *    y is formed from it before its rounding.
+ *  - weight, bias [C], or [B][C] with per_seq; gate [B][C]; scale, post_weight,
+ *    post_bias [C]; each of `dtype`, or NULL: 1 (bias: 0).  A vector of something
+ *    that is not there is LAPNYS_EINVAL.
+ *  - stats (16-byte aligned, float [B N][4]) is what the backward needs; may be NULL.
+ * lapnys_norm_bwd: dh, dy are the outputs' gradients (NULL: 0), the others the
+ * inputs' (NULL: not wanted).  Sums are float32 in a fixed order.  Workspace:
+ * lapnys_norm_workspace_bytes (seqs != 0 with a gate or per_seq), only where a
+ * gradient of a vector is wanted. */
+#define LAPNYS_NONE 0
+#define LAPNYS_RMS 1
+#define LAPNYS_LAYER 2
+size_t lapnys_norm_workspace_bytes(int B, int N, int C, int seqs);
+int lapnys_norm_fwd(const void* x, const void* u, const void* weight, const void* bias,
+                    const void* post_weight, const void* post_bias, const void* gate,
+                    const void* scale, void* h, void* y, float* stats, int B, int N, int C,
+                    int per_seq, int pre, int post, float eps, cudaStream_t stream, int dtype);
+int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void* post_weight,
+                    const void* post_bias, const void* gate, const void* scale, const float* stats,
+                    const void* dh, const void* dy, void* dx, void* du, void* dweight, void* dbias,
+                    void* dpost_weight, void* dpost_bias, void* dgate, void* dscale, int B, int N,
+                    int C, int per_seq, int pre, int post, cudaStream_t stream, int dtype, void* ws,
+                    size_t ws_bytes);
+
 /* Synchronises the current device and reports what kernels recorded since the
  * last clear: LAPNYS_ETIMEOUT if a bounded device-side wait (tensor-core
  * pipeline barriers) expired (the affected results are invalid), LAPNYS_EPAGE if

@@ -15,6 +15,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblapnys.s
  LAPNYS_ESCRATCH, LAPNYS_EPAGE) = range(8)
 LAPNYS_F32, LAPNYS_BF16 = 0, 1
 LAPNYS_NORM, LAPNYS_GAUSS, LAPNYS_NORM_BATCH = 1, 2, 4
+LAPNYS_HALF, LAPNYS_INTERLEAVED = 0, 1
+LAPNYS_NONE, LAPNYS_RMS, LAPNYS_LAYER = 0, 1, 2
 
 # every symbol include/lapnys.h declares
 EXPORTS = (
@@ -26,6 +28,7 @@ EXPORTS = (
     "lapnys_fma_probe",
     "lapnys_window_workspace_bytes", "lapnys_window_fwd", "lapnys_window_bwd",
     "lapnys_cache_append", "lapnys_cache_workspace_bytes", "lapnys_cache_attention",
+    "lapnys_rotary", "lapnys_norm_workspace_bytes", "lapnys_norm_fwd", "lapnys_norm_bwd",
 )
 
 
@@ -104,6 +107,14 @@ def load() -> ctypes.CDLL:
     lib.lapnys_cache_workspace_bytes.restype = S
     lib.lapnys_cache_attention.argtypes = [P] * 9 + [I] * 11 + [F, P, I, P, S]
     lib.lapnys_cache_attention.restype = I
+    lib.lapnys_rotary.argtypes = [P] * 7 + [I] * 7 + [F, I, P, I]
+    lib.lapnys_rotary.restype = I
+    lib.lapnys_norm_workspace_bytes.argtypes = [I] * 4
+    lib.lapnys_norm_workspace_bytes.restype = S
+    lib.lapnys_norm_fwd.argtypes = [P] * 11 + [I] * 6 + [F, P, I]
+    lib.lapnys_norm_fwd.restype = I
+    lib.lapnys_norm_bwd.argtypes = [P] * 18 + [I] * 6 + [P, I, P, S]
+    lib.lapnys_norm_bwd.restype = I
     _lib = lib
     return lib
 

@@ -1,0 +1,491 @@
+// The residual of a block with the norms around it:
+//
+//   h = x + m n(u),  m = gate scale,  n(u) = unit(u) post_weight + post_bias,
+//   y = unit(h) weight + bias,        unit(z) = (z - mean) / sqrt(var + eps)
+//                                     or  z / sqrt(mean of z^2 + eps).
+//
+// Backward, with e = dy weight and means over the row's features:
+//   dh' = dh + r_h (e - mean(e) - unit(h) mean(e unit(h)))     (no mean(e): root mean square)
+//   dx = dh',  du = the same of (dh' m post_weight) through unit(u),
+//   dweight = sum dy unit(h), dbias = sum dy, and with S3 = sum dh' unit(u),
+//   S4 = sum dh' over a sequence's rows: dpost_weight = sum_b m S3,
+//   dpost_bias = sum_b m S4, dgate = scale (post_weight S3 + post_bias S4),
+//   dscale = sum_b gate (post_weight S3 + post_bias S4).
+//
+// Bound by memory: a row is read once, kept in registers (16 features a thread) and
+// written once; h is formed again from x and u in the backward, which reads as much
+// as h would and has no rounding in it.  Statistics are of centred values, in fp32,
+// by one warp for rows of up to 512 features (no barrier), by more above.  The
+// backward's sums over rows stay in registers over a block's rows, are joined over
+// its row groups in shared memory and over the blocks by k_norm_seq, in one order.
+#include "common.cuh"
+#include "internal.h"
+#include "layer.cuh"
+
+namespace lapnys {
+namespace {
+
+__device__ __forceinline__ float as_f(float x) { return x; }
+__device__ __forceinline__ float as_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// the EPT features of a thread's share of a row: pieces of 16 bytes, `threads`
+// pieces apart (WIDE), or single ones
+template <typename T, int EPT, bool WIDE>
+struct Share {
+  static constexpr int V = WIDE ? 16 / (int)sizeof(T) : 1;
+  static constexpr int NP = EPT / V;
+  struct Raw {
+    uint4 w[WIDE ? NP : 1];
+    T s[WIDE ? 1 : EPT];
+  };
+  int t, threads, C;
+  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * V; }
+  __device__ __forceinline__ Raw raw(const T* p) const {
+    Raw r;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c = col(j);
+      if constexpr (WIDE)
+        r.w[j] = c < C ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+      else
+        r.s[j] = c < C ? p[c] : T(0.f);
+    }
+    return r;
+  }
+  __device__ __forceinline__ static void open(const Raw& r, float (&v)[EPT]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if constexpr (!WIDE) {
+        v[j] = as_f(r.s[j]);
+      } else if constexpr (sizeof(T) == 4) {
+        v[4 * j] = __uint_as_float(r.w[j].x);
+        v[4 * j + 1] = __uint_as_float(r.w[j].y);
+        v[4 * j + 2] = __uint_as_float(r.w[j].z);
+        v[4 * j + 3] = __uint_as_float(r.w[j].w);
+      } else {
+        const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
+          v[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const T* p, float (&v)[EPT]) const { open(raw(p), v); }
+  __device__ __forceinline__ void store(T* p, const float (&v)[EPT]) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c = col(j);
+      if (c >= C) continue;
+      if constexpr (!WIDE) {
+        from_f(p + c, v[j]);
+      } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p + c) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  // whether element i of the share lies in the row
+  __device__ __forceinline__ bool in(int i) const { return col(i / V) < C; }
+};
+
+// sums over the `warps` warps of a row group: by shuffles, then shared memory
+struct RowSum {
+  float2* slot;     // [2][32] of this group
+  int warps, group, threads;
+  int turn = 0;
+  __device__ __forceinline__ float2 operator()(float2 v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if (warps == 1) return v;
+    float2* s = slot + 32 * turn;
+    turn ^= 1;      // the other half is free again after the next barrier
+    const int w = (threadIdx.x >> 5) % warps;
+    if ((threadIdx.x & 31) == 0) s[w] = v;
+    asm volatile("barrier.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    v = make_float2(0.f, 0.f);
+    for (int i = 0; i < warps; ++i) {
+      v.x += s[i].x;
+      v.y += s[i].y;
+    }
+    return v;
+  }
+  __device__ __forceinline__ float operator()(float v) { return (*this)(make_float2(v, 0.f)).x; }
+};
+
+// mean and 1 / deviation of a row's values
+template <typename S, int EPT>
+__device__ __forceinline__ float2 row_stats(const float (&z)[EPT], int kind, float eps, const S& sh,
+                                            RowSum& sum) {
+  float mean = 0.f;
+  const float inv = 1.f / (float)sh.C;
+  if (kind == kNormLayer) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) t += z[i];       // 0 behind the row
+    mean = sum(t) * inv;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const float e = sh.in(i) ? z[i] - mean : 0.f;
+    q = fmaf(e, e, q);
+  }
+  return make_float2(mean, rsqrtf(sum(q) * inv + eps));
+}
+
+template <typename T, int EPT, bool WIDE>
+struct Rows {
+  Share<T, EPT, WIDE> sh;
+  RowSum sum;
+  int group, groups;
+  __device__ __forceinline__ Rows(const NormArgs& a, int warps, float2 (*slots)[64]) {
+    const int warp = threadIdx.x >> 5;
+    group = warp / warps;
+    groups = (blockDim.x >> 5) / warps;
+    sh.threads = 32 * warps;
+    sh.t = threadIdx.x - group * sh.threads;
+    sh.C = a.C;
+    sum.slot = slots[group];
+    sum.warps = warps;
+    sum.group = group;
+    sum.threads = sh.threads;
+  }
+};
+
+// weight and bias of this thread's features, applied
+template <typename S, typename T, int EPT>
+__device__ __forceinline__ void affine(const S& sh, const T* w, const T* b, float (&v)[EPT]) {
+  float t[EPT];
+  if (w) {
+    sh.load(w, t);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) v[i] *= t[i];
+  }
+  if (b) {
+    sh.load(b, t);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) v[i] += t[i];
+  }
+}
+template <typename S, typename T, int EPT>
+__device__ __forceinline__ void times(const S& sh, const T* w, float (&v)[EPT]) {
+  affine(sh, w, (const T*)nullptr, v);
+}
+
+template <typename T, int EPT, bool WIDE, int TB>
+__global__ void __launch_bounds__(TB) k_norm_fwd(NormArgs a, int warps) {
+  __shared__ float2 slots[8][64];
+  Rows<T, EPT, WIDE> r(a, warps, slots);
+  const auto& sh = r.sh;
+  const long long rows = (long long)a.B * a.N;
+  for (long long row = (long long)blockIdx.x * r.groups + r.group; row < rows;
+       row += (long long)gridDim.x * r.groups) {
+    const size_t at = (size_t)row * a.C;
+    const size_t seq = (size_t)(row / a.N) * a.C;
+    float h[EPT];
+    float2 su = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+    const auto xr = sh.raw((const T*)a.x + at);
+    if (a.u) {
+      float u[EPT], x[EPT];
+      sh.load((const T*)a.u + at, u);
+      if (a.post != kNormNone) {
+        su = row_stats(u, a.post, a.eps, sh, r.sum);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) u[i] = (u[i] - su.x) * su.y;
+        affine(sh, (const T*)a.post_weight, (const T*)a.post_bias, u);
+      }
+      if (a.gate) times(sh, (const T*)a.gate + seq, u);
+      times(sh, (const T*)a.scale, u);
+      sh.open(xr, x);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) h[i] = sh.in(i) ? x[i] + u[i] : 0.f;
+      if (a.h) sh.store((T*)a.h + at, h);
+    } else {
+      sh.open(xr, h);
+      if (a.h) sh.store((T*)a.h + at, h);
+    }
+    if (a.y) {
+      s = row_stats(h, a.pre, a.eps, sh, r.sum);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) h[i] = (h[i] - s.x) * s.y;
+      const size_t of = a.per_seq ? seq : 0;
+      affine(sh, a.weight ? (const T*)a.weight + of : nullptr,
+             a.bias ? (const T*)a.bias + of : nullptr, h);
+      sh.store((T*)a.y + at, h);
+    }
+    if (a.stats && sh.t == 0)
+      reinterpret_cast<float4*>(a.stats)[row] = make_float4(su.x, su.y, s.x, s.y);
+  }
+}
+
+// A block takes one range of one sequence's rows: blockIdx.x = b * parts + part.
+template <typename T, int EPT, bool WIDE, int TB>
+__global__ void __launch_bounds__(TB) k_norm_bwd(NormArgs a, int warps) {
+  __shared__ float2 slots[8][64];
+  extern __shared__ float join[];          // [4][C], where a block has several row groups
+  Rows<T, EPT, WIDE> r(a, warps, slots);
+  const auto& sh = r.sh;
+  const int b = blockIdx.x / a.parts, part = blockIdx.x - b * a.parts;
+  const int n0 = (int)((long long)a.N * part / a.parts), n1 = (int)((long long)a.N * (part + 1) / a.parts);
+  const size_t seq = (size_t)b * a.C;
+  const float inv = 1.f / (float)a.C;
+  float A[4][EPT];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) A[k][i] = 0.f;
+  for (int n = n0 + r.group; n < n1; n += r.groups) {
+    const size_t row = (size_t)b * a.N + n, at = row * a.C;
+    const float4 st = reinterpret_cast<const float4*>(a.stats)[row];
+    float uh[EPT], hh[EPT], d[EPT];
+    const auto xr = sh.raw((const T*)a.x + at);
+    if (a.u) {
+      float t[EPT];
+      sh.load((const T*)a.u + at, uh);
+      if (a.post != kNormNone)
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) uh[i] = (uh[i] - st.x) * st.y;
+      sh.open(xr, hh);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) t[i] = uh[i];
+      if (a.post != kNormNone) affine(sh, (const T*)a.post_weight, (const T*)a.post_bias, t);
+      if (a.gate) times(sh, (const T*)a.gate + seq, t);
+      times(sh, (const T*)a.scale, t);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) hh[i] += t[i];
+    } else {
+      sh.open(xr, hh);
+    }
+    if (a.dh) {
+      sh.load((const T*)a.dh + at, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) d[i] = 0.f;
+    }
+    if (a.dy) {
+      float e[EPT];
+      sh.load((const T*)a.dy + at, e);
+      float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        hh[i] = (hh[i] - st.z) * st.w;
+        A[0][i] = fmaf(e[i], hh[i], A[0][i]);
+        A[1][i] += e[i];
+      }
+      if (a.weight) times(sh, (const T*)a.weight + (a.per_seq ? seq : 0), e);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {     // e is 0 behind the row
+        m.x = fmaf(e[i], hh[i], m.x);
+        m.y += e[i];
+      }
+      m = r.sum(m);
+      const float m1 = m.x * inv, m0 = a.pre == kNormLayer ? m.y * inv : 0.f;
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) d[i] = fmaf(st.w, e[i] - m0 - hh[i] * m1, d[i]);
+    }
+    if (a.dx) sh.store((T*)a.dx + at, d);
+    if (a.u) {
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        A[2][i] = fmaf(d[i], uh[i], A[2][i]);
+        A[3][i] += d[i];
+      }
+      if (a.gate) times(sh, (const T*)a.gate + seq, d);
+      times(sh, (const T*)a.scale, d);
+      if (a.post != kNormNone) {
+        times(sh, (const T*)a.post_weight, d);
+        float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          const float e = sh.in(i) ? d[i] : 0.f;
+          m.x = fmaf(e, uh[i], m.x);
+          m.y += e;
+        }
+        m = r.sum(m);
+        const float m1 = m.x * inv, m0 = a.post == kNormLayer ? m.y * inv : 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) d[i] = st.y * (d[i] - m0 - uh[i] * m1);
+      }
+      if (a.du) sh.store((T*)a.du + at, d);
+    }
+  }
+  if (a.sums == 0) return;
+  constexpr int V = Share<T, EPT, WIDE>::V;
+  float* out = a.part + (size_t)blockIdx.x * 4 * a.C;
+  if (r.groups > 1) {
+    for (int g = 0; g < r.groups; ++g) {
+      if (r.group == g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (a.sums >> k & 1)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+              if (sh.in(i)) {
+                const int c = k * a.C + sh.col(i / V) + i % V;
+                join[c] = g ? join[c] + A[k][i] : A[k][i];
+              }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 4 * a.C; c += blockDim.x)
+      if (a.sums >> (c / a.C) & 1) out[c] = join[c];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (a.sums >> k & 1)
+#pragma unroll
+        for (int i = 0; i < EPT; ++i)
+          if (sh.in(i)) out[k * a.C + sh.col(i / V) + i % V] = A[k][i];
+  }
+}
+
+constexpr int JY = 32;   // threads that share a column of the joins
+
+// seq[b][k][c] = sum over the parts of a sequence: part y, y + 32, .. by thread y, then
+// the threads' sums in order
+__global__ void __launch_bounds__(32 * JY) k_norm_seq(NormArgs a) {
+  __shared__ float s[JY][33];
+  const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y, b = blockIdx.z;
+  if (!(a.sums >> k & 1)) return;
+  float t = 0.f;
+  if (c < a.C)
+#pragma unroll 4
+    for (int p = threadIdx.y; p < a.parts; p += JY) t += a.part[(((size_t)b * a.parts + p) * 4 + k) * a.C + c];
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < a.C) {
+#pragma unroll
+    for (int y = 1; y < JY; ++y) t += s[y][threadIdx.x];
+    a.seq[((size_t)b * 4 + k) * a.C + c] = t;
+  }
+}
+
+// the gradients of the vectors from the sequences' sums: sequences y, y + 32, .. by
+// thread y, then the threads' sums in order
+template <typename T>
+__global__ void __launch_bounds__(32 * JY) k_norm_final(NormArgs a) {
+  __shared__ float s[5][JY][33];
+  const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
+  float t[5] = {0.f, 0.f, 0.f, 0.f, 0.f};   // weight, bias, post weight, post bias, scale
+  if (c < a.C) {
+    auto at = [&](const void* p, size_t i, float none) { return p ? as_f(((const T*)p)[i]) : none; };
+    const float pw = at(a.post_weight, c, 1.f), pb = at(a.post_bias, c, 0.f), sc = at(a.scale, c, 1.f);
+#pragma unroll 4
+    for (int b = y; b < a.B; b += JY) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = a.sums >> k & 1 ? a.seq[((size_t)b * 4 + k) * a.C + c] : 0.f;
+      const size_t i = (size_t)b * a.C + c;
+      const float g = at(a.gate, i, 1.f), G = pw * v[2] + pb * v[3];
+      if (a.per_seq) {
+        if (a.dweight) from_f((T*)a.dweight + i, v[0]);
+        if (a.dbias) from_f((T*)a.dbias + i, v[1]);
+      }
+      if (a.dgate) from_f((T*)a.dgate + i, sc * G);
+      t[0] += v[0];
+      t[1] += v[1];
+      t[2] = fmaf(g * sc, v[2], t[2]);
+      t[3] = fmaf(g * sc, v[3], t[3]);
+      t[4] = fmaf(g, G, t[4]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 5; ++k) s[k][y][threadIdx.x] = t[k];
+  __syncthreads();
+  if (y < 5 && c < a.C) {
+    void* out[5] = {a.per_seq ? nullptr : a.dweight, a.per_seq ? nullptr : a.dbias, a.dpost_weight,
+                    a.dpost_bias, a.dscale};
+    float v = 0.f;
+    for (int i = 0; i < JY; ++i) v += s[y][i][threadIdx.x];
+    void* o = y == 0 ? out[0] : y == 1 ? out[1] : y == 2 ? out[2] : y == 3 ? out[3] : out[4];
+    if (o) from_f((T*)o + c, v);
+  }
+}
+
+// features a thread, warps a row, row groups a block
+struct Shape {
+  int ept, warps, groups;
+};
+Shape shape(int C) {
+  Shape s;
+  s.ept = C <= 256 ? 8 : 16;
+  s.warps = (C + 32 * s.ept - 1) / (32 * s.ept);
+  s.groups = s.warps < 8 ? 8 / s.warps : 1;
+  return s;
+}
+
+template <typename T, int EPT, bool WIDE>
+cudaError_t go(const NormArgs& a, bool backward, const Shape& s, cudaStream_t st) {
+  const int threads = 32 * s.warps * s.groups;
+  const dim3 block(threads);
+  if (!backward) {
+    const long long rows = (long long)a.B * a.N, all = (rows + s.groups - 1) / s.groups;
+    const dim3 grid((unsigned)(all < 152 * 64 ? all : 152 * 64));
+    if (threads <= 256)
+      return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 256>, grid, block, 0, st, a, s.warps);
+    return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 1024>, grid, block, 0, st, a, s.warps);
+  }
+  const dim3 grid((unsigned)(a.B * a.parts));
+  const size_t smem = s.groups > 1 ? 16 * (size_t)a.C : 0;
+  if (threads <= 256)
+    return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 256>, grid, block, smem, st, a, s.warps);
+  if (threads <= 512)
+    return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 512>, grid, block, smem, st, a, s.warps);
+  return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 1024>, grid, block, smem, st, a, s.warps);
+}
+
+template <typename T>
+cudaError_t pick(const NormArgs& a, bool backward, cudaStream_t st) {
+  const Shape s = shape(a.C);
+  bool wide = a.C % (16 / (int)sizeof(T)) == 0;
+  const void* all[] = {a.x, a.u, a.weight, a.bias, a.post_weight, a.post_bias, a.gate, a.scale,
+                       a.h, a.y, a.dh, a.dy, a.dx, a.du};
+  for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
+  if (s.ept == 8) return wide ? go<T, 8, true>(a, backward, s, st) : go<T, 8, false>(a, backward, s, st);
+  return wide ? go<T, 16, true>(a, backward, s, st) : go<T, 16, false>(a, backward, s, st);
+}
+
+}  // namespace
+
+// ranges of a sequence's rows: blocks for two an SM, each group of a block eight rows
+// or more
+int norm_parts(int B, int N, int C) {
+  const Shape s = shape(C);
+  const long long most = (N + 8LL * s.groups - 1) / (8LL * s.groups), want = (304 + B - 1) / B;
+  const long long p = want < most ? want : most;
+  return (int)(p < 1 ? 1 : p);
+}
+
+cudaError_t run_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t st) {
+  return bf16 ? pick<__nv_bfloat16>(a, false, st) : pick<float>(a, false, st);
+}
+
+cudaError_t run_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t st) {
+  cudaError_t e = bf16 ? pick<__nv_bfloat16>(a, true, st) : pick<float>(a, true, st);
+  if (e != cudaSuccess || a.sums == 0) return e;
+  NormArgs f = a;
+  const unsigned cols = (unsigned)((a.C + 31) / 32);
+  if (a.parts > 1) {
+    e = launch("norm_seq", k_norm_seq, dim3(cols, 4, (unsigned)a.B), dim3(32, JY), 0, st, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    f.seq = a.part;
+  }
+  if (bf16) return launch("norm_final", k_norm_final<__nv_bfloat16>, dim3(cols), dim3(32, JY), 0, st, f);
+  return launch("norm_final", k_norm_final<float>, dim3(cols), dim3(32, JY), 0, st, f);
+}
+
+}  // namespace lapnys
