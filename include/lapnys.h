@@ -408,6 +408,30 @@ int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void
                     int C, int per_seq, int pre, int post, cudaStream_t stream, int dtype, void* ws,
                     size_t ws_bytes);
 
+/* ---- the gated feed-forward block ---------------------------------------
+ *     (g | u) = x w_in + b_in,  h = act(g) u,  y = h w_out + b_out
+ * x, y [T][C], w_in [C][2 F] (the gate's columns, then the others), w_out [F][C],
+ * b_in [2 F], b_out [C] (biases may be NULL), all of `dtype`, 16-byte aligned; any
+ * T <= 2^28, C, F <= 2^20 (C and F multiples of 8 in bf16 are read where they lie,
+ * others through copies in the workspace).  act: z / (1 + exp(-z)) (LAPNYS_SILU),
+ * z (1 + erf(z / sqrt 2)) / 2 (LAPNYS_GELU), or its tanh form (LAPNYS_GELU_TANH).
+ * Sums are float32 (bf16 calls round h, and in the backward the gradient of (g | u),
+ * to bf16 between the products); results repeat bit for bit.
+ *  - ctx (lapnys_mlp_ctx_bytes): what the backward needs; NULL: none.
+ *  - lapnys_mlp_bwd: gradients that are NULL are not computed.
+ * Workspaces: lapnys_mlp_workspace_bytes. */
+#define LAPNYS_SILU 0
+#define LAPNYS_GELU 1
+#define LAPNYS_GELU_TANH 2
+size_t lapnys_mlp_ctx_bytes(int T, int C, int F, int dtype);
+size_t lapnys_mlp_workspace_bytes(int T, int C, int F, int dtype, int backward);
+int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void* w_out,
+                   const void* b_out, void* y, int T, int C, int F, int act, cudaStream_t stream,
+                   int dtype, void* ctx, size_t ctx_bytes, void* ws, size_t ws_bytes);
+int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const void* dy,
+                   const void* ctx, void* dx, void* dw_in, void* db_in, void* dw_out, void* db_out,
+                   int T, int C, int F, cudaStream_t stream, int dtype, void* ws, size_t ws_bytes);
+
 /* Synchronises the current device and reports what kernels recorded since the
  * last clear: LAPNYS_ETIMEOUT if a bounded device-side wait (tensor-core
  * pipeline barriers) expired (the affected results are invalid), LAPNYS_EPAGE if

@@ -17,6 +17,7 @@ LAPNYS_F32, LAPNYS_BF16 = 0, 1
 LAPNYS_NORM, LAPNYS_GAUSS, LAPNYS_NORM_BATCH = 1, 2, 4
 LAPNYS_HALF, LAPNYS_INTERLEAVED = 0, 1
 LAPNYS_NONE, LAPNYS_RMS, LAPNYS_LAYER = 0, 1, 2
+LAPNYS_SILU, LAPNYS_GELU, LAPNYS_GELU_TANH = 0, 1, 2
 
 # every symbol include/lapnys.h declares
 EXPORTS = (
@@ -29,6 +30,7 @@ EXPORTS = (
     "lapnys_window_workspace_bytes", "lapnys_window_fwd", "lapnys_window_bwd",
     "lapnys_cache_append", "lapnys_cache_workspace_bytes", "lapnys_cache_attention",
     "lapnys_rotary", "lapnys_norm_workspace_bytes", "lapnys_norm_fwd", "lapnys_norm_bwd",
+    "lapnys_mlp_ctx_bytes", "lapnys_mlp_workspace_bytes", "lapnys_mlp_fwd", "lapnys_mlp_bwd",
 )
 
 
@@ -115,6 +117,14 @@ def load() -> ctypes.CDLL:
     lib.lapnys_norm_fwd.restype = I
     lib.lapnys_norm_bwd.argtypes = [P] * 18 + [I] * 6 + [P, I, P, S]
     lib.lapnys_norm_bwd.restype = I
+    lib.lapnys_mlp_ctx_bytes.argtypes = [I] * 4
+    lib.lapnys_mlp_ctx_bytes.restype = S
+    lib.lapnys_mlp_workspace_bytes.argtypes = [I] * 5
+    lib.lapnys_mlp_workspace_bytes.restype = S
+    lib.lapnys_mlp_fwd.argtypes = [P] * 6 + [I] * 4 + [P, I, P, S, P, S]
+    lib.lapnys_mlp_fwd.restype = I
+    lib.lapnys_mlp_bwd.argtypes = [P] * 10 + [I] * 3 + [P, I, P, S]
+    lib.lapnys_mlp_bwd.restype = I
     _lib = lib
     return lib
 

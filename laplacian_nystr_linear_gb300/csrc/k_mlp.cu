@@ -1,0 +1,867 @@
+// The products of the gated feed-forward block on the tcgen05 tensor cores, by pairs
+// of CTAs (cta_group::2), with the activation, its gradient and the biases in the
+// epilogues.  T rows, C features, F hidden (sizes M x N x K):
+//     forward   g | u = x w_in, h = act(g) u       T x 2 F x C   epilogue: glu
+//               y = h w_out                        T x C x F     rows
+//     backward  dh = dy w_out^T, dg = dh q,
+//               du = dh p                          T x F x C     dglu
+//               dx = (dg | du) w_in^T              T x C x 2 F   rows
+//               dw_in = x^T (dg | du)              C x 2 F x T   rows or part
+//               dw_out = h^T dy                    F x C x T     rows or part
+//
+// A pair computes 256 x 256 of D = sum_k A(m, k) B(n, k): each CTA copies its 128 rows
+// of A and 128 of the 256 rows of B, 32 KB a step of 64 k (a single CTA's 128 x 256 tile
+// would take 48 KB for half the work, and L2 gives all SMs about 64 bytes a cycle each
+// at the tensor cores' rate).  The leader's one thread issues the products for both.  In
+// the glu product the leader's rows of B are the gate's columns, its partner's the
+// other half's: both halves of a hidden feature land in one row of tensor memory.
+//
+// Operands lie as the tensors do, K contiguous (K-major) or not (MN-major), in the
+// 128-byte swizzle; maps of four dimensions {inner, part, row, plane} fill what lies
+// behind a row, a part (g | u) or the last row with zeros.
+//
+// fp32 operands are three bf16 planes each (24 bits) and a product six of theirs, a0 b0
+// apart from the five smaller ones in tensor memory: the instruction cuts its sums off,
+// which costs 2^-24 of the sum or so each time, so a0 b0 is summed over KCH steps there
+// and by the epilogue's threads, in registers, beyond; the others together are 2^-8 of
+// the sum.  A step's planes are copied once and read from shared memory by all six.
+//
+// 384 threads a CTA: warp 0 copies (one thread, a ring of NST slots), warp 1 issues
+// (leader) and holds the tensor memory, warps 4 to 11 read the accumulators, a row a
+// thread, half the columns each, while the next tile accumulates.  Every wait is
+// bounded; a role whose wait expired sets the error word and stops issuing, and all
+// threads meet at the cluster barrier before tensor memory is freed.
+#include <cuda_fp16.h>
+
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mlp.cuh"
+#include "win_tc.cuh"
+
+namespace lapnys {
+namespace {
+
+constexpr int BM = 128;                  // rows of A a CTA
+constexpr int BK = kMlpTileK;
+constexpr int NTH = 384;
+constexpr int EPW = 8;                   // epilogue warps
+constexpr int GROUP = 8;                 // tiles of M that tiles of N are run over together
+constexpr uint32_t BLK64 = 64 * BK * 2;  // 64 rows of an MN-major operand: 8 KB
+
+template <bool F32>
+struct Cfg {
+  static constexpr int BN = F32 ? 128 : 256;        // columns of a pair's tile
+  static constexpr int BNC = BN / 2;                // rows of B a CTA
+  static constexpr uint32_t A_BYTES = BM * BK * 2;
+  static constexpr uint32_t B_BYTES = BNC * BK * 2;
+  static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
+  static constexpr int NST = F32 ? 9 : 6;
+  static constexpr int PLANES = F32 ? 3 : 1;
+  static constexpr int KCH = F32 ? 2 : 1 << 30;     // K steps of an accumulator
+  static constexpr uint32_t SMEM = NST * SLOT + 1024;
+};
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+__device__ __forceinline__ uint32_t rank_of_cta() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the leader's copy of a shared-memory address of this CTA
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// mbarrier wait that also orders what the partner CTA did before its arrival
+__device__ __forceinline__ bool wait_pair(int* err, uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < tc::kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  atomicOr(err, 1);
+  return false;
+}
+__device__ __forceinline__ void arrive_leader(uint32_t remote) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+// a tile into this CTA's shared memory, its bytes counted on the leader's barrier
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                     int c3, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(mbar)
+      : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// arrives on the barrier of both CTAs when all products issued so far are done
+__device__ __forceinline__ void commit2(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          mbar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// barrier of the epilogue's warps (named barrier 1) that ORs a flag over them
+__device__ __forceinline__ bool epilogue_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+struct Item {
+  int m0, n0, part, ks0, ks1, sp;   // n0: first column of the tile in its part
+};
+template <int TN>
+__device__ __forceinline__ Item decode(const MlpGemmArgs& a, long long it) {
+  Item r;
+  const int ntot = a.nt * a.nparts;
+  const long long tiles = (long long)a.mt * ntot;
+  r.sp = (int)(it / tiles);
+  const long long t = it - r.sp * tiles;
+  const int g = (int)(t / ((long long)GROUP * ntot)), first = g * GROUP;
+  const int gm = min(GROUP, a.mt - first);
+  const int q = (int)(t - (long long)g * GROUP * ntot);
+  const int n = q / gm;
+  r.m0 = (first + q - n * gm) * (2 * BM);
+  r.part = n / a.nt;
+  r.n0 = (n - r.part * a.nt) * TN;
+  const int all = a.kst * a.kparts;
+  r.ks0 = (int)((long long)all * r.sp / a.splits);
+  r.ks1 = (int)((long long)all * (r.sp + 1) / a.splits);
+  return r;
+}
+
+// sixteen consecutive 16-byte pieces' worth of a lane's row: 32 fp32 values
+__device__ __forceinline__ void store_f32(float* tile, size_t ld, int first, int rows, int cols,
+                                          const float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
+                        __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+    wtc::store_rows(tile + 16 * h, 4 * ld, first, rows, (cols - 16 * h + 3) / 4, c);
+  }
+}
+// 32 values of a lane's row as bf16: one plane, or the three of fp32 values
+template <bool F32>
+__device__ __forceinline__ void store_planes(__nv_bfloat16* tile, size_t ld, size_t plane, int first,
+                                             int rows, int cols, const float (&v)[32]) {
+  if constexpr (!F32) {
+    uint4 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = make_uint4(wtc::pack(v[8 * i], v[8 * i + 1]), wtc::pack(v[8 * i + 2], v[8 * i + 3]),
+                        wtc::pack(v[8 * i + 4], v[8 * i + 5]), wtc::pack(v[8 * i + 6], v[8 * i + 7]));
+    wtc::store_rows(tile, 2 * ld, first, rows, (cols + 7) / 8, c);
+  } else {
+    uint32_t w[16][3];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) split3_bf16x2(v[2 * i], v[2 * i + 1], w[i]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint4 c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = make_uint4(w[4 * i][p], w[4 * i + 1][p], w[4 * i + 2][p], w[4 * i + 3][p]);
+      wtc::store_rows(tile + p * plane, 2 * ld, first, rows, (cols + 7) / 8, c);
+    }
+  }
+}
+
+// the power of two 2^e by which a block row's largest finite value falls into [2^14, 2^15)
+__device__ __forceinline__ int row_exponent(float m) {
+  const int e = (int)(__float_as_uint(m) >> 23) - 127 - 14;
+  return max(e, -126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <bool F32>
+__device__ __forceinline__ void keep(const MlpKept& k, size_t block, const float (&p)[32],
+                                     const float (&q)[32]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (F32) {
+    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 2 * 8 * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i * 32] = make_uint4(__float_as_uint(p[4 * i]), __float_as_uint(p[4 * i + 1]),
+                             __float_as_uint(p[4 * i + 2]), __float_as_uint(p[4 * i + 3]));
+      o[(8 + i) * 32] = make_uint4(__float_as_uint(q[4 * i]), __float_as_uint(q[4 * i + 1]),
+                                   __float_as_uint(q[4 * i + 2]), __float_as_uint(q[4 * i + 3]));
+    }
+  } else {
+    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 2 * 4 * 32 + lane;
+    uint32_t word = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* v = h ? q : p;
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float a = fabsf(v[i]);
+        m = fmaxf(m, a <= 3.4e38f ? a : 0.f);
+      }
+      const int e = row_exponent(m);
+      const float f = pow2(-e);
+      word |= (uint32_t)(e + 128) << (8 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 x = __floats2half2_rn(v[8 * i + 2 * j] * f, v[8 * i + 2 * j + 1] * f);
+          w[j] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        o[(4 * h + i) * 32] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    k.scale[block * 32 + lane] = (uint16_t)word;
+  }
+}
+// p (h = 0) or q (h = 1) of a lane's row
+template <bool F32>
+__device__ __forceinline__ void kept(const MlpKept& k, size_t block, int h, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (F32) {
+    const uint4* o = reinterpret_cast<const uint4*>(k.pq) + (block * 2 + h) * 8 * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 w = o[i * 32];
+      v[4 * i] = __uint_as_float(w.x);
+      v[4 * i + 1] = __uint_as_float(w.y);
+      v[4 * i + 2] = __uint_as_float(w.z);
+      v[4 * i + 3] = __uint_as_float(w.w);
+    }
+  } else {
+    const uint4* o = reinterpret_cast<const uint4*>(k.pq) + (block * 2 + h) * 4 * 32 + lane;
+    const float f = pow2((int)((k.scale[block * 32 + lane] >> (8 * h)) & 0xff) - 128);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 c = o[i * 32];
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[8 * i + 2 * j] = x.x * f;
+        v[8 * i + 2 * j + 1] = x.y * f;
+      }
+    }
+  }
+}
+
+template <bool F32, int KIND>
+__device__ __forceinline__ void gate(float (&g)[32], float (&u)[32], float (&h)[32]) {
+  // g becomes p, u becomes q
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float p, s;
+    mlp_act<F32, KIND>(g[i], p, s);
+    h[i] = p * u[i];
+    g[i] = p;
+    u[i] *= s;
+  }
+}
+
+// 32 columns of this lane's row; `first`: the warp's first row in the tile, rows: of the
+// tile that are in M, m0: the CTA's first row
+template <bool F32>
+__device__ __forceinline__ void out_rows(const MlpGemmArgs& a, const Item& r, int m0, int n, int first,
+                                         int rows, const float* bias, float (&v)[32]) {
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  if (bias)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += bias[i];
+  T* tile = (T*)a.out + (size_t)m0 * a.ldo + r.part * a.part_out + n;
+  if (a.wide) {
+    if constexpr (F32)
+      store_f32(tile, a.ldo, first, rows, min(32, a.N - n), v);
+    else
+      store_planes<false>(tile, a.ldo, 0, first, rows, min(32, a.N - n), v);
+    return;
+  }
+  const int row = first + (threadIdx.x & 31);
+  if (row >= rows) return;
+  T* o = tile + (size_t)row * a.ldo;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (n + i < a.N) {
+      if constexpr (F32)
+        o[i] = v[i];
+      else
+        o[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+template <bool F32, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
+    k_mlp_gemm(const __grid_constant__ Maps mp, MlpGemmArgs a) {
+  using G = Cfg<F32>;
+  constexpr int NST = G::NST, BN = G::BN, BNC = G::BNC, TN = EPI == kMlpGlu ? BNC : BN;
+  constexpr int PLANES = G::PLANES, KCH = G::KCH;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full[NST];   // leader: both CTAs' copies landed
+  __shared__ __align__(8) uint64_t empty[NST];  // a slot's products done
+  __shared__ __align__(8) uint64_t accf[2];     // an accumulator's products done
+  __shared__ __align__(8) uint64_t acce[2];     // leader: read out by both CTAs' warps
+  __shared__ uint32_t tmem_s;
+  __shared__ int issued_s, consumed_s, bad_s;
+  __shared__ float bias_s[2][BN];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = rank_of_cta();
+  const uint32_t sm = (tc::smem_u32(sm_raw) + 1023u) & ~1023u;
+  const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32(&tmem_s)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(tc::smem_u32(&full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&accf[i]), 1);
+      tc::mbar_init(tc::smem_u32(&acce[i]), 2 * EPW);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    issued_s = 0;
+    consumed_s = 0;
+    bad_s = 0;
+  }
+  tc::fence_before();
+  __syncthreads();
+  cluster_sync();      // the partner's barriers and tensor memory are there too
+  tc::fence_after();
+  const uint32_t tmem = tmem_s;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    if (wtc::elect_one()) {
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      bool bad = false;
+      for (long long it = pair; it < a.items && !bad; it += pairs) {
+        const Item r = decode<TN>(a, it);
+        const int am = r.m0 + (int)rank * BM;
+        const int bn = EPI == kMlpGlu ? r.n0 : r.n0 + (int)rank * BNC;
+        for (int ks = r.ks0; ks < r.ks1 && !bad; ++ks) {
+          const int kp = a.kparts > 1 ? ks / a.kst : 0, k0 = (ks - kp * a.kst) * BK;
+          const int bp = EPI == kMlpGlu ? (int)rank : (a.kparts > 1 ? kp : r.part);
+#pragma unroll 1
+          for (int p = 0; p < PLANES; ++p) {
+            if (!wait_pair(a.err, tc::smem_u32(&empty[st]), ph ^ 1u)) { bad = true; break; }
+            const uint32_t bar = at_leader(tc::smem_u32(&full[st]));
+            if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[st]), 2 * G::SLOT);
+            const uint32_t sa = sm + st * G::SLOT, sb = sa + G::A_BYTES;
+            if (a.amn) {
+#pragma unroll
+              for (int i = 0; i < BM / 64; ++i) tma4(sa + i * BLK64, &mp.a, am + 64 * i, kp, k0, p, bar);
+            } else {
+              tma4(sa, &mp.a, k0, kp, am, p, bar);
+            }
+            if (a.bmn) {
+#pragma unroll
+              for (int i = 0; i < BNC / 64; ++i) tma4(sb + i * BLK64, &mp.b, bn + 64 * i, bp, k0, p, bar);
+            } else {
+              tma4(sb, &mp.b, k0, bp, bn, p, bar);
+            }
+            ++issued;
+            if (++st == NST) { st = 0; ph ^= 1u; }
+          }
+        }
+      }
+      // the products of the last slots are done in both CTAs: their arrivals here come
+      // before this CTA ends
+      for (int i = 0; i < NST && i < issued && !bad; ++i) {
+        const int k = issued - 1 - i;
+        bad = !wait_pair(a.err, tc::smem_u32(&empty[k % NST]), (uint32_t)(k / NST) & 1u);
+      }
+      issued_s = issued;
+      if (bad) atomicOr(&bad_s, 1);
+    }
+  } else if (warp == 1) {
+    // ---------------- products, of the leader ----------------
+    if (rank == 0 && wtc::elect_one()) {
+      int st = 0, consumed = 0;
+      uint32_t ph = 0, u = 0;           // u: accumulators used so far
+      long long li = 0;
+      bool bad = false;
+      const uint32_t id = tc::idesc_bf16(2 * BM, BN) | (a.amn ? 1u << 15 : 0u) | (a.bmn ? 1u << 16 : 0u);
+      // K slices of 16: 32 bytes on in a K-major row, 16 rows on in an MN-major block
+      const uint64_t sta = (a.amn ? 2048 : 32) >> 4, stb = (a.bmn ? 2048 : 32) >> 4;
+      const uint64_t da0 = a.amn ? wtc::desc_mn(sm, BLK64) : wtc::desc_k(sm);
+      const uint64_t db0 = a.bmn ? wtc::desc_mn(sm + G::A_BYTES, BLK64) : wtc::desc_k(sm + G::A_BYTES);
+      for (long long it = pair; it < a.items && !bad; it += pairs, ++li) {
+        const Item r = decode<TN>(a, it);
+        const uint32_t small = tmem + 256 + (uint32_t)(li & 1) * 128;   // F32
+        for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
+          const int k1 = KCH < r.ks1 - k0 ? k0 + KCH : r.ks1;
+          const int acc = (int)(u & 1);
+          if (!wait_pair(a.err, tc::smem_u32(&acce[acc]), ((u >> 1) & 1u) ^ 1u)) { bad = true; break; }
+          tc::fence_after();
+          const uint32_t d = tmem + (uint32_t)(acc * BN);
+          for (int ks = k0; ks < k1; ++ks) {
+            uint64_t da[PLANES], db[PLANES];
+            int at[PLANES];
+            // planes as they come: all products of the planes that are there
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+              if (!wait_pair(a.err, tc::smem_u32(&full[st]), ph)) { bad = true; break; }
+              tc::fence_after();
+              at[p] = st;
+              da[p] = da0 + (uint64_t)((uint32_t)st * G::SLOT >> 4);
+              db[p] = db0 + (uint64_t)((uint32_t)st * G::SLOT >> 4);
+              if (p == 0) {
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                  mma2(d, da[0] + k * sta, db[0] + k * stb, id, ks > k0 || k > 0);
+              } else if (p == 1) {
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) {
+                  mma2(small, da[0] + k * sta, db[1 % PLANES] + k * stb, id, ks > r.ks0 || k > 0);
+                  mma2(small, da[1 % PLANES] + k * sta, db[0] + k * stb, id, 1);
+                  mma2(small, da[1 % PLANES] + k * sta, db[1 % PLANES] + k * stb, id, 1);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) {
+                  mma2(small, da[0] + k * sta, db[2 % PLANES] + k * stb, id, 1);
+                  mma2(small, da[2 % PLANES] + k * sta, db[0] + k * stb, id, 1);
+                }
+              }
+              ++consumed;
+              if (++st == NST) { st = 0; ph ^= 1u; }
+            }
+            if (bad) break;
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) commit2(tc::smem_u32(&empty[at[p]]));
+          }
+          if (bad) break;
+          commit2(tc::smem_u32(&accf[acc]));
+        }
+      }
+      consumed_s = consumed;
+      if (bad) atomicOr(&bad_s, 1);
+    }
+  } else if (warp >= 4) {
+    // ---------------- accumulators ----------------
+    const int et = tid - 128, q = warp & 3, hf = (warp - 4) >> 2;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t acce0 = at_leader(tc::smem_u32(&acce[0])), acce1 = at_leader(tc::smem_u32(&acce[1]));
+    // columns of this warp's chunks: glu, the gate's and BNC on the other half's
+    constexpr int NCH = EPI == kMlpGlu ? BN / 128 : BN / 64;
+    const int col0 = EPI == kMlpGlu ? hf * (BNC / 2) : hf * BNC;
+    uint32_t u = 0;
+    long long li = 0;
+    bool bad = false;
+    const bool biased = (EPI == kMlpRows || EPI == kMlpGlu) && a.bias != nullptr;
+    for (long long it = pair; it < a.items && (biased || !bad); it += pairs, ++li) {
+      const Item r = decode<TN>(a, it);
+      const int m0 = r.m0 + (int)rank * BM, rows = min(BM, a.M - m0);
+      const float* bias = nullptr;
+      if (biased) {
+        float* bs = bias_s[li & 1];     // the other one may still be read
+        if (et < BN) {
+          const int half = EPI == kMlpGlu ? et / BNC : r.part, n = r.n0 + (EPI == kMlpGlu ? et % BNC : et);
+          const size_t i = (size_t)half * a.N + n;
+          bs[et] = n >= a.N ? 0.f : F32 ? ((const float*)a.bias)[i]
+                                        : __bfloat162float(((const __nv_bfloat16*)a.bias)[i]);
+        }
+        // all eight warps go on, or none
+        if (epilogue_any(bad)) {
+          bad = true;
+          break;
+        }
+        bias = bs;
+      }
+      const size_t block0 = (size_t)((m0 + 32 * q) / 32) * a.fblocks;   // of p and q
+      const bool some = 32 * q < rows;
+      // what becomes of 32 columns from `col`, or of 32 of the gate and of the other half
+      auto finish = [&](int col, float(&v)[32], float(&w)[32]) {
+        const int n = r.n0 + col;
+        if (n >= a.N || !some) return;
+        if constexpr (EPI == kMlpRows) {
+          out_rows<F32>(a, r, m0, n, 32 * q, rows, bias ? bias + col : nullptr, v);
+        } else if constexpr (EPI == kMlpPart) {
+          float* tile = (float*)a.out + ((size_t)r.sp * a.M + m0) * a.ldo + r.part * a.part_out + n;
+          store_f32(tile, a.ldo, 32 * q, rows, min(32, (a.N - n + 3) & ~3), v);
+        } else if constexpr (EPI == kMlpGlu) {
+          if (bias)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] += bias[col + i];
+              w[i] += bias[BNC + col + i];
+            }
+          float h[32];
+          if (a.act == kActSilu)
+            gate<F32, kActSilu>(v, w, h);
+          else if (a.act == kActGelu)
+            gate<F32, kActGelu>(v, w, h);
+          else
+            gate<F32, kActGeluTanh>(v, w, h);
+          if (a.kept.pq) keep<F32>(a.kept, block0 + n / 32, v, w);
+          store_planes<F32>((__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n, a.ldo, a.plane_out, 32 * q, rows,
+                            min(32, (a.N - n + 7) & ~7), h);
+        } else {
+          __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
+          const int cols = min(32, (a.N - n + 7) & ~7);
+          kept<F32>(a.kept, block0 + n / 32, 1, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] *= v[i];
+          store_planes<F32>(o, a.ldo, a.plane_out, 32 * q, rows, cols, w);
+          kept<F32>(a.kept, block0 + n / 32, 0, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] *= v[i];
+          store_planes<F32>(o + a.part_out, a.ldo, a.plane_out, 32 * q, rows, cols, w);
+        }
+      };
+      float R[2][32];                  // F32: the sums so far
+      for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
+        const int acc = (int)(u & 1);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, wait_pair(a.err, tc::smem_u32(&accf[acc]), (u >> 1) & 1u))) {
+          bad = true;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t d = tmem + lanes + (uint32_t)(acc * BN);
+        if constexpr (F32) {
+          const bool last = k0 + KCH >= r.ks1;
+          const uint32_t sd = tmem + lanes + 256 + (uint32_t)(li & 1) * 128;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t c = (uint32_t)(EPI == kMlpGlu ? col0 + j * BNC : col0 + 32 * j);
+            uint32_t x[32];
+            wtc::ld32(d + c, x);
+            wtc::ld_wait(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              R[j][i] = k0 == r.ks0 ? __uint_as_float(x[i]) : R[j][i] + __uint_as_float(x[i]);
+            if (last) {
+              wtc::ld32(sd + c, x);
+              wtc::ld_wait(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) R[j][i] += __uint_as_float(x[i]);
+            }
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(acc ? acce1 : acce0);
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < NCH; ++ch) {
+            const int c = col0 + 32 * ch;
+            uint32_t x[32], y[32];
+            __syncwarp();
+            wtc::ld32(d + c, x);
+            if constexpr (EPI == kMlpGlu) {
+              wtc::ld32(d + BNC + c, y);
+              wtc::ld_wait(y);
+            }
+            wtc::ld_wait(x);
+            if (ch == NCH - 1) {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_leader(acc ? acce1 : acce0);
+            }
+            finish(c, reinterpret_cast<float(&)[32]>(x), reinterpret_cast<float(&)[32]>(y));
+          }
+        }
+      }
+      if constexpr (F32) {
+        if (bad) continue;
+        if constexpr (EPI == kMlpGlu) {
+          finish(col0, R[0], R[1]);
+        } else {
+          float t[32];
+          finish(col0, R[0], t);
+          finish(col0 + 32, R[1], t);
+        }
+      }
+    }
+    if (bad) atomicOr(&bad_s, 1);
+  }
+
+  // ---- drain and free the tensor memory ----
+  // On a healthy run every copy and every product has been waited for.  After an expired
+  // wait: the last products (their commit covers all earlier ones), then the copies that
+  // were issued and not consumed.
+  __syncthreads();
+  if (bad_s && rank == 0 && tid == 32) {
+    const int c = consumed_s, n = issued_s;
+    if (c > 0) wait_pair(a.err, tc::smem_u32(&empty[(c - 1) % NST]), (uint32_t)((c - 1) / NST) & 1u);
+    for (int k = c; k < n; ++k) wait_pair(a.err, tc::smem_u32(&full[k % NST]), (uint32_t)(k / NST) & 1u);
+  }
+  tc::fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc::fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// sums of the ranges in order, + bias, four columns a thread where they are whole
+template <typename T>
+__global__ void __launch_bounds__(256) k_mlp_reduce(MlpReduceArgs a, int quads) {
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long per = (long long)a.nparts * quads;
+  const long long m = id / per;
+  if (m >= a.M) return;
+  const int q = (int)(id - m * per), part = q / quads, n = (q - part * quads) * 4;
+  const float* src = a.part + m * a.ldp + part * a.part_in + n;
+  float4 s = *reinterpret_cast<const float4*>(src);
+  for (int i = 1; i < a.splits; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(src + i * a.split_stride);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  float v[4] = {s.x, s.y, s.z, s.w};
+  T* o = (T*)a.out + m * a.ldo + part * a.part_out + n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) {
+      const size_t b = (size_t)part * a.N + n + i;
+      if constexpr (sizeof(T) == 4) {
+        if (a.bias) v[i] += ((const float*)a.bias)[b];
+      } else {
+        if (a.bias) v[i] += __bfloat162float(((const __nv_bfloat16*)a.bias)[b]);
+      }
+    }
+  if (n + 4 <= a.N && ((uintptr_t)o & (4 * sizeof(T) - 1)) == 0) {
+    st4(o, make_float4(v[0], v[1], v[2], v[3]));
+    return;
+  }
+  for (int i = 0; i < 4 && n + i < a.N; ++i) {
+    if constexpr (sizeof(T) == 4)
+      o[i] = v[i];
+    else
+      o[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+
+
+template <bool F32>
+__global__ void __launch_bounds__(256) k_mlp_pack(MlpPackArgs a) {
+  int j = 0;
+  while (j + 1 < a.jobs && (long long)blockIdx.x >= a.first[j + 1]) ++j;
+  const MlpPackJob& b = a.job[j];
+  // eight columns of a row a thread, of the padded row
+  const long long id = ((long long)blockIdx.x - a.first[j]) * 256 + threadIdx.x;
+  const int per = b.ld / 8;
+  const long long row = id / per;
+  if (row >= b.rows) return;
+  const int c = (int)(id - row * per) * 8;
+  __nv_bfloat16* o = b.dst + row * b.ld + c;
+  const long long at = row * b.inner + c;
+  if constexpr (F32) {
+    const float* s = (const float*)b.src + at;
+    float v[8];
+    if (c + 8 <= b.inner && ((uintptr_t)s & 15) == 0) {
+      const float4 x = ld4(s), y = ld4(s + 4);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < b.inner ? s[i] : 0.f;
+    }
+    uint32_t w[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split3_bf16x2(v[2 * i], v[2 * i + 1], w[i]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint4*>(o + p * b.rows * b.ld) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+  } else {
+    const __nv_bfloat16* s = (const __nv_bfloat16*)b.src + at;
+    __align__(16) __nv_bfloat16 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < b.inner ? s[i] : __nv_bfloat16(0.f);
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(v);
+  }
+}
+
+// rows of range blockIdx.y, 32 columns of blockIdx.x: row y, y + 8, .. by thread y
+__global__ void __launch_bounds__(256) k_mlp_colsum(MlpColsumArgs a) {
+  __shared__ float s[8][33];
+  const int cols = a.parts * a.inner, c = blockIdx.x * 32 + threadIdx.x;
+  const int r0 = (int)((long long)a.rows * blockIdx.y / a.ranges);
+  const int r1 = (int)((long long)a.rows * (blockIdx.y + 1) / a.ranges);
+  float t = 0.f;
+  if (c < cols) {
+    const int part = c / a.inner;
+    const size_t at = (size_t)part * a.pstride + (c - part * a.inner);
+#pragma unroll 4
+    for (int r = r0 + threadIdx.y; r < r1; r += 8) {
+      const size_t i = r * a.ld + at;
+      if (a.planes == 0) {
+        t += ((const float*)a.src)[i];
+      } else {
+        const __nv_bfloat16* p = (const __nv_bfloat16*)a.src + i;
+        float v = __bfloat162float(p[0]);
+        for (int k = 1; k < a.planes; ++k) v += __bfloat162float(p[k * a.plane_stride]);
+        t += v;
+      }
+    }
+  }
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < cols) {
+    for (int y = 1; y < 8; ++y) t += s[y][threadIdx.x];
+    a.part[(size_t)blockIdx.y * cols + c] = t;
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) k_mlp_colsum_join(MlpColsumArgs a) {
+  __shared__ float s[8][33];
+  const int cols = a.parts * a.inner, c = blockIdx.x * 32 + threadIdx.x;
+  float t = 0.f;
+  if (c < cols)
+#pragma unroll 4
+    for (int r = threadIdx.y; r < a.ranges; r += 8) t += a.part[(size_t)r * cols + c];
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < cols) {
+    for (int y = 1; y < 8; ++y) t += s[y][threadIdx.x];
+    if constexpr (sizeof(T) == 4)
+      ((T*)a.out)[c] = t;
+    else
+      ((T*)a.out)[c] = __float2bfloat16_rn(t);
+  }
+}
+
+bool map_view(CUtensorMap* t, const MlpView& v, int box_rows) {
+  const cuuint64_t dim[4] = {(cuuint64_t)v.inner, (cuuint64_t)v.parts, (cuuint64_t)v.rows,
+                             (cuuint64_t)v.planes};
+  const cuuint64_t stride[3] = {(cuuint64_t)v.part_stride * 2, (cuuint64_t)v.row_stride * 2,
+                                (cuuint64_t)v.plane_stride * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+  return encode_tiled_bf16_sw128(t, 4, v.p, dim, stride, box);
+}
+
+template <bool F32, int EPI>
+cudaError_t go(const char* name, const Maps& mp, const MlpGemmArgs& g, int dev, int sms, cudaStream_t st) {
+  static SmemOnce once;
+  const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI>, Cfg<F32>::SMEM, dev);
+  if (e != cudaSuccess) return e;
+  const long long pairs = g.items < sms / 2 ? g.items : sms / 2;
+  return launch(name, k_mlp_gemm<F32, EPI>, dim3((unsigned)(2 * pairs)), dim3(NTH), (size_t)Cfg<F32>::SMEM,
+                st, mp, g);
+}
+
+}  // namespace
+
+int mlp_tile_n(bool f32) { return f32 ? Cfg<true>::BN : Cfg<false>::BN; }
+
+// The ranges that take the least time, by K steps of the longest pair: a tile costs
+// about four steps beside its own (its first copies and its last epilogue), a range's
+// partial sums are written and read at memory's rate (a step of 64 is 0.27 us in bf16,
+// 0.8 us in fp32)
+int mlp_splits(long long tiles, int ksteps, double mn, bool f32) {
+  const double step = f32 ? 0.8e-6 : 0.27e-6, pairs = 76;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 32 && (s == 1 || ksteps / s >= 4); ++s) {
+    const double waves = (double)((tiles * s + (long long)pairs - 1) / (long long)pairs);
+    double t = waves * ((ksteps + s - 1) / s + 4) * step;
+    if (s > 1) t += 3e-6 + s * mn * 8.0 / 5e12;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, const MlpView& b,
+                         MlpGemmArgs& g, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  g.err = wait_error_address();
+  if (g.err == nullptr) return cudaErrorInvalidSymbol;
+  const int bn = mlp_tile_n(f32), tn = epi == kMlpGlu ? bn / 2 : bn;
+  g.mt = (g.M + kMlpTileM - 1) / kMlpTileM;
+  g.nt = (g.N + tn - 1) / tn;
+  g.kst = ((g.amn ? a.rows : a.inner) + BK - 1) / BK;
+  g.items = (long long)g.mt * g.nt * g.nparts * g.splits;
+  Maps mp;
+  memset(&mp, 0, sizeof(mp));
+  if (!map_view(&mp.a, a, g.amn ? 64 : BM) || !map_view(&mp.b, b, g.bmn ? 64 : bn / 2))
+    return cudaErrorInvalidValue;
+#define GO(E) return f32 ? go<true, E>(name, mp, g, dev, sms, st) : go<false, E>(name, mp, g, dev, sms, st)
+  switch (epi) {
+    case kMlpRows: GO(kMlpRows);
+    case kMlpPart: GO(kMlpPart);
+    case kMlpGlu: GO(kMlpGlu);
+    default: GO(kMlpDglu);
+  }
+#undef GO
+}
+
+cudaError_t run_mlp_reduce(const char* name, const MlpReduceArgs& a, bool bf16, cudaStream_t st) {
+  const int quads = (a.N + 3) / 4;
+  const long long n = (long long)a.M * a.nparts * quads;
+  const dim3 grid((unsigned)((n + 255) / 256));
+  if (bf16) return launch(name, k_mlp_reduce<__nv_bfloat16>, grid, dim3(256), 0, st, a, quads);
+  return launch(name, k_mlp_reduce<float>, grid, dim3(256), 0, st, a, quads);
+}
+
+cudaError_t run_mlp_pack(MlpPackArgs& a, bool bf16, cudaStream_t st) {
+  long long n = 0;
+  for (int j = 0; j < a.jobs; ++j) {
+    a.first[j] = n;
+    n += (a.job[j].rows * (a.job[j].ld / 8) + 255) / 256;
+  }
+  if (n == 0) return cudaSuccess;
+  if (n >= 1LL << 31) return cudaErrorInvalidValue;
+  if (bf16) return launch("mlp_pack", k_mlp_pack<false>, dim3((unsigned)n), dim3(256), 0, st, a);
+  return launch("mlp_pack", k_mlp_pack<true>, dim3((unsigned)n), dim3(256), 0, st, a);
+}
+
+// ranges of rows: blocks for four an SM, 64 rows each or more
+int mlp_colsum_ranges(int rows, int cols) {
+  const int cb = (cols + 31) / 32, want = (608 + cb - 1) / cb, most = (rows + 63) / 64;
+  return want < most ? want : most;
+}
+
+cudaError_t run_mlp_colsum(const MlpColsumArgs& a, bool bf16, cudaStream_t st) {
+  const unsigned cb = (unsigned)((a.parts * a.inner + 31) / 32);
+  cudaError_t e = launch("mlp_colsum", k_mlp_colsum, dim3(cb, a.ranges), dim3(32, 8), 0, st, a);
+  if (e != cudaSuccess) return e;
+  if (bf16) return launch("mlp_colsum_join", k_mlp_colsum_join<__nv_bfloat16>, dim3(cb), dim3(32, 8), 0, st, a);
+  return launch("mlp_colsum_join", k_mlp_colsum_join<float>, dim3(cb), dim3(32, 8), 0, st, a);
+}
+
+}  // namespace lapnys

@@ -1,0 +1,136 @@
+// The gated feed-forward block: what its kernels and its host code share.
+//
+//   z = x w_in + b_in,  (g, u) = the halves of z,  h = act(g) u,  y = h w_out + b_out
+//
+// with T rows, C features in and out, F hidden.  For the backward the forward keeps
+// h and the two factors that the gradient of h is multiplied by,
+//   p = act(g)  (of du)   and   q = u act'(g)  (of dg).
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace lapnys {
+
+enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
+
+// p and q in blocks of 32 rows x 32 features, in the order in which a warp of an
+// epilogue (a row a lane) writes and reads them: 16-byte pieces of a row, 32 lanes of a
+// piece together.  bf16 calls keep them as f16 times a power of two for each row of a
+// block (11 bits of the block row's largest: one rounding of 2^-12 beside the gradients'
+// own of 2^-9), fp32 calls in fp32.
+struct MlpKept {
+  uint8_t* pq;        // [ceil(T / 32)][ceil(F / 32)][p, q][pieces][32 lanes] of 16 bytes
+  uint16_t* scale;    // [ceil(T / 32)][ceil(F / 32)][32]: exponents of p | q << 8, + 128
+};
+
+// values of the activation and its slope
+template <bool EXACT>
+__device__ __forceinline__ float mlp_sigmoid(float x) {
+  if constexpr (EXACT) return 1.f / (1.f + expf(-x));
+  float e, r;     // both instructions within 2^-22 of the value
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+template <bool EXACT, int KIND>
+__device__ __forceinline__ void mlp_act(float g, float& p, float& slope) {
+  if constexpr (KIND == kActSilu) {
+    const float s = mlp_sigmoid<EXACT>(g);
+    p = g * s;
+    slope = fmaf(p, 1.f - s, s);
+  } else if constexpr (KIND == kActGelu) {
+    const float c = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+    p = g * c;
+    const float e = EXACT ? expf(-0.5f * g * g) : __expf(-0.5f * g * g);
+    slope = fmaf(g * 0.39894228040143268f, e, c);
+  } else {
+    // 0.5 (1 + tanh z) = sigmoid(2 z)
+    const float g2 = g * g, k = 1.5957691216057308f;      // 2 sqrt(2 / pi)
+    const float s = mlp_sigmoid<EXACT>(k * g * fmaf(0.044715f, g2, 1.f));
+    p = g * s;
+    slope = fmaf(p * (1.f - s), k * fmaf(3.f * 0.044715f, g2, 1.f), s);
+  }
+}
+
+// ---- host side -------------------------------------------------------------
+// A matrix of bf16 as the products read it: `planes` of `rows` rows of `parts` runs of
+// `inner` elements (fp32 values are three planes)
+struct MlpView {
+  const void* p;
+  int inner, parts, rows, planes;
+  size_t part_stride, row_stride, plane_stride;   // elements
+};
+
+enum : int { kMlpRows = 0, kMlpPart = 1, kMlpGlu = 2, kMlpDglu = 3 };
+
+struct MlpGemmArgs {
+  int M, N;              // rows; columns of a part
+  int nparts;            // column parts that tiles run over
+  int mt, nt;            // tiles of M and of a part's N
+  int kst, kparts;       // K steps of a part, parts that K runs over
+  int splits;
+  long long items;
+  int amn, bmn;          // operands stored [k][m], [k][n]
+  int act;
+  const void* bias;      // [nparts][N] (rows), [2][N] (glu), or null
+  void* out;             // rows: [M][ldo], part p of the columns at p * part_out;
+                         // part: fp32 [splits][M][ldo]; glu: h; dglu: dg, du [M][2][N padded]
+  size_t ldo, part_out, plane_out;
+  int wide;              // out takes 16-byte stores
+  MlpKept kept;          // glu: written where set; dglu: read
+  int fblocks;           // blocks of 32 features
+  int* err;
+};
+
+// the product of two views: a's rows are M (or its inner, with amn), K the other
+cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, const MlpView& b,
+                         MlpGemmArgs& g, cudaStream_t st);
+// K ranges of a product with `tiles` tiles of `ksteps` steps, M x N of fp32 a range
+int mlp_splits(long long tiles, int ksteps, double mn, bool f32);
+int mlp_tile_n(bool f32);     // columns of a tile
+constexpr int kMlpTileM = 256;
+constexpr int kMlpTileK = 64;
+
+// out[m][part][n] = sum over `splits` of part[s][m][part][n] + bias, in order
+struct MlpReduceArgs {
+  const float* part;
+  size_t ldp, part_in, split_stride;
+  int splits, M, N, nparts;
+  const void* bias;
+  void* out;
+  size_t ldo, part_out;
+};
+cudaError_t run_mlp_reduce(const char* name, const MlpReduceArgs& a, bool bf16, cudaStream_t st);
+
+// up to four matrices into planes of bf16 (one of bf16 input, three of fp32)
+struct MlpPackJob {
+  const void* src;      // [rows][inner]
+  __nv_bfloat16* dst;   // planes of [rows][ld]
+  long long rows;
+  int inner, ld;
+};
+struct MlpPackArgs {
+  MlpPackJob job[4];
+  long long first[5];   // first block of each
+  int jobs;
+};
+cudaError_t run_mlp_pack(MlpPackArgs& a, bool bf16, cudaStream_t st);
+
+// sums over rows of planes of bf16 [rows][ld] (columns [0, cols)), or of fp32 when
+// `wide32`, in ranges of rows: part [ranges][cols], then out
+struct MlpColsumArgs {
+  const void* src;
+  size_t ld, plane_stride;
+  int planes;           // 0: src is fp32
+  int rows, inner, parts, pstride;   // columns: `parts` runs of `inner`, `pstride` apart
+  float* part;
+  int ranges;
+  void* out;            // [parts][inner]
+};
+int mlp_colsum_ranges(int rows, int cols);
+cudaError_t run_mlp_colsum(const MlpColsumArgs& a, bool bf16, cudaStream_t st);
+
+}  // namespace lapnys

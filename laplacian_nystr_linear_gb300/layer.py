@@ -1,5 +1,5 @@
-"""What stands around the attentions in a layer: rotary positions and the residual with its norms.
-Marshalling only: every step runs in liblapnys kernels."""
+"""What stands around the attentions in a layer: rotary positions, the residual with its norms, and the
+gated feed-forward block.  Marshalling only: every step runs in liblapnys kernels."""
 from __future__ import annotations
 
 import functools
@@ -15,6 +15,7 @@ from .api import _DT, _dtype
 from .window import _at, _nbytes, _no_tangent, _on, _on_stream, _sizes, _tensor, _workspace
 
 _LAYOUT = {"half": _lib.LAPNYS_HALF, "interleaved": _lib.LAPNYS_INTERLEAVED}
+_ACT = {"silu": _lib.LAPNYS_SILU, "gelu": _lib.LAPNYS_GELU, "gelu_tanh": _lib.LAPNYS_GELU_TANH}
 _NORM = {None: _lib.LAPNYS_NONE, "rms": _lib.LAPNYS_RMS, "layer": _lib.LAPNYS_LAYER}
 
 
@@ -304,3 +305,108 @@ def residual_norm(x, u=None, weight=None, bias=None, post_weight=None, post_bias
     else:
         h, y, _ = norm_fwd(x, u, weight, bias, p, post_weight, post_bias, gate, scale, need_stats=False)
     return x if u is None else h, y
+
+
+# ---------------------------------------------------------------------------
+# the gated feed-forward block
+# ---------------------------------------------------------------------------
+class MlpParams(NamedTuple):
+    """Shape of one call: T rows of C features, F hidden."""
+    T: int
+    C: int
+    F: int
+    act: str = "silu"
+
+    def sizes(self):
+        return _sizes(self.T, self.C, self.F)
+
+
+@functools.lru_cache(maxsize=256)
+def mlp_ctx_bytes(p: MlpParams, dtype: torch.dtype) -> int:
+    return load().lapnys_mlp_ctx_bytes(*p.sizes(), _DT[dtype])
+
+
+@functools.lru_cache(maxsize=256)
+def mlp_workspace_bytes(p: MlpParams, dtype: torch.dtype, backward: bool = False) -> int:
+    return load().lapnys_mlp_workspace_bytes(*p.sizes(), _DT[dtype], int(backward))
+
+
+def _check_mlp(x, w_in, b_in, w_out, b_out, p: MlpParams):
+    _dtype(x)
+    dev, dt = x.device, x.dtype
+    if not isinstance(x, torch.Tensor) or x.dim() < 2 or x.shape[-1] != p.C or x.numel() != p.T * p.C:
+        raise ValueError(f"x must be a tensor of {p.T} rows of {p.C}")
+    _tensor(x, "x", x.shape, dt, dev)
+    _tensor(w_in, "w_in", (p.C, 2 * p.F), dt, dev)
+    _tensor(w_out, "w_out", (p.F, p.C), dt, dev)
+    _vector(b_in, "b_in", (2 * p.F,), x)
+    _vector(b_out, "b_out", (p.C,), x)
+
+
+def mlp_fwd(x, w_in, b_in, w_out, b_out, p: MlpParams, y=None, ctx=None, ws=None, need_ctx=True):
+    """lapnys_mlp_fwd: returns (y, ctx); ctx is None when need_ctx is False."""
+    _check_mlp(x, w_in, b_in, w_out, b_out, p)
+    act, dev = _chosen(_ACT, p.act, "activation"), x.device
+    _vector(y, "y", x.shape, x)
+    with _on(dev):
+        y = torch.empty_like(x) if y is None else y
+        ctx = _workspace(ctx, mlp_ctx_bytes(p, x.dtype), dev) if need_ctx else None
+        ws = _workspace(ws, mlp_workspace_bytes(p, x.dtype), dev)
+        rc = load().lapnys_mlp_fwd(
+            x.data_ptr(), w_in.data_ptr(), _at(b_in), w_out.data_ptr(), _at(b_out), y.data_ptr(),
+            *p.sizes(), act, _on_stream(dev), _dtype(x), _at(ctx), _nbytes(ctx), _at(ws), _nbytes(ws))
+    check(rc, "lapnys_mlp_fwd")
+    return y, ctx
+
+
+def mlp_bwd(x, w_in, w_out, dy, ctx, p: MlpParams, want=(True,) * 5, ws=None):
+    """lapnys_mlp_bwd: the gradients of (x, w_in, b_in, w_out, b_out), those wanted."""
+    _check_mlp(x, w_in, None, w_out, None, p)
+    dev = x.device
+    _tensor(dy, "dy", x.shape, x.dtype, dev)
+    need = mlp_ctx_bytes(p, x.dtype)
+    if ctx is None or not ctx.is_cuda or ctx.device != dev or not ctx.is_contiguous() or ctx.nbytes < need:
+        raise ValueError(f"ctx must be the forward's, {need} bytes on {dev}")
+    shapes = (x.shape, w_in.shape, (2 * p.F,), w_out.shape, (p.C,))
+    with _on(dev):
+        grads = [torch.empty(s, dtype=x.dtype, device=dev) if w else None for s, w in zip(shapes, want)]
+        ws = _workspace(ws, mlp_workspace_bytes(p, x.dtype, True), dev)
+        rc = load().lapnys_mlp_bwd(
+            x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), dy.data_ptr(), ctx.data_ptr(),
+            *(_at(g) for g in grads), *p.sizes(), _on_stream(dev), _dtype(x), _at(ws), _nbytes(ws))
+    check(rc, "lapnys_mlp_bwd")
+    return grads
+
+
+class _Mlp(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, x, w_in, b_in, w_out, b_out, p: MlpParams):
+        y, ctx = mlp_fwd(x, w_in, b_in, w_out, b_out, p)
+        fctx.p = p
+        fctx.save_for_backward(x, w_in, w_out, ctx)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(fctx, dy):
+        _no_tangent("gated_mlp's backward", dy)
+        x, w_in, w_out, ctx = fctx.saved_tensors
+        return *mlp_bwd(x, w_in, w_out, dy.contiguous(), ctx, fctx.p, fctx.needs_input_grad[:5]), None
+
+
+def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
+    """The gated feed-forward block, with autograd: (g | u) = x w_in + b_in,
+    y = (act(g) * u) w_out + b_out.
+
+    x: CUDA tensor (float32 or bfloat16) of rows of C features, [.., C]; w_in: [C, 2 F], the gate's
+    columns, then the others; w_out: [F, C]; biases [2 F] and [C] or None; act: "silu", "gelu" or
+    "gelu_tanh".  Gradients are of first order, by reverse mode only.
+    """
+    tensors = (x, w_in, b_in, w_out, b_out)
+    _no_tangent("gated_mlp", *tensors)
+    if x.dim() < 2 or w_out.dim() != 2:
+        raise ValueError("x must be [.., C] and w_out [F, C]")
+    p = MlpParams(x.numel() // max(1, x.shape[-1]), x.shape[-1], w_out.shape[0], act)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return _Mlp.apply(*tensors, p)
+    return mlp_fwd(*tensors, p, need_ctx=False)[0]
