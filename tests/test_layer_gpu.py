@@ -46,7 +46,7 @@ def test_two_blocks_train():
         out.append([h, y, *torch.autograd.grad((h * d).sum() + (y * d).sum(), [xl, *leaves.values()])])
     # the attention's own fp32 tolerance against 64 bits, on both sides of the comparison
     for n, a, b in zip(["h", "y", "x", *par], *out):
-            assert float((a - b).detach().norm() / b.detach().norm()) < 2e-4, n
+        assert float((a - b).detach().norm() / b.detach().norm()) < 2e-4, n
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
