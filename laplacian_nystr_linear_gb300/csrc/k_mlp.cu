@@ -26,9 +26,10 @@
 // and by the epilogue's threads, in registers, beyond; the others together are 2^-8 of
 // the sum.  A step's planes are copied once and read from shared memory by all six.
 //
-// 384 threads a CTA: warp 0 copies (one thread, a ring of NST slots), warp 1 issues
-// (leader) and holds the tensor memory, warps 4 to 11 read the accumulators, a row a
-// thread, half the columns each, while the next tile accumulates.  Every wait is
+// 640 threads a CTA (384 for dglu): warp 0 copies (one thread, a ring of NST slots), warp 1 issues
+// (leader) and holds the tensor memory, warps 4 to 19 read the accumulators, a row a
+// thread, a quarter of the columns each, while the next tile accumulates (with eight warps
+// the chain of a thread's instructions took longer than the products: XXX).  Every wait is
 // bounded; a role whose wait expired sets the error word and stops issuing, and all
 // threads meet at the cluster barrier before tensor memory is freed.
 #include <cuda_fp16.h>
@@ -45,8 +46,10 @@ namespace {
 
 constexpr int BM = 128;                  // rows of A a CTA
 constexpr int BK = kMlpTileK;
-constexpr int NTH = 384;
-constexpr int EPW = 8;                   // epilogue warps
+// epilogue warps: the gradient of the hidden layer has p and q on their way in registers
+// (96 a thread beside sixteen warps, 168 beside eight)
+__host__ __device__ constexpr int epilogue_warps(int epi) { return epi == kMlpDglu ? 8 : 16; }
+__host__ __device__ constexpr int threads_of(int epi) { return 128 + 32 * epilogue_warps(epi); }
 constexpr int GROUP = 8;                 // tiles of M that tiles of N are run over together
 constexpr uint32_t BLK64 = 64 * BK * 2;  // 64 rows of an MN-major operand: 8 KB
 
@@ -81,23 +84,8 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// mbarrier wait that also orders what the partner CTA did before its arrival
-__device__ __forceinline__ bool wait_pair(int* err, uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < tc::kWaitLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  atomicOr(err, 1);
-  return false;
-}
 __device__ __forceinline__ void arrive_leader(uint32_t remote) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 // a tile into this CTA's shared memory, its bytes counted on the leader's barrier
 __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
@@ -125,13 +113,14 @@ __device__ __forceinline__ void commit2(uint32_t mbar) {
 }
 
 // barrier of the epilogue's warps (named barrier 1) that ORs a flag over them
+template <int THREADS>
 __device__ __forceinline__ bool epilogue_any(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, 256, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, %2, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -139,23 +128,28 @@ __device__ __forceinline__ bool epilogue_any(bool v) {
 struct Item {
   int m0, n0, part, ks0, ks1, sp;   // n0: first column of the tile in its part
 };
+// (32-bit divisions: 64-bit ones took a third of an epilogue's instructions)
 template <int TN>
-__device__ __forceinline__ Item decode(const MlpGemmArgs& a, long long it) {
+__device__ __forceinline__ Item decode(const MlpGemmArgs& a, int it) {
   Item r;
-  const int ntot = a.nt * a.nparts;
-  const long long tiles = (long long)a.mt * ntot;
-  r.sp = (int)(it / tiles);
-  const long long t = it - r.sp * tiles;
-  const int g = (int)(t / ((long long)GROUP * ntot)), first = g * GROUP;
-  const int gm = min(GROUP, a.mt - first);
-  const int q = (int)(t - (long long)g * GROUP * ntot);
-  const int n = q / gm;
-  r.m0 = (first + q - n * gm) * (2 * BM);
-  r.part = n / a.nt;
-  r.n0 = (n - r.part * a.nt) * TN;
-  const int all = a.kst * a.kparts;
-  r.ks0 = (int)((long long)all * r.sp / a.splits);
-  r.ks1 = (int)((long long)all * (r.sp + 1) / a.splits);
+  const unsigned ntot = a.nt * a.nparts, tiles = a.mt * ntot, all = a.kst * a.kparts;
+  r.sp = 0;
+  r.ks0 = 0;
+  r.ks1 = (int)all;
+  unsigned t = it;
+  if (a.splits > 1) {
+    r.sp = (int)(t / tiles);
+    t -= r.sp * tiles;
+    r.ks0 = (int)((unsigned long long)all * r.sp / (unsigned)a.splits);
+    r.ks1 = (int)((unsigned long long)all * (r.sp + 1) / (unsigned)a.splits);
+  }
+  const unsigned g = t / (GROUP * ntot), first = g * GROUP;
+  const unsigned gm = min((unsigned)GROUP, a.mt - first);
+  const unsigned q = t - g * GROUP * ntot;
+  const unsigned n = gm == GROUP ? q / GROUP : q / gm;
+  r.m0 = (int)(first + q - n * gm) * (2 * BM);
+  r.part = a.nparts > 1 ? (int)(n / a.nt) : 0;
+  r.n0 = (int)(n - r.part * a.nt) * TN;
   return r;
 }
 
@@ -172,29 +166,30 @@ __device__ __forceinline__ void store_f32(float* tile, size_t ld, int first, int
     wtc::store_rows(tile + 16 * h, 4 * ld, first, rows, (cols - 16 * h + 3) / 4, c);
   }
 }
-// 32 values of a lane's row as bf16: one plane, or the three of fp32 values
-template <bool F32>
+// 32 values of a lane's row as bf16
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* tile, size_t ld, int first, int rows, int cols,
+                                           const uint32_t (&w)[16]) {
+  uint4 c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  wtc::store_rows(tile, 2 * ld, first, rows, (cols + 7) / 8, c);
+}
+// N (16 or 32) fp32 values of a lane's row as their three planes
+template <int N>
 __device__ __forceinline__ void store_planes(__nv_bfloat16* tile, size_t ld, size_t plane, int first,
-                                             int rows, int cols, const float (&v)[32]) {
-  if constexpr (!F32) {
+                                             int rows, int cols, const float (&v)[N]) {
+  uint32_t w[N / 2][3];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) split3_bf16x2(v[2 * i], v[2 * i + 1], w[i]);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
     uint4 c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = make_uint4(wtc::pack(v[8 * i], v[8 * i + 1]), wtc::pack(v[8 * i + 2], v[8 * i + 3]),
-                        wtc::pack(v[8 * i + 4], v[8 * i + 5]), wtc::pack(v[8 * i + 6], v[8 * i + 7]));
-    wtc::store_rows(tile, 2 * ld, first, rows, (cols + 7) / 8, c);
-  } else {
-    uint32_t w[16][3];
+    for (int i = 0; i < N / 8; ++i)
+      c[i] = make_uint4(w[4 * i][p], w[4 * i + 1][p], w[4 * i + 2][p], w[4 * i + 3][p]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) split3_bf16x2(v[2 * i], v[2 * i + 1], w[i]);
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      uint4 c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[i] = make_uint4(w[4 * i][p], w[4 * i + 1][p], w[4 * i + 2][p], w[4 * i + 3][p]);
-      wtc::store_rows(tile + p * plane, 2 * ld, first, rows, (cols + 7) / 8, c);
-    }
+    for (int i = N / 8; i < 4; ++i) c[i] = make_uint4(0, 0, 0, 0);
+    wtc::store_rows(tile + p * plane, 2 * ld, first, rows, min((cols + 7) / 8, N / 8), c);
   }
 }
 
@@ -205,128 +200,197 @@ __device__ __forceinline__ int row_exponent(float m) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// p and q of a lane's row into a block
 template <bool F32>
-__device__ __forceinline__ void keep(const MlpKept& k, size_t block, const float (&p)[32],
-                                     const float (&q)[32]) {
+__device__ __forceinline__ void keep(const MlpKept& k, size_t block, const float (&p)[16],
+                                     const float (&q)[16]) {
   const int lane = threadIdx.x & 31;
   if constexpr (F32) {
-    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 2 * 8 * 32 + lane;
+    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 8 * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       o[i * 32] = make_uint4(__float_as_uint(p[4 * i]), __float_as_uint(p[4 * i + 1]),
                              __float_as_uint(p[4 * i + 2]), __float_as_uint(p[4 * i + 3]));
-      o[(8 + i) * 32] = make_uint4(__float_as_uint(q[4 * i]), __float_as_uint(q[4 * i + 1]),
+      o[(4 + i) * 32] = make_uint4(__float_as_uint(q[4 * i]), __float_as_uint(q[4 * i + 1]),
                                    __float_as_uint(q[4 * i + 2]), __float_as_uint(q[4 * i + 3]));
     }
   } else {
-    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 2 * 4 * 32 + lane;
+    uint4* o = reinterpret_cast<uint4*>(k.pq) + block * 4 * 32 + lane;
     uint32_t word = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float* v = h ? q : p;
+      const float(&v)[16] = h ? q : p;
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float a = fabsf(v[i]);
-        m = fmaxf(m, a <= 3.4e38f ? a : 0.f);
+      for (int i = 0; i < 16; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
+      if (m > 3.4e38f) {               // infinities stay themselves: the largest of the others
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]) <= 3.4e38f ? fabsf(v[i]) : 0.f);
       }
       const int e = row_exponent(m);
-      const float f = pow2(-e);
+      const f32x2 f = pack2(pow2(-e), pow2(-e));
       word |= (uint32_t)(e + 128) << (8 * h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const __half2 x = __floats2half2_rn(v[8 * i + 2 * j] * f, v[8 * i + 2 * j + 1] * f);
+          const float2 y = unpack2(wtc::mul2(pack2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), f));
+          const __half2 x = __floats2half2_rn(y.x, y.y);
           w[j] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        o[(4 * h + i) * 32] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[(2 * h + i) * 32] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     k.scale[block * 32 + lane] = (uint16_t)word;
   }
 }
-// p (h = 0) or q (h = 1) of a lane's row
-template <bool F32>
-__device__ __forceinline__ void kept(const MlpKept& k, size_t block, int h, float (&v)[32]) {
+// p and q of a lane's row as they are kept (bf16 calls)
+struct Kept {
+  uint4 w[4];
+  uint32_t scale;
+};
+__device__ __forceinline__ void fetch(const MlpKept& k, size_t block, Kept& r) {
   const int lane = threadIdx.x & 31;
-  if constexpr (F32) {
-    const uint4* o = reinterpret_cast<const uint4*>(k.pq) + (block * 2 + h) * 8 * 32 + lane;
+  const uint4* o = reinterpret_cast<const uint4*>(k.pq) + block * 4 * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 w = o[i * 32];
-      v[4 * i] = __uint_as_float(w.x);
-      v[4 * i + 1] = __uint_as_float(w.y);
-      v[4 * i + 2] = __uint_as_float(w.z);
-      v[4 * i + 3] = __uint_as_float(w.w);
-    }
-  } else {
-    const uint4* o = reinterpret_cast<const uint4*>(k.pq) + (block * 2 + h) * 4 * 32 + lane;
-    const float f = pow2((int)((k.scale[block * 32 + lane] >> (8 * h)) & 0xff) - 128);
+  for (int i = 0; i < 4; ++i) r.w[i] = __ldcs(o + i * 32);
+  r.scale = k.scale[block * 32 + lane];
+}
+// p (h = 0) or q (h = 1), times x, as bf16 pairs
+__device__ __forceinline__ void times_kept(const Kept& k, int h, const uint32_t (&x)[16], uint32_t* out) {
+  const float s = pow2((int)((k.scale >> (8 * h)) & 0xff) - 128);
+  const f32x2 f = pack2(s, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 c = o[i * 32];
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  for (int i = 0; i < 2; ++i) {
+    const uint4 c = k.w[2 * h + i];
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[8 * i + 2 * j] = x.x * f;
-        v[8 * i + 2 * j + 1] = x.y * f;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int e = 8 * i + 2 * j;
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      const float2 z = unpack2(wtc::mul2(wtc::mul2(pack2(y.x, y.y), f),
+                                         pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
+      out[4 * i + j] = wtc::pack(z.x, z.y);
     }
   }
 }
-
-template <bool F32, int KIND>
-__device__ __forceinline__ void gate(float (&g)[32], float (&u)[32], float (&h)[32]) {
-  // g becomes p, u becomes q
+// p (h = 0) or q (h = 1) of a lane's row, fp32 calls
+__device__ __forceinline__ void kept_f32(const MlpKept& k, size_t block, int h, float (&v)[16]) {
+  const uint4* o = reinterpret_cast<const uint4*>(k.pq) + (block * 2 + h) * 4 * 32 + (threadIdx.x & 31);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float p, s;
-    mlp_act<F32, KIND>(g[i], p, s);
-    h[i] = p * u[i];
-    g[i] = p;
-    u[i] *= s;
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = o[i * 32];
+    v[4 * i] = __uint_as_float(w.x);
+    v[4 * i + 1] = __uint_as_float(w.y);
+    v[4 * i + 2] = __uint_as_float(w.z);
+    v[4 * i + 3] = __uint_as_float(w.w);
   }
+}
+
+// g becomes p, u becomes q, h = p u
+template <bool F32, int KIND>
+__device__ __forceinline__ void gate(float (&g)[16], float (&u)[16], float (&h)[16]) {
+  if constexpr (!F32 && KIND == kActSilu) {
+    const f32x2 one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f), l2e = pack2(-1.4426950408889634f, -1.4426950408889634f);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const f32x2 g2 = pack2(g[i], g[i + 1]), u2 = pack2(u[i], u[i + 1]);
+      float2 e = unpack2(wtc::mul2(g2, l2e));
+      asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+      asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+      e = unpack2(wtc::add2(pack2(e.x, e.y), one));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+      const f32x2 s = pack2(e.x, e.y), p = wtc::mul2(g2, s);
+      const float2 hh = unpack2(wtc::mul2(p, u2)), pp = unpack2(p);
+      const float2 qq = unpack2(wtc::mul2(u2, fma2(p, fma2(s, minus, one), s)));
+      h[i] = hh.x; h[i + 1] = hh.y;
+      g[i] = pp.x; g[i + 1] = pp.y;
+      u[i] = qq.x; u[i + 1] = qq.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float p, s;
+      mlp_act<F32, KIND>(g[i], p, s);
+      h[i] = p * u[i];
+      g[i] = p;
+      u[i] *= s;
+    }
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void gate(int act, float (&g)[16], float (&u)[16], float (&h)[16]) {
+  if (act == kActSilu)
+    gate<F32, kActSilu>(g, u, h);
+  else if (act == kActGelu)
+    gate<F32, kActGelu>(g, u, h);
+  else
+    gate<F32, kActGeluTanh>(g, u, h);
+}
+
+// 16 columns of this lane's row, not waited for
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// the registers as operands keep their uses behind the wait
+__device__ __forceinline__ void wait16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                 "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
 // 32 columns of this lane's row; `first`: the warp's first row in the tile, rows: of the
 // tile that are in M, m0: the CTA's first row
 template <bool F32>
-__device__ __forceinline__ void out_rows(const MlpGemmArgs& a, const Item& r, int m0, int n, int first,
+__device__ __forceinline__ void out_rows(const MlpGemmArgs& a, int part, int m0, int n, int first,
                                          int rows, const float* bias, float (&v)[32]) {
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   if (bias)
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] += bias[i];
-  T* tile = (T*)a.out + (size_t)m0 * a.ldo + r.part * a.part_out + n;
+  T* tile = (T*)a.out + (size_t)m0 * a.ldo + part * a.part_out + n;
   if (a.wide) {
-    if constexpr (F32)
+    if constexpr (F32) {
       store_f32(tile, a.ldo, first, rows, min(32, a.N - n), v);
-    else
-      store_planes<false>(tile, a.ldo, 0, first, rows, min(32, a.N - n), v);
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = wtc::pack(v[2 * i], v[2 * i + 1]);
+      store_bf16(tile, a.ldo, first, rows, min(32, a.N - n), w);
+    }
     return;
   }
   const int row = first + (threadIdx.x & 31);
-  if (row >= rows) return;
-  T* o = tile + (size_t)row * a.ldo;
+  if (row < rows) {
+    T* o = tile + (size_t)row * a.ldo;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (n + i < a.N) {
-      if constexpr (F32)
-        o[i] = v[i];
-      else
-        o[i] = __float2bfloat16_rn(v[i]);
-    }
+    for (int i = 0; i < 32; ++i)
+      if (n + i < a.N) {
+        if constexpr (F32)
+          o[i] = v[i];
+        else
+          o[i] = __float2bfloat16_rn(v[i]);
+      }
+  }
+  __syncwarp();
 }
 
 template <bool F32, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     k_mlp_gemm(const __grid_constant__ Maps mp, MlpGemmArgs a) {
   using G = Cfg<F32>;
   constexpr int NST = G::NST, BN = G::BN, BNC = G::BNC, TN = EPI == kMlpGlu ? BNC : BN;
-  constexpr int PLANES = G::PLANES, KCH = G::KCH;
+  constexpr int PLANES = G::PLANES, KCH = G::KCH, EPW = epilogue_warps(EPI);
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[NST];   // leader: both CTAs' copies landed
   __shared__ __align__(8) uint64_t empty[NST];  // a slot's products done
@@ -338,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = rank_of_cta();
   const uint32_t sm = (tc::smem_u32(sm_raw) + 1023u) & ~1023u;
-  const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -373,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool bad = false;
-      for (long long it = pair; it < a.items && !bad; it += pairs) {
+      for (int it = pair; it < a.items && !bad; it += pairs) {
         const Item r = decode<TN>(a, it);
         const int am = r.m0 + (int)rank * BM;
         const int bn = EPI == kMlpGlu ? r.n0 : r.n0 + (int)rank * BNC;
@@ -382,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
           const int bp = EPI == kMlpGlu ? (int)rank : (a.kparts > 1 ? kp : r.part);
 #pragma unroll 1
           for (int p = 0; p < PLANES; ++p) {
-            if (!wait_pair(a.err, tc::smem_u32(&empty[st]), ph ^ 1u)) { bad = true; break; }
+            if (!wtc::wait_or_flag(a.err, tc::smem_u32(&empty[st]), ph ^ 1u)) { bad = true; break; }
             const uint32_t bar = at_leader(tc::smem_u32(&full[st]));
             if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[st]), 2 * G::SLOT);
             const uint32_t sa = sm + st * G::SLOT, sb = sa + G::A_BYTES;
@@ -407,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
       // before this CTA ends
       for (int i = 0; i < NST && i < issued && !bad; ++i) {
         const int k = issued - 1 - i;
-        bad = !wait_pair(a.err, tc::smem_u32(&empty[k % NST]), (uint32_t)(k / NST) & 1u);
+        bad = !wtc::wait_or_flag(a.err, tc::smem_u32(&empty[k % NST]), (uint32_t)(k / NST) & 1u);
       }
       issued_s = issued;
       if (bad) atomicOr(&bad_s, 1);
@@ -417,20 +481,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
     if (rank == 0 && wtc::elect_one()) {
       int st = 0, consumed = 0;
       uint32_t ph = 0, u = 0;           // u: accumulators used so far
-      long long li = 0;
+      int li = 0;
       bool bad = false;
       const uint32_t id = tc::idesc_bf16(2 * BM, BN) | (a.amn ? 1u << 15 : 0u) | (a.bmn ? 1u << 16 : 0u);
       // K slices of 16: 32 bytes on in a K-major row, 16 rows on in an MN-major block
       const uint64_t sta = (a.amn ? 2048 : 32) >> 4, stb = (a.bmn ? 2048 : 32) >> 4;
       const uint64_t da0 = a.amn ? wtc::desc_mn(sm, BLK64) : wtc::desc_k(sm);
       const uint64_t db0 = a.bmn ? wtc::desc_mn(sm + G::A_BYTES, BLK64) : wtc::desc_k(sm + G::A_BYTES);
-      for (long long it = pair; it < a.items && !bad; it += pairs, ++li) {
+      for (int it = pair; it < a.items && !bad; it += pairs, ++li) {
         const Item r = decode<TN>(a, it);
         const uint32_t small = tmem + 256 + (uint32_t)(li & 1) * 128;   // F32
         for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
           const int k1 = KCH < r.ks1 - k0 ? k0 + KCH : r.ks1;
           const int acc = (int)(u & 1);
-          if (!wait_pair(a.err, tc::smem_u32(&acce[acc]), ((u >> 1) & 1u) ^ 1u)) { bad = true; break; }
+          if (!wtc::wait_or_flag(a.err, tc::smem_u32(&acce[acc]), ((u >> 1) & 1u) ^ 1u)) { bad = true; break; }
           tc::fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * BN);
           for (int ks = k0; ks < k1; ++ks) {
@@ -439,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
             // planes as they come: all products of the planes that are there
 #pragma unroll
             for (int p = 0; p < PLANES; ++p) {
-              if (!wait_pair(a.err, tc::smem_u32(&full[st]), ph)) { bad = true; break; }
+              if (!wtc::wait_or_flag(a.err, tc::smem_u32(&full[st]), ph)) { bad = true; break; }
               tc::fence_after();
               at[p] = st;
               da[p] = da0 + (uint64_t)((uint32_t)st * G::SLOT >> 4);
@@ -478,17 +542,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
     }
   } else if (warp >= 4) {
     // ---------------- accumulators ----------------
-    const int et = tid - 128, q = warp & 3, hf = (warp - 4) >> 2;
+    const int et = tid - 128, q = warp & 3, sub = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t acce0 = at_leader(tc::smem_u32(&acce[0])), acce1 = at_leader(tc::smem_u32(&acce[1]));
-    // columns of this warp's chunks: glu, the gate's and BNC on the other half's
-    constexpr int NCH = EPI == kMlpGlu ? BN / 128 : BN / 64;
-    const int col0 = EPI == kMlpGlu ? hf * (BNC / 2) : hf * BNC;
+    // this warp's columns of a tile (glu: of the gate's, and BNC on those of the other half)
+    constexpr int COLS = TN / (EPW / 4);
+    const int col0 = sub * COLS;
     uint32_t u = 0;
-    long long li = 0;
+    int li = 0;
     bool bad = false;
+    // dglu of bf16 calls: p and q of four blocks, each fetched again for four blocks later
+    // as soon as it is used (read when they were needed, a tile's waits for memory took
+    // longer than its products: XXX)
+    constexpr int DEEP = 4;
+    Kept kept2[DEEP];
+    auto ahead = [&](const Item& r, int col, Kept& k) {
+      const int m = r.m0 + (int)rank * BM + 32 * q, n = r.n0 + col;
+      if (m < a.M && n < a.N) fetch(a.kept, (size_t)(m / 32) * a.fblocks + n / 16, k);
+    };
+    if constexpr (!F32 && EPI == kMlpDglu)
+      if (pair < a.items) {
+        const Item r = decode<TN>(a, pair);
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i) ahead(r, col0 + 16 * i, kept2[i]);
+      }
     const bool biased = (EPI == kMlpRows || EPI == kMlpGlu) && a.bias != nullptr;
-    for (long long it = pair; it < a.items && (biased || !bad); it += pairs, ++li) {
+    for (int it = pair; it < a.items && (biased || !bad); it += pairs, ++li) {
       const Item r = decode<TN>(a, it);
       const int m0 = r.m0 + (int)rank * BM, rows = min(BM, a.M - m0);
       const float* bias = nullptr;
@@ -500,8 +579,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
           bs[et] = n >= a.N ? 0.f : F32 ? ((const float*)a.bias)[i]
                                         : __bfloat162float(((const __nv_bfloat16*)a.bias)[i]);
         }
-        // all eight warps go on, or none
-        if (epilogue_any(bad)) {
+        // all warps go on, or none
+        if (epilogue_any<32 * EPW>(bad)) {
           bad = true;
           break;
         }
@@ -509,106 +588,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
       }
       const size_t block0 = (size_t)((m0 + 32 * q) / 32) * a.fblocks;   // of p and q
       const bool some = 32 * q < rows;
-      // what becomes of 32 columns from `col`, or of 32 of the gate and of the other half
-      auto finish = [&](int col, float(&v)[32], float(&w)[32]) {
+      // 32 columns of rows or partial sums
+      auto plain = [&](int col, float(&v)[32]) {
         const int n = r.n0 + col;
         if (n >= a.N || !some) return;
-        if constexpr (EPI == kMlpRows) {
-          out_rows<F32>(a, r, m0, n, 32 * q, rows, bias ? bias + col : nullptr, v);
-        } else if constexpr (EPI == kMlpPart) {
+        if constexpr (EPI == kMlpPart) {
           float* tile = (float*)a.out + ((size_t)r.sp * a.M + m0) * a.ldo + r.part * a.part_out + n;
           store_f32(tile, a.ldo, 32 * q, rows, min(32, (a.N - n + 3) & ~3), v);
-        } else if constexpr (EPI == kMlpGlu) {
-          if (bias)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] += bias[col + i];
-              w[i] += bias[BNC + col + i];
-            }
-          float h[32];
-          if (a.act == kActSilu)
-            gate<F32, kActSilu>(v, w, h);
-          else if (a.act == kActGelu)
-            gate<F32, kActGelu>(v, w, h);
-          else
-            gate<F32, kActGeluTanh>(v, w, h);
-          if (a.kept.pq) keep<F32>(a.kept, block0 + n / 32, v, w);
-          store_planes<F32>((__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n, a.ldo, a.plane_out, 32 * q, rows,
-                            min(32, (a.N - n + 7) & ~7), h);
         } else {
-          __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
-          const int cols = min(32, (a.N - n + 7) & ~7);
-          kept<F32>(a.kept, block0 + n / 32, 1, w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] *= v[i];
-          store_planes<F32>(o, a.ldo, a.plane_out, 32 * q, rows, cols, w);
-          kept<F32>(a.kept, block0 + n / 32, 0, w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] *= v[i];
-          store_planes<F32>(o + a.part_out, a.ldo, a.plane_out, 32 * q, rows, cols, w);
+          out_rows<F32>(a, r.part, m0, n, 32 * q, rows, bias ? bias + col : nullptr, v);
         }
       };
-      float R[2][32];                  // F32: the sums so far
+      // 16 of the gate and of the other half
+      auto gated = [&](int col, float(&g)[16], float(&v)[16], float(&h)[16]) {
+        if (bias)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            g[i] += bias[col + i];
+            v[i] += bias[BNC + col + i];
+          }
+        gate<F32>(a.act, g, v, h);
+        if (a.kept.pq && some && r.n0 + col < a.N) keep<F32>(a.kept, block0 + (r.n0 + col) / 16, g, v);
+      };
+      constexpr int NR = EPI == kMlpGlu ? 2 : COLS / 16;
+      float R[F32 ? NR : 1][16];       // fp32 calls: the sums so far
       for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
         const int acc = (int)(u & 1);
         __syncwarp();
-        if (!__all_sync(0xffffffffu, wait_pair(a.err, tc::smem_u32(&accf[acc]), (u >> 1) & 1u))) {
+        if (!wtc::wait_warp(a.err, tc::smem_u32(&accf[acc]), (u >> 1) & 1u)) {
           bad = true;
           break;
         }
         tc::fence_after();
-        const uint32_t d = tmem + lanes + (uint32_t)(acc * BN);
-        if constexpr (F32) {
-          const bool last = k0 + KCH >= r.ks1;
-          const uint32_t sd = tmem + lanes + 256 + (uint32_t)(li & 1) * 128;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t c = (uint32_t)(EPI == kMlpGlu ? col0 + j * BNC : col0 + 32 * j);
-            uint32_t x[32];
-            wtc::ld32(d + c, x);
-            wtc::ld_wait(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              R[j][i] = k0 == r.ks0 ? __uint_as_float(x[i]) : R[j][i] + __uint_as_float(x[i]);
-            if (last) {
-              wtc::ld32(sd + c, x);
-              wtc::ld_wait(x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) R[j][i] += __uint_as_float(x[i]);
-            }
-          }
+        const uint32_t d = tmem + lanes + (uint32_t)(acc * BN + col0);
+        auto release = [&]() {
           tc::fence_before();
           __syncwarp();
           if (lane == 0) arrive_leader(acc ? acce1 : acce0);
+        };
+        if constexpr (F32) {
+          const bool last = k0 + KCH >= r.ks1;
+          const uint32_t sd = tmem + lanes + 256 + (uint32_t)((li & 1) * 128 + col0);
+          constexpr uint32_t OTHER = EPI == kMlpGlu ? BNC : 16;
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            uint32_t x[16];
+            ld16(d + j * OTHER, x);
+            wait16(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              R[j][i] = k0 == r.ks0 ? __uint_as_float(x[i]) : R[j][i] + __uint_as_float(x[i]);
+            if (last) {
+              ld16(sd + j * OTHER, x);
+              wait16(x);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) R[j][i] += __uint_as_float(x[i]);
+            }
+          }
+          release();
+        } else if constexpr (EPI == kMlpGlu) {
+          uint32_t w[16];
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t x[16], y[16];
+            ld16(d + 16 * ch, x);
+            ld16(d + BNC + 16 * ch, y);
+            wait16(x);
+            wait16(y);
+            if (ch == 1) release();
+            float h[16];
+            gated(col0 + 16 * ch, reinterpret_cast<float(&)[16]>(x), reinterpret_cast<float(&)[16]>(y), h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[8 * ch + i] = wtc::pack(h[2 * i], h[2 * i + 1]);
+          }
+          const int n = r.n0 + col0;
+          if (some && n < a.N)
+            store_bf16((__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n, a.ldo, 32 * q, rows,
+                       min(32, (a.N - n + 7) & ~7), w);
+        } else if constexpr (EPI == kMlpDglu) {
+const bool more = it + pairs < a.items;
+          const Item after = more ? decode<TN>(a, it + pairs) : r;
+#pragma unroll 1
+          for (int c0 = 0; c0 < COLS; c0 += 16 * DEEP) {
+            uint32_t dg[16], du[16];
+#pragma unroll
+            for (int j = 0; j < DEEP; ++j) {
+              const int c = c0 + 16 * j;
+              uint32_t x[16];
+              ld16(d + c, x);
+              wait16(x);
+              if (j == DEEP - 1 && c == COLS - 16) release();
+              times_kept(kept2[j], 1, x, dg + 8 * (j & 1));    // dg = dh q, du = dh p
+              times_kept(kept2[j], 0, x, du + 8 * (j & 1));
+              const bool here = c + 16 * DEEP < COLS;
+              if (here || more) ahead(here ? r : after, col0 + (here ? c + 16 * DEEP : 16 * j), kept2[j]);
+              const int n = r.n0 + col0 + c - 16;
+              if ((j & 1) && some && n < a.N) {
+                __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
+                const int cols = min(32, (a.N - n + 7) & ~7);
+                store_bf16(o, a.ldo, 32 * q, rows, cols, dg);
+                store_bf16(o + a.part_out, a.ldo, 32 * q, rows, cols, du);
+              }
+            }
+          }
         } else {
 #pragma unroll 1
-          for (int ch = 0; ch < NCH; ++ch) {
-            const int c = col0 + 32 * ch;
-            uint32_t x[32], y[32];
-            __syncwarp();
-            wtc::ld32(d + c, x);
-            if constexpr (EPI == kMlpGlu) {
-              wtc::ld32(d + BNC + c, y);
-              wtc::ld_wait(y);
-            }
+          for (int ch = 0; ch < COLS / 32; ++ch) {
+            uint32_t x[32];
+            wtc::ld32(d + 32 * ch, x);
             wtc::ld_wait(x);
-            if (ch == NCH - 1) {
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) arrive_leader(acc ? acce1 : acce0);
-            }
-            finish(c, reinterpret_cast<float(&)[32]>(x), reinterpret_cast<float(&)[32]>(y));
+            if (ch == COLS / 32 - 1) release();
+            plain(col0 + 32 * ch, reinterpret_cast<float(&)[32]>(x));
           }
         }
       }
       if constexpr (F32) {
         if (bad) continue;
+        const int n = r.n0 + col0;
+        __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
+        const int cols = (a.N - n + 7) & ~7;
         if constexpr (EPI == kMlpGlu) {
-          finish(col0, R[0], R[1]);
+          float h[16];
+          gated(col0, R[0], R[1], h);
+          if (some && n < a.N) store_planes(o, a.ldo, a.plane_out, 32 * q, rows, cols, h);
+        } else if constexpr (EPI == kMlpDglu) {
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+            if (some && n + 16 * j < a.N)
+#pragma unroll
+              for (int h = 1; h >= 0; --h) {
+                float w[16];
+                kept_f32(a.kept, block0 + n / 16 + j, h, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] *= R[j][i];
+                store_planes((h ? o : o + a.part_out) + 16 * j, a.ldo, a.plane_out, 32 * q, rows,
+                             cols - 16 * j, w);
+              }
         } else {
-          float t[32];
-          finish(col0, R[0], t);
-          finish(col0 + 32, R[1], t);
+          plain(col0, reinterpret_cast<float(&)[32]>(R));
         }
       }
     }
@@ -622,8 +739,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTH, 1)
   __syncthreads();
   if (bad_s && rank == 0 && tid == 32) {
     const int c = consumed_s, n = issued_s;
-    if (c > 0) wait_pair(a.err, tc::smem_u32(&empty[(c - 1) % NST]), (uint32_t)((c - 1) / NST) & 1u);
-    for (int k = c; k < n; ++k) wait_pair(a.err, tc::smem_u32(&full[k % NST]), (uint32_t)(k / NST) & 1u);
+    if (c > 0) wtc::wait_or_flag(a.err, tc::smem_u32(&empty[(c - 1) % NST]), (uint32_t)((c - 1) / NST) & 1u);
+    for (int k = c; k < n; ++k) wtc::wait_or_flag(a.err, tc::smem_u32(&full[k % NST]), (uint32_t)(k / NST) & 1u);
   }
   tc::fence_before();
   __syncthreads();
@@ -775,8 +892,8 @@ cudaError_t go(const char* name, const Maps& mp, const MlpGemmArgs& g, int dev, 
   static SmemOnce once;
   const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI>, Cfg<F32>::SMEM, dev);
   if (e != cudaSuccess) return e;
-  const long long pairs = g.items < sms / 2 ? g.items : sms / 2;
-  return launch(name, k_mlp_gemm<F32, EPI>, dim3((unsigned)(2 * pairs)), dim3(NTH), (size_t)Cfg<F32>::SMEM,
+  const int pairs = g.items < sms / 2 ? g.items : sms / 2;
+  return launch(name, k_mlp_gemm<F32, EPI>, dim3((unsigned)(2 * pairs)), dim3(threads_of(EPI)), (size_t)Cfg<F32>::SMEM,
                 st, mp, g);
 }
 
@@ -815,7 +932,9 @@ cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, 
   g.mt = (g.M + kMlpTileM - 1) / kMlpTileM;
   g.nt = (g.N + tn - 1) / tn;
   g.kst = ((g.amn ? a.rows : a.inner) + BK - 1) / BK;
-  g.items = (long long)g.mt * g.nt * g.nparts * g.splits;
+  const long long items = (long long)g.mt * g.nt * g.nparts * g.splits;
+  if (items >= 1LL << 30) return cudaErrorInvalidValue;   // refused before (check_mlp)
+  g.items = (int)items;
   Maps mp;
   memset(&mp, 0, sizeof(mp));
   if (!map_view(&mp.a, a, g.amn ? 64 : BM) || !map_view(&mp.b, b, g.bmn ? 64 : bn / 2))

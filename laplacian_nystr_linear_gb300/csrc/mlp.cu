@@ -28,6 +28,10 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   if (T <= 0 || C <= 0 || F <= 0) return LAPNYS_EINVAL;
   if (dtype != LAPNYS_F32 && dtype != LAPNYS_BF16) return LAPNYS_EINVAL;
   if (T > 1 << 28 || C > 1 << 20 || F > 1 << 20) return LAPNYS_EINVAL;
+  // tiles of every product, and their ranges, are counted in 32 bits
+  const long long wide = C > F ? C : F, narrow = C > F ? F : C;
+  if ((T / kMlpTileM + 1LL) * (wide / 64 + 1) >= 1 << 28 || (wide / 128 + 1) * (narrow / 64 + 1) >= 1 << 24)
+    return LAPNYS_EINVAL;
   m.T = T; m.C = C; m.F = F; m.Cp = up8(C); m.Fp = up8(F);
   m.f32 = dtype == LAPNYS_F32;
   m.planes = m.f32 ? 3 : 1;
@@ -36,6 +40,8 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   return LAPNYS_OK;
 }
 
+int feature_blocks(const Mlp& m) { return (m.F + kMlpBlock - 1) / kMlpBlock; }
+
 // ctx: h, then p and q, then their rows' powers of two
 struct Ctx {
   size_t h, pq, scale, total;
@@ -43,10 +49,10 @@ struct Ctx {
 size_t h_bytes(const Mlp& m) { return align256((size_t)m.planes * m.T * m.Fp * 2); }
 Ctx ctx_of(const Mlp& m) {
   Ctx c;
-  const size_t blocks = (size_t)((m.T + 31) / 32) * ((m.F + 31) / 32);
+  const size_t blocks = (size_t)((m.T + 31) / 32) * feature_blocks(m);
   c.h = 0;
   c.pq = h_bytes(m);
-  c.scale = c.pq + align256(blocks * 2 * 32 * 32 * (m.f32 ? 4 : 2));
+  c.scale = c.pq + align256(blocks * 2 * 32 * kMlpBlock * (m.f32 ? 4 : 2));
   c.total = c.scale + (m.f32 ? 0 : align256(blocks * 32 * 2));
   return c;
 }
@@ -245,7 +251,7 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
     g.ldo = m.Fp;
     g.plane_out = (size_t)T * m.Fp;
     g.kept = kept_of(m, ctx);
-    g.fblocks = (F + 31) / 32;
+    g.fblocks = feature_blocks(m);
     r.e = run_mlp_gemm("mlp_in", kMlpGlu, m.f32, vx, vi, g, stream);
   }
   const MlpView vh = view(h, F, 1, T, m.planes, m.Fp);
@@ -287,7 +293,7 @@ int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const voi
     g.part_out = m.Fp;
     g.plane_out = (size_t)T * 2 * m.Fp;
     g.kept = kept_of(m, const_cast<void*>(ctx));
-    g.fblocks = (F + 31) / 32;
+    g.fblocks = feature_blocks(m);
     r.e = run_mlp_gemm("mlp_dhidden", kMlpDglu, m.f32, vy, vo, g, stream);
   }
   if (dx) r.rows("mlp_dx", vz, false, vi, false, T, C, 1, 2, F, nullptr, dx, w.part);

@@ -16,14 +16,15 @@ namespace lapnys {
 
 enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
 
-// p and q in blocks of 32 rows x 32 features, in the order in which a warp of an
+// p and q in blocks of 32 rows x 16 features, in the order in which a warp of an
 // epilogue (a row a lane) writes and reads them: 16-byte pieces of a row, 32 lanes of a
 // piece together.  bf16 calls keep them as f16 times a power of two for each row of a
 // block (11 bits of the block row's largest: one rounding of 2^-12 beside the gradients'
 // own of 2^-9), fp32 calls in fp32.
+constexpr int kMlpBlock = 16;   // features of a block
 struct MlpKept {
-  uint8_t* pq;        // [ceil(T / 32)][ceil(F / 32)][p, q][pieces][32 lanes] of 16 bytes
-  uint16_t* scale;    // [ceil(T / 32)][ceil(F / 32)][32]: exponents of p | q << 8, + 128
+  uint8_t* pq;        // [ceil(T / 32)][ceil(F / 16)][p, q][pieces][32 lanes] of 16 bytes
+  uint16_t* scale;    // [ceil(T / 32)][ceil(F / 16)][32]: exponents of p | q << 8, + 128
 };
 
 // values of the activation and its slope
@@ -71,8 +72,7 @@ struct MlpGemmArgs {
   int nparts;            // column parts that tiles run over
   int mt, nt;            // tiles of M and of a part's N
   int kst, kparts;       // K steps of a part, parts that K runs over
-  int splits;
-  long long items;
+  int splits, items;
   int amn, bmn;          // operands stored [k][m], [k][n]
   int act;
   const void* bias;      // [nparts][N] (rows), [2][N] (glu), or null
@@ -81,7 +81,7 @@ struct MlpGemmArgs {
   size_t ldo, part_out, plane_out;
   int wide;              // out takes 16-byte stores
   MlpKept kept;          // glu: written where set; dglu: read
-  int fblocks;           // blocks of 32 features
+  int fblocks;           // blocks of features
   int* err;
 };
 
