@@ -18,7 +18,7 @@ SOURCES = ["lapnys.cu", "k_landmark.cu", "k_gemm.cu", "k_pass.cu", "k_bwd.cu", "
            "k_probe.cu", "k_bwd_tc.cu", "k_dv.cu", "k_proj.cu", "window.cu", "k_win.cu",
            "k_win_tc.cu", "k_win_tc_bwd.cu",
            "k_token.cu", "k_cache.cu", "layer.cu", "k_rotary.cu", "k_norm.cu",
-           "mlp.cu", "k_mlp.cu"]
+           "mlp.cu", "k_mlp.cu", "k_mlp_few.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "internal.h", "tc.cuh", "win.cuh", "win_tc.cuh",
                                              "layer.cuh", "mlp.cuh")] + [
     os.path.join(ROOT, "include", "lapnys.h")]

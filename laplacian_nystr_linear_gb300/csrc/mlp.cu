@@ -77,6 +77,7 @@ struct Ws {
 };
 Ws ws_of(const Mlp& m, bool backward) {
   Ws w;
+  memset(&w, 0, sizeof(w));
   size_t o = 0;
   auto room = [&](size_t& at, size_t bytes) {
     at = o;
@@ -90,9 +91,7 @@ Ws ws_of(const Mlp& m, bool backward) {
   if (!backward) {
     room(w.h, h_bytes(m));
     part = split_of(m, m.T, m.C, 1, m.F, 1).bytes;
-    w.dy = w.dz = w.colsum = 0;
   } else {
-    w.h = 0;
     room(w.dy, m.pack_c ? two * m.T * m.Cp : 0);
     room(w.dz, two * m.T * 2 * m.Fp);
     part = split_of(m, m.T, m.C, 1, m.F, 2).bytes;
@@ -105,6 +104,12 @@ Ws ws_of(const Mlp& m, bool backward) {
   }
   room(w.part, part);
   w.total = o;
+  if (!backward && mlp_few_ok(m.T, m.C, m.F, m.f32)) {
+    // h and the partial sums of one product, then the other's; without a ctx that is all
+    const size_t a = mlp_few_bytes(m.T, m.F, 2), b = mlp_few_bytes(m.T, m.C, 1);
+    const size_t few = align256((size_t)m.T * m.F * (m.f32 ? 4 : 2)) + (a > b ? a : b);
+    w.total = few > w.total ? few : w.total;
+  }
   return w;
 }
 
@@ -234,6 +239,19 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
   const Ws w = ws_of(m, false);
   if (!ws || !aligned(ws, 16)) return LAPNYS_EINVAL;
   if (ws_bytes < w.total || (ctx && ctx_bytes < ctx_of(m).total)) return LAPNYS_ENOSPC;
+  if (!ctx && mlp_few_ok(T, C, F, m.f32)) {
+    MlpFewArgs f;
+    memset(&f, 0, sizeof(f));
+    f.x = x; f.w = w_in; f.bias = b_in; f.out = ws;
+    f.part = (float*)((uint8_t*)ws + align256((size_t)T * F * (m.f32 ? 4 : 2)));
+    f.T = T; f.K = C; f.N = F; f.parts = 2; f.act = act;
+    const cudaError_t e = run_mlp_few(f, m.f32, stream);
+    if (e != cudaSuccess) return status(e);
+    f.x = ws; f.w = w_out; f.bias = b_out; f.out = y;
+    f.K = F; f.N = C; f.parts = 1; f.act = -1;
+    f.second = true;
+    return status(run_mlp_few(f, m.f32, stream));
+  }
   Run r(m, ws, stream);
   const MlpView vx = r.operand(x, m.pack_c, w.x, T, 1, C);
   const MlpView vi = r.operand(w_in, m.pack_f, w.w_in, C, 2, F);

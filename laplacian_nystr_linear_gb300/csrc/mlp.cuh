@@ -133,4 +133,24 @@ struct MlpColsumArgs {
 int mlp_colsum_ranges(int rows, int cols);
 cudaError_t run_mlp_colsum(const MlpColsumArgs& a, bool bf16, cudaStream_t st);
 
+// A few rows: out[t][n] = sum_k x[t][k] w[k][n], w [K][parts][N], through fp32 partial
+// sums that a second kernel adds and finishes: + bias, and with act >= 0 the gate of
+// w's two parts (T x N of h), else rows.
+struct MlpFewArgs {
+  const void* x;        // [T][K]
+  const void* w;        // [K][parts][N]
+  const void* bias;     // [parts][N] or null
+  void* out;            // [T][N]
+  float* part;          // [blocks of columns + blocks of the grid][T][columns of a block]
+  int T, K, N, parts, act;
+  bool second;          // x comes from the kernel before, which is one of these
+  // filled by the launcher
+  int nb, ks, grid;     // column blocks of a part, K steps, blocks of the grid
+  int* err;
+};
+// whether a call of T rows goes this way
+bool mlp_few_ok(int T, int C, int F, bool f32);
+size_t mlp_few_bytes(int T, int N, int parts);
+cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st);
+
 }  // namespace lapnys

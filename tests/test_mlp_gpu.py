@@ -45,6 +45,18 @@ def test_forward_and_gradients(dtype, T, C, Fh, act, bias):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 17, 48, 63, 64, 65])
+@pytest.mark.parametrize("C,Fh,act", [(512, 2048, "silu"), (2048, 520, "gelu"), (1000, 3000, "gelu_tanh"), (66, 70, "silu")])
+def test_few_rows_alone(dtype, T, C, Fh, act):
+    """Without a gradient, few rows go their own way (weights read once, split over all SMs)."""
+    t, _ = _inputs(T, C, Fh, dtype, T % 2 == 0, 6)
+    ref = reference(**t, kind=act)
+    first = lap.gated_mlp(**t, act=act)
+    check("y", first, ref["y"], dtype)
+    assert torch.equal(lap.gated_mlp(**t, act=act), first)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
 def test_long_sums_stay_close(dtype):
     """The drift of long sums, measured as a whole: 2-norm of the error over the value's."""
     t, dy = _inputs(4096, 1024, 1536, dtype, False)
