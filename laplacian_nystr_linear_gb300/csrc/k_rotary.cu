@@ -121,8 +121,9 @@ __global__ void __launch_bounds__(RT) k_rotary(RotaryArgs a) {
             T& u = PAIR ? x[i].v[e] : x[i].v[(2 * e) % V];
             T& w = PAIR ? z[i].v[e] : x[i].v[(2 * e + 1) % V];
             const float f = to_f(u), g = to_f(w);
-            of_f(u, f * c[e] - g * s[e]);
-            of_f(w, g * c[e] + f * s[e]);
+            // the same roundings in every variant
+            of_f(u, __fmaf_rn(f, c[e], -__fmul_rn(g, s[e])));
+            of_f(w, __fmaf_rn(g, c[e], __fmul_rn(f, s[e])));
           }
         }
         put<T, V>(o, x[i]);

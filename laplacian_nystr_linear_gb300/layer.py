@@ -26,6 +26,13 @@ def _chosen(table, name, what):
         raise ValueError(f"unknown {what} {name!r}: one of {', '.join(map(repr, table))}") from None
 
 
+def _any_requires_grad(tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
+
+
 # ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------
@@ -87,66 +94,91 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, context=None
     return RotaryFrequencies.of(w, grow, device)
 
 
+@functools.lru_cache(maxsize=256)
+def _rotary_plan(q_shape, k_shape, pairs, layout, dtype):
+    """What the C call takes of one kind of call, checked once: sizes, layout, element type."""
+    if len(q_shape) != 4 or (k_shape is not None and len(k_shape) != 4):
+        raise ValueError("q and k must be [B, H, N, d] tensors")
+    B, Hq, N, d = q_shape
+    Hkv = 0 if k_shape is None else k_shape[1]
+    if k_shape is not None and k_shape != (B, Hkv, N, d):
+        raise ValueError(f"k must be {(B, Hkv, N, d)}: {tuple(k_shape)}")
+    return (*_sizes(B, Hq, Hkv, N, d, 2 * pairs), _chosen(_LAYOUT, layout, "layout")), _DT[dtype]
+
+
+def _check_rotary(q, k, freqs, start, positions, layout):
+    _dtype(q)
+    dev, dt, shape = q.device, q.dtype, q.shape
+    if not isinstance(freqs, RotaryFrequencies) or freqs.turns.dim() != 1:
+        raise ValueError("freqs must be RotaryFrequencies (rotary_frequencies makes them)")
+    turns = freqs.turns
+    plan = _rotary_plan(shape, None if k is None else k.shape, turns.shape[0], layout, dt)
+    _tensor(q, "q", shape, dt, dev)
+    if k is not None:
+        _tensor(k, "k", k.shape, dt, dev)
+    _tensor(turns, "freqs.turns", turns.shape, torch.int64, dev)
+    if start is not None:
+        if positions is not None:
+            raise ValueError("start or positions, not both")
+        _tensor(start, "start", shape[:1], torch.int32, dev)
+    elif positions is not None:
+        _tensor(positions, "positions", (shape[0], shape[2]), torch.int32, dev)
+    return plan
+
+
+def _rotary(q, k, turns, start, positions, plan, factor, inverse, q_out=None, k_out=None):
+    dev = q.device
+    with _on(dev):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        check(load().lapnys_rotary(
+            q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), turns.data_ptr(), _at(start),
+            _at(positions), *plan[0], factor, inverse, _on_stream(dev), plan[1]), "lapnys_rotary")
+    return q_out, k_out
+
+
 def rotary_apply(q, k, freqs: RotaryFrequencies, start=None, positions=None, layout="half", inverse=False,
                  q_out=None, k_out=None):
     """lapnys_rotary: returns (q, k) turned; q_out, k_out may be q and k themselves.  No derivatives."""
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q and k must be [B, H, N, d] tensors")
-    B, Hq, N, d = q.shape
-    dev, dt = q.device, _dtype(q)
-    lay = _chosen(_LAYOUT, layout, "layout")
-    Hkv = 0 if k is None else k.shape[1]
-    _tensor(q, "q", q.shape, q.dtype, dev)
-    if k is not None:
-        _tensor(k, "k", (B, Hkv, N, d), q.dtype, dev)
-    if not isinstance(freqs, RotaryFrequencies) or freqs.turns.dim() != 1:
-        raise ValueError("freqs must be RotaryFrequencies (rotary_frequencies makes them)")
-    _tensor(freqs.turns, "freqs.turns", freqs.turns.shape, torch.int64, dev)
-    if start is not None and positions is not None:
-        raise ValueError("start or positions, not both")
-    if start is not None:
-        _tensor(start, "start", (B,), torch.int32, dev)
-    if positions is not None:
-        _tensor(positions, "positions", (B, N), torch.int32, dev)
+    plan = _check_rotary(q, k, freqs, start, positions, layout)
     if q_out is not None:
-        _tensor(q_out, "q_out", q.shape, q.dtype, dev)
+        _tensor(q_out, "q_out", q.shape, q.dtype, q.device)
     if k_out is not None:
         if k is None:
             raise ValueError("k_out without k")
-        _tensor(k_out, "k_out", k.shape, q.dtype, dev)
-    with _on(dev):
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k)
-        rc = load().lapnys_rotary(
-            q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), freqs.turns.data_ptr(), _at(start),
-            _at(positions), *_sizes(B, Hq, Hkv, N, d, 2 * freqs.turns.shape[0]), lay, freqs.factor,
-            int(inverse), _on_stream(dev), dt)
-    check(rc, "lapnys_rotary")
-    return q_out, k_out
+        _tensor(k_out, "k_out", k.shape, q.dtype, q.device)
+    return _rotary(q, k, freqs.turns, start, positions, plan, freqs.factor, int(inverse), q_out, k_out)
 
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(fctx, q, k, turns, start, positions, factor, layout):
-        fctx.save_for_backward(turns, start, positions)
-        fctx.how = factor, layout
+    def forward(fctx, q, k, freqs, start, positions, layout):
+        plan = _check_rotary(q, k, freqs, start, positions, layout)
+        fctx.save_for_backward(freqs.turns, start, positions)
+        fctx.how = plan, freqs.factor
         fctx.set_materialize_grads(False)
-        return rotary_apply(q, k, RotaryFrequencies(turns, factor), start, positions, layout)
+        return _rotary(q, k, freqs.turns, start, positions, plan, freqs.factor, 0)
 
     @staticmethod
     @once_differentiable
     def backward(fctx, dq, dk):
         _no_tangent("rotary's backward", dq, dk)
         turns, start, positions = fctx.saved_tensors
-        factor, layout = fctx.how
-        freqs = RotaryFrequencies(turns, factor)
-        grads = [None if g is None else g.contiguous() for g in (dq, dk)]
-        if grads[0] is not None:
-            grads = rotary_apply(*grads, freqs, start, positions, layout, True)
-        elif grads[1] is not None:      # one tensor is enough to the call
-            grads[1] = rotary_apply(grads[1], None, freqs, start, positions, layout, True)[0]
-        return *grads, None, None, None, None, None
+        plan, factor = fctx.how
+        dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))
+        if dq is None:                  # the call takes one tensor or two
+            if dk is not None:
+                B, _, Hkv, *rest = plan[0]
+                plan = (B, Hkv, 0, *rest), plan[1]
+                dk = _rotary(dk, None, turns, start, positions, plan, factor, 1)[0]
+        else:
+            if dk is None:
+                B, Hq, _, *rest = plan[0]
+                plan = (B, Hq, 0, *rest), plan[1]
+            dq, dk = _rotary(dq, dk, turns, start, positions, plan, factor, 1)
+        return dq, dk, None, None, None, None
 
 
 def rotary(q, k, freqs: RotaryFrequencies, start=None, positions=None, layout="half"):
@@ -159,11 +191,10 @@ def rotary(q, k, freqs: RotaryFrequencies, start=None, positions=None, layout="h
     order, by reverse mode only.  rotary_apply does the same in place.
     """
     _no_tangent("rotary", q, k)
-    if not isinstance(freqs, RotaryFrequencies):
-        raise ValueError("freqs must be RotaryFrequencies (rotary_frequencies makes them)")
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
-        return _Rotary.apply(q, k, freqs.turns, start, positions, freqs.factor, layout)
-    return rotary_apply(q, k, freqs, start, positions, layout)
+        return _Rotary.apply(q, k, freqs, start, positions, layout)
+    plan = _check_rotary(q, k, freqs, start, positions, layout)
+    return _rotary(q, k, freqs.turns, start, positions, plan, freqs.factor, 0)
 
 
 # ---------------------------------------------------------------------------
@@ -189,16 +220,21 @@ def _vector(t, name, shape, x):
         _tensor(t, name, shape, x.dtype, x.device)
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_dims(p: NormParams):
+    return p.dims()
+
+
 def _check_norm(x, u, weight, bias, post_weight, post_bias, gate, scale, p: NormParams):
     _dtype(x)
-    _tensor(x, "x", (p.B, p.N, p.C), x.dtype, x.device)
-    _vector(u, "u", x.shape, x)
-    wide = (p.B, p.C) if p.per_seq else (p.C,)
-    _vector(weight, "weight", wide, x)
-    _vector(bias, "bias", wide, x)
-    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"), (scale, "scale")):
-        _vector(t, name, (p.C,), x)
-    _vector(gate, "gate", (p.B, p.C), x)
+    C = (p.C,)
+    _tensor(x, "x", p[:3], x.dtype, x.device)
+    wide = (p.B, p.C) if p.per_seq else C
+    for t, name, shape in ((u, "u", p[:3]), (weight, "weight", wide), (bias, "bias", wide),
+                           (post_weight, "post_weight", C), (post_bias, "post_bias", C),
+                           (gate, "gate", (p.B, p.C)), (scale, "scale", C)):
+        if t is not None:
+            _tensor(t, name, shape, x.dtype, x.device)
 
 
 @functools.lru_cache(maxsize=256)
@@ -207,12 +243,29 @@ def norm_workspace_bytes(B, N, C, seqs) -> int:
     return load().lapnys_norm_workspace_bytes(*_sizes(B, N, C), int(seqs))
 
 
+def _norm_fwd(x, u, weight, bias, post_weight, post_bias, gate, scale, p, h, y, stats, need_stats):
+    dev = x.device
+    with _on(dev):
+        if h is None and u is not None:
+            h = torch.empty_like(x)
+        if y is None and p.pre is not None:
+            y = torch.empty_like(x)
+        if not need_stats:
+            stats = None
+        elif stats is None:
+            stats = torch.empty((p.B, p.N, 4), dtype=torch.float32, device=dev)
+        check(load().lapnys_norm_fwd(
+            x.data_ptr(), _at(u), _at(weight), _at(bias), _at(post_weight), _at(post_bias), _at(gate),
+            _at(scale), _at(h), _at(y), _at(stats), *_norm_dims(p), p.eps, _on_stream(dev),
+            _DT[x.dtype]), "lapnys_norm_fwd")
+    return h, y, stats
+
+
 def norm_fwd(x, u, weight, bias, p: NormParams, post_weight=None, post_bias=None, gate=None, scale=None,
              h=None, y=None, stats=None, need_stats=True):
     """lapnys_norm_fwd: returns (h, y, stats); h is None without u, y without a norm of h, stats when
     need_stats is False."""
     _check_norm(x, u, weight, bias, post_weight, post_bias, gate, scale, p)
-    dims, dev = p.dims(), x.device
     if u is None and h is not None:
         raise ValueError("h without u")
     if p.pre is None and y is not None:
@@ -220,19 +273,26 @@ def norm_fwd(x, u, weight, bias, p: NormParams, post_weight=None, post_bias=None
     _vector(h, "h", x.shape, x)
     _vector(y, "y", x.shape, x)
     if stats is not None:
-        _tensor(stats, "stats", (p.B, p.N, 4), torch.float32, dev)
+        _tensor(stats, "stats", (p.B, p.N, 4), torch.float32, x.device)
+    return _norm_fwd(x, u, weight, bias, post_weight, post_bias, gate, scale, p, h, y, stats, need_stats)
+
+
+def _norm_bwd(x, u, weight, stats, dh, dy, p, post_weight, post_bias, gate, scale, want, ws):
+    dev = x.device
+    C = (p.C,)
+    wide = (p.B, p.C) if p.per_seq else C
+    shapes = (None, None, wide, wide, C, C, (p.B, p.C), C)
     with _on(dev):
-        h = torch.empty_like(x) if h is None and u is not None else h
-        y = torch.empty_like(x) if y is None and p.pre is not None else y
-        if not need_stats:
-            stats = None
-        elif stats is None:
-            stats = torch.empty((p.B, p.N, 4), dtype=torch.float32, device=dev)
-        rc = load().lapnys_norm_fwd(
-            x.data_ptr(), _at(u), _at(weight), _at(bias), _at(post_weight), _at(post_bias), _at(gate),
-            _at(scale), _at(h), _at(y), _at(stats), *dims, p.eps, _on_stream(dev), _dtype(x))
-    check(rc, "lapnys_norm_fwd")
-    return h, y, stats
+        grads = [(torch.empty_like(x) if s is None else torch.empty(s, dtype=x.dtype, device=dev)) if w else None
+                 for s, w in zip(shapes, want)]
+        if ws is None and any(want[2:]):
+            ws = torch.empty(norm_workspace_bytes(p.B, p.N, p.C, p.per_seq or gate is not None),
+                             dtype=torch.uint8, device=dev)
+        check(load().lapnys_norm_bwd(
+            x.data_ptr(), _at(u), _at(weight), _at(post_weight), _at(post_bias), _at(gate), _at(scale),
+            stats.data_ptr(), _at(dh), _at(dy), *map(_at, grads), *_norm_dims(p), _on_stream(dev),
+            _DT[x.dtype], _at(ws), _nbytes(ws)), "lapnys_norm_bwd")
+    return grads
 
 
 def norm_bwd(x, u, weight, stats, dh, dy, p: NormParams, post_weight=None, post_bias=None, gate=None,
@@ -240,28 +300,19 @@ def norm_bwd(x, u, weight, stats, dh, dy, p: NormParams, post_weight=None, post_
     """lapnys_norm_bwd: the gradients of (x, u, weight, bias, post_weight, post_bias, gate, scale), those
     wanted; dh, dy: the outputs', or None."""
     _check_norm(x, u, weight, None, post_weight, post_bias, gate, scale, p)
-    dims, dev = p.dims(), x.device
-    _tensor(stats, "stats", (p.B, p.N, 4), torch.float32, dev)
+    _tensor(stats, "stats", (p.B, p.N, 4), torch.float32, x.device)
     _vector(dh, "dh", x.shape, x)
     _vector(dy, "dy", x.shape, x)
-    wide = (p.B, p.C) if p.per_seq else (p.C,)
-    shapes = (x.shape, x.shape, wide, wide, (p.C,), (p.C,), (p.B, p.C), (p.C,))
-    with _on(dev):
-        grads = [torch.empty(s, dtype=x.dtype, device=dev) if w else None for s, w in zip(shapes, want)]
-        if any(want[2:]):
-            ws = _workspace(ws, norm_workspace_bytes(p.B, p.N, p.C, p.per_seq or gate is not None), dev)
-        rc = load().lapnys_norm_bwd(
-            x.data_ptr(), _at(u), _at(weight), _at(post_weight), _at(post_bias), _at(gate), _at(scale),
-            stats.data_ptr(), _at(dh), _at(dy), *(_at(g) for g in grads), *dims, _on_stream(dev),
-            _dtype(x), _at(ws), _nbytes(ws))
-    check(rc, "lapnys_norm_bwd")
-    return grads
+    if ws is not None:
+        _workspace(ws, 0, x.device)
+    return _norm_bwd(x, u, weight, stats, dh, dy, p, post_weight, post_bias, gate, scale, want, ws)
 
 
 class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, u, weight, bias, post_weight, post_bias, gate, scale, p: NormParams):
-        h, y, stats = norm_fwd(x, u, weight, bias, p, post_weight, post_bias, gate, scale)
+        h, y, stats = _norm_fwd(x, u, weight, bias, post_weight, post_bias, gate, scale, p, None, None, None,
+                                True)
         fctx.p = p
         fctx.set_materialize_grads(False)
         fctx.save_for_backward(x, u, weight, stats, post_weight, post_bias, gate, scale)
@@ -271,15 +322,14 @@ class _ResidualNorm(torch.autograd.Function):
     @once_differentiable
     def backward(fctx, dh, dy):
         _no_tangent("residual_norm's backward", dh, dy)
-        x, u, weight, stats, post_weight, post_bias, gate, scale = fctx.saved_tensors
+        x, u, weight, stats, *others = fctx.saved_tensors
         if dh is None and dy is None:
             return (None,) * 9
         dh, dy = (None if g is None else g.contiguous() for g in (dh, dy))
         want = list(fctx.needs_input_grad[:8])
         if dy is None:
             want[2] = want[3] = False
-        return *norm_bwd(x, u, weight, stats, dh, dy, fctx.p, post_weight, post_bias, gate, scale,
-                         want), None
+        return *_norm_bwd(x, u, weight, stats, dh, dy, fctx.p, *others, want, None), None
 
 
 def residual_norm(x, u=None, weight=None, bias=None, post_weight=None, post_bias=None, gate=None, scale=None,
@@ -298,12 +348,14 @@ def residual_norm(x, u=None, weight=None, bias=None, post_weight=None, post_bias
         raise ValueError("x must be [B, N, C]")
     if u is None and pre is None:
         raise ValueError("neither u nor a norm: nothing to do")
-    per_seq = any(t is not None and t.dim() == 2 for t in (weight, bias))
+    per_seq = (weight is not None and weight.dim() == 2) or (bias is not None and bias.dim() == 2)
     p = NormParams(*x.shape, per_seq, pre, post, float(eps))
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    _norm_dims(p)
+    _check_norm(*tensors, p)
+    if torch.is_grad_enabled() and _any_requires_grad(tensors):
         h, y = _ResidualNorm.apply(*tensors, p)
     else:
-        h, y, _ = norm_fwd(x, u, weight, bias, p, post_weight, post_bias, gate, scale, need_stats=False)
+        h, y, _ = _norm_fwd(*tensors, p, None, None, None, False)
     return x if u is None else h, y
 
 
@@ -331,32 +383,74 @@ def mlp_workspace_bytes(p: MlpParams, dtype: torch.dtype, backward: bool = False
     return load().lapnys_mlp_workspace_bytes(*p.sizes(), _DT[dtype], int(backward))
 
 
+@functools.lru_cache(maxsize=256)
+def _mlp_plan(shape, F, act):
+    """(parameters, sizes and activation as the C call takes them) of x's shape."""
+    if len(shape) < 2:
+        raise ValueError("x must be [.., C]")
+    C = shape[-1]
+    T = math.prod(shape[:-1])
+    p = MlpParams(T, C, F, act)
+    return p, p.sizes(), _chosen(_ACT, act, "activation")
+
+
 def _check_mlp(x, w_in, b_in, w_out, b_out, p: MlpParams):
     _dtype(x)
-    dev, dt = x.device, x.dtype
-    if not isinstance(x, torch.Tensor) or x.dim() < 2 or x.shape[-1] != p.C or x.numel() != p.T * p.C:
-        raise ValueError(f"x must be a tensor of {p.T} rows of {p.C}")
+    dev, dt, C, F = x.device, x.dtype, p.C, p.F
+    if x.dim() < 2 or x.shape[-1] != C or x.numel() != p.T * C:
+        raise ValueError(f"x must be a tensor of {p.T} rows of {C}")
     _tensor(x, "x", x.shape, dt, dev)
-    _tensor(w_in, "w_in", (p.C, 2 * p.F), dt, dev)
-    _tensor(w_out, "w_out", (p.F, p.C), dt, dev)
-    _vector(b_in, "b_in", (2 * p.F,), x)
-    _vector(b_out, "b_out", (p.C,), x)
+    _tensor(w_in, "w_in", (C, 2 * F), dt, dev)
+    _tensor(w_out, "w_out", (F, C), dt, dev)
+    if b_in is not None:
+        _tensor(b_in, "b_in", (2 * F,), dt, dev)
+    if b_out is not None:
+        _tensor(b_out, "b_out", (C,), dt, dev)
+
+
+def _mlp_fwd(x, w_in, b_in, w_out, b_out, plan, y, ctx, ws, need_ctx):
+    p, sizes, act = plan
+    dev, dt = x.device, x.dtype
+    with _on(dev):
+        if y is None:
+            y = torch.empty_like(x)
+        if not need_ctx:
+            ctx = None
+        elif ctx is None:
+            ctx = torch.empty(mlp_ctx_bytes(p, dt), dtype=torch.uint8, device=dev)
+        if ws is None:
+            ws = torch.empty(mlp_workspace_bytes(p, dt), dtype=torch.uint8, device=dev)
+        check(load().lapnys_mlp_fwd(
+            x.data_ptr(), w_in.data_ptr(), _at(b_in), w_out.data_ptr(), _at(b_out), y.data_ptr(), *sizes,
+            act, _on_stream(dev), _DT[dt], _at(ctx), _nbytes(ctx), ws.data_ptr(), ws.nbytes),
+            "lapnys_mlp_fwd")
+    return y, ctx
 
 
 def mlp_fwd(x, w_in, b_in, w_out, b_out, p: MlpParams, y=None, ctx=None, ws=None, need_ctx=True):
     """lapnys_mlp_fwd: returns (y, ctx); ctx is None when need_ctx is False."""
     _check_mlp(x, w_in, b_in, w_out, b_out, p)
-    act, dev = _chosen(_ACT, p.act, "activation"), x.device
     _vector(y, "y", x.shape, x)
+    for t in (ctx, ws):
+        if t is not None:
+            _workspace(t, 0, x.device)
+    return _mlp_fwd(x, w_in, b_in, w_out, b_out, (p, p.sizes(), _chosen(_ACT, p.act, "activation")), y, ctx,
+                    ws, need_ctx)
+
+
+def _mlp_bwd(x, w_in, w_out, dy, ctx, plan, want, ws):
+    p, sizes, _ = plan
+    dev, dt = x.device, x.dtype
+    like = (x, w_in, (2 * p.F,), w_out, (p.C,))
     with _on(dev):
-        y = torch.empty_like(x) if y is None else y
-        ctx = _workspace(ctx, mlp_ctx_bytes(p, x.dtype), dev) if need_ctx else None
-        ws = _workspace(ws, mlp_workspace_bytes(p, x.dtype), dev)
-        rc = load().lapnys_mlp_fwd(
-            x.data_ptr(), w_in.data_ptr(), _at(b_in), w_out.data_ptr(), _at(b_out), y.data_ptr(),
-            *p.sizes(), act, _on_stream(dev), _dtype(x), _at(ctx), _nbytes(ctx), _at(ws), _nbytes(ws))
-    check(rc, "lapnys_mlp_fwd")
-    return y, ctx
+        grads = [(torch.empty(t, dtype=dt, device=dev) if isinstance(t, tuple) else torch.empty_like(t)) if w
+                 else None for t, w in zip(like, want)]
+        if ws is None:
+            ws = torch.empty(mlp_workspace_bytes(p, dt, True), dtype=torch.uint8, device=dev)
+        check(load().lapnys_mlp_bwd(
+            x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), dy.data_ptr(), ctx.data_ptr(),
+            *map(_at, grads), *sizes, _on_stream(dev), _DT[dt], ws.data_ptr(), ws.nbytes), "lapnys_mlp_bwd")
+    return grads
 
 
 def mlp_bwd(x, w_in, w_out, dy, ctx, p: MlpParams, want=(True,) * 5, ws=None):
@@ -367,22 +461,16 @@ def mlp_bwd(x, w_in, w_out, dy, ctx, p: MlpParams, want=(True,) * 5, ws=None):
     need = mlp_ctx_bytes(p, x.dtype)
     if ctx is None or not ctx.is_cuda or ctx.device != dev or not ctx.is_contiguous() or ctx.nbytes < need:
         raise ValueError(f"ctx must be the forward's, {need} bytes on {dev}")
-    shapes = (x.shape, w_in.shape, (2 * p.F,), w_out.shape, (p.C,))
-    with _on(dev):
-        grads = [torch.empty(s, dtype=x.dtype, device=dev) if w else None for s, w in zip(shapes, want)]
-        ws = _workspace(ws, mlp_workspace_bytes(p, x.dtype, True), dev)
-        rc = load().lapnys_mlp_bwd(
-            x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), dy.data_ptr(), ctx.data_ptr(),
-            *(_at(g) for g in grads), *p.sizes(), _on_stream(dev), _dtype(x), _at(ws), _nbytes(ws))
-    check(rc, "lapnys_mlp_bwd")
-    return grads
+    if ws is not None:
+        _workspace(ws, 0, dev)
+    return _mlp_bwd(x, w_in, w_out, dy, ctx, (p, p.sizes(), None), want, ws)
 
 
 class _Mlp(torch.autograd.Function):
     @staticmethod
-    def forward(fctx, x, w_in, b_in, w_out, b_out, p: MlpParams):
-        y, ctx = mlp_fwd(x, w_in, b_in, w_out, b_out, p)
-        fctx.p = p
+    def forward(fctx, x, w_in, b_in, w_out, b_out, plan):
+        y, ctx = _mlp_fwd(x, w_in, b_in, w_out, b_out, plan, None, None, None, True)
+        fctx.plan = plan
         fctx.save_for_backward(x, w_in, w_out, ctx)
         return y
 
@@ -391,7 +479,7 @@ class _Mlp(torch.autograd.Function):
     def backward(fctx, dy):
         _no_tangent("gated_mlp's backward", dy)
         x, w_in, w_out, ctx = fctx.saved_tensors
-        return *mlp_bwd(x, w_in, w_out, dy.contiguous(), ctx, fctx.p, fctx.needs_input_grad[:5]), None
+        return *_mlp_bwd(x, w_in, w_out, dy.contiguous(), ctx, fctx.plan, fctx.needs_input_grad, None), None
 
 
 def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
@@ -404,9 +492,10 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
     """
     tensors = (x, w_in, b_in, w_out, b_out)
     _no_tangent("gated_mlp", *tensors)
-    if x.dim() < 2 or w_out.dim() != 2:
-        raise ValueError("x must be [.., C] and w_out [F, C]")
-    p = MlpParams(x.numel() // max(1, x.shape[-1]), x.shape[-1], w_out.shape[0], act)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        return _Mlp.apply(*tensors, p)
-    return mlp_fwd(*tensors, p, need_ctx=False)[0]
+    if w_out.dim() != 2:
+        raise ValueError("w_out must be [F, C]")
+    plan = _mlp_plan(x.shape, w_out.shape[0], act)
+    _check_mlp(*tensors, plan[0])
+    if torch.is_grad_enabled() and _any_requires_grad(tensors):
+        return _Mlp.apply(*tensors, plan)
+    return _mlp_fwd(*tensors, plan, None, None, None, False)[0]
