@@ -12,15 +12,23 @@
 //   dpost_bias = sum_b m S4, dgate = scale (post_weight S3 + post_bias S4),
 //   dscale = sum_b gate (post_weight S3 + post_bias S4).
 //
-// Bound by memory: a row is read once, kept in registers (16 features a thread) and
-// written once; h is formed again from x and u in the backward, which reads as much
-// as h would and has no rounding in it.  Statistics are of centred values, in fp32,
-// by one warp for rows of up to 512 features (no barrier), by more above.  The
-// backward's sums over rows stay in registers over a block's rows, are joined over
-// its row groups in shared memory and over the blocks by k_norm_seq, in one order.
+// Bound by memory: a row is read once, kept in registers and written once; h is formed
+// again from x and u in the backward, which reads as much as h would and has no rounding
+// in it.  Statistics are of centred values, in fp32.
+//
+// Backward, rows of whole 16-byte pieces, up to 4096 features (k_norm_bwd_ring): a block
+// an SM takes an even stretch of all rows, in tiles of as many rows as its sixteen warps
+// work on at once (8 features a thread), which one more warp copies into a ring in shared
+// memory (bulk copies; a tile's rows lie side by side).  What a feature is multiplied by is
+// laid out there once a sequence, in fp32.  XXX
+// Other rows, and the forward: k_norm_bwd, k_norm_fwd, loads by the threads themselves.
+//
+// The backward's sums over rows stay in registers, are joined over a block's row groups
+// in shared memory and over the blocks by k_norm_seq, in one order.
 #include "common.cuh"
 #include "internal.h"
 #include "layer.cuh"
+#include "win_tc.cuh"
 
 namespace lapnys {
 namespace {
@@ -110,7 +118,14 @@ struct RowSum {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
-    if (warps == 1) return v;
+    return warps == 1 ? v : over_warps(v);
+  }
+  __device__ __forceinline__ float operator()(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return warps == 1 ? v : over_warps(make_float2(v, 0.f)).x;
+  }
+  __device__ __forceinline__ float2 over_warps(float2 v) {
     float2* s = slot + 32 * turn;
     turn ^= 1;      // the other half is free again after the next barrier
     const int w = (threadIdx.x >> 5) % warps;
@@ -123,7 +138,6 @@ struct RowSum {
     }
     return v;
   }
-  __device__ __forceinline__ float operator()(float v) { return (*this)(make_float2(v, 0.f)).x; }
 };
 
 // mean and 1 / deviation of a row's values
@@ -352,24 +366,334 @@ __global__ void __launch_bounds__(TB) k_norm_bwd(NormArgs a, int warps) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// the backward's rows through a ring in shared memory
+// ---------------------------------------------------------------------------
+constexpr int RW = 16;            // working warps at the most; one more copies
+constexpr int RING = 6;           // tiles of the ring at the most
+constexpr int RE = 8, RH = RE / 2;   // features a thread, pairs of them
+constexpr int kRingWidth = 32 * RW * RE;
+constexpr size_t kRingBytes = 216 * 1024;
+
+// shared memory of a block: ring tiles, then vectors, then the join of the sums
+struct RingShape {
+  int warps, rows, nst;           // warps of a row, rows of a tile, tiles of the ring
+  uint32_t tensor, tile;          // bytes of a tensor's share of a tile, of a tile
+  uint32_t vec, join, total;      // bytes: where the vectors and the join start, and in all
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ f32x2 pair_of(uint32_t x, uint32_t y) {
+  return pack2(__uint_as_float(x), __uint_as_float(y));
+}
+
+// The copying thread: tile by tile, the tensors that are there and the rows' statistics.
+__device__ __forceinline__ void ring_fill(const NormArgs& a, const RingShape& s, int u0, int u1, uint32_t sm,
+                                          uint64_t* full, uint64_t* empty, int es, int* err) {
+  const void* src[4] = {a.x, a.u, a.dh, a.dy};
+  int st = 0, issued = 0;
+  uint32_t ph = 0;
+  for (int u = u0; u < u1; ++u) {
+    const int b = u / a.tiles, n = (u - b * a.tiles) * s.rows, rows = min(s.rows, a.N - n);
+    if (!wtc::wait_or_flag(err, tc::smem_u32(&empty[st]), ph ^ 1u)) break;
+    const uint32_t bar = tc::smem_u32(&full[st]), base = sm + st * s.tile;
+    const size_t row = (size_t)b * a.N + n, at = row * a.C * es;
+    const uint32_t bytes = (uint32_t)rows * a.C * es;
+    uint32_t all = rows * 16u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all += src[i] ? bytes : 0u;
+    tc::mbar_expect_tx(bar, all);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (src[i]) tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + at, bytes, bar);
+    tc::bulk_g2s(base + 4 * s.tensor, a.stats + row * 4, rows * 16u, bar);
+    ++issued;
+    if (++st == s.nst) { st = 0; ph ^= 1u; }
+  }
+  // no copy is in flight when the block ends
+  for (int i = 0; i < s.nst && i < issued; ++i) {
+    const int k = issued - 1 - i;
+    wtc::wait_or_flag(err, tc::smem_u32(&full[k % s.nst]), (uint32_t)(k / s.nst) & 1u);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
+  constexpr int V = 16 / (int)sizeof(T), NP = RE / V;   // features of a piece, pieces a thread
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 slots[RW][64];
+  __shared__ __align__(8) uint64_t full[RING], empty[RING];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, workers = s.warps * s.rows;
+  const uint32_t sm = tc::smem_u32(smem);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < s.nst; ++i) {
+      tc::mbar_init(tc::smem_u32(&full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&empty[i]), workers);
+    }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  const long long units = (long long)a.B * a.tiles;
+  const int u0 = (int)(units * blockIdx.x / a.grid), u1 = (int)(units * (blockIdx.x + 1) / a.grid);
+  if (warp == workers) {
+    if (lane == 0) ring_fill(a, s, u0, u1, sm, full, empty, sizeof(T), err);
+    return;
+  }
+  const int group = warp / s.warps, threads = 32 * s.warps, workerst = 32 * workers;
+  const int t = threadIdx.x - group * threads;
+  RowSum sum{slots[group], s.warps, group, threads};
+  auto col = [&](int j) { return (j * threads + t) * V; };      // of piece j
+  auto sync = [&]() { asm volatile("barrier.sync 0, %0;" ::"r"(workerst) : "memory"); };
+  const float inv = 1.f / (float)a.C;
+
+  // Vectors: weight, m post_weight, m post_bias in fp32, quarters of pieces side by side.
+  const bool has_w = a.weight != nullptr && a.dy, has_m = a.u && (a.post != kNormNone || a.gate || a.scale);
+  const bool has_b = a.post_bias != nullptr;
+  const uint32_t vw = s.vec, vm = vw + (has_w ? 4u * a.C : 0u), vb = vm + (has_m ? 4u * a.C : 0u);
+  auto vectors = [&](int b) {
+    sync();                                           // nobody reads the last one's
+    const size_t seq = (size_t)b * a.C;
+    for (int c = threadIdx.x; c < a.C; c += workerst) {
+      const int piece = c / V, i = c % V, at = ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
+      float m = 1.f;
+      if (a.gate) m *= as_f(((const T*)a.gate)[seq + c]);
+      if (a.scale) m *= as_f(((const T*)a.scale)[c]);
+      if (has_w) reinterpret_cast<float*>(smem + vw)[at] = as_f(((const T*)a.weight)[a.per_seq ? seq + c : c]);
+      if (has_m) reinterpret_cast<float*>(smem + vm)[at] = a.post_weight ? m * as_f(((const T*)a.post_weight)[c]) : m;
+      if (has_b) reinterpret_cast<float*>(smem + vb)[at] = m * as_f(((const T*)a.post_bias)[c]);
+    }
+    sync();
+  };
+  auto vec = [&](uint32_t base, f32x2(&p)[RH]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        uint4 f = make_uint4(0, 0, 0, 0);
+        if (col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
+        p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
+        p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
+      }
+  };
+  // this thread's share of a tensor's row in the tile at `tile`
+  const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + 16 * t;
+  auto share = [&](uint32_t tile, int tensor, f32x2(&p)[RH]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      uint4 f = make_uint4(0, 0, 0, 0);
+      if (col(j) < a.C) f = lds16(tile + tensor * s.tensor + row_at + 16 * j * threads);
+      if constexpr (V == 4) {
+        p[2 * j] = pair_of(f.x, f.y);
+        p[2 * j + 1] = pair_of(f.z, f.w);
+      } else {
+        p[0] = pair_of(f.x << 16, f.x & 0xffff0000u);
+        p[1] = pair_of(f.y << 16, f.y & 0xffff0000u);
+        p[2] = pair_of(f.z << 16, f.z & 0xffff0000u);
+        p[3] = pair_of(f.w << 16, f.w & 0xffff0000u);
+      }
+    }
+  };
+  auto store = [&](void* base, size_t row, const f32x2(&p)[RH]) {
+    T* o = (T*)base + row * a.C;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if (col(j) >= a.C) continue;
+      if constexpr (V == 4) {
+        const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
+        *reinterpret_cast<float4*>(o + col(j)) = make_float4(x.x, x.y, y.x, y.y);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2(p[i]);
+          w[i] = wtc::pack(x.x, x.y);
+        }
+        *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+
+  f32x2 A[4][RH];
+  auto clear = [&]() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < RH; ++i) A[k][i] = pack2(0.f, 0.f);
+  };
+  // the sums of sequence b into this block's slot
+  auto flush = [&](int b) {
+    float* out = a.part + ((size_t)b + blockIdx.x) * 4 * a.C;
+    float* join = reinterpret_cast<float*>(smem + s.join);
+    for (int g = 0; g < s.rows; ++g) {
+      if (group == g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (a.sums >> k & 1)
+#pragma unroll
+            for (int i = 0; i < RH; ++i) {
+              const int c = col(2 * i / V) + 2 * i % V;
+              if (c >= a.C) continue;
+              float2 v = unpack2(A[k][i]);
+              float2* o = reinterpret_cast<float2*>((s.rows > 1 ? join : out) + k * a.C + c);
+              if (g > 0) {
+                const float2 p = *o;
+                v.x += p.x;
+                v.y += p.y;
+              }
+              *o = v;
+            }
+      if (s.rows > 1) sync();
+    }
+    if (s.rows > 1) {
+      for (int c = threadIdx.x; c < 4 * a.C; c += workerst)
+        if (a.sums >> (c / a.C) & 1) out[c] = join[c];
+      sync();
+    }
+  };
+  // z becomes (z - mean) / deviation
+  auto unit = [](f32x2(&z)[RH], float mean, float r) {
+    const f32x2 rr = pack2(r, r), minus = pack2(-mean * r, -mean * r);
+#pragma unroll
+    for (int i = 0; i < RH; ++i) z[i] = fma2(z[i], rr, minus);
+  };
+  // (sum of a b, sum of a) over the row
+  auto moments = [&](const f32x2(&x)[RH], const f32x2(&y)[RH]) {
+    f32x2 p = wtc::mul2(x[0], y[0]), q = x[0];
+#pragma unroll
+    for (int i = 1; i < RH; ++i) {
+      p = fma2(x[i], y[i], p);
+      q = wtc::add2(q, x[i]);
+    }
+    const float2 v = unpack2(p), w = unpack2(q);
+    return sum(make_float2(v.x + v.y, w.x + w.y));
+  };
+
+  int st = 0, cur = -1;
+  uint32_t ph = 0;
+  bool late = false;
+  for (int u = u0; u < u1; ++u) {
+    const int b = a.B == 1 ? 0 : u / a.tiles, n = (u - b * a.tiles) * s.rows + group;
+    if (b != cur) {
+      if (cur >= 0 && a.sums) flush(cur);
+      clear();
+      if (cur < 0 || a.gate || a.per_seq) vectors(b);
+      cur = b;
+    }
+    // after an expired wait (the error word is set) no other is waited for: every warp goes
+    // on to its end, since the sums and the barriers need all
+    late = late || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
+    if (n < a.N) {
+      const size_t row = (size_t)b * a.N + n;
+      const uint32_t tile = sm + st * s.tile;
+      const uint4 qw = lds16(tile + 4 * s.tensor + 16 * group);
+      const float mu = __uint_as_float(qw.x), ru = __uint_as_float(qw.y), mh = __uint_as_float(qw.z),
+                  rh = __uint_as_float(qw.w);
+      f32x2 uh[RH], d[RH], v[RH];
+      if (a.u) {
+        share(tile, 1, uh);
+        if (a.post != kNormNone) unit(uh, mu, ru);
+      }
+      if (a.dh) {
+        share(tile, 2, d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < RH; ++i) d[i] = pack2(0.f, 0.f);
+      }
+      if (a.dy) {
+        f32x2 e[RH], hh[RH];
+        share(tile, 0, hh);
+        share(tile, 3, e);
+        if (a.u) {
+          if (has_m) {
+            vec(vm, v);
+#pragma unroll
+            for (int i = 0; i < RH; ++i) hh[i] = fma2(uh[i], v[i], hh[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < RH; ++i) hh[i] = wtc::add2(uh[i], hh[i]);
+          }
+          if (has_b) {
+            vec(vb, v);
+#pragma unroll
+            for (int i = 0; i < RH; ++i) hh[i] = wtc::add2(hh[i], v[i]);
+          }
+        }
+        unit(hh, mh, rh);
+#pragma unroll
+        for (int i = 0; i < RH; ++i) {
+          A[0][i] = fma2(e[i], hh[i], A[0][i]);
+          A[1][i] = wtc::add2(e[i], A[1][i]);
+        }
+        if (has_w) {
+          vec(vw, v);
+#pragma unroll
+          for (int i = 0; i < RH; ++i) e[i] = wtc::mul2(e[i], v[i]);
+        }
+        const float2 m = moments(e, hh);           // e is 0 behind the row
+        const float k1 = -rh * (m.x * inv), k0 = a.pre == kNormLayer ? -rh * (m.y * inv) : 0.f;
+        const f32x2 rr = pack2(rh, rh), kk1 = pack2(k1, k1), kk0 = pack2(k0, k0);
+#pragma unroll
+        for (int i = 0; i < RH; ++i) d[i] = fma2(e[i], rr, fma2(hh[i], kk1, wtc::add2(d[i], kk0)));
+      }
+      if (a.dx) store(a.dx, row, d);
+      if (a.u) {
+#pragma unroll
+        for (int i = 0; i < RH; ++i) {
+          A[2][i] = fma2(d[i], uh[i], A[2][i]);
+          A[3][i] = wtc::add2(d[i], A[3][i]);
+        }
+        if (has_m) {
+          vec(vm, v);
+#pragma unroll
+          for (int i = 0; i < RH; ++i) d[i] = wtc::mul2(d[i], v[i]);   // 0 behind the row
+        }
+        if (a.post != kNormNone) {
+          const float2 m = moments(d, uh);
+          const float k1 = -ru * (m.x * inv), k0 = a.post == kNormLayer ? -ru * (m.y * inv) : 0.f;
+          const f32x2 rr = pack2(ru, ru), kk1 = pack2(k1, k1), kk0 = pack2(k0, k0);
+#pragma unroll
+          for (int i = 0; i < RH; ++i) d[i] = fma2(d[i], rr, fma2(uh[i], kk1, kk0));
+        }
+        if (a.du) store(a.du, row, d);
+      }
+    }
+    wtc::arrive_warp(tc::smem_u32(&empty[st]));
+    if (++st == s.nst) { st = 0; ph ^= 1u; }
+  }
+  if (cur >= 0 && a.sums) flush(cur);
+}
+
 constexpr int JY = 32;   // threads that share a column of the joins
 
-// seq[b][k][c] = sum over the parts of a sequence: part y, y + 32, .. by thread y, then
-// the threads' sums in order
+// seq[b][k][c] = sum over a sequence's slots: slot y, y + 32, .. by thread y, then the
+// threads' sums in order
 __global__ void __launch_bounds__(32 * JY) k_norm_seq(NormArgs a) {
   __shared__ float s[JY][33];
-  const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y, b = blockIdx.z;
+  const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
   if (!(a.sums >> k & 1)) return;
-  float t = 0.f;
-  if (c < a.C)
+  for (long long b = blockIdx.z; b < a.B; b += gridDim.z) {
+    size_t p0 = (size_t)b * a.parts, p1 = p0 + a.parts;
+    if (a.grid > 0) {
+      // block of tile u: the greatest c with tiles c / grid <= u
+      const long long units = (long long)a.B * a.tiles, first = b * a.tiles;
+      p0 = b + ((first + 1) * a.grid - 1) / units;
+      p1 = b + ((first + a.tiles) * a.grid - 1) / units + 1;
+    }
+    float t = 0.f;
+    if (c < a.C)
 #pragma unroll 4
-    for (int p = threadIdx.y; p < a.parts; p += JY) t += a.part[(((size_t)b * a.parts + p) * 4 + k) * a.C + c];
-  s[threadIdx.y][threadIdx.x] = t;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < a.C) {
+      for (size_t p = p0 + threadIdx.y; p < p1; p += JY) t += a.part[(p * 4 + k) * a.C + c];
+    __syncthreads();
+    s[threadIdx.y][threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < a.C) {
 #pragma unroll
-    for (int y = 1; y < JY; ++y) t += s[y][threadIdx.x];
-    a.seq[((size_t)b * 4 + k) * a.C + c] = t;
+      for (int y = 1; y < JY; ++y) t += s[y][threadIdx.x];
+      a.seq[((size_t)b * 4 + k) * a.C + c] = t;
+    }
   }
 }
 
@@ -427,6 +751,8 @@ Shape shape(int C) {
   return s;
 }
 
+// rows without the ring: a block's threads bound its registers (8 features a thread: rows
+// of up to 256, eight of them a block)
 template <typename T, int EPT, bool WIDE>
 cudaError_t go(const NormArgs& a, bool backward, const Shape& s, cudaStream_t st) {
   const int threads = 32 * s.warps * s.groups;
@@ -436,29 +762,22 @@ cudaError_t go(const NormArgs& a, bool backward, const Shape& s, cudaStream_t st
     const dim3 grid((unsigned)(all < 152 * 64 ? all : 152 * 64));
     if (threads <= 256)
       return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 256>, grid, block, 0, st, a, s.warps);
-    return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 1024>, grid, block, 0, st, a, s.warps);
+    if constexpr (EPT > 8)
+      return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 1024>, grid, block, 0, st, a, s.warps);
+  } else {
+    const dim3 grid((unsigned)(a.B * a.parts));
+    const size_t smem = s.groups > 1 ? 16 * (size_t)a.C : 0;
+    if constexpr (!WIDE)          // whole pieces: beyond the ring's width only
+      if (threads <= 256)
+        return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 256>, grid, block, smem, st, a, s.warps);
+    if constexpr (EPT > 8) {
+      if (threads <= 512)
+        return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 512>, grid, block, smem, st, a, s.warps);
+      return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 1024>, grid, block, smem, st, a, s.warps);
+    }
   }
-  const dim3 grid((unsigned)(a.B * a.parts));
-  const size_t smem = s.groups > 1 ? 16 * (size_t)a.C : 0;
-  if (threads <= 256)
-    return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 256>, grid, block, smem, st, a, s.warps);
-  if (threads <= 512)
-    return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 512>, grid, block, smem, st, a, s.warps);
-  return launch("norm_bwd", k_norm_bwd<T, EPT, WIDE, 1024>, grid, block, smem, st, a, s.warps);
+  return cudaErrorInvalidValue;
 }
-
-template <typename T>
-cudaError_t pick(const NormArgs& a, bool backward, cudaStream_t st) {
-  const Shape s = shape(a.C);
-  bool wide = a.C % (16 / (int)sizeof(T)) == 0;
-  const void* all[] = {a.x, a.u, a.weight, a.bias, a.post_weight, a.post_bias, a.gate, a.scale,
-                       a.h, a.y, a.dh, a.dy, a.dx, a.du};
-  for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
-  if (s.ept == 8) return wide ? go<T, 8, true>(a, backward, s, st) : go<T, 8, false>(a, backward, s, st);
-  return wide ? go<T, 16, true>(a, backward, s, st) : go<T, 16, false>(a, backward, s, st);
-}
-
-}  // namespace
 
 // ranges of a sequence's rows: blocks for two an SM, each group of a block eight rows
 // or more
@@ -469,20 +788,77 @@ int norm_parts(int B, int N, int C) {
   return (int)(p < 1 ? 1 : p);
 }
 
-cudaError_t run_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t st) {
+// the ring's shape; nst 0: rows that do not go through it
+RingShape ring_shape(int C, int es) {
+  RingShape r;
+  r.warps = (C + 32 * RE - 1) / (32 * RE);
+  r.rows = r.warps <= RW ? RW / r.warps : 1;
+  r.tensor = (uint32_t)(r.rows * C * es);
+  r.tile = 4 * r.tensor + 16 * RW;
+  const uint32_t vec = 3u * C * 4, join = r.rows > 1 ? 16u * C : 0u;
+  const size_t n = vec + join < kRingBytes ? (kRingBytes - vec - join) / r.tile : 0;
+  r.nst = C > kRingWidth || n < 2 ? 0 : (int)(n < RING ? n : RING);
+  r.vec = r.nst * r.tile;
+  r.join = r.vec + vec;
+  r.total = r.join + join;
+  return r;
+}
+
+template <typename T>
+cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  int* err = wait_error_address();
+  if (err == nullptr) return cudaErrorInvalidSymbol;
+  a.tiles = (a.N + r.rows - 1) / r.rows;
+  const long long tiles = (long long)a.B * a.tiles;
+  a.grid = (int)(tiles < 152 ? tiles : 152);
+  static SmemOnce once;
+  if ((e = once.allow(k_norm_bwd_ring<T>, kRingBytes, dev)) != cudaSuccess) return e;
+  return launch("norm_bwd", k_norm_bwd_ring<T>, dim3(a.grid), dim3(32 * (r.warps * r.rows + 1)), r.total, st,
+                a, r, err);
+}
+
+template <typename T>
+cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
+  const Shape s = shape(a.C);
+  bool wide = a.C % (16 / (int)sizeof(T)) == 0;
+  const void* all[] = {a.x, a.u, a.weight, a.bias, a.post_weight, a.post_bias, a.gate, a.scale,
+                       a.h, a.y, a.dh, a.dy, a.dx, a.du};
+  for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
+  if (wide && backward) {
+    const RingShape r = ring_shape(a.C, sizeof(T));
+    if (r.nst > 0) return go_ring<T>(a, r, st);
+  }
+  a.parts = norm_parts(a.B, a.N, a.C);
+  if (s.ept == 8) return wide ? go<T, 8, true>(a, backward, s, st) : go<T, 8, false>(a, backward, s, st);
+  return wide ? go<T, 16, true>(a, backward, s, st) : go<T, 16, false>(a, backward, s, st);
+}
+
+}  // namespace
+
+int norm_slots(int B, int N, int C) {
+  const long long a = (long long)B * norm_parts(B, N, C), b = (long long)B + 152;
+  return (int)(a > b ? a : b);
+}
+
+cudaError_t run_norm_fwd(NormArgs& a, bool bf16, cudaStream_t st) {
   return bf16 ? pick<__nv_bfloat16>(a, false, st) : pick<float>(a, false, st);
 }
 
-cudaError_t run_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t st) {
+cudaError_t run_norm_bwd(NormArgs& a, bool bf16, cudaStream_t st) {
+  a.grid = 0;
   cudaError_t e = bf16 ? pick<__nv_bfloat16>(a, true, st) : pick<float>(a, true, st);
   if (e != cudaSuccess || a.sums == 0) return e;
-  NormArgs f = a;
   const unsigned cols = (unsigned)((a.C + 31) / 32);
-  if (a.parts > 1) {
-    e = launch("norm_seq", k_norm_seq, dim3(cols, 4, (unsigned)a.B), dim3(32, JY), 0, st, a);
-    if (e != cudaSuccess) return e;
-  } else {
+  NormArgs f = a;
+  if (a.grid == 0 && a.parts == 1) {
     f.seq = a.part;
+  } else {
+    e = launch("norm_seq", k_norm_seq, dim3(cols, 4, (unsigned)(a.B < 65535 ? a.B : 65535)),
+               dim3(32, JY), 0, st, a);
+    if (e != cudaSuccess) return e;
   }
   if (bf16) return launch("norm_final", k_norm_final<__nv_bfloat16>, dim3(cols), dim3(32, JY), 0, st, f);
   return launch("norm_final", k_norm_final<float>, dim3(cols), dim3(32, JY), 0, st, f);

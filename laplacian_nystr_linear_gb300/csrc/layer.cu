@@ -32,15 +32,13 @@ void flatten(NormArgs& a, bool seqs) {
 }
 
 struct NormWs {
-  int parts;
   size_t part, seq, total;
 };
 NormWs norm_ws(const NormArgs& a) {
   NormWs w;
-  w.parts = norm_parts(a.B, a.N, a.C);
   w.part = 0;
-  w.seq = align256((size_t)a.B * w.parts * 4 * a.C * 4);
-  w.total = w.seq + (w.parts > 1 ? align256((size_t)a.B * 4 * a.C * 4) : 0);
+  w.seq = align256((size_t)norm_slots(a.B, a.N, a.C) * 4 * a.C * 4);
+  w.total = w.seq + align256((size_t)a.B * 4 * a.C * 4);
   return w;
 }
 
@@ -143,7 +141,6 @@ int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void
            (dpost_bias || ((dgate || dscale) && post_bias) ? kSumDh : 0);
   flatten(a, gate || a.per_seq);
   const NormWs w = norm_ws(a);
-  a.parts = w.parts;
   if (a.sums) {
     if (!ws || !aligned(ws, 16)) return LAPNYS_EINVAL;
     if (ws_bytes < w.total) return LAPNYS_ENOSPC;

@@ -45,22 +45,24 @@ struct NormArgs {
   const void* dy;           // null: 0
   void* dx;
   void* du;
-  float* part;              // [B][parts][sums][C]: sums over the rows of a part, by kind
-  float* seq;               // [B][sums][C]: over the rows of a sequence
+  float* part;              // [slots][4][C]: sums over the rows of a part, by kind
+  float* seq;               // [B][4][C]: over the rows of a sequence
   void* dweight;            // each may be null
   void* dbias;
   void* dpost_weight;
   void* dpost_bias;
   void* dgate;
   void* dscale;
-  int parts;                // ranges of a sequence's rows
   int sums;                 // bits of kSum*
+  // filled by the launcher: a sequence's parts are slots b * parts .., or, where blocks take
+  // even stretches of all tiles, slot b + block for each block that meets it
+  int parts, grid, tiles;   // ranges of a sequence; blocks; tiles of a sequence
 };
 // sums over rows, of dy * (unit norm of h), dy, dh' * (unit norm of u), dh'
 enum : int { kSumDyH = 1, kSumDy = 2, kSumDhU = 4, kSumDh = 8 };
 constexpr int kNormMaxWidth = 16384;
-int norm_parts(int B, int N, int C);
-cudaError_t run_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t st);
-cudaError_t run_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t st);
+int norm_slots(int B, int N, int C);     // at the most, of either kind
+cudaError_t run_norm_fwd(NormArgs& a, bool bf16, cudaStream_t st);
+cudaError_t run_norm_bwd(NormArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace lapnys
