@@ -131,10 +131,11 @@ struct RowSum {
     const int w = (threadIdx.x >> 5) % warps;
     if ((threadIdx.x & 31) == 0) s[w] = v;
     asm volatile("barrier.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-    v = make_float2(0.f, 0.f);
-    for (int i = 0; i < warps; ++i) {
-      v.x += s[i].x;
-      v.y += s[i].y;
+    v = s[0];
+    for (int i = 1; i < warps; ++i) {
+      const float2 y = s[i];
+      v.x += y.x;
+      v.y += y.y;
     }
     return v;
   }
@@ -391,14 +392,31 @@ __device__ __forceinline__ f32x2 pair_of(uint32_t x, uint32_t y) {
   return pack2(__uint_as_float(x), __uint_as_float(y));
 }
 
+// sequence and first row of a tile, tile by tile
+struct Place {
+  int b, n;
+  __device__ __forceinline__ void next(const NormArgs& a, int rows) {
+    n += rows;
+    if (n >= a.N) {
+      n = 0;
+      ++b;
+    }
+  }
+};
+__device__ __forceinline__ Place place_of(const NormArgs& a, int u, int rows) {
+  const int b = u / a.tiles;
+  return {b, (u - b * a.tiles) * rows};
+}
+
 // The copying thread: tile by tile, the tensors that are there and the rows' statistics.
 __device__ __forceinline__ void ring_fill(const NormArgs& a, const RingShape& s, int u0, int u1, uint32_t sm,
                                           uint64_t* full, uint64_t* empty, int es, int* err) {
   const void* src[4] = {a.x, a.u, a.dh, a.dy};
   int st = 0, issued = 0;
   uint32_t ph = 0;
-  for (int u = u0; u < u1; ++u) {
-    const int b = u / a.tiles, n = (u - b * a.tiles) * s.rows, rows = min(s.rows, a.N - n);
+  Place at_tile = place_of(a, u0, s.rows);
+  for (int u = u0; u < u1; ++u, at_tile.next(a, s.rows)) {
+    const int b = at_tile.b, n = at_tile.n, rows = min(s.rows, a.N - n);
     if (!wtc::wait_or_flag(err, tc::smem_u32(&empty[st]), ph ^ 1u)) break;
     const uint32_t bar = tc::smem_u32(&full[st]), base = sm + st * s.tile;
     const size_t row = (size_t)b * a.N + n, at = row * a.C * es;
@@ -421,7 +439,8 @@ __device__ __forceinline__ void ring_fill(const NormArgs& a, const RingShape& s,
   }
 }
 
-template <typename T>
+// FULL: the warps' features are the row's, none behind it
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
   constexpr int V = 16 / (int)sizeof(T), NP = RE / V;   // features of a piece, pieces a thread
   extern __shared__ __align__(128) uint8_t smem[];
@@ -473,7 +492,7 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
         uint4 f = make_uint4(0, 0, 0, 0);
-        if (col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
+        if (FULL || col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
         p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
         p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
       }
@@ -484,15 +503,15 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       uint4 f = make_uint4(0, 0, 0, 0);
-      if (col(j) < a.C) f = lds16(tile + tensor * s.tensor + row_at + 16 * j * threads);
+      if (FULL || col(j) < a.C) f = lds16(tile + tensor * s.tensor + row_at + 16 * j * threads);
       if constexpr (V == 4) {
         p[2 * j] = pair_of(f.x, f.y);
         p[2 * j + 1] = pair_of(f.z, f.w);
       } else {
-        p[0] = pair_of(f.x << 16, f.x & 0xffff0000u);
-        p[1] = pair_of(f.y << 16, f.y & 0xffff0000u);
-        p[2] = pair_of(f.z << 16, f.z & 0xffff0000u);
-        p[3] = pair_of(f.w << 16, f.w & 0xffff0000u);
+        p[4 * j] = pair_of(f.x << 16, f.x & 0xffff0000u);
+        p[4 * j + 1] = pair_of(f.y << 16, f.y & 0xffff0000u);
+        p[4 * j + 2] = pair_of(f.z << 16, f.z & 0xffff0000u);
+        p[4 * j + 3] = pair_of(f.w << 16, f.w & 0xffff0000u);
       }
     }
   };
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
     T* o = (T*)base + row * a.C;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      if (col(j) >= a.C) continue;
+      if (!FULL && col(j) >= a.C) continue;
       if constexpr (V == 4) {
         const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
         *reinterpret_cast<float4*>(o + col(j)) = make_float4(x.x, x.y, y.x, y.y);
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 x = unpack2(p[i]);
+          const float2 x = unpack2(p[4 * j + i]);
           w[i] = wtc::pack(x.x, x.y);
         }
         *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -574,8 +593,9 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
   int st = 0, cur = -1;
   uint32_t ph = 0;
   bool late = false;
-  for (int u = u0; u < u1; ++u) {
-    const int b = a.B == 1 ? 0 : u / a.tiles, n = (u - b * a.tiles) * s.rows + group;
+  Place here = place_of(a, u0, s.rows);
+  for (int u = u0; u < u1; ++u, here.next(a, s.rows)) {
+    const int b = here.b, n = here.n + group;
     if (b != cur) {
       if (cur >= 0 && a.sums) flush(cur);
       clear();
@@ -664,6 +684,222 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
     if (++st == s.nst) { st = 0; ph ^= 1u; }
   }
   if (cur >= 0 && a.sums) flush(cur);
+}
+
+// ---------------------------------------------------------------------------
+// forward, rows of whole 16-byte pieces
+// ---------------------------------------------------------------------------
+constexpr int FW = 8;             // warps of a block at the most
+constexpr int FD = 3;             // rows of the ring, the one that is worked on among them
+
+// the E features of a thread's share of a row, as pairs
+template <typename T, int E, bool FULL>
+struct Pairs {
+  static constexpr int V = 16 / (int)sizeof(T), NP = E / V, H = E / 2;
+  int t, threads, C;
+  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * V; }
+  __device__ __forceinline__ bool in(int j) const { return FULL || col(j) < C; }
+  // this thread's pieces of a row into its own places of a ring (zeros behind the row), and
+  // out of it again
+  __device__ __forceinline__ void fetch(const T* p, uint32_t slot) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      cp_async16(slot + (j * blockDim.x + threadIdx.x) * 16, in(j) ? p + col(j) : p, in(j));
+  }
+  __device__ __forceinline__ static void take(uint32_t slot, uint4 (&w)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) w[j] = lds16(slot + (j * blockDim.x + threadIdx.x) * 16);
+  }
+  __device__ __forceinline__ static void open(const uint4 (&w)[NP], f32x2 (&p)[H]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if constexpr (V == 4) {
+        p[2 * j] = pack2(__uint_as_float(w[j].x), __uint_as_float(w[j].y));
+        p[2 * j + 1] = pack2(__uint_as_float(w[j].z), __uint_as_float(w[j].w));
+      } else {
+        const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[4 * j + i] = pack2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* o, const f32x2 (&p)[H]) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      uint32_t w[4];
+      if constexpr (V == 4) {
+        const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
+        w[0] = __float_as_uint(x.x); w[1] = __float_as_uint(x.y);
+        w[2] = __float_as_uint(y.x); w[3] = __float_as_uint(y.y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2(p[4 * j + i]);
+          w[i] = wtc::pack(x.x, x.y);
+        }
+      }
+      if (in(j)) *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // a vector in shared memory (fp32, quarters of pieces side by side)
+  __device__ __forceinline__ void vec(uint32_t base, f32x2 (&p)[H]) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        uint4 f = make_uint4(0, 0, 0, 0);
+        if (in(j)) f = lds16(base + (i * (C / V) + j * threads + t) * 16);
+        p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
+        p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
+      }
+  }
+};
+
+// Threads copy their own pieces of a row (cp.async) two rows ahead, so that neither a
+// barrier nor registers are needed for them.
+template <typename T, int E, bool FULL>
+__global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int warps, int rows) {
+  using P = Pairs<T, E, FULL>;
+  constexpr int V = P::V, NP = P::NP, H = P::H;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 slots[FW][64];
+  const int group = (threadIdx.x >> 5) / warps;
+  P sh;
+  sh.threads = 32 * warps;
+  sh.t = threadIdx.x - group * sh.threads;
+  sh.C = a.C;
+  RowSum sum{slots[group], warps, group, sh.threads};
+  const float inv = 1.f / (float)a.C;
+  const uint32_t sm = tc::smem_u32(smem);
+
+  // vectors in fp32: weight, bias, m post_weight, m post_bias
+  const bool has_m = a.u && (a.post != kNormNone || a.gate || a.scale);
+  const uint32_t part = NP * 16 * blockDim.x, ring = sm;           // a tensor's share of a slot
+  const uint32_t size = 4u * a.C, vw = FD * 2 * part, vy = vw + (a.weight ? size : 0), vm = vy + (a.bias ? size : 0),
+                 vb = vm + (has_m ? size : 0);
+  auto vectors = [&](int b) {
+    __syncthreads();
+    const size_t seq = (size_t)b * a.C;
+    for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
+      const int piece = c / V, i = c % V, at = ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
+      const size_t of = a.per_seq ? seq + c : c;
+      float m = 1.f;
+      if (a.gate) m *= as_f(((const T*)a.gate)[seq + c]);
+      if (a.scale) m *= as_f(((const T*)a.scale)[c]);
+      if (a.weight) reinterpret_cast<float*>(smem + vw)[at] = as_f(((const T*)a.weight)[of]);
+      if (a.bias) reinterpret_cast<float*>(smem + vy)[at] = as_f(((const T*)a.bias)[of]);
+      if (has_m) reinterpret_cast<float*>(smem + vm)[at] = a.post_weight ? m * as_f(((const T*)a.post_weight)[c]) : m;
+      if (a.post_bias) reinterpret_cast<float*>(smem + vb)[at] = m * as_f(((const T*)a.post_bias)[c]);
+    }
+    __syncthreads();
+  };
+  // z becomes its unit norm; returns (mean, 1 / deviation)
+  auto unit = [&](f32x2(&z)[H], int kind) {
+    float mean = 0.f;
+    if (kind == kNormLayer) {
+      f32x2 s = z[0];
+#pragma unroll
+      for (int i = 1; i < H; ++i) s = wtc::add2(s, z[i]);     // 0 behind the row
+      const float2 v = unpack2(s);
+      mean = sum(v.x + v.y) * inv;
+      const f32x2 minus = pack2(-mean, -mean);
+#pragma unroll
+      for (int i = 0; i < H; ++i) z[i] = wtc::add2(z[i], minus);
+    }
+    f32x2 q = pack2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      if (sh.in(2 * i / V)) q = fma2(z[i], z[i], q);
+    const float2 v = unpack2(q);
+    const float r = rsqrtf(sum(v.x + v.y) * inv + a.eps);
+    const f32x2 rr = pack2(r, r);
+#pragma unroll
+    for (int i = 0; i < H; ++i) z[i] = wtc::mul2(z[i], rr);
+    return make_float2(mean, r);
+  };
+
+  const long long units = (long long)a.B * a.tiles;
+  const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  Place here = place_of(a, u0, rows), there = here;
+  uint32_t slot_in = ring;
+  int left = u1 - u0;                 // tiles that are not on their way
+  auto ahead = [&]() {
+    const uint32_t slot = slot_in;
+    slot_in = slot_in + 2 * part == ring + FD * 2 * part ? ring : slot_in + 2 * part;
+    const long long row = (long long)there.b * a.N + there.n + group;
+    const bool is = left > 0 && there.n + group < a.N;
+    --left;
+    there.next(a, rows);
+    if (is) {
+      sh.fetch((const T*)a.x + row * a.C, slot);
+      if (a.u) sh.fetch((const T*)a.u + row * a.C, slot + part);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < FD - 1; ++i) ahead();
+  int cur = -1;
+  uint32_t slot_out = ring;
+  for (int u = u0; u < u1; ++u, here.next(a, rows)) {
+    const int b = here.b;
+    const long long row = here.n + group < a.N ? (long long)b * a.N + here.n + group : -1;
+    if (b != cur) {
+      if (cur < 0 || a.gate || a.per_seq) vectors(b);
+      cur = b;
+    }
+    ahead();                          // into the slot of the row before
+    asm volatile("cp.async.wait_group %0;" ::"n"(FD - 1) : "memory");
+    f32x2 h[H], z[H];
+    {
+      const uint32_t slot = slot_out;
+      slot_out = slot_out + 2 * part == ring + FD * 2 * part ? ring : slot_out + 2 * part;
+      uint4 w[NP];
+      P::take(slot, w);
+      P::open(w, h);
+      if (a.u) {
+        P::take(slot + part, w);
+        P::open(w, z);
+      }
+    }
+    if (row < 0) continue;
+    float2 su = make_float2(0.f, 0.f), sy = make_float2(0.f, 0.f);
+    f32x2 v[H];
+    if (a.u) {
+      if (a.post != kNormNone) su = unit(z, a.post);
+      if (has_m) {
+        sh.vec(sm + vm, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = fma2(z[i], v[i], h[i]);     // 0 behind the row
+      } else {
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = wtc::add2(z[i], h[i]);
+      }
+      if (a.post_bias) {
+        sh.vec(sm + vb, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = wtc::add2(h[i], v[i]);
+      }
+      if (a.h) sh.store((T*)a.h + row * a.C, h);
+    } else if (a.h) {
+      sh.store((T*)a.h + row * a.C, h);
+    }
+    if (a.y) {
+      sy = unit(h, a.pre);
+      if (a.weight) {
+        sh.vec(sm + vw, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = wtc::mul2(h[i], v[i]);
+      }
+      if (a.bias) {
+        sh.vec(sm + vy, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = wtc::add2(h[i], v[i]);
+      }
+      sh.store((T*)a.y + row * a.C, h);
+    }
+    if (a.stats && sh.t == 0) reinterpret_cast<float4*>(a.stats)[row] = make_float4(su.x, su.y, sy.x, sy.y);
+  }
 }
 
 constexpr int JY = 32;   // threads that share a column of the joins
@@ -760,8 +996,9 @@ cudaError_t go(const NormArgs& a, bool backward, const Shape& s, cudaStream_t st
   if (!backward) {
     const long long rows = (long long)a.B * a.N, all = (rows + s.groups - 1) / s.groups;
     const dim3 grid((unsigned)(all < 152 * 64 ? all : 152 * 64));
-    if (threads <= 256)
-      return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 256>, grid, block, 0, st, a, s.warps);
+    if constexpr (!WIDE)
+      if (threads <= 256)
+        return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 256>, grid, block, 0, st, a, s.warps);
     if constexpr (EPT > 8)
       return launch("norm_fwd", k_norm_fwd<T, EPT, WIDE, 1024>, grid, block, 0, st, a, s.warps);
   } else {
@@ -814,10 +1051,31 @@ cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
   a.tiles = (a.N + r.rows - 1) / r.rows;
   const long long tiles = (long long)a.B * a.tiles;
   a.grid = (int)(tiles < 152 ? tiles : 152);
-  static SmemOnce once;
-  if ((e = once.allow(k_norm_bwd_ring<T>, kRingBytes, dev)) != cudaSuccess) return e;
-  return launch("norm_bwd", k_norm_bwd_ring<T>, dim3(a.grid), dim3(32 * (r.warps * r.rows + 1)), r.total, st,
-                a, r, err);
+  static SmemOnce once[2];
+  const bool full = a.C == 32 * r.warps * RE;
+  auto* k = full ? k_norm_bwd_ring<T, true> : k_norm_bwd_ring<T, false>;
+  if ((e = once[full].allow(k, kRingBytes, dev)) != cudaSuccess) return e;
+  return launch("norm_bwd", k, dim3(a.grid), dim3(32 * (r.warps * r.rows + 1)), r.total, st, a, r, err);
+}
+
+template <typename T, int E>
+cudaError_t go_rows(NormArgs& a, const Shape& s, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  static SmemOnce once[2];
+  const bool full = a.C == 32 * s.warps * E;
+  auto* k = full ? k_norm_fwd_rows<T, E, true> : k_norm_fwd_rows<T, E, false>;
+  // ring, and the vectors that there are
+  const int vecs = (a.weight != nullptr) + (a.bias != nullptr) + (a.post_bias != nullptr) +
+                   (a.u && (a.post != kNormNone || a.gate || a.scale));
+  const size_t threads = 32 * s.warps * s.groups, smem = FD * 2 * threads * E * sizeof(T) + (size_t)vecs * a.C * 4;
+  if ((e = once[full].allow(k, FD * 2 * 32 * FW * E * sizeof(T) + 4 * 32 * FW * E * 4, dev)) != cudaSuccess) return e;
+  a.tiles = (a.N + s.groups - 1) / s.groups;
+  // as many blocks as an SM's shared memory takes (4 KB are static, 1 KB reserved), two at the most
+  const long long tiles = (long long)a.B * a.tiles, most = 152LL * (2 * (smem + 5120) <= 228 * 1024 ? 2 : 1);
+  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
+  return launch("norm_fwd", k, dim3(grid), dim3(32 * s.warps * s.groups), smem, st, a, s.warps, s.groups);
 }
 
 template <typename T>
@@ -831,8 +1089,10 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
     const RingShape r = ring_shape(a.C, sizeof(T));
     if (r.nst > 0) return go_ring<T>(a, r, st);
   }
+  if (wide && !backward && s.warps <= FW)
+    return s.ept == 8 ? go_rows<T, 8>(a, s, st) : go_rows<T, 16>(a, s, st);
   a.parts = norm_parts(a.B, a.N, a.C);
-  if (s.ept == 8) return wide ? go<T, 8, true>(a, backward, s, st) : go<T, 8, false>(a, backward, s, st);
+  if (s.ept == 8) return go<T, 8, false>(a, backward, s, st);
   return wide ? go<T, 16, true>(a, backward, s, st) : go<T, 16, false>(a, backward, s, st);
 }
 

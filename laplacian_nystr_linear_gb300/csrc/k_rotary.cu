@@ -20,33 +20,69 @@ namespace {
 
 constexpr int RT = 128;   // threads of a block
 
-// V elements at a time, 16 bytes of them or one
+// V elements as they lie: words of two bf16, single bf16, or fp32
 template <typename T, int V>
 struct Piece {
-  T v[V];
+  static constexpr int W = V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1;
+  uint32_t w[W];
+  __device__ __forceinline__ void get(const T* p) {
+    if constexpr (W == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x; w[1] = x.y;
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void put(T* p) const {
+    if constexpr (W == 4)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (W == 2)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+  }
+  __device__ __forceinline__ void open(float (&v)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (V == 1) {
+      v[0] = __uint_as_float(w[0] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        v[i] = __uint_as_float(w[i / 2] << 16);
+        v[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void close(const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (V == 1) {
+      w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
 };
-template <typename T, int V>
-__device__ __forceinline__ Piece<T, V> get(const T* p) {
-  Piece<T, V> r;
-  if constexpr (V * sizeof(T) == 16)
-    *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(p);
-  else
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = p[i];
-  return r;
+// (a, b) turned; the same roundings in every variant
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+  const float x = __fmaf_rn(a, c, -__fmul_rn(b, s));
+  b = __fmaf_rn(b, c, __fmul_rn(a, s));
+  a = x;
 }
-template <typename T, int V>
-__device__ __forceinline__ void put(T* p, const Piece<T, V>& r) {
-  if constexpr (V * sizeof(T) == 16)
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
-  else
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = r.v[i];
-}
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void of_f(float& o, float x) { o = x; }
-__device__ __forceinline__ void of_f(__nv_bfloat16& o, float x) { o = __float2bfloat16_rn(x); }
 
 // A work item is V pairs of a token in the half layout, V features interleaved
 // (V / 2 pairs; one pair when V is 1), and last the pieces that are copied.
@@ -88,48 +124,47 @@ __global__ void __launch_bounds__(RT) k_rotary(RotaryArgs a) {
       s[i] = (a.inverse ? -sn : sn) * a.factor;
     }
   }
-  const int heads = a.Hq + a.Hkv;
-  const int h0 = blockIdx.y * a.heads, h1 = min(heads, h0 + a.heads);
-  const size_t row = (size_t)a.d, head = (size_t)a.N * a.d;
-  auto from = [&](int h) {
-    const T* base = h < a.Hq ? (const T*)a.q + ((size_t)b * a.Hq + h) * head
-                             : (const T*)a.k + ((size_t)b * a.Hkv + (h - a.Hq)) * head;
-    return base + n * row + at;
-  };
-  auto to = [&](int h) {
-    T* base = h < a.Hq ? (T*)a.q_out + ((size_t)b * a.Hq + h) * head
-                       : (T*)a.k_out + ((size_t)b * a.Hkv + (h - a.Hq)) * head;
-    return base + n * row + at;
-  };
   if (!turn && a.q_out == a.q && a.k_out == a.k) return;   // in place
-  for (int h = h0; h < h1; h += DEEP) {
-    Piece<T, V> x[DEEP], z[DEEP];
+  const int h0 = blockIdx.y * a.heads, h1 = min(a.Hq + a.Hkv, h0 + a.heads);
+  const size_t head = (size_t)a.N * a.d, in_head = (size_t)n * a.d + at;
+  // heads [lo, hi) of a tensor that has H of them
+  auto run = [&](const void* in, void* out, int H, int lo, int hi) {
+    if (lo >= hi) return;
+    const size_t first = ((size_t)b * H + lo) * head + in_head;
+    const T* src = (const T*)in + first;
+    T* dst = (T*)out + first;
+    for (int left = hi - lo; left > 0; left -= DEEP, src += DEEP * head, dst += DEEP * head) {
+      Piece<T, V> x[DEEP], z[DEEP];
 #pragma unroll
-    for (int i = 0; i < DEEP; ++i)
-      if (h + i < h1) {
-        const T* p = from(h + i);
-        x[i] = get<T, V>(p);
-        if (PAIR && second) z[i] = get<T, V>(p + gap);
-      }
-#pragma unroll
-    for (int i = 0; i < DEEP; ++i)
-      if (h + i < h1) {
-        T* o = to(h + i);
-        if (turn) {
-#pragma unroll
-          for (int e = 0; e < P; ++e) {
-            T& u = PAIR ? x[i].v[e] : x[i].v[(2 * e) % V];
-            T& w = PAIR ? z[i].v[e] : x[i].v[(2 * e + 1) % V];
-            const float f = to_f(u), g = to_f(w);
-            // the same roundings in every variant
-            of_f(u, __fmaf_rn(f, c[e], -__fmul_rn(g, s[e])));
-            of_f(w, __fmaf_rn(g, c[e], __fmul_rn(f, s[e])));
-          }
+      for (int i = 0; i < DEEP; ++i)
+        if (i < left) {
+          x[i].get(src + i * head);
+          if (PAIR && second) z[i].get(src + i * head + gap);
         }
-        put<T, V>(o, x[i]);
-        if (PAIR && second) put<T, V>(o + gap, z[i]);
-      }
-  }
+#pragma unroll
+      for (int i = 0; i < DEEP; ++i)
+        if (i < left) {
+          if (turn) {
+            float f[V], g[V];
+            x[i].open(f);
+            if constexpr (PAIR) {
+              z[i].open(g);
+#pragma unroll
+              for (int e = 0; e < V; ++e) turn_pair(f[e], g[e], c[e], s[e]);
+              z[i].close(g);
+            } else {
+#pragma unroll
+              for (int e = 0; e < P; ++e) turn_pair(f[2 * e], f[2 * e + 1], c[e], s[e]);
+            }
+            x[i].close(f);
+          }
+          x[i].put(dst + i * head);
+          if (PAIR && second) z[i].put(dst + i * head + gap);
+        }
+    }
+  };
+  run(a.q, a.q_out, a.Hq, h0, min(h1, a.Hq));
+  run(a.k, a.k_out, a.Hkv, max(h0 - a.Hq, 0), h1 - a.Hq);
 }
 
 template <typename T, bool HALF, int V>
@@ -160,12 +195,12 @@ cudaError_t pick(RotaryArgs& a, bool half, bool whole, cudaStream_t st) {
 }  // namespace
 
 cudaError_t run_rotary(RotaryArgs& a, bool half, bool bf16, cudaStream_t st) {
-  const int v = bf16 ? 8 : 4;
-  auto al = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
+  const int v = 4;
+  auto al = [&](const void* p) { return ((uintptr_t)p & (bf16 ? 7 : 15)) == 0; };
   // 16-byte pieces where every piece of every row starts on 16 bytes
   const bool whole = al(a.q) && al(a.k) && al(a.q_out) && al(a.k_out) && a.d % v == 0 &&
                      a.rot % v == 0 && (!half || a.rot / 2 % v == 0);
-  return bf16 ? pick<__nv_bfloat16, 8>(a, half, whole, st) : pick<float, 4>(a, half, whole, st);
+  return bf16 ? pick<__nv_bfloat16, 4>(a, half, whole, st) : pick<float, 4>(a, half, whole, st);
 }
 
 }  // namespace lapnys

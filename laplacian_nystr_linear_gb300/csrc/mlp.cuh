@@ -49,7 +49,8 @@ __device__ __forceinline__ void mlp_act(float g, float& p, float& slope) {
     slope = fmaf(g * 0.39894228040143268f, e, c);
   } else {
     // 0.5 (1 + tanh z) = sigmoid(2 z)
-    const float g2 = g * g, k = 1.5957691216057308f;      // 2 sqrt(2 / pi)
+    // (far out both are 0 or 1 long before; bounded, the square stays finite)
+    const float g2 = fminf(g * g, 1e18f), k = 1.5957691216057308f;      // 2 sqrt(2 / pi)
     const float s = mlp_sigmoid<EXACT>(k * g * fmaf(0.044715f, g2, 1.f));
     p = g * s;
     slope = fmaf(p * (1.f - s), k * fmaf(3.f * 0.044715f, g2, 1.f), s);
