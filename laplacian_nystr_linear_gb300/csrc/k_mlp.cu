@@ -132,7 +132,7 @@ struct Item {
 template <int TN>
 __device__ __forceinline__ Item decode(const MlpGemmArgs& a, int it) {
   Item r;
-  const unsigned ntot = a.nt * a.nparts, tiles = a.mt * ntot, all = a.kst * a.kparts;
+  const unsigned ntot = a.nt * a.nparts, tiles = a.mt * ntot, all = a.kst * a.kparts * a.kplanes;
   r.sp = 0;
   r.ks0 = 0;
   r.ks1 = (int)all;
@@ -258,8 +258,17 @@ __device__ __forceinline__ void fetch(const MlpKept& k, size_t block, Kept& r) {
   for (int i = 0; i < 4; ++i) r.w[i] = __ldcs(o + i * 32);
   r.scale = k.scale[block * 32 + lane];
 }
-// p (h = 0) or q (h = 1), times x, as bf16 pairs
-__device__ __forceinline__ void times_kept(const Kept& k, int h, const uint32_t (&x)[16], uint32_t* out) {
+// what the rounding of a pair left (h: the pair as bf16); infinities leave nothing
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t h) {
+  uint32_t r = wtc::pack_rest(a, b, h);
+  if ((h & 0x7f80u) == 0x7f80u) r &= 0xffff0000u;
+  if ((h & 0x7f800000u) == 0x7f800000u) r &= 0x0000ffffu;
+  return r;
+}
+// p (h = 0) or q (h = 1), times x, as bf16 pairs, and (TWO) what their rounding left
+template <bool TWO>
+__device__ __forceinline__ void times_kept(const Kept& k, int h, const uint32_t (&x)[16], uint32_t* out,
+                                           uint32_t* rest) {
   const float s = pow2((int)((k.scale >> (8 * h)) & 0xff) - 128);
   const f32x2 f = pack2(s, s);
 #pragma unroll
@@ -273,6 +282,7 @@ __device__ __forceinline__ void times_kept(const Kept& k, int h, const uint32_t 
       const float2 z = unpack2(wtc::mul2(wtc::mul2(pack2(y.x, y.y), f),
                                          pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
       out[4 * i + j] = wtc::pack(z.x, z.y);
+      if (TWO) rest[4 * i + j] = rest_of(z.x, z.y, out[4 * i + j]);
     }
   }
 }
@@ -385,7 +395,7 @@ __device__ __forceinline__ void out_rows(const MlpGemmArgs& a, int part, int m0,
   __syncwarp();
 }
 
-template <bool F32, int EPI>
+template <bool F32, int EPI, bool TWO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     k_mlp_gemm(const __grid_constant__ Maps mp, MlpGemmArgs a) {
   using G = Cfg<F32>;
@@ -442,25 +452,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
         const int am = r.m0 + (int)rank * BM;
         const int bn = EPI == kMlpGlu ? r.n0 : r.n0 + (int)rank * BNC;
         for (int ks = r.ks0; ks < r.ks1 && !bad; ++ks) {
-          const int kp = a.kparts > 1 ? ks / a.kst : 0, k0 = (ks - kp * a.kst) * BK;
+          const int pl = a.kplanes > 1 && ks >= a.kst * a.kparts ? 1 : 0, kr = ks - pl * a.kst * a.kparts;
+          const int kp = a.kparts > 1 && kr >= a.kst ? 1 : 0, k0 = (kr - kp * a.kst) * BK;
           const int bp = EPI == kMlpGlu ? (int)rank : (a.kparts > 1 ? kp : r.part);
 #pragma unroll 1
           for (int p = 0; p < PLANES; ++p) {
+            const int pa = F32 ? p : (a.two_a ? pl : 0), pb = F32 ? p : (a.two_b ? pl : 0);
             if (!wtc::wait_or_flag(a.err, tc::smem_u32(&empty[st]), ph ^ 1u)) { bad = true; break; }
             const uint32_t bar = at_leader(tc::smem_u32(&full[st]));
             if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[st]), 2 * G::SLOT);
             const uint32_t sa = sm + st * G::SLOT, sb = sa + G::A_BYTES;
             if (a.amn) {
 #pragma unroll
-              for (int i = 0; i < BM / 64; ++i) tma4(sa + i * BLK64, &mp.a, am + 64 * i, kp, k0, p, bar);
+              for (int i = 0; i < BM / 64; ++i) tma4(sa + i * BLK64, &mp.a, am + 64 * i, kp, k0, pa, bar);
             } else {
-              tma4(sa, &mp.a, k0, kp, am, p, bar);
+              tma4(sa, &mp.a, k0, kp, am, pa, bar);
             }
             if (a.bmn) {
 #pragma unroll
-              for (int i = 0; i < BNC / 64; ++i) tma4(sb + i * BLK64, &mp.b, bn + 64 * i, bp, k0, p, bar);
+              for (int i = 0; i < BNC / 64; ++i) tma4(sb + i * BLK64, &mp.b, bn + 64 * i, bp, k0, pb, bar);
             } else {
-              tma4(sb, &mp.b, k0, bp, bn, p, bar);
+              tma4(sb, &mp.b, k0, bp, bn, pb, bar);
             }
             ++issued;
             if (++st == NST) { st = 0; ph ^= 1u; }
@@ -551,10 +563,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     uint32_t u = 0;
     int li = 0;
     bool bad = false;
-    // dglu of bf16 calls: p and q of four blocks, each fetched again for four blocks later
+    // dglu of bf16 calls: p and q of DEEP blocks, each fetched again for DEEP blocks later
     // as soon as it is used (read when they were needed, a tile's waits for memory took
     // longer than its products: XXX)
-    constexpr int DEEP = 4;
+    constexpr int DEEP = TWO ? 2 : 4;   // (two planes take the registers of two)
     Kept kept2[DEEP];
     auto ahead = [&](const Item& r, int col, Kept& k) {
       const int m = r.m0 + (int)rank * BM + 32 * q, n = r.n0 + col;
@@ -647,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
           }
           release();
         } else if constexpr (EPI == kMlpGlu) {
-          uint32_t w[16];
+          uint32_t w[16], rest[TWO ? 16 : 1];
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             uint32_t x[16], y[16];
@@ -659,18 +671,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
             float h[16];
             gated(col0 + 16 * ch, reinterpret_cast<float(&)[16]>(x), reinterpret_cast<float(&)[16]>(y), h);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[8 * ch + i] = wtc::pack(h[2 * i], h[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) {
+              w[8 * ch + i] = wtc::pack(h[2 * i], h[2 * i + 1]);
+              if constexpr (TWO) rest[8 * ch + i] = rest_of(h[2 * i], h[2 * i + 1], w[8 * ch + i]);
+            }
           }
-          const int n = r.n0 + col0;
-          if (some && n < a.N)
-            store_bf16((__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n, a.ldo, 32 * q, rows,
-                       min(32, (a.N - n + 7) & ~7), w);
+          const int n = r.n0 + col0, cols = min(32, (a.N - n + 7) & ~7);
+          if (some && n < a.N) {
+            __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
+            store_bf16(o, a.ldo, 32 * q, rows, cols, w);
+            if constexpr (TWO) store_bf16(o + a.plane_out, a.ldo, 32 * q, rows, cols, rest);
+          }
         } else if constexpr (EPI == kMlpDglu) {
 const bool more = it + pairs < a.items;
           const Item after = more ? decode<TN>(a, it + pairs) : r;
 #pragma unroll 1
           for (int c0 = 0; c0 < COLS; c0 += 16 * DEEP) {
-            uint32_t dg[16], du[16];
+            uint32_t dg[16], du[16], rg[TWO ? 16 : 1], ru[TWO ? 16 : 1];
 #pragma unroll
             for (int j = 0; j < DEEP; ++j) {
               const int c = c0 + 16 * j;
@@ -678,8 +695,9 @@ const bool more = it + pairs < a.items;
               ld16(d + c, x);
               wait16(x);
               if (j == DEEP - 1 && c == COLS - 16) release();
-              times_kept(kept2[j], 1, x, dg + 8 * (j & 1));    // dg = dh q, du = dh p
-              times_kept(kept2[j], 0, x, du + 8 * (j & 1));
+              const int o8 = 8 * (j & 1);
+              times_kept<TWO>(kept2[j], 1, x, dg + o8, rg + (TWO ? o8 : 0));    // dg = dh q, du = dh p
+              times_kept<TWO>(kept2[j], 0, x, du + o8, ru + (TWO ? o8 : 0));
               const bool here = c + 16 * DEEP < COLS;
               if (here || more) ahead(here ? r : after, col0 + (here ? c + 16 * DEEP : 16 * j), kept2[j]);
               const int n = r.n0 + col0 + c - 16;
@@ -688,6 +706,10 @@ const bool more = it + pairs < a.items;
                 const int cols = min(32, (a.N - n + 7) & ~7);
                 store_bf16(o, a.ldo, 32 * q, rows, cols, dg);
                 store_bf16(o + a.part_out, a.ldo, 32 * q, rows, cols, du);
+                if constexpr (TWO) {
+                  store_bf16(o + a.plane_out, a.ldo, 32 * q, rows, cols, rg);
+                  store_bf16(o + a.plane_out + a.part_out, a.ldo, 32 * q, rows, cols, ru);
+                }
               }
             }
           }
@@ -887,13 +909,13 @@ bool map_view(CUtensorMap* t, const MlpView& v, int box_rows) {
   return encode_tiled_bf16_sw128(t, 4, v.p, dim, stride, box);
 }
 
-template <bool F32, int EPI>
+template <bool F32, int EPI, bool TWO = false>
 cudaError_t go(const char* name, const Maps& mp, const MlpGemmArgs& g, int dev, int sms, cudaStream_t st) {
   static SmemOnce once;
-  const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI>, Cfg<F32>::SMEM, dev);
+  const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI, TWO>, Cfg<F32>::SMEM, dev);
   if (e != cudaSuccess) return e;
   const int pairs = g.items < sms / 2 ? g.items : sms / 2;
-  return launch(name, k_mlp_gemm<F32, EPI>, dim3((unsigned)(2 * pairs)), dim3(threads_of(EPI)), (size_t)Cfg<F32>::SMEM,
+  return launch(name, k_mlp_gemm<F32, EPI, TWO>, dim3((unsigned)(2 * pairs)), dim3(threads_of(EPI)), (size_t)Cfg<F32>::SMEM,
                 st, mp, g);
 }
 
@@ -921,7 +943,7 @@ int mlp_splits(long long tiles, int ksteps, double mn, bool f32) {
   return best;
 }
 
-cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, const MlpView& b,
+cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, bool two, const MlpView& a, const MlpView& b,
                          MlpGemmArgs& g, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
@@ -939,6 +961,12 @@ cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, 
   memset(&mp, 0, sizeof(mp));
   if (!map_view(&mp.a, a, g.amn ? 64 : BM) || !map_view(&mp.b, b, g.bmn ? 64 : bn / 2))
     return cudaErrorInvalidValue;
+  g.two_a = !f32 && a.planes == 2;
+  g.two_b = !f32 && b.planes == 2;
+  g.kplanes = g.two_a || g.two_b ? 2 : 1;
+  if (!f32 && two)
+    return epi == kMlpGlu ? go<false, kMlpGlu, true>(name, mp, g, dev, sms, st)
+                          : go<false, kMlpDglu, true>(name, mp, g, dev, sms, st);
 #define GO(E) return f32 ? go<true, E>(name, mp, g, dev, sms, st) : go<false, E>(name, mp, g, dev, sms, st)
   switch (epi) {
     case kMlpRows: GO(kMlpRows);

@@ -13,7 +13,8 @@
 // into a ring of 32 KB slots (about 190 KB in flight an SM), one issues tcgen05 products,
 // four warps read the sums.  fp32: on the FP32 pipe, 128 columns a warp, four a lane, rows
 // in packed pairs, x from shared memory; 16 rows a CTA, further rows by CTAs beside it that
-// read the same weights out of L2.
+// read the same weights out of L2.  bf16 calls of up to 32 rows keep h in two bf16 parts, the
+// second as further rows of the second product, which is bound by its weights all the same.
 #include <cuda.h>
 
 #include <cstring>
@@ -308,8 +309,14 @@ __global__ void __launch_bounds__(256) k_mlp_few_join(MlpFewArgs a) {
     // the CTA of unit u: the greatest c with units c / grid <= u
     const int c0 = (int)(((first + 1) * a.grid - 1) / units), c1 = (int)(((last + 1) * a.grid - 1) / units);
     const float* s = a.part + ((size_t)(block + c0) * a.T + t) * FN + threadIdx.x;
+    float lo = 0.f;                   // of the rows that are what rounding left of x
+    const bool both = a.T > a.rows;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c, s += (size_t)a.T * FN) v[p] += *s;
+    for (int c = c0; c <= c1; ++c, s += (size_t)a.T * FN) {
+      v[p] += *s;
+      if (both) lo += s[(size_t)a.rows * FN];
+    }
+    v[p] += lo;
     if (a.bias && n < a.N) {
       if constexpr (sizeof(T) == 4)
         v[p] += ((const T*)a.bias)[(size_t)p * a.N + n];
@@ -332,8 +339,11 @@ __global__ void __launch_bounds__(256) k_mlp_few_join(MlpFewArgs a) {
   T* o = (T*)a.out + (size_t)t * a.N + n;
   if constexpr (sizeof(T) == 4)
     *o = v[0];
-  else
+  else {
     *o = __float2bfloat16_rn(v[0]);
+    const float hi = __bfloat162float(__float2bfloat16_rn(v[0]));
+    if (a.two) o[(size_t)a.rows * a.N] = __float2bfloat16_rn(isinf(hi) ? 0.f : v[0] - hi);
+  }
 }
 
 // grid and units of a product: a CTA for each SM (fp32: two), as far as there are units
@@ -362,6 +372,10 @@ bool mlp_few_ok(int T, int C, int F, bool f32) {
   if ((double)C * F >= 1e12) return false;      // units are counted in 32 bits
   return f32 ? T <= FEW_F32 : T <= FEW_BF16 && C % 8 == 0 && F % 8 == 0;
 }
+
+// bf16: what rounding leaves of h goes along as further rows of the second product, as far
+// as they fit (they cost it nothing: it is bound by the weights)
+bool mlp_few_two(int T, bool f32) { return !f32 && 2 * T <= FEW_BF16; }
 
 size_t mlp_few_bytes(int T, int N, int parts) {
   // slots of FNF or FNB columns: as many of the one, half as wide, as are needed of either
@@ -399,7 +413,7 @@ cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st) {
                  : launch("mlp_few", k_mlp_few_tc, dim3(a.grid), dim3(NTC), smem, st, mp, a, rows, nst);
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.nb, a.T);
+  const dim3 grid(a.nb, a.rows);
   if (f32) return launch_after("mlp_few_join", k_mlp_few_join<float>, grid, dim3(FNF), 0, st, a);
   return launch_after("mlp_few_join", k_mlp_few_join<__nv_bfloat16>, grid, dim3(FNB), 0, st, a);
 }

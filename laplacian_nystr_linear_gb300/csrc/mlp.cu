@@ -18,7 +18,8 @@ int up8(int x) { return (x + 7) & ~7; }
 struct Mlp {
   int T, C, F, Cp, Fp;
   bool f32;
-  int planes;
+  int planes;   // of packed operands
+  int hidden;   // of h and of (dg | du)
   // operands that the products cannot read where they lie: fp32 (three planes), or rows
   // that are not whole 16-byte pieces
   bool pack_c, pack_f;
@@ -35,6 +36,13 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   m.T = T; m.C = C; m.F = F; m.Cp = up8(C); m.Fp = up8(F);
   m.f32 = dtype == LAPNYS_F32;
   m.planes = m.f32 ? 3 : 1;
+  // bf16 calls round h and the gradient of (g | u) between the products, which puts the
+  // results' errors at 1.4 times their own rounding's, more where few values are summed
+  // (1.7 at 4 rows of 64).  Calls of up to 2^28 multiply-adds a product, whose time is
+  // launches and latency, keep them in two parts, and the products that read them run over
+  // both (8 + 8 bits: their own rounding is left alone; a training step of 256 rows, 512 x
+  // 2048 features: XXX); larger ones would take half as long again.
+  m.hidden = m.f32 ? 3 : (double)T * C * F <= 268435456.0 ? 2 : 1;
   m.pack_c = m.f32 || C % 8 != 0;
   m.pack_f = m.f32 || F % 8 != 0;
   return LAPNYS_OK;
@@ -46,7 +54,9 @@ int feature_blocks(const Mlp& m) { return (m.F + kMlpBlock - 1) / kMlpBlock; }
 struct Ctx {
   size_t h, pq, scale, total;
 };
-size_t h_bytes(const Mlp& m) { return align256((size_t)m.planes * m.T * m.Fp * 2); }
+size_t h_bytes(const Mlp& m) { return align256((size_t)m.hidden * m.T * m.Fp * 2); }
+// parts that K runs over beyond the operands' own: the two of h or (dg | du)
+int twice(const Mlp& m) { return m.hidden == 2 ? 2 : 1; }
 Ctx ctx_of(const Mlp& m) {
   Ctx c;
   const size_t blocks = (size_t)((m.T + 31) / 32) * feature_blocks(m);
@@ -90,12 +100,13 @@ Ws ws_of(const Mlp& m, bool backward) {
   size_t part;
   if (!backward) {
     room(w.h, h_bytes(m));
-    part = split_of(m, m.T, m.C, 1, m.F, 1).bytes;
+    part = split_of(m, m.T, m.C, 1, m.F, twice(m)).bytes;
   } else {
     room(w.dy, m.pack_c ? two * m.T * m.Cp : 0);
-    room(w.dz, two * m.T * 2 * m.Fp);
-    part = split_of(m, m.T, m.C, 1, m.F, 2).bytes;
-    const size_t wi = split_of(m, m.C, m.F, 2, m.T, 1).bytes, wo = split_of(m, m.F, m.C, 1, m.T, 1).bytes;
+    room(w.dz, 2 * (size_t)m.hidden * m.T * 2 * m.Fp);
+    part = split_of(m, m.T, m.C, 1, m.F, 2 * twice(m)).bytes;
+    const size_t wi = split_of(m, m.C, m.F, 2, m.T, twice(m)).bytes;
+    const size_t wo = split_of(m, m.F, m.C, 1, m.T, twice(m)).bytes;
     part = part > wi ? part : wi;
     part = part > wo ? part : wo;
     const size_t ci = (size_t)mlp_colsum_ranges(m.T, 2 * m.F) * 2 * m.F * 4;
@@ -106,8 +117,9 @@ Ws ws_of(const Mlp& m, bool backward) {
   w.total = o;
   if (!backward && mlp_few_ok(m.T, m.C, m.F, m.f32)) {
     // h and the partial sums of one product, then the other's; without a ctx that is all
-    const size_t a = mlp_few_bytes(m.T, m.F, 2), b = mlp_few_bytes(m.T, m.C, 1);
-    const size_t few = align256((size_t)m.T * m.F * (m.f32 ? 4 : 2)) + (a > b ? a : b);
+    const int rows = mlp_few_two(m.T, m.f32) ? 2 * m.T : m.T;
+    const size_t a = mlp_few_bytes(m.T, m.F, 2), b = mlp_few_bytes(rows, m.C, 1);
+    const size_t few = align256((size_t)rows * m.F * (m.f32 ? 4 : 2)) + (a > b ? a : b);
     w.total = few > w.total ? few : w.total;
   }
   return w;
@@ -151,7 +163,7 @@ struct Run {
   void rows(const char* name, const MlpView& a, bool amn, const MlpView& b, bool bmn, int M, int N,
             int nparts, int kparts, int K, const void* bias, void* out, size_t part_at) {
     if (e != cudaSuccess) return;
-    const Split s = split_of(m, M, N, nparts, K, kparts);
+    const Split s = split_of(m, M, N, nparts, K, kparts * twice(m));   // every one reads h or (dg | du)
     MlpGemmArgs g;
     memset(&g, 0, sizeof(g));
     g.M = M; g.N = N; g.nparts = nparts; g.kparts = kparts; g.splits = s.n;
@@ -162,13 +174,13 @@ struct Run {
       g.ldo = (size_t)nparts * N;
       g.part_out = N;
       g.wide = N % (m.f32 ? 4 : 8) == 0;
-      e = run_mlp_gemm(name, kMlpRows, m.f32, a, b, g, st);
+      e = run_mlp_gemm(name, kMlpRows, m.f32, false, a, b, g, st);
       return;
     }
     g.out = ws + part_at;
     g.part_out = up8(N);
     g.ldo = g.part_out * nparts;
-    e = run_mlp_gemm(name, kMlpPart, m.f32, a, b, g, st);
+    e = run_mlp_gemm(name, kMlpPart, m.f32, false, a, b, g, st);
     if (e != cudaSuccess) return;
     MlpReduceArgs r;
     memset(&r, 0, sizeof(r));
@@ -243,12 +255,14 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
     MlpFewArgs f;
     memset(&f, 0, sizeof(f));
     f.x = x; f.w = w_in; f.bias = b_in; f.out = ws;
-    f.part = (float*)((uint8_t*)ws + align256((size_t)T * F * (m.f32 ? 4 : 2)));
-    f.T = T; f.K = C; f.N = F; f.parts = 2; f.act = act;
+    const bool two = mlp_few_two(T, m.f32);
+    const int rows = two ? 2 * T : T;       // of h
+    f.part = (float*)((uint8_t*)ws + align256((size_t)rows * F * (m.f32 ? 4 : 2)));
+    f.T = T; f.rows = T; f.K = C; f.N = F; f.parts = 2; f.act = act; f.two = two;
     const cudaError_t e = run_mlp_few(f, m.f32, stream);
     if (e != cudaSuccess) return status(e);
     f.x = ws; f.w = w_out; f.bias = b_out; f.out = y;
-    f.K = F; f.N = C; f.parts = 1; f.act = -1;
+    f.T = rows; f.K = F; f.N = C; f.parts = 1; f.act = -1; f.two = 0;
     f.second = true;
     return status(run_mlp_few(f, m.f32, stream));
   }
@@ -270,9 +284,9 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
     g.plane_out = (size_t)T * m.Fp;
     g.kept = kept_of(m, ctx);
     g.fblocks = feature_blocks(m);
-    r.e = run_mlp_gemm("mlp_in", kMlpGlu, m.f32, vx, vi, g, stream);
+    r.e = run_mlp_gemm("mlp_in", kMlpGlu, m.f32, m.hidden == 2, vx, vi, g, stream);
   }
-  const MlpView vh = view(h, F, 1, T, m.planes, m.Fp);
+  const MlpView vh = view(h, F, 1, T, m.hidden, m.Fp);
   r.rows("mlp_out", vh, false, vo, true, T, C, 1, 1, F, b_out, y, w.part);
   return status(r.e);
 }
@@ -301,7 +315,7 @@ int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const voi
   if (hidden || dw_out) vy = r.operand(dy, m.pack_c, w.dy, T, 1, C);
   r.packs();
   __nv_bfloat16* dz = (__nv_bfloat16*)(r.ws + w.dz);
-  const MlpView vz = view(dz, F, 2, T, m.planes, m.Fp);
+  const MlpView vz = view(dz, F, 2, T, m.hidden, m.Fp);
   if (hidden && r.e == cudaSuccess) {
     MlpGemmArgs g;
     memset(&g, 0, sizeof(g));
@@ -312,14 +326,14 @@ int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const voi
     g.plane_out = (size_t)T * 2 * m.Fp;
     g.kept = kept_of(m, const_cast<void*>(ctx));
     g.fblocks = feature_blocks(m);
-    r.e = run_mlp_gemm("mlp_dhidden", kMlpDglu, m.f32, vy, vo, g, stream);
+    r.e = run_mlp_gemm("mlp_dhidden", kMlpDglu, m.f32, m.hidden == 2, vy, vo, g, stream);
   }
   if (dx) r.rows("mlp_dx", vz, false, vi, false, T, C, 1, 2, F, nullptr, dx, w.part);
   if (dw_in) r.rows("mlp_dw_in", vx, true, vz, true, C, F, 2, 1, T, nullptr, dw_in, w.part);
-  const MlpView vh = view(ctx, F, 1, T, m.planes, m.Fp);
+  const MlpView vh = view(ctx, F, 1, T, m.hidden, m.Fp);
   if (dw_out) r.rows("mlp_dw_out", vh, true, vy, true, F, C, 1, 1, T, nullptr, dw_out, w.part);
   if (db_in)
-    r.colsum(dz, m.planes, 2 * (size_t)m.Fp, (size_t)T * 2 * m.Fp, 2, F, m.Fp, db_in, w.colsum);
+    r.colsum(dz, m.hidden, 2 * (size_t)m.Fp, (size_t)T * 2 * m.Fp, 2, F, m.Fp, db_in, w.colsum);
   if (db_out) r.colsum(dy, m.f32 ? 0 : 1, C, 0, 1, C, C, db_out, w.colsum);
   return status(r.e);
 }

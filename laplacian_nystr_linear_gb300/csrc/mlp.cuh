@@ -73,6 +73,8 @@ struct MlpGemmArgs {
   int nparts;            // column parts that tiles run over
   int mt, nt;            // tiles of M and of a part's N
   int kst, kparts;       // K steps of a part, parts that K runs over
+  int kplanes;           // bf16 calls: 2 where an operand is in two parts (K runs over both)
+  int two_a, two_b;      // ... which
   int splits, items;
   int amn, bmn;          // operands stored [k][m], [k][n]
   int act;
@@ -86,8 +88,9 @@ struct MlpGemmArgs {
   int* err;
 };
 
-// the product of two views: a's rows are M (or its inner, with amn), K the other
-cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, const MlpView& a, const MlpView& b,
+// the product of two views: a's rows are M (or its inner, with amn), K the other; two: h,
+// or dg and du, of a bf16 call into two planes
+cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, bool two, const MlpView& a, const MlpView& b,
                          MlpGemmArgs& g, cudaStream_t st);
 // K ranges of a product with `tiles` tiles of `ksteps` steps, M x N of fp32 a range
 int mlp_splits(long long tiles, int ksteps, double mn, bool f32);
@@ -143,14 +146,17 @@ struct MlpFewArgs {
   const void* bias;     // [parts][N] or null
   void* out;            // [T][N]
   float* part;          // [blocks of columns + blocks of the grid][T][columns of a block]
-  int T, K, N, parts, act;
+  int T, K, N, parts, act;   // T: rows of x
+  int rows;             // of the result: T, or T / 2 where x is hi rows, then lo rows
+  int two;              // out is rows, then what their rounding left (bf16)
   bool second;          // x comes from the kernel before, which is one of these
   // filled by the launcher
   int nb, ks, grid;     // column blocks of a part, K steps, blocks of the grid
   int* err;
 };
-// whether a call of T rows goes this way
+// whether a call of T rows goes this way, and whether its h is in two parts
 bool mlp_few_ok(int T, int C, int F, bool f32);
+bool mlp_few_two(int T, bool f32);
 size_t mlp_few_bytes(int T, int N, int parts);
 cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st);
 

@@ -8,7 +8,10 @@ out, and of nine products of parts three, below 3 * 2^-24; a0 b0 is summed over 
 (2^-7 with both orders), in K / 16 * 5 steps: (8 + K / 128 / 4 + 2^-7 K / 3.2) 2^-22 + 5 * 2^-24.
 Activation.  An activation's and its slope's own error is taken as 2^-19 (bf16 calls: approximate
 exponential and reciprocal, 2^-22 each, times small factors) or 2^-21 (fp32) of 1 + |g|; their slopes are
-below 1.2.  Kept for the backward: p, q rounded to f16 (bf16 calls), 2^-12 of the value and 2^-38 of the
+below 1.2.
+Between the products bf16 calls round h and the gradient of (g | u), half a step; with two parts (few rows
+without a gradient, or T C F <= 2^28) half a step of what the first left, 2^-16 in all, and their products
+run over both parts, one after the other: twice the steps.  Kept for the backward: p, q rounded to f16 (bf16 calls), 2^-12 of the value and 2^-38 of the
 largest of 32.
 """
 import math
@@ -47,10 +50,23 @@ def act(g, kind):
     return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
 
 
-def reference(x, w_in, b_in, w_out, b_out, kind, dy=None):
+def mm2(a, b, two):
+    """mm of bf16 values that are kept in one part or two (rounded here), summed over both"""
+    def kept(o):
+        return Off(o.v, o.off + (2.0 ** -16 if two else 2.0 ** -8) * (o.v.abs() + o.off))
+    a, b = (kept(a[0]), b) if isinstance(a, tuple) else (a, kept(b[0]))
+    s = steps(a.v.shape[-1], False) * (2 if two else 1)
+    A, B = a.v.abs() + a.off, b.v.abs() + b.off
+    return Off(a.v @ b.v, a.off @ B + A @ b.off + s * (A @ B) + 1e-37)
+
+
+def reference(x, w_in, b_in, w_out, b_out, kind, dy=None, two=None):
     """{name: Off} of y and, with dy, of the gradients; x, dy [T, C]"""
     f32, dt = x.dtype == torch.float32, x.dtype
     Fh = w_out.shape[0]
+    if two is None:
+        two = x.shape[0] * w_in.shape[0] * Fh <= 2 ** 28
+    part = lambda o: (o,)  # noqa: E731
     X, W, V = Off.of(x), Off.of(w_in), Off.of(w_out)
     z = mm(X, W, f32)
     if b_in is not None:
@@ -60,8 +76,7 @@ def reference(x, w_in, b_in, w_out, b_out, kind, dy=None):
     own = (2.0 ** -21 if f32 else 2.0 ** -19) * (1 + g.v.abs())
     p, s = Off(p, 1.2 * g.off + own), Off(s, 1.2 * g.off + own)
     h = p * u
-    h = h if f32 else h.stored(dt)
-    y = mm(h, V, f32)
+    y = mm(h, V, True) if f32 else mm2(part(h), V, two)
     out = {"y": y if b_out is None else y + Off.of(b_out)}
     if dy is None:
         return out
@@ -75,10 +90,12 @@ def reference(x, w_in, b_in, w_out, b_out, kind, dy=None):
     dh = mm(D, tr(V), f32)
     dg, du = dh * q, dh * p
     dz = Off(torch.cat([dg.v, du.v], 1), torch.cat([dg.off, du.off], 1))
-    dz = dz if f32 else dz.stored(dt)
-    out["x"] = mm(dz, tr(W), f32)
-    out["w_in"] = mm(tr(X), dz, f32)
-    out["w_out"] = mm(tr(h), D, f32)
+    if f32:
+        out["x"], out["w_in"], out["w_out"] = mm(dz, tr(W), True), mm(tr(X), dz, True), mm(tr(h), D, True)
+    else:
+        out["x"], out["w_in"] = mm2(part(dz), tr(W), two), mm2(tr(X), part(dz), two)
+        out["w_out"] = mm2(part(tr(h)), D, two)
+        dz = Off(dz.v, dz.off + (2.0 ** -16 if two else 2.0 ** -8) * (dz.v.abs() + dz.off))
     rows = x.shape[0] + 64
     out["b_in"], out["b_out"] = dz.sum(0, rows), D.sum(0, rows)
     return out
