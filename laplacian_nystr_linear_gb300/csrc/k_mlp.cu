@@ -26,7 +26,8 @@
 // and by the epilogue's threads, in registers, beyond; the others together are 2^-8 of
 // the sum.  A step's planes are copied once and read from shared memory by all six.
 //
-// 640 threads a CTA (384 for dglu): warp 0 copies (one thread, a ring of NST slots), warp 1 issues
+// 640 threads a CTA (384 for dglu): warps 0 and 2 copy (one thread each, A and B, into a ring
+// of NST slots), warp 1 issues
 // (leader) and holds the tensor memory, warps 4 to 19 read the accumulators, a row a
 // thread, a quarter of the columns each, while the next tile accumulates (with eight warps
 // the chain of a thread's instructions took longer than the products: XXX).  Every wait is
@@ -407,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
   __shared__ __align__(8) uint64_t accf[2];     // an accumulator's products done
   __shared__ __align__(8) uint64_t acce[2];     // leader: read out by both CTAs' warps
   __shared__ uint32_t tmem_s;
-  __shared__ int issued_s, consumed_s, bad_s;
+  __shared__ int issued_s[2], consumed_s, bad_s;
   __shared__ float bias_s[2][BN];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = rank_of_cta();
@@ -423,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
   }
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(tc::smem_u32(&full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&full[i]), 2);
       tc::mbar_init(tc::smem_u32(&empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -431,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
       tc::mbar_init(tc::smem_u32(&acce[i]), 2 * EPW);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    issued_s = 0;
+    issued_s[0] = issued_s[1] = 0;
     consumed_s = 0;
     bad_s = 0;
   }
@@ -441,41 +442,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
   tc::fence_after();
   const uint32_t tmem = tmem_s;
 
-  if (warp == 0) {
-    // ---------------- copies ----------------
+  if (warp == 0 || warp == 2) {
+    // ---------------- copies: of A by warp 0, of B by warp 2 ----------------
     if (wtc::elect_one()) {
+      const bool is_a = warp == 0;
+      const CUtensorMap* map = is_a ? &mp.a : &mp.b;
+      const bool mn = is_a ? a.amn : a.bmn, two = is_a ? a.two_a : a.two_b;
+      const int boxes = mn ? (is_a ? BM : BNC) / 64 : 1;
+      const uint32_t bytes = 2 * (is_a ? G::A_BYTES : G::B_BYTES), sm0 = sm + (is_a ? 0 : G::A_BYTES);
+      const uint32_t empty0 = tc::smem_u32(&empty[0]), full0 = tc::smem_u32(&full[0]);
+      const uint32_t lead0 = at_leader(full0);
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool bad = false;
       for (int it = pair; it < a.items && !bad; it += pairs) {
         const Item r = decode<TN>(a, it);
-        const int am = r.m0 + (int)rank * BM;
-        const int bn = EPI == kMlpGlu ? r.n0 : r.n0 + (int)rank * BNC;
+        // first row of this CTA, and the operand's part where K does not run over parts
+        const int row = is_a ? r.m0 + (int)rank * BM : (EPI == kMlpGlu ? r.n0 : r.n0 + (int)rank * BNC);
+        const int part = is_a ? 0 : (EPI == kMlpGlu ? (int)rank : r.part);
+        // K step: plane, part of K, k (divisions once a tile: one a step took a sixth of the
+        // whole product of dx)
+        int pl = 0, kp = 0, kt = r.ks0;
+        if (a.kplanes > 1 && kt >= a.kst * a.kparts) {
+          pl = 1;
+          kt -= a.kst * a.kparts;
+        }
+        if (a.kparts > 1 && kt >= a.kst) {
+          kp = 1;
+          kt -= a.kst;
+        }
         for (int ks = r.ks0; ks < r.ks1 && !bad; ++ks) {
-          const int pl = a.kplanes > 1 && ks >= a.kst * a.kparts ? 1 : 0, kr = ks - pl * a.kst * a.kparts;
-          const int kp = a.kparts > 1 && kr >= a.kst ? 1 : 0, k0 = (kr - kp * a.kst) * BK;
-          const int bp = EPI == kMlpGlu ? (int)rank : (a.kparts > 1 ? kp : r.part);
+          const int k0 = kt * BK, pp = a.kparts > 1 ? kp : part;
 #pragma unroll 1
           for (int p = 0; p < PLANES; ++p) {
-            const int pa = F32 ? p : (a.two_a ? pl : 0), pb = F32 ? p : (a.two_b ? pl : 0);
-            if (!wtc::wait_or_flag(a.err, tc::smem_u32(&empty[st]), ph ^ 1u)) { bad = true; break; }
-            const uint32_t bar = at_leader(tc::smem_u32(&full[st]));
-            if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&full[st]), 2 * G::SLOT);
-            const uint32_t sa = sm + st * G::SLOT, sb = sa + G::A_BYTES;
-            if (a.amn) {
+            const int plane = F32 ? p : (two ? pl : 0);
+            if (!wtc::wait_or_flag(a.err, empty0 + 8 * st, ph ^ 1u)) { bad = true; break; }
+            if (rank == 0) tc::mbar_expect_tx(full0 + 8 * st, bytes);
+            const uint32_t dst = sm0 + st * G::SLOT, bar = lead0 + 8 * st;
+            if (mn) {
 #pragma unroll
-              for (int i = 0; i < BM / 64; ++i) tma4(sa + i * BLK64, &mp.a, am + 64 * i, kp, k0, pa, bar);
+              for (int i = 0; i < BM / 64; ++i)
+                if (i < boxes) tma4(dst + i * BLK64, map, row + 64 * i, pp, k0, plane, bar);
             } else {
-              tma4(sa, &mp.a, k0, kp, am, pa, bar);
-            }
-            if (a.bmn) {
-#pragma unroll
-              for (int i = 0; i < BNC / 64; ++i) tma4(sb + i * BLK64, &mp.b, bn + 64 * i, bp, k0, pb, bar);
-            } else {
-              tma4(sb, &mp.b, k0, bp, bn, pb, bar);
+              tma4(dst, map, k0, pp, row, plane, bar);
             }
             ++issued;
             if (++st == NST) { st = 0; ph ^= 1u; }
+          }
+          if (++kt == a.kst) {
+            kt = 0;
+            if (++kp == a.kparts) {
+              kp = 0;
+              ++pl;
+            }
           }
         }
       }
@@ -483,9 +502,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
       // before this CTA ends
       for (int i = 0; i < NST && i < issued && !bad; ++i) {
         const int k = issued - 1 - i;
-        bad = !wtc::wait_or_flag(a.err, tc::smem_u32(&empty[k % NST]), (uint32_t)(k / NST) & 1u);
+        bad = !wtc::wait_or_flag(a.err, empty0 + 8 * (k % NST), (uint32_t)(k / NST) & 1u);
       }
-      issued_s = issued;
+      issued_s[is_a ? 0 : 1] = issued;
       if (bad) atomicOr(&bad_s, 1);
     }
   } else if (warp == 1) {
@@ -568,15 +587,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     // longer than its products: XXX)
     constexpr int DEEP = TWO ? 2 : 4;   // (two planes take the registers of two)
     Kept kept2[DEEP];
-    auto ahead = [&](const Item& r, int col, Kept& k) {
-      const int m = r.m0 + (int)rank * BM + 32 * q, n = r.n0 + col;
+    auto ahead = [&](int tile_m, int n, Kept& k) {
+      const int m = tile_m + (int)rank * BM + 32 * q;
       if (m < a.M && n < a.N) fetch(a.kept, (size_t)(m / 32) * a.fblocks + n / 16, k);
     };
     if constexpr (!F32 && EPI == kMlpDglu)
       if (pair < a.items) {
         const Item r = decode<TN>(a, pair);
 #pragma unroll
-        for (int i = 0; i < DEEP; ++i) ahead(r, col0 + 16 * i, kept2[i]);
+        for (int i = 0; i < DEEP; ++i) ahead(r.m0, r.n0 + col0 + 16 * i, kept2[i]);
       }
     const bool biased = (EPI == kMlpRows || EPI == kMlpGlu) && a.bias != nullptr;
     for (int it = pair; it < a.items && (biased || !bad); it += pairs, ++li) {
@@ -684,7 +703,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
           }
         } else if constexpr (EPI == kMlpDglu) {
 const bool more = it + pairs < a.items;
-          const Item after = more ? decode<TN>(a, it + pairs) : r;
+          int after_m = 0, after_n = 0;
+          if (more) {
+            const Item after = decode<TN>(a, it + pairs);
+            after_m = after.m0;
+            after_n = after.n0 + col0;
+          }
 #pragma unroll 1
           for (int c0 = 0; c0 < COLS; c0 += 16 * DEEP) {
             uint32_t dg[16], du[16], rg[TWO ? 16 : 1], ru[TWO ? 16 : 1];
@@ -699,7 +723,8 @@ const bool more = it + pairs < a.items;
               times_kept<TWO>(kept2[j], 1, x, dg + o8, rg + (TWO ? o8 : 0));    // dg = dh q, du = dh p
               times_kept<TWO>(kept2[j], 0, x, du + o8, ru + (TWO ? o8 : 0));
               const bool here = c + 16 * DEEP < COLS;
-              if (here || more) ahead(here ? r : after, col0 + (here ? c + 16 * DEEP : 16 * j), kept2[j]);
+              if (here || more)
+                ahead(here ? r.m0 : after_m, here ? r.n0 + col0 + c + 16 * DEEP : after_n + 16 * j, kept2[j]);
               const int n = r.n0 + col0 + c - 16;
               if ((j & 1) && some && n < a.N) {
                 __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
@@ -760,7 +785,7 @@ const bool more = it + pairs < a.items;
   // were issued and not consumed.
   __syncthreads();
   if (bad_s && rank == 0 && tid == 32) {
-    const int c = consumed_s, n = issued_s;
+    const int c = consumed_s, n = max(issued_s[0], issued_s[1]);
     if (c > 0) wtc::wait_or_flag(a.err, tc::smem_u32(&empty[(c - 1) % NST]), (uint32_t)((c - 1) / NST) & 1u);
     for (int k = c; k < n; ++k) wtc::wait_or_flag(a.err, tc::smem_u32(&full[k % NST]), (uint32_t)(k / NST) & 1u);
   }
