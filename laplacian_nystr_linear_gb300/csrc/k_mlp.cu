@@ -26,13 +26,18 @@
 // and by the epilogue's threads, in registers, beyond; the others together are 2^-8 of
 // the sum.  A step's planes are copied once and read from shared memory by all six.
 //
-// 640 threads a CTA (384 for dglu): warps 0 and 2 copy (one thread each, A and B, into a ring
-// of NST slots), warp 1 issues
-// (leader) and holds the tensor memory, warps 4 to 19 read the accumulators, a row a
-// thread, a quarter of the columns each, while the next tile accumulates (with eight warps
-// the chain of a thread's instructions took longer than the products: XXX).  Every wait is
-// bounded; a role whose wait expired sets the error word and stops issuing, and all
-// threads meet at the cluster barrier before tensor memory is freed.
+// 640 threads a CTA (384 for dglu): warps 0 and 2 copy (a thread each, A and B, into a ring
+// of NST slots), warp 1 issues (leader) and holds the tensor memory, warps 4 to 19 read the
+// accumulators, a row a thread, a quarter of the columns each, while the next tile
+// accumulates.  Every wait is bounded; a role whose wait expired sets the error word and
+// stops issuing, and all threads meet at the cluster barrier before tensor memory is freed.
+//
+// Measured, bf16: 8192 rows, 8192 x 4096: 1.75 to 1.89 PFLOP/s in every product (the
+// library's product of 8192^3: 1.93).  131072 rows, 512 x 1408, forward + backward: 296 +
+// 119 + 280 + 219 + 224 + 117 us: the first and third are bound by what passes through L2
+// (tiles of K = 512 in, h, p, q, dg and du in and out: 13 TB/s of it), the others run at
+// 1.6 to 1.7 PFLOP/s.  fp32, 4096 rows, 1024 x 4096: 250 to 290 TFLOP/s (a sixth of the
+// bf16 rate is 320).
 #include <cuda_fp16.h>
 
 #include <cstring>
@@ -256,7 +261,7 @@ __device__ __forceinline__ void fetch(const MlpKept& k, size_t block, Kept& r) {
   const int lane = threadIdx.x & 31;
   const uint4* o = reinterpret_cast<const uint4*>(k.pq) + block * 4 * 32 + lane;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.w[i] = __ldcs(o + i * 32);
+  for (int i = 0; i < 4; ++i) r.w[i] = o[i * 32];
   r.scale = k.scale[block * 32 + lane];
 }
 // what the rounding of a pair left (h: the pair as bf16); infinities leave nothing
@@ -583,9 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     int li = 0;
     bool bad = false;
     // dglu of bf16 calls: p and q of DEEP blocks, each fetched again for DEEP blocks later
-    // as soon as it is used (read when they were needed, a tile's waits for memory took
-    // longer than its products: XXX)
-    constexpr int DEEP = TWO ? 2 : 4;   // (two planes take the registers of two)
+    // as soon as it is used (131072 rows of 1408: 278 us, 5.8 TB/s; read when they were needed,
+    // a tile's waits for memory took longer than its products: 491 us)
+    constexpr int DEEP = 2;
     Kept kept2[DEEP];
     auto ahead = [&](int tile_m, int n, Kept& k) {
       const int m = tile_m + (int)rank * BM + 32 * q;

@@ -10,7 +10,10 @@
 //
 // Bound by memory: queries and keys are read and written once.  A thread keeps its
 // pairs' cosines and sines in registers over the heads of its token, so they cost a
-// few instructions a head; loads of four heads are in flight at once.
+// few instructions a head; loads of four heads are in flight at once.  2 x 8192 tokens,
+// 20 heads of 128: 32 us (bf16, 5.3 TB/s; interleaved 30), 55 us (fp32, 6.1 TB/s); pieces
+// of 16 bytes of bf16 instead of 8, converted one by one, took 45 and 51 us.  Single
+// tokens: the launch.
 #include "common.cuh"
 #include "internal.h"
 #include "layer.cuh"
@@ -176,7 +179,8 @@ cudaError_t go(RotaryArgs& a, cudaStream_t st) {
   const long long items = (long long)a.B * a.N * a.units;
   const int heads = a.Hq + a.Hkv;
   // all heads by one thread (its sines once), or fewer where that leaves SMs without
-  // threads: half of 152 x 2048
+  // threads: half of 152 x 2048 (twice or four times as many: 31 to 33 us for the 32 above,
+  // 16 for 14 at 4096 tokens)
   const long long want = (152LL * 1024 + items - 1) / items;
   int groups = (int)(want < heads ? want : heads);
   a.heads = (heads + groups - 1) / groups;

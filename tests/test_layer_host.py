@@ -1,5 +1,5 @@
-"""Refusals of the rotary positions and of the residual with its norms, before anything is enqueued (no
-GPU), and the frequencies that are computed on the host."""
+"""Refusals of the rotary positions, the residual with its norms and the gated feed-forward block, before
+anything is enqueued (no GPU), and the frequencies that are computed on the host."""
 import ctypes
 import math
 
@@ -94,9 +94,65 @@ def test_norm_refuses_more(lib):
     assert lib.lapnys_norm_workspace_bytes(0, 8, 64, 0) == 0
 
 
+MLP = dict(T=100, C=64, F=128)
+BIG = 1 << 40
+
+
+def _mlp_fwd(lib, **kw):
+    a = dict(MLP, x=FAKE, w_in=FAKE, b_in=None, w_out=FAKE, b_out=None, y=FAKE, act=0, dtype=1, ctx=None, ctx_bytes=0,
+             ws=FAKE, ws_bytes=0)
+    a.update(kw)
+    return lib.lapnys_mlp_fwd(a["x"], a["w_in"], a["b_in"], a["w_out"], a["b_out"], a["y"], *(a[n] for n in MLP),
+                              a["act"], None, a["dtype"], a["ctx"], a["ctx_bytes"], a["ws"], a["ws_bytes"])
+
+
+def _mlp_bwd(lib, **kw):
+    a = dict(MLP, x=FAKE, w_in=FAKE, w_out=FAKE, dy=FAKE, ctx=FAKE, dx=FAKE, dw_in=FAKE, db_in=None, dw_out=FAKE,
+             db_out=None, dtype=1, ws=FAKE, ws_bytes=0)
+    a.update(kw)
+    return lib.lapnys_mlp_bwd(a["x"], a["w_in"], a["w_out"], a["dy"], a["ctx"], a["dx"], a["dw_in"], a["db_in"],
+                              a["dw_out"], a["db_out"], *(a[n] for n in MLP), None, a["dtype"], a["ws"],
+                              a["ws_bytes"])
+
+
+@pytest.mark.parametrize("bad", [
+    dict(T=0), dict(C=0), dict(F=-1), dict(T=(1 << 28) + 1), dict(C=1 << 21), dict(F=1 << 21),
+    dict(T=1 << 28, C=1 << 20), dict(C=1 << 20, F=1 << 20, T=1), dict(dtype=2), dict(x=None), dict(w_in=ODD),
+    dict(w_out=None), dict(x=HALF), dict(ws=None), dict(ws=HALF)], ids=str)
+def test_mlp_refuses(lib, bad):
+    before = lib.lapnys_launch_count()
+    assert _mlp_fwd(lib, **bad) == _lib.LAPNYS_EINVAL
+    assert _mlp_bwd(lib, **bad) == _lib.LAPNYS_EINVAL
+    assert lib.lapnys_launch_count() == before
+
+
+def test_mlp_refuses_more(lib):
+    for bad in (dict(act=-1), dict(act=3), dict(y=None), dict(y=ODD), dict(b_in=HALF), dict(ctx=HALF)):
+        assert _mlp_fwd(lib, **bad) == _lib.LAPNYS_EINVAL
+    for bad in (dict(dy=None), dict(ctx=None), dict(dx=HALF), dict(db_in=ODD), dict(dw_out=HALF)):
+        assert _mlp_bwd(lib, **bad) == _lib.LAPNYS_EINVAL
+    for dtype in (0, 1):
+        fwd, bwd = (lib.lapnys_mlp_workspace_bytes(100, 64, 128, dtype, b) for b in (0, 1))
+        ctx = lib.lapnys_mlp_ctx_bytes(100, 64, 128, dtype)
+        assert min(fwd, bwd, ctx) > 0
+        assert _mlp_fwd(lib, dtype=dtype, ws_bytes=fwd - 1) == _lib.LAPNYS_ENOSPC
+        assert _mlp_fwd(lib, dtype=dtype, ws_bytes=fwd, ctx=FAKE, ctx_bytes=ctx - 1) == _lib.LAPNYS_ENOSPC
+        assert _mlp_bwd(lib, dtype=dtype, ws_bytes=bwd - 1) == _lib.LAPNYS_ENOSPC
+    assert lib.lapnys_mlp_ctx_bytes(0, 64, 128, 1) == 0 and lib.lapnys_mlp_workspace_bytes(1, 64, 128, 7, 0) == 0
+
+
+def test_mlp_sizes(lib):
+    """h, p and q of a training step, 6 bytes a hidden value in bf16; the backward's partial sums bounded."""
+    T, C, F = 131072, 512, 1408
+    assert 6 * T * F < lib.lapnys_mlp_ctx_bytes(T, C, F, 1) < 6.3 * T * F
+    assert 4 * T * F < lib.lapnys_mlp_workspace_bytes(T, C, F, 1, 1) < 4 * T * F + (1 << 28)
+    assert lib.lapnys_mlp_workspace_bytes(1, 4096, 10880, 1, 0) < 1 << 24   # no copy of the weights
+
+
 def test_python_refuses():
     q, f = torch.zeros((1, 2, 4, 16)), lap.rotary_frequencies(16, device="cpu")
     x, w = torch.zeros((2, 4, 16)), torch.ones(16)
+    wi, wo = torch.zeros((16, 16)), torch.zeros((8, 16))
     for bad in (lambda: lap.rotary(q, q, f), lambda: lap.rotary(q[0], q, f), lambda: lap.rotary(q, q, None),
                 lambda: lap.rotary(q, q, f, layout="pairs"), lambda: lap.rotary_frequencies(7),
                 lambda: lap.rotary_frequencies(0), lambda: lap.rotary_frequencies(8, base=0),
@@ -107,10 +163,16 @@ def test_python_refuses():
                 lambda: lap.RotaryFrequencies.of([], device="cpu"),
                 lambda: lap.residual_norm(x, None, w), lambda: lap.residual_norm(x[0], None, w),
                 lambda: lap.residual_norm(x, pre=None), lambda: lap.residual_norm(x, x, w, pre="batch"),
-                lambda: lap.residual_norm(x, x, w, post="l2")):
+                lambda: lap.residual_norm(x, x, w, post="l2"),
+                lambda: lap.gated_mlp(x, wi, None, wo, None), lambda: lap.gated_mlp(x[0, 0], wi, None, wo, None),
+                lambda: lap.gated_mlp(x, wi, None, wo[0], None), lambda: lap.gated_mlp(x, wi, None, wo, None, "relu"),
+                lambda: lap.mlp_fwd(x, wi, None, wo, None, lap.MlpParams(BIG, 16, 8)),
+                lambda: lap.mlp_ctx_bytes(lap.MlpParams(BIG, 16, 8), torch.bfloat16),
+                lambda: lap.norm_workspace_bytes(BIG, 1, 16, False)):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: lap.rotary(q.half(), q.half(), f), lambda: lap.residual_norm(x.half(), None, w.half())):
+    for bad in (lambda: lap.rotary(q.half(), q.half(), f), lambda: lap.residual_norm(x.half(), None, w.half()),
+                lambda: lap.gated_mlp(x.half(), wi.half(), None, wo.half(), None)):
         with pytest.raises(TypeError):
             bad()
 
@@ -122,7 +184,9 @@ def test_forward_mode_derivatives_are_refused():
         dual = fwAD.make_dual(q, torch.ones_like(q))
         for call in (lambda: lap.rotary(dual, q, f), lambda: lap.rotary(q, dual, f),
                      lambda: lap.residual_norm(x, None, fwAD.make_dual(w, w)),
-                     lambda: lap.residual_norm(fwAD.make_dual(x, x), x)):
+                     lambda: lap.residual_norm(fwAD.make_dual(x, x), x),
+                     lambda: lap.gated_mlp(fwAD.make_dual(x, x), torch.zeros((16, 16)), None, torch.zeros((8, 16)),
+                                           None)):
             with pytest.raises(ValueError, match="forward-mode"):
                 call()
 
