@@ -366,8 +366,8 @@ int lapnys_cache_attention(const void* q, const void* k_cache, const void* v_cac
  *    [B][N]); not both.
  *  - inverse != 0 turns back (by the same factor): the gradient.
  *  - q_out, k_out: like q, k; each may be its input itself, and overlaps nothing
- *    else.  Any alignment of the elements' own (16 bytes, with d, rot and, in the
- *    half layout, rot / 2 multiples of 16 bytes of elements, is faster). */
+ *    else.  Any alignment of the elements' own (that of four, with d, rot and, in
+ *    the half layout, rot / 2 multiples of four, is faster). */
 #define LAPNYS_HALF 0
 #define LAPNYS_INTERLEAVED 1
 int lapnys_rotary(const void* q, const void* k, void* q_out, void* k_out, const uint64_t* turns,

@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(RT) k_rotary(RotaryArgs a) {
   }
   float c[P], s[P];
   if (turn) {
-    const int32_t p = a.positions ? a.positions[tok] : (a.start ? a.start[b] : 0) + n;
-    const uint64_t at_p = (uint64_t)(int64_t)p;
+    const int64_t p = a.positions ? a.positions[tok] : (int64_t)(a.start ? a.start[b] : 0) + n;
+    const uint64_t at_p = (uint64_t)p;
     const int i0 = HALF ? unit * V : unit * P;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -183,10 +183,11 @@ cudaError_t go(RotaryArgs& a, cudaStream_t st) {
   // 16 for 14 at 4096 tokens)
   const long long want = (152LL * 1024 + items - 1) / items;
   int groups = (int)(want < heads ? want : heads);
+  groups = groups < 65535 ? groups : 65535;        // the grid's y
   a.heads = (heads + groups - 1) / groups;
   groups = (heads + a.heads - 1) / a.heads;
   const long long blocks = (items + RT - 1) / RT;
-  if (blocks >= 1LL << 31 || groups > 65535) return cudaErrorInvalidValue;
+  if (blocks >= 1LL << 31) return cudaErrorInvalidValue;
   return launch("rotary", k_rotary<T, HALF, V>, dim3((unsigned)blocks, groups), dim3(RT), 0, st, a);
 }
 
@@ -201,7 +202,7 @@ cudaError_t pick(RotaryArgs& a, bool half, bool whole, cudaStream_t st) {
 cudaError_t run_rotary(RotaryArgs& a, bool half, bool bf16, cudaStream_t st) {
   const int v = 4;
   auto al = [&](const void* p) { return ((uintptr_t)p & (bf16 ? 7 : 15)) == 0; };
-  // 16-byte pieces where every piece of every row starts on 16 bytes
+  // pieces of four elements where each of every row starts on its size
   const bool whole = al(a.q) && al(a.k) && al(a.q_out) && al(a.k_out) && a.d % v == 0 &&
                      a.rot % v == 0 && (!half || a.rot / 2 % v == 0);
   return bf16 ? pick<__nv_bfloat16, 4>(a, half, whole, st) : pick<float, 4>(a, half, whole, st);

@@ -1,5 +1,9 @@
 """What stands around the attentions in a layer: rotary positions, the residual with its norms, and the
-gated feed-forward block.  Marshalling only: every step runs in liblapnys kernels."""
+gated feed-forward block.  Marshalling only: every step runs in liblapnys kernels.
+
+A step that is captured into a CUDA graph takes leaves that no eager autograd graph still holds, as
+window_attention's does (their gradients would be added up on that graph's stream).
+"""
 from __future__ import annotations
 
 import functools
@@ -67,7 +71,7 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, context=None
                 fastest stays;
       "parts"   a pair that makes `high` turns or more over `context` positions (the length trained on)
                 stays, one of `low` turns or fewer is divided by factor, others in between linearly;
-                turned features are multiplied by 1 + 0.1 ln(factor).
+                turned features are multiplied by 1 + 0.1 ln(factor) (factors above 1).
     """
     rot = int(rot)
     if rot < 2 or rot % 2:

@@ -84,7 +84,7 @@ def _inputs(B, N, C, dtype, seed, given):
 ALL = ("u", "weight", "bias", "post_weight", "post_bias", "gate", "scale")
 SHAPES = [(1, 1, 1), (2, 3, 8), (1, 40, 16), (3, 37, 100), (2, 65, 256), (2, 33, 264), (1, 50, 512),
           (4, 19, 520), (2, 21, 1000), (1, 9, 1032), (1, 3, 2048), (2, 5, 4104), (1, 2, 8192), (1, 3, 16384),
-          (70, 2, 64), (400, 1, 24)]
+          (70, 2, 64), (400, 1, 24), (1, 3, 4101), (2, 2, 9001)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])

@@ -107,6 +107,28 @@ def test_in_place_back_and_elsewhere(dtype, layout, d, rot):
     assert ((back.double() - q.double()).abs() <= 2 * u * size).all()
 
 
+def test_a_start_whose_last_positions_pass_32_bits():
+    q = torch.randn((1, 2, 6, 32), device="cuda")
+    f = lap.rotary_frequencies(32)
+    got, _ = lap.rotary(q, None, f, start=torch.tensor([2 ** 31 - 3], dtype=torch.int32, device="cuda"))
+    turns = [t % 2 ** 64 for t in f.turns.tolist()]
+    phase = torch.tensor([[((2 ** 31 - 3 + n) * t % 2 ** 64) / 2.0 ** 64 for t in turns] for n in range(6)],
+                         dtype=torch.float64, device="cuda") * (2 * math.pi)
+    z = torch.complex(q.double()[..., :16], q.double()[..., 16:]) * torch.polar(torch.ones_like(phase), phase)
+    off = 10 * 2.0 ** -24 * (q[..., :16].abs() + q[..., 16:].abs()).double()
+    assert ((got[..., :16].double() - z.real).abs() <= off).all()
+    assert ((got[..., 16:].double() - z.imag).abs() <= off).all()
+
+
+def test_more_heads_than_a_grid_has_rows():
+    q = torch.randn((1, 70000, 1, 8), device="cuda")
+    f = lap.rotary_frequencies(8)
+    start = torch.tensor([5], dtype=torch.int32, device="cuda")
+    got, _ = lap.rotary(q, None, f, start=start)
+    want, _ = lap.rotary(q.view(10, 7000, 1, 8), None, f, start=start.expand(10).contiguous())
+    assert torch.equal(got.view(10, 7000, 1, 8), want)
+
+
 def test_one_gradient_alone_and_none():
     q, k = (torch.randn((1, 2, 6, 16), device="cuda", requires_grad=True) for _ in range(2))
     f = lap.rotary_frequencies(16)
