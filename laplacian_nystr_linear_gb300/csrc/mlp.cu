@@ -18,6 +18,7 @@ int up8(int x) { return (x + 7) & ~7; }
 struct Mlp {
   int T, C, F, Cp, Fp;
   bool f32;
+  bool few;     // few rows: k_mlp_few.cu
   int planes;   // of packed operands
   int hidden;   // of h and of (dg | du)
   // operands that the products cannot read where they lie: fp32 (three planes), or rows
@@ -36,14 +37,15 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   m.T = T; m.C = C; m.F = F; m.Cp = up8(C); m.Fp = up8(F);
   m.f32 = dtype == LAPNYS_F32;
   m.planes = m.f32 ? 3 : 1;
+  m.few = mlp_few_ok(T, C, F, m.f32);
   // bf16 calls round h and the gradient of (g | u) between the products, which puts the
   // results' errors at 1.4 times their own rounding's, more where few values are summed
   // (1.7 at 4 rows of 64).  Calls of up to 2^28 multiply-adds a product, whose time is
   // launches and latency, keep them in two parts, and the products that read them run over
   // both (16 bits: what is left is the results' own rounding; a training step of 256 rows,
-  // 512 x 2048 features: kernels of 112 us for 104, 277 us a step either way).  Larger ones
-  // would take half as long again.
-  m.hidden = m.f32 ? 3 : (double)T * C * F <= 268435456.0 ? 2 : 1;
+  // 512 x 2048 features: kernels of 112 us for 104, 277 us a step either way).  So do few
+  // rows, whose time is the weights' bytes.  Others would take half as long again.
+  m.hidden = m.f32 ? 3 : m.few || (double)T * C * F <= 268435456.0 ? 2 : 1;
   m.pack_c = m.f32 || C % 8 != 0;
   m.pack_f = m.f32 || F % 8 != 0;
   return LAPNYS_OK;
@@ -51,7 +53,8 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
 
 int feature_blocks(const Mlp& m) { return (m.F + kMlpBlock - 1) / kMlpBlock; }
 
-// ctx: h, then p and q, then their rows' powers of two
+// ctx: h, then p and q, then their rows' powers of two; of few rows h, then p and q in fp32
+// rows
 struct Ctx {
   size_t h, pq, scale, total;
 };
@@ -63,6 +66,11 @@ Ctx ctx_of(const Mlp& m) {
   const size_t blocks = (size_t)((m.T + 31) / 32) * feature_blocks(m);
   c.h = 0;
   c.pq = h_bytes(m);
+  if (m.few) {
+    c.scale = 0;
+    c.total = c.pq + align256((size_t)2 * m.T * m.F * 4);
+    return c;
+  }
   c.scale = c.pq + align256(blocks * 2 * 32 * kMlpBlock * (m.f32 ? 4 : 2));
   c.total = c.scale + (m.f32 ? 0 : align256(blocks * 32 * 2));
   return c;
@@ -96,33 +104,35 @@ Ws ws_of(const Mlp& m, bool backward) {
   };
   const size_t two = 2 * (size_t)m.planes;
   room(w.x, m.pack_c ? two * m.T * m.Cp : 0);
-  room(w.w_in, m.pack_f ? two * m.C * 2 * m.Fp : 0);
-  room(w.w_out, m.pack_c ? two * m.F * m.Cp : 0);
-  size_t part;
+  room(w.w_in, m.pack_f && !m.few ? two * m.C * 2 * m.Fp : 0);
+  room(w.w_out, m.pack_c && !m.few ? two * m.F * m.Cp : 0);
+  size_t part = 0;
+  auto most = [&](size_t bytes) { part = bytes > part ? bytes : part; };
   if (!backward) {
     room(w.h, h_bytes(m));
-    part = split_of(m, m.T, m.C, 1, m.F, twice(m)).bytes;
+    if (m.few) {
+      most(mlp_few_bytes(m.T, m.planes, m.F, 2, m.f32));
+      most(mlp_few_bytes(m.T, m.hidden, m.C, 1, m.f32));
+    } else {
+      most(split_of(m, m.T, m.C, 1, m.F, twice(m)).bytes);
+    }
   } else {
     room(w.dy, m.pack_c ? two * m.T * m.Cp : 0);
     room(w.dz, 2 * (size_t)m.hidden * m.T * 2 * m.Fp);
-    part = split_of(m, m.T, m.C, 1, m.F, 2 * twice(m)).bytes;
-    const size_t wi = split_of(m, m.C, m.F, 2, m.T, twice(m)).bytes;
-    const size_t wo = split_of(m, m.F, m.C, 1, m.T, twice(m)).bytes;
-    part = part > wi ? part : wi;
-    part = part > wo ? part : wo;
+    if (m.few) {
+      most(mlp_few_bytes(m.T, m.planes, m.F, 1, m.f32));
+      most(mlp_few_bytes(m.T, m.hidden, m.C, 1, m.f32));
+    } else {
+      most(split_of(m, m.T, m.C, 1, m.F, 2 * twice(m)).bytes);
+    }
+    most(split_of(m, m.C, m.F, 2, m.T, twice(m)).bytes);
+    most(split_of(m, m.F, m.C, 1, m.T, twice(m)).bytes);
     const size_t ci = (size_t)mlp_colsum_ranges(m.T, 2 * m.F) * 2 * m.F * 4;
     const size_t co = (size_t)mlp_colsum_ranges(m.T, m.C) * m.C * 4;
     room(w.colsum, ci > co ? ci : co);
   }
   room(w.part, part);
   w.total = o;
-  if (!backward && mlp_few_ok(m.T, m.C, m.F, m.f32)) {
-    // h and the partial sums of one product, then the other's; without a ctx that is all
-    const int rows = mlp_few_two(m.T, m.f32) ? 2 * m.T : m.T;
-    const size_t a = mlp_few_bytes(m.T, m.F, 2), b = mlp_few_bytes(rows, m.C, 1);
-    const size_t few = align256((size_t)rows * m.F * (m.f32 ? 4 : 2)) + (a > b ? a : b);
-    w.total = few > w.total ? few : w.total;
-  }
   return w;
 }
 
@@ -159,6 +169,20 @@ struct Run {
   }
   void packs() {
     if (e == cudaSuccess && pack.jobs > 0) e = run_mlp_pack(pack, !m.f32, st);
+  }
+  // x [T][kparts][K] (planes) times w, few rows
+  MlpFewArgs few(const MlpView& x, const void* w, bool kmajor, int N, int nparts, size_t part_at) const {
+    MlpFewArgs f;
+    memset(&f, 0, sizeof(f));
+    f.x = x.p; f.w = w;
+    f.ldx = x.row_stride; f.xpart = x.part_stride;
+    f.T = m.T; f.planes = x.planes; f.K = x.inner; f.kparts = x.parts; f.N = N; f.nparts = nparts;
+    f.kmajor = kmajor;
+    f.part = (float*)(ws + part_at);
+    return f;
+  }
+  void run(MlpFewArgs& f) {
+    if (e == cudaSuccess) e = run_mlp_few(f, m.f32, st);
   }
   // out[M][nparts][N] = sum over K, split where that is faster
   void rows(const char* name, const MlpView& a, bool amn, const MlpView& b, bool bmn, int M, int N,
@@ -252,27 +276,29 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
   const Ws w = ws_of(m, false);
   if (!ws || !aligned(ws, 16)) return LAPNYS_EINVAL;
   if (ws_bytes < w.total || (ctx && ctx_bytes < ctx_of(m).total)) return LAPNYS_ENOSPC;
-  if (!ctx && mlp_few_ok(T, C, F, m.f32)) {
-    MlpFewArgs f;
-    memset(&f, 0, sizeof(f));
-    f.x = x; f.w = w_in; f.bias = b_in; f.out = ws;
-    const bool two = mlp_few_two(T, m.f32);
-    const int rows = two ? 2 * T : T;       // of h
-    f.part = (float*)((uint8_t*)ws + align256((size_t)rows * F * (m.f32 ? 4 : 2)));
-    f.T = T; f.rows = T; f.K = C; f.N = F; f.parts = 2; f.act = act; f.two = two;
-    const cudaError_t e = run_mlp_few(f, m.f32, stream);
-    if (e != cudaSuccess) return status(e);
-    f.x = ws; f.w = w_out; f.bias = b_out; f.out = y;
-    f.T = rows; f.K = F; f.N = C; f.parts = 1; f.act = -1; f.two = 0;
-    f.second = true;
-    return status(run_mlp_few(f, m.f32, stream));
-  }
   Run r(m, ws, stream);
   const MlpView vx = r.operand(x, m.pack_c, w.x, T, 1, C);
+  void* h = ctx ? ctx : r.ws + w.h;
+  const MlpView vh = view(h, F, 1, T, m.hidden, m.Fp);
+  if (m.few) {
+    r.packs();
+    MlpFewArgs f = r.few(vx, w_in, false, F, 2, w.part);
+    f.mode = kFewGlu; f.act = act; f.out_planes = m.hidden;
+    f.bias = b_in; f.out = h; f.ldo = m.Fp;
+    if (ctx) {
+      f.p = (float*)((uint8_t*)ctx + ctx_of(m).pq);
+      f.q = f.p + (size_t)T * F;
+    }
+    r.run(f);
+    f = r.few(vh, w_out, false, C, 1, w.part);
+    f.mode = kFewRows; f.second = true;
+    f.bias = b_out; f.out = y; f.ldo = C;
+    r.run(f);
+    return status(r.e);
+  }
   const MlpView vi = r.operand(w_in, m.pack_f, w.w_in, C, 2, F);
   const MlpView vo = r.operand(w_out, m.pack_c, w.w_out, F, 1, C);
   r.packs();
-  void* h = ctx ? ctx : r.ws + w.h;
   if (r.e == cudaSuccess) {
     MlpGemmArgs g;
     memset(&g, 0, sizeof(g));
@@ -287,7 +313,6 @@ int lapnys_mlp_fwd(const void* x, const void* w_in, const void* b_in, const void
     g.fblocks = feature_blocks(m);
     r.e = run_mlp_gemm("mlp_in", kMlpGlu, m.f32, m.hidden == 2, vx, vi, g, stream);
   }
-  const MlpView vh = view(h, F, 1, T, m.hidden, m.Fp);
   r.rows("mlp_out", vh, false, vo, true, T, C, 1, 1, F, b_out, y, w.part);
   return status(r.e);
 }
@@ -311,13 +336,26 @@ int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const voi
   const bool hidden = dx || dw_in || db_in;     // the gradient of z is needed
   MlpView vx, vi, vo, vy;
   if (dw_in) vx = r.operand(x, m.pack_c, w.x, T, 1, C);
-  if (dx) vi = r.operand(w_in, m.pack_f, w.w_in, C, 2, F);
-  if (hidden) vo = r.operand(w_out, m.pack_c, w.w_out, F, 1, C);
+  if (dx && !m.few) vi = r.operand(w_in, m.pack_f, w.w_in, C, 2, F);
+  if (hidden && !m.few) vo = r.operand(w_out, m.pack_c, w.w_out, F, 1, C);
   if (hidden || dw_out) vy = r.operand(dy, m.pack_c, w.dy, T, 1, C);
   r.packs();
   __nv_bfloat16* dz = (__nv_bfloat16*)(r.ws + w.dz);
   const MlpView vz = view(dz, F, 2, T, m.hidden, m.Fp);
-  if (hidden && r.e == cudaSuccess) {
+  if (hidden && m.few) {
+    MlpFewArgs f = r.few(vy, w_out, true, F, 1, w.part);
+    f.mode = kFewDglu; f.out_planes = m.hidden;
+    f.out = dz; f.ldo = m.Fp;
+    f.p = (float*)((uint8_t*)const_cast<void*>(ctx) + ctx_of(m).pq);
+    f.q = f.p + (size_t)T * F;
+    r.run(f);
+    if (dx) {
+      f = r.few(vz, w_in, true, C, 1, w.part);
+      f.mode = kFewRows; f.second = true;
+      f.out = dx; f.ldo = C;
+      r.run(f);
+    }
+  } else if (hidden && r.e == cudaSuccess) {
     MlpGemmArgs g;
     memset(&g, 0, sizeof(g));
     g.M = T; g.N = F; g.nparts = 1; g.kparts = 1; g.splits = 1;
@@ -329,7 +367,7 @@ int lapnys_mlp_bwd(const void* x, const void* w_in, const void* w_out, const voi
     g.fblocks = feature_blocks(m);
     r.e = run_mlp_gemm("mlp_dhidden", kMlpDglu, m.f32, m.hidden == 2, vy, vo, g, stream);
   }
-  if (dx) r.rows("mlp_dx", vz, false, vi, false, T, C, 1, 2, F, nullptr, dx, w.part);
+  if (dx && !m.few) r.rows("mlp_dx", vz, false, vi, false, T, C, 1, 2, F, nullptr, dx, w.part);
   if (dw_in) r.rows("mlp_dw_in", vx, true, vz, true, C, F, 2, 1, T, nullptr, dw_in, w.part);
   const MlpView vh = view(ctx, F, 1, T, m.hidden, m.Fp);
   if (dw_out) r.rows("mlp_dw_out", vh, true, vy, true, F, C, 1, 1, T, nullptr, dw_out, w.part);

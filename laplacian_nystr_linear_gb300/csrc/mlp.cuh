@@ -137,27 +137,35 @@ struct MlpColsumArgs {
 int mlp_colsum_ranges(int rows, int cols);
 cudaError_t run_mlp_colsum(const MlpColsumArgs& a, bool bf16, cudaStream_t st);
 
-// A few rows: out[t][n] = sum_k x[t][k] w[k][n], w [K][parts][N], through fp32 partial
-// sums that a second kernel adds and finishes: + bias, and with act >= 0 the gate of
-// w's two parts (T x N of h), else rows.
+// A few rows: out[t][n] = sum_k x[t][k] w[k][n], through fp32 partial sums that a second
+// kernel adds and finishes.
+//   w: [K][nparts][N], or with kmajor [N][kparts][K] (K runs over the parts);
+//   x: bf16 planes of T rows, one after the other, rows ldx apart, K's parts xpart: one or
+//      two planes beside bf16 weights, three beside fp32 ones (padded with zeros to 8).
+enum : int { kFewRows = 0, kFewGlu = 1, kFewDglu = 2 };
 struct MlpFewArgs {
-  const void* x;        // [T][K]
-  const void* w;        // [K][parts][N]
-  const void* bias;     // [parts][N] or null
-  void* out;            // [T][N]
-  float* part;          // [blocks of columns + blocks of the grid][T][columns of a block]
-  int T, K, N, parts, act;   // T: rows of x
-  int rows;             // of the result: T, or T / 2 where x is hi rows, then lo rows
-  int two;              // out is rows, then what their rounding left (bf16)
+  const void* x;
+  const void* w;
+  size_t ldx, xpart;
+  int T, planes, K, kparts, N, nparts, kmajor;
+  float* part;          // [blocks of columns + blocks of the grid][rows][columns of a block]
   bool second;          // x comes from the kernel before, which is one of these
+  // the join: rows: out [T][N] + bias; glu: planes of h [T][ldo] with bias [2][N], p and q
+  // [T][N] fp32 where set; dglu: planes of (dg | du) [T][2][ldo] from p and q
+  int mode, act, out_planes;
+  const void* bias;
+  void* out;
+  size_t ldo;
+  float* p;
+  float* q;
   // filled by the launcher
-  int nb, ks, grid;     // column blocks of a part, K steps, blocks of the grid
+  int nb, ks, kst, grid;   // column blocks of a part, K steps (of a part), blocks of the grid
   int* err;
 };
-// whether a call of T rows goes this way, and whether its h is in two parts
+// whether a call of T rows goes this way
 bool mlp_few_ok(int T, int C, int F, bool f32);
-bool mlp_few_two(int T, bool f32);
-size_t mlp_few_bytes(int T, int N, int parts);
+// bytes of the partial sums
+size_t mlp_few_bytes(int T, int planes, int N, int nparts, bool f32);
 cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st);
 
 }  // namespace lapnys

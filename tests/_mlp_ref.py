@@ -9,8 +9,8 @@ out, and of nine products of parts three, below 3 * 2^-24; a0 b0 is summed over 
 Activation.  An activation's and its slope's own error is taken as 2^-19 (bf16 calls: approximate
 exponential and reciprocal, 2^-22 each, times small factors) or 2^-21 (fp32) of 1 + |g|; their slopes are
 below 1.2.
-Between the products bf16 calls round h and the gradient of (g | u), half a step; with two parts (few rows
-without a gradient, or T C F <= 2^28) half a step of what the first left, 2^-16 in all, and their products
+Between the products bf16 calls round h and the gradient of (g | u), half a step; with two parts (up to 64
+rows of whole 16-byte pieces, or T C F <= 2^28) half a step of what the first left, 2^-16 in all, and their products
 run over both parts, one after the other: twice the steps.  Kept for the backward: p, q rounded to f16 (bf16 calls), 2^-12 of the value and 2^-38 of the
 largest of 32.
 """
@@ -60,12 +60,12 @@ def mm2(a, b, two):
     return Off(a.v @ b.v, a.off @ B + A @ b.off + s * (A @ B) + 1e-37)
 
 
-def reference(x, w_in, b_in, w_out, b_out, kind, dy=None, two=None):
+def reference(x, w_in, b_in, w_out, b_out, kind, dy=None):
     """{name: Off} of y and, with dy, of the gradients; x, dy [T, C]"""
     f32, dt = x.dtype == torch.float32, x.dtype
     Fh = w_out.shape[0]
-    if two is None:
-        two = x.shape[0] * w_in.shape[0] * Fh <= 2 ** 28
+    T, C = x.shape
+    two = T * C * Fh <= 2 ** 28 or (T <= 64 and C % 8 == 0 and Fh % 8 == 0)
     part = lambda o: (o,)  # noqa: E731
     X, W, V = Off.of(x), Off.of(w_in), Off.of(w_out)
     z = mm(X, W, f32)

@@ -41,13 +41,10 @@ def test_forward_and_gradients(dtype, T, C, Fh, act, bias):
     for n, g in grads.items():
         check("d" + n, g, ref[n], dtype)
     with torch.no_grad():
-        y = lap.gated_mlp(**t, act=act)
-    if 32 < T <= 64:       # one part of h: half a step more
-        ref = reference(**t, kind=act, two=False)
-    check("y alone", y, ref["y"], dtype)
+        check("y alone", lap.gated_mlp(**t, act=act), ref["y"], dtype)
 
 
-@pytest.mark.parametrize("T,C,Fh", [(2, 24, 40), (6, 32, 72), (16, 32, 64), (200, 64, 128), (256, 512, 2048)])
+@pytest.mark.parametrize("T,C,Fh", [(2, 24, 40), (6, 32, 72), (16, 32, 64), (200, 64, 128), (256, 512, 2048), (40, 2048, 4096)])
 def test_small_calls_add_next_to_nothing_to_the_roundings_of_their_results(T, C, Fh):
     """h and the gradient of (g | u) in two parts: the 2-norm of the error is that of rounding the exact
     values, but for 2^-12 (p, q) and 2^-16, a tenth of a rounding's 2^-9 or so, squared beside it."""
@@ -62,15 +59,20 @@ def test_small_calls_add_next_to_nothing_to_the_roundings_of_their_results(T, C,
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
-@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 17, 48, 63, 64, 65])
-@pytest.mark.parametrize("C,Fh,act", [(512, 2048, "silu"), (2048, 520, "gelu"), (1000, 3000, "gelu_tanh"), (66, 70, "silu")])
-def test_few_rows_alone(dtype, T, C, Fh, act):
-    """Without a gradient, few rows go their own way (weights read once, split over all SMs)."""
-    t, _ = _inputs(T, C, Fh, dtype, T % 2 == 0, 6)
-    ref = reference(**t, kind=act, two=T <= 32 or T * C * Fh <= 2 ** 28 and T > 64)
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 16, 17, 33, 48, 63, 64, 65, 100, 128, 129])
+@pytest.mark.parametrize("C,Fh,act", [(512, 2048, "silu"), (2048, 520, "gelu"), (1000, 3000, "gelu_tanh"), (66, 70, "silu"),
+                                      (333, 1021, "silu")])
+def test_few_rows(dtype, T, C, Fh, act):
+    """Few rows go their own way (weights read once, split over all SMs), up to 64 in bf16, 128 in fp32."""
+    t, dy = _inputs(T, C, Fh, dtype, T % 2 == 0, 6)
+    ref = reference(**t, kind=act, dy=dy)
     first = lap.gated_mlp(**t, act=act)
     check("y", first, ref["y"], dtype)
     assert torch.equal(lap.gated_mlp(**t, act=act), first)
+    y, grads = _step(t, dy, act)
+    assert torch.equal(y, first) or T > 64
+    for n, g in grads.items():
+        check("d" + n, g, ref[n], dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
