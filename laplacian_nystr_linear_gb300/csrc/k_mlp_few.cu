@@ -36,8 +36,9 @@ constexpr int FEW_BF16 = 64, FEW_F32 = 128;   // rows of a call
 constexpr int FR = 64;                // rows of an fp32 CTA
 constexpr int NTC = 192, NST = 6;     // bf16: threads, slots at the most
 constexpr uint32_t A_BYTES = FNB * FK * 2;
-// fp32: a warp that issues, eight that load, four that read the sums
-constexpr int LW = 8, NF32 = 32 * (1 + LW + 4), NSF = 3;
+// fp32: a warp that issues, three idle beside it, sixteen that load, eight that read the sums
+constexpr int LW = 16, EW = 8, NF32 = 32 * (4 + LW + EW), NSF = 3;
+constexpr int LP = 128 * 8 / (32 * LW);       // pieces of eight weights a loading thread
 constexpr uint32_t PLANE = FNF * FK * 2;      // of the weights' tile
 constexpr int KCH = 2;                        // units of an accumulator
 
@@ -241,9 +242,9 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&accf[i]), 1);
-      tc::mbar_init(tc::smem_u32(&acce[i]), 4);
+      tc::mbar_init(tc::smem_u32(&acce[i]), EW);
     }
-    tc::mbar_init(tc::smem_u32(&smalle), 4);
+    tc::mbar_init(tc::smem_u32(&smalle), EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     consumed_s = 0;
     bad_s = 0;
@@ -298,109 +299,144 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
       consumed_s = consumed;
       if (bad) atomicOr(&bad_s, 1);
     }
-  } else if (warp <= LW) {
+  } else if (warp >= 4 && warp < 4 + LW) {
     // ---------------- loads ----------------
-    const int lt = tid - 32;
+    const int lt = tid - 128;
     const float* w = (const float*)a.w;
     const size_t ldw = a.kmajor ? (size_t)a.kparts * a.K : (size_t)a.nparts * a.N;
-    // eight values of a tile's row: row r, piece c; MN-major rows are k in two blocks of 64
-    // columns, K-major ones columns
-    auto fetch = [&](int u, float(&v)[4][8]) {
-      const int block = u / a.ks, ku = u - block * a.ks, kp = ku >= a.kst ? 1 : 0;
-      const int part = block / a.nb, n0 = (block - part * a.nb) * FNF, k0 = (ku - kp * a.kst) * FK;
+    // Pieces of eight values of a tile's rows: MN-major rows are k in two blocks of 64
+    // columns, K-major ones columns.  Of the unit that is fetched next: column block, k step,
+    // pointers; divisions once a column block.
+    int nu = u0, nk = u0 % a.ks, nblock = u0 / a.ks;
+    const float* at[LP];
+    int left[LP];                            // values of the row from there (MN-major)
+    auto place = [&]() {
+      const int part = nblock / a.nb, n0 = (nblock - part * a.nb) * FNF, kp = nk >= a.kst ? 1 : 0;
+      const int k0 = (nk - kp * a.kst) * FK;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (lt + 256 * j) >> 3, c = (lt & 7) * 8;
+      for (int j = 0; j < LP; ++j) {
+        const int r = (lt + 32 * LW * j) >> 3, c = (lt & 7) * 8;
         const int k = a.kmajor ? k0 + c : k0 + (r & 63), n = a.kmajor ? n0 + r : n0 + (r & 64) + c;
-        const float* p = a.kmajor ? w + (size_t)n * ldw + (size_t)kp * a.K + k
-                                  : w + (size_t)k * ldw + (size_t)part * a.N + n;
-        const bool in = a.kmajor ? n < a.N : k < a.K;
-        const int left = in ? (a.kmajor ? a.K - k : a.N - n) : 0;      // of the row
+        at[j] = a.kmajor ? w + (size_t)n * ldw + (size_t)kp * a.K + k : w + (size_t)k * ldw + (size_t)part * a.N + n;
+        left[j] = a.kmajor ? (n < a.N ? a.K : 0) : a.N - n;
+      }
+    };
+    auto fetch = [&](float(&v)[LP][8]) {
+      const int k0 = (nk >= a.kst ? nk - a.kst : nk) * FK;
+#pragma unroll
+      for (int j = 0; j < LP; ++j) {
+        const int r = (lt + 32 * LW * j) >> 3, c = (lt & 7) * 8;
+        const int m = a.kmajor ? left[j] - k0 - c : (k0 + (r & 63) < a.K ? left[j] : 0);   // of the piece's row
         if constexpr (WIDE) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float4 f = left > 4 * h ? __ldcs(reinterpret_cast<const float4*>(p) + h)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 f = m > 4 * h ? __ldcs(reinterpret_cast<const float4*>(at[j]) + h)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             v[j][4 * h] = f.x; v[j][4 * h + 1] = f.y; v[j][4 * h + 2] = f.z; v[j][4 * h + 3] = f.w;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[j][i] = left > i ? __ldcs(p + i) : 0.f;
+          for (int i = 0; i < 8; ++i) v[j][i] = m > i ? __ldcs(at[j] + i) : 0.f;
         }
+        at[j] += a.kmajor ? (size_t)FK : FK * ldw;
+      }
+      ++nu;
+      if (++nk == a.ks) {
+        nk = 0;
+        ++nblock;
+        if (nu < u1) place();
+      } else if (nk == a.kst) {
+        place();                             // K's second part
       }
     };
-    // x's three planes of a unit, rows padded with zeros
+    // x's three planes of a unit, rows padded with zeros: this thread's pieces
+    constexpr int XP = 3 * FR * 8 / (32 * LW);
     const __nv_bfloat16* x = (const __nv_bfloat16*)a.x;
-    auto fetch_x = [&](int u, int st) {
-      const int ku = u % a.ks, kp = ku >= a.kst ? 1 : 0, k0 = (ku - kp * a.kst) * FK;
-      const uint32_t base = sm + st * slot + 3 * PLANE;
-      for (int e = lt; e < 3 * rows * 8; e += 32 * LW) {
-        const int rr = e >> 3, c = e & 7, plane = rr / rows, t = rr - plane * rows;
-        const bool in = t < T && k0 + 8 * c < ((a.K + 7) & ~7);
-        const __nv_bfloat16* p = x + ((size_t)plane * a.T + row0 + t) * a.ldx + kp * a.xpart + k0 + 8 * c;
-        cp_async16(base + rr * 128 + ((c ^ (rr & 7)) << 4), in ? p : x, in);
-      }
+    const __nv_bfloat16* xat[XP];
+    uint32_t xto[XP];
+    bool xin[XP];
+    const int pieces = 3 * rows * 8, xc = (lt & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int e = lt + 32 * LW * i, rr = e >> 3, plane = rr / rows, t = rr - plane * rows;
+      xin[i] = e < pieces && t < T;
+      xat[i] = x + ((size_t)plane * a.T + row0 + t) * a.ldx + xc;
+      xto[i] = sm + 3 * PLANE + rr * 128 + (((lt & 7) ^ (rr & 7)) << 4);
+    }
+    int xk = u0 % a.ks;                      // k step of the unit whose rows come next
+    auto fetch_x = [&](int st) {
+      const int kp = xk >= a.kst ? 1 : 0, k0 = (xk - kp * a.kst) * FK;
+      const size_t off = kp * a.xpart + k0;
+      const bool in = k0 + xc < ((a.K + 7) & ~7);
+#pragma unroll
+      for (int i = 0; i < XP; ++i)
+        if (lt + 32 * LW * i < pieces)
+          cp_async16(xto[i] + st * slot, xin[i] && in ? xat[i] + off : x, xin[i] && in);
       cp_commit();
+      if (++xk == a.ks) xk = 0;
     };
-    float v0[4][8], v1[4][8];
+    float v0[LP][8], v1[LP][8];
     bool bad = false;
-    int n = 0;                               // units so far
-    auto ready = [&](int i) {                // the slot of the CTA's unit i is free
-      if (!bad && !wtc::wait_warp(a.err, tc::smem_u32(&empty[i % NSF]), ((uint32_t)(i / NSF) & 1u) ^ 1u)) bad = true;
-    };
+    int n = 0, st = 0;                       // units so far, slot
     // one unit, its weights in v: split, written, and v filled for two units later
-    auto work = [&](int u, float(&v)[4][8]) {
-      const int st = n % NSF;
+    auto work = [&](int u, float(&v)[LP][8]) {
+      const int after = st + 1 == NSF ? 0 : st + 1;
       if (u + 1 < u1) {
-        ready(n + 1);
-        if (bad) return;
-        fetch_x(u + 1, (n + 1) % NSF);
+        // the next unit's slot is free
+        if (!wtc::wait_warp(a.err, tc::smem_u32(&empty[after]), ((uint32_t)((n + 1) / NSF) & 1u) ^ 1u)) {
+          bad = true;
+          return;
+        }
+        fetch_x(after);
       } else {
         cp_commit();
       }
       const uint32_t base = sm + st * slot;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (lt + 256 * j) >> 3, c = lt & 7;
+      for (int j = 0; j < LP; ++j) {
+        const int r = (lt + 32 * LW * j) >> 3, c = lt & 7;
         uint32_t s[4][3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split3_bf16x2(v[j][2 * i], v[j][2 * i + 1], s[i]);
-        const uint32_t at = base + r * 128 + ((c ^ (r & 7)) << 4);
+        const uint32_t to = base + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + p * PLANE), "r"(s[0][p]), "r"(s[1][p]),
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + p * PLANE), "r"(s[0][p]), "r"(s[1][p]),
                        "r"(s[2][p]), "r"(s[3][p])
                        : "memory");
       }
-      if (u + 2 < u1) fetch(u + 2, v);
+      if (u + 2 < u1) fetch(v);
       asm volatile("cp.async.wait_group 1;" ::: "memory");     // this unit's x
       tc::fence_async_smem();
       wtc::arrive_warp(tc::smem_u32(&full[st]));
       ++n;
+      st = after;
     };
     if (!a.second) wait_before();
-    fetch(u0, v0);
-    if (u0 + 1 < u1) fetch(u0 + 1, v1);
+    place();
+    fetch(v0);
+    if (u0 + 1 < u1) fetch(v1);
     if (a.second) wait_before();             // the weights are no other kernel's output
-    fetch_x(u0, 0);
+    fetch_x(0);
     for (int u = u0; u < u1 && !bad; u += 2) {
       work(u, v0);
       if (u + 1 < u1 && !bad) work(u + 1, v1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (bad) atomicOr(&bad_s, 1);
-  } else {
-    // ---------------- sums ----------------
+  } else if (warp >= 4 + LW) {
+    // ---------------- sums: half of the rows a warp ----------------
     wait_before();
-    const int q = warp & 3;
+    constexpr int HR = FR / 2;
+    const int q = warp & 3, h0 = warp >= 8 + LW ? HR : 0;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     bool bad = false;
     uint32_t ch = 0;
     for (int u = u0; u < u1 && !bad;) {
       const int block = u / a.ks, end = min(u1, (block + 1) * a.ks);
-      float R[FR];
+      float R[HR];
 #pragma unroll
-      for (int i = 0; i < FR; ++i) R[i] = 0.f;
+      for (int i = 0; i < HR; ++i) R[i] = 0.f;
       for (; u < end; u = min(end, u + KCH), ++ch) {
         __syncwarp();
         if (!wtc::wait_warp(a.err, tc::smem_u32(&accf[ch & 1]), (ch >> 1) & 1u)) {
@@ -410,16 +446,16 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
         tc::fence_after();
         const bool last = u + KCH >= end;
 #pragma unroll
-        for (int t0 = 0; t0 < FR; t0 += 16)
-          if (t0 < rows) {
+        for (int t0 = 0; t0 < HR; t0 += 16)
+          if (h0 + t0 < rows) {
             uint32_t x[16];
-            tc::tmem_ld<16>(tmem + lanes + (ch & 1) * 64 + t0, x);
+            tc::tmem_ld<16>(tmem + lanes + (ch & 1) * 64 + h0 + t0, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) R[t0 + i] += __uint_as_float(x[i]);
             if (last)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                tc::tmem_ld<16>(tmem + lanes + 128 + h * rows + t0, x);
+                tc::tmem_ld<16>(tmem + lanes + 128 + h * rows + h0 + t0, x);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) R[t0 + i] += __uint_as_float(x[i]);
               }
@@ -429,10 +465,10 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
         if (last) wtc::arrive_warp(tc::smem_u32(&smalle));
       }
       if (bad) break;
-      float* o = a.part + ((size_t)(block + blockIdx.x) * a.T + row0) * FNF + 32 * q + lane;
+      float* o = a.part + ((size_t)(block + blockIdx.x) * a.T + row0 + h0) * FNF + 32 * q + lane;
 #pragma unroll
-      for (int t = 0; t < FR; ++t)
-        if (t < T) o[t * FNF] = R[t];
+      for (int t = 0; t < HR; ++t)
+        if (h0 + t < T) o[t * FNF] = R[t];
     }
     if (bad) atomicOr(&bad_s, 1);
   }
