@@ -417,8 +417,8 @@ int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void
  * workspace.  act: z / (1 + exp(-z)) (LAPNYS_SILU),
  * z (1 + erf(z / sqrt 2)) / 2 (LAPNYS_GELU), or its tanh form (LAPNYS_GELU_TANH).
  * Sums are float32.  bf16 calls round h, and in the backward the gradient of (g | u),
- * between the products: to bf16, or to two bf16 parts (16 bits) where T C F <= 2^28 or,
- * without a ctx, T <= 32.  fp32 operands are taken as three bf16 parts (24 bits; magnitudes
+ * between the products: to bf16, or to two bf16 parts (16 bits) where T C F <= 2^28 or
+ * T <= 64 (with C and F multiples of 8).  fp32 operands are taken as three bf16 parts (24 bits; magnitudes
  * below 2^-110 keep fewer, and a row of x with an infinity comes out as NaN).  Results
  * repeat bit for bit.
  *  - ctx (lapnys_mlp_ctx_bytes): what the backward needs; NULL: none.

@@ -14,10 +14,14 @@
 // sums; h and (dg | du) are two bf16 planes (16 bits), the second as further rows of x,
 // which costs a call bound by its weights nothing.  16 tokens, 4096 x 10880: 55 us, 5.3 TB/s
 // while a product runs.
-// fp32 (k_mlp_few_f32): eight warps load the weights two units ahead, split them into three
-// bf16 planes (x comes as three) and write those as operand tiles; six products of planes,
-// a0 b0 summed over 128 k by the instruction and beyond by the epilogue's registers, as in
-// the large products.  More than 64 rows: a second CTA beside, weights out of L2.  XXX
+// fp32, up to 8 rows (k_mlp_few_fma, forward, and k_mlp_few_fma_k, backward): on the FP32
+// pipe; a token of 4096 x 10880: 102 us, 5.5 TB/s while a product runs.  9 to 128 rows
+// (k_mlp_few_f32): sixteen warps load the weights two units ahead, split them into three bf16
+// planes (x comes as three) and write those as operand tiles; six products of planes, a0 b0
+// summed over 128 k by the instruction and beyond by the epilogue's registers, as in the large
+// products.  148 us at 16 rows (the loading warps' instructions; in two groups with a unit
+// each: 169), 216 at 64 (the products of 64 columns); the large products take 464 through
+// their packed weights.  More than 64 rows: a second CTA beside, weights out of L2.
 #include <cuda.h>
 
 #include <cstring>
@@ -32,7 +36,7 @@ namespace {
 
 constexpr int FNB = 256, FNF = 128;   // columns of a unit (bf16, fp32)
 constexpr int FK = 64;                // k of a unit
-constexpr int FEW_BF16 = 64, FEW_F32 = 128;   // rows of a call
+constexpr int FEW_BF16 = 64, FEW_F32 = 128, FEW_FMA = 8;   // rows of a call
 constexpr int FR = 64;                // rows of an fp32 CTA
 constexpr int NTC = 192, NST = 6;     // bf16: threads, slots at the most
 constexpr uint32_t A_BYTES = FNB * FK * 2;
@@ -483,6 +487,198 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
   if (warp == 0) tc::tmem_dealloc(tmem, 256);
 }
 
+// fp32, up to 8 rows (TT, padded), on the FP32 pipe: no more than eight multiply-adds a
+// weight, which it does as fast as weights come.  x is summed up again from its three planes
+// (exactly what it was, or h to 2^-24).  A segment is a CTA's stretch of one column block.
+constexpr int FT = 256;               // threads
+constexpr int XC = 256;               // k of x in shared memory
+
+// x[t][k0 .. k0 + XC) of K's part kp
+template <int TT>
+__device__ __forceinline__ void rows_in(const MlpFewArgs& a, int kp, int k0, float* to, int ldt, int ldk) {
+  const __nv_bfloat16* x = (const __nv_bfloat16*)a.x + kp * a.xpart + k0;
+  const size_t plane = (size_t)a.T * a.ldx;
+  for (int e = threadIdx.x; e < XC * TT; e += FT) {
+    const int t = e / XC, k = e % XC;
+    float v = 0.f;
+    if (t < a.T && k0 + k < a.K) {
+      const __nv_bfloat16* p = x + (size_t)t * a.ldx + k;
+      v = __bfloat162float(p[0]) + (__bfloat162float(p[plane]) + __bfloat162float(p[2 * plane]));
+    }
+    to[t * ldt + k * ldk] = v;
+  }
+}
+
+// w [K][nparts][N]: four columns a lane, rows of x in packed pairs; the warps take a
+// segment's k in turn and their sums are joined in shared memory, halves of the warps at a
+// time, in one order
+template <int TT, bool WIDE>
+__global__ void __launch_bounds__(FT, 2) k_mlp_few_fma(MlpFewArgs a) {
+  __shared__ __align__(16) float xs[XC][TT];
+  __shared__ __align__(16) float4 join[4][TT][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int u0, u1;
+  stretch(a, blockIdx.x, &u0, &u1);
+  let_next();
+  wait_before();
+  const size_t ld = (size_t)a.nparts * a.N;
+  for (int u = u0; u < u1;) {
+    const int block = u / a.ks, part = block / a.nb, n = (block - part * a.nb) * FNF + 4 * lane;
+    const int end = min(u1, (block + 1) * a.ks);
+    const int k0 = (u - block * a.ks) * FK, k1 = min(a.K, (end - block * a.ks) * FK);
+    u = end;
+    f32x2 acc[4][TT / 2];                   // column, rows 2 t and 2 t + 1
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int t = 0; t < TT / 2; ++t) acc[c][t] = pack2(0.f, 0.f);
+    const float* w = (const float*)a.w + (size_t)part * a.N + n;
+    for (int kc = k0; kc < k1; kc += XC) {
+      const int m = min(XC, k1 - kc);
+      __syncthreads();
+      rows_in<TT>(a, 0, kc, &xs[0][0], 1, TT);
+      __syncthreads();
+#pragma unroll 8
+      for (int k = warp; k < m; k += FT / 32) {
+        const float* p = w + (size_t)(kc + k) * ld;
+        float v[4];
+        if constexpr (WIDE) {
+          const float4 f = n < a.N ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = n + c < a.N ? __ldcs(p + c) : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < TT; t += 4) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&xs[k][t]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const f32x2 ww = pack2(v[c], v[c]);
+            acc[c][t / 2] = fma2(ww, x.x, acc[c][t / 2]);
+            acc[c][t / 2 + 1] = fma2(ww, x.y, acc[c][t / 2 + 1]);
+          }
+        }
+      }
+    }
+    auto row = [&](int t) {
+      float f[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 y = unpack2(acc[c][t / 2]);
+        f[c] = t & 1 ? y.y : y.x;
+      }
+      return make_float4(f[0], f[1], f[2], f[3]);
+    };
+#pragma unroll
+    for (int half = 4; half >= 1; half >>= 1) {
+      __syncthreads();
+      if (warp >= half && warp < 2 * half)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) join[warp - half][t][lane] = row(t);
+      __syncthreads();
+      if (warp < half)
+#pragma unroll
+        for (int t = 0; t < TT; t += 2) {
+          const float4 y = join[warp][t][lane], z = join[warp][t + 1][lane];
+          acc[0][t / 2] = wtc::add2(acc[0][t / 2], pack2(y.x, z.x));
+          acc[1][t / 2] = wtc::add2(acc[1][t / 2], pack2(y.y, z.y));
+          acc[2][t / 2] = wtc::add2(acc[2][t / 2], pack2(y.z, z.z));
+          acc[3][t / 2] = wtc::add2(acc[3][t / 2], pack2(y.w, z.w));
+        }
+    }
+    if (warp == 0) {
+      float* o = a.part + (size_t)(block + blockIdx.x) * a.T * FNF + 4 * lane;
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        if (t < a.T) *reinterpret_cast<float4*>(o + t * FNF) = row(t);
+    }
+  }
+}
+
+// w [N][kparts][K]: a warp takes 16 of a block's columns (rows of w), four at a time, its
+// lanes along k; x is read from shared memory once for the four
+template <int TT, bool WIDE>
+__global__ void __launch_bounds__(FT, 2) k_mlp_few_fma_k(MlpFewArgs a) {
+  constexpr int RB = 4;               // rows of w at a time
+  __shared__ __align__(16) float xs[TT][XC];
+  __shared__ float sums[FNF][TT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int u0, u1;
+  stretch(a, blockIdx.x, &u0, &u1);
+  let_next();
+  wait_before();
+  const size_t ld = (size_t)a.kparts * a.K;
+  for (int u = u0; u < u1;) {
+    const int block = u / a.ks, end = min(u1, (block + 1) * a.ks), n0 = block * FNF + 16 * warp;
+    int ku = u - block * a.ks;
+    const int kend = end - block * a.ks;
+    u = end;
+    for (int i = lane; i < 16 * TT; i += 32) sums[16 * warp + i / TT][i % TT] = 0.f;
+    while (ku < kend) {
+      // as many steps as lie in one part of K and in shared memory
+      const int kp = ku >= a.kst ? 1 : 0, k0 = (ku - kp * a.kst) * FK;
+      const int steps = min(min(kend, (kp + 1) * a.kst) - ku, XC / FK), m = min(a.K - k0, steps * FK);
+      ku += steps;
+      __syncthreads();
+      rows_in<TT>(a, kp, k0, &xs[0][0], XC, 1);
+      __syncthreads();
+#pragma unroll 1
+      for (int r = 0; r < 16; r += RB) {
+        f32x2 acc[RB][TT];
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[i][t] = pack2(0.f, 0.f);
+        const float* w = (const float*)a.w + (size_t)(n0 + r) * ld + (size_t)kp * a.K + k0 + 4 * lane;
+        float4 f[RB][XC / 128];
+#pragma unroll
+        for (int j = 0; j < XC / 128; ++j)
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            const float* p = w + i * ld + 128 * j;
+            const int left = n0 + r + i < a.N ? m - 128 * j - 4 * lane : 0;
+            f[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (WIDE) {
+              if (left > 0) f[i][j] = __ldcs(reinterpret_cast<const float4*>(p));
+            } else {
+              if (left > 0) f[i][j].x = __ldcs(p);
+              if (left > 1) f[i][j].y = __ldcs(p + 1);
+              if (left > 2) f[i][j].z = __ldcs(p + 2);
+              if (left > 3) f[i][j].w = __ldcs(p + 3);
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < XC / 128; ++j)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&xs[t][128 * j + 4 * lane]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+              acc[i][t] = fma2(pack2(f[i][j].x, f[i][j].y), x.x, acc[i][t]);
+              acc[i][t] = fma2(pack2(f[i][j].z, f[i][j].w), x.y, acc[i][t]);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const float2 y = unpack2(acc[i][t]);
+            float v = y.x + y.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) sums[16 * warp + r + i][t] += v;
+          }
+      }
+    }
+    __syncwarp();
+    float* o = a.part + (size_t)(block + blockIdx.x) * a.T * FNF + 16 * warp;
+    for (int i = lane; i < 16 * TT; i += 32)
+      if (i / 16 < a.T) o[(i / 16) * FNF + i % 16] = sums[16 * warp + i % 16][i / 16];
+    __syncwarp();
+  }
+}
+
 // v as `planes` bf16 values, plane elements apart (infinities leave nothing to the later ones)
 __device__ __forceinline__ void put_planes(__nv_bfloat16* o, size_t plane, int planes, float v) {
   for (int i = 0; i < planes; ++i) {
@@ -554,20 +750,22 @@ __global__ void __launch_bounds__(256) k_mlp_few_join(MlpFewArgs a) {
   }
 }
 
-// grid and units of a product: a CTA for each SM, as far as there are units
+// grid and units of a product: a CTA for each SM (two on the FP32 pipe), as far as there are
+// units
 void shape(MlpFewArgs& a, bool f32) {
   const int fn = f32 ? FNF : FNB;
   a.nb = (a.N + fn - 1) / fn;
   a.kst = (a.K + FK - 1) / FK;
   a.ks = a.kst * a.kparts;
-  const long long units = (long long)a.nparts * a.nb * a.ks, most = f32 ? 152 / ((a.T + FR - 1) / FR) : 152;
+  const long long units = (long long)a.nparts * a.nb * a.ks, most = !f32 ? 152 : a.T <= FEW_FMA ? 304 : 152 / ((a.T + FR - 1) / FR);
   a.grid = (int)(units < most ? units : most);
 }
 
 }  // namespace
 
 // Few enough rows to read all weights once; bf16 rows and columns have to be whole 16-byte
-// pieces.  (fp32, 4096 x 10880: XXX.  bf16: 70 us at 64 rows, 83 by the large products at 65.)
+// pieces.  (bf16, 4096 x 10880: 73 us at 64 rows, 81 by the large products at 65.  fp32, 3782 x
+// 15128, forward + backward: 1452 us at 128 rows, 1531 by the large products at 129.)
 bool mlp_few_ok(int T, int C, int F, bool f32) {
   if ((double)C * F >= 1e12) return false;      // units are counted in 32 bits
   return f32 ? T <= FEW_F32 : T <= FEW_BF16 && C % 8 == 0 && F % 8 == 0;
@@ -575,7 +773,15 @@ bool mlp_few_ok(int T, int C, int F, bool f32) {
 
 size_t mlp_few_bytes(int T, int planes, int N, int nparts, bool f32) {
   const int fn = f32 ? FNF : FNB;
-  return ((size_t)nparts * ((N + fn - 1) / fn) + 152) * T * (f32 ? 1 : planes) * fn * 4;
+  return ((size_t)nparts * ((N + fn - 1) / fn) + 304) * T * (f32 ? 1 : planes) * fn * 4;
+}
+
+template <int TT>
+static cudaError_t go_fma(const MlpFewArgs& a, bool wide, cudaStream_t st) {
+  auto* k = a.kmajor ? (wide ? k_mlp_few_fma_k<TT, true> : k_mlp_few_fma_k<TT, false>)
+                     : (wide ? k_mlp_few_fma<TT, true> : k_mlp_few_fma<TT, false>);
+  if (a.second) return launch_after("mlp_few", k, dim3(a.grid), dim3(FT), 0, st, a);
+  return launch("mlp_few", k, dim3(a.grid), dim3(FT), 0, st, a);
 }
 
 cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st) {
@@ -585,9 +791,12 @@ cudaError_t run_mlp_few(MlpFewArgs& a, bool f32, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.err = wait_error_address();
   if (a.err == nullptr) return cudaErrorInvalidSymbol;
-  if (f32) {
+  const bool pieces = ((uintptr_t)a.w & 15) == 0 && (a.kmajor ? a.K : a.N) % 4 == 0;
+  if (f32 && a.T <= FEW_FMA) {
+    e = a.T <= 4 ? go_fma<4>(a, pieces, st) : go_fma<8>(a, pieces, st);
+  } else if (f32) {
     const int groups = (a.T + FR - 1) / FR, most = a.T < FR ? a.T : FR, rows = (most + 15) / 16 * 16;
-    const bool wide = ((uintptr_t)a.w & 15) == 0 && (a.kmajor ? a.K : a.N) % 4 == 0;
+    const bool wide = pieces;
     auto* k = wide ? k_mlp_few_f32<true> : k_mlp_few_f32<false>;
     static SmemOnce once[2];
     const size_t smem = NSF * (3 * PLANE + 3 * (size_t)rows * 128) + 1024;
