@@ -383,7 +383,7 @@ int lapnys_rotary(const void* q, const void* k, void* q_out, void* k_out, const 
  * norm of h, post that of u; LAPNYS_NONE: y is not formed, n(u) = u.
  *  - x, u, h, y [B][N][C] of `dtype`, any alignment of the elements' own (16 bytes
  *    and C a multiple of 16 bytes of elements is faster); C <= 16384
- *    (LAPNYS_ENOTSUP above).  u NULL: h = x, and h may be NULL.  h is rounded once,
+ *    (LAPNYS_ENOTSUP above), B N at most 2^31 - 1024.  u NULL: h = x, and h may be NULL.  h is rounded once,
  *    y is formed from it before its rounding.
  *  - weight, bias [C], or [B][C] with per_seq; gate [B][C]; scale, post_weight,
  *    post_bias [C]; each of `dtype`, or NULL: 1 (bias: 0).  A vector of something

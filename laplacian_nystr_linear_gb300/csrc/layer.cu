@@ -16,7 +16,8 @@ int status(cudaError_t e) { return e == cudaSuccess ? LAPNYS_OK : LAPNYS_ECUDA; 
 bool known(int dtype) { return dtype == LAPNYS_F32 || dtype == LAPNYS_BF16; }
 
 int check_norm(NormArgs& a, int B, int N, int C, int per_seq, int pre, int post, float eps) {
-  if (B <= 0 || N <= 0 || C <= 0 || (long long)B * N >= 1LL << 31) return LAPNYS_EINVAL;
+  // rows are counted in 32 bits, with room for a tile or the joins' threads behind the last
+  if (B <= 0 || N <= 0 || C <= 0 || (long long)B * N > (1LL << 31) - 1024) return LAPNYS_EINVAL;
   if (pre < kNormNone || pre > kNormLayer || post < kNormNone || post > kNormLayer) return LAPNYS_EINVAL;
   if (!(eps >= 0.f) || !isfinite(eps)) return LAPNYS_EINVAL;
   if (C > kNormMaxWidth) return LAPNYS_ENOTSUP;

@@ -94,6 +94,16 @@ def test_norm_refuses_more(lib):
     assert lib.lapnys_norm_workspace_bytes(0, 8, 64, 0) == 0
 
 
+def test_norm_rows_stay_countable(lib):
+    """Rows, and the places just behind the last one, are counted in 32 bits."""
+    most = 2 ** 31 - 1024
+    for B, N in ((1, most + 1), (most + 1, 1), (1, 2 ** 31 - 1)):
+        assert _fwd(lib, B=B, N=N) == _lib.LAPNYS_EINVAL and _bwd(lib, B=B, N=N) == _lib.LAPNYS_EINVAL
+        assert lib.lapnys_norm_workspace_bytes(B, N, 1, 1) == 0
+    # a sequence a row: sums of four kinds of every slot and sequence
+    assert 2 * 16 * most < lib.lapnys_norm_workspace_bytes(most, 1, 1, 1) < 2 * 16 * (most + 1024)
+
+
 MLP = dict(T=100, C=64, F=128)
 BIG = 1 << 40
 
