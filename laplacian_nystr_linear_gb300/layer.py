@@ -483,7 +483,10 @@ class _Mlp(torch.autograd.Function):
     def backward(fctx, dy):
         _no_tangent("gated_mlp's backward", dy)
         x, w_in, w_out, ctx = fctx.saved_tensors
-        return *_mlp_bwd(x, w_in, w_out, dy.contiguous(), ctx, fctx.plan, fctx.needs_input_grad, None), None
+        dy = dy.contiguous()
+        if dy.data_ptr() % 16:      # a piece of another tensor, as a concatenation's gradient is
+            dy = dy.clone()
+        return *_mlp_bwd(x, w_in, w_out, dy, ctx, fctx.plan, fctx.needs_input_grad, None), None
 
 
 def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
@@ -491,8 +494,8 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
     y = (act(g) * u) w_out + b_out.
 
     x: CUDA tensor (float32 or bfloat16) of rows of C features, [.., C]; w_in: [C, 2 F], the gate's
-    columns, then the others; w_out: [F, C]; biases [2 F] and [C] or None; act: "silu", "gelu" or
-    "gelu_tanh".  Gradients are of first order, by reverse mode only.
+    columns, then the others; w_out: [F, C]; biases [2 F] and [C] or None; all 16-byte aligned; act:
+    "silu", "gelu" or "gelu_tanh".  Gradients are of first order, by reverse mode only.
     """
     tensors = (x, w_in, b_in, w_out, b_out)
     _no_tangent("gated_mlp", *tensors)

@@ -132,9 +132,51 @@ def test_shapes_of_x_and_rows_that_are_not_finite():
     assert torch.equal(got[keep], y[keep]) and got[4].isnan().all() and not got[20].isfinite().any()
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,C", [(5, 33), (130, 33)])
+def test_gradient_that_is_a_piece_of_another(dtype, T, C):
+    """Rows of no whole 16-byte pieces, concatenated: the second part's gradient starts anywhere."""
+    t, dy = _inputs(T, C, 40, dtype, False, 9)
+    leaves = {n: None if v is None else v.clone().requires_grad_(True) for n, v in t.items()}
+    y = torch.cat([torch.zeros((1, C), dtype=dtype, device="cuda"), lap.gated_mlp(**leaves)])
+    whole = torch.cat([dy[:1], dy])
+    assert whole[1:].data_ptr() % 16 and whole[1:].is_contiguous()
+    got = torch.autograd.grad(y, [v for v in leaves.values() if v is not None], whole)
+    want = _step(t, dy, "silu", ("x", "w_in", "w_out"))[1]
+    assert all(torch.equal(a, b) for a, b in zip(got, want.values()))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [3, 40])
+def test_partial_gradients_of_few_rows(dtype, T):
+    t, dy = _inputs(T, 96, 200, dtype, True, 1)
+    whole = _step(t, dy, "gelu")[1]
+    for n in NAMES:
+        assert torch.equal(_step(t, dy, "gelu", (n,))[1][n], whole[n]), n
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_two_streams_at_once(dtype):
+    """Calls of few and of many rows side by side on two streams, each with its own workspace."""
+    torch.cuda.synchronize()
+    a, b = (_inputs(T, 1024, 2048, dtype, True, 7)[0] for T in (6, 40))
+    c = _inputs(300, 128, 256, dtype, True, 7)[0]
+    want = [lap.gated_mlp(**t) for t in (a, b, c)]
+    torch.cuda.synchronize()
+    streams, got = (torch.cuda.Stream(), torch.cuda.Stream()), []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append([lap.gated_mlp(**t) for t in (a, b, c)])
+    torch.cuda.synchronize()
+    for run in got:
+        assert all(torch.equal(x, y) for x, y in zip(run, want))
+    assert lap.api.load().lapnys_device_status(0) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
 @pytest.mark.parametrize("T", [1, 40, 300])
-def test_captured_and_on_another_stream(T):
-    t, dy = _inputs(T, 128, 256, torch.bfloat16, True, 5)
+def test_captured_and_on_another_stream(T, dtype):
+    t, dy = _inputs(T, 128, 256, dtype, True, 5)
     p = lap.MlpParams(T, 128, 256, "silu")
 
     def step():
