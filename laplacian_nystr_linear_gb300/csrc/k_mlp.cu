@@ -387,8 +387,8 @@ __device__ __forceinline__ void out_rows(const MlpGemmArgs& a, int part, int m0,
     return;
   }
   // rows that are no whole 16-byte pieces: the warp's 32 x 32 values turned, so that its
-  // lanes write one row side by side (each writing its own row took 430 us of a gradient of
-  // 15128 x 3782, 99 so)
+  // lanes write one row side by side (each writing its own row took 426 us of a gradient of
+  // 15128 x 3782, 80 so)
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1)
@@ -719,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
             if constexpr (TWO) store_bf16(o + a.plane_out, a.ldo, 32 * q, rows, cols, rest);
           }
         } else if constexpr (EPI == kMlpDglu) {
-const bool more = it + pairs < a.items;
+          const bool more = it + pairs < a.items;
           int after_m = 0, after_n = 0;
           if (more) {
             const Item after = decode<TN>(a, it + pairs);
@@ -851,8 +851,6 @@ __global__ void __launch_bounds__(256) k_mlp_reduce(MlpReduceArgs a, int quads) 
       o[i] = __float2bfloat16_rn(v[i]);
   }
 }
-
-
 
 template <bool F32>
 __global__ void __launch_bounds__(256) k_mlp_pack(MlpPackArgs a) {
