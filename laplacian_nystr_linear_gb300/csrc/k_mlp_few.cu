@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
   const uint32_t b_bytes = (uint32_t)rows * FK * 2, slot = A_BYTES + b_bytes;
   int u0, u1;
   stretch(a, blockIdx.x, &u0, &u1);
-  let_next();
   if (warp == 1) tc::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -99,6 +98,7 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_s;
+  let_next();      // this block has its tensor memory: no later one holds it back
   if (!(warp == 0 && a.second)) wait_before();
 
   if (warp == 0) {
@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
   const uint32_t slot = 3 * PLANE + 3 * (uint32_t)rows * 128;
   int u0, u1;
   stretch(a, blockIdx.x, &u0, &u1);
-  let_next();
   if (warp == 0) tc::tmem_alloc(&tmem_s, 256);
   if (tid == 0) {
     for (int i = 0; i < NSF; ++i) {
@@ -257,6 +256,7 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_s;
+  let_next();      // this block has its tensor memory: no later one holds it back
 
   if (warp == 0) {
     // ---------------- products ----------------
