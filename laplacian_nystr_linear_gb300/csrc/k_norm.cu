@@ -17,13 +17,14 @@
 // in it.  Statistics are of centred values, in fp32.
 //
 // Backward, rows of whole 16-byte pieces, up to 4096 features (k_norm_bwd_ring): a block
-// an SM takes an even stretch of all rows, in tiles of as many rows as its sixteen warps
-// work on at once (8 features a thread), which one more warp copies into a ring in shared
-// memory (bulk copies; a tile's rows lie side by side).  What a feature is multiplied by is
-// laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both norms, gate and
-// scale: 228 us, 3.5 TB/s, issue slots half busy: sums over a row (shuffles, then shared
-// memory between its two warps) are what a row waits for.  16 features a thread of eight
-// warps take as long; loads by the warps themselves beside 255 registers a thread took 390.
+// an SM takes an even stretch of all rows, in tiles of as many rows as its warps work on at
+// once (8 or 16 features a thread of sixteen or twelve warps), which one thread copies into a
+// ring in shared memory (bulk copies; a tile's rows lie side by side).  What a feature is
+// multiplied by is laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both
+// norms, gate and scale: 173 us, 4.7 TB/s: sums over a row are what a row waits for, so rows
+// in flight and registers count (a warp of its own for the copies costs the registers of
+// four: eight warps of 16 features, or sixteen of 8, took 228); loads by the warps
+// themselves beside 255 registers a thread took 390.
 //
 // Forward, such rows (k_norm_fwd_rows): threads copy their own pieces two rows ahead
 // (cp.async), two blocks an SM: 98 us for the same rows, 5.5 TB/s; 32768 rows of 4096, two
@@ -380,10 +381,11 @@ __global__ void __launch_bounds__(TB) k_norm_bwd(NormArgs a, int warps) {
 // ---------------------------------------------------------------------------
 // the backward's rows through a ring in shared memory
 // ---------------------------------------------------------------------------
-constexpr int RW = 16;            // working warps at the most; one more copies
+// warps of a block at the most, with E features a thread (by their registers)
+constexpr int ring_warps(int E) { return E == 8 ? 16 : 12; }
+constexpr int RW = ring_warps(8);
 constexpr int RING = 6;           // tiles of the ring at the most
-constexpr int RE = 8, RH = RE / 2;   // features a thread, pairs of them
-constexpr int kRingWidth = 32 * RW * RE;
+constexpr int kRingWidth = 32 * RW * 8;
 constexpr size_t kRingBytes = 216 * 1024;
 
 // shared memory of a block: ring tiles, then vectors, then the join of the sums
@@ -418,18 +420,19 @@ __device__ __forceinline__ Place place_of(const NormArgs& a, int u, int rows) {
   return {b, (u - b * a.tiles) * rows};
 }
 
-// The copying thread: tile by tile, the tensors that are there and the rows' statistics.
-__device__ __forceinline__ void ring_fill(const NormArgs& a, const RingShape& s, int u0, int u1, uint32_t sm,
-                                          uint64_t* full, uint64_t* empty, int es, int* err) {
-  const void* src[4] = {a.x, a.u, a.dh, a.dy};
+// What one thread copies: tile by tile, the tensors that are there and the rows' statistics.
+struct Fill {
   int st = 0, issued = 0;
   uint32_t ph = 0;
-  Place at_tile = place_of(a, u0, s.rows);
-  for (int u = u0; u < u1; ++u, at_tile.next(a, s.rows)) {
-    const int b = at_tile.b, n = at_tile.n, rows = min(s.rows, a.N - n);
-    if (!wtc::wait_or_flag(err, tc::smem_u32(&empty[st]), ph ^ 1u)) break;
+  Place at;
+  // one tile into the next slot, once all warps are done with what was there
+  __device__ __forceinline__ bool tile(const NormArgs& a, const RingShape& s, uint32_t sm, uint64_t* full,
+                                       uint64_t* empty, int es, int* err) {
+    const void* src[4] = {a.x, a.u, a.dh, a.dy};
+    if (!wtc::wait_or_flag(err, tc::smem_u32(&empty[st]), ph ^ 1u)) return false;
+    const int rows = min(s.rows, a.N - at.n);
     const uint32_t bar = tc::smem_u32(&full[st]), base = sm + st * s.tile;
-    const size_t row = (size_t)b * a.N + n, at = row * a.C * es;
+    const size_t row = (size_t)at.b * a.N + at.n, first = row * a.C * es;
     const uint32_t bytes = (uint32_t)rows * a.C * es;
     uint32_t all = rows * 16u;
 #pragma unroll
@@ -437,26 +440,24 @@ __device__ __forceinline__ void ring_fill(const NormArgs& a, const RingShape& s,
     tc::mbar_expect_tx(bar, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (src[i]) tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + at, bytes, bar);
+      if (src[i]) tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + first, bytes, bar);
     tc::bulk_g2s(base + 4 * s.tensor, a.stats + row * 4, rows * 16u, bar);
+    at.next(a, s.rows);
     ++issued;
     if (++st == s.nst) { st = 0; ph ^= 1u; }
+    return true;
   }
-  // no copy is in flight when the block ends
-  for (int i = 0; i < s.nst && i < issued; ++i) {
-    const int k = issued - 1 - i;
-    wtc::wait_or_flag(err, tc::smem_u32(&full[k % s.nst]), (uint32_t)(k / s.nst) & 1u);
-  }
-}
+};
 
 // FULL: the warps' features are the row's, none behind it
-template <typename T, bool FULL>
-__global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
-  constexpr int V = 16 / (int)sizeof(T), NP = RE / V;   // features of a piece, pieces a thread
+template <typename T, int E, bool FULL>
+__global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
+  constexpr int V = 16 / (int)sizeof(T), NP = E / V;    // features of a piece, pieces a thread
+  constexpr int RH = E / 2;                             // pairs of features
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[RW][64];
   __shared__ __align__(8) uint64_t full[RING], empty[RING];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, workers = s.warps * s.rows;
+  const int warp = threadIdx.x >> 5, workers = s.warps * s.rows;
   const uint32_t sm = tc::smem_u32(smem);
   if (threadIdx.x == 0)
     for (int i = 0; i < s.nst; ++i) {
@@ -467,15 +468,20 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
   __syncthreads();
   const long long units = (long long)a.B * a.tiles;
   const int u0 = (int)(units * blockIdx.x / a.grid), u1 = (int)(units * (blockIdx.x + 1) / a.grid);
-  if (warp == workers) {
-    if (lane == 0) ring_fill(a, s, u0, u1, sm, full, empty, sizeof(T), err);
-    return;
-  }
   const int group = warp / s.warps, threads = 32 * s.warps, workerst = 32 * workers;
+  // thread 0 copies: all slots at first, then one a tile, that of `lag` tiles ago, so that it
+  // need not wait for the slowest warp
+  Fill fill;
+  fill.at = place_of(a, u0, s.rows);
+  bool late = false;
+  const int lag = s.nst > 3 ? 2 : 1;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < s.nst && u0 + i < u1; ++i) late = late || !fill.tile(a, s, sm, full, empty, sizeof(T), err);
+  __syncwarp();
   const int t = threadIdx.x - group * threads;
   RowSum sum{slots[group], s.warps, group, threads};
   auto col = [&](int j) { return (j * threads + t) * V; };      // of piece j
-  auto sync = [&]() { asm volatile("barrier.sync 0, %0;" ::"r"(workerst) : "memory"); };
+  auto sync = [&]() { __syncthreads(); };
   const float inv = 1.f / (float)a.C;
 
   // Vectors: weight, m post_weight, m post_bias in fp32, quarters of pieces side by side.
@@ -602,10 +608,12 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
 
   int st = 0, cur = -1;
   uint32_t ph = 0;
-  bool late = false;
   Place here = place_of(a, u0, s.rows);
   for (int u = u0; u < u1; ++u, here.next(a, s.rows)) {
     const int b = here.b, n = here.n + group;
+    if (threadIdx.x == 0 && u - u0 >= lag && u - lag + s.nst < u1)
+      late = late || !fill.tile(a, s, sm, full, empty, sizeof(T), err);
+    __syncwarp();
     if (b != cur) {
       if (cur >= 0 && a.sums) flush(cur);
       clear();
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
     }
     // after an expired wait (the error word is set) no other is waited for: every warp goes
     // on to its end, since the sums and the barriers need all
-    late = late || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
+    late = __any_sync(0xffffffffu, late) || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
     if (n < a.N) {
       const size_t row = (size_t)b * a.N + n;
       const uint32_t tile = sm + st * s.tile;
@@ -694,6 +702,12 @@ __global__ void __launch_bounds__(32 * (RW + 1), 1) k_norm_bwd_ring(NormArgs a, 
     if (++st == s.nst) { st = 0; ph ^= 1u; }
   }
   if (cur >= 0 && a.sums) flush(cur);
+  // no copy is in flight when the block ends: all were waited for, but after an expired wait
+  if (threadIdx.x == 0 && late)
+    for (int i = 0; i < s.nst && i < fill.issued; ++i) {
+      const int k = fill.issued - 1 - i;
+      wtc::wait_or_flag(err, tc::smem_u32(&full[k % s.nst]), (uint32_t)(k / s.nst) & 1u);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1035,11 +1049,11 @@ int norm_parts(int B, int N, int C) {
   return (int)(p < 1 ? 1 : p);
 }
 
-// the ring's shape; nst 0: rows that do not go through it
-RingShape ring_shape(int C, int es) {
+// the ring's shape with E features a thread; nst 0: rows that do not go through it
+RingShape ring_shape(int C, int es, int E) {
   RingShape r;
-  r.warps = (C + 32 * RE - 1) / (32 * RE);
-  r.rows = r.warps <= RW ? RW / r.warps : 1;
+  r.warps = (C + 32 * E - 1) / (32 * E);
+  r.rows = r.warps <= ring_warps(E) ? ring_warps(E) / r.warps : 1;
   r.tensor = (uint32_t)(r.rows * C * es);
   r.tile = 4 * r.tensor + 16 * RW;
   const uint32_t vec = 3u * C * 4, join = r.rows > 1 ? 16u * C : 0u;
@@ -1051,7 +1065,7 @@ RingShape ring_shape(int C, int es) {
   return r;
 }
 
-template <typename T>
+template <typename T, int E>
 cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
@@ -1062,10 +1076,10 @@ cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
   const long long tiles = (long long)a.B * a.tiles;
   a.grid = (int)(tiles < 152 ? tiles : 152);
   static SmemOnce once[2];
-  const bool full = a.C == 32 * r.warps * RE;
-  auto* k = full ? k_norm_bwd_ring<T, true> : k_norm_bwd_ring<T, false>;
+  const bool full = a.C == 32 * r.warps * E;
+  auto* k = full ? k_norm_bwd_ring<T, E, true> : k_norm_bwd_ring<T, E, false>;
   if ((e = once[full].allow(k, kRingBytes, dev)) != cudaSuccess) return e;
-  return launch("norm_bwd", k, dim3(a.grid), dim3(32 * (r.warps * r.rows + 1)), r.total, st, a, r, err);
+  return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.warps * r.rows), r.total, st, a, r, err);
 }
 
 template <typename T, int E>
@@ -1096,8 +1110,12 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
                        a.h, a.y, a.dh, a.dy, a.dx, a.du};
   for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
   if (wide && backward) {
-    const RingShape r = ring_shape(a.C, sizeof(T));
-    if (r.nst > 0) return go_ring<T>(a, r, st);
+    const RingShape r = ring_shape(a.C, sizeof(T), 8), r16 = ring_shape(a.C, sizeof(T), 16);
+    // 16 features a thread where that works on a third more rows at once and leaves a ring of
+    // three tiles (bf16 rows of 512, 12 for 8: 173 us for 242; of 1536, 4 for 2: 199 for 306; of
+    // 640, 6 for 5: 334 for 322; fp32 rows of 512, two tiles: 146 for 139)
+    if (r16.nst > 2 && 3 * r16.rows >= 4 * r.rows) return go_ring<T, 16>(a, r16, st);
+    if (r.nst > 0) return go_ring<T, 8>(a, r, st);
   }
   if (wide && !backward && s.warps <= FW)
     return s.ept == 8 ? go_rows<T, 8>(a, s, st) : go_rows<T, 16>(a, s, st);
