@@ -124,29 +124,53 @@ struct RowSum {
   int warps, group, threads;
   int turn = 0;
   __device__ __forceinline__ float2 operator()(float2 v) {
+    if (warps == 1) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      }
+      return v;
     }
-    return warps == 1 ? v : over_warps(v);
+    // a half of the warp each
+    const bool upper = threadIdx.x & 16;
+    float t = upper ? v.y : v.x;
+    t += __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    float* s = reinterpret_cast<float*>(slot + 32 * turn) + (upper ? 1 : 0);
+    turn ^= 1;      // the other half is free again after the next barrier
+    const int w = (threadIdx.x >> 5) % warps, i = threadIdx.x & 15;
+    if (i == 0) s[2 * w] = t;
+    asm volatile("barrier.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    if (warps <= 4) {
+      t = s[0];
+      for (int j = 1; j < warps; ++j) t += s[2 * j];
+    } else {
+      t = i < warps ? s[2 * i] : 0.f;
+      if (i + 16 < warps) t += s[2 * i + 32];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    const float z = __shfl_xor_sync(0xffffffffu, t, 16);
+    return upper ? make_float2(z, t) : make_float2(t, z);
   }
   __device__ __forceinline__ float operator()(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return warps == 1 ? v : over_warps(make_float2(v, 0.f)).x;
-  }
-  __device__ __forceinline__ float2 over_warps(float2 v) {
-    float2* s = slot + 32 * turn;
-    turn ^= 1;      // the other half is free again after the next barrier
-    const int w = (threadIdx.x >> 5) % warps;
-    if ((threadIdx.x & 31) == 0) s[w] = v;
+    if (warps == 1) return v;
+    float* s = reinterpret_cast<float*>(slot + 32 * turn);
+    turn ^= 1;
+    const int w = (threadIdx.x >> 5) % warps, i = threadIdx.x & 31;
+    if (i == 0) s[w] = v;
     asm volatile("barrier.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-    v = s[0];
-    for (int i = 1; i < warps; ++i) {
-      const float2 y = s[i];
-      v.x += y.x;
-      v.y += y.y;
+    if (warps <= 4) {
+      v = s[0];
+      for (int j = 1; j < warps; ++j) v += s[j];
+    } else {
+      v = i < warps ? s[i] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     return v;
   }
