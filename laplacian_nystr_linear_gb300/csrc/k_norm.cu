@@ -21,7 +21,7 @@
 // once (8 or 16 features a thread of sixteen or twelve warps), which one thread copies into a
 // ring in shared memory (bulk copies; a tile's rows lie side by side).  What a feature is
 // multiplied by is laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both
-// norms, gate and scale: 173 us, 4.7 TB/s: sums over a row are what a row waits for, so rows
+// norms, gate and scale: 152 us, 5.3 TB/s: sums over a row are what a row waits for, so rows
 // in flight and registers count (a warp of its own for the copies costs the registers of
 // four: eight warps of 16 features, or sixteen of 8, took 228); loads by the warps
 // themselves beside 255 registers a thread took 390.
@@ -582,34 +582,43 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
 #pragma unroll
       for (int i = 0; i < RH; ++i) A[k][i] = pack2(0.f, 0.f);
   };
-  // the sums of sequence b into this block's slot
+  // The sums of sequence b into this block's slot: half of a kind's pairs at a time side by
+  // side in shared memory, [group][pair][thread], and the groups' sums in order.
   auto flush = [&](int b) {
+    constexpr int HP = RH / 2;
     float* out = a.part + ((size_t)b + blockIdx.x) * 4 * a.C;
-    float* join = reinterpret_cast<float*>(smem + s.join);
-    for (int g = 0; g < s.rows; ++g) {
-      if (group == g)
+    float2* join = reinterpret_cast<float2*>(smem + s.join);
+    // pair i of thread t of a row
+    auto put = [&](int k, int i, int t, float2 v) {
+      const int c = ((2 * i / V) * threads + t) * V + 2 * i % V;
+      if (c < a.C) *reinterpret_cast<float2*>(out + k * a.C + c) = v;
+    };
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (a.sums >> k & 1)
+    for (int k = 0; k < 4; ++k) {
+      if (!(a.sums >> k & 1)) continue;
+      if (s.rows == 1) {
 #pragma unroll
-            for (int i = 0; i < RH; ++i) {
-              const int c = col(2 * i / V) + 2 * i % V;
-              if (c >= a.C) continue;
-              float2 v = unpack2(A[k][i]);
-              float2* o = reinterpret_cast<float2*>((s.rows > 1 ? join : out) + k * a.C + c);
-              if (g > 0) {
-                const float2 p = *o;
-                v.x += p.x;
-                v.y += p.y;
-              }
-              *o = v;
-            }
-      if (s.rows > 1) sync();
-    }
-    if (s.rows > 1) {
-      for (int c = threadIdx.x; c < 4 * a.C; c += workerst)
-        if (a.sums >> (c / a.C) & 1) out[c] = join[c];
-      sync();
+        for (int i = 0; i < RH; ++i) put(k, i, t, unpack2(A[k][i]));
+        continue;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < HP; ++i) join[(group * HP + i) * threads + t] = unpack2(A[k][h * HP + i]);
+        sync();
+#pragma unroll 1
+        for (int e = threadIdx.x; e < HP * threads; e += workerst) {
+          float2 v = join[e];
+#pragma unroll 4
+          for (int g = 1; g < s.rows; ++g) {
+            const float2 y = join[g * HP * threads + e];
+            v.x += y.x;
+            v.y += y.y;
+          }
+          put(k, h * HP + e / threads, e % threads, v);
+        }
+        sync();
+      }
     }
   };
   // z becomes (z - mean) / deviation
@@ -952,32 +961,35 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
 
 constexpr int JY = 32;   // threads that share a column of the joins
 
-// seq[b][k][c] = sum over a sequence's slots: slot y, y + 32, .. by thread y, then the
-// threads' sums in order
-__global__ void __launch_bounds__(32 * JY) k_norm_seq(NormArgs a) {
+// seq[b][k][c] = sum over a sequence's slots: `share` threads to a sequence, every one's
+// slots, then the threads' sums in order; JY / share sequences a block
+__global__ void __launch_bounds__(32 * JY) k_norm_seq(NormArgs a, int share) {
   __shared__ float s[JY][33];
   const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
   if (!(a.sums >> k & 1)) return;
-  for (long long b = blockIdx.z; b < a.B; b += gridDim.z) {
-    size_t p0 = (size_t)b * a.parts, p1 = p0 + a.parts;
-    if (a.grid > 0) {
-      // block of tile u: the greatest c with tiles c / grid <= u
-      const long long units = (long long)a.B * a.tiles, first = b * a.tiles;
-      p0 = b + ((first + 1) * a.grid - 1) / units;
-      p1 = b + ((first + a.tiles) * a.grid - 1) / units + 1;
-    }
+  const int y = threadIdx.y % share, some = JY / share;
+  for (long long b0 = (long long)blockIdx.z * some; b0 < a.B; b0 += (long long)gridDim.z * some) {
+    const long long b = b0 + threadIdx.y / share;
     float t = 0.f;
-    if (c < a.C)
+    if (c < a.C && b < a.B) {
+      size_t p0 = (size_t)b * a.parts, p1 = p0 + a.parts;
+      if (a.grid > 0) {
+        // block of tile u: the greatest c with tiles c / grid <= u
+        const long long units = (long long)a.B * a.tiles, first = b * a.tiles;
+        p0 = b + ((first + 1) * a.grid - 1) / units;
+        p1 = b + ((first + a.tiles) * a.grid - 1) / units + 1;
+      }
 #pragma unroll 4
-      for (size_t p = p0 + threadIdx.y; p < p1; p += JY) t += a.part[(p * 4 + k) * a.C + c];
-    __syncthreads();
-    s[threadIdx.y][threadIdx.x] = t;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < a.C) {
-#pragma unroll
-      for (int y = 1; y < JY; ++y) t += s[y][threadIdx.x];
-      a.seq[((size_t)b * 4 + k) * a.C + c] = t;
+      for (size_t p = p0 + y; p < p1; p += share) t += a.part[(p * 4 + k) * a.C + c];
     }
+    if (share > 1) {
+      __syncthreads();
+      s[threadIdx.y][threadIdx.x] = t;
+      __syncthreads();
+      if (y == 0)
+        for (int i = 1; i < share; ++i) t += s[threadIdx.y + i][threadIdx.x];
+    }
+    if (y == 0 && c < a.C && b < a.B) a.seq[((size_t)b * 4 + k) * a.C + c] = t;
   }
 }
 
@@ -1080,7 +1092,7 @@ RingShape ring_shape(int C, int es, int E) {
   r.rows = r.warps <= ring_warps(E) ? ring_warps(E) / r.warps : 1;
   r.tensor = (uint32_t)(r.rows * C * es);
   r.tile = 4 * r.tensor + 16 * RW;
-  const uint32_t vec = 3u * C * 4, join = r.rows > 1 ? 16u * C : 0u;
+  const uint32_t vec = 3u * C * 4, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
   const size_t n = vec + join < kRingBytes ? (kRingBytes - vec - join) / r.tile : 0;
   r.nst = C > kRingWidth || n < 2 ? 0 : (int)(n < RING ? n : RING);
   r.vec = r.nst * r.tile;
@@ -1168,8 +1180,14 @@ cudaError_t run_norm_bwd(NormArgs& a, bool bf16, cudaStream_t st) {
   if (a.grid == 0 && a.parts == 1) {
     f.seq = a.part;
   } else {
-    e = launch("norm_seq", k_norm_seq, dim3(cols, 4, (unsigned)(a.B < 65535 ? a.B : 65535)),
-               dim3(32, JY), 0, st, a);
+    // about four slots a thread (4096 sequences of a slot or two each: 76 us, 1560 with 32
+    // threads to each)
+    const long long slots = a.grid > 0 ? (a.grid + a.B - 1) / a.B + 1 : a.parts;
+    int share = 1;
+    while (share < JY && 4 * share < slots) share *= 2;
+    const long long blocks = (a.B + JY / share - 1) / (JY / share);
+    e = launch("norm_seq", k_norm_seq, dim3(cols, 4, (unsigned)(blocks < 65535 ? blocks : 65535)),
+               dim3(32, JY), 0, st, a, share);
     if (e != cudaSuccess) return e;
   }
   if (bf16) return launch("norm_final", k_norm_final<__nv_bfloat16>, dim3(cols), dim3(32, JY), 0, st, f);
