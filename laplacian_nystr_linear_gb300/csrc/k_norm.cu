@@ -16,7 +16,7 @@
 // again from x and u in the backward, which reads as much as h would and has no rounding
 // in it.  Statistics are of centred values, in fp32.
 //
-// Backward, rows of whole 16-byte pieces, up to 4096 features (k_norm_bwd_ring): a block
+// Backward, up to 4096 features (k_norm_bwd_ring): a block
 // an SM takes an even stretch of all rows, in tiles of as many rows as its warps work on at
 // once (8 or 16 features a thread of sixteen or twelve warps), which one thread copies into a
 // ring in shared memory (bulk copies; a tile's rows lie side by side).  What a feature is
@@ -24,15 +24,18 @@
 // norms, gate and scale: 152 us, 5.3 TB/s: sums over a row are what a row waits for, so rows
 // in flight and registers count (a warp of its own for the copies costs the registers of
 // four: eight warps of 16 features, or sixteen of 8, took 228); loads by the warps
-// themselves beside 255 registers a thread took 390.
+// themselves beside 255 registers a thread took 390.  Rows that are no whole 16 bytes lie in
+// the ring as they lie in memory and are read from it by pairs or single elements: 1001
+// features, 517 us for 847 of the loads by the threads; 514, 461 for 1425 (2^27 bytes a tensor).
 //
 // Forward, such rows (k_norm_fwd_rows): threads copy their own pieces two rows ahead
 // (cp.async), two blocks an SM: 98 us for the same rows, 5.5 TB/s; 32768 rows of 4096, two
 // norms: 204 us, 5.3 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
 // the row ahead: 243.)
 //
-// Other rows (single elements, more features): k_norm_fwd, k_norm_bwd, loads by the threads
-// as they are needed.
+// Other rows (forward: no whole pieces, more than 4096 features; backward: more than 4096, or
+// tensors that start anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are
+// needed.
 //
 // The backward's sums over rows stay in registers, are joined over a block's row groups
 // in shared memory and over the blocks by k_norm_seq, in one order.
@@ -416,12 +419,26 @@ constexpr size_t kRingBytes = 216 * 1024;
 struct RingShape {
   int warps, rows, nst;           // warps of a row, rows of a tile, tiles of the ring
   uint32_t tensor, tile;          // bytes of a tensor's share of a tile, of a tile
+  uint32_t tail;                  // bytes of a tensor behind its last whole 16
   uint32_t vec, join, total;      // bytes: where the vectors and the join start, and in all
 };
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+// two or four bytes
+template <int BYTES>
+__device__ __forceinline__ uint32_t lds_piece(uint32_t addr) {
+  uint32_t v;
+  if constexpr (BYTES == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
+    v = h;
+  }
   return v;
 }
 __device__ __forceinline__ f32x2 pair_of(uint32_t x, uint32_t y) {
@@ -444,7 +461,14 @@ __device__ __forceinline__ Place place_of(const NormArgs& a, int u, int rows) {
   return {b, (u - b * a.tiles) * rows};
 }
 
+// bytes before a tile's first row in its share of the ring: copies start at whole 16 bytes
+__device__ __forceinline__ uint32_t ring_skip(const NormArgs& a, const Place& p, uint32_t es) {
+  return ((uint32_t)p.b * (uint32_t)a.N + (uint32_t)p.n) * (uint32_t)a.C * es & 15u;
+}
+
 // What one thread copies: tile by tile, the tensors that are there and the rows' statistics.
+// Rows that are no whole 16 bytes: with what lies around them, as far as the tensor goes; the
+// last bytes of a tensor one by one.
 struct Fill {
   int st = 0, issued = 0;
   uint32_t ph = 0;
@@ -457,14 +481,26 @@ struct Fill {
     const int rows = min(s.rows, a.N - at.n);
     const uint32_t bar = tc::smem_u32(&full[st]), base = sm + st * s.tile;
     const size_t row = (size_t)at.b * a.N + at.n, first = row * a.C * es;
-    const uint32_t bytes = (uint32_t)rows * a.C * es;
+    const uint32_t skip = (uint32_t)first & 15u;
+    uint32_t bytes = (skip + (uint32_t)rows * a.C * es + 15u) & ~15u;
+    if (first - skip + bytes > (size_t)a.B * a.N * a.C * es) {
+      bytes -= 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (src[i])
+          for (uint32_t o = 0; o < s.tail; o += 2) {
+            const uint16_t v = *reinterpret_cast<const uint16_t*>((const uint8_t*)src[i] + first - skip + bytes + o);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + i * s.tensor + bytes + o), "h"(v) : "memory");
+          }
+    }
     uint32_t all = rows * 16u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) all += src[i] ? bytes : 0u;
     tc::mbar_expect_tx(bar, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (src[i]) tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + first, bytes, bar);
+      if (src[i] && bytes > 0)
+        tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + first - skip, bytes, bar);
     tc::bulk_g2s(base + 4 * s.tensor, a.stats + row * 4, rows * 16u, bar);
     at.next(a, s.rows);
     ++issued;
@@ -473,10 +509,11 @@ struct Fill {
   }
 };
 
-// FULL: the warps' features are the row's, none behind it
-template <typename T, int E, bool FULL>
+// V: features of a piece; FULL: the warps' features are the row's, none behind it
+template <typename T, int V, int E, bool FULL>
 __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
-  constexpr int V = 16 / (int)sizeof(T), NP = E / V;    // features of a piece, pieces a thread
+  constexpr int NP = E / V;                             // pieces a thread
+  constexpr bool WHOLE = V * sizeof(T) == 16;           // rows of whole 16 bytes
   constexpr int RH = E / 2;                             // pairs of features
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[RW][64];
@@ -516,7 +553,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     sync();                                           // nobody reads the last one's
     const size_t seq = (size_t)b * a.C;
     for (int c = threadIdx.x; c < a.C; c += workerst) {
-      const int piece = c / V, i = c % V, at = ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
+      const int piece = c / V, i = c % V, at = V < 4 ? c : ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
       float m = 1.f;
       if (a.gate) m *= as_f(((const T*)a.gate)[seq + c]);
       if (a.scale) m *= as_f(((const T*)a.scale)[c]);
@@ -527,31 +564,64 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     sync();
   };
   auto vec = [&](uint32_t base, f32x2(&p)[RH]) {
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
+      for (int j = 0; j < NP; ++j)
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        uint4 f = make_uint4(0, 0, 0, 0);
-        if (FULL || col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
-        p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
-        p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
+        for (int i = 0; i < V / 4; ++i) {
+          uint4 f = make_uint4(0, 0, 0, 0);
+          if (FULL || col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
+          p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
+          p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
+        }
+    } else if constexpr (V == 2) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float2 f = col(j) < a.C ? *reinterpret_cast<const float2*>(smem + base + 4 * col(j)) : make_float2(0.f, 0.f);
+        p[j] = pack2(f.x, f.y);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; j += 2) {
+        const float* f = reinterpret_cast<const float*>(smem + base);
+        p[j / 2] = pack2(col(j) < a.C ? f[col(j)] : 0.f, col(j + 1) < a.C ? f[col(j + 1)] : 0.f);
+      }
+    }
   };
   // this thread's share of a tensor's row in the tile at `tile`
-  const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + 16 * t;
+  const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + V * sizeof(T) * t;
   auto share = [&](uint32_t tile, int tensor, f32x2(&p)[RH]) {
+    const uint32_t at = tile + tensor * s.tensor + row_at;
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      uint4 f = make_uint4(0, 0, 0, 0);
-      if (FULL || col(j) < a.C) f = lds16(tile + tensor * s.tensor + row_at + 16 * j * threads);
-      if constexpr (V == 4) {
-        p[2 * j] = pair_of(f.x, f.y);
-        p[2 * j + 1] = pair_of(f.z, f.w);
-      } else {
-        p[4 * j] = pair_of(f.x << 16, f.x & 0xffff0000u);
-        p[4 * j + 1] = pair_of(f.y << 16, f.y & 0xffff0000u);
-        p[4 * j + 2] = pair_of(f.z << 16, f.z & 0xffff0000u);
-        p[4 * j + 3] = pair_of(f.w << 16, f.w & 0xffff0000u);
+      for (int j = 0; j < NP; ++j) {
+        uint4 f = make_uint4(0, 0, 0, 0);
+        if (FULL || col(j) < a.C) f = lds16(at + 16 * j * threads);
+        if constexpr (V == 4) {
+          p[2 * j] = pair_of(f.x, f.y);
+          p[2 * j + 1] = pair_of(f.z, f.w);
+        } else {
+          p[4 * j] = pair_of(f.x << 16, f.x & 0xffff0000u);
+          p[4 * j + 1] = pair_of(f.y << 16, f.y & 0xffff0000u);
+          p[4 * j + 2] = pair_of(f.z << 16, f.z & 0xffff0000u);
+          p[4 * j + 3] = pair_of(f.w << 16, f.w & 0xffff0000u);
+        }
+      }
+    } else {
+      uint32_t f[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        f[j] = 0;
+        if (col(j) < a.C) f[j] = lds_piece<V * sizeof(T)>(at + V * (uint32_t)sizeof(T) * j * threads);
+      }
+#pragma unroll
+      for (int i = 0; i < RH; ++i) {
+        if constexpr (V == 2)
+          p[i] = pair_of(f[i] << 16, f[i] & 0xffff0000u);
+        else if constexpr (sizeof(T) == 2)
+          p[i] = pair_of(f[2 * i] << 16, f[2 * i + 1] << 16);
+        else
+          p[i] = pair_of(f[2 * i], f[2 * i + 1]);
       }
     }
   };
@@ -560,7 +630,13 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       if (!FULL && col(j) >= a.C) continue;
-      if constexpr (V == 4) {
+      if constexpr (V == 1) {
+        const float2 x = unpack2(p[j / 2]);
+        from_f(o + col(j), j & 1 ? x.y : x.x);
+      } else if constexpr (V == 2) {
+        const float2 x = unpack2(p[j]);
+        *reinterpret_cast<uint32_t*>(o + col(j)) = wtc::pack(x.x, x.y);
+      } else if constexpr (V == 4) {
         const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
         *reinterpret_cast<float4*>(o + col(j)) = make_float4(x.x, x.y, y.x, y.y);
       } else {
@@ -591,7 +667,12 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     // pair i of thread t of a row
     auto put = [&](int k, int i, int t, float2 v) {
       const int c = ((2 * i / V) * threads + t) * V + 2 * i % V;
-      if (c < a.C) *reinterpret_cast<float2*>(out + k * a.C + c) = v;
+      if constexpr (V == 1) {
+        if (c < a.C) out[k * a.C + c] = v.x;
+        if (c + threads < a.C) out[k * a.C + c + threads] = v.y;
+      } else {
+        if (c < a.C) *reinterpret_cast<float2*>(out + k * a.C + c) = v;
+      }
     };
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -658,8 +739,8 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     late = __any_sync(0xffffffffu, late) || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
     if (n < a.N) {
       const size_t row = (size_t)b * a.N + n;
-      const uint32_t tile = sm + st * s.tile;
-      const uint4 qw = lds16(tile + 4 * s.tensor + 16 * group);
+      const uint32_t tile = sm + st * s.tile + (WHOLE ? 0u : ring_skip(a, here, sizeof(T)));
+      const uint4 qw = lds16(sm + st * s.tile + 4 * s.tensor + 16 * group);
       const float mu = __uint_as_float(qw.x), ru = __uint_as_float(qw.y), mh = __uint_as_float(qw.z),
                   rh = __uint_as_float(qw.w);
       f32x2 uh[RH], d[RH], v[RH];
@@ -1090,9 +1171,11 @@ RingShape ring_shape(int C, int es, int E) {
   RingShape r;
   r.warps = (C + 32 * E - 1) / (32 * E);
   r.rows = r.warps <= ring_warps(E) ? ring_warps(E) / r.warps : 1;
-  r.tensor = (uint32_t)(r.rows * C * es);
+  // rows that are no whole 16 bytes: with up to 15 bytes before and behind
+  r.tensor = (uint32_t)((r.rows * C * es + (C * es % 16 ? 30 : 0) + 15) & ~15);
   r.tile = 4 * r.tensor + 16 * RW;
-  const uint32_t vec = 3u * C * 4, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
+  r.tail = 0;
+  const uint32_t vec = (12u * C + 15) & ~15u, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
   const size_t n = vec + join < kRingBytes ? (kRingBytes - vec - join) / r.tile : 0;
   r.nst = C > kRingWidth || n < 2 ? 0 : (int)(n < RING ? n : RING);
   r.vec = r.nst * r.tile;
@@ -1101,8 +1184,8 @@ RingShape ring_shape(int C, int es, int E) {
   return r;
 }
 
-template <typename T, int E>
-cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
+template <typename T, int V, int E>
+cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
@@ -1112,8 +1195,10 @@ cudaError_t go_ring(NormArgs& a, const RingShape& r, cudaStream_t st) {
   const long long tiles = (long long)a.B * a.tiles;
   a.grid = (int)(tiles < 152 ? tiles : 152);
   static SmemOnce once[2];
-  const bool full = a.C == 32 * r.warps * E;
-  auto* k = full ? k_norm_bwd_ring<T, E, true> : k_norm_bwd_ring<T, E, false>;
+  r.tail = (uint32_t)((size_t)a.B * a.N * a.C * sizeof(T) % 16);
+  constexpr bool WHOLE = V * sizeof(T) == 16;
+  const bool full = WHOLE && a.C == 32 * r.warps * E;
+  auto* k = full ? k_norm_bwd_ring<T, V, E, WHOLE> : k_norm_bwd_ring<T, V, E, false>;
   if ((e = once[full].allow(k, kRingBytes, dev)) != cudaSuccess) return e;
   return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.warps * r.rows), r.total, st, a, r, err);
 }
@@ -1145,13 +1230,22 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
   const void* all[] = {a.x, a.u, a.weight, a.bias, a.post_weight, a.post_bias, a.gate, a.scale,
                        a.h, a.y, a.dh, a.dy, a.dx, a.du};
   for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
-  if (wide && backward) {
+  auto al = [](const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; };
+  if (backward && al(a.x, 16) && al(a.u, 16) && al(a.dh, 16) && al(a.dy, 16)) {
     const RingShape r = ring_shape(a.C, sizeof(T), 8), r16 = ring_shape(a.C, sizeof(T), 16);
     // 16 features a thread where that works on a third more rows at once and leaves a ring of
     // three tiles (bf16 rows of 512, 12 for 8: 173 us for 242; of 1536, 4 for 2: 199 for 306; of
     // 640, 6 for 5: 334 for 322; fp32 rows of 512, two tiles: 146 for 139)
-    if (r16.nst > 2 && 3 * r16.rows >= 4 * r.rows) return go_ring<T, 16>(a, r16, st);
-    if (r.nst > 0) return go_ring<T, 8>(a, r, st);
+    const bool more = r16.nst > 2 && 3 * r16.rows >= 4 * r.rows;
+    constexpr int V = 16 / (int)sizeof(T);
+    if (r.nst > 0) {
+      if (a.C % V == 0 && al(a.dx, 16) && al(a.du, 16))
+        return more ? go_ring<T, V, 16>(a, r16, st) : go_ring<T, V, 8>(a, r, st);
+      if constexpr (sizeof(T) == 2)
+        if (a.C % 2 == 0 && al(a.dx, 4) && al(a.du, 4))
+          return more ? go_ring<T, 2, 16>(a, r16, st) : go_ring<T, 2, 8>(a, r, st);
+      return more ? go_ring<T, 1, 16>(a, r16, st) : go_ring<T, 1, 8>(a, r, st);
+    }
   }
   if (wide && !backward && s.warps <= FW)
     return s.ept == 8 ? go_rows<T, 8>(a, s, st) : go_rows<T, 16>(a, s, st);

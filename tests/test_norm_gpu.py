@@ -213,3 +213,30 @@ def test_captured_step():
     g.replay()
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,N,C", [(1, 3, 1), (3, 5, 1), (2, 7, 3), (1, 17, 5), (3, 33, 7), (5, 16, 2), (1, 129, 9),
+                                   (2, 100, 33), (4, 37, 514), (2, 301, 321), (1, 29, 1001), (2, 13, 2047), (3, 9, 4095),
+                                   (2, 700, 258), (1, 2000, 301)])
+def test_rows_that_are_no_whole_pieces(dtype, B, N, C):
+    """Rows that start anywhere in 16 bytes, tensors that end anywhere; guard rows behind the inputs hold NaN,
+    which no sum may meet; the gradients of inputs that start at an odd element agree within the same bounds."""
+    t = _inputs(B, N, C, dtype, B + N + C, ALL)
+    dh, dy = torch.randn_like(t["x"]), torch.randn_like(t["x"])
+    ref = _reference(t, "layer", "layer", 1e-6, dh, dy)
+    p = lap.NormParams(B, N, C, False, "layer", "layer", 1e-6)
+    vec = {n: t[n] for n in ("post_weight", "post_bias", "gate", "scale")}
+    for off in (0, 1):
+        def put(v):
+            buf = torch.full((v.numel() + off + 64,), float("nan"), dtype=dtype, device="cuda")
+            moved = buf[off:off + v.numel()].view(v.shape)
+            moved.copy_(v)
+            return moved
+
+        x, u, gh, gy = (put(v) for v in (t["x"], t["u"], dh, dy))
+        h, y, st = lap.norm_fwd(x, u, t["weight"], t["bias"], p, **vec)
+        check("h", h, ref["h"], dtype)
+        check("y", y, ref["y"], dtype)
+        for n, g in zip(NAMES, lap.norm_bwd(x, u, t["weight"], st, gh, gy, p, **vec)):
+            check("d" + n, g, ref[n], dtype)
