@@ -26,16 +26,15 @@
 // four: eight warps of 16 features, or sixteen of 8, took 228); loads by the warps
 // themselves beside 255 registers a thread took 390.  Rows that are no whole 16 bytes lie in
 // the ring as they lie in memory and are read from it by pairs or single elements: 1001
-// features, 517 us for 847 of the loads by the threads; 514, 461 for 1425 (2^27 bytes a tensor).
+// features, 400 us for 847 of the loads by the threads; 514, 449 for 1425 (2^27 bytes a tensor).
 //
-// Forward, such rows (k_norm_fwd_rows): threads copy their own pieces two rows ahead
-// (cp.async), two blocks an SM: 98 us for the same rows, 5.5 TB/s; 32768 rows of 4096, two
-// norms: 204 us, 5.3 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
+// Forward, rows of whole 16 bytes (bf16: or 4), up to 4096 features (k_norm_fwd_rows): threads
+// copy their own pieces two rows ahead (cp.async), two blocks an SM: 98 us for the same rows,
+// 5.5 TB/s; 32768 rows of 4096, two norms: 204 us, 5.3 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
 // the row ahead: 243.)
 //
-// Other rows (forward: no whole pieces, more than 4096 features; backward: more than 4096, or
-// tensors that start anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are
-// needed.
+// Other rows (more features, forward of single elements, backward of tensors that start
+// anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are needed.
 //
 // The backward's sums over rows stay in registers, are joined over a block's row groups
 // in shared memory and over the blocks by k_norm_seq, in one order.
@@ -441,9 +440,115 @@ __device__ __forceinline__ uint32_t lds_piece(uint32_t addr) {
   }
   return v;
 }
+// 16 or 4 bytes to shared memory, zeros where `in` is not set
+template <int BYTES>
+__device__ __forceinline__ void cp_async_piece(uint32_t dst, const void* src, bool in) {
+  if constexpr (BYTES == 16)
+    cp_async16(dst, src, in);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ f32x2 pair_of(uint32_t x, uint32_t y) {
   return pack2(__uint_as_float(x), __uint_as_float(y));
 }
+
+// The E features of a thread's share of a row, as pairs: pieces of V, `threads` pieces apart.
+// FULL: the threads' features are the row's, none behind it.
+template <typename T, int V, int E, bool FULL>
+struct Pairs {
+  static constexpr int NP = E / V, H = E / 2, B = V * (int)sizeof(T);   // pieces, pairs, bytes of a piece
+  static constexpr bool WHOLE = B == 16;
+  int t, threads, C;
+  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * V; }
+  __device__ __forceinline__ bool in(int j) const { return FULL || col(j) < C; }
+  // pieces in shared memory, the first at `at`, others `apart` bytes on; zeros behind the row
+  __device__ __forceinline__ void load(uint32_t at, uint32_t apart, f32x2 (&p)[H]) const {
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        uint4 f = make_uint4(0, 0, 0, 0);
+        if (in(j)) f = lds16(at + j * apart);
+        if constexpr (V == 4) {
+          p[2 * j] = pair_of(f.x, f.y);
+          p[2 * j + 1] = pair_of(f.z, f.w);
+        } else {
+          const uint32_t x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[4 * j + i] = pair_of(x[i] << 16, x[i] & 0xffff0000u);
+        }
+      }
+    } else {
+      uint32_t f[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        f[j] = 0;
+        if (in(j)) f[j] = lds_piece<B>(at + j * apart);
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        if constexpr (V == 2)
+          p[i] = pair_of(f[i] << 16, f[i] & 0xffff0000u);
+        else if constexpr (sizeof(T) == 2)
+          p[i] = pair_of(f[2 * i] << 16, f[2 * i + 1] << 16);
+        else
+          p[i] = pair_of(f[2 * i], f[2 * i + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* o, const f32x2 (&p)[H]) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if (!in(j)) continue;
+      if constexpr (V == 1) {
+        const float2 x = unpack2(p[j / 2]);
+        from_f(o + col(j), j & 1 ? x.y : x.x);
+      } else if constexpr (V == 2) {
+        const float2 x = unpack2(p[j]);
+        *reinterpret_cast<uint32_t*>(o + col(j)) = wtc::pack(x.x, x.y);
+      } else if constexpr (V == 4) {
+        const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
+        *reinterpret_cast<float4*>(o + col(j)) = make_float4(x.x, x.y, y.x, y.y);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2(p[4 * j + i]);
+          w[i] = wtc::pack(x.x, x.y);
+        }
+        *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  // A vector in shared memory, fp32: quarters of whole pieces side by side, others in order.
+  // Where feature c of it lies:
+  __device__ __forceinline__ int place(int c) const {
+    return WHOLE ? (c % V / 4 * (C / V) + c / V) * 4 + c % 4 : c;
+  }
+  __device__ __forceinline__ void vec(uint32_t base, f32x2 (&p)[H]) const {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if constexpr (WHOLE) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          uint4 f = make_uint4(0, 0, 0, 0);
+          if (in(j)) f = lds16(base + (i * (C / V) + j * threads + t) * 16);
+          p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
+          p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
+        }
+      } else {
+        uint32_t f[2] = {0, 0};
+        if (V == 2 && in(j)) {
+          f[0] = lds_piece<4>(base + 4 * col(j));
+          f[1] = lds_piece<4>(base + 4 * col(j) + 4);
+        } else if (V == 1 && j % 2 == 0) {
+          if (in(j)) f[0] = lds_piece<4>(base + 4 * col(j));
+          if (in(j + 1)) f[1] = lds_piece<4>(base + 4 * col(j + 1));
+        }
+        if (V == 2 || j % 2 == 0) p[V * j / 2] = pair_of(f[0], f[1]);
+      }
+    }
+  }
+};
 
 // sequence and first row of a tile, tile by tile
 struct Place {
@@ -467,31 +572,38 @@ __device__ __forceinline__ uint32_t ring_skip(const NormArgs& a, const Place& p,
 }
 
 // What one thread copies: tile by tile, the tensors that are there and the rows' statistics.
-// Rows that are no whole 16 bytes: with what lies around them, as far as the tensor goes; the
-// last bytes of a tensor one by one.
+// Rows that are no whole 16 bytes (WHOLE not set): with what lies around them, as far as the
+// tensor goes; the last bytes of a tensor one by one.  (It is on the way of every tile: six
+// 64-bit multiplications here took 4 % of the kernel.)
+template <bool WHOLE>
 struct Fill {
+  size_t row;                     // the next tile's first
+  int n;                          // its place in the sequence
   int st = 0, issued = 0;
   uint32_t ph = 0;
-  Place at;
+  __device__ __forceinline__ Fill(const NormArgs& a, const Place& at) : row((size_t)at.b * a.N + at.n), n(at.n) {}
   // one tile into the next slot, once all warps are done with what was there
   __device__ __forceinline__ bool tile(const NormArgs& a, const RingShape& s, uint32_t sm, uint64_t* full,
                                        uint64_t* empty, int es, int* err) {
     const void* src[4] = {a.x, a.u, a.dh, a.dy};
     if (!wtc::wait_or_flag(err, tc::smem_u32(&empty[st]), ph ^ 1u)) return false;
-    const int rows = min(s.rows, a.N - at.n);
+    const int rows = min(s.rows, a.N - n);
     const uint32_t bar = tc::smem_u32(&full[st]), base = sm + st * s.tile;
-    const size_t row = (size_t)at.b * a.N + at.n, first = row * a.C * es;
-    const uint32_t skip = (uint32_t)first & 15u;
-    uint32_t bytes = (skip + (uint32_t)rows * a.C * es + 15u) & ~15u;
-    if (first - skip + bytes > (size_t)a.B * a.N * a.C * es) {
-      bytes -= 16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (src[i])
-          for (uint32_t o = 0; o < s.tail; o += 2) {
-            const uint16_t v = *reinterpret_cast<const uint16_t*>((const uint8_t*)src[i] + first - skip + bytes + o);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + i * s.tensor + bytes + o), "h"(v) : "memory");
-          }
+    size_t first = row * (uint32_t)(a.C * es);
+    uint32_t bytes = (uint32_t)rows * a.C * es;
+    if constexpr (!WHOLE) {
+      const uint32_t skip = (uint32_t)first & 15u;
+      first -= skip;
+      bytes = (skip + bytes + 15u) & ~15u;
+      if (first + bytes > (size_t)a.B * a.N * a.C * es) {
+        bytes -= 16;
+        for (int i = 0; i < 4; ++i)
+          if (src[i])
+            for (uint32_t o = bytes; o < bytes + s.tail; o += 2) {
+              const uint16_t v = *reinterpret_cast<const uint16_t*>((const uint8_t*)src[i] + first + o);
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + i * s.tensor + o), "h"(v) : "memory");
+            }
+      }
     }
     uint32_t all = rows * 16u;
 #pragma unroll
@@ -499,22 +611,22 @@ struct Fill {
     tc::mbar_expect_tx(bar, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (src[i] && bytes > 0)
-        tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + first - skip, bytes, bar);
+      if (src[i] && (WHOLE || bytes > 0))
+        tc::bulk_g2s(base + i * s.tensor, (const uint8_t*)src[i] + first, bytes, bar);
     tc::bulk_g2s(base + 4 * s.tensor, a.stats + row * 4, rows * 16u, bar);
-    at.next(a, s.rows);
+    row += rows;
+    n += rows;
+    if (n >= a.N) n = 0;
     ++issued;
     if (++st == s.nst) { st = 0; ph ^= 1u; }
     return true;
   }
 };
 
-// V: features of a piece; FULL: the warps' features are the row's, none behind it
 template <typename T, int V, int E, bool FULL>
 __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
-  constexpr int NP = E / V;                             // pieces a thread
-  constexpr bool WHOLE = V * sizeof(T) == 16;           // rows of whole 16 bytes
-  constexpr int RH = E / 2;                             // pairs of features
+  using P = Pairs<T, V, E, FULL>;
+  constexpr int RH = P::H;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[RW][64];
   __shared__ __align__(8) uint64_t full[RING], empty[RING];
@@ -532,8 +644,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
   const int group = warp / s.warps, threads = 32 * s.warps, workerst = 32 * workers;
   // thread 0 copies: all slots at first, then one a tile, that of `lag` tiles ago, so that it
   // need not wait for the slowest warp
-  Fill fill;
-  fill.at = place_of(a, u0, s.rows);
+  Fill<P::WHOLE> fill(a, place_of(a, u0, s.rows));
   bool late = false;
   const int lag = s.nst > 3 ? 2 : 1;
   if (threadIdx.x == 0)
@@ -541,7 +652,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
   __syncwarp();
   const int t = threadIdx.x - group * threads;
   RowSum sum{slots[group], s.warps, group, threads};
-  auto col = [&](int j) { return (j * threads + t) * V; };      // of piece j
+  const P sh{t, threads, a.C};
   auto sync = [&]() { __syncthreads(); };
   const float inv = 1.f / (float)a.C;
 
@@ -553,7 +664,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     sync();                                           // nobody reads the last one's
     const size_t seq = (size_t)b * a.C;
     for (int c = threadIdx.x; c < a.C; c += workerst) {
-      const int piece = c / V, i = c % V, at = V < 4 ? c : ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
+      const int at = sh.place(c);
       float m = 1.f;
       if (a.gate) m *= as_f(((const T*)a.gate)[seq + c]);
       if (a.scale) m *= as_f(((const T*)a.scale)[c]);
@@ -563,93 +674,13 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     }
     sync();
   };
-  auto vec = [&](uint32_t base, f32x2(&p)[RH]) {
-    if constexpr (WHOLE) {
-#pragma unroll
-      for (int j = 0; j < NP; ++j)
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          uint4 f = make_uint4(0, 0, 0, 0);
-          if (FULL || col(j) < a.C) f = lds16(sm + base + (i * (a.C / V) + j * threads + t) * 16);
-          p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
-          p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
-        }
-    } else if constexpr (V == 2) {
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float2 f = col(j) < a.C ? *reinterpret_cast<const float2*>(smem + base + 4 * col(j)) : make_float2(0.f, 0.f);
-        p[j] = pack2(f.x, f.y);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NP; j += 2) {
-        const float* f = reinterpret_cast<const float*>(smem + base);
-        p[j / 2] = pack2(col(j) < a.C ? f[col(j)] : 0.f, col(j + 1) < a.C ? f[col(j + 1)] : 0.f);
-      }
-    }
-  };
+  auto vec = [&](uint32_t base, f32x2(&p)[RH]) { sh.vec(sm + base, p); };
   // this thread's share of a tensor's row in the tile at `tile`
-  const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + V * sizeof(T) * t;
+  const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + P::B * t;
   auto share = [&](uint32_t tile, int tensor, f32x2(&p)[RH]) {
-    const uint32_t at = tile + tensor * s.tensor + row_at;
-    if constexpr (WHOLE) {
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        uint4 f = make_uint4(0, 0, 0, 0);
-        if (FULL || col(j) < a.C) f = lds16(at + 16 * j * threads);
-        if constexpr (V == 4) {
-          p[2 * j] = pair_of(f.x, f.y);
-          p[2 * j + 1] = pair_of(f.z, f.w);
-        } else {
-          p[4 * j] = pair_of(f.x << 16, f.x & 0xffff0000u);
-          p[4 * j + 1] = pair_of(f.y << 16, f.y & 0xffff0000u);
-          p[4 * j + 2] = pair_of(f.z << 16, f.z & 0xffff0000u);
-          p[4 * j + 3] = pair_of(f.w << 16, f.w & 0xffff0000u);
-        }
-      }
-    } else {
-      uint32_t f[NP];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        f[j] = 0;
-        if (col(j) < a.C) f[j] = lds_piece<V * sizeof(T)>(at + V * (uint32_t)sizeof(T) * j * threads);
-      }
-#pragma unroll
-      for (int i = 0; i < RH; ++i) {
-        if constexpr (V == 2)
-          p[i] = pair_of(f[i] << 16, f[i] & 0xffff0000u);
-        else if constexpr (sizeof(T) == 2)
-          p[i] = pair_of(f[2 * i] << 16, f[2 * i + 1] << 16);
-        else
-          p[i] = pair_of(f[2 * i], f[2 * i + 1]);
-      }
-    }
+    sh.load(tile + tensor * s.tensor + row_at, P::B * threads, p);
   };
-  auto store = [&](void* base, size_t row, const f32x2(&p)[RH]) {
-    T* o = (T*)base + row * a.C;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      if (!FULL && col(j) >= a.C) continue;
-      if constexpr (V == 1) {
-        const float2 x = unpack2(p[j / 2]);
-        from_f(o + col(j), j & 1 ? x.y : x.x);
-      } else if constexpr (V == 2) {
-        const float2 x = unpack2(p[j]);
-        *reinterpret_cast<uint32_t*>(o + col(j)) = wtc::pack(x.x, x.y);
-      } else if constexpr (V == 4) {
-        const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
-        *reinterpret_cast<float4*>(o + col(j)) = make_float4(x.x, x.y, y.x, y.y);
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = unpack2(p[4 * j + i]);
-          w[i] = wtc::pack(x.x, x.y);
-        }
-        *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  };
+  auto store = [&](void* base, size_t row, const f32x2(&p)[RH]) { sh.store((T*)base + row * a.C, p); };
 
   f32x2 A[4][RH];
   auto clear = [&]() {
@@ -739,7 +770,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
     late = __any_sync(0xffffffffu, late) || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
     if (n < a.N) {
       const size_t row = (size_t)b * a.N + n;
-      const uint32_t tile = sm + st * s.tile + (WHOLE ? 0u : ring_skip(a, here, sizeof(T)));
+      const uint32_t tile = sm + st * s.tile + (P::WHOLE ? 0u : ring_skip(a, here, sizeof(T)));
       const uint4 qw = lds16(sm + st * s.tile + 4 * s.tensor + 16 * group);
       const float mu = __uint_as_float(qw.x), ru = __uint_as_float(qw.y), mh = __uint_as_float(qw.z),
                   rh = __uint_as_float(qw.w);
@@ -830,97 +861,30 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
 constexpr int FW = 8;             // warps of a block at the most
 constexpr int FD = 3;             // rows of the ring, the one that is worked on among them
 
-// the E features of a thread's share of a row, as pairs
-template <typename T, int E, bool FULL>
-struct Pairs {
-  static constexpr int V = 16 / (int)sizeof(T), NP = E / V, H = E / 2;
-  int t, threads, C;
-  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * V; }
-  __device__ __forceinline__ bool in(int j) const { return FULL || col(j) < C; }
-  // this thread's pieces of a row into its own places of a ring (zeros behind the row), and
-  // out of it again
-  __device__ __forceinline__ void fetch(const T* p, uint32_t slot) const {
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-      cp_async16(slot + (j * blockDim.x + threadIdx.x) * 16, in(j) ? p + col(j) : p, in(j));
-  }
-  __device__ __forceinline__ static void take(uint32_t slot, uint4 (&w)[NP]) {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) w[j] = lds16(slot + (j * blockDim.x + threadIdx.x) * 16);
-  }
-  __device__ __forceinline__ static void open(const uint4 (&w)[NP], f32x2 (&p)[H]) {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      if constexpr (V == 4) {
-        p[2 * j] = pack2(__uint_as_float(w[j].x), __uint_as_float(w[j].y));
-        p[2 * j + 1] = pack2(__uint_as_float(w[j].z), __uint_as_float(w[j].w));
-      } else {
-        const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[4 * j + i] = pack2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u));
-      }
-    }
-  }
-  __device__ __forceinline__ void store(T* o, const f32x2 (&p)[H]) const {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      uint32_t w[4];
-      if constexpr (V == 4) {
-        const float2 x = unpack2(p[2 * j]), y = unpack2(p[2 * j + 1]);
-        w[0] = __float_as_uint(x.x); w[1] = __float_as_uint(x.y);
-        w[2] = __float_as_uint(y.x); w[3] = __float_as_uint(y.y);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = unpack2(p[4 * j + i]);
-          w[i] = wtc::pack(x.x, x.y);
-        }
-      }
-      if (in(j)) *reinterpret_cast<uint4*>(o + col(j)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  // a vector in shared memory (fp32, quarters of pieces side by side)
-  __device__ __forceinline__ void vec(uint32_t base, f32x2 (&p)[H]) const {
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        uint4 f = make_uint4(0, 0, 0, 0);
-        if (in(j)) f = lds16(base + (i * (C / V) + j * threads + t) * 16);
-        p[(V * j + 4 * i) / 2] = pair_of(f.x, f.y);
-        p[(V * j + 4 * i) / 2 + 1] = pair_of(f.z, f.w);
-      }
-  }
-};
-
 // Threads copy their own pieces of a row (cp.async) two rows ahead, so that neither a
 // barrier nor registers are needed for them.
-template <typename T, int E, bool FULL>
+template <typename T, int V, int E, bool FULL>
 __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int warps, int rows) {
-  using P = Pairs<T, E, FULL>;
-  constexpr int V = P::V, NP = P::NP, H = P::H;
-  extern __shared__ __align__(16) uint8_t smem[];
+  using P = Pairs<T, V, E, FULL>;
+  constexpr int H = P::H;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[FW][64];
   const int group = (threadIdx.x >> 5) / warps;
-  P sh;
-  sh.threads = 32 * warps;
-  sh.t = threadIdx.x - group * sh.threads;
-  sh.C = a.C;
+  const P sh{(int)threadIdx.x - group * 32 * warps, 32 * warps, a.C};
   RowSum sum{slots[group], warps, group, sh.threads};
   const float inv = 1.f / (float)a.C;
   const uint32_t sm = tc::smem_u32(smem);
 
   // vectors in fp32: weight, bias, m post_weight, m post_bias
   const bool has_m = a.u && (a.post != kNormNone || a.gate || a.scale);
-  const uint32_t part = NP * 16 * blockDim.x, ring = sm;           // a tensor's share of a slot
+  const uint32_t part = E * sizeof(T) * blockDim.x, ring = sm;     // a tensor's share of a slot
   const uint32_t size = 4u * a.C, vw = FD * 2 * part, vy = vw + (a.weight ? size : 0), vm = vy + (a.bias ? size : 0),
                  vb = vm + (has_m ? size : 0);
   auto vectors = [&](int b) {
     __syncthreads();
     const size_t seq = (size_t)b * a.C;
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-      const int piece = c / V, i = c % V, at = ((i / 4) * (a.C / V) + piece) * 4 + i % 4;
+      const int at = sh.place(c);
       const size_t of = a.per_seq ? seq + c : c;
       float m = 1.f;
       if (a.gate) m *= as_f(((const T*)a.gate)[seq + c]);
@@ -948,7 +912,13 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
     f32x2 q = pack2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < H; ++i)
-      if (sh.in(2 * i / V)) q = fma2(z[i], z[i], q);
+      if constexpr (V == 1) {
+        const float2 v = unpack2(z[i]);
+        const f32x2 e = pack2(sh.in(2 * i) ? v.x : 0.f, sh.in(2 * i + 1) ? v.y : 0.f);
+        q = fma2(e, e, q);
+      } else {
+        if (sh.in(2 * i / V)) q = fma2(z[i], z[i], q);
+      }
     const float2 v = unpack2(q);
     const float r = rsqrtf(sum(v.x + v.y) * inv + a.eps);
     const f32x2 rr = pack2(r, r);
@@ -962,6 +932,12 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
   Place here = place_of(a, u0, rows), there = here;
   uint32_t slot_in = ring;
   int left = u1 - u0;                 // tiles that are not on their way
+  // this thread's pieces of a row into its own places of a slot (zeros behind the row)
+  auto fetch = [&](const T* p, uint32_t slot) {
+#pragma unroll
+    for (int j = 0; j < P::NP; ++j)
+      cp_async_piece<P::B>(slot + (j * blockDim.x + threadIdx.x) * P::B, sh.in(j) ? p + sh.col(j) : p, sh.in(j));
+  };
   auto ahead = [&]() {
     const uint32_t slot = slot_in;
     slot_in = slot_in + 2 * part == ring + FD * 2 * part ? ring : slot_in + 2 * part;
@@ -970,8 +946,8 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
     --left;
     there.next(a, rows);
     if (is) {
-      sh.fetch((const T*)a.x + row * a.C, slot);
-      if (a.u) sh.fetch((const T*)a.u + row * a.C, slot + part);
+      fetch((const T*)a.x + row * a.C, slot);
+      if (a.u) fetch((const T*)a.u + row * a.C, slot + part);
     }
     cp_commit();
   };
@@ -992,13 +968,9 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
     {
       const uint32_t slot = slot_out;
       slot_out = slot_out + 2 * part == ring + FD * 2 * part ? ring : slot_out + 2 * part;
-      uint4 w[NP];
-      P::take(slot, w);
-      P::open(w, h);
-      if (a.u) {
-        P::take(slot + part, w);
-        P::open(w, z);
-      }
+      const uint32_t mine = slot + threadIdx.x * P::B, apart = blockDim.x * P::B;
+      sh.load(mine, apart, h);
+      if (a.u) sh.load(mine + part, apart, z);
     }
     if (row < 0) continue;
     float2 su = make_float2(0.f, 0.f), sy = make_float2(0.f, 0.f);
@@ -1203,14 +1175,15 @@ cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.warps * r.rows), r.total, st, a, r, err);
 }
 
-template <typename T, int E>
+template <typename T, int V, int E>
 cudaError_t go_rows(NormArgs& a, const Shape& s, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   static SmemOnce once[2];
-  const bool full = a.C == 32 * s.warps * E;
-  auto* k = full ? k_norm_fwd_rows<T, E, true> : k_norm_fwd_rows<T, E, false>;
+  constexpr bool WHOLE = V * sizeof(T) == 16;
+  const bool full = WHOLE && a.C == 32 * s.warps * E;
+  auto* k = full ? k_norm_fwd_rows<T, V, E, WHOLE> : k_norm_fwd_rows<T, V, E, false>;
   // ring, and the vectors that there are
   const int vecs = (a.weight != nullptr) + (a.bias != nullptr) + (a.post_bias != nullptr) +
                    (a.u && (a.post != kNormNone || a.gate || a.scale));
@@ -1231,13 +1204,13 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
                        a.h, a.y, a.dh, a.dy, a.dx, a.du};
   for (const void* p : all) wide = wide && ((uintptr_t)p & 15) == 0;
   auto al = [](const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; };
+  constexpr int V = 16 / (int)sizeof(T);   // features of 16 bytes
   if (backward && al(a.x, 16) && al(a.u, 16) && al(a.dh, 16) && al(a.dy, 16)) {
     const RingShape r = ring_shape(a.C, sizeof(T), 8), r16 = ring_shape(a.C, sizeof(T), 16);
     // 16 features a thread where that works on a third more rows at once and leaves a ring of
     // three tiles (bf16 rows of 512, 12 for 8: 173 us for 242; of 1536, 4 for 2: 199 for 306; of
     // 640, 6 for 5: 334 for 322; fp32 rows of 512, two tiles: 146 for 139)
     const bool more = r16.nst > 2 && 3 * r16.rows >= 4 * r.rows;
-    constexpr int V = 16 / (int)sizeof(T);
     if (r.nst > 0) {
       if (a.C % V == 0 && al(a.dx, 16) && al(a.du, 16))
         return more ? go_ring<T, V, 16>(a, r16, st) : go_ring<T, V, 8>(a, r, st);
@@ -1247,8 +1220,14 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
       return more ? go_ring<T, 1, 16>(a, r16, st) : go_ring<T, 1, 8>(a, r, st);
     }
   }
-  if (wide && !backward && s.warps <= FW)
-    return s.ept == 8 ? go_rows<T, 8>(a, s, st) : go_rows<T, 16>(a, s, st);
+  if (!backward && s.warps <= FW) {
+    auto rows = [&](size_t n) { return a.C % (n / sizeof(T)) == 0 && al(a.x, n) && al(a.u, n) && al(a.h, n) && al(a.y, n); };
+    if (rows(16)) return s.ept == 8 ? go_rows<T, V, 8>(a, s, st) : go_rows<T, V, 16>(a, s, st);
+    // pairs of bf16 (rows of 514, 2^27 bytes a tensor: 420 us, 552 by k_norm_fwd; single fp32
+    // values of rows of 1001 took 245 us for 182)
+    if constexpr (sizeof(T) == 2)
+      if (rows(4)) return s.ept == 8 ? go_rows<T, 2, 8>(a, s, st) : go_rows<T, 2, 16>(a, s, st);
+  }
   a.parts = norm_parts(a.B, a.N, a.C);
   if (s.ept == 8) return go<T, 8, false>(a, backward, s, st);
   return wide ? go<T, 16, true>(a, backward, s, st) : go<T, 16, false>(a, backward, s, st);
