@@ -16,10 +16,10 @@
 // again from x and u in the backward, which reads as much as h would and has no rounding
 // in it.  Statistics are of centred values, in fp32.
 //
-// Backward, up to 4096 features (k_norm_bwd_ring): a block
-// an SM takes an even stretch of all rows, in tiles of as many rows as its warps work on at
-// once (8 or 16 features a thread of sixteen or twelve warps), which one thread copies into a
-// ring in shared memory (bulk copies; a tile's rows lie side by side).  What a feature is
+// Backward, up to 6144 features, 8192 without biases (k_norm_bwd_ring): a block an SM takes an
+// even stretch of all rows, in tiles of as many rows as its warps work on at once (8 or 16
+// features a thread of twelve or sixteen warps), which one thread copies into a ring in shared
+// memory (bulk copies; a tile's rows lie side by side).  What a feature is
 // multiplied by is laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both
 // norms, gate and scale: 152 us, 5.3 TB/s: sums over a row are what a row waits for, so rows
 // in flight and registers count (a warp of its own for the copies costs the registers of
@@ -42,6 +42,8 @@
 #include "internal.h"
 #include "layer.cuh"
 #include "win_tc.cuh"
+
+#include <type_traits>
 
 namespace lapnys {
 namespace {
@@ -407,11 +409,10 @@ __global__ void __launch_bounds__(TB) k_norm_bwd(NormArgs a, int warps) {
 // ---------------------------------------------------------------------------
 // the backward's rows through a ring in shared memory
 // ---------------------------------------------------------------------------
-// warps of a block at the most, with E features a thread (by their registers)
-constexpr int ring_warps(int E) { return E == 8 ? 16 : 12; }
-constexpr int RW = ring_warps(8);
+// warps of a block at the most, with E features a thread and KINDS of sums (by their registers)
+constexpr int ring_warps(int E, int KINDS) { return E == 8 || KINDS == 2 ? 16 : 12; }
+constexpr int RW = ring_warps(8, 4);
 constexpr int RING = 6;           // tiles of the ring at the most
-constexpr int kRingWidth = 32 * RW * 8;
 constexpr size_t kRingBytes = 216 * 1024;
 
 // shared memory of a block: ring tiles, then vectors, then the join of the sums
@@ -623,8 +624,10 @@ struct Fill {
   }
 };
 
-template <typename T, int V, int E, bool FULL>
-__global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
+// KINDS: of sums over the rows; two: those through the unit norms alone (no bias's gradient)
+template <typename T, int V, int E, int KINDS, bool FULL>
+__global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
+    k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
   using P = Pairs<T, V, E, FULL>;
   constexpr int RH = P::H;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -682,10 +685,11 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
   };
   auto store = [&](void* base, size_t row, const f32x2(&p)[RH]) { sh.store((T*)base + row * a.C, p); };
 
-  f32x2 A[4][RH];
+  f32x2 A[KINDS][RH];
+  constexpr int AT_U = KINDS / 2;     // of dh' unit(u)
   auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < KINDS; ++k)
 #pragma unroll
       for (int i = 0; i < RH; ++i) A[k][i] = pack2(0.f, 0.f);
   };
@@ -706,17 +710,18 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
       }
     };
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int n = 0; n < KINDS; ++n) {
+      const int k = n * (4 / KINDS);
       if (!(a.sums >> k & 1)) continue;
       if (s.rows == 1) {
 #pragma unroll
-        for (int i = 0; i < RH; ++i) put(k, i, t, unpack2(A[k][i]));
+        for (int i = 0; i < RH; ++i) put(k, i, t, unpack2(A[n][i]));
         continue;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < HP; ++i) join[(group * HP + i) * threads + t] = unpack2(A[k][h * HP + i]);
+        for (int i = 0; i < HP; ++i) join[(group * HP + i) * threads + t] = unpack2(A[n][h * HP + i]);
         sync();
 #pragma unroll 1
         for (int e = threadIdx.x; e < HP * threads; e += workerst) {
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
 #pragma unroll
         for (int i = 0; i < RH; ++i) {
           A[0][i] = fma2(e[i], hh[i], A[0][i]);
-          A[1][i] = wtc::add2(e[i], A[1][i]);
+          if constexpr (KINDS == 4) A[1][i] = wtc::add2(e[i], A[1][i]);
         }
         if (has_w) {
           vec(vw, v);
@@ -825,8 +830,8 @@ __global__ void __launch_bounds__(32 * ring_warps(E), 1) k_norm_bwd_ring(NormArg
       if (a.u) {
 #pragma unroll
         for (int i = 0; i < RH; ++i) {
-          A[2][i] = fma2(d[i], uh[i], A[2][i]);
-          A[3][i] = wtc::add2(d[i], A[3][i]);
+          A[AT_U][i] = fma2(d[i], uh[i], A[AT_U][i]);
+          if constexpr (KINDS == 4) A[3][i] = wtc::add2(d[i], A[3][i]);
         }
         if (has_m) {
           vec(vm, v);
@@ -1138,25 +1143,27 @@ int norm_parts(int B, int N, int C) {
   return (int)(p < 1 ? 1 : p);
 }
 
-// the ring's shape with E features a thread; nst 0: rows that do not go through it
-RingShape ring_shape(int C, int es, int E) {
+// the ring's shape with E features a thread and `vecs` vectors; nst 0: rows that do not go
+// through it
+RingShape ring_shape(int C, int es, int E, int kinds, int vecs) {
   RingShape r;
+  const int most = ring_warps(E, kinds);
   r.warps = (C + 32 * E - 1) / (32 * E);
-  r.rows = r.warps <= ring_warps(E) ? ring_warps(E) / r.warps : 1;
+  r.rows = r.warps <= most ? most / r.warps : 1;
   // rows that are no whole 16 bytes: with up to 15 bytes before and behind
   r.tensor = (uint32_t)((r.rows * C * es + (C * es % 16 ? 30 : 0) + 15) & ~15);
   r.tile = 4 * r.tensor + 16 * RW;
   r.tail = 0;
-  const uint32_t vec = (12u * C + 15) & ~15u, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
+  const uint32_t vec = (4u * vecs * C + 15) & ~15u, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
   const size_t n = vec + join < kRingBytes ? (kRingBytes - vec - join) / r.tile : 0;
-  r.nst = C > kRingWidth || n < 2 ? 0 : (int)(n < RING ? n : RING);
+  r.nst = r.warps > most || n < 2 ? 0 : (int)(n < RING ? n : RING);
   r.vec = r.nst * r.tile;
   r.join = r.vec + vec;
   r.total = r.join + join;
   return r;
 }
 
-template <typename T, int V, int E>
+template <typename T, int V, int E, int KINDS>
 cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
@@ -1170,7 +1177,7 @@ cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   r.tail = (uint32_t)((size_t)a.B * a.N * a.C * sizeof(T) % 16);
   constexpr bool WHOLE = V * sizeof(T) == 16;
   const bool full = WHOLE && a.C == 32 * r.warps * E;
-  auto* k = full ? k_norm_bwd_ring<T, V, E, WHOLE> : k_norm_bwd_ring<T, V, E, false>;
+  auto* k = full ? k_norm_bwd_ring<T, V, E, KINDS, WHOLE> : k_norm_bwd_ring<T, V, E, KINDS, false>;
   if ((e = once[full].allow(k, kRingBytes, dev)) != cudaSuccess) return e;
   return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.warps * r.rows), r.total, st, a, r, err);
 }
@@ -1206,18 +1213,34 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
   auto al = [](const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; };
   constexpr int V = 16 / (int)sizeof(T);   // features of 16 bytes
   if (backward && al(a.x, 16) && al(a.u, 16) && al(a.dh, 16) && al(a.dy, 16)) {
-    const RingShape r = ring_shape(a.C, sizeof(T), 8), r16 = ring_shape(a.C, sizeof(T), 16);
+    const bool whole = a.C % V == 0 && al(a.dx, 16) && al(a.du, 16);
+    // fewer sums over the rows leave registers for sixteen warps of 16 features (bf16 rows of
+    // 4096, two root mean squares: 170 us, 258 by 8 features; of 8192: 191, 364 by k_norm_bwd);
+    // pairs and single elements have none left (rows of 1001: 428 us for 356)
+    const bool two = whole && !(a.sums & (kSumDy | kSumDh));
+    const int vecs = (a.weight && a.dy) + (a.u && (a.post != kNormNone || a.gate || a.scale)) + (a.post_bias != nullptr);
+    const RingShape r = ring_shape(a.C, sizeof(T), 8, 4, vecs),
+                    r16 = ring_shape(a.C, sizeof(T), 16, two ? 2 : 4, vecs);
     // 16 features a thread where that works on a third more rows at once and leaves a ring of
-    // three tiles (bf16 rows of 512, 12 for 8: 173 us for 242; of 1536, 4 for 2: 199 for 306; of
-    // 640, 6 for 5: 334 for 322; fp32 rows of 512, two tiles: 146 for 139)
-    const bool more = r16.nst > 2 && 3 * r16.rows >= 4 * r.rows;
-    if (r.nst > 0) {
-      if (a.C % V == 0 && al(a.dx, 16) && al(a.du, 16))
-        return more ? go_ring<T, V, 16>(a, r16, st) : go_ring<T, V, 8>(a, r, st);
+    // three tiles, or on twice the rows (bf16 rows of 512, 12 for 8: 173 us for 242; of 1536, 4
+    // for 2: 199 for 306; of 640, 6 for 5: 334 for 322; fp32 rows of 512, two tiles: 146 for
+    // 139); on two thirds more where only 8 fill their warps (768, 8 for 5: 287 for 255; 1280, 5
+    // for 3: 238 for 260); and where 8 do not reach over the row
+    const bool only8 = a.C % 256 == 0 && a.C % 512 != 0;
+    const bool more = r.nst == 0 || (r16.nst > 2 && 3 * r16.rows >= (only8 ? 5 : 4) * r.rows) ||
+                      (r16.nst == 2 && r16.rows >= 2 * r.rows);
+    if (!more || r16.nst > 0) {
+      auto with = [&](auto v) {
+        constexpr int P = decltype(v)::value;
+        if (!more) return go_ring<T, P, 8, 4>(a, r, st);
+        if constexpr (P == V)
+          if (two) return go_ring<T, P, 16, 2>(a, r16, st);
+        return go_ring<T, P, 16, 4>(a, r16, st);
+      };
+      if (whole) return with(std::integral_constant<int, V>{});
       if constexpr (sizeof(T) == 2)
-        if (a.C % 2 == 0 && al(a.dx, 4) && al(a.du, 4))
-          return more ? go_ring<T, 2, 16>(a, r16, st) : go_ring<T, 2, 8>(a, r, st);
-      return more ? go_ring<T, 1, 16>(a, r16, st) : go_ring<T, 1, 8>(a, r, st);
+        if (a.C % 2 == 0 && al(a.dx, 4) && al(a.du, 4)) return with(std::integral_constant<int, 2>{});
+      return with(std::integral_constant<int, 1>{});
     }
   }
   if (!backward && s.warps <= FW) {

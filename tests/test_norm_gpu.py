@@ -240,3 +240,22 @@ def test_rows_that_are_no_whole_pieces(dtype, B, N, C):
         check("y", y, ref["y"], dtype)
         for n, g in zip(NAMES, lap.norm_bwd(x, u, t["weight"], st, gh, gy, p, **vec)):
             check("d" + n, g, ref[n], dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,N,C", [(2, 200, 512), (3, 77, 1000), (1, 333, 514), (2, 300, 321), (2, 200, 2048), (2, 100, 4096),
+                                   (1, 90, 4608), (2, 60, 5001), (2, 80, 6144), (1, 170, 8192)])
+def test_weights_without_biases(dtype, B, N, C):
+    """Two kinds of sums over the rows instead of four: more rows at once, and wider ones."""
+    t = _inputs(B, N, C, dtype, B + N + C, ("u", "weight", "post_weight", "gate"))
+    dh, dy = torch.randn_like(t["x"]), torch.randn_like(t["x"])
+    p = lap.NormParams(B, N, C, False, "rms", "rms", 1e-6)
+    ref = _reference(t, "rms", "rms", 1e-6, dh, dy)
+    vec = {n: t[n] for n in ("post_weight", "post_bias", "gate", "scale")}
+    _, _, st = lap.norm_fwd(t["x"], t["u"], t["weight"], None, p, **vec)
+    want = tuple(t[n] is not None for n in NAMES)
+    grads = lap.norm_bwd(t["x"], t["u"], t["weight"], st, dh, dy, p, **vec, want=want)
+    for n, g in zip(NAMES, grads):
+        assert (g is not None) == (t[n] is not None)
+        if g is not None:
+            check("d" + n, g, ref[n], dtype)
