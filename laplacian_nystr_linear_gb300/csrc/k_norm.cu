@@ -30,7 +30,7 @@
 //
 // Forward, rows of whole 16 bytes (bf16: or 4), up to 4096 features (k_norm_fwd_rows): threads
 // copy their own pieces two rows ahead (cp.async), two blocks an SM: 98 us for the same rows,
-// 5.5 TB/s; 32768 rows of 4096, two norms: 204 us, 5.3 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
+// 5.5 TB/s; 32768 rows of 4096, two norms: 198 us, 5.4 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
 // the row ahead: 243.)
 //
 // Other rows (more features, forward of single elements, backward of tensors that start
