@@ -19,19 +19,19 @@
 // Backward, up to 6144 features, 8192 without biases (k_norm_bwd_ring): a block an SM takes an
 // even stretch of all rows, in tiles of as many rows as its warps work on at once (8 or 16
 // features a thread of twelve or sixteen warps), which one thread copies into a ring in shared
-// memory (bulk copies; a tile's rows lie side by side).  What a feature is
-// multiplied by is laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both
-// norms, gate and scale: 152 us, 5.3 TB/s: sums over a row are what a row waits for, so rows
-// in flight and registers count (a warp of its own for the copies costs the registers of
-// four: eight warps of 16 features, or sixteen of 8, took 228); loads by the warps
-// themselves beside 255 registers a thread took 390.  Rows that are no whole 16 bytes lie in
-// the ring as they lie in memory and are read from it by pairs or single elements: 1001
-// features, 400 us for 847 of the loads by the threads; 514, 449 for 1425 (2^27 bytes a tensor).
+// memory (bulk copies; a tile's rows lie side by side).  What a feature is multiplied by is
+// laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both norms, gate and
+// scale: 154 us, 5.2 TB/s: sums over a row are what a row waits for, so rows in flight and
+// registers count (a warp of its own for the copies costs the registers of four: eight warps
+// of 16 features, or sixteen of 8, took 228); loads by the warps themselves beside 255
+// registers a thread took 390.  Rows that are no whole 16 bytes lie in the ring as they lie in
+// memory and are read from it by pairs or single elements: 1001 features, 400 us for 847 of
+// the loads by the threads; 514, 446 for 1425 (2^27 bytes a tensor).
 //
 // Forward, rows of whole 16 bytes (bf16: or 4), up to 4096 features (k_norm_fwd_rows): threads
 // copy their own pieces two rows ahead (cp.async), two blocks an SM: 98 us for the same rows,
-// 5.5 TB/s; 32768 rows of 4096, two norms: 198 us, 5.4 TB/s.  (A ring of bulk copies as above: 434 us there; registers for
-// the row ahead: 243.)
+// 5.5 TB/s; 32768 rows of 4096, two norms: 198 us, 5.4 TB/s.  (A ring of bulk copies as above:
+// 434 us there; registers for the row ahead: 243.)
 //
 // Other rows (more features, forward of single elements, backward of tensors that start
 // anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are needed.
