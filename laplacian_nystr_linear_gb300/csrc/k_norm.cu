@@ -33,6 +33,10 @@
 // 5.5 TB/s; 32768 rows of 4096, two norms: 198 us, 5.4 TB/s.  (A ring of bulk copies as above:
 // 434 us there; registers for the row ahead: 243.)
 //
+// Rows of up to 128 features (a head's): several to a warp in both directions, 8 features a
+// lane. bf16 rows of 64, both layer norms: backward 197 us for 720 with a warp a row, forward
+// 123 for 564; of 128: 202 for 367, 132 for 287 (2^27 bytes a tensor).
+//
 // Other rows (more features, forward of single elements, backward of tensors that start
 // anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are needed.
 //
@@ -122,15 +126,17 @@ struct Share {
   __device__ __forceinline__ bool in(int i) const { return col(i / V) < C; }
 };
 
-// sums over the `warps` warps of a row group: by shuffles, then shared memory
+// sums over the `warps` warps of a row group: by shuffles, then shared memory; SUB: over the
+// `threads` lanes of a row that is less than a warp's
+template <bool SUB = false>
 struct RowSum {
   float2* slot;     // [2][32] of this group
   int warps, group, threads;
   int turn = 0;
   __device__ __forceinline__ float2 operator()(float2 v) {
-    if (warps == 1) {
+    if (SUB || warps == 1) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
+      for (int o = SUB ? threads >> 1 : 16; o > 0; o >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
       }
@@ -161,8 +167,8 @@ struct RowSum {
   }
   __device__ __forceinline__ float operator()(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (warps == 1) return v;
+    for (int o = SUB ? threads >> 1 : 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (SUB || warps == 1) return v;
     float* s = reinterpret_cast<float*>(slot + 32 * turn);
     turn ^= 1;
     const int w = (threadIdx.x >> 5) % warps, i = threadIdx.x & 31;
@@ -183,7 +189,7 @@ struct RowSum {
 // mean and 1 / deviation of a row's values
 template <typename S, int EPT>
 __device__ __forceinline__ float2 row_stats(const float (&z)[EPT], int kind, float eps, const S& sh,
-                                            RowSum& sum) {
+                                            RowSum<>& sum) {
   float mean = 0.f;
   const float inv = 1.f / (float)sh.C;
   if (kind == kNormLayer) {
@@ -204,7 +210,7 @@ __device__ __forceinline__ float2 row_stats(const float (&z)[EPT], int kind, flo
 template <typename T, int EPT, bool WIDE>
 struct Rows {
   Share<T, EPT, WIDE> sh;
-  RowSum sum;
+  RowSum<> sum;
   int group, groups;
   __device__ __forceinline__ Rows(const NormArgs& a, int warps, float2 (*slots)[64]) {
     const int warp = threadIdx.x >> 5;
@@ -418,6 +424,7 @@ constexpr size_t kRingBytes = 216 * 1024;
 // shared memory of a block: ring tiles, then vectors, then the join of the sums
 struct RingShape {
   int warps, rows, nst;           // warps of a row, rows of a tile, tiles of the ring
+  int lanes, workers;             // threads of a row, warps of the block
   uint32_t tensor, tile;          // bytes of a tensor's share of a tile, of a tile
   uint32_t tail;                  // bytes of a tensor behind its last whole 16
   uint32_t vec, join, total;      // bytes: where the vectors and the join start, and in all
@@ -624,8 +631,9 @@ struct Fill {
   }
 };
 
+// SUB: rows of less than a warp's features, several to a warp.
 // KINDS: of sums over the rows; two: those through the unit norms alone (no bias's gradient)
-template <typename T, int V, int E, int KINDS, bool FULL>
+template <typename T, int V, int E, int KINDS, bool FULL, bool SUB>
 __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
     k_norm_bwd_ring(NormArgs a, RingShape s, int* err) {
   using P = Pairs<T, V, E, FULL>;
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[RW][64];
   __shared__ __align__(8) uint64_t full[RING], empty[RING];
-  const int warp = threadIdx.x >> 5, workers = s.warps * s.rows;
+  const int workers = s.workers;
   const uint32_t sm = tc::smem_u32(smem);
   if (threadIdx.x == 0)
     for (int i = 0; i < s.nst; ++i) {
@@ -644,7 +652,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   __syncthreads();
   const long long units = (long long)a.B * a.tiles;
   const int u0 = (int)(units * blockIdx.x / a.grid), u1 = (int)(units * (blockIdx.x + 1) / a.grid);
-  const int group = warp / s.warps, threads = 32 * s.warps, workerst = 32 * workers;
+  const int threads = s.lanes, group = threadIdx.x / threads, workerst = 32 * workers;
   // thread 0 copies: all slots at first, then one a tile, that of `lag` tiles ago, so that it
   // need not wait for the slowest warp
   Fill<P::WHOLE> fill(a, place_of(a, u0, s.rows));
@@ -654,8 +662,9 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
     for (int i = 0; i < s.nst && u0 + i < u1; ++i) late = late || !fill.tile(a, s, sm, full, empty, sizeof(T), err);
   __syncwarp();
   const int t = threadIdx.x - group * threads;
-  RowSum sum{slots[group], s.warps, group, threads};
+  RowSum<SUB> sum{slots[SUB ? 0 : group], s.warps, group, threads};
   const P sh{t, threads, a.C};
+  bool is = true;      // SUB: this thread's row is there
   auto sync = [&]() { __syncthreads(); };
   const float inv = 1.f / (float)a.C;
 
@@ -682,6 +691,9 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   const uint32_t row_at = (uint32_t)(group * a.C) * sizeof(T) + P::B * t;
   auto share = [&](uint32_t tile, int tensor, f32x2(&p)[RH]) {
     sh.load(tile + tensor * s.tensor + row_at, P::B * threads, p);
+    if (SUB && !is)
+#pragma unroll
+      for (int i = 0; i < RH; ++i) p[i] = pack2(0.f, 0.f);
   };
   auto store = [&](void* base, size_t row, const f32x2(&p)[RH]) { sh.store((T*)base + row * a.C, p); };
 
@@ -695,6 +707,8 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   };
   // The sums of sequence b into this block's slot: half of a kind's pairs at a time side by
   // side in shared memory, [group][pair][thread], and the groups' sums in order.
+  // (both here: chosen inside the lambda by SUB, the compiler lost the sums of the other kind)
+  const int share_of = SUB ? (int)(threadIdx.x >> 5) : group, shares = SUB ? s.workers : s.rows;
   auto flush = [&](int b) {
     constexpr int HP = RH / 2;
     float* out = a.part + ((size_t)b + blockIdx.x) * 4 * a.C;
@@ -721,13 +735,20 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < HP; ++i) join[(group * HP + i) * threads + t] = unpack2(A[n][h * HP + i]);
+        for (int i = 0; i < HP; ++i) {
+          float2 v = unpack2(A[n][h * HP + i]);
+          for (int o = threads; o < 32; o <<= 1) {     // the rows of a warp
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+          }
+          if ((int)(threadIdx.x & 31) < threads) join[(share_of * HP + i) * threads + t] = v;
+        }
         sync();
 #pragma unroll 1
         for (int e = threadIdx.x; e < HP * threads; e += workerst) {
           float2 v = join[e];
 #pragma unroll 4
-          for (int g = 1; g < s.rows; ++g) {
+          for (int g = 1; g < shares; ++g) {
             const float2 y = join[g * HP * threads + e];
             v.x += y.x;
             v.y += y.y;
@@ -773,12 +794,14 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
     // after an expired wait (the error word is set) no other is waited for: every warp goes
     // on to its end, since the sums and the barriers need all
     late = __any_sync(0xffffffffu, late) || !wtc::wait_warp(err, tc::smem_u32(&full[st]), ph);
-    if (n < a.N) {
+    is = n < a.N;
+    if (SUB ? __any_sync(0xffffffffu, is) : is) {
       const size_t row = (size_t)b * a.N + n;
       const uint32_t tile = sm + st * s.tile + (P::WHOLE ? 0u : ring_skip(a, here, sizeof(T)));
       const uint4 qw = lds16(sm + st * s.tile + 4 * s.tensor + 16 * group);
-      const float mu = __uint_as_float(qw.x), ru = __uint_as_float(qw.y), mh = __uint_as_float(qw.z),
-                  rh = __uint_as_float(qw.w);
+      float mu = __uint_as_float(qw.x), ru = __uint_as_float(qw.y), mh = __uint_as_float(qw.z),
+            rh = __uint_as_float(qw.w);
+      if (SUB && !is) mu = ru = mh = rh = 0.f;
       f32x2 uh[RH], d[RH], v[RH];
       if (a.u) {
         share(tile, 1, uh);
@@ -826,7 +849,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
 #pragma unroll
         for (int i = 0; i < RH; ++i) d[i] = fma2(e[i], rr, fma2(hh[i], kk1, wtc::add2(d[i], kk0)));
       }
-      if (a.dx) store(a.dx, row, d);
+      if (a.dx && (!SUB || is)) store(a.dx, row, d);
       if (a.u) {
 #pragma unroll
         for (int i = 0; i < RH; ++i) {
@@ -845,7 +868,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
 #pragma unroll
           for (int i = 0; i < RH; ++i) d[i] = fma2(d[i], rr, fma2(uh[i], kk1, kk0));
         }
-        if (a.du) store(a.du, row, d);
+        if (a.du && (!SUB || is)) store(a.du, row, d);
       }
     }
     wtc::arrive_warp(tc::smem_u32(&empty[st]));
@@ -868,15 +891,15 @@ constexpr int FD = 3;             // rows of the ring, the one that is worked on
 
 // Threads copy their own pieces of a row (cp.async) two rows ahead, so that neither a
 // barrier nor registers are needed for them.
-template <typename T, int V, int E, bool FULL>
-__global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int warps, int rows) {
+template <typename T, int V, int E, bool FULL, bool SUB>
+__global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int warps, int rows, int lanes) {
   using P = Pairs<T, V, E, FULL>;
   constexpr int H = P::H;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 slots[FW][64];
-  const int group = (threadIdx.x >> 5) / warps;
-  const P sh{(int)threadIdx.x - group * 32 * warps, 32 * warps, a.C};
-  RowSum sum{slots[group], warps, group, sh.threads};
+  const int group = threadIdx.x / lanes;
+  const P sh{(int)threadIdx.x - group * lanes, lanes, a.C};
+  RowSum<SUB> sum{slots[SUB ? 0 : group], warps, group, lanes};
   const float inv = 1.f / (float)a.C;
   const uint32_t sm = tc::smem_u32(smem);
 
@@ -977,7 +1000,8 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
       sh.load(mine, apart, h);
       if (a.u) sh.load(mine + part, apart, z);
     }
-    if (row < 0) continue;
+    const bool is = row >= 0;
+    if (SUB ? !__any_sync(0xffffffffu, is) : !is) continue;
     float2 su = make_float2(0.f, 0.f), sy = make_float2(0.f, 0.f);
     f32x2 v[H];
     if (a.u) {
@@ -995,8 +1019,8 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
 #pragma unroll
         for (int i = 0; i < H; ++i) h[i] = wtc::add2(h[i], v[i]);
       }
-      if (a.h) sh.store((T*)a.h + row * a.C, h);
-    } else if (a.h) {
+      if (a.h && is) sh.store((T*)a.h + row * a.C, h);
+    } else if (a.h && is) {
       sh.store((T*)a.h + row * a.C, h);
     }
     if (a.y) {
@@ -1011,9 +1035,9 @@ __global__ void __launch_bounds__(32 * FW, 2) k_norm_fwd_rows(NormArgs a, int wa
 #pragma unroll
         for (int i = 0; i < H; ++i) h[i] = wtc::add2(h[i], v[i]);
       }
-      sh.store((T*)a.y + row * a.C, h);
+      if (is) sh.store((T*)a.y + row * a.C, h);
     }
-    if (a.stats && sh.t == 0) reinterpret_cast<float4*>(a.stats)[row] = make_float4(su.x, su.y, sy.x, sy.y);
+    if (a.stats && sh.t == 0 && is) reinterpret_cast<float4*>(a.stats)[row] = make_float4(su.x, su.y, sy.x, sy.y);
   }
 }
 
@@ -1143,18 +1167,31 @@ int norm_parts(int B, int N, int C) {
   return (int)(p < 1 ? 1 : p);
 }
 
-// the ring's shape with E features a thread and `vecs` vectors; nst 0: rows that do not go
-// through it
-RingShape ring_shape(int C, int es, int E, int kinds, int vecs) {
+// lanes of a row of 8 features a lane: a power of two; 32 of more than 128 features
+int lanes_of(int C) {
+  int n = 1;
+  while (n < 32 && 8 * n < C) n *= 2;
+  return n;
+}
+
+// the ring's shape with E features a thread and `vecs` vectors, several rows a warp where
+// `sub`; nst 0: rows that do not go through it
+RingShape ring_shape(int C, int es, int E, int kinds, int vecs, bool sub = false) {
   RingShape r;
   const int most = ring_warps(E, kinds);
   r.warps = (C + 32 * E - 1) / (32 * E);
   r.rows = r.warps <= most ? most / r.warps : 1;
+  r.lanes = 32 * r.warps;
+  r.workers = r.warps * r.rows;
+  if (sub) {
+    r.lanes = lanes_of(C);
+    r.rows *= 32 / r.lanes;
+  }
   // rows that are no whole 16 bytes: with up to 15 bytes before and behind
   r.tensor = (uint32_t)((r.rows * C * es + (C * es % 16 ? 30 : 0) + 15) & ~15);
-  r.tile = 4 * r.tensor + 16 * RW;
+  r.tile = 4 * r.tensor + 16 * r.rows;
   r.tail = 0;
-  const uint32_t vec = (4u * vecs * C + 15) & ~15u, join = r.rows > 1 ? 64u * r.warps * r.rows * E : 0u;
+  const uint32_t vec = (4u * vecs * C + 15) & ~15u, join = r.rows > 1 ? 64u * r.workers * E : 0u;
   const size_t n = vec + join < kRingBytes ? (kRingBytes - vec - join) / r.tile : 0;
   r.nst = r.warps > most || n < 2 ? 0 : (int)(n < RING ? n : RING);
   r.vec = r.nst * r.tile;
@@ -1163,7 +1200,7 @@ RingShape ring_shape(int C, int es, int E, int kinds, int vecs) {
   return r;
 }
 
-template <typename T, int V, int E, int KINDS>
+template <typename T, int V, int E, int KINDS, bool SUB = false>
 cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
@@ -1176,31 +1213,32 @@ cudaError_t go_ring(NormArgs& a, RingShape r, cudaStream_t st) {
   static SmemOnce once[2];
   r.tail = (uint32_t)((size_t)a.B * a.N * a.C * sizeof(T) % 16);
   constexpr bool WHOLE = V * sizeof(T) == 16;
-  const bool full = WHOLE && a.C == 32 * r.warps * E;
-  auto* k = full ? k_norm_bwd_ring<T, V, E, KINDS, WHOLE> : k_norm_bwd_ring<T, V, E, KINDS, false>;
+  const bool full = WHOLE && a.C == r.lanes * E;
+  auto* k = full ? k_norm_bwd_ring<T, V, E, KINDS, WHOLE, SUB> : k_norm_bwd_ring<T, V, E, KINDS, false, SUB>;
   if ((e = once[full].allow(k, kRingBytes, dev)) != cudaSuccess) return e;
-  return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.warps * r.rows), r.total, st, a, r, err);
+  return launch("norm_bwd", k, dim3(a.grid), dim3(32 * r.workers), r.total, st, a, r, err);
 }
 
-template <typename T, int V, int E>
+template <typename T, int V, int E, bool SUB = false>
 cudaError_t go_rows(NormArgs& a, const Shape& s, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   static SmemOnce once[2];
   constexpr bool WHOLE = V * sizeof(T) == 16;
-  const bool full = WHOLE && a.C == 32 * s.warps * E;
-  auto* k = full ? k_norm_fwd_rows<T, V, E, WHOLE> : k_norm_fwd_rows<T, V, E, false>;
+  const int lanes = SUB ? lanes_of(a.C) : 32 * s.warps, rows = 32 * s.warps * s.groups / lanes;
+  const bool full = WHOLE && a.C == lanes * E;
+  auto* k = full ? k_norm_fwd_rows<T, V, E, WHOLE, SUB> : k_norm_fwd_rows<T, V, E, false, SUB>;
   // ring, and the vectors that there are
   const int vecs = (a.weight != nullptr) + (a.bias != nullptr) + (a.post_bias != nullptr) +
                    (a.u && (a.post != kNormNone || a.gate || a.scale));
   const size_t threads = 32 * s.warps * s.groups, smem = FD * 2 * threads * E * sizeof(T) + (size_t)vecs * a.C * 4;
   if ((e = once[full].allow(k, FD * 2 * 32 * FW * E * sizeof(T) + 4 * 32 * FW * E * 4, dev)) != cudaSuccess) return e;
-  a.tiles = (a.N + s.groups - 1) / s.groups;
+  a.tiles = (a.N + rows - 1) / rows;
   // as many blocks as an SM's shared memory takes (4 KB are static, 1 KB reserved), two at the most
   const long long tiles = (long long)a.B * a.tiles, most = 152LL * (2 * (smem + 5120) <= 228 * 1024 ? 2 : 1);
   const unsigned grid = (unsigned)(tiles < most ? tiles : most);
-  return launch("norm_fwd", k, dim3(grid), dim3(32 * s.warps * s.groups), smem, st, a, s.warps, s.groups);
+  return launch("norm_fwd", k, dim3(grid), dim3(32 * s.warps * s.groups), smem, st, a, s.warps, rows, lanes);
 }
 
 template <typename T>
@@ -1230,8 +1268,12 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
     const bool more = r.nst == 0 || (r16.nst > 2 && 3 * r16.rows >= (only8 ? 5 : 4) * r.rows) ||
                       (r16.nst == 2 && r16.rows >= 2 * r.rows);
     if (!more || r16.nst > 0) {
+      // several rows a warp, where a sequence's rows fill half a tile of them
+      const RingShape rs = ring_shape(a.C, sizeof(T), 8, 4, vecs, true);
+      const bool sub = a.C <= 128 && rs.nst > 0 && 2LL * a.N >= rs.rows;
       auto with = [&](auto v) {
         constexpr int P = decltype(v)::value;
+        if (sub) return go_ring<T, P, 8, 4, true>(a, rs, st);
         if (!more) return go_ring<T, P, 8, 4>(a, r, st);
         if constexpr (P == V)
           if (two) return go_ring<T, P, 16, 2>(a, r16, st);
@@ -1245,11 +1287,17 @@ cudaError_t pick(NormArgs& a, bool backward, cudaStream_t st) {
   }
   if (!backward && s.warps <= FW) {
     auto rows = [&](size_t n) { return a.C % (n / sizeof(T)) == 0 && al(a.x, n) && al(a.u, n) && al(a.h, n) && al(a.y, n); };
-    if (rows(16)) return s.ept == 8 ? go_rows<T, V, 8>(a, s, st) : go_rows<T, V, 16>(a, s, st);
+    // several rows a warp, where a sequence's rows fill half a tile of them
+    const bool sub = a.C <= 128 && 2LL * a.N >= 32 * FW / lanes_of(a.C);
+    if (rows(16))
+      return sub ? go_rows<T, V, 8, true>(a, s, st)
+                 : s.ept == 8 ? go_rows<T, V, 8>(a, s, st) : go_rows<T, V, 16>(a, s, st);
     // pairs of bf16 (rows of 514, 2^27 bytes a tensor: 420 us, 552 by k_norm_fwd; single fp32
     // values of rows of 1001 took 245 us for 182)
     if constexpr (sizeof(T) == 2)
-      if (rows(4)) return s.ept == 8 ? go_rows<T, 2, 8>(a, s, st) : go_rows<T, 2, 16>(a, s, st);
+      if (rows(4))
+        return sub ? go_rows<T, 2, 8, true>(a, s, st)
+                   : s.ept == 8 ? go_rows<T, 2, 8>(a, s, st) : go_rows<T, 2, 16>(a, s, st);
   }
   a.parts = norm_parts(a.B, a.N, a.C);
   if (s.ept == 8) return go<T, 8, false>(a, backward, s, st);

@@ -259,3 +259,14 @@ def test_weights_without_biases(dtype, B, N, C):
         assert (g is not None) == (t[n] is not None)
         if g is not None:
             check("d" + n, g, ref[n], dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,N,C", [(1, 1000, 64), (4, 300, 128), (2, 777, 18), (3, 500, 40), (1, 3000, 5), (2, 130, 127),
+                                   (1, 600, 8), (2, 1025, 1), (3, 33, 96), (40, 17, 64)])
+@pytest.mark.parametrize("pre,post,given", [
+    ("rms", None, ("weight",)), ("layer", "layer", ALL), ("layer", "rms", ALL + ("per_seq",)),
+    ("rms", "rms", ("u", "weight", "post_weight"))], ids=["norm", "all", "per_seq", "rms2"])
+def test_narrow_rows(dtype, B, N, C, pre, post, given):
+    """Several rows to a warp (a head's features), tiles that a sequence ends in."""
+    test_forward_and_gradients(dtype, B, N, C, pre, post, given)
