@@ -707,7 +707,8 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   };
   // The sums of sequence b into this block's slot: half of a kind's pairs at a time side by
   // side in shared memory, [group][pair][thread], and the groups' sums in order.
-  // (both here: chosen inside the lambda by SUB, the compiler lost the sums of the other kind)
+  // (chosen out here: chosen by SUB inside the lambda, kernels of a warp or more a row came
+  // out with sums that were never written)
   const int share_of = SUB ? (int)(threadIdx.x >> 5) : group, shares = SUB ? s.workers : s.rows;
   auto flush = [&](int b) {
     constexpr int HP = RH / 2;
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
 #pragma unroll
         for (int i = 0; i < HP; ++i) {
           float2 v = unpack2(A[n][h * HP + i]);
-          for (int o = threads; o < 32; o <<= 1) {     // the rows of a warp
+          for (int o = SUB ? threads : 32; o < 32; o <<= 1) {     // the rows of a warp
             v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
             v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
           }
