@@ -20,11 +20,18 @@
 // 128-byte swizzle; maps of four dimensions {inner, part, row, plane} fill what lies
 // behind a row, a part (g | u) or the last row with zeros.
 //
+// The instruction cuts its sums off: 2^-23 of a sum of terms of one sign for every 16 k
+// (2^24 rows summed in ranges of 2^19: 4.0e-3 lost, 2^26 rows: 1.2e-2).  So no accumulator of
+// bf16 products takes more than 256 steps (16384 k: 2^-13 of the sum, where a bf16 result's own
+// rounding is up to 2^-8) but those of g, u and dh, whose K are the features (up to 1024 steps,
+// 2^-11); beyond, the epilogue's threads add up to nearest, rows in registers, partial sums where
+// they lie, in L2 (LONG; a backward of 131072 rows, 512 x 1408: 858 us, 840 with ranges in one
+// accumulator each, 893 with partial sums in registers, which spill).
+//
 // fp32 operands are three bf16 planes each (24 bits) and a product six of theirs, a0 b0
-// apart from the five smaller ones in tensor memory: the instruction cuts its sums off,
-// which costs 2^-24 of the sum or so each time, so a0 b0 is summed over KCH steps there
-// and by the epilogue's threads, in registers, beyond; the others together are 2^-8 of
-// the sum.  A step's planes are copied once and read from shared memory by all six.
+// apart from the five smaller ones in tensor memory: a0 b0 is summed over two steps there and
+// in registers beyond, the others, 2^-7 of the sum at the most, over 32.  A step's planes are
+// copied once and read from shared memory by all six.
 //
 // 640 threads a CTA (384 for dglu): warps 0 and 2 copy (a thread each, A and B, into a ring
 // of NST slots), warp 1 issues (leader) and holds the tensor memory, warps 4 to 19 read the
@@ -68,7 +75,8 @@ struct Cfg {
   static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
   static constexpr int NST = F32 ? 9 : 6;
   static constexpr int PLANES = F32 ? 3 : 1;
-  static constexpr int KCH = F32 ? 2 : 1 << 30;     // K steps of an accumulator
+  static constexpr int KCH = F32 ? 2 : 256;         // K steps of an accumulator (bf16: LONG)
+  static constexpr int KSM = 32;                    // F32: of the smaller products'
   static constexpr uint32_t SMEM = NST * SLOT + 1024;
 };
 
@@ -160,8 +168,9 @@ __device__ __forceinline__ Item decode(const MlpGemmArgs& a, int it) {
 }
 
 // sixteen consecutive 16-byte pieces' worth of a lane's row: 32 fp32 values
+template <bool ADD = false>
 __device__ __forceinline__ void store_f32(float* tile, size_t ld, int first, int rows, int cols,
-                                          const float (&v)[32]) {
+                                          const float (&v)[32], bool add = false) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4 c[4];
@@ -169,7 +178,7 @@ __device__ __forceinline__ void store_f32(float* tile, size_t ld, int first, int
     for (int i = 0; i < 4; ++i)
       c[i] = make_uint4(__float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
                         __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
-    wtc::store_rows(tile + 16 * h, 4 * ld, first, rows, (cols - 16 * h + 3) / 4, c);
+    wtc::store_rows<ADD>(tile + 16 * h, 4 * ld, first, rows, (cols - 16 * h + 3) / 4, c, add);
   }
 }
 // 32 values of a lane's row as bf16
@@ -413,12 +422,14 @@ __device__ __forceinline__ void out_rows(const MlpGemmArgs& a, int part, int m0,
   __syncwarp();
 }
 
-template <bool F32, int EPI, bool TWO>
+// LONG: bf16 products into rows or partial sums whose ranges are longer than an accumulator's
+template <bool F32, int EPI, bool TWO, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     k_mlp_gemm(const __grid_constant__ Maps mp, MlpGemmArgs a) {
   using G = Cfg<F32>;
   constexpr int NST = G::NST, BN = G::BN, BNC = G::BNC, TN = EPI == kMlpGlu ? BNC : BN;
-  constexpr int PLANES = G::PLANES, KCH = G::KCH, EPW = epilogue_warps(EPI);
+  constexpr int PLANES = G::PLANES, KCH = F32 || LONG ? G::KCH : 1 << 30, EPW = epilogue_warps(EPI);
+  static_assert(!LONG || (!F32 && (EPI == kMlpRows || EPI == kMlpPart)), "");
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[NST];   // leader: both CTAs' copies landed
   __shared__ __align__(8) uint64_t empty[NST];  // a slot's products done
@@ -529,22 +540,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     if (rank == 0 && wtc::elect_one()) {
       int st = 0, consumed = 0;
       uint32_t ph = 0, u = 0;           // u: accumulators used so far
-      int li = 0;
+      int si = 0;                       // F32: accumulators of the smaller products
       bool bad = false;
       const uint32_t id = tc::idesc_bf16(2 * BM, BN) | (a.amn ? 1u << 15 : 0u) | (a.bmn ? 1u << 16 : 0u);
       // K slices of 16: 32 bytes on in a K-major row, 16 rows on in an MN-major block
       const uint64_t sta = (a.amn ? 2048 : 32) >> 4, stb = (a.bmn ? 2048 : 32) >> 4;
       const uint64_t da0 = a.amn ? wtc::desc_mn(sm, BLK64) : wtc::desc_k(sm);
       const uint64_t db0 = a.bmn ? wtc::desc_mn(sm + G::A_BYTES, BLK64) : wtc::desc_k(sm + G::A_BYTES);
-      for (int it = pair; it < a.items && !bad; it += pairs, ++li) {
+      for (int it = pair; it < a.items && !bad; it += pairs, ++si) {
         const Item r = decode<TN>(a, it);
-        const uint32_t small = tmem + 256 + (uint32_t)(li & 1) * 128;   // F32
+        int ks1 = r.ks0;                // F32: first step of the smaller products' accumulator
         for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
           const int k1 = KCH < r.ks1 - k0 ? k0 + KCH : r.ks1;
           const int acc = (int)(u & 1);
           if (!wtc::wait_or_flag(a.err, tc::smem_u32(&acce[acc]), ((u >> 1) & 1u) ^ 1u)) { bad = true; break; }
           tc::fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * BN);
+          // (the one before last is read out with a chunk that was released before this one)
+          if (F32 && k0 - ks1 == G::KSM) {
+            ks1 = k0;
+            ++si;
+          }
+          const uint32_t small = tmem + 256 + (uint32_t)(si & 1) * 128;   // F32
           for (int ks = k0; ks < k1; ++ks) {
             uint64_t da[PLANES], db[PLANES];
             int at[PLANES];
@@ -563,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
               } else if (p == 1) {
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k) {
-                  mma2(small, da[0] + k * sta, db[1 % PLANES] + k * stb, id, ks > r.ks0 || k > 0);
+                  mma2(small, da[0] + k * sta, db[1 % PLANES] + k * stb, id, ks > ks1 || k > 0);
                   mma2(small, da[1 % PLANES] + k * sta, db[0] + k * stb, id, 1);
                   mma2(small, da[1 % PLANES] + k * sta, db[1 % PLANES] + k * stb, id, 1);
                 }
@@ -597,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
     constexpr int COLS = TN / (EPW / 4);
     const int col0 = sub * COLS;
     uint32_t u = 0;
-    int li = 0;
+    int li = 0, si = 0;
     bool bad = false;
     // dglu of bf16 calls: p and q of DEEP blocks, each fetched again for DEEP blocks later
     // as soon as it is used (131072 rows of 1408: 278 us, 5.8 TB/s; read when they were needed,
@@ -615,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
         for (int i = 0; i < DEEP; ++i) ahead(r.m0, r.n0 + col0 + 16 * i, kept2[i]);
       }
     const bool biased = (EPI == kMlpRows || EPI == kMlpGlu) && a.bias != nullptr;
-    for (int it = pair; it < a.items && (biased || !bad); it += pairs, ++li) {
+    for (int it = pair; it < a.items && (biased || !bad); it += pairs, ++li, ++si) {
       const Item r = decode<TN>(a, it);
       const int m0 = r.m0 + (int)rank * BM, rows = min(BM, a.M - m0);
       const float* bias = nullptr;
@@ -636,13 +653,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
       }
       const size_t block0 = (size_t)((m0 + 32 * q) / 32) * a.fblocks;   // of p and q
       const bool some = 32 * q < rows;
-      // 32 columns of rows or partial sums
-      auto plain = [&](int col, float(&v)[32]) {
+      // 32 columns of rows or partial sums (add: to those of the chunks before)
+      auto plain = [&](int col, float(&v)[32], bool add) {
         const int n = r.n0 + col;
         if (n >= a.N || !some) return;
         if constexpr (EPI == kMlpPart) {
           float* tile = (float*)a.out + ((size_t)r.sp * a.M + m0) * a.ldo + r.part * a.part_out + n;
-          store_f32(tile, a.ldo, 32 * q, rows, min(32, (a.N - n + 3) & ~3), v);
+          store_f32<LONG>(tile, a.ldo, 32 * q, rows, min(32, (a.N - n + 3) & ~3), v, add);
         } else {
           out_rows<F32>(a, r.part, m0, n, 32 * q, rows, bias ? bias + col : nullptr, v);
         }
@@ -659,7 +676,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
         if (a.kept.pq && some && r.n0 + col < a.N) keep<F32>(a.kept, block0 + (r.n0 + col) / 16, g, v);
       };
       constexpr int NR = EPI == kMlpGlu ? 2 : COLS / 16;
-      float R[F32 ? NR : 1][16];       // fp32 calls: the sums so far
+      constexpr bool SUMS = F32 || (LONG && EPI == kMlpRows);
+      float R[SUMS ? NR : 1][16];      // the sums so far
       for (int k0 = r.ks0; k0 < r.ks1 && !bad; k0 += KCH < r.ks1 - k0 ? KCH : r.ks1 - k0, ++u) {
         const int acc = (int)(u & 1);
         __syncwarp();
@@ -674,9 +692,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
           __syncwarp();
           if (lane == 0) arrive_leader(acc ? acce1 : acce0);
         };
-        if constexpr (F32) {
-          const bool last = k0 + KCH >= r.ks1;
-          const uint32_t sd = tmem + lanes + 256 + (uint32_t)((li & 1) * 128 + col0);
+        if constexpr (SUMS) {
+          // F32: whether the smaller products' accumulator ends here
+          const bool end = F32 && (k0 + KCH >= r.ks1 || (k0 + KCH - r.ks0) % G::KSM == 0);
+          const uint32_t sd = tmem + lanes + 256 + (uint32_t)((si & 1) * 128 + col0);
+          if (end && k0 + KCH < r.ks1) ++si;
           constexpr uint32_t OTHER = EPI == kMlpGlu ? BNC : 16;
 #pragma unroll
           for (int j = 0; j < NR; ++j) {
@@ -686,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               R[j][i] = k0 == r.ks0 ? __uint_as_float(x[i]) : R[j][i] + __uint_as_float(x[i]);
-            if (last) {
+            if (end) {
               ld16(sd + j * OTHER, x);
               wait16(x);
 #pragma unroll
@@ -762,11 +782,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
             wtc::ld32(d + 32 * ch, x);
             wtc::ld_wait(x);
             if (ch == COLS / 32 - 1) release();
-            plain(col0 + 32 * ch, reinterpret_cast<float(&)[32]>(x));
+            plain(col0 + 32 * ch, reinterpret_cast<float(&)[32]>(x), k0 > r.ks0);
           }
         }
       }
-      if constexpr (F32) {
+      if constexpr (SUMS && LONG) {
+        if (bad) continue;
+#pragma unroll
+        for (int j = 0; j < NR / 2; ++j) plain(col0 + 32 * j, reinterpret_cast<float(&)[32]>(R[2 * j]), false);
+      } else if constexpr (F32) {
         if (bad) continue;
         const int n = r.n0 + col0;
         __nv_bfloat16* o = (__nv_bfloat16*)a.out + (size_t)m0 * a.ldo + n;
@@ -789,7 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
                              cols - 16 * j, w);
               }
         } else {
-          plain(col0, reinterpret_cast<float(&)[32]>(R));
+          plain(col0, reinterpret_cast<float(&)[32]>(R), false);
         }
       }
     }
@@ -949,13 +973,13 @@ bool map_view(CUtensorMap* t, const MlpView& v, int box_rows) {
   return encode_tiled_bf16_sw128(t, 4, v.p, dim, stride, box);
 }
 
-template <bool F32, int EPI, bool TWO = false>
+template <bool F32, int EPI, bool TWO = false, bool LONG = false>
 cudaError_t go(const char* name, const Maps& mp, const MlpGemmArgs& g, int dev, int sms, cudaStream_t st) {
   static SmemOnce once;
-  const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI, TWO>, Cfg<F32>::SMEM, dev);
+  const cudaError_t e = once.allow(k_mlp_gemm<F32, EPI, TWO, LONG>, Cfg<F32>::SMEM, dev);
   if (e != cudaSuccess) return e;
   const int pairs = g.items < sms / 2 ? g.items : sms / 2;
-  return launch(name, k_mlp_gemm<F32, EPI, TWO>, dim3((unsigned)(2 * pairs)), dim3(threads_of(EPI)), (size_t)Cfg<F32>::SMEM,
+  return launch(name, k_mlp_gemm<F32, EPI, TWO, LONG>, dim3((unsigned)(2 * pairs)), dim3(threads_of(EPI)), (size_t)Cfg<F32>::SMEM,
                 st, mp, g);
 }
 
@@ -1007,6 +1031,10 @@ cudaError_t run_mlp_gemm(const char* name, int epi, bool f32, bool two, const Ml
   if (!f32 && two)
     return epi == kMlpGlu ? go<false, kMlpGlu, true>(name, mp, g, dev, sms, st)
                           : go<false, kMlpDglu, true>(name, mp, g, dev, sms, st);
+  if (!f32 && ((long long)g.kst * g.kparts * g.kplanes + g.splits - 1) / g.splits > Cfg<false>::KCH) {
+    if (epi == kMlpRows) return go<false, kMlpRows, false, true>(name, mp, g, dev, sms, st);
+    if (epi == kMlpPart) return go<false, kMlpPart, false, true>(name, mp, g, dev, sms, st);
+  }
 #define GO(E) return f32 ? go<true, E>(name, mp, g, dev, sms, st) : go<false, E>(name, mp, g, dev, sms, st)
   switch (epi) {
     case kMlpRows: GO(kMlpRows);

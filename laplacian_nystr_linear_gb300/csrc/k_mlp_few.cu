@@ -45,6 +45,10 @@ constexpr int LW = 16, EW = 8, NF32 = 32 * (4 + LW + EW), NSF = 3;
 constexpr int LP = 128 * 8 / (32 * LW);       // pieces of eight weights a loading thread
 constexpr uint32_t PLANE = FNF * FK * 2;      // of the weights' tile
 constexpr int KCH = 2;                        // units of an accumulator
+// Units of an accumulator, since the instruction cuts its sums off (k_mlp.cu): of bf16 weights
+// (a CTA adds the next ones to its slot), and of the smaller products of fp32 ones
+constexpr int CUT_BF16 = 256, CUT_F32 = 32;
+static_assert(CUT_F32 % KCH == 0, "");
 
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
       const uint64_t da0 = a.kmajor ? wtc::desc_k(sm) : wtc::desc_mn(sm, 8192), db0 = wtc::desc_k(sm + A_BYTES);
       const uint64_t step = a.kmajor ? 2 : 128;      // a slice of 16 k
       for (int u = u0; u < u1 && !bad; ++seg) {
-        const int end = min(u1, (u / a.ks + 1) * a.ks), first = u;
+        const int end = min(min(u1, (u / a.ks + 1) * a.ks), u + CUT_BF16), first = u;
         if (!wtc::wait_or_flag(a.err, tc::smem_u32(&acce[seg & 1]), ((uint32_t)(seg >> 1) & 1u) ^ 1u)) {
           bad = true;
           break;
@@ -186,7 +190,8 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
     bool bad = false;
     for (int u = u0, seg = 0; u < u1 && !bad; ++seg) {
       const int block = u / a.ks;
-      u = min(u1, (block + 1) * a.ks);
+      const bool more = u > u0 && u > block * a.ks;      // this thread's values are there
+      u = min(min(u1, (block + 1) * a.ks), u + CUT_BF16);
       __syncwarp();
       if (!wtc::wait_warp(a.err, tc::smem_u32(&accf[seg & 1]), (uint32_t)(seg >> 1) & 1u)) {
         bad = true;
@@ -200,6 +205,11 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
         for (int half = 0; half < 2; ++half) {
           uint32_t x[16];
           tc::tmem_ld<16>(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)((seg & 1) * 256 + 128 * half + t0), x);
+          if (more)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (t0 + i < xrows)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) + o[(t0 + i) * FNB + 128 * half]);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (t0 + i < xrows) o[(t0 + i) * FNB + 128 * half] = __uint_as_float(x[i]);
@@ -223,12 +233,12 @@ __global__ void __launch_bounds__(NTC, 1) k_mlp_few_tc(const __grid_constant__ F
 }
 
 // fp32 weights.  WIDE: their rows are whole 16-byte pieces.  Tensor memory: a0 b0 of two
-// chunks, 64 columns each; from 128 on the smaller products, a0 b1 + a1 b0 and
-// a0 b2 + a1 b1 + a2 b0.
+// chunks, 64 columns each; from 128 and from 256 on the smaller products, a0 b1 + a1 b0 and
+// a0 b2 + a1 b1 + a2 b0, of a segment: up to CUT_F32 units of a column block.
 template <bool WIDE>
 __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows) {
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t full[NSF], empty[NSF], accf[2], acce[2], smalle;
+  __shared__ __align__(8) uint64_t full[NSF], empty[NSF], accf[2], acce[2], smalle[2];
   __shared__ uint32_t tmem_s;
   __shared__ int consumed_s, bad_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
   const uint32_t slot = 3 * PLANE + 3 * (uint32_t)rows * 128;
   int u0, u1;
   stretch(a, blockIdx.x, &u0, &u1);
-  if (warp == 0) tc::tmem_alloc(&tmem_s, 256);
+  if (warp == 0) tc::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
     for (int i = 0; i < NSF; ++i) {
       tc::mbar_init(tc::smem_u32(&full[i]), LW);
@@ -246,8 +256,8 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&accf[i]), 1);
       tc::mbar_init(tc::smem_u32(&acce[i]), EW);
+      tc::mbar_init(tc::smem_u32(&smalle[i]), EW);
     }
-    tc::mbar_init(tc::smem_u32(&smalle), EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     consumed_s = 0;
     bad_s = 0;
@@ -269,10 +279,13 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
       const uint64_t da0 = a.kmajor ? wtc::desc_k(sm) : wtc::desc_mn(sm, 8192);
       const uint64_t db0 = wtc::desc_k(sm + 3 * PLANE);
       const uint64_t step = a.kmajor ? 2 : 128, pa = PLANE >> 4, pb = (uint64_t)rows * 128 >> 4;
-      const uint32_t small = tmem + 128;
       for (int u = u0; u < u1 && !bad; ++seg) {
-        const int end = min(u1, (u / a.ks + 1) * a.ks), first = u;
-        if (!wtc::wait_or_flag(a.err, tc::smem_u32(&smalle), ((uint32_t)seg & 1u) ^ 1u)) { bad = true; break; }
+        const int end = min(min(u1, (u / a.ks + 1) * a.ks), u + CUT_F32), first = u;
+        const uint32_t small = tmem + 128 + (uint32_t)(seg & 1) * 128;
+        if (!wtc::wait_or_flag(a.err, tc::smem_u32(&smalle[seg & 1]), ((uint32_t)(seg >> 1) & 1u) ^ 1u)) {
+          bad = true;
+          break;
+        }
         for (; u < end && !bad; ++ch) {
           const int stop = min(end, u + KCH), c0 = u;
           if (!wtc::wait_or_flag(a.err, tc::smem_u32(&acce[ch & 1]), ((ch >> 1) & 1u) ^ 1u)) { bad = true; break; }
@@ -436,8 +449,10 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     bool bad = false;
     uint32_t ch = 0;
+    int seg = 0;
     for (int u = u0; u < u1 && !bad;) {
       const int block = u / a.ks, end = min(u1, (block + 1) * a.ks);
+      int cut = min(end, u + CUT_F32);       // where the segment ends
       float R[HR];
 #pragma unroll
       for (int i = 0; i < HR; ++i) R[i] = 0.f;
@@ -448,7 +463,8 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
           break;
         }
         tc::fence_after();
-        const bool last = u + KCH >= end;
+        const bool last = u + KCH >= cut;
+        const uint32_t small = tmem + lanes + 128 + (uint32_t)(seg & 1) * 128 + h0;
 #pragma unroll
         for (int t0 = 0; t0 < HR; t0 += 16)
           if (h0 + t0 < rows) {
@@ -459,14 +475,18 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
             if (last)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                tc::tmem_ld<16>(tmem + lanes + 128 + h * rows + h0 + t0, x);
+                tc::tmem_ld<16>(small + h * rows + t0, x);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) R[t0 + i] += __uint_as_float(x[i]);
               }
           }
         tc::fence_before();
         wtc::arrive_warp(tc::smem_u32(&acce[ch & 1]));
-        if (last) wtc::arrive_warp(tc::smem_u32(&smalle));
+        if (last) {
+          wtc::arrive_warp(tc::smem_u32(&smalle[seg & 1]));
+          ++seg;
+          cut = min(end, cut + CUT_F32);
+        }
       }
       if (bad) break;
       float* o = a.part + ((size_t)(block + blockIdx.x) * a.T + row0 + h0) * FNF + 32 * q + lane;
@@ -484,7 +504,7 @@ __global__ void __launch_bounds__(NF32, 1) k_mlp_few_f32(MlpFewArgs a, int rows)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 0) tc::tmem_dealloc(tmem, 256);
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
 // fp32, up to 8 rows (TT, padded), on the FP32 pipe: no more than eight multiply-adds a

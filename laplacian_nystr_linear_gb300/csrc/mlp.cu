@@ -29,7 +29,8 @@ struct Mlp {
 int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   if (T <= 0 || C <= 0 || F <= 0) return LAPNYS_EINVAL;
   if (dtype != LAPNYS_F32 && dtype != LAPNYS_BF16) return LAPNYS_EINVAL;
-  if (T > 1 << 28 || C > 1 << 20 || F > 1 << 20) return LAPNYS_EINVAL;
+  // C: what g, u and the gradient of h are summed over, in one accumulator (k_mlp.cu)
+  if (T > 1 << 28 || C > 1 << 16 || F > 1 << 20) return LAPNYS_EINVAL;
   // tiles of every product, and their ranges, are counted in 32 bits
   const long long wide = C > F ? C : F, narrow = C > F ? F : C;
   if ((T / kMlpTileM + 1LL) * (wide / 64 + 1) >= 1 << 28 || (wide / 128 + 1) * (narrow / 64 + 1) >= 1 << 24)

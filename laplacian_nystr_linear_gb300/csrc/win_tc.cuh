@@ -188,9 +188,11 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t h) {
 // Writes 16-byte pieces c of the warp's 32 rows (a row per lane, rows `first`..,
 // `stride` bytes apart, only those below `rows`; only `pieces` of 4).  Fours of lanes
 // change places first, so that they write 64 bytes of a row: a store then touches 8 rows
-// instead of 32, whose lines the load-store unit takes one by one.
+// instead of 32, whose lines the load-store unit takes one by one.  ADD: fp32 values, added
+// to what this thread wrote there before where `add` is set.
+template <bool ADD = false>
 __device__ __forceinline__ void store_rows(void* tile, size_t stride, int first, int rows, int pieces,
-                                           uint4 (&c)[4]) {
+                                           uint4 (&c)[4], bool add = false) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int x = 1; x <= 2; x <<= 1) {
@@ -213,6 +215,16 @@ __device__ __forceinline__ void store_rows(void* tile, size_t stride, int first,
   }
   const int row = first + (lane & ~3), i = lane & 3;
   uint8_t* dst = (uint8_t*)tile + row * stride + 16 * i;
+  if (ADD && add)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (row + r < rows && i < pieces) {
+        const float4 v = *reinterpret_cast<const float4*>(dst + r * stride);
+        c[r].x = __float_as_uint(v.x + __uint_as_float(c[r].x));
+        c[r].y = __float_as_uint(v.y + __uint_as_float(c[r].y));
+        c[r].z = __float_as_uint(v.z + __uint_as_float(c[r].z));
+        c[r].w = __float_as_uint(v.w + __uint_as_float(c[r].w));
+      }
 #pragma unroll
   for (int r = 0; r < 4; ++r)
     if (row + r < rows && i < pieces) *reinterpret_cast<uint4*>(dst + r * stride) = c[r];

@@ -215,3 +215,10 @@ def test_frequencies():
     assert parts.factor == pytest.approx(1 + 0.1 * math.log(4))
     back = lap.RotaryFrequencies.of([-0.5, 7.0], device="cpu")
     assert turns(back) == pytest.approx([1 - 0.5 / (2 * math.pi), 7 / (2 * math.pi) - 1])
+
+
+def test_mlp_refuses_more_features_than_an_accumulator_sums(lib):
+    for C in ((1 << 16) + 1, 1 << 17, 1 << 20):
+        assert _mlp_fwd(lib, C=C) == _lib.LAPNYS_EINVAL and _mlp_bwd(lib, C=C) == _lib.LAPNYS_EINVAL
+        assert lib.lapnys_mlp_ctx_bytes(100, C, 128, 1) == 0
+    assert lib.lapnys_mlp_ctx_bytes(100, 1 << 16, 128, 1) > 0
