@@ -21,12 +21,14 @@
 // features a thread of twelve or sixteen warps), which one thread copies into a ring in shared
 // memory (bulk copies; a tile's rows lie side by side).  What a feature is multiplied by is
 // laid out there once a sequence, in fp32.  8 x 16384 bf16 rows of 512, both norms, gate and
-// scale: 154 us, 5.2 TB/s: sums over a row are what a row waits for, so rows in flight and
+// scale: 158 us, 5.1 TB/s: sums over a row are what a row waits for, so rows in flight and
 // registers count (a warp of its own for the copies costs the registers of four: eight warps
 // of 16 features, or sixteen of 8, took 228); loads by the warps themselves beside 255
 // registers a thread took 390.  Rows that are no whole 16 bytes lie in the ring as they lie in
-// memory and are read from it by pairs or single elements: 1001 features, 400 us for 847 of
-// the loads by the threads; 514, 446 for 1425 (2^27 bytes a tensor).
+// memory and are read from it by pairs or single elements: 1001 features, 428 us for 847 of
+// the loads by the threads; 514, 450 for 1425 (2^27 bytes a tensor).  The mean is taken off
+// before the product with 1 / deviation, 2 to 4 % of the time: rows of a mean of 1000 deviations
+// have gradients as near as in 32-bit operations (as one multiply-add: twice as far off).
 //
 // Forward, rows of whole 16 bytes (bf16: or 4), up to 4096 features (k_norm_fwd_rows): threads
 // copy their own pieces two rows ahead (cp.async), two blocks an SM: 98 us for the same rows,
@@ -34,8 +36,8 @@
 // 434 us there; registers for the row ahead: 243.)
 //
 // Rows of up to 128 features (a head's): several to a warp in both directions, 8 features a
-// lane. bf16 rows of 64, both layer norms: backward 197 us for 720 with a warp a row, forward
-// 123 for 564; of 128: 202 for 367, 132 for 287 (2^27 bytes a tensor).
+// lane. bf16 rows of 64, both layer norms: backward 203 us for 720 with a warp a row, forward
+// 123 for 564; of 128: 210 for 367, 132 for 287 (2^27 bytes a tensor).
 //
 // Other rows (more features, forward of single elements, backward of tensors that start
 // anywhere): k_norm_fwd, k_norm_bwd, loads by the threads as they are needed.
@@ -760,11 +762,15 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
       }
     }
   };
-  // z becomes (z - mean) / deviation
-  auto unit = [](f32x2(&z)[RH], float mean, float r) {
-    const f32x2 rr = pack2(r, r), minus = pack2(-mean * r, -mean * r);
+  // z becomes (z - mean) / deviation, the mean taken off first as in the forward (z r - mean r
+  // would be off by the rounding of mean r, alike in all features)
+  auto unit = [](f32x2(&z)[RH], int kind, float mean, float r) {
+    const f32x2 rr = pack2(r, r), minus = pack2(-mean, -mean);
+    if (kind == kNormLayer)
 #pragma unroll
-    for (int i = 0; i < RH; ++i) z[i] = fma2(z[i], rr, minus);
+      for (int i = 0; i < RH; ++i) z[i] = wtc::add2(z[i], minus);
+#pragma unroll
+    for (int i = 0; i < RH; ++i) z[i] = wtc::mul2(z[i], rr);
   };
   // (sum of a b, sum of a) over the row
   auto moments = [&](const f32x2(&x)[RH], const f32x2(&y)[RH]) {
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
       f32x2 uh[RH], d[RH], v[RH];
       if (a.u) {
         share(tile, 1, uh);
-        if (a.post != kNormNone) unit(uh, mu, ru);
+        if (a.post != kNormNone) unit(uh, a.post, mu, ru);
       }
       if (a.dh) {
         share(tile, 2, d);
@@ -833,7 +839,7 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
             for (int i = 0; i < RH; ++i) hh[i] = wtc::add2(hh[i], v[i]);
           }
         }
-        unit(hh, mh, rh);
+        unit(hh, a.pre, mh, rh);
 #pragma unroll
         for (int i = 0; i < RH; ++i) {
           A[0][i] = fma2(e[i], hh[i], A[0][i]);
