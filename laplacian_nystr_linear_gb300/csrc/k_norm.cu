@@ -709,8 +709,9 @@ __global__ void __launch_bounds__(32 * ring_warps(E, KINDS), 1)
   };
   // The sums of sequence b into this block's slot: half of a kind's pairs at a time side by
   // side in shared memory, [group][pair][thread], and the groups' sums in order.
-  // (nvcc 13.0's front end drops the statement behind a discarded `if constexpr (..) for (..) {..}`
-  // in a lambda of a template: no such form in here, where the join's store was lost to it)
+  // (nvcc 13.0's front end drops the statement behind a loop that is the bare substatement of a
+  // discarded constexpr if, in a lambda of a template: no such form in flush, where the join's
+  // store was lost to it)
   const int share_of = SUB ? (int)(threadIdx.x >> 5) : group, shares = SUB ? s.workers : s.rows;
   auto flush = [&](int b) {
     constexpr int HP = RH / 2;
