@@ -3,9 +3,9 @@
 //   (a, b) -> factor (a cos t - b sin t, b cos t + a sin t),  t = 2 pi p w_i,
 // pair i of rot / 2: features (i, i + rot / 2) in the half layout, (2 i, 2 i + 1)
 // interleaved; features from rot on pass unchanged.  w_i is in turns a position, as
-// a fraction of 2^64: p w_i modulo 2^64 is the phase to 2^-64 of a turn for every
-// 32-bit position, exactly, where 32-bit angles lose all of it (at p = 10^6 a
-// rounded fp32 angle is off by 0.03).  The gradient is the turn back, by the same
+// a fraction of 2^64: modulo 2^64 p times that is exact, so the phase is off by p times
+// w_i's own rounding, 2^-34 of a turn at p = 2^31, where 32-bit angles lose all of it (at
+// p = 10^6 a rounded fp32 angle is off by 0.03).  The gradient is the turn back, by the same
 // factor.
 //
 // Bound by memory: queries and keys are read and written once.  A thread keeps its

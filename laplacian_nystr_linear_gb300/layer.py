@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import functools
 import math
+from decimal import Context, Decimal, localcontext
 from typing import NamedTuple, Optional
 
 import torch
@@ -40,6 +41,12 @@ def _any_requires_grad(tensors):
 # ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------
+# far positions multiply what an angle is off by, and doubles (2^-53 of it) would be a quarter of a
+# feature's 24 bits off at 2^31: angles are computed to 60 digits and rounded once, to 2^-64 of a turn
+_DIGITS = Context(prec=60)
+_TURN = Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257")
+
+
 class RotaryFrequencies(NamedTuple):
     """turns: int64 [pairs], turns a position in units of 2^-64; factor: of the turned features."""
     turns: torch.Tensor
@@ -47,16 +54,18 @@ class RotaryFrequencies(NamedTuple):
 
     @staticmethod
     def of(radians, factor: float = 1.0, device="cuda") -> "RotaryFrequencies":
-        """From angles a position, one for each pair (numbers or a tensor)."""
+        """From angles a position, one for each pair (numbers, of any precision, or a tensor)."""
         if isinstance(radians, torch.Tensor):
             radians = radians.double().cpu().tolist()
         turns = []
-        for w in radians:
-            w = float(w)
-            if not math.isfinite(w):
-                raise ValueError(f"angles must be finite: {w}")
-            n = round(math.ldexp(math.fmod(w / (2.0 * math.pi), 1.0), 64)) % 2 ** 64
-            turns.append(n - 2 ** 64 if n >= 2 ** 63 else n)
+        with localcontext(_DIGITS):
+            for w in radians:
+                w = w if isinstance(w, Decimal) else Decimal(float(w))
+                if not w.is_finite():
+                    raise ValueError(f"angles must be finite: {w}")
+                w /= _TURN
+                n = int(((w - w.to_integral_value()) * 2 ** 64).to_integral_value()) % 2 ** 64
+                turns.append(n - 2 ** 64 if n >= 2 ** 63 else n)
         if not turns:
             raise ValueError("no pairs")
         return RotaryFrequencies(torch.tensor(turns, dtype=torch.int64, device=device), float(factor))
@@ -72,6 +81,8 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, context=None
       "parts"   a pair that makes `high` turns or more over `context` positions (the length trained on)
                 stays, one of `low` turns or fewer is divided by factor, others in between linearly;
                 turned features are multiplied by 1 + 0.1 ln(factor) (factors above 1).
+    Other rules (by a pair's index, or without a factor of the features): RotaryFrequencies.of, which
+    takes any angles and any factor.
     """
     rot = int(rot)
     if rot < 2 or rot % 2:
@@ -81,20 +92,23 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, context=None
         raise ValueError("base and factor must be positive")
     if scaling not in (None, "linear", "base", "parts"):
         raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'base' or 'parts'")
-    if scaling == "base" and rot > 2:
-        base *= f ** (rot / (rot - 2.0))
-    w = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
-    grow = 1.0
-    if scaling == "linear":
-        w = [x / f for x in w]
-    elif scaling == "parts":
-        if context is None or not context > 0 or not high > low:
-            raise ValueError("'parts' takes the context trained on, and high > low")
-        for i, x in enumerate(w):
-            turns = context * x / (2.0 * math.pi)
-            keep = min(1.0, max(0.0, (turns - low) / (high - low)))
-            w[i] = x * (keep + (1.0 - keep) / f)
-        grow = 1.0 + 0.1 * math.log(f) if f > 1.0 else 1.0
+    if scaling == "parts" and (context is None or not context > 0 or not high > low):
+        raise ValueError("'parts' takes the context trained on, and high > low")
+    with localcontext(_DIGITS):
+        grow, by = 1.0, Decimal(f)
+        log = Decimal(base).ln()
+        if scaling == "base" and rot > 2:
+            log += by.ln() * rot / (rot - 2)
+        w = [(log * (-2 * i) / rot).exp() for i in range(rot // 2)]
+        if scaling == "linear":
+            w = [x / by for x in w]
+        elif scaling == "parts":
+            low, high, context = (Decimal(float(x)) for x in (low, high, context))
+            for i, x in enumerate(w):
+                turns = context * x / _TURN
+                keep = min(Decimal(1), max(Decimal(0), (turns - low) / (high - low)))
+                w[i] = x * (keep + (1 - keep) / by)
+            grow = 1.0 + 0.1 * math.log(f) if f > 1.0 else 1.0
     return RotaryFrequencies.of(w, grow, device)
 
 

@@ -222,3 +222,40 @@ def test_mlp_refuses_more_features_than_an_accumulator_sums(lib):
         assert _mlp_fwd(lib, C=C) == _lib.LAPNYS_EINVAL and _mlp_bwd(lib, C=C) == _lib.LAPNYS_EINVAL
         assert lib.lapnys_mlp_ctx_bytes(100, C, 128, 1) == 0
     assert lib.lapnys_mlp_ctx_bytes(100, 1 << 16, 128, 1) > 0
+
+
+def _turn(digits):
+    """2 pi 10^digits, in whole numbers: pi / 4 = 4 atan(1 / 5) - atan(1 / 239)"""
+    one = 10 ** (digits + 10)
+
+    def atan(n):
+        t = s = one // n
+        k = 1
+        while t:
+            t //= -n * n
+            k += 2
+            s += t // k
+        return s
+
+    return 8 * (4 * atan(5) - atan(239)) // 10 ** 10
+
+
+def test_frequencies_to_the_last_bit():
+    """base^(-2 i / 16) with base 10^4 is 10^(-i / 2): square roots in whole numbers, to 60 digits."""
+    D = 60
+    turn = _turn(D)
+    for scaling, by in ((None, 1), ("linear", 7)):
+        got = lap.rotary_frequencies(16, scaling=scaling, factor=by, device="cpu").turns.tolist()
+        for i, t in enumerate(got):
+            w = math.isqrt(10 ** (2 * D - i)) // by
+            assert abs(t % 2 ** 64 - w * 2 ** 64 / turn) <= 2 ** 12      # (a double's view of it)
+            assert abs(t % 2 ** 64 - (w * 2 ** 64 + turn // 2) // turn) <= 1, (scaling, i)
+    # the slowest pair with a raised base: exactly divided by the factor
+    base = lap.rotary_frequencies(16, scaling="base", factor=4, device="cpu").turns.tolist()
+    assert abs(base[-1] - (math.isqrt(10 ** (2 * D - 7)) // 4 * 2 ** 64 + turn // 2) // turn) <= 1
+    # given angles are taken as the numbers they are
+    got = lap.RotaryFrequencies.of([0.1, -3.0, 1e6], device="cpu").turns.tolist()
+    for w, t in zip((0.1, -3.0, 1e6), got):
+        n, d = w.as_integer_ratio()
+        want = (n * 10 ** D * 2 ** 64 + d * turn // 2) // (d * turn)
+        assert (t - want + 1) % 2 ** 64 <= 2, w
