@@ -99,7 +99,9 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, context=None
         log = Decimal(base).ln()
         if scaling == "base" and rot > 2:
             log += by.ln() * rot / (rot - 2)
-        w = [(log * (-2 * i) / rot).exp() for i in range(rot // 2)]
+        step, w = (log * -2 / rot).exp(), [Decimal(1)]
+        for _ in range(rot // 2 - 1):
+            w.append(w[-1] * step)
         if scaling == "linear":
             w = [x / by for x in w]
         elif scaling == "parts":
