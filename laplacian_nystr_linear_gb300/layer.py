@@ -187,7 +187,8 @@ class _Rotary(torch.autograd.Function):
         _no_tangent("rotary's backward", dq, dk)
         turns, start, positions = fctx.saved_tensors
         plan, factor = fctx.how
-        dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))
+        dq, dk = (g.contiguous() if g is not None and need else None
+                  for g, need in zip((dq, dk), fctx.needs_input_grad))
         if dq is None:                  # the call takes one tensor or two
             if dk is not None:
                 B, _, Hkv, *rest = plan[0]
