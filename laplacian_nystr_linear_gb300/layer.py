@@ -317,9 +317,13 @@ def _norm_bwd(x, u, weight, stats, dh, dy, p, post_weight, post_bias, gate, scal
 
 
 def norm_bwd(x, u, weight, stats, dh, dy, p: NormParams, post_weight=None, post_bias=None, gate=None,
-             scale=None, want=(True,) * 8, ws=None):
+             scale=None, want=None, ws=None):
     """lapnys_norm_bwd: the gradients of (x, u, weight, bias, post_weight, post_bias, gate, scale), those
-    wanted; dh, dy: the outputs', or None."""
+    wanted (None: of all that there are, and of a bias where there is a norm); dh, dy: the outputs', or None."""
+    if want is None:
+        there = (u, weight, post_weight, post_bias, gate, scale)
+        has_u, has_w, *others = (t is not None for t in there)
+        want = (True, has_u, has_w, p.pre is not None, *others)
     _check_norm(x, u, weight, None, post_weight, post_bias, gate, scale, p)
     _tensor(stats, "stats", (p.B, p.N, 4), torch.float32, x.device)
     _vector(dh, "dh", x.shape, x)

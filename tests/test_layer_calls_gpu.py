@@ -27,3 +27,23 @@ def test_rotary_turns_back_only_what_needs_a_gradient(which, monkeypatch):
     got, = torch.autograd.grad(out, some[which], [dq, dk])
     assert torch.equal(got, want[which])
     assert turned == [((dq, dk)[which].shape, None)]
+
+
+@pytest.mark.parametrize("given,pre,post", [(("weight",), "rms", None), (("u", "weight", "gate"), "layer", None),
+                                            (("u", "post_weight"), None, "rms"), (("u",), None, None),
+                                            (("u", "weight", "post_weight", "post_bias", "gate", "scale"), "rms", "layer")])
+def test_norm_bwd_gives_the_gradients_of_what_there_is(given, pre, post):
+    B, N, C = 2, 11, 64
+    shapes = dict(u=(B, N, C), weight=(C,), post_weight=(C,), post_bias=(C,), gate=(B, C), scale=(C,))
+    t = {n: _rand(*s, seed=i) if n in given else None for i, (n, s) in enumerate(shapes.items())}
+    x, dh, dy = (_rand(B, N, C, seed=i) for i in (7, 8, 9))
+    dh, dy = dh if "u" in given else None, dy if pre else None
+    p = lap.NormParams(B, N, C, False, pre, post, 1e-6)
+    vec = {n: t[n] for n in ("post_weight", "post_bias", "gate", "scale")}
+    _, _, st = lap.norm_fwd(x, t["u"], t["weight"], None, p, **vec)
+    got = lap.norm_bwd(x, t["u"], t["weight"], st, dh, dy, p, **vec)
+    want = (True, "u" in given, "weight" in given, pre is not None,
+            *(n in given for n in ("post_weight", "post_bias", "gate", "scale")))
+    again = lap.norm_bwd(x, t["u"], t["weight"], st, dh, dy, p, **vec, want=want)
+    assert [g is not None for g in got] == list(want)
+    assert all(torch.equal(a, b) for a, b in zip(got, again) if a is not None)
