@@ -514,9 +514,9 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
     """The gated feed-forward block, with autograd: (g | u) = x w_in + b_in,
     y = (act(g) * u) w_out + b_out.
 
-    x: CUDA tensor (float32 or bfloat16) of rows of C features, [.., C]; w_in: [C, 2 F], the gate's
-    columns, then the others; w_out: [F, C]; biases [2 F] and [C] or None; all 16-byte aligned; act:
-    "silu", "gelu" or "gelu_tanh".  Gradients are of first order, by reverse mode only.
+    x: CUDA tensor (float32 or bfloat16) of rows of C features, [.., C] (copied where it does not start on
+    16 bytes); w_in: [C, 2 F], the gate's columns, then the others; w_out: [F, C]; biases [2 F] and [C] or
+    None; all these 16-byte aligned; act: "silu", "gelu" or "gelu_tanh".  Gradients are of first order, by reverse mode only.
     """
     tensors = (x, w_in, b_in, w_out, b_out)
     _no_tangent("gated_mlp", *tensors)
@@ -524,6 +524,8 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
         raise ValueError("w_out must be [F, C]")
     plan = _mlp_plan(x.shape, w_out.shape[0], act)
     _check_mlp(*tensors, plan[0])
+    if x.data_ptr() % 16:           # a piece of another tensor
+        tensors = (x.clone(), *tensors[1:])
     if torch.is_grad_enabled() and _any_requires_grad(tensors):
         return _Mlp.apply(*tensors, plan)
     return _mlp_fwd(*tensors, plan, None, None, None, False)[0]

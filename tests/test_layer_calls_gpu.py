@@ -47,3 +47,19 @@ def test_norm_bwd_gives_the_gradients_of_what_there_is(given, pre, post):
     again = lap.norm_bwd(x, t["u"], t["weight"], st, dh, dy, p, **vec, want=want)
     assert [g is not None for g in got] == list(want)
     assert all(torch.equal(a, b) for a, b in zip(got, again) if a is not None)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,C", [(5, 33), (130, 33)])
+def test_rows_that_are_a_piece_of_others(dtype, T, C):
+    """gated_mlp of rows behind the first one, whose storage starts anywhere."""
+    whole = _rand(T + 1, C, seed=1, dtype=dtype)
+    w_in, w_out = _rand(C, 80, seed=2, dtype=dtype), _rand(40, C, seed=3, dtype=dtype)
+    dy = _rand(T, C, seed=4, dtype=dtype)
+    out = []
+    for x in (whole[1:], whole[1:].clone()):
+        leaves = [v.detach().requires_grad_(True) for v in (x, w_in, w_out)]
+        y = lap.gated_mlp(leaves[0], leaves[1], None, leaves[2], None)
+        out.append([y.detach(), lap.gated_mlp(x, w_in, None, w_out, None), *torch.autograd.grad(y, leaves, dy)])
+    assert whole[1:].data_ptr() % 16
+    assert all(torch.equal(a, b) for a, b in zip(*out))
