@@ -63,3 +63,35 @@ def test_rows_that_are_a_piece_of_others(dtype, T, C):
         out.append([y.detach(), lap.gated_mlp(x, w_in, None, w_out, None), *torch.autograd.grad(y, leaves, dy)])
     assert whole[1:].data_ptr() % 16
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan"), 3.4e38])
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_values_that_are_not_finite_in_fp32(T, bad):
+    """They stay in the sums that they are part of: a row of x in its row, a column of w_out in its column, a row of dy
+    in dx's row, in all of the weights' gradients and its column of b_out's."""
+    C, F = 64, 96
+    t = dict(x=_rand(T, C, seed=1), w_in=_rand(C, 2 * F, seed=2) / 8, b_in=_rand(2 * F, seed=3),
+             w_out=_rand(F, C, seed=4) / 8, b_out=_rand(C, seed=5))
+    dy = _rand(T, C, seed=6)
+    p = lap.MlpParams(T, C, F)
+    y, ctx = lap.mlp_fwd(**t, p=p)
+    grads = lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)
+
+    def put(name, *at):
+        v = t[name].clone()
+        v[at] = bad
+        return lap.mlp_fwd(**{**t, name: v}, p=p)[0]
+
+    rows, cols = torch.arange(T, device="cuda") != 2, torch.arange(C, device="cuda") != 5
+    got = put("x", 2, 7)
+    assert torch.equal(got[rows], y[rows]) and not got[2].isfinite().any()
+    got = put("w_out", 11, 5)
+    itself = T <= 8 and bad == 3.4e38       # few rows take weights in fp32: finite sums
+    assert torch.equal(got[:, cols], y[:, cols]) and (itself or not got[:, 5].isfinite().any())
+    assert itself or not put("w_in", 3, 20).isfinite().any()
+    dy[2, 5] = bad
+    dx, dw_in, db_in, dw_out, db_out = lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)
+    assert torch.equal(dx[rows], grads[0][rows]) and not dx[2].isfinite().any()
+    assert not dw_in.isfinite().any() and not db_in.isfinite().any() and not dw_out[:, 5].isfinite().any()
+    assert torch.equal(dw_out[:, cols], grads[3][:, cols]) and torch.equal(db_out[cols], grads[4][cols])
