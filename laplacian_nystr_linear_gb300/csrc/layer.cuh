@@ -20,7 +20,7 @@ struct RotaryArgs {
   float factor;              // of the turned features
   int inverse;               // turn back
   // filled by the launcher
-  int units, heads, groups;  // work items a token; heads of one, and groups of them
+  int units, heads;          // work items a token; heads of one
 };
 cudaError_t run_rotary(RotaryArgs& a, bool half, bool bf16, cudaStream_t st);
 

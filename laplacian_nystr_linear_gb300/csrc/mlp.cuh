@@ -123,8 +123,8 @@ struct MlpPackArgs {
 };
 cudaError_t run_mlp_pack(MlpPackArgs& a, bool bf16, cudaStream_t st);
 
-// sums over rows of planes of bf16 [rows][ld] (columns [0, cols)), or of fp32 when
-// `wide32`, in ranges of rows: part [ranges][cols], then out
+// sums over rows of planes of bf16 [rows][ld], or of fp32 (no planes), in ranges of rows:
+// part [ranges][columns], then out
 struct MlpColsumArgs {
   const void* src;
   size_t ld, plane_stride;
