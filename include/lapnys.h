@@ -412,13 +412,14 @@ int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void
  *     (g | u) = x w_in + b_in,  h = act(g) u,  y = h w_out + b_out
  * x, y [T][C], w_in [C][2 F] (the gate's columns, then the others), w_out [F][C],
  * b_in [2 F], b_out [C] (biases may be NULL), all of `dtype`, 16-byte aligned; any
- * T <= 2^28, C <= 2^16, F <= 2^20 with (T / 256 + 1) (w / 64 + 1) < 2^28 and (w / 128 + 1)
+ * T <= 2^28, C, F <= 2^20 (bf16 calls of more than 64 rows, or with C or F no multiple of 8:
+ * C <= 2^16) with (T / 256 + 1) (w / 64 + 1) < 2^28 and (w / 128 + 1)
  * (n / 64 + 1) < 2^24, w the greater, n the lesser of C and F (LAPNYS_EINVAL beyond); C
  * and F multiples of 8 in bf16 are read where they lie, others through copies in the
  * workspace.  act: z / (1 + exp(-z)) (LAPNYS_SILU), z (1 + erf(z / sqrt 2)) / 2
  * (LAPNYS_GELU), or its tanh form (LAPNYS_GELU_TANH).
  * Sums are float32; the tensor cores cut theirs off by up to 2^-22 for every 16 terms, which
- * is let go on for 2^14 terms of bf16 (g, u and the gradient of h: C terms), 2^11 of the
+ * is let go on for 2^14 terms of bf16 (g, u and the gradient of h: 2^16), 2^11 of the
  * smaller parts of fp32, and added up to nearest beyond.  bf16 calls round h, and in the
  * backward the gradient of (g | u), between the products: to bf16, or to two bf16 parts (16
  * bits) where T C F <= 2^28 or T <= 64 (with C and F multiples of 8).  fp32 operands are taken

@@ -29,8 +29,7 @@ struct Mlp {
 int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   if (T <= 0 || C <= 0 || F <= 0) return LAPNYS_EINVAL;
   if (dtype != LAPNYS_F32 && dtype != LAPNYS_BF16) return LAPNYS_EINVAL;
-  // C: what g, u and the gradient of h are summed over, in one accumulator (k_mlp.cu)
-  if (T > 1 << 28 || C > 1 << 16 || F > 1 << 20) return LAPNYS_EINVAL;
+  if (T > 1 << 28 || C > 1 << 20 || F > 1 << 20) return LAPNYS_EINVAL;
   // tiles of every product, and their ranges, are counted in 32 bits
   const long long wide = C > F ? C : F, narrow = C > F ? F : C;
   if ((T / kMlpTileM + 1LL) * (wide / 64 + 1) >= 1 << 28 || (wide / 128 + 1) * (narrow / 64 + 1) >= 1 << 24)
@@ -39,6 +38,8 @@ int check_mlp(Mlp& m, int T, int C, int F, int dtype) {
   m.f32 = dtype == LAPNYS_F32;
   m.planes = m.f32 ? 3 : 1;
   m.few = mlp_few_ok(T, C, F, m.f32);
+  // what g, u and the gradient of h are summed over in one accumulator (k_mlp.cu)
+  if (!m.f32 && !m.few && C > 1 << 16) return LAPNYS_EINVAL;
   // bf16 calls round h and the gradient of (g | u) between the products, which puts the
   // results' errors at 1.4 times their own rounding's, more where few values are summed
   // (1.7 at 4 rows of 64).  Calls of up to 2^28 multiply-adds a product, whose time is

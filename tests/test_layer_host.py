@@ -220,7 +220,9 @@ def test_frequencies():
 def test_mlp_refuses_more_features_than_an_accumulator_sums(lib):
     for C in ((1 << 16) + 1, 1 << 17, 1 << 20):
         assert _mlp_fwd(lib, C=C) == _lib.LAPNYS_EINVAL and _mlp_bwd(lib, C=C) == _lib.LAPNYS_EINVAL
-        assert lib.lapnys_mlp_ctx_bytes(100, C, 128, 1) == 0
+        assert lib.lapnys_mlp_ctx_bytes(100, C, 128, 1) == 0 and lib.lapnys_mlp_ctx_bytes(64, C | 1, 128, 1) == 0
+        # few rows and fp32 sum such products up in registers
+        assert lib.lapnys_mlp_ctx_bytes(100, C, 128, 0) > 0 and lib.lapnys_mlp_ctx_bytes(64, C & -8, 128, 1) > 0
     assert lib.lapnys_mlp_ctx_bytes(100, 1 << 16, 128, 1) > 0
 
 

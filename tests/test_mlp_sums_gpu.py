@@ -104,3 +104,19 @@ def test_rows_summed_over_many_features(act):
     ref = reference(**t, kind=act, dy=dy)
     check("y", y, ref["y"], torch.bfloat16)
     check("dx", dx, ref["x"], torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype,T", [(torch.bfloat16, 3), (torch.float32, 3), (torch.float32, 20), (torch.float32, 200)])
+def test_wide_rows(dtype, T):
+    """C beyond what one accumulator of a large bf16 product sums."""
+    C, F = 131080, 40
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda s, *shape: (torch.randn(shape, generator=gen, device="cuda") * s).to(dtype)  # noqa: E731
+    t = dict(x=r(1.0, T, C), w_in=r(C ** -0.5, C, 2 * F), b_in=r(0.3, 2 * F), w_out=r(F ** -0.5, F, C), b_out=r(0.3, C))
+    dy = r(1.0, T, C)
+    p = lap.MlpParams(T, C, F)
+    y, ctx = lap.mlp_fwd(**t, p=p)
+    ref = reference(**t, kind="silu", dy=dy)
+    check("y", y, ref["y"], dtype)
+    for n, g in zip(("x", "w_in", "b_in", "w_out", "b_out"), lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)):
+        check("d" + n, g, ref[n], dtype)
