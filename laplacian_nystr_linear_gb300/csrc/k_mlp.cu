@@ -40,8 +40,8 @@
 // stops issuing, and all threads meet at the cluster barrier before tensor memory is freed.
 //
 // Measured, bf16: 8192 rows, 8192 x 4096: 1.75 to 1.89 PFLOP/s in every product (the
-// library's product of 8192^3: 1.93).  131072 rows, 512 x 1408, forward + backward: 296 +
-// 119 + 280 + 219 + 224 + 117 us: the first and third are bound by what passes through L2
+// library's product of 8192^3: 1.93).  131072 rows, 512 x 1408, forward + backward: 290 +
+// 117 + 278 + 214 + 230 + 123 us: the first and third are bound by what passes through L2
 // (tiles of K = 512 in, h, p, q, dg and du in and out: 13 TB/s of it), the others run at
 // 1.6 to 1.7 PFLOP/s.  fp32, 4096 rows, 1024 x 4096: 250 to 290 TFLOP/s (a sixth of the
 // bf16 rate is 320).

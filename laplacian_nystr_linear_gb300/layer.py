@@ -516,7 +516,9 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
 
     x: CUDA tensor (float32 or bfloat16) of rows of C features, [.., C] (copied where it does not start on
     16 bytes); w_in: [C, 2 F], the gate's columns, then the others; w_out: [F, C]; biases [2 F] and [C] or
-    None; all these 16-byte aligned; act: "silu", "gelu" or "gelu_tanh".  Gradients are of first order, by reverse mode only.
+    None; all these 16-byte aligned; act: "silu", "gelu" or "gelu_tanh".  bf16 calls of more than 2^28
+    multiply-adds a product and more than 64 rows (or C or F no multiple of 8) hold the hidden values in bf16
+    between the products, others in 16 bits, so a row's last bits depend on how many are in the call.  Gradients are of first order, by reverse mode only.
     """
     tensors = (x, w_in, b_in, w_out, b_out)
     _no_tangent("gated_mlp", *tensors)
