@@ -422,7 +422,8 @@ int lapnys_norm_bwd(const void* x, const void* u, const void* weight, const void
  * is let go on for 2^14 terms of bf16 (g, u and the gradient of h: 2^16), 2^11 of the
  * smaller parts of fp32, and added up to nearest beyond.  bf16 calls round h, and in the
  * backward the gradient of (g | u), between the products: to bf16, or to two bf16 parts (16
- * bits) where T C F <= 2^28 or T <= 64 (with C and F multiples of 8).  fp32 operands are taken
+ * bits) where T C F <= 2^28 or T <= 64 (with C and F multiples of 8); ctx holds act(g) and
+ * u act'(g) in 11 bits but for those few rows.  fp32 operands are taken
  * as three bf16 parts (24 bits; magnitudes below 2^-110 keep fewer; a sum over an infinity
  * of x, a weight, dy, h or their like, or over a magnitude from 2^128 (1 - 2^-9) on, may come
  * out as infinite or NaN, whatever it would be).  Results repeat bit for bit.

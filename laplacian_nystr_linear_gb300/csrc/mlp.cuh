@@ -19,8 +19,8 @@ enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
 // p and q in blocks of 32 rows x 16 features, in the order in which a warp of an
 // epilogue (a row a lane) writes and reads them: 16-byte pieces of a row, 32 lanes of a
 // piece together.  bf16 calls keep them as f16 times a power of two for each row of a
-// block (11 bits of the block row's largest: one rounding of 2^-12 beside the gradients'
-// own of 2^-9), fp32 calls in fp32.
+// block (11 bits: half a step is up to 2^-11 of the value, beside the gradients' own of up to
+// 2^-8; below 2^-28 of the block row's largest 2^-39 of that), fp32 calls and few rows in fp32.
 constexpr int kMlpBlock = 16;   // features of a block
 struct MlpKept {
   uint8_t* pq;        // [ceil(T / 32)][ceil(F / 16)][p, q][pieces][32 lanes] of 16 bytes

@@ -11,7 +11,7 @@ exponential and reciprocal, 2^-22 each, times small factors) or 2^-21 (fp32) of 
 below 1.2.
 Between the products bf16 calls round h and the gradient of (g | u), half a step; with two parts (up to 64
 rows of whole 16-byte pieces, or T C F <= 2^28) half a step of what the first left, 2^-16 in all, and their products
-run over both parts, one after the other: twice the steps.  Kept for the backward: p, q rounded to f16 (bf16 calls), 2^-12 of the value and 2^-38 of the
+run over both parts, one after the other: twice the steps.  Kept for the backward: p, q rounded to f16 (bf16 calls), `kept` of the value and 2^-38 of the
 largest of a block (`block` features: 16 in the kernels).
 """
 import math
@@ -60,8 +60,9 @@ def mm2(a, b, two):
     return Off(a.v @ b.v, a.off @ B + A @ b.off + s * (A @ B) + 1e-37)
 
 
-def reference(x, w_in, b_in, w_out, b_out, kind, dy=None, block=32):
-    """{name: Off} of y and, with dy, of the gradients; x, dy [T, C]; block: features of a row with one scale"""
+def reference(x, w_in, b_in, w_out, b_out, kind, dy=None, block=32, kept=2.0 ** -12):
+    """{name: Off} of y and, with dy, of the gradients; x, dy [T, C]; block: features of a row with one scale;
+    kept: how far an f16 value may be off (half a step of its 11 bits is up to 2^-11)"""
     f32, dt = x.dtype == torch.float32, x.dtype
     Fh = w_out.shape[0]
     T, C = x.shape
@@ -85,7 +86,7 @@ def reference(x, w_in, b_in, w_out, b_out, kind, dy=None, block=32):
         for o in (p, q):
             pad = (-Fh) % block
             big = torch.nn.functional.pad(o.v.abs(), (0, pad)).unflatten(1, (-1, block)).amax(-1)
-            o.off = o.off + 2.0 ** -12 * (o.v.abs() + o.off) + 2.0 ** -38 * big.repeat_interleave(block, 1)[:, :Fh]
+            o.off = o.off + kept * (o.v.abs() + o.off) + 2.0 ** -38 * big.repeat_interleave(block, 1)[:, :Fh]
     D = Off.of(dy)
     dh = mm(D, tr(V), f32)
     dg, du = dh * q, dh * p
