@@ -90,10 +90,10 @@ def test_few_rows_over_many_features_f32(T):
     assert torch.equal(y, y[:1].expand_as(y))
 
 
-@pytest.mark.parametrize("act", ["silu", "gelu"])
-def test_rows_summed_over_many_features(act):
+@pytest.mark.parametrize("act,C", [("silu", 1024), ("gelu", 1024), ("silu", 1001)])
+def test_rows_summed_over_many_features(act, C):
     """y and dx over more features than an accumulator takes, without ranges of them."""
-    T, C, F = 4864, 1024, 20480
+    T, F = 4864, 20480
     gen = torch.Generator(device="cuda").manual_seed(5)
     r = lambda s, *shape: (torch.randn(shape, generator=gen, device="cuda") * s).bfloat16()  # noqa: E731
     t = dict(x=r(1.0, T, C), w_in=r(C ** -0.5, C, 2 * F), b_in=None, w_out=r(F ** -0.5, F, C), b_out=r(0.3, C))
@@ -120,3 +120,26 @@ def test_wide_rows(dtype, T):
     check("y", y, ref["y"], dtype)
     for n, g in zip(("x", "w_in", "b_in", "w_out", "b_out"), lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)):
         check("d" + n, g, ref[n], dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_many_rows_of_odd_sizes(dtype):
+    T, C, F = (1 << 21) + 77, 33, 21
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda s, *shape: (torch.randn(shape, generator=gen, device="cuda") * s).to(dtype)  # noqa: E731
+    t = dict(x=r(1.0, T, C), w_in=r(C ** -0.5, C, 2 * F), b_in=r(0.3, 2 * F), w_out=r(F ** -0.5, F, C), b_out=r(0.3, C))
+    dy = r(1.0, T, C)
+    p = lap.MlpParams(T, C, F)
+    y, ctx = lap.mlp_fwd(**t, p=p)
+    grads = lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)
+    again = lap.mlp_bwd(t["x"], t["w_in"], t["w_out"], dy, ctx, p)
+    ref = reference(**t, kind="silu", dy=dy, block=16, kept=2.0 ** -11)
+    check("y", y, ref["y"], dtype)
+    for n, g, h in zip(("x", "w_in", "b_in", "w_out", "b_out"), grads, again):
+        check("d" + n, g, ref[n], dtype)
+        assert torch.equal(g, h), n
+        # the bounds grow with the sum; the errors are those of roundings (fp32: 5 2^-24 of parts left out, and as much
+        # again for each of activation, sums in registers and ranges, whose signs are mixed: below 32 2^-24)
+        if n in ("w_in", "w_out"):
+            off = float((g.double() - ref[n].v).norm() / ref[n].v.norm())
+            assert off < (2.0 ** -19 if dtype == torch.float32 else 2.0 ** -8), (n, off)
