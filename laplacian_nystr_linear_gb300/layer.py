@@ -54,7 +54,7 @@ class RotaryFrequencies(NamedTuple):
 
     @staticmethod
     def of(radians, factor: float = 1.0, device="cuda") -> "RotaryFrequencies":
-        """From angles a position, one for each pair (numbers, of any precision, or a tensor)."""
+        """From angles a position, one for each pair (numbers, Decimal ones as they are, or a tensor)."""
         if isinstance(radians, torch.Tensor):
             radians = radians.double().cpu().tolist()
         turns = []
@@ -518,7 +518,8 @@ def gated_mlp(x, w_in, b_in, w_out, b_out, act="silu"):
     16 bytes); w_in: [C, 2 F], the gate's columns, then the others; w_out: [F, C]; biases [2 F] and [C] or
     None; all these 16-byte aligned; act: "silu", "gelu" or "gelu_tanh".  bf16 calls of more than 2^28
     multiply-adds a product and more than 64 rows (or C or F no multiple of 8) hold the hidden values in bf16
-    between the products, others in 16 bits, so a row's last bits depend on how many are in the call.  Gradients are of first order, by reverse mode only.
+    between the products, others in 16 bits, so a row's last bits depend on how many are in the call.
+    Gradients are of first order, by reverse mode only.
     """
     tensors = (x, w_in, b_in, w_out, b_out)
     _no_tangent("gated_mlp", *tensors)
